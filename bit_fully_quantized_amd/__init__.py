@@ -14,15 +14,17 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import (BF16, F32, FP8, GROUP_COL, GROUP_ROW, NVFP4, NVFP6, OSCI_ACCUM, OSCI_INIT, OSCI_WINDOW_END, RISK_BINS, RTN,
+from ._lib import (BF16, F32, FP8, GROUP_COL, GROUP_ROW, MXFP4, NVFP4, NVFP6, OSCI_ACCUM, OSCI_INIT, OSCI_WINDOW_END, RISK_BINS, RTN,
                    SR, Tj2Error, check, lib)
 
 __all__ = ["QTensor", "OutlierPlan", "quantize", "gemm", "gemm_workspace", "linear_fwd", "linear_fwd_workspace",
            "linear_bwd", "linear_bwd_workspace", "osci_reset_step", "osci_reset_step_multi", "OsciBatch",
            "master_update_step", "master_update_step_multi", "MasterBatch", "NextBwd", "bwd_operands", "channel_sumsq",
            "select_outliers",
-           "mfma_peak_probe", "rht_signs", "lib", "Tj2Error", "NVFP4", "FP8", "NVFP6", "BF16", "F32", "GROUP_ROW", "GROUP_COL",
-           "RTN", "SR", "OSCI_INIT", "OSCI_ACCUM", "OSCI_WINDOW_END", "RISK_BINS"]
+           "mfma_peak_probe", "rht_signs", "lib", "Tj2Error", "NVFP4", "FP8", "NVFP6", "MXFP4", "BF16", "F32", "GROUP_ROW", "GROUP_COL",
+           "RTN", "SR", "OSCI_INIT", "OSCI_ACCUM", "OSCI_WINDOW_END", "RISK_BINS",
+           "mx_quantize", "mx_dequantize", "mx_gemm", "mx_gemm_workspace", "mx_linear_fwd", "mx_linear_bwd",
+           "mx_linear_bwd_workspace"]
 
 
 def _stream():
@@ -66,35 +68,61 @@ _I32 = (torch.int32,)
 class QTensor:
     """A quantized operand of `rows` x `len` elements grouped along `len` (device storage).
 
-    codes    uint8 [rows, nb*64] (NVFP4) or [rows, nb*128] (FP8, NVFP6), nb = ceil(len/128)
-    scale16  uint8 [rows, nb*8] E4M3 (NVFP4, NVFP6)
-    scale128 float32 [rows, nb]
+    codes    uint8 [rows, nb*64] (NVFP4, MXFP4) or [rows, nb*128] (FP8, NVFP6), nb = ceil(len/128)
+    scale16  uint8 [rows, nb*8] E4M3 (NVFP4, NVFP6); MXFP4: [rows, nb*4], 2^(byte - 127) per 32
+    scale128 float32 [rows, nb] (not MXFP4)
     """
 
     def __init__(self, fmt: int, rows: int, length: int, device="cuda"):
-        if length % 16 or length <= 0 or rows <= 0:
+        if fmt == MXFP4:
+            if length <= 0 or rows <= 0:
+                raise ValueError("len and rows must be positive")
+        elif length % 16 or length <= 0 or rows <= 0:
             raise ValueError("len must be a positive multiple of 16 and rows positive")
         self.fmt, self.rows, self.len = fmt, rows, length
         nb = (length + 127) // 128
         self.nb = nb
-        self.codes = torch.empty((rows, nb * (64 if fmt == NVFP4 else 128)), dtype=torch.uint8, device=device)
-        self.scale16 = torch.empty((rows, nb * 8), dtype=torch.uint8, device=device) if fmt != FP8 else None
-        self.scale128 = torch.empty((rows, nb), dtype=torch.float32, device=device)
+        self.codes = torch.empty((rows, nb * (64 if fmt in (NVFP4, MXFP4) else 128)), dtype=torch.uint8, device=device)
+        self.scale16 = (torch.empty((rows, nb * (4 if fmt == MXFP4 else 8)), dtype=torch.uint8, device=device)
+                        if fmt != FP8 else None)
+        self.scale128 = torch.empty((rows, nb), dtype=torch.float32, device=device) if fmt != MXFP4 else None
+
+    @staticmethod
+    def wrap(fmt: int, rows: int, length: int, codes: torch.Tensor, scale16: torch.Tensor | None,
+             scale128: torch.Tensor | None = None) -> "QTensor":
+        """A quantized operand over arrays that exist already, in the layout above (stored weights); they are
+        not copied."""
+        nb = (length + 127) // 128
+        if rows <= 0 or length <= 0 or (fmt != MXFP4 and length % 16):
+            raise ValueError("rows must be positive and len a positive multiple of 16 (MXFP4: any positive length)")
+        if fmt not in (NVFP4, FP8, NVFP6, MXFP4):
+            raise ValueError(f"bad format {fmt}")
+        u8, f32 = (torch.uint8,), (torch.float32,)
+        _dense(codes, "codes", u8, shape=(rows, nb * (64 if fmt in (NVFP4, MXFP4) else 128)))
+        _dense(scale16, "scale16", u8, shape=(rows, nb * (4 if fmt == MXFP4 else 8)), optional=fmt == FP8)
+        _dense(scale128, "scale128", f32, shape=(rows, nb), optional=fmt == MXFP4)
+        q = QTensor.__new__(QTensor)
+        q.fmt, q.rows, q.len, q.nb = fmt, rows, length, nb
+        q.codes, q.scale16, q.scale128 = codes, scale16, scale128
+        return q
 
     def c(self) -> _lib.QTensorC:
         return _lib.QTensorC(self.codes.data_ptr(), 0 if self.scale16 is None else self.scale16.data_ptr(),
-                             self.scale128.data_ptr(), self.rows, self.len, self.fmt, 0)
+                             0 if self.scale128 is None else self.scale128.data_ptr(), self.rows, self.len, self.fmt, 0)
 
     def clone(self) -> "QTensor":
         q = QTensor.__new__(QTensor)
         q.fmt, q.rows, q.len, q.nb = self.fmt, self.rows, self.len, self.nb
-        q.codes, q.scale128 = self.codes.clone(), self.scale128.clone()
+        q.codes = self.codes.clone()
+        q.scale128 = self.scale128.clone() if self.scale128 is not None else None
         q.scale16 = self.scale16.clone() if self.scale16 is not None else None
         return q
 
     # host views of the unpadded content (for tests)
     def host(self):
         codes = self.codes.cpu().numpy()
+        if self.fmt == MXFP4:
+            return codes[:, : (self.len + 1) // 2], self.scale16.cpu().numpy()[:, : (self.len + 31) // 32], None
         if self.fmt == NVFP4:
             return (codes[:, : self.len // 2], self.scale16.cpu().numpy()[:, : self.len // 16],
                     self.scale128.cpu().numpy())
@@ -592,3 +620,7 @@ def select_outliers(scores, p: float, device="cuda") -> OutlierPlan:
 
 def n_outliers(K: int, p: float) -> int:
     return int(math.ceil(p * K / 16.0)) * 16
+
+
+from .mx import (mx_dequantize, mx_gemm, mx_gemm_workspace, mx_linear_bwd, mx_linear_bwd_workspace,  # noqa: E402
+                 mx_linear_fwd, mx_quantize)

@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtj2.so")
 MEASURE_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtj2_measure.so")
 
 TJ2_OK, TJ2_ERR_ARG, TJ2_ERR_SHAPE, TJ2_ERR_ALIGN, TJ2_ERR_HIP, TJ2_ERR_UNSUPPORTED = range(6)
-BF16, F32, NVFP4, FP8, NVFP6 = 0, 1, 2, 3, 4
+BF16, F32, NVFP4, FP8, NVFP6, MXFP4 = 0, 1, 2, 3, 4, 5
 GROUP_ROW, GROUP_COL = 0, 1
 RTN, SR = 0, 1
 OSCI_INIT, OSCI_ACCUM, OSCI_WINDOW_END = 0, 1, 2
@@ -116,6 +116,13 @@ SIGNATURES = {
     "tj2_channel_sumsq_workspace_size": (SZ, [I64, I64]),
     "tj2_channel_sumsq": (I32, [P, I64, I64, P, P, SZ, P]),
     "tj2_select_outliers": (I32, [P, I64, ctypes.c_double, P, P, ctypes.POINTER(I32)]),
+    "mxfp4_quantize": (I32, [P, I32, QP, I64, I64, I32, I32, I32, U32, U64, U64, QP, P]),
+    "mxfp4_dequantize": (I32, [QP, P, I32, P]),
+    "mxfp4_gemm": (I32, [QP, QP, P, I32, I64, I32, P, SZ, P]),
+    "mxfp4_gemm_workspace_size": (SZ, [I64, I64, I64]),
+    "mxfp4_linear_fwd": (I32, [P, I64, I64, I64, P, QP, QP, P, I32, P, SZ, P]),
+    "mxfp4_linear_bwd": (I32, [P, I64, I64, I64, QP, QP, I32, I32, U64, U64, P, I32, P, P, SZ, P]),
+    "mxfp4_linear_bwd_workspace_size": (SZ, [I64, I64, I64]),
 }
 
 

@@ -88,9 +88,9 @@ tj2_status check_dims(int64_t v, const char* name) {
 
 size_t qbytes(int fmt, int64_t rows, int64_t len, size_t* c, size_t* s16, size_t* s128) {
   const int64_t nb = (len + 127) / 128;
-  *c = (size_t)(rows * nb * (fmt == TJ2_NVFP4 ? 64 : 128));
-  *s16 = fmt == TJ2_FP8 ? 0 : (size_t)(rows * nb * 8);
-  *s128 = (size_t)(rows * nb * 4);
+  *c = (size_t)(rows * nb * (fmt == TJ2_NVFP4 || fmt == TJ2_MXFP4 ? 64 : 128));
+  *s16 = fmt == TJ2_FP8 ? 0 : (size_t)(rows * nb * (fmt == TJ2_MXFP4 ? 4 : 8));
+  *s128 = fmt == TJ2_MXFP4 ? 0 : (size_t)(rows * nb * 4);
   return *c + *s16 + *s128;
 }
 
@@ -413,9 +413,10 @@ const char* tj2_version(void) { return "tj2 0.1.0 gfx950"; }
 
 tj2_status tj2_qtensor_bytes(int32_t fmt, int64_t rows, int64_t len, size_t* codes_bytes, size_t* scale16_bytes,
                              size_t* scale128_bytes) {
-  if (fmt != TJ2_NVFP4 && fmt != TJ2_FP8 && fmt != TJ2_NVFP6)
-    return fail(TJ2_ERR_ARG, "format must be TJ2_NVFP4, TJ2_FP8 or TJ2_NVFP6");
-  if (rows <= 0 || len <= 0 || len % 16) return fail(TJ2_ERR_SHAPE, "rows > 0 and len a positive multiple of 16 required");
+  if (fmt != TJ2_NVFP4 && fmt != TJ2_FP8 && fmt != TJ2_NVFP6 && fmt != TJ2_MXFP4)
+    return fail(TJ2_ERR_ARG, "format must be TJ2_NVFP4, TJ2_FP8, TJ2_NVFP6 or TJ2_MXFP4");
+  if (rows <= 0 || len <= 0 || (fmt != TJ2_MXFP4 && len % 16))
+    return fail(TJ2_ERR_SHAPE, "rows > 0 and len a positive multiple of 16 (TJ2_MXFP4: any positive len) required");
   size_t c, s16, s128;
   qbytes(fmt, rows, len, &c, &s16, &s128);
   if (codes_bytes) *codes_bytes = c;
@@ -996,6 +997,187 @@ tj2_status tj2_select_outliers(const double* scores, int64_t K, double p, int32_
     else rest[nr++] = (int32_t)k;
   }
   *n_outliers = (int32_t)n;
+  return ok();
+}
+
+}  // extern "C"
+
+// ---- MXFP4 (mx.hip) ------------------------------------------------------------------
+namespace {
+
+// Longest MXFP4 row: a tile's 256 rows are addressed with 31-bit byte offsets.
+constexpr int64_t kMxMaxLen = (int64_t)1 << 23;
+
+tj2_status check_mx(const tj2_qtensor* q, const char* name, int64_t rows, int64_t len) {
+  if (!q) return fail(TJ2_ERR_ARG, "%s is NULL", name);
+  if (q->fmt != TJ2_MXFP4) return fail(TJ2_ERR_ARG, "%s has format %d, expected TJ2_MXFP4", name, q->fmt);
+  if (q->rows != rows || q->len != len)
+    return fail(TJ2_ERR_SHAPE, "%s is [%lld, %lld], expected [%lld, %lld]", name, (long long)q->rows, (long long)q->len,
+                (long long)rows, (long long)len);
+  if (rows <= 0 || len <= 0) return fail(TJ2_ERR_SHAPE, "%s: rows and len must be positive", name);
+  if (len > kMxMaxLen) return fail(TJ2_ERR_SHAPE, "%s: len %lld is above 2^23", name, (long long)len);
+  if (rows > (int64_t)1 << 30 || rows * ((len + 127) / 128) >= (int64_t)1 << 28)
+    return fail(TJ2_ERR_SHAPE, "%s: too many elements", name);
+  if (!q->codes || !q->scale16) return fail(TJ2_ERR_ARG, "%s: NULL array", name);
+  if (!aligned16(q->codes) || !aligned16(q->scale16)) return fail(TJ2_ERR_ALIGN, "%s: arrays must be 16-byte aligned", name);
+  return TJ2_OK;
+}
+
+// Shape rules of an MXFP4 quantizer call (out apart).
+tj2_status check_mx_input(const void* x, int32_t x_dtype, const tj2_qtensor* x_q, int64_t rows, int64_t cols, int32_t grouping,
+                          int32_t rounding) {
+  if (grouping != TJ2_GROUP_ROW && grouping != TJ2_GROUP_COL) return fail(TJ2_ERR_ARG, "bad grouping %d", grouping);
+  if (rounding != TJ2_RTN && rounding != TJ2_SR) return fail(TJ2_ERR_ARG, "bad rounding %d", rounding);
+  if (rows <= 0 || cols <= 0) return fail(TJ2_ERR_SHAPE, "rows and cols must be positive");
+  if (rows > (int64_t)1 << 30 || cols > (int64_t)1 << 30) return fail(TJ2_ERR_SHAPE, "dimension too large");
+  if (cols % 16) return fail(TJ2_ERR_SHAPE, "cols = %lld must be a multiple of 16", (long long)cols);
+  if (x_dtype == TJ2_BF16 || x_dtype == TJ2_F32) {
+    if (!x) return fail(TJ2_ERR_ARG, "x is NULL");
+    if (!aligned16(x)) return fail(TJ2_ERR_ALIGN, "x must be 16-byte aligned");
+  } else if (x_dtype == TJ2_MXFP4) {
+    if (grouping != TJ2_GROUP_COL) return fail(TJ2_ERR_UNSUPPORTED, "row grouping of a quantized input is not implemented");
+    TJ2_TRY(check_mx(x_q, "x_q", rows, cols));
+  } else {
+    return fail(TJ2_ERR_ARG, "bad x_dtype %d", x_dtype);
+  }
+  return TJ2_OK;
+}
+
+tj2_status run_mx_quant(const void* x, int x_dtype, const tj2_qtensor* x_q, int64_t rows, int64_t cols, int grouping,
+                        int rounding, int rht, uint32_t mask, uint64_t seed, uint64_t offset, const tj2_qtensor* out,
+                        hipStream_t s) {
+  MxQuantParams p = {};
+  p.in_dtype = x_dtype;
+  p.x = x;
+  if (x_dtype == TJ2_MXFP4) p.xq = make_view(*x_q);
+  p.rows = rows;
+  p.cols = cols;
+  p.grouping = grouping;
+  p.rounding = rounding;
+  p.rht = rht != 0;
+  p.rht_mask = mask & 0xFFFFu;
+  p.seed = seed;
+  p.offset = offset;
+  p.out = make_view(*out);
+  return hip_check(launch_mx_quant(p, s), "MXFP4 quantize launch");
+}
+
+tj2_status run_mx_gemm(const tj2_qtensor* A, const tj2_qtensor* B, void* C, int c_dtype, int64_t ldc, int accumulate,
+                       void* ws, hipStream_t s) {
+  return hip_check(launch_mx_gemm(make_view(*A), make_view(*B), C, c_dtype, ldc, accumulate, reinterpret_cast<float*>(ws), s),
+                   "MXFP4 gemm launch");
+}
+
+tj2_status check_mx_workspace(const void* ws, size_t ws_bytes, size_t need) {
+  if (ws && !aligned16(ws)) return fail(TJ2_ERR_ALIGN, "workspace must be 16-byte aligned");
+  if (ws && ws_bytes < need)
+    return fail(TJ2_ERR_ARG, "workspace has %zu bytes, %zu needed", ws_bytes, need);
+  return TJ2_OK;
+}
+
+tj2_status check_out_dtype(int32_t dtype, const char* name) {
+  if (dtype != TJ2_F32 && dtype != TJ2_BF16) return fail(TJ2_ERR_ARG, "%s must be TJ2_F32 or TJ2_BF16", name);
+  return TJ2_OK;
+}
+
+size_t mx_linear_bwd_gemm_ws(int64_t M, int64_t N, int64_t K) {
+  return std::max(mx_gemm_workspace_bytes(M, K, N), mx_gemm_workspace_bytes(N, K, M));
+}
+
+}  // namespace
+
+extern "C" {
+
+tj2_status mxfp4_quantize(const void* x, int32_t x_dtype, const tj2_qtensor* x_q, int64_t rows, int64_t cols,
+                          int32_t grouping, int32_t rounding, int32_t rht, uint32_t rht_signs, uint64_t seed,
+                          uint64_t offset, tj2_qtensor* out, void* stream) {
+  TJ2_TRY(check_mx_input(x, x_dtype, x_q, rows, cols, grouping, rounding));
+  TJ2_TRY(grouping == TJ2_GROUP_ROW ? check_mx(out, "out", rows, cols) : check_mx(out, "out", cols, rows));
+  TJ2_TRY(run_mx_quant(x, x_dtype, x_q, rows, cols, grouping, rounding, rht, rht_signs, seed, offset, out, (hipStream_t)stream));
+  return ok();
+}
+
+tj2_status mxfp4_dequantize(const tj2_qtensor* q, void* out, int32_t out_dtype, void* stream) {
+  if (!q) return fail(TJ2_ERR_ARG, "q is NULL");
+  TJ2_TRY(check_mx(q, "q", q->rows, q->len));
+  TJ2_TRY(check_out_dtype(out_dtype, "out_dtype"));
+  if (!out) return fail(TJ2_ERR_ARG, "out is NULL");
+  if (!aligned16(out)) return fail(TJ2_ERR_ALIGN, "out must be 16-byte aligned");
+  TJ2_TRY(hip_check(launch_mx_values(make_view(*q), out, out_dtype, (hipStream_t)stream), "MXFP4 dequantize launch"));
+  return ok();
+}
+
+size_t mxfp4_gemm_workspace_size(int64_t I, int64_t J, int64_t K) {
+  if (I <= 0 || J <= 0 || K <= 0) return 0;
+  return mx_gemm_workspace_bytes(I, J, K);
+}
+
+tj2_status mxfp4_gemm(const tj2_qtensor* A, const tj2_qtensor* B, void* C, int32_t c_dtype, int64_t ldc, int32_t accumulate,
+                      void* workspace, size_t ws_bytes, void* stream) {
+  if (!A || !B) return fail(TJ2_ERR_ARG, "A and B are required");
+  TJ2_TRY(check_mx(A, "A", A->rows, A->len));
+  TJ2_TRY(check_mx(B, "B", B->rows, A->len));
+  TJ2_TRY(check_out_dtype(c_dtype, "c_dtype"));
+  if (!C) return fail(TJ2_ERR_ARG, "C is NULL");
+  if (accumulate && c_dtype != TJ2_F32) return fail(TJ2_ERR_UNSUPPORTED, "accumulate needs an fp32 output");
+  if (ldc < B->rows) return fail(TJ2_ERR_SHAPE, "ldc < J");
+  TJ2_TRY(check_mx_workspace(workspace, ws_bytes, mx_gemm_workspace_bytes(A->rows, B->rows, A->len)));
+  TJ2_TRY(run_mx_gemm(A, B, C, c_dtype, ldc, accumulate, workspace, (hipStream_t)stream));
+  return ok();
+}
+
+tj2_status mxfp4_linear_fwd(const void* X, int64_t M, int64_t K, int64_t N, const float* W_master, tj2_qtensor* Wq,
+                            tj2_qtensor* Xq, void* Y, int32_t y_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  if (!X || !Y) return fail(TJ2_ERR_ARG, "X and Y are required");
+  if (M <= 0) return fail(TJ2_ERR_SHAPE, "M must be positive");
+  TJ2_TRY(check_dims(K, "K"));
+  TJ2_TRY(check_dims(N, "N"));
+  TJ2_TRY(check_mx(Xq, "Xq", M, K));
+  TJ2_TRY(check_mx(Wq, "Wq", N, K));
+  TJ2_TRY(check_out_dtype(y_dtype, "y_dtype"));
+  if (!aligned16(X) || !aligned16(W_master) || !aligned16(Y)) return fail(TJ2_ERR_ALIGN, "X, W_master and Y must be 16-byte aligned");
+  TJ2_TRY(check_mx_workspace(workspace, ws_bytes, mx_gemm_workspace_bytes(M, N, K)));
+  TJ2_TRY(run_mx_quant(X, TJ2_BF16, nullptr, M, K, TJ2_GROUP_ROW, TJ2_RTN, 0, 0, 0, 0, Xq, s));
+  if (W_master) TJ2_TRY(run_mx_quant(W_master, TJ2_F32, nullptr, N, K, TJ2_GROUP_ROW, TJ2_RTN, 0, 0, 0, 0, Wq, s));
+  TJ2_TRY(run_mx_gemm(Xq, Wq, Y, y_dtype, N, 0, workspace, s));
+  return ok();
+}
+
+size_t mxfp4_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return carve_size(TJ2_MXFP4, M, N) + carve_size(TJ2_MXFP4, N, M) + carve_size(TJ2_MXFP4, K, N) +
+         carve_size(TJ2_MXFP4, K, M) + 256 + align256(mx_linear_bwd_gemm_ws(M, N, K));
+}
+
+tj2_status mxfp4_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, const tj2_qtensor* Xq, const tj2_qtensor* Wq,
+                            int32_t rounding, int32_t rht, uint64_t seed, uint64_t offset, void* dX, int32_t dx_dtype,
+                            float* dW, void* workspace, size_t ws_bytes, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  if (!dY || !dX || !dW || !workspace) return fail(TJ2_ERR_ARG, "dY, dX, dW and workspace are required");
+  if (rounding != TJ2_RTN && rounding != TJ2_SR) return fail(TJ2_ERR_ARG, "bad rounding %d", rounding);
+  if (M <= 0) return fail(TJ2_ERR_SHAPE, "M must be positive");
+  TJ2_TRY(check_dims(K, "K"));
+  TJ2_TRY(check_dims(N, "N"));
+  TJ2_TRY(check_mx(Xq, "Xq", M, K));
+  TJ2_TRY(check_mx(Wq, "Wq", N, K));
+  TJ2_TRY(check_out_dtype(dx_dtype, "dx_dtype"));
+  if (!aligned16(dY) || !aligned16(dX) || !aligned16(dW)) return fail(TJ2_ERR_ALIGN, "dY, dX and dW must be 16-byte aligned");
+  TJ2_TRY(check_mx_workspace(workspace, ws_bytes, mxfp4_linear_bwd_workspace_size(M, N, K)));
+  uint8_t* cur = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~(uintptr_t)255);
+  const tj2_qtensor dYq = carve(cur, TJ2_MXFP4, M, N), dYt = carve(cur, TJ2_MXFP4, N, M), Wt = carve(cur, TJ2_MXFP4, K, N),
+                    Xt = carve(cur, TJ2_MXFP4, K, M);
+  TJ2_TRY(check_mx(&dYq, "dYq", M, N));
+  TJ2_TRY(check_mx(&dYt, "dYt", N, M));
+  TJ2_TRY(check_mx(&Wt, "Wt", K, N));
+  TJ2_TRY(check_mx(&Xt, "Xt", K, M));
+  const uint32_t sx = rht ? tj2_rht_signs(seed, offset) : 0, sw = rht ? tj2_rht_signs(seed, offset + 2) : 0;
+  TJ2_TRY(run_mx_quant(dY, TJ2_BF16, nullptr, M, N, TJ2_GROUP_ROW, rounding, rht, sx, seed, offset, &dYq, s));
+  TJ2_TRY(run_mx_quant(nullptr, TJ2_MXFP4, Wq, N, K, TJ2_GROUP_COL, rounding, rht, sx, seed, offset + 1, &Wt, s));
+  TJ2_TRY(run_mx_quant(dY, TJ2_BF16, nullptr, M, N, TJ2_GROUP_COL, rounding, rht, sw, seed, offset + 2, &dYt, s));
+  TJ2_TRY(run_mx_quant(nullptr, TJ2_MXFP4, Xq, M, K, TJ2_GROUP_COL, rounding, rht, sw, seed, offset + 3, &Xt, s));
+  TJ2_TRY(run_mx_gemm(&dYq, &Wt, dX, dx_dtype, K, 0, cur, s));
+  TJ2_TRY(run_mx_gemm(&dYt, &Xt, dW, TJ2_F32, K, 0, cur, s));
   return ok();
 }
 

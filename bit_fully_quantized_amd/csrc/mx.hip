@@ -1,0 +1,493 @@
+// Microscaled 4-bit floating point (MXFP4) for gfx950: quantiser, its inverse and
+// the product.
+//
+// A group of 32 consecutive elements shares one power of two, v = q 2^e with q
+// in E2M1 {0, .5, 1, 1.5, 2, 3, 4, 6} and the byte e + 127.  gfx950 multiplies the
+// format as it is stored (v_mfma_scale_f32_16x16x128_f8f6f4: four times the bf16
+// rate, a quarter of the bytes), where the double block's E4M3 scales have to be
+// decoded to f16 first.
+#include <algorithm>
+
+#include "tj2_tile.h"
+
+namespace tj2 {
+namespace {
+
+// ---- quantiser -------------------------------------------------------------------
+// Scale byte of a group whose largest magnitude has the fp32 bits `top`.
+//   RTN: e = floor(log2 top) - 2, so the group's top binade is E2M1's (4 to 8; values
+//        above 6 saturate), the rule of the OCP microscaling formats.
+//   SR:  the smallest e with top <= 6 2^e: nothing saturates, so the rounding stays
+//        unbiased.
+// Clamped to byte 0 (2^-127); a group with an infinity or NaN gets 255 (NaN).
+template <bool SR>
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
+  if (top >= 0x7F800000u) return 255u;
+  const int e = (int)(top >> 23) - ((SR && (top & 0x7FFFFFu) > 0x400000u) ? 1 : 2);
+  return (uint32_t)max(e, 0);
+}
+
+// 2^-e of a scale byte: exact, and v * 2^-e too (below 8; subnormal v become normal)
+__device__ __forceinline__ float mx_inverse(uint32_t byte) {
+  return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+// 2^e of a scale byte
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7FC00000u) : byte ? __uint_as_float(byte << 23) : 0x1p-127f;
+}
+
+// 16 values to 8 bytes of codes; a group with a NaN scale gets zeros.
+template <bool SR>
+__device__ __forceinline__ uint2 mx_codes16(const float v[16], uint32_t byte, uint64_t block, uint64_t seed, uint64_t offset) {
+  const float inv = mx_inverse(byte);
+  float y[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) y[i] = v[i] * inv;
+  uint32_t c[2];
+  if constexpr (SR) {
+    uint32_t r[16];
+    draws8(block, seed, offset, r);
+    draws8(block + 1, seed, offset, r + 8);
+    e2m1_sr16(y, r, c);
+  } else {
+    e2m1_rtn16(y, c);
+  }
+  return byte == 255u ? uint2{0u, 0u} : uint2{c[0], c[1]};
+}
+
+__device__ __forceinline__ uint32_t top_bits16(const float v[16]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+template <class T>
+__device__ __forceinline__ void load16(const T* p, float v[16]);
+template <>
+__device__ __forceinline__ void load16<uint16_t>(const uint16_t* p, float v[16]) {
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+  const uint4 a = q[0], b = q[1];
+  const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void load16<float>(const float* p, float v[16]) {
+  const float4* q = reinterpret_cast<const float4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 a = q[i];
+    v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = a.z; v[4 * i + 3] = a.w;
+  }
+}
+
+struct MxRowArgs {
+  const void* x;
+  uint8_t* codes;
+  uint8_t* scale;
+  int64_t rows;
+  int32_t cols, nb;  // elements and 128-element blocks per row
+  uint32_t mask;
+  uint64_t seed, offset;
+};
+
+// Groups along the rows.  A thread takes 16 neighbouring elements, a pair of lanes
+// a group (the pair's larger top by one DPP swap), eight threads a 128-element
+// block, padding included.
+template <class T, bool SR, bool RHT>
+__global__ __launch_bounds__(256) void mx_row_kernel(MxRowArgs p) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int32_t per = p.nb * 8;
+  const int64_t row = id / per;
+  if (row >= p.rows) return;
+  const int32_t h = (int32_t)(id - row * per), c = h * 16;
+  float v[16];
+  if (c < p.cols) {
+    load16<T>(reinterpret_cast<const T*>(p.x) + row * p.cols + c, v);
+    if constexpr (RHT) rht16(v, p.mask);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+  }
+  uint32_t top = top_bits16(v);
+  top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xF, 0xF, false));  // the other half of the group
+  const uint32_t byte = mx_scale_byte<SR>(top);
+  const int64_t padded = ((int64_t)p.cols + 31) / 32 * 32;
+  const uint2 q = mx_codes16<SR>(v, byte, (uint64_t)(row * padded + c) >> 3, p.seed, p.offset);
+  *reinterpret_cast<uint2*>(p.codes + (row * per + h) * 8) = c < p.cols ? q : uint2{0u, 0u};
+  if (!(h & 1)) p.scale[(row * per + h) >> 1] = (uint8_t)byte;
+}
+
+struct MxColArgs {
+  const void* x;       // dense [rows, cols], or codes of an MXFP4 operand [rows, cols]
+  const uint8_t* xs;   // its scale bytes
+  int64_t ldx, lds;    // codes and scale bytes per row of it
+  uint8_t* codes;      // [cols][nb * 64]
+  uint8_t* scale;      // [cols][nb * 4]
+  int32_t rows, cols, nb;
+  uint32_t mask;
+  uint64_t seed, offset;
+};
+
+struct MxIn {};  // tag: MXFP4 input
+
+// Groups along the columns, stored transposed.  A workgroup takes 128 rows by 64
+// columns through LDS: rows are read whole, then each thread owns 32 rows of one
+// column, a group, and writes its 16 bytes (four groups of a column make a line of
+// 64).  MXFP4 input is decoded to bf16 on the way, which holds its values exactly.
+template <class T, bool SR, bool RHT>
+__global__ __launch_bounds__(256) void mx_col_kernel(MxColArgs p) {
+  constexpr bool kMx = std::is_same<T, MxIn>::value;
+  constexpr bool kF32 = std::is_same<T, float>::value;
+  using E = std::conditional_t<kF32, float, uint16_t>;
+  __shared__ __attribute__((aligned(16))) E tile[128][64];
+  __shared__ __attribute__((aligned(4))) uint8_t sb[64][4];
+  const int t = threadIdx.x;
+  const int32_t r0 = (int32_t)blockIdx.y * 128, c0 = (int32_t)blockIdx.x * 64;
+  // 8 elements a load: 8 loads a row
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int q = i * 256 + t, r = q >> 3, c = (q & 7) * 8;
+    const bool in = r0 + r < p.rows && c0 + c < p.cols;
+    const int64_t row = r0 + r;
+    if constexpr (kF32) {
+      float4 a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
+      if (in) {
+        const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.x) + row * p.ldx + c0 + c);
+        a = s[0];
+        b = s[1];
+      }
+      *reinterpret_cast<float4*>(&tile[r][c]) = a;
+      *reinterpret_cast<float4*>(&tile[r][c + 4]) = b;
+    } else if constexpr (!kMx) {
+      uint4 a = {0u, 0u, 0u, 0u};
+      if (in) a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.x) + row * p.ldx + c0 + c);
+      *reinterpret_cast<uint4*>(&tile[r][c]) = a;
+    } else {
+      uint4 a = {0u, 0u, 0u, 0u};
+      if (in) {
+        const uint32_t codes = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(p.x) + row * p.ldx + (c0 + c) / 2);
+        const float s = mx_scale(p.xs[row * p.lds + (c0 + c) / 32]);
+        uint32_t w[4];
+        static_for<4>([&](auto k) __attribute__((always_inline)) {
+          constexpr int b = decltype(k)::value;
+          const f32x2v_t v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, b);
+          // exact in bf16: an E2M1 value times a power of two (2^-128 and up)
+          w[b] = (__float_as_uint(v.x * s) >> 16) | (__float_as_uint(v.y * s) & 0xFFFF0000u);
+        });
+        a = uint4{w[0], w[1], w[2], w[3]};
+      }
+      *reinterpret_cast<uint4*>(&tile[r][c]) = a;
+    }
+  }
+  __syncthreads();
+  const int c = t & 63, rg = t >> 6;
+  float v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const E e = tile[rg * 32 + i][c];
+    if constexpr (kF32) v[i] = e;
+    else v[i] = __uint_as_float((uint32_t)e << 16);
+  }
+  const int32_t first = r0 + rg * 32;
+  if constexpr (RHT) {
+    // a last piece of fewer than 16 rows stays as it is
+    if (first + 16 <= p.rows) rht16(v, p.mask);
+    if (first + 32 <= p.rows) rht16(v + 16, p.mask);
+  }
+  const uint32_t byte = mx_scale_byte<SR>(max(top_bits16(v), top_bits16(v + 16)));
+  const int64_t col = c0 + c;
+  const int64_t padded = ((int64_t)p.rows + 31) / 32 * 32;
+  const uint64_t block = (uint64_t)(col * padded + first) >> 3;
+  const uint2 a = mx_codes16<SR>(v, byte, block, p.seed, p.offset);
+  const uint2 b = mx_codes16<SR>(v + 16, byte, block + 2, p.seed, p.offset);
+  sb[c][rg] = (uint8_t)byte;
+  if (col < p.cols)
+    *reinterpret_cast<uint4*>(p.codes + (col * p.nb + blockIdx.y) * 64 + rg * 16) = uint4{a.x, a.y, b.x, b.y};
+  __syncthreads();
+  if (t < 64 && c0 + t < p.cols)
+    *reinterpret_cast<uint32_t*>(p.scale + ((int64_t)(c0 + t) * p.nb + blockIdx.y) * 4) = *reinterpret_cast<const uint32_t*>(sb[t]);
+}
+
+// ---- values ----------------------------------------------------------------------
+// 8 elements (one code word) a thread; rows of the output are `len` elements.
+template <bool F32>
+__global__ __launch_bounds__(256) void mx_values_kernel(const uint8_t* codes, const uint8_t* scale, int64_t rows, int32_t len,
+                                                        int32_t nb, void* out) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int32_t per = (len + 7) / 8;
+  const int64_t row = id / per;
+  if (row >= rows) return;
+  const int32_t c = (int32_t)(id - row * per) * 8;
+  const uint32_t q = *reinterpret_cast<const uint32_t*>(codes + row * nb * 64 + c / 2);
+  const float s = mx_scale(scale[row * nb * 4 + c / 32]);
+  float v[8];
+  static_for<4>([&](auto k) __attribute__((always_inline)) {
+    constexpr int b = decltype(k)::value;
+    const f32x2v_t f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, b);
+    v[2 * b] = f.x * s;
+    v[2 * b + 1] = f.y * s;
+  });
+  const int64_t at = row * len + c;
+  if constexpr (F32) {
+    float* o = reinterpret_cast<float*>(out) + at;
+    if (!(len & 3) && c + 8 <= len) {
+      reinterpret_cast<float4*>(o)[0] = float4{v[0], v[1], v[2], v[3]};
+      reinterpret_cast<float4*>(o)[1] = float4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < len) o[i] = v[i];
+    }
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(out) + at;
+    if (!(len & 7)) {
+      *reinterpret_cast<uint4*>(o) = uint4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < len) o[i] = (uint16_t)bf16_pair(v[i], 0.0f);
+    }
+  }
+}
+
+// ---- product ---------------------------------------------------------------------
+struct MxGemmArgs {
+  TileOp P, Q;        // P: B [J, K] (columns of C), Q: A [I, K] (rows of C)
+  void* C;
+  int64_t ldc;
+  float* partial;     // [splits][I][J] when the reduction is split
+  uint32_t tiles_p, tiles_q;
+  int32_t nch, splits;
+  int32_t bf16, accumulate, vec;  // vec: rows of C may be stored 16 bytes at a time
+};
+
+// N (a multiple of 4) neighbouring results of row i from column j on
+template <int N>
+__device__ __forceinline__ void store_run(const MxGemmArgs& p, int64_t i, int64_t j, const float (&v)[N]) {
+  const int64_t J = p.P.rows;
+  if (j >= J) return;
+  const bool whole = p.vec && j + N <= J;
+  if (p.bf16) {
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.C) + i * p.ldc + j;
+    if (whole && N % 8 == 0) {
+#pragma unroll
+      for (int k = 0; k + 8 <= N; k += 8)
+        *reinterpret_cast<uint4*>(o + k) = uint4{bf16_pair(v[k], v[k + 1]), bf16_pair(v[k + 2], v[k + 3]),
+                                                bf16_pair(v[k + 4], v[k + 5]), bf16_pair(v[k + 6], v[k + 7])};
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (j + k < J) o[k] = (uint16_t)bf16_pair(v[k], 0.0f);
+    }
+  } else {
+    float* o = reinterpret_cast<float*>(p.C) + i * p.ldc + j;
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < N; k += 4) {
+        float4 a = {v[k], v[k + 1], v[k + 2], v[k + 3]};
+        if (p.accumulate) {
+          const float4 c = *reinterpret_cast<const float4*>(o + k);
+          a.x += c.x; a.y += c.y; a.z += c.z; a.w += c.w;
+        }
+        *reinterpret_cast<float4*>(o + k) = a;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (j + k < J) o[k] = p.accumulate ? o[k] + v[k] : v[k];
+    }
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(T::NT, 1) void mx_gemm_kernel(MxGemmArgs p) {
+  __shared__ __attribute__((aligned(128))) typename T::Smem sm;
+  uint32_t tp, tq;
+  const uint32_t tiles = p.tiles_p * p.tiles_q;
+  const uint32_t z = blockIdx.x / tiles;
+  tile_of(blockIdx.x - z * tiles, tiles, p.tiles_q, p.tiles_p, tq, tp);
+  const int64_t p0 = (int64_t)tp * T::BM, q0 = (int64_t)tq * T::BN;
+  const int c0 = (int)((int64_t)p.nch * z / p.splits), c1 = (int)((int64_t)p.nch * (z + 1) / p.splits);
+  typename T::Acc acc = {};
+  T::run(p.P, p0, p.Q, q0, c0, c1, sm, acc);
+
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16;
+  MxGemmArgs o = p;
+  if (p.splits > 1) {
+    o.C = p.partial + (size_t)z * (size_t)p.Q.rows * (size_t)p.P.rows;
+    o.ldc = p.P.rows;
+    o.bf16 = 0;
+    o.accumulate = 0;
+    o.vec = (p.P.rows & 3) == 0;
+  }
+#pragma unroll
+  for (int tn = 0; tn < T::kTN; ++tn) {
+    const int64_t i = qw + T::q_row(tn, n);
+    if (i < p.Q.rows) {
+#pragma unroll
+      for (int tb = 0; tb < T::kTM / T::PB; ++tb) {
+        float v[4 * T::PB];
+#pragma unroll
+        for (int k = 0; k < 4 * T::PB; ++k) v[k] = acc[tb * T::PB + k / 4][tn][k % 4];
+        store_run<4 * T::PB>(o, i, pw + tb * 16 * T::PB, v);
+      }
+    }
+  }
+}
+
+// C = (C +) the sum of the splits' results in order, 4 a thread.
+__global__ __launch_bounds__(256) void mx_join_kernel(MxGemmArgs p) {
+  const int64_t I = p.Q.rows, J = p.P.rows, n = I * J, per = (J + 3) / 4;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, i = id / per, j = (id - i * per) * 4;
+  if (i >= I) return;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const float* s = p.partial + i * J + j;
+  if ((J & 3) == 0) {
+    for (int z = 0; z < p.splits; ++z, s += n) {
+      const float4 a = *reinterpret_cast<const float4*>(s);
+      v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    }
+  } else {
+    for (int z = 0; z < p.splits; ++z, s += n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + k < J) v[k] += s[k];
+  }
+  store_run<4>(p, i, j, v);
+}
+
+using TileBig = Tile<EL_MX, 2, 4, 8, 4>;
+
+template <class T>
+hipError_t launch_tile(MxGemmArgs a, hipStream_t s) {
+  a.tiles_p = (uint32_t)((a.P.rows + T::BM - 1) / T::BM);
+  a.tiles_q = (uint32_t)((a.Q.rows + T::BN - 1) / T::BN);
+  mx_gemm_kernel<T><<<a.tiles_p * a.tiles_q * (uint32_t)a.splits, T::NT, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+TileOp mx_operand(const QView& q) {
+  TileOp o;
+  o.p = q.codes;
+  o.s = q.s16;
+  o.rows = q.rows;
+  o.ld = q.nb * 64;
+  o.lds = q.nb * 4;
+  o.kb = (int32_t)(q.nb * 64);
+  o.sb = (int32_t)(q.nb * 4);
+  return o;
+}
+
+}  // namespace
+
+int mx_gemm_splits(int64_t I, int64_t J, int64_t K) {
+  const int64_t tiles = ((I + 255) / 256) * ((J + 255) / 256), nch = (K + 255) / 256;
+  int64_t z = 256 / std::max<int64_t>(tiles, 1);
+  z = std::min<int64_t>(z, nch / 4);
+  return (int)std::max<int64_t>(z, 1);
+}
+
+size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K) {
+  const int z = mx_gemm_splits(I, J, K);
+  return z > 1 ? (size_t)z * (size_t)I * (size_t)J * 4 : 0;
+}
+
+hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
+                          hipStream_t s) {
+  MxGemmArgs a = {};
+  a.P = mx_operand(B);
+  a.Q = mx_operand(A);
+  a.C = C;
+  a.ldc = ldc;
+  a.nch = (int32_t)((A.nb + 1) / 2);
+  a.bf16 = c_dtype == TJ2_BF16;
+  a.accumulate = accumulate;
+  const int64_t es = a.bf16 ? 2 : 4;
+  a.vec = (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && (ldc * es) % 16 == 0;
+  a.partial = partial;
+  a.splits = partial ? mx_gemm_splits(A.rows, B.rows, A.len) : 1;
+  hipError_t e = launch_tile<TileBig>(a, s);
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t n = A.rows * ((B.rows + 3) / 4);
+  mx_join_kernel<<<(uint32_t)((n + 255) / 256), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_values(const QView& q, void* out, int dtype, hipStream_t s) {
+  const int64_t n = q.rows * ((q.len + 7) / 8);
+  const uint32_t grid = (uint32_t)((n + 255) / 256);
+  if (dtype == TJ2_F32) mx_values_kernel<true><<<grid, 256, 0, s>>>(q.codes, q.s16, q.rows, (int32_t)q.len, (int32_t)q.nb, out);
+  else mx_values_kernel<false><<<grid, 256, 0, s>>>(q.codes, q.s16, q.rows, (int32_t)q.len, (int32_t)q.nb, out);
+  return hipGetLastError();
+}
+
+namespace {
+template <class T>
+hipError_t launch_row(const MxRowArgs& a, bool sr, bool rht, uint32_t grid, hipStream_t s) {
+  if (sr) {
+    if (rht) mx_row_kernel<T, true, true><<<grid, 256, 0, s>>>(a);
+    else mx_row_kernel<T, true, false><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (rht) mx_row_kernel<T, false, true><<<grid, 256, 0, s>>>(a);
+    else mx_row_kernel<T, false, false><<<grid, 256, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+template <class T>
+hipError_t launch_col(const MxColArgs& a, bool sr, bool rht, dim3 grid, hipStream_t s) {
+  if (sr) {
+    if (rht) mx_col_kernel<T, true, true><<<grid, 256, 0, s>>>(a);
+    else mx_col_kernel<T, true, false><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (rht) mx_col_kernel<T, false, true><<<grid, 256, 0, s>>>(a);
+    else mx_col_kernel<T, false, false><<<grid, 256, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_mx_quant(const MxQuantParams& q, hipStream_t s) {
+  const bool sr = q.rounding == TJ2_SR;
+  if (q.grouping == TJ2_GROUP_ROW) {
+    MxRowArgs a = {};
+    a.x = q.x;
+    a.codes = q.out.codes;
+    a.scale = q.out.s16;
+    a.rows = q.rows;
+    a.cols = (int32_t)q.cols;
+    a.nb = (int32_t)q.out.nb;
+    a.mask = q.rht_mask;
+    a.seed = q.seed;
+    a.offset = q.offset;
+    const uint32_t grid = (uint32_t)((q.rows * q.out.nb * 8 + 255) / 256);
+    return q.in_dtype == TJ2_BF16 ? launch_row<uint16_t>(a, sr, q.rht, grid, s) : launch_row<float>(a, sr, q.rht, grid, s);
+  }
+  MxColArgs a = {};
+  a.x = q.x;
+  a.ldx = q.cols;
+  if (q.in_dtype == TJ2_MXFP4) {
+    a.x = q.xq.codes;
+    a.xs = q.xq.s16;
+    a.ldx = q.xq.nb * 64;
+    a.lds = q.xq.nb * 4;
+  }
+  a.codes = q.out.codes;
+  a.scale = q.out.s16;
+  a.rows = (int32_t)q.rows;
+  a.cols = (int32_t)q.cols;
+  a.nb = (int32_t)q.out.nb;
+  a.mask = q.rht_mask;
+  a.seed = q.seed;
+  a.offset = q.offset;
+  const dim3 grid((uint32_t)((q.cols + 63) / 64), (uint32_t)q.out.nb);
+  if (q.in_dtype == TJ2_MXFP4) return launch_col<MxIn>(a, sr, q.rht, grid, s);
+  return q.in_dtype == TJ2_BF16 ? launch_col<uint16_t>(a, sr, q.rht, grid, s) : launch_col<float>(a, sr, q.rht, grid, s);
+}
+
+}  // namespace tj2

@@ -27,9 +27,9 @@ inline QView make_view(const tj2_qtensor& q) {
   v.len = q.len;
   v.nb = (q.len + 127) / 128;
   v.fmt = q.fmt;
-  v.ld_codes = q.fmt == TJ2_NVFP4 ? v.nb * 64 : v.nb * 128;  // FP8 / NVFP6: one byte per element
-  v.ld_s16 = v.nb * 8;
-  v.ld_s128 = v.nb;
+  v.ld_codes = q.fmt == TJ2_NVFP4 || q.fmt == TJ2_MXFP4 ? v.nb * 64 : v.nb * 128;  // FP8 / NVFP6: one byte per element
+  v.ld_s16 = q.fmt == TJ2_MXFP4 ? v.nb * 4 : v.nb * 8;
+  v.ld_s128 = q.fmt == TJ2_MXFP4 ? 0 : v.nb;
   return v;
 }
 
@@ -157,6 +157,27 @@ bool gemm_image_pays(int64_t I);
 bool gemm_image_two_segments(const GemmParams& p);
 
 hipError_t launch_gemm(const GemmParams& p, hipStream_t s);
+
+// MXFP4 (mx.hip): quantiser of a dense or (column grouping) MXFP4 input, the
+// values of codes, and the product C = A B^T with the reduction split over
+// mx_gemm_splits() workgroups when `partial` is given.
+struct MxQuantParams {
+  int in_dtype;  // TJ2_BF16, TJ2_F32 or TJ2_MXFP4
+  const void* x;
+  QView xq;
+  int64_t rows, cols;
+  int grouping, rounding;
+  bool rht;
+  uint32_t rht_mask;
+  uint64_t seed, offset;
+  QView out;
+};
+hipError_t launch_mx_quant(const MxQuantParams& q, hipStream_t s);
+hipError_t launch_mx_values(const QView& q, void* out, int dtype, hipStream_t s);
+int mx_gemm_splits(int64_t I, int64_t J, int64_t K);
+size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K);
+hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
+                          hipStream_t s);
 
 // OsciReset and the fused master-weight pass (AdamW, then OsciReset), on up to
 // kOsciMultiMax weight matrices per launch.  Parameters shared by the

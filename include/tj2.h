@@ -46,6 +46,7 @@ typedef int32_t tj2_status;
 #define TJ2_NVFP4 2
 #define TJ2_FP8 3
 #define TJ2_NVFP6 4 /* E2M3 elements in the NVFP4 double block (the FP6 x FP4 variant) */
+#define TJ2_MXFP4 5 /* E2M1 elements under one power-of-two scale per 32 (microscaled; the mxfp4_ entry points) */
 
 /* grouping of a quantizer */
 #define TJ2_GROUP_ROW 0 /* 1x16 groups along the contiguous (column) dimension   */
@@ -76,8 +77,13 @@ typedef int32_t tj2_status;
  *                                            E4M3FN byte of that value
  *              scale16  uint8 [rows][nb*8]   E4M3FN, one per 16 elements
  *              scale128 float [rows][nb]     one per 128 elements (amax / 3360)
+ *   TJ2_MXFP4: codes    uint8 [rows][nb*64]  E2M1, as for TJ2_NVFP4
+ *              scale16  uint8 [rows][nb*4]   one byte b per 32 elements, the scale
+ *                                            2^(b - 127); 255 is NaN
+ *              scale128 unused (may be NULL)
  * Element positions beyond `len` in each row are padding; producers write
- * them as zero.  `len` must be a positive multiple of 16.
+ * them as zero.  `len` must be a positive multiple of 16 (TJ2_MXFP4: any
+ * positive length).
  * E2M1 code: bit 3 sign, bits 2..0 index into {0, 0.5, 1, 1.5, 2, 3, 4, 6}.
  */
 typedef struct {
@@ -130,7 +136,8 @@ const char* tj2_version(void);
 /*
  * Bytes needed by each array of a tj2_qtensor of the given format and shape
  * (see the storage table above).  Host-only; returns TJ2_ERR_ARG / _SHAPE for
- * a bad format or a len that is not a positive multiple of 16.
+ * a bad format or a len that is not a positive multiple of 16 (TJ2_MXFP4: not
+ * positive).
  */
 tj2_status tj2_qtensor_bytes(int32_t fmt, int64_t rows, int64_t len, size_t* codes_bytes,
                              size_t* scale16_bytes, size_t* scale128_bytes);
@@ -544,6 +551,77 @@ tj2_status tj2_channel_sumsq(const void* X, int64_t M, int64_t K, double* acc, v
  */
 tj2_status tj2_select_outliers(const double* scores, int64_t K, double p, int32_t* outliers, int32_t* rest,
                                int32_t* n_outliers);
+
+/*
+ * Microscaled 4-bit floating point (MXFP4: groups of 32 under one power of two,
+ * the OCP microscaling formats' 4-bit member), which gfx950 multiplies as it is
+ * stored.  Operands are tj2_qtensor of format TJ2_MXFP4, at most 2^23 elements
+ * long.
+ *
+ * mxfp4_quantize: a logical [rows, cols] tensor, cols a multiple of 16, dense
+ * (x_dtype TJ2_BF16 / TJ2_F32, contiguous) or, for TJ2_GROUP_COL, MXFP4
+ * (x_dtype TJ2_MXFP4, *x_q grouped along cols, dequantized first; values exact).
+ * grouping TJ2_GROUP_ROW: groups along cols, *out is [rows, cols]; TJ2_GROUP_COL:
+ * groups along rows, *out is [cols, rows] (transposed).  rows need not be a
+ * multiple of 16 or 32; a group at the end of a row may hold fewer than 32.
+ * Per group with largest magnitude a > 0 (a = 0: scale byte 0, codes +-0):
+ *   TJ2_RTN: scale 2^e, e = floor(log2 a) - 2 (not below -127); x / 2^e to the
+ *            nearest E2M1 value, ties to the even code, above 6 to 6.
+ *   TJ2_SR:  the smallest e >= -127 with a <= 6 * 2^e, so that nothing saturates;
+ *            stochastic rounding with the draws of nvfp4_quantize, element index
+ *            r * ceil32(len) + position (r: row of *out; ceil32: rounded up to a
+ *            multiple of 32).
+ * A group that holds an infinity or NaN gets scale byte 255 (NaN) and zero codes.
+ * rht != 0: the 16-wide Hadamard transform with sign mask rht_signs along the
+ * grouped dimension first; a last piece of fewer than 16 positions is left as
+ * it is (both operands of a product are transformed alike, so it cancels there).
+ */
+tj2_status mxfp4_quantize(const void* x, int32_t x_dtype, const tj2_qtensor* x_q, int64_t rows, int64_t cols,
+                          int32_t grouping, int32_t rounding, int32_t rht, uint32_t rht_signs, uint64_t seed,
+                          uint64_t offset, tj2_qtensor* out, void* stream);
+
+/*
+ * The values of q as out [rows, len], contiguous, TJ2_BF16 or TJ2_F32: exact in
+ * both, but for magnitudes of 2^128 and more, which become infinite.
+ */
+tj2_status mxfp4_dequantize(const tj2_qtensor* q, void* out, int32_t out_dtype, void* stream);
+
+/*
+ * C[i, j] (+)= sum_k A[i, k] B[j, k], A [I, K] and B [J, K] MXFP4 grouped along K,
+ * fp32 sums.  c_dtype TJ2_F32 or TJ2_BF16 (round to nearest even), ldc >= J in
+ * elements; accumulate != 0 adds into C (TJ2_F32 only).  A NaN scale in a row of
+ * A (or B) makes that row (column) of C NaN.
+ * workspace: partial sums of a reduction that is split because C has few tiles,
+ * mxfp4_gemm_workspace_size(I, J, K) bytes (0: none needed); NULL runs unsplit,
+ * a smaller non-NULL workspace is TJ2_ERR_ARG.  The order of the sums depends on
+ * the sizes and on whether a workspace is given, and on nothing else.
+ */
+tj2_status mxfp4_gemm(const tj2_qtensor* A, const tj2_qtensor* B, void* C, int32_t c_dtype, int64_t ldc, int32_t accumulate,
+                      void* workspace, size_t ws_bytes, void* stream);
+size_t mxfp4_gemm_workspace_size(int64_t I, int64_t J, int64_t K);
+
+/*
+ * Forward of a linear layer Y = X W^T on MXFP4 operands: X [M, K] bf16 to *Xq
+ * (TJ2_RTN, saved for the backward), W_master [N, K] fp32 (or NULL: *Wq as given)
+ * to *Wq, Y [M, N] TJ2_BF16 or TJ2_F32.  Any M >= 1; K and N multiples of 16.
+ * workspace as for mxfp4_gemm with mxfp4_gemm_workspace_size(M, N, K).
+ */
+tj2_status mxfp4_linear_fwd(const void* X, int64_t M, int64_t K, int64_t N, const float* W_master, tj2_qtensor* Wq,
+                            tj2_qtensor* Xq, void* Y, int32_t y_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Its backward from dY [M, N] bf16 and the forward's quantized tensors:
+ *   dX [M, K] (TJ2_BF16 or TJ2_F32) = Q(dY T) . Q(T^T W-hat)
+ *   dW [N, K] fp32                  = Q(dY^T T) . Q(T^T X-hat)
+ * with the roundings' Philox offsets (dY +0, W-hat +1, dY^T +2, X-hat +3) and the
+ * transforms' signs (dX: offset + 0, dW: offset + 2) of nvfp4_linear_bwd; rht == 0
+ * leaves the transforms T out; rounding TJ2_SR or TJ2_RTN applies to all four.
+ * workspace: mxfp4_linear_bwd_workspace_size(M, N, K) bytes, required.
+ */
+tj2_status mxfp4_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, const tj2_qtensor* Xq, const tj2_qtensor* Wq,
+                            int32_t rounding, int32_t rht, uint64_t seed, uint64_t offset, void* dX, int32_t dx_dtype,
+                            float* dW, void* workspace, size_t ws_bytes, void* stream);
+size_t mxfp4_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
 
 #ifdef __cplusplus
 }
