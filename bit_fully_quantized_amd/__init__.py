@@ -24,7 +24,8 @@ __all__ = ["QTensor", "OutlierPlan", "quantize", "gemm", "gemm_workspace", "line
            "mfma_peak_probe", "rht_signs", "lib", "Tj2Error", "NVFP4", "FP8", "NVFP6", "MXFP4", "BF16", "F32", "GROUP_ROW", "GROUP_COL",
            "RTN", "SR", "OSCI_INIT", "OSCI_ACCUM", "OSCI_WINDOW_END", "RISK_BINS",
            "mx_quantize", "mx_dequantize", "mx_gemm", "mx_gemm_workspace", "mx_linear_fwd", "mx_linear_bwd",
-           "mx_linear_bwd_workspace"]
+           "mx_linear_bwd_workspace", "linear_ce_fwd", "linear_ce_bwd", "linear_cross_entropy", "distill_topk",
+           "distillation_loss"]
 
 
 def _stream():
@@ -624,3 +625,5 @@ def n_outliers(K: int, p: float) -> int:
 
 from .mx import (mx_dequantize, mx_gemm, mx_gemm_workspace, mx_linear_bwd, mx_linear_bwd_workspace,  # noqa: E402
                  mx_linear_fwd, mx_quantize)
+from .losses import (distill_topk, distillation_loss, linear_ce_bwd, linear_ce_fwd,  # noqa: E402
+                     linear_cross_entropy)

@@ -123,6 +123,11 @@ SIGNATURES = {
     "mxfp4_linear_fwd": (I32, [P, I64, I64, I64, P, QP, QP, P, I32, P, SZ, P]),
     "mxfp4_linear_bwd": (I32, [P, I64, I64, I64, QP, QP, I32, I32, U64, U64, P, I32, P, P, SZ, P]),
     "mxfp4_linear_bwd_workspace_size": (SZ, [I64, I64, I64]),
+    "tj2_linear_ce_fwd": (I32, [P, I64, P, I64, P, I64, I64, I64, I64, P, P, P, SZ, P]),
+    "tj2_linear_ce_fwd_workspace_size": (SZ, [I64, I64, I64]),
+    "tj2_linear_ce_bwd": (I32, [P, I64, P, I64, P, I64, I64, I64, I64, P, P, P, I32, P, I32, P, SZ, P]),
+    "tj2_linear_ce_bwd_workspace_size": (SZ, [I64, I64, I64]),
+    "tj2_distill_topk": (I32, [P, I32, I64, I64, I64, P, P, I32, ctypes.c_float, ctypes.c_float, P, I64, P, P, P, I64, P]),
 }
 
 

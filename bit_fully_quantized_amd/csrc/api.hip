@@ -1182,3 +1182,145 @@ tj2_status mxfp4_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, con
 }
 
 }  // extern "C"
+
+// ---- losses at the head (loss.hip) -----------------------------------------------------
+namespace {
+
+// Sizes both passes of the head's cross entropy take: 256 rows of any operand (the
+// transposed ones have a token or a vocabulary entry per column) are addressed with
+// 31-bit byte offsets.
+tj2_status check_ce(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t T, int64_t K,
+                    int64_t V) {
+  if (!X || !W || !targets) return fail(TJ2_ERR_ARG, "X, W and targets are required");
+  if (T <= 0 || V <= 0) return fail(TJ2_ERR_SHAPE, "T and V must be positive");
+  TJ2_TRY(check_dims(K, "K"));
+  constexpr int64_t most = (int64_t)1 << 21;
+  if (T > most || V > most || K > most || ldx > most || ldw > most) return fail(TJ2_ERR_SHAPE, "T, V, K, ldx and ldw are at most 2^21");
+  if (T * V > (int64_t)1 << 40) return fail(TJ2_ERR_SHAPE, "T * V is above 2^40");
+  if (ldx < K || ldw < K || ldx % 8 || ldw % 8) return fail(TJ2_ERR_SHAPE, "ldx and ldw must be multiples of 8 and at least K");
+  if (!aligned16(X) || !aligned16(W)) return fail(TJ2_ERR_ALIGN, "X and W must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(targets) & 7u) return fail(TJ2_ERR_ALIGN, "targets must be 8-byte aligned");
+  return TJ2_OK;
+}
+
+tj2_status check_f32(const void* p, const char* name, bool required) {
+  if (!p && required) return fail(TJ2_ERR_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(TJ2_ERR_ALIGN, "%s must be 4-byte aligned", name);
+  return TJ2_OK;
+}
+
+tj2_status check_ce_workspace(const void* ws, size_t ws_bytes, size_t need) {
+  if (!ws) return fail(TJ2_ERR_ARG, "workspace is NULL");
+  return check_mx_workspace(ws, ws_bytes, need);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tj2_linear_ce_fwd_workspace_size(int64_t T, int64_t K, int64_t V) {
+  return T <= 0 || K <= 0 || V <= 0 ? 0 : ce_fwd_workspace_bytes(T, V);
+}
+
+tj2_status tj2_linear_ce_fwd(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t T,
+                             int64_t K, int64_t V, int64_t ignore_index, float* loss, float* lse, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  TJ2_TRY(check_ce(X, ldx, W, ldw, targets, T, K, V));
+  TJ2_TRY(check_f32(loss, "loss", false));
+  TJ2_TRY(check_f32(lse, "lse", true));
+  TJ2_TRY(check_ce_workspace(workspace, ws_bytes, ce_fwd_workspace_bytes(T, V)));
+  CeParams c = {};
+  c.X = X;
+  c.W = W;
+  c.y = targets;
+  c.T = T;
+  c.K = K;
+  c.V = V;
+  c.ldx = ldx;
+  c.ldw = ldw;
+  c.ignore = ignore_index;
+  c.loss = loss;
+  c.lse = lse;
+  TJ2_TRY(hip_check(launch_ce_fwd(c, workspace, (hipStream_t)stream), "cross entropy launch"));
+  return ok();
+}
+
+size_t tj2_linear_ce_bwd_workspace_size(int64_t T, int64_t K, int64_t V) {
+  return T <= 0 || K <= 0 || V <= 0 ? 0 : ce_bwd_workspace_bytes(T, K, V);
+}
+
+tj2_status tj2_linear_ce_bwd(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t T,
+                             int64_t K, int64_t V, int64_t ignore_index, const float* lse, const float* dloss, void* dX,
+                             int32_t dx_dtype, void* dW, int32_t dw_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  TJ2_TRY(check_ce(X, ldx, W, ldw, targets, T, K, V));
+  TJ2_TRY(check_f32(lse, "lse", true));
+  TJ2_TRY(check_f32(dloss, "dloss", true));
+  if (!dX && !dW) return fail(TJ2_ERR_ARG, "dX or dW is required");
+  TJ2_TRY(check_out_dtype(dx_dtype, "dx_dtype"));
+  TJ2_TRY(check_out_dtype(dw_dtype, "dw_dtype"));
+  if (!aligned16(dX) || !aligned16(dW)) return fail(TJ2_ERR_ALIGN, "dX and dW must be 16-byte aligned");
+  TJ2_TRY(check_ce_workspace(workspace, ws_bytes, ce_bwd_workspace_bytes(T, K, V)));
+  CeParams c = {};
+  c.X = X;
+  c.W = W;
+  c.y = targets;
+  c.T = T;
+  c.K = K;
+  c.V = V;
+  c.ldx = ldx;
+  c.ldw = ldw;
+  c.ignore = ignore_index;
+  c.lse = const_cast<float*>(lse);
+  c.dloss = dloss;
+  c.dX = dX;
+  c.dW = dW;
+  c.dx_dtype = dx_dtype;
+  c.dw_dtype = dw_dtype;
+  TJ2_TRY(hip_check(launch_ce_bwd(c, workspace, (hipStream_t)stream), "cross entropy backward launch"));
+  return ok();
+}
+
+tj2_status tj2_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ldl, const int32_t* ids,
+                            const void* teacher, int32_t k, float temperature, float alpha, const int64_t* targets,
+                            int64_t ignore_index, const float* weight, float* loss, void* dlogits, int64_t ldd,
+                            void* stream) {
+  if (!logits || !ids || !teacher) return fail(TJ2_ERR_ARG, "logits, ids and teacher are required");
+  TJ2_TRY(check_out_dtype(dtype, "dtype"));
+  if (!loss && !dlogits) return fail(TJ2_ERR_ARG, "loss or dlogits is required");
+  if (T <= 0 || V <= 0) return fail(TJ2_ERR_SHAPE, "T and V must be positive");
+  if (T > (int64_t)1 << 22 || V > (int64_t)1 << 30) return fail(TJ2_ERR_SHAPE, "T is at most 2^22 and V at most 2^30");
+  if (k <= 0 || k > distill_max_k()) return fail(TJ2_ERR_SHAPE, "k = %d must be from 1 to %d", k, distill_max_k());
+  if (ldl < V || (dlogits && ldd < V)) return fail(TJ2_ERR_SHAPE, "rows of logits and dlogits must be at least V apart");
+  if (dlogits == logits && ldd != ldl) return fail(TJ2_ERR_SHAPE, "dlogits in place of logits needs the same row pitch");
+  if (!(temperature > 0.0f) || isinf(temperature)) return fail(TJ2_ERR_ARG, "temperature must be positive and finite");
+  if (!(alpha >= 0.0f && alpha <= 1.0f)) return fail(TJ2_ERR_ARG, "alpha must be from 0 to 1");
+  if (alpha != 1.0f && !targets) return fail(TJ2_ERR_ARG, "alpha below 1 needs targets");
+  const uintptr_t es = dtype == TJ2_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(logits) % es || reinterpret_cast<uintptr_t>(dlogits) % es || reinterpret_cast<uintptr_t>(teacher) % es)
+    return fail(TJ2_ERR_ALIGN, "logits, teacher and dlogits must be aligned to their elements");
+  if (reinterpret_cast<uintptr_t>(targets) & 7u) return fail(TJ2_ERR_ALIGN, "targets must be 8-byte aligned");
+  TJ2_TRY(check_f32(ids, "ids", true));
+  TJ2_TRY(check_f32(weight, "weight", false));
+  TJ2_TRY(check_f32(loss, "loss", false));
+  DistillParams d = {};
+  d.z = logits;
+  d.dz = dlogits;
+  d.ldz = ldl;
+  d.ldd = ldd;
+  d.T = T;
+  d.V = V;
+  d.ignore = ignore_index;
+  d.ids = ids;
+  d.u = teacher;
+  d.y = targets;
+  d.w = weight;
+  d.loss = loss;
+  d.k = k;
+  d.dtype = dtype;
+  d.tau = temperature;
+  d.alpha = alpha;
+  TJ2_TRY(hip_check(launch_distill(d, (hipStream_t)stream), "distillation launch"));
+  return ok();
+}
+
+}  // extern "C"

@@ -179,6 +179,40 @@ size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K);
 hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
                           hipStream_t s);
 
+// Cross entropy of X W^T (loss.hip): bf16 X [T, K] at pitch ldx, W [V, K] at ldw.
+struct CeParams {
+  const void* X;
+  const void* W;
+  const int64_t* y;
+  int64_t T, K, V, ldx, ldw, ignore;
+  float* loss;         // forward, optional
+  float* lse;          // forward: written; backward: read
+  const float* dloss;  // backward
+  void* dX;            // backward, each optional
+  void* dW;
+  int dx_dtype, dw_dtype;
+};
+size_t ce_fwd_workspace_bytes(int64_t T, int64_t V);
+hipError_t launch_ce_fwd(const CeParams& c, void* ws, hipStream_t s);
+size_t ce_bwd_workspace_bytes(int64_t T, int64_t K, int64_t V);
+hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s);
+
+// Distillation from a teacher's top logits (loss.hip).
+struct DistillParams {
+  const void* z;
+  void* dz;
+  int64_t ldz, ldd, T, V, ignore;
+  const int32_t* ids;
+  const void* u;
+  const int64_t* y;
+  const float* w;
+  float* loss;
+  int k, dtype;
+  float tau, alpha;
+};
+int distill_max_k();
+hipError_t launch_distill(const DistillParams& d, hipStream_t s);
+
 // OsciReset and the fused master-weight pass (AdamW, then OsciReset), on up to
 // kOsciMultiMax weight matrices per launch.  Parameters shared by the
 // matrices of a call:

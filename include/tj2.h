@@ -623,6 +623,66 @@ tj2_status mxfp4_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, con
                             float* dW, void* workspace, size_t ws_bytes, void* stream);
 size_t mxfp4_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
 
+/*
+ * Losses at the language-model head.
+ *
+ * Cross entropy of the logits z = X W^T, X [T, K] (tokens' final states) and W
+ * [V, K] (the head) bf16 with rows ldx and ldw elements apart (multiples of 8),
+ * against one target per token, without the logits in memory.  K a multiple of
+ * 16; T, V, K, ldx, ldw at most 2^21.
+ *
+ * tj2_linear_ce_fwd: lse[t] = log sum_v exp z[t, v] (fp32 [T], saved for the
+ * backward) and, if loss is not NULL, loss[t] = lse[t] - z[t, targets[t]] (fp32 [T]; 0
+ * where targets[t] == ignore_index; NaN where a target lies outside the
+ * vocabulary).  Logits are fp32 sums of exact products and are not rounded;
+ * probabilities below 2^-126 count as 0.
+ * workspace: tj2_linear_ce_fwd_workspace_size(T, K, V) bytes, 16-byte aligned,
+ * required.
+ */
+tj2_status tj2_linear_ce_fwd(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t T,
+                             int64_t K, int64_t V, int64_t ignore_index, float* loss, float* lse, void* workspace,
+                             size_t ws_bytes, void* stream);
+size_t tj2_linear_ce_fwd_workspace_size(int64_t T, int64_t K, int64_t V);
+
+/*
+ * tj2_linear_ce_bwd: with dloss [T] the gradient of each token's loss and
+ *   dz[t, v] = dloss[t] (exp(z[t, v] - lse[t]) - [v == targets[t]])
+ * (0 for an ignored token, whatever its logits; NaN for a target outside the
+ * vocabulary), dX [T, K] = dz W and dW [V, K] = dz^T X, contiguous, each TJ2_BF16
+ * or TJ2_F32, either may be NULL.  The vocabulary is taken in pieces; dz of a
+ * piece is rounded to bf16, divided by the largest |dloss|, for the two products,
+ * whose sums are fp32.  The results do not depend on scheduling.  workspace:
+ * tj2_linear_ce_bwd_workspace_size(T, K, V) bytes, 16-byte aligned, required.
+ */
+tj2_status tj2_linear_ce_bwd(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t T,
+                             int64_t K, int64_t V, int64_t ignore_index, const float* lse, const float* dloss, void* dX,
+                             int32_t dx_dtype, void* dW, int32_t dw_dtype, void* workspace, size_t ws_bytes, void* stream);
+size_t tj2_linear_ce_bwd_workspace_size(int64_t T, int64_t K, int64_t V);
+
+/*
+ * Distillation from a teacher's top logits.  logits [T, V] (dtype TJ2_BF16 or
+ * TJ2_F32, rows ldl elements apart, aligned to their elements); ids [T, k] the
+ * teacher's kept entries (a negative id stands for none, so rows may keep fewer
+ * than k; an entry listed twice counts twice) and teacher [T, k] their logits
+ * (dtype's type), 1 <= k <= 512.  With tau = temperature, p = softmax of the kept
+ * teacher logits / tau, q_tau = softmax(logits / tau) over the whole vocabulary:
+ *   loss[t]       = alpha tau^2 sum_j p_j (log p_j - log q_tau[id_j])
+ *                   + (1 - alpha) (-log q_1[targets[t]])
+ *   dlogits[t, v] = weight[t] (alpha tau (q_tau[v] - sum_{id_j = v} p_j)
+ *                   + (1 - alpha) (q_1[v] - [v == targets[t]]))
+ * loss (fp32 [T]) or dlogits (dtype, rows ldd apart; may be logits itself with ldd
+ * == ldl) may be NULL; weight (fp32 [T], NULL: 1) is the gradient of each token's
+ * loss.  targets may be NULL if alpha is 1; a token with targets[t] ==
+ * ignore_index has loss and gradient 0 whatever its logits.  A row of which the
+ * teacher kept nothing has no teacher's term.  An id of V or more, or a target
+ * outside the vocabulary that is used (alpha < 1), gives NaN.  Logits of -inf
+ * have probability 0.
+ */
+tj2_status tj2_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ldl, const int32_t* ids,
+                            const void* teacher, int32_t k, float temperature, float alpha, const int64_t* targets,
+                            int64_t ignore_index, const float* weight, float* loss, void* dlogits, int64_t ldd,
+                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif
