@@ -1219,7 +1219,7 @@ tj2_status check_ce_workspace(const void* ws, size_t ws_bytes, size_t need) {
 extern "C" {
 
 size_t tj2_linear_ce_fwd_workspace_size(int64_t T, int64_t K, int64_t V) {
-  return T <= 0 || K <= 0 || V <= 0 ? 0 : ce_fwd_workspace_bytes(T, V);
+  return T <= 0 || K <= 0 || V <= 0 ? 0 : ce_fwd_workspace_bytes(T, K, V);
 }
 
 tj2_status tj2_linear_ce_fwd(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t T,
@@ -1228,7 +1228,7 @@ tj2_status tj2_linear_ce_fwd(const void* X, int64_t ldx, const void* W, int64_t 
   TJ2_TRY(check_ce(X, ldx, W, ldw, targets, T, K, V));
   TJ2_TRY(check_f32(loss, "loss", false));
   TJ2_TRY(check_f32(lse, "lse", true));
-  TJ2_TRY(check_ce_workspace(workspace, ws_bytes, ce_fwd_workspace_bytes(T, V)));
+  TJ2_TRY(check_ce_workspace(workspace, ws_bytes, ce_fwd_workspace_bytes(T, K, V)));
   CeParams c = {};
   c.X = X;
   c.W = W;

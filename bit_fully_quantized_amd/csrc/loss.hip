@@ -29,18 +29,19 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // however large they are (a fused v c - m c is off by a half step of m c)
 __device__ __forceinline__ float exp_scaled(float v, float m, float c) { return __builtin_amdgcn_exp2f((v - m) * c); }
 
-// (m, s) of sum exp: s exp(m) in total; m = -inf stands for nothing
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-  const float M = fmaxf(m, m2);
-  const float b = M == -INFINITY ? 0.0f : M;
-  s = s * __builtin_amdgcn_exp2f((m - b) * kLog2e) + s2 * __builtin_amdgcn_exp2f((m2 - b) * kLog2e);
-  m = M;
+// (r, s): s 2^r in total; r = -inf stands for nothing
+__device__ __forceinline__ void join(float& r, float& s, float r2, float s2) {
+  const float R = fmaxf(r, r2);
+  const float b = R == -INFINITY ? 0.0f : R;
+  s = s * __builtin_amdgcn_exp2f(r - b) + s2 * __builtin_amdgcn_exp2f(r2 - b);
+  r = R;
 }
+
+constexpr float kNan = __builtin_nanf("");
 
 struct CeArgs {
   TileOp P, Q;                 // P: W [V, K] (or a piece of it), Q: X [T, K]
   const int64_t* y;
-  int64_t V, ignore;
   uint32_t tiles_p, tiles_q;
   int32_t nch;
   float2* part;                // forward: [parts][T]
@@ -49,52 +50,81 @@ struct CeArgs {
   const float* lse;
   const float* c;              // [T] weights over their largest magnitude, 0 where ignored
   int64_t v0;                  // first vocabulary entry of the piece
-  uint16_t* d;                 // dz of the piece [T][ldd]
-  uint16_t* dt;                // and transposed [piece rows][ldt]
-  int64_t ldd, ldt;
+  uint16_t* d;                 // dz of the piece [T, entries], blocked
+  uint16_t* dt;                // and transposed [entries, T], blocked
+  int32_t nd, nt;              // chunks of 64 entries and of 64 tokens in them, zero past the last one
 };
 
+// Logits of a tile reduced to one (r, s) per token and wave (16 TM entries), and the
+// targets' logits.  What is rare is asked for once a wave: entries past the
+// vocabulary's end, targets among the wave's entries, logits so large that a fused
+// v c - r (one instruction instead of two; r the rounded m c, so nothing but the
+// result is rounded) could overflow the exponential.
 template <class T>
 __global__ __launch_bounds__(T::NT, 1) void ce_fwd_kernel(CeArgs p) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
-  uint32_t tp, tq;
-  tile_of(blockIdx.x, gridDim.x, p.tiles_q, p.tiles_p, tq, tp);
-  const int64_t p0 = (int64_t)tp * T::BM, q0 = (int64_t)tq * T::BN;
-  typename T::Acc acc = {};
-  T::run(p.P, p0, p.Q, q0, 0, p.nch, sm, acc);
-
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-  const int wm = w / T::kWN;
-  const int64_t pw = p0 + wm * T::kTM * 16, qw = q0 + (w % T::kWN) * T::kTN * 16;
-  const int there = (int)min(p.P.rows - pw, (int64_t)(16 * T::kTM));  // vocabulary entries of this wave
-  const int left = there - g * 4 * T::PB;
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, 1);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+  T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t, typename T::Acc& acc) __attribute__((always_inline)) {
+    const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16, qw = q0 + (w % T::kWN) * T::kTN * 16;
+    const int there = (int)min(p.P.rows - pw, (int64_t)(16 * T::kTM));  // vocabulary entries of this wave
+    const int mine = g * 4 * T::PB;                                     // this lane's first
+    if (there < 16 * T::kTM) {
 #pragma unroll
-  for (int tn = 0; tn < T::kTN; ++tn) {
-    const int64_t t = qw + T::q_row(tn, n);
-    const bool in = t < p.Q.rows;
-    // the target's place among the wave's entries, -1: not among them
-    const int64_t yw = in ? p.y[t] - pw : -1;
-    const int y = yw >= 0 && yw < there ? (int)yw - g * 4 * T::PB : -1;
-    float m = -INFINITY;
+      for (int tm = 0; tm < T::kTM; ++tm)
 #pragma unroll
-    for (int tm = 0; tm < T::kTM; ++tm)
+        for (int r = 0; r < 4; ++r)
+          if (T::p_row(tm, 0, r) + mine >= there) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int v = T::p_row(tm, 0, r);
-        if (v >= left) acc[tm][tn][r] = -INFINITY;
-        else if (v == y) p.zt[t] = acc[tm][tn][r];
-        m = fmaxf(m, acc[tm][tn][r]);
+            for (int tn = 0; tn < T::kTN; ++tn) acc[tm][tn][r] = -INFINITY;
+          }
+    }
+    float2* part = p.part + pw / (16 * T::kTM) * p.Q.rows;
+#pragma unroll
+    for (int tn = 0; tn < T::kTN; ++tn) {
+      const int64_t t = qw + T::q_row(tn, n);
+      const bool in = t < p.Q.rows;
+      const int64_t yw = in ? p.y[t] - pw : -1;
+      const bool here = yw >= 0 && yw < there;
+      if (__any(here)) {
+        const int y = here ? (int)yw - mine : -1;
+        float z = 0.0f;
+        bool found = false;
+#pragma unroll
+        for (int tm = 0; tm < T::kTM; ++tm)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const bool is = T::p_row(tm, 0, r) == y;
+            z = is ? acc[tm][tn][r] : z;
+            found |= is;
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        if (found) p.zt[t] = z;
       }
-    const float b = m == -INFINITY ? 0.0f : m;
-    float s = 0.0f;
+      float m = -INFINITY;
 #pragma unroll
-    for (int tm = 0; tm < T::kTM; ++tm)
+      for (int tm = 0; tm < T::kTM; ++tm)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) s += exp_scaled(acc[tm][tn][r], b, kLog2e);
-    join(m, s, __shfl_xor(m, 16), __shfl_xor(s, 16));
-    join(m, s, __shfl_xor(m, 32), __shfl_xor(s, 32));
-    if (g == 0 && in) p.part[((int64_t)tp * (T::NT / 64 / T::kWN) + wm) * p.Q.rows + t] = float2{m, s};
-  }
+        for (int r = 0; r < 4; ++r) m = fmaxf(m, acc[tm][tn][r]);
+      float r = m * kLog2e, s = 0.0f;
+      const float b = m == -INFINITY ? 0.0f : r;
+      if (__any(fabsf(m) > 0x1p24f && m != -INFINITY)) {
+        const float mb = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int tm = 0; tm < T::kTM; ++tm)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s += exp_scaled(acc[tm][tn][k], mb, kLog2e);
+      } else {
+#pragma unroll
+        for (int tm = 0; tm < T::kTM; ++tm)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s += __builtin_amdgcn_exp2f(fmaf(acc[tm][tn][k], kLog2e, -b));
+      }
+      join(r, s, __shfl_xor(r, 16), __shfl_xor(s, 16));
+      join(r, s, __shfl_xor(r, 32), __shfl_xor(s, 32));
+      if (g == 0 && in) part[t] = float2{r, s};
+    }
+  });
 }
 
 // Token by token: the parts of its sum joined (four quarters of them at a time),
@@ -104,26 +134,26 @@ __global__ __launch_bounds__(256) void ce_join_kernel(const float2* part, int pa
   __shared__ float2 sh[4][64];
   const int l = threadIdx.x & 63, q = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * 64 + l;
-  float m = -INFINITY, s = 0.0f;
+  float r = -INFINITY, s = 0.0f;
   if (t < T) {
     const int a = (int)((int64_t)parts * q / 4), b = (int)((int64_t)parts * (q + 1) / 4);
     const float2* at = part + (int64_t)a * T + t;
 #pragma unroll 8
     for (int i = a; i < b; ++i, at += T) {
       const float2 v = *at;
-      join(m, s, v.x, v.y);
+      join(r, s, v.x, v.y);
     }
   }
-  sh[q][l] = float2{m, s};
+  sh[q][l] = float2{r, s};
   __syncthreads();
   if (q || t >= T) return;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) join(m, s, sh[i][l].x, sh[i][l].y);
-  const float e = m + __builtin_amdgcn_logf(s) * kLn2;
+  for (int i = 1; i < 4; ++i) join(r, s, sh[i][l].x, sh[i][l].y);
+  const float e = (r + __builtin_amdgcn_logf(s)) * kLn2;
   lse[t] = e;
   if (loss) {
     const int64_t k = y[t];
-    loss[t] = k == ignore ? 0.0f : (uint64_t)k < (uint64_t)V ? e - zt[t] : __uint_as_float(0x7FC00000u);
+    loss[t] = k == ignore ? 0.0f : (uint64_t)k < (uint64_t)V ? e - zt[t] : kNan;
   }
 }
 
@@ -145,74 +175,108 @@ __global__ __launch_bounds__(1024) void ce_weights_kernel(const float* w, const 
   if (m == 0.0f) m = 1.0f;
   for (int64_t t = threadIdx.x; t < T; t += 1024) {
     const int64_t k = y[t];
-    c[t] = k == ignore ? 0.0f : (uint64_t)k < (uint64_t)V ? w[t] / m : __uint_as_float(0x7FC00000u);
+    c[t] = k == ignore ? 0.0f : (uint64_t)k < (uint64_t)V ? w[t] / m : kNan;
   }
   if (threadIdx.x == 0) *top = m;
 }
 
+// dz of a tile in bf16, both ways.  The exponential is clamped to [0, 1], which costs
+// nothing (an output modifier) and holds where the fused v c - r overflows; it turns a
+// NaN into 0, so a token whose lse is NaN gets a NaN weight instead.
 template <class T>
 __global__ __launch_bounds__(T::NT, 1) void ce_dz_kernel(CeArgs p) {
+  static_assert(T::kTN == 4 && T::PB == 4, "64 tokens, and entries 16 a lane");
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
-  uint32_t tp, tq;
-  tile_of(blockIdx.x, gridDim.x, p.tiles_q, p.tiles_p, tq, tp);
-  const int64_t p0 = (int64_t)tp * T::BM, q0 = (int64_t)tq * T::BN;
-  typename T::Acc acc = {};
-  T::run(p.P, p0, p.Q, q0, 0, p.nch, sm, acc);
-
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-  const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16 + n * T::kTN;
-  const int64_t left = p.P.rows - pw;
-  float c[T::kTN], b[T::kTN];
-  int64_t y[T::kTN];
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, 1);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+  T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t, typename T::Acc& acc) __attribute__((always_inline)) {
+    const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16, qw = q0 + (w % T::kWN) * 64, t0 = qw + n * 4;
+    const int there = (int)min(p.P.rows - pw, (int64_t)(16 * T::kTM));
+    const int mine = g * 16;
+    float c[4], b[4];
+    int y[4];
+    bool any = false;
 #pragma unroll
-  for (int tn = 0; tn < T::kTN; ++tn) {
-    const bool in = qw + tn < p.Q.rows;
-    c[tn] = in ? p.c[qw + tn] : 0.0f;
-    b[tn] = in ? p.lse[qw + tn] : 0.0f;
-    y[tn] = in ? p.y[qw + tn] - p.v0 - pw : -1;
-  }
+    for (int tn = 0; tn < 4; ++tn) {
+      const bool in = t0 + tn < p.Q.rows;
+      const float l = in ? p.lse[t0 + tn] : 0.0f;
+      c[tn] = in ? p.c[t0 + tn] : 0.0f;
+      if (l != l && c[tn] != 0.0f) c[tn] = kNan;
+      b[tn] = l * kLog2e;
+      const int64_t yw = in ? p.y[t0 + tn] - p.v0 - pw : -1;
+      const bool here = yw >= 0 && yw < there;
+      y[tn] = here ? (int)yw - mine : -1;
+      any |= here;
+    }
 #pragma unroll
-  for (int tm = 0; tm < T::kTM; ++tm)
+    for (int tm = 0; tm < T::kTM; ++tm)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int v = T::p_row(tm, 0, r);
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int tn = 0; tn < T::kTN; ++tn) {
-        float e = exp_scaled(acc[tm][tn][r], b[tn], kLog2e);
-        e = c[tn] * (v == y[tn] ? e - 1.0f : e);
-        // an ignored token has no gradient, whatever its logits are
-        acc[tm][tn][r] = v < left && c[tn] != 0.0f ? e : 0.0f;
-      }
-      // four neighbouring tokens of one vocabulary entry
-      if (pw + v < p.ldd && qw < p.ldt) {
-        static_assert(T::kTN == 4, "four tokens a lane");
-        *reinterpret_cast<uint2*>(p.dt + (pw + v) * p.ldt + qw) =
-            uint2{bf16_pair(acc[tm][0][r], acc[tm][1][r]), bf16_pair(acc[tm][2][r], acc[tm][3][r])};
+        for (int tn = 0; tn < 4; ++tn)
+          acc[tm][tn][r] = c[tn] * __builtin_amdgcn_fmed3f(__builtin_amdgcn_exp2f(fmaf(acc[tm][tn][r], kLog2e, -b[tn])), 0.0f, 1.0f);
+    if (__any(any)) {
+#pragma unroll
+      for (int tm = 0; tm < T::kTM; ++tm) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int tn = 0; tn < 4; ++tn)
+            acc[tm][tn][r] = T::p_row(tm, 0, r) == y[tn] ? acc[tm][tn][r] - c[tn] : acc[tm][tn][r];
+        // (in this order: the compiler would first form all conditions, in more
+        // registers than there are)
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
-  // 4 PB neighbouring vocabulary entries of one token
+    if (there < 16 * T::kTM) {
 #pragma unroll
-  for (int tn = 0; tn < T::kTN; ++tn) {
-    if (qw + tn >= p.Q.rows) continue;
+      for (int tm = 0; tm < T::kTM; ++tm)
 #pragma unroll
-    for (int tb = 0; tb < T::kTM / T::PB; ++tb) {
-      const int64_t j = pw + tb * 16 * T::PB;
-      if (j >= p.ldd) continue;  // ldd is a multiple of 64
-      uint16_t* o = p.d + (qw + tn) * p.ldd + j;
+        for (int r = 0; r < 4; ++r)
+          if (T::p_row(tm, 0, r) + mine >= there) {
 #pragma unroll
-      for (int k = 0; k < T::PB; k += 2) {
-        const float4_t a = acc[tb * T::PB + k][tn], e = acc[tb * T::PB + k + 1][tn];
-        *reinterpret_cast<uint4*>(o + 4 * k) =
-            uint4{bf16_pair(a.x, a.y), bf16_pair(a.z, a.w), bf16_pair(e.x, e.y), bf16_pair(e.z, e.w)};
+            for (int tn = 0; tn < 4; ++tn) acc[tm][tn][r] = 0.0f;
+          }
+    }
+    // transposed: four neighbouring tokens of an entry, 128 bytes over 16 lanes
+    const int ct = (int)(qw >> 6);
+    if (ct < p.nt) {
+      uint16_t* dt = p.dt + ((pw >> 7) * p.nt + ct) * 8192 + ((pw & 127) + mine) * 64 + n * 4;
+      static_assert(16 * T::kTM <= 128 && 128 % (16 * T::kTM) == 0, "a wave's entries are of one block");
+#pragma unroll
+      for (int tm = 0; tm < T::kTM; ++tm)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (T::p_row(tm, 0, r) + mine < there)
+            *reinterpret_cast<uint2*>(dt + T::p_row(tm, 0, r) * 64) =
+                uint2{bf16_pair(acc[tm][0][r], acc[tm][1][r]), bf16_pair(acc[tm][2][r], acc[tm][3][r])};
+    }
+    // as it is: 16 neighbouring entries of a token
+#pragma unroll
+    for (int tn = 0; tn < 4; ++tn) {
+      const int64_t t = t0 + tn;
+      if (t >= p.Q.rows) continue;
+#pragma unroll
+      for (int tb = 0; tb < T::kTM / 4; ++tb) {
+        const int cd = (int)(pw >> 6) + tb;
+        if (cd >= p.nd) continue;
+        uint16_t* o = p.d + ((t >> 7) * p.nd + cd) * 8192 + (t & 127) * 64 + mine;
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          const float4_t a = acc[tb * 4 + k][tn], e = acc[tb * 4 + k + 1][tn];
+          *reinterpret_cast<uint4*>(o + 4 * k) =
+              uint4{bf16_pair(a.x, a.y), bf16_pair(a.z, a.w), bf16_pair(e.x, e.y), bf16_pair(e.z, e.w)};
+        }
       }
     }
-  }
+  });
 }
 
-// out[c][r] = in[r][c] for rows r < rows (zero up to ld) of a bf16 matrix with
-// `cols` (a multiple of 16) columns: 64 x 64 through LDS.
-__global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* in, int64_t rows, int64_t cols, int64_t ldi, uint16_t* out,
-                                                        int64_t ld) {
+// A bf16 matrix [rows, cols] (cols a multiple of 16) into blocked operands: `copy`
+// [rows, cols] and `turned` [cols, rows], zero up to whole chunks; either may be
+// NULL.  64 x 64 through LDS.
+__global__ __launch_bounds__(256) void block_kernel(const uint16_t* in, int64_t rows, int64_t cols, int64_t ldi, uint16_t* copy,
+                                                    uint16_t* turned) {
   __shared__ uint16_t tile[64][66];
   const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
   const int t = threadIdx.x;
@@ -221,9 +285,12 @@ __global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* in, int6
     const int r = i * 32 + (t >> 3), c = (t & 7) * 8;
     uint4 v = {0u, 0u, 0u, 0u};
     if (r0 + r < rows && c0 + c < cols) v = *reinterpret_cast<const uint4*>(in + (r0 + r) * ldi + c0 + c);
+    if (copy && r0 + r < rows)
+      *reinterpret_cast<uint4*>(copy + ((r0 >> 7) * gridDim.y + blockIdx.y) * 8192 + ((r0 & 127) + r) * 64 + c) = v;
     uint32_t* s = reinterpret_cast<uint32_t*>(&tile[r][c]);
     s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
   }
+  if (!turned) return;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -232,7 +299,8 @@ __global__ __launch_bounds__(256) void transpose_kernel(const uint16_t* in, int6
     uint32_t v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = tile[r + 2 * k][c] | ((uint32_t)tile[r + 2 * k + 1][c] << 16);
-    *reinterpret_cast<uint4*>(out + (c0 + c) * ld + r0 + r) = uint4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<uint4*>(turned + ((c0 >> 7) * gridDim.x + blockIdx.x) * 8192 + ((c0 & 127) + c) * 64 + r) =
+        uint4{v[0], v[1], v[2], v[3]};
   }
 }
 
@@ -253,15 +321,9 @@ struct ProductArgs {
 template <class T>
 __global__ __launch_bounds__(T::NT, 1) void ce_product_kernel(ProductArgs p) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
-  uint32_t tp, tq;
-  const uint32_t tiles = p.tiles_p * p.tiles_q, z = blockIdx.x / tiles;
-  tile_of(blockIdx.x - z * tiles, tiles, p.tiles_q, p.tiles_p, tq, tp);
-  const int64_t p0 = (int64_t)tp * T::BM, q0 = (int64_t)tq * T::BN;
-  const int c0 = (int)((int64_t)p.nch * z / p.splits), c1 = (int)((int64_t)p.nch * (z + 1) / p.splits);
-  typename T::Acc acc = {};
-  T::run(p.P, p0, p.Q, q0, c0, c1, sm, acc);
-
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t z, typename T::Acc& acc) __attribute__((always_inline)) {
   const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16 + n * T::kTN;
   const float scale = p.out ? *p.scale : 1.0f;
   float* sum = p.sum ? p.sum + (size_t)z * (size_t)p.Q.rows * (size_t)p.P.rows : nullptr;
@@ -299,6 +361,7 @@ __global__ __launch_bounds__(T::NT, 1) void ce_product_kernel(ProductArgs p) {
       }
     }
   }
+  });
 }
 
 // out = scale * (sum of `parts` fp32 slices), in order; 4 a thread (n a multiple of 16).
@@ -330,17 +393,32 @@ TileOp bf16_operand(const void* p, int64_t rows, int64_t cols, int64_t ld) {
   o.p = reinterpret_cast<const uint8_t*>(p);
   o.rows = rows;
   o.ld = ld * 2;
+  o.cs = 128;
+  o.bs = 128 * o.ld;
+  o.kb = (int32_t)(cols * 2);
+  return o;
+}
+
+// A workspace operand in blocks of 128 rows by 64 columns.
+TileOp blocked_operand(const void* p, int64_t rows, int64_t cols) {
+  TileOp o = {};
+  o.p = reinterpret_cast<const uint8_t*>(p);
+  o.rows = rows;
+  o.ld = 128;
+  o.cs = 128 * 128;
+  o.bs = (cols + 63) / 64 * o.cs;
   o.kb = (int32_t)(cols * 2);
   return o;
 }
 
 int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+size_t blocked_bytes(int64_t rows, int64_t cols) { return (size_t)(up(rows, 128) * up(cols, 64) * 2); }
 
-// Vocabulary entries of a piece of the backward (a multiple of 256): dz of the
-// piece, and its transpose, stay near the 256 MB of the memory-side cache.
+// Vocabulary entries of a piece of the backward (a multiple of 256): dz of a piece
+// has up to 2^28 elements.
 int64_t ce_piece(int64_t T, int64_t V) {
-  const int64_t most = ((int64_t)64 << 20) / std::max<int64_t>(up(T, 64), 1) / 256 * 256;
+  const int64_t most = ((int64_t)1 << 28) / std::max<int64_t>(up(T, 64), 1) / 256 * 256;
   return std::min(up(V, 256), std::max<int64_t>(most, 1024));
 }
 
@@ -349,54 +427,93 @@ int ce_splits(int64_t p_rows, int64_t q_rows, int64_t k) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(256 / tiles, nch / 8));
 }
 
+// Tokens from which the operands of the logits are copied into blocks first.
+constexpr int64_t kBlockTokens = 2048;
+
+struct CeFwdSpace {
+  size_t part, zt, xb, wb, bytes;
+  bool blocked;
+};
+CeFwdSpace ce_fwd_space(int64_t T, int64_t K, int64_t V) {
+  CeFwdSpace s;
+  size_t at = 0;
+  auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
+  s.blocked = T >= kBlockTokens;
+  s.part = take((size_t)(up(V, TileCe::BM) / 128) * (size_t)T * 8);
+  s.zt = take((size_t)T * 4);
+  s.xb = take(s.blocked ? blocked_bytes(T, K) : 0);
+  s.wb = take(s.blocked ? blocked_bytes(V, K) : 0);
+  s.bytes = at;
+  return s;
+}
+
 struct CeBwdSpace {
-  size_t c, top, xt, wt, d, dt, dx, part, bytes;
-  int64_t piece, ldd, ldt;
+  size_t c, top, xb, xt, wb, wt, d, dt, dx, part, bytes;
+  int64_t piece;
   int sx, sw;
+  bool blocked;
 };
 CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   CeBwdSpace s;
   s.piece = ce_piece(T, V);
-  s.ldd = s.piece;
-  s.ldt = up(T, 64);
   s.sx = ce_splits(K, T, s.piece);
   s.sw = ce_splits(K, s.piece, T);
+  s.blocked = T >= kBlockTokens;
   size_t at = 0;
   auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
   s.c = take((size_t)T * 4);
   s.top = take(4);
-  s.xt = take((size_t)(K * s.ldt * 2));
-  s.wt = take((size_t)(K * s.ldd * 2));
-  s.d = take((size_t)(T * s.ldd * 2));
-  s.dt = take((size_t)(s.ldd * s.ldt * 2));
+  s.xb = take(s.blocked ? blocked_bytes(T, K) : 0);
+  s.xt = take(blocked_bytes(K, T));
+  s.wb = take(s.blocked ? blocked_bytes(s.piece, K) : 0);
+  s.wt = take(blocked_bytes(K, s.piece));
+  s.d = take(blocked_bytes(T, s.piece));
+  s.dt = take(blocked_bytes(s.piece, T));
   s.dx = take((size_t)(T * K * 4));
   s.part = take(std::max(s.sx > 1 ? (size_t)s.sx * (size_t)(T * K * 4) : 0, s.sw > 1 ? (size_t)s.sw * (size_t)(s.piece * K * 4) : 0));
   s.bytes = at;
   return s;
 }
 
-}  // namespace
-
-size_t ce_fwd_workspace_bytes(int64_t T, int64_t V) {
-  const int64_t parts = up(V, TileCe::BM) / TileCe::BM * 2;
-  return up256((size_t)parts * (size_t)T * 8) + up256((size_t)T * 4);
+void launch_block(const void* in, int64_t rows, int64_t cols, int64_t ld, void* copy, void* turned, hipStream_t s) {
+  const dim3 grid((uint32_t)((rows + 63) / 64), (uint32_t)((cols + 63) / 64));
+  block_kernel<<<grid, 256, 0, s>>>(reinterpret_cast<const uint16_t*>(in), rows, cols, ld, reinterpret_cast<uint16_t*>(copy),
+                                    reinterpret_cast<uint16_t*>(turned));
 }
 
+}  // namespace
+
+size_t ce_fwd_workspace_bytes(int64_t T, int64_t K, int64_t V) { return ce_fwd_space(T, K, V).bytes; }
+
+#define TJ2_STEP()                                                      \
+  do {                                                                  \
+    if (hipError_t e_ = hipGetLastError(); e_ != hipSuccess) return e_; \
+  } while (0)
+
 hipError_t launch_ce_fwd(const CeParams& c, void* ws, hipStream_t s) {
+  const CeFwdSpace sp = ce_fwd_space(c.T, c.K, c.V);
+  uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   CeArgs a = {};
-  a.P = bf16_operand(c.W, c.V, c.K, c.ldw);
-  a.Q = bf16_operand(c.X, c.T, c.K, c.ldx);
+  if (sp.blocked) {
+    launch_block(c.W, c.V, c.K, c.ldw, w + sp.wb, nullptr, s);
+    TJ2_STEP();
+    launch_block(c.X, c.T, c.K, c.ldx, w + sp.xb, nullptr, s);
+    TJ2_STEP();
+    a.P = blocked_operand(w + sp.wb, c.V, c.K);
+    a.Q = blocked_operand(w + sp.xb, c.T, c.K);
+  } else {
+    a.P = bf16_operand(c.W, c.V, c.K, c.ldw);
+    a.Q = bf16_operand(c.X, c.T, c.K, c.ldx);
+  }
   a.y = c.y;
-  a.V = c.V;
-  a.ignore = c.ignore;
   a.tiles_p = (uint32_t)(up(c.V, TileCe::BM) / TileCe::BM);
   a.tiles_q = (uint32_t)(up(c.T, TileCe::BN) / TileCe::BN);
   a.nch = (int32_t)(up(c.K, 64) / 64);
-  const int parts = (int)a.tiles_p * 2;
-  a.part = reinterpret_cast<float2*>(ws);
-  a.zt = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ws) + up256((size_t)parts * (size_t)c.T * 8));
-  ce_fwd_kernel<TileCe><<<a.tiles_p * a.tiles_q, TileCe::NT, 0, s>>>(a);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  a.part = reinterpret_cast<float2*>(w + sp.part);
+  a.zt = reinterpret_cast<float*>(w + sp.zt);
+  ce_fwd_kernel<TileCe><<<tile_grid((uint64_t)a.tiles_p * a.tiles_q), TileCe::NT, 0, s>>>(a);
+  TJ2_STEP();
+  const int parts = (int)((c.V + 127) / 128);
   ce_join_kernel<<<(uint32_t)((c.T + 63) / 64), 256, 0, s>>>(a.part, parts, a.zt, c.y, c.T, c.V, c.ignore, c.loss, c.lse);
   return hipGetLastError();
 }
@@ -407,27 +524,20 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
   const CeBwdSpace sp = ce_bwd_space(c.T, c.K, c.V);
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   float* top = reinterpret_cast<float*>(w + sp.top);
-  uint16_t *xt = reinterpret_cast<uint16_t*>(w + sp.xt), *wt = reinterpret_cast<uint16_t*>(w + sp.wt);
-  uint16_t *d = reinterpret_cast<uint16_t*>(w + sp.d), *dt = reinterpret_cast<uint16_t*>(w + sp.dt);
   float *dx = reinterpret_cast<float*>(w + sp.dx), *part = reinterpret_cast<float*>(w + sp.part);
-#define TJ2_STEP()                                                    \
-  do {                                                                \
-    if (hipError_t e_ = hipGetLastError(); e_ != hipSuccess) return e_; \
-  } while (0)
   ce_weights_kernel<<<1, 1024, 0, s>>>(c.dloss, c.y, c.T, c.V, c.ignore, reinterpret_cast<float*>(w + sp.c), top);
   TJ2_STEP();
-  const uint32_t kt = (uint32_t)((c.K + 63) / 64);
-  transpose_kernel<<<dim3((uint32_t)(sp.ldt / 64), kt), 256, 0, s>>>(reinterpret_cast<const uint16_t*>(c.X), c.T, c.K, c.ldx, xt, sp.ldt);
+  launch_block(c.X, c.T, c.K, c.ldx, sp.blocked ? w + sp.xb : nullptr, w + sp.xt, s);
   TJ2_STEP();
   const bool one = sp.piece >= c.V;
   for (int64_t v0 = 0; v0 < c.V; v0 += sp.piece) {
-    const int64_t vn = std::min(sp.piece, c.V - v0), ldd = up(vn, 64);
+    const int64_t vn = std::min(sp.piece, c.V - v0);
     const uint16_t* W = reinterpret_cast<const uint16_t*>(c.W) + v0 * c.ldw;
-    transpose_kernel<<<dim3((uint32_t)(ldd / 64), kt), 256, 0, s>>>(W, vn, c.K, c.ldw, wt, ldd);
+    launch_block(W, vn, c.K, c.ldw, sp.blocked ? w + sp.wb : nullptr, w + sp.wt, s);
     TJ2_STEP();
     CeArgs a = {};
-    a.P = bf16_operand(W, vn, c.K, c.ldw);
-    a.Q = bf16_operand(c.X, c.T, c.K, c.ldx);
+    a.P = sp.blocked ? blocked_operand(w + sp.wb, vn, c.K) : bf16_operand(W, vn, c.K, c.ldw);
+    a.Q = sp.blocked ? blocked_operand(w + sp.xb, c.T, c.K) : bf16_operand(c.X, c.T, c.K, c.ldx);
     a.y = c.y;
     a.tiles_p = (uint32_t)(up(vn, TileCe::BM) / TileCe::BM);
     a.tiles_q = (uint32_t)(up(c.T, TileCe::BN) / TileCe::BN);
@@ -435,20 +545,20 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
     a.lse = c.lse;
     a.c = reinterpret_cast<float*>(w + sp.c);
     a.v0 = v0;
-    a.d = d;
-    a.dt = dt;
-    a.ldd = ldd;
-    a.ldt = sp.ldt;
-    ce_dz_kernel<TileCe><<<a.tiles_p * a.tiles_q, TileCe::NT, 0, s>>>(a);
+    a.d = reinterpret_cast<uint16_t*>(w + sp.d);
+    a.dt = reinterpret_cast<uint16_t*>(w + sp.dt);
+    a.nd = (int32_t)(up(vn, 64) / 64);
+    a.nt = (int32_t)(up(c.T, 64) / 64);
+    ce_dz_kernel<TileCe><<<tile_grid((uint64_t)a.tiles_p * a.tiles_q), TileCe::NT, 0, s>>>(a);
     TJ2_STEP();
     if (c.dX) {
       ProductArgs x = {};
-      x.P = bf16_operand(wt, c.K, ldd, ldd);
-      x.Q = bf16_operand(d, c.T, ldd, ldd);
+      x.P = blocked_operand(w + sp.wt, c.K, up(vn, 64));
+      x.Q = blocked_operand(w + sp.d, c.T, up(vn, 64));
       x.tiles_p = (uint32_t)(up(c.K, TileCe::BM) / TileCe::BM);
       x.tiles_q = a.tiles_q;
-      x.nch = (int32_t)(ldd / 64);
-      x.splits = std::min(sp.sx, std::max(1, x.nch));
+      x.nch = a.nd;
+      x.splits = std::min(sp.sx, x.nch);
       x.scale = top;
       x.bf16 = c.dx_dtype == TJ2_BF16;
       x.ldo = c.K;
@@ -456,7 +566,7 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
       if (x.splits > 1) x.sum = part;
       else if (one) x.out = c.dX;
       else x.sum = dx;
-      ce_product_kernel<TileCe><<<x.tiles_p * x.tiles_q * (uint32_t)x.splits, TileCe::NT, 0, s>>>(x);
+      ce_product_kernel<TileCe><<<tile_grid((uint64_t)x.tiles_p * x.tiles_q * (uint32_t)x.splits), TileCe::NT, 0, s>>>(x);
       TJ2_STEP();
       const int64_t n = c.T * c.K;
       const uint32_t grid = (uint32_t)((n / 4 + 255) / 256);
@@ -470,12 +580,12 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
     }
     if (c.dW) {
       ProductArgs x = {};
-      x.P = bf16_operand(xt, c.K, sp.ldt, sp.ldt);
-      x.Q = bf16_operand(dt, vn, sp.ldt, sp.ldt);
+      x.P = blocked_operand(w + sp.xt, c.K, up(c.T, 64));
+      x.Q = blocked_operand(w + sp.dt, vn, up(c.T, 64));
       x.tiles_p = (uint32_t)(up(c.K, TileCe::BM) / TileCe::BM);
       x.tiles_q = (uint32_t)(up(vn, TileCe::BN) / TileCe::BN);
-      x.nch = (int32_t)(sp.ldt / 64);
-      x.splits = std::min(sp.sw, std::max(1, x.nch));
+      x.nch = a.nt;
+      x.splits = std::min(sp.sw, x.nch);
       x.scale = top;
       x.bf16 = c.dw_dtype == TJ2_BF16;
       x.ldo = c.K;
@@ -483,16 +593,16 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
       uint8_t* out = reinterpret_cast<uint8_t*>(c.dW) + (size_t)(v0 * c.K) * (x.bf16 ? 2 : 4);
       if (x.splits > 1) x.sum = part;
       else x.out = out;
-      ce_product_kernel<TileCe><<<x.tiles_p * x.tiles_q * (uint32_t)x.splits, TileCe::NT, 0, s>>>(x);
+      ce_product_kernel<TileCe><<<tile_grid((uint64_t)x.tiles_p * x.tiles_q * (uint32_t)x.splits), TileCe::NT, 0, s>>>(x);
       TJ2_STEP();
       const int64_t n = vn * c.K;
       if (x.splits > 1) ce_sum_kernel<<<(uint32_t)((n / 4 + 255) / 256), 256, 0, s>>>(part, x.splits, n, top, out, x.bf16);
       TJ2_STEP();
     }
   }
-#undef TJ2_STEP
   return hipSuccess;
 }
+#undef TJ2_STEP
 
 // ---- distillation -------------------------------------------------------------------
 namespace {
@@ -647,7 +757,7 @@ __global__ __launch_bounds__(kDistillThreads) void distill_kernel(DistillArgs p)
   const float ze = edge ? to_f32<T>(z[ei]) : 0.0f;
   // read before anything is written: dz may be z
   float zy = 0.0f;
-  if constexpr (HARD) zy = (uint64_t)y < (uint64_t)V ? to_f32<T>(z[y]) : __uint_as_float(0x7FC00000u);
+  if constexpr (HARD) zy = (uint64_t)y < (uint64_t)V ? to_f32<T>(z[y]) : kNan;
 
   // the teacher's probabilities: softmax of its kept logits over tau
   const bool has_k = t < p.k;
@@ -689,7 +799,7 @@ __global__ __launch_bounds__(kDistillThreads) void distill_kernel(DistillArgs p)
   const float pt = some ? eu / su : 0.0f;
   const float lt = __builtin_amdgcn_logf(st) * kLn2;  // lse / tau - m / tau
   // an id outside the vocabulary makes the row NaN
-  const float wrong = kept && my >= V ? __uint_as_float(0x7FC00000u) : 0.0f;
+  const float wrong = kept && my >= V ? kNan : 0.0f;
   float kl = wrong;
   if (pt > 0.0f || pt != pt) kl += pt * ((u - mu) - __builtin_amdgcn_logf(su) * kLn2 - ((zi[t] - m) / p.tau - lt));
   kl = block_reduce(kl, sh, SumOp{});
@@ -700,7 +810,7 @@ __global__ __launch_bounds__(kDistillThreads) void distill_kernel(DistillArgs p)
 
   // dz = w (alpha tau (q_tau - p) + (1 - alpha)(q_1 - [target])): the softmax
   // parts everywhere, then the few entries with a teacher's or target's part
-  const float bad = loss != loss ? __uint_as_float(0x7FC00000u) : 0.0f;
+  const float bad = loss != loss ? kNan : 0.0f;
   const float at = some ? p.alpha * p.tau * w : 0.0f, gt = at / st + bad;
   const float a1 = (1.0f - p.alpha) * w, g1 = HARD ? a1 / s1 : 0.0f;
   auto grad = [&](float v) __attribute__((always_inline)) {

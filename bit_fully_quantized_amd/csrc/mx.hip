@@ -258,22 +258,23 @@ __global__ __launch_bounds__(256) void mx_values_kernel(const uint8_t* codes, co
 // ---- product ---------------------------------------------------------------------
 struct MxGemmArgs {
   TileOp P, Q;        // P: B [J, K] (columns of C), Q: A [I, K] (rows of C)
-  void* C;
-  int64_t ldc;
-  float* partial;     // [splits][I][J] when the reduction is split
+  void* C;            // split: fp32 partial sums [splits][I][J], joined by mx_join_kernel
+  int64_t ldc, zstride;
+  const float* partial;
   uint32_t tiles_p, tiles_q;
   int32_t nch, splits;
   int32_t bf16, accumulate, vec;  // vec: rows of C may be stored 16 bytes at a time
 };
 
-// N (a multiple of 4) neighbouring results of row i from column j on
+// N (a multiple of 4) neighbouring results from column j on of the row that starts
+// at element `row` of C
 template <int N>
-__device__ __forceinline__ void store_run(const MxGemmArgs& p, int64_t i, int64_t j, const float (&v)[N]) {
+__device__ __forceinline__ void store_run(const MxGemmArgs& p, int64_t row, int64_t j, const float (&v)[N]) {
   const int64_t J = p.P.rows;
   if (j >= J) return;
   const bool whole = p.vec && j + N <= J;
   if (p.bf16) {
-    uint16_t* o = reinterpret_cast<uint16_t*>(p.C) + i * p.ldc + j;
+    uint16_t* o = reinterpret_cast<uint16_t*>(p.C) + row + j;
     if (whole && N % 8 == 0) {
 #pragma unroll
       for (int k = 0; k + 8 <= N; k += 8)
@@ -285,7 +286,7 @@ __device__ __forceinline__ void store_run(const MxGemmArgs& p, int64_t i, int64_
         if (j + k < J) o[k] = (uint16_t)bf16_pair(v[k], 0.0f);
     }
   } else {
-    float* o = reinterpret_cast<float*>(p.C) + i * p.ldc + j;
+    float* o = reinterpret_cast<float*>(p.C) + row + j;
     if (whole) {
 #pragma unroll
       for (int k = 0; k < N; k += 4) {
@@ -307,38 +308,25 @@ __device__ __forceinline__ void store_run(const MxGemmArgs& p, int64_t i, int64_
 template <class T>
 __global__ __launch_bounds__(T::NT, 1) void mx_gemm_kernel(MxGemmArgs p) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
-  uint32_t tp, tq;
-  const uint32_t tiles = p.tiles_p * p.tiles_q;
-  const uint32_t z = blockIdx.x / tiles;
-  tile_of(blockIdx.x - z * tiles, tiles, p.tiles_q, p.tiles_p, tq, tp);
-  const int64_t p0 = (int64_t)tp * T::BM, q0 = (int64_t)tq * T::BN;
-  const int c0 = (int)((int64_t)p.nch * z / p.splits), c1 = (int)((int64_t)p.nch * (z + 1) / p.splits);
-  typename T::Acc acc = {};
-  T::run(p.P, p0, p.Q, q0, c0, c1, sm, acc);
-
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-  const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16;
-  MxGemmArgs o = p;
-  if (p.splits > 1) {
-    o.C = p.partial + (size_t)z * (size_t)p.Q.rows * (size_t)p.P.rows;
-    o.ldc = p.P.rows;
-    o.bf16 = 0;
-    o.accumulate = 0;
-    o.vec = (p.P.rows & 3) == 0;
-  }
+  T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t z, typename T::Acc& acc) __attribute__((always_inline)) {
+    const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16;
+    const int64_t at = p.zstride * z;
 #pragma unroll
-  for (int tn = 0; tn < T::kTN; ++tn) {
-    const int64_t i = qw + T::q_row(tn, n);
-    if (i < p.Q.rows) {
+    for (int tn = 0; tn < T::kTN; ++tn) {
+      const int64_t i = qw + T::q_row(tn, n);
+      if (i < p.Q.rows) {
 #pragma unroll
-      for (int tb = 0; tb < T::kTM / T::PB; ++tb) {
-        float v[4 * T::PB];
+        for (int tb = 0; tb < T::kTM / T::PB; ++tb) {
+          float v[4 * T::PB];
 #pragma unroll
-        for (int k = 0; k < 4 * T::PB; ++k) v[k] = acc[tb * T::PB + k / 4][tn][k % 4];
-        store_run<4 * T::PB>(o, i, pw + tb * 16 * T::PB, v);
+          for (int k = 0; k < 4 * T::PB; ++k) v[k] = acc[tb * T::PB + k / 4][tn][k % 4];
+          store_run<4 * T::PB>(p, at + i * p.ldc, pw + tb * 16 * T::PB, v);
+        }
       }
     }
-  }
+  });
 }
 
 // C = (C +) the sum of the splits' results in order, 4 a thread.
@@ -359,7 +347,7 @@ __global__ __launch_bounds__(256) void mx_join_kernel(MxGemmArgs p) {
       for (int k = 0; k < 4; ++k)
         if (j + k < J) v[k] += s[k];
   }
-  store_run<4>(p, i, j, v);
+  store_run<4>(p, i * p.ldc, j, v);
 }
 
 using TileBig = Tile<EL_MX, 2, 4, 8, 4>;
@@ -368,7 +356,7 @@ template <class T>
 hipError_t launch_tile(MxGemmArgs a, hipStream_t s) {
   a.tiles_p = (uint32_t)((a.P.rows + T::BM - 1) / T::BM);
   a.tiles_q = (uint32_t)((a.Q.rows + T::BN - 1) / T::BN);
-  mx_gemm_kernel<T><<<a.tiles_p * a.tiles_q * (uint32_t)a.splits, T::NT, 0, s>>>(a);
+  mx_gemm_kernel<T><<<tile_grid((uint64_t)a.tiles_p * a.tiles_q * (uint32_t)a.splits), T::NT, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -378,6 +366,8 @@ TileOp mx_operand(const QView& q) {
   o.s = q.s16;
   o.rows = q.rows;
   o.ld = q.nb * 64;
+  o.bs = 128 * o.ld;
+  o.cs = 128;
   o.lds = q.nb * 4;
   o.kb = (int32_t)(q.nb * 64);
   o.sb = (int32_t)(q.nb * 4);
@@ -412,8 +402,15 @@ hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, 
   a.vec = (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && (ldc * es) % 16 == 0;
   a.partial = partial;
   a.splits = partial ? mx_gemm_splits(A.rows, B.rows, A.len) : 1;
-  hipError_t e = launch_tile<TileBig>(a, s);
-  if (e != hipSuccess || a.splits == 1) return e;
+  if (a.splits == 1) return launch_tile<TileBig>(a, s);
+  MxGemmArgs part = a;
+  part.C = partial;
+  part.ldc = B.rows;
+  part.zstride = A.rows * B.rows;
+  part.bf16 = 0;
+  part.accumulate = 0;
+  part.vec = (B.rows & 3) == 0;
+  if (hipError_t e = launch_tile<TileBig>(part, s); e != hipSuccess) return e;
   const int64_t n = A.rows * ((B.rows + 3) / 4);
   mx_join_kernel<<<(uint32_t)((n + 255) / 256), 256, 0, s>>>(a);
   return hipGetLastError();

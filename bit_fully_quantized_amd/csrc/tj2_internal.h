@@ -192,7 +192,7 @@ struct CeParams {
   void* dW;
   int dx_dtype, dw_dtype;
 };
-size_t ce_fwd_workspace_bytes(int64_t T, int64_t V);
+size_t ce_fwd_workspace_bytes(int64_t T, int64_t K, int64_t V);
 hipError_t launch_ce_fwd(const CeParams& c, void* ws, hipStream_t s);
 size_t ce_bwd_workspace_bytes(int64_t T, int64_t K, int64_t V);
 hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s);

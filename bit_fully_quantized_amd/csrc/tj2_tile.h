@@ -9,6 +9,9 @@
 // and run in 16 cycles, so one loop serves both: a chunk is 128 bytes of every
 // row (64 bf16 or 256 E2M1), two instruction steps.
 //
+// Workgroups go to the 8 XCDs in turn, each with its own L2, so an XCD takes a
+// contiguous range of the tiles.
+//
 // Work of a workgroup: BM = 16 WM TM rows of P by BN = 16 WN TN rows of Q; wave
 // (wm, wn) owns 16 TM by 16 TN of it in registers.  P is the side whose rows are
 // contiguous in the output, so a lane's four results of one instruction lie next
@@ -22,8 +25,8 @@
 // operand's end and 16-byte pieces past the row's end get an offset beyond the
 // buffer's size).  Such a load writes lane after lane, so a row's eight pieces
 // are permuted by permuting what each lane fetches: piece g of row r sits in slot
-// g ^ key(r), with key so chosen that 8 lanes reading the same piece of their
-// tile's rows touch all 32 banks once.
+// g ^ key(r), with key so chosen that 16 lanes reading the same piece of their
+// tile's rows touch all 64 banks once.
 //
 // One barrier a chunk, placed between its two steps: the loads of the next chunk
 // were issued a whole chunk earlier and must have landed, every wave has read
@@ -36,6 +39,7 @@
 namespace tj2 {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -49,20 +53,26 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2v_t{a, b}, bf16x2v_t));
 }
 
-// An operand of a tile product: rows of `kb` bytes (a multiple of 16) at a pitch
-// of `ld` bytes; MXFP4: `sb` scale bytes (a multiple of 4) per row at a pitch of
-// `lds` bytes.
+// An operand of a tile product: rows of `kb` bytes (a multiple of 16).  Row r's
+// bytes [128 c, 128 c + 128) start at (r / 128) bs + (r % 128) ld + c cs:
+//   row-major:  ld the pitch, cs 128, bs 128 ld;
+//   blocked:    ld 128, cs the 16 KB of 128 rows' chunk, bs all chunks of 128 rows,
+// the latter for operands that a pass of this library writes: a chunk of a tile is
+// contiguous, where a long pitch spreads its rows over as many pages and, if it is a
+// power of two, over few memory channels.  MXFP4: `sb` scale bytes (a multiple of 4)
+// per row at a pitch of `lds` bytes, the same for both operands.
 struct TileOp {
   const uint8_t* p;
   const uint8_t* s;
-  int64_t rows, ld, lds;
-  int32_t kb, sb;
+  int64_t rows, ld, bs, lds;
+  int32_t kb, sb, cs;
 };
 
 constexpr uint32_t kOutside = 0x80000000u;  // lane offset beyond every buffer below
 
 // Raw buffer at `base` (same for all lanes) of 2^31 - 1 bytes: lane offsets of
-// kOutside and above read zero; the others are the caller's to keep in range.
+// kOutside and above read zero (with or without the scalar offset, which is below
+// 2^31); the others are the caller's to keep in range.
 __device__ __forceinline__ u32x4_t raw_buffer(const uint8_t* base) {
   const uint64_t a = (uint64_t)(uintptr_t)base;
   u32x4_t d;
@@ -78,27 +88,27 @@ __device__ __forceinline__ u32x4_t raw_buffer(const uint8_t* base) {
 // compiler does not pad.
 __device__ __forceinline__ void settle(u32x4_t& a, u32x4_t& b) { asm volatile("s_nop 4" : "+s"(a), "+s"(b)); }
 
-// 16 (or 4) bytes per lane from buffer d at lane offset v into LDS at byte
+// 16 (or 4) bytes per lane from buffer d at lane offset v + s into LDS at byte
 // address m (of the wave's first lane), lane after lane.  In assembly because
 // the compiler's own form waits for every such load before the next LDS read;
 // here the chunk's barrier carries the wait.  m0, which holds the LDS address, is
 // left changed: nothing else in these kernels reads it.
-__device__ __forceinline__ void load_lds16(u32x4_t d, uint32_t v, uint32_t m) {
+__device__ __forceinline__ void load_lds16(u32x4_t d, uint32_t v, uint32_t s, uint32_t m) {
   asm volatile(
-      "s_mov_b32 m0, %2\n\t"
+      "s_mov_b32 m0, %3\n\t"
       "s_nop 0\n\t"
-      "buffer_load_dwordx4 %0, %1, 0 offen lds"
+      "buffer_load_dwordx4 %0, %1, %2 offen lds"
       :
-      : "v"(v), "s"(d), "s"(m)
+      : "v"(v), "s"(d), "s"(s), "s"(m)
       : "memory");
 }
-__device__ __forceinline__ void load_lds4(u32x4_t d, uint32_t v, uint32_t m) {
+__device__ __forceinline__ void load_lds4(u32x4_t d, uint32_t v, uint32_t s, uint32_t m) {
   asm volatile(
-      "s_mov_b32 m0, %2\n\t"
+      "s_mov_b32 m0, %3\n\t"
       "s_nop 0\n\t"
-      "buffer_load_dword %0, %1, 0 offen lds"
+      "buffer_load_dword %0, %1, %2 offen lds"
       :
-      : "v"(v), "s"(d), "s"(m)
+      : "v"(v), "s"(d), "s"(s), "s"(m)
       : "memory");
 }
 
@@ -117,6 +127,20 @@ __device__ __forceinline__ void tile_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// Tile number -> (tm, tn): in groups of 8 along the first axis, that axis fastest,
+// so that neighbours share few row blocks of both operands.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
+  const uint32_t group = 8 * tiles_n, gi = id / group, first = gi * 8;
+  const uint32_t rows = min(tiles_m - first, 8u), in = id - gi * group;
+  tm = __builtin_amdgcn_readfirstlane(first + in % rows);
+  tn = __builtin_amdgcn_readfirstlane(in / rows);
+}
+
+// Workgroups of a launch over `items` tiles: one a CU (their LDS fills it), each
+// going on to further tiles by itself.
+constexpr uint32_t kTileGrid = 256;
+inline uint32_t tile_grid(uint64_t items) { return (uint32_t)(items < kTileGrid ? items : kTileGrid); }
+
 template <int EL, int WM, int WN, int TM, int TN>
 struct Tile {
   static constexpr int kWN = WN, kTM = TM, kTN = TN;
@@ -128,7 +152,8 @@ struct Tile {
   static constexpr int LP = BM / RPI, LQ = BN / RPI;
   static constexpr int SCALE_DW = EL == EL_MX ? ROWS * 2 : 0;  // scale words of a chunk
   static_assert(BM % RPI == 0 && BN % RPI == 0, "whole load instructions");
-  static_assert(8 * PB <= RPI && 8 * TN <= RPI, "a thread's key is the same in all its rows");
+  static_assert(RPI % (16 * PB) == 0 && RPI % (16 * TN) == 0, "a thread's key is the same in all its rows");
+  static_assert(TN == 1 || TN % 2 == 0, "q_place pairs rows");
   static_assert(TM % PB == 0, "whole row blocks");
 
   struct Smem {
@@ -144,27 +169,72 @@ struct Tile {
   }
   // row of the wave's Q rows that lane n (0..15) of tile tn holds
   static __device__ __forceinline__ constexpr int q_row(int tn, int n) { return n * TN + tn; }
-  static __device__ __forceinline__ constexpr int p_key(int row) { return (row & 3) | (((row / (4 * PB)) & 1) << 2); }
-  static __device__ __forceinline__ constexpr int q_key(int row) { return (row / TN) & 7; }
+  // A read of 16 lanes takes one pass if they touch all 64 banks (256 bytes) once.
+  // P: rows of one tile differ in their low two bits and in row / (4 PB), of which
+  // the lowest picks the half of 256 bytes by itself.  Q: rows of one tile are TN
+  // apart, so for even TN every other of them trades places with its neighbour.
+  static __device__ __forceinline__ constexpr int p_key(int row) { return ((row >> 1) & 1) | (((row / (4 * PB)) & 3) << 1); }
+  static __device__ __forceinline__ constexpr int q_key(int row) { return (row / (2 * TN)) & 7; }
+  static __device__ __forceinline__ constexpr int q_place(int row) { return TN % 2 ? row : row ^ ((row / TN) & 1); }
 
-  // Chunks [c0, c1) of the product of P rows p0.. and Q rows q0.., added to acc.
-  // Every thread of the workgroup calls it with the same arguments.
-  static __device__ __forceinline__ void run(const TileOp& P, int64_t p0, const TileOp& Q, int64_t q0, int c0, int c1,
-                                             Smem& sm, Acc& acc) {
+  // The launch's tiles (times the splits of their reduction) in the order of
+  // tile_of; a workgroup takes every step-th of its XCD's range.
+  struct Items {
+    uint32_t tiles_p, tiles_q, nch, splits;
+    uint32_t at, end, step;
+    __device__ __forceinline__ Items(uint32_t tp, uint32_t tq, uint32_t chunks, uint32_t z)
+        : tiles_p(tp), tiles_q(tq), nch(chunks), splits(z) {
+      const uint32_t total = tp * tq * z, n = gridDim.x, b = blockIdx.x;
+      if (n < 8) {
+        at = b;
+        end = total;
+        step = n;
+      } else {
+        const uint32_t x = b % 8, lo = (uint32_t)((uint64_t)total * x / 8);
+        at = lo + b / 8;
+        end = (uint32_t)((uint64_t)total * (x + 1) / 8);
+        step = (n - x + 7) / 8;
+      }
+    }
+  };
+  struct Item {
+    uint32_t tp, tq, z;
+    int c, c1;
+    __device__ __forceinline__ void set(const Items& s, uint32_t at) {
+      const uint32_t tiles = s.tiles_p * s.tiles_q;
+      z = __builtin_amdgcn_readfirstlane(at / tiles);
+      tile_of(at - z * tiles, s.tiles_q, s.tiles_p, tq, tp);
+      c = __builtin_amdgcn_readfirstlane((int)(s.nch * z / s.splits));
+      c1 = __builtin_amdgcn_readfirstlane((int)(s.nch * (z + 1) / s.splits));
+    }
+  };
+
+  // All items of this workgroup as one sequence of chunks: the loads run two chunks
+  // ahead, across the items' borders, so that an item's first chunks arrive while
+  // the last one's results are stored.  epilogue(p0, q0, z, acc) takes an item's sums.
+  template <class Epilogue>
+  static __device__ __forceinline__ void run(const TileOp& P, const TileOp& Q, const Items& items, Smem& sm,
+                                             Epilogue&& epilogue) {
+    if (items.at >= items.end) return;
     const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = w / WN, wn = w % WN, n = lane & 15, g = lane >> 4;
+    Acc acc = {};
+    Item now;
+    now.set(items, items.at);
 
     // what this thread loads: row i * RPI + t / 8, slot t % 8
     const int lr = t >> 3;
-    const int np = (int)min(P.rows - p0, (int64_t)BM), nq = (int)min(Q.rows - q0, (int64_t)BN);
     const uint32_t gp = (uint32_t)((t & 7) ^ p_key(lr)) * 16, gq = (uint32_t)((t & 7) ^ q_key(lr)) * 16;
-    uint32_t vp[LP], vq[LQ];
-#pragma unroll
-    for (int i = 0; i < LP; ++i) vp[i] = i * RPI + lr < np ? (uint32_t)(i * RPI + lr) * (uint32_t)P.ld + gp : kOutside;
-#pragma unroll
-    for (int i = 0; i < LQ; ++i) vq[i] = i * RPI + lr < nq ? (uint32_t)(i * RPI + lr) * (uint32_t)Q.ld + gq : kOutside;
-    const uint8_t* pb = P.p + p0 * P.ld;
-    const uint8_t* qb = Q.p + q0 * Q.ld;
+    const int lrq = q_place(lr);
+    const uint32_t vp = (uint32_t)lr * (uint32_t)P.ld + gp, vq = (uint32_t)lrq * (uint32_t)Q.ld + gq;
+    // and the uniform offset of its row i * RPI
+    static_assert(128 % RPI == 0 && (BM < 128 || BM % 128 == 0) && (BN < 128 || BN % 128 == 0), "rows of a block");
+    auto far_p = [&](int i) __attribute__((always_inline)) {
+      return (uint32_t)(i * RPI / 128) * (uint32_t)P.bs + (uint32_t)(i * RPI % 128) * (uint32_t)P.ld;
+    };
+    auto far_q = [&](int i) __attribute__((always_inline)) {
+      return (uint32_t)(i * RPI / 128) * (uint32_t)Q.bs + (uint32_t)(i * RPI % 128) * (uint32_t)Q.ld;
+    };
     const uint32_t lds_w = lds_address(sm.stage[0]) + (uint32_t)w * 1024u;
     constexpr uint32_t kStage = ROWS * 128;
 
@@ -172,44 +242,76 @@ struct Tile {
     // of Q: BM is a multiple of 32)
     constexpr int SJ = EL == EL_MX ? SCALE_DW / NT : 1;
     static_assert(SCALE_DW % NT == 0 && BM % 32 == 0, "whole scale loads");
-    uint32_t vs[SJ];
-    if constexpr (EL == EL_MX) {
-#pragma unroll
-      for (int j = 0; j < SJ; ++j) {
-        const int r0 = w * 32 + j * (NT / 2), r = r0 + (lane >> 1);
-        const bool isp = r0 < BM;
-        const uint32_t pitch = (uint32_t)(isp ? P.lds : Q.lds);
-        vs[j] = (isp ? r < np : r - BM < nq) ? (uint32_t)(isp ? r : r - BM) * pitch + (lane & 1) * 4 : kOutside;
-      }
-    }
+    const uint32_t vs = (uint32_t)(lane >> 1) * (uint32_t)P.lds + (lane & 1) * 4;  // P and Q have the same pitch
 
-    auto load = [&](int c, uint32_t stage) __attribute__((always_inline)) {
-      const uint32_t at = (uint32_t)c * 128u;
-      u32x4_t dp = raw_buffer(pb + at), dq = raw_buffer(qb + at);
-      settle(dp, dq);
-      const uint32_t badp = at + gp >= (uint32_t)P.kb ? kOutside : 0u;
-      const uint32_t badq = at + gq >= (uint32_t)Q.kb ? kOutside : 0u;
-      const uint32_t dst = lds_w + stage * kStage;
-#pragma unroll
-      for (int i = 0; i < LP; ++i) load_lds16(dp, vp[i] | badp, dst + i * (RPI * 128));
-#pragma unroll
-      for (int i = 0; i < LQ; ++i) load_lds16(dq, vq[i] | badq, dst + (LP + i) * (RPI * 128));
+    // The load cursor: its item and the item's rows (none once the items are done).
+    Item ahead = now;
+    uint32_t ahead_at = items.at;
+    const uint8_t *pb, *qb, *psb = nullptr, *qsb = nullptr;
+    int np, nq;
+    auto enter = [&]() __attribute__((always_inline)) {
+      const int64_t p0 = (int64_t)ahead.tp * BM, q0 = (int64_t)ahead.tq * BN;
+      pb = P.p + (p0 >> 7) * P.bs + (p0 & 127) * P.ld;
+      qb = Q.p + (q0 >> 7) * Q.bs + (q0 & 127) * Q.ld;
       if constexpr (EL == EL_MX) {
-        const uint32_t ats = (uint32_t)c * 8u;
-        u32x4_t sp = raw_buffer(P.s + p0 * P.lds + ats), sq = raw_buffer(Q.s + q0 * Q.lds + ats);
-        settle(sp, sq);
-        const uint32_t bad = ats + (lane & 1) * 4 >= (uint32_t)P.sb ? kOutside : 0u;
-        const uint32_t sd = lds_address(sm.scale[0]) + stage * (SCALE_DW * 4) + (uint32_t)w * 256u;
-#pragma unroll
-        for (int j = 0; j < SJ; ++j) {
-          const bool isp = w * 32 + j * (NT / 2) < BM;
-          u32x4_t d;
-          d.x = isp ? sp.x : sq.x;
-          d.y = isp ? sp.y : sq.y;
-          d.z = sp.z;
-          d.w = sp.w;
-          load_lds4(d, vs[j] | bad, sd + j * (NT * 4));
+        psb = P.s + p0 * P.lds;
+        qsb = Q.s + q0 * Q.lds;
+      }
+      np = __builtin_amdgcn_readfirstlane((int)min(P.rows - p0, (int64_t)BM));
+      nq = __builtin_amdgcn_readfirstlane((int)min(Q.rows - q0, (int64_t)BN));
+    };
+    enter();
+    // The loads of the cursor's chunk into `stage`, one at a time: begin() sets them up.
+    u32x4_t dp, dq, dsp, dsq;
+    uint32_t badp, badq, bads = 0, dst = 0, sdst = 0;
+    auto begin = [&](uint32_t stage) __attribute__((always_inline)) {
+      const uint32_t at = (uint32_t)ahead.c * 128u;
+      dp = raw_buffer(pb + mul32(ahead.c, P.cs));
+      dq = raw_buffer(qb + mul32(ahead.c, Q.cs));
+      settle(dp, dq);
+      badp = at + gp >= (uint32_t)P.kb ? kOutside : 0u;
+      badq = at + gq >= (uint32_t)Q.kb ? kOutside : 0u;
+      dst = lds_w + stage * kStage;
+      if constexpr (EL == EL_MX) {
+        const uint32_t ats = (uint32_t)ahead.c * 8u;
+        dsp = raw_buffer(psb + ats);
+        dsq = raw_buffer(qsb + ats);
+        settle(dsp, dsq);
+        bads = ats + (lane & 1) * 4 >= (uint32_t)P.sb ? kOutside : 0u;
+        sdst = lds_address(sm.scale[0]) + stage * (SCALE_DW * 4) + (uint32_t)w * 256u;
+      }
+    };
+    // after the chunk's last load: on to the next one
+    auto advance = [&]() __attribute__((always_inline)) {
+      if (++ahead.c == ahead.c1) {
+        ahead_at += items.step;
+        if (ahead_at < items.end) {
+          ahead.set(items, ahead_at);
+          enter();
+        } else {
+          np = nq = 0;
+          ahead.c = 0;
+          ahead.c1 = 1 << 30;
         }
+      }
+    };
+    constexpr int LOADS = LP + LQ + (EL == EL_MX ? SJ : 0);
+    auto load = [&](int i) __attribute__((always_inline)) {
+      if (i < LP) {
+        load_lds16(dp, lr < np - i * RPI ? vp | badp : kOutside, far_p(i), dst + i * (RPI * 128));
+      } else if (i < LP + LQ) {
+        load_lds16(dq, lrq < nq - (i - LP) * RPI ? vq | badq : kOutside, far_q(i - LP), dst + i * (RPI * 128));
+      } else if constexpr (EL == EL_MX) {
+        const int j = i - LP - LQ, r0 = w * 32 + j * (NT / 2);
+        const bool isp = r0 < BM;
+        const int first = isp ? r0 : r0 - BM;
+        u32x4_t d;
+        d.x = isp ? dsp.x : dsq.x;
+        d.y = isp ? dsp.y : dsq.y;
+        d.z = dsp.z;
+        d.w = dsp.w;
+        load_lds4(d, (lane >> 1) < (isp ? np : nq) - first ? vs | bads : kOutside, (uint32_t)first * (uint32_t)P.lds,
+                  sdst + j * (NT * 4));
       }
     };
 
@@ -217,116 +319,142 @@ struct Tile {
     // kept once: those of the next step are read into a tile's registers as soon
     // as its instructions have issued.  Q's, which every tile needs, twice.
     i32x4_t fp[TM], fq[2][TN];
-    uint32_t sp[TM], sq[TN], sqn[TN];
+    // scale bytes of both steps, two tiles a register
+    constexpr int NSP = (TM + 1) / 2, NSQ = (TN + 1) / 2;
+    u16x2_t sp[NSP], sq[NSQ], sqn[NSQ];
     const int pr0 = wm * TM * 16, qr0 = BM + wn * TN * 16;
-    const int pk = p_key((n >> 2) * 4 * PB + (n & 3)), qk = q_key(n * TN);
+    const int pk = p_key(p_row(0, n >> 2, n & 3)), qk = q_key(q_row(0, n));
     // LDS byte addresses; the two steps' pieces are neighbours, 16 bytes apart
     const uint32_t lp = lds_address(sm.stage[0]) + (uint32_t)(pr0 + p_row(0, n >> 2, n & 3)) * 128u + ((2 * g) ^ pk) * 16;
-    const uint32_t lq = lds_address(sm.stage[0]) + (uint32_t)(qr0 + q_row(0, n)) * 128u + ((2 * g) ^ qk) * 16;
+    // even and odd tiles of Q: a lane's rows trade places in pairs
+    const uint32_t lq0 = lds_address(sm.stage[0]) + (uint32_t)(qr0 + q_place(q_row(0, n))) * 128u + ((2 * g) ^ qk) * 16;
+    const uint32_t lq1 = lds_address(sm.stage[0]) + (uint32_t)(qr0 + q_place(q_row(TN > 1 ? 1 : 0, n))) * 128u + ((2 * g) ^ qk) * 16;
     const uint32_t lsp = lds_address(sm.scale[0]) + (uint32_t)(pr0 + p_row(0, n >> 2, n & 3)) * 8u + 2 * g;
     const uint32_t lsq = lds_address(sm.scale[0]) + (uint32_t)(qr0 + q_row(0, n)) * 8u + 2 * g;
     auto read_p = [&](uint32_t stage, int s, int tm) __attribute__((always_inline)) {
       fp[tm] = lds_read<i32x4_t>(((lp ^ (s * 16)) + stage * kStage) + p_row(tm, 0, 0) * 128);
     };
     auto read_q = [&](uint32_t stage, int s, int tn) __attribute__((always_inline)) {
-      fq[s][tn] = lds_read<i32x4_t>(((lq ^ (s * 16)) + stage * kStage) + q_row(tn, 0) * 128);
+      fq[s][tn] = lds_read<i32x4_t>((((tn & 1 ? lq1 : lq0) ^ (s * 16)) + stage * kStage) + (tn & ~1) * 128);
     };
     auto read_sp = [&](uint32_t stage, int tm) __attribute__((always_inline)) {
-      if constexpr (EL == EL_MX) sp[tm] = lds_read<uint16_t>(lsp + stage * (SCALE_DW * 4) + p_row(tm, 0, 0) * 8);
+      if constexpr (EL == EL_MX) sp[tm / 2][tm % 2] = lds_read<uint16_t>(lsp + stage * (SCALE_DW * 4) + p_row(tm, 0, 0) * 8);
     };
     auto read_sq = [&](uint32_t stage, int tn) __attribute__((always_inline)) {
-      if constexpr (EL == EL_MX) sqn[tn] = lds_read<uint16_t>(lsq + stage * (SCALE_DW * 4) + q_row(tn, 0) * 8);
+      if constexpr (EL == EL_MX) sqn[tn / 2][tn % 2] = lds_read<uint16_t>(lsq + stage * (SCALE_DW * 4) + q_row(tn, 0) * 8);
     };
-    auto mma = [&](auto sc, int tm) __attribute__((always_inline)) {
-      constexpr int s = decltype(sc)::value;
-#pragma unroll
-      for (int tn = 0; tn < TN; ++tn) {
+    auto mma = [&](auto sc, auto tmc) __attribute__((always_inline)) {
+      constexpr int s = decltype(sc)::value, tm = decltype(tmc)::value;
+      static_for<TN>([&](auto tnc) __attribute__((always_inline)) {
+        constexpr int tn = decltype(tnc)::value;
         if constexpr (EL == EL_BF16) {
           acc[tm][tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, fp[tm]),
                                                                 __builtin_bit_cast(bf16x8_t, fq[s][tn]), acc[tm][tn], 0, 0, 0);
         } else {
           const i32x8_t a = __builtin_shufflevector(fp[tm], i32x4_t{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
           const i32x8_t b = __builtin_shufflevector(fq[s][tn], i32x4_t{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
-          acc[tm][tn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[tm][tn], 4, 4, s, (int)sp[tm], s, (int)sq[tn]);
+          acc[tm][tn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              a, b, acc[tm][tn], 4, 4, s + 2 * (tm % 2), __builtin_bit_cast(int, sp[tm / 2]), s + 2 * (tn % 2),
+              __builtin_bit_cast(int, sq[tn / 2]));
         }
-      }
+      });
     };
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
     // the tiles of the second step before which the barrier is crossed
     constexpr int LEAD = TM >= 4 ? 2 : 1;
-    load(c0, 0);
+    // loads are dealt out over the instruction tiles, so that no burst of them keeps
+    // the waves from issuing: LATE of them are left for the next chunk's first step
+    constexpr int SLOTS = TM - LEAD, EARLY = (LOADS + SLOTS - 1) / SLOTS <= 1 ? LOADS : SLOTS;
+    constexpr int LATE = LOADS > EARLY ? LOADS - EARLY : 0;
+    begin(0);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) load(i);
+    advance();
     tile_barrier();
-    load(c0 + 1, 1);
+    begin(1);
 #pragma unroll
-    for (int tn = 0; tn < TN; ++tn) {
-      read_q(0, 0, tn);
-      read_sq(0, tn);
-    }
+    for (int i = 0; i < LOADS - LATE; ++i) load(i);
+    // Every chunk runs the same straight line: past the last item the loads bring
+    // zeros, and the fragments read then are not used.
+    uint32_t st = 0, at = items.at;
+    for (;;) {
+      // the item's first fragments (read again after an epilogue, which has the
+      // registers to itself)
 #pragma unroll
-    for (int tm = 0; tm < TM; ++tm) {
-      read_p(0, 0, tm);
-      read_sp(0, tm);
-    }
-#pragma unroll
-    for (int tn = 0; tn < TN; ++tn) sq[tn] = sqn[tn];
-    // Every chunk runs the same straight line: past the last one the loads bring
-    // zeros (or the next split's chunks) and the fragments read then are not used.
-    uint32_t st = 0;
-#pragma nounroll
-    for (int c = c0; c < c1; ++c) {
-#pragma unroll
-      for (int tn = 0; tn < TN; ++tn) read_q(st, 1, tn);
-#pragma unroll
-      for (int tm = 0; tm < TM; ++tm) {
-        mma(S0{}, tm);
-        __builtin_amdgcn_sched_barrier(0);
-        read_p(st, 1, tm);
+      for (int tn = 0; tn < TN; ++tn) {
+        read_q(st, 0, tn);
+        read_sq(st, tn);
       }
 #pragma unroll
       for (int tm = 0; tm < TM; ++tm) {
-        mma(S1{}, tm);
-        __builtin_amdgcn_sched_barrier(0);
-        if (tm == LEAD - 1) {
-          tile_barrier();
-          load(c + 2, st);
-#pragma unroll
-          for (int tn = 0; tn < TN; ++tn) {
-            read_q(st ^ 1u, 0, tn);
-            read_sq(st ^ 1u, tn);
-          }
-#pragma unroll
-          for (int k = 0; k < LEAD; ++k) {
-            read_p(st ^ 1u, 0, k);
-            read_sp(st ^ 1u, k);
-          }
-        } else if (tm >= LEAD) {
-          read_p(st ^ 1u, 0, tm);
-          read_sp(st ^ 1u, tm);
-        }
+        read_p(st, 0, tm);
+        read_sp(st, tm);
       }
       if constexpr (EL == EL_MX) {
 #pragma unroll
-        for (int tn = 0; tn < TN; ++tn) sq[tn] = sqn[tn];
+        for (int k = 0; k < NSQ; ++k) sq[k] = sqn[k];
       }
-      st ^= 1u;
+#pragma nounroll
+      for (; now.c < now.c1; ++now.c) {
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) read_q(st, 1, tn);
+        static_for<TM>([&](auto tmc) __attribute__((always_inline)) {
+          constexpr int tm = decltype(tmc)::value;
+          mma(S0{}, tmc);
+          __builtin_amdgcn_sched_barrier(0);
+          read_p(st, 1, tm);
+#pragma unroll
+          for (int i = LOADS - LATE; i < LOADS; ++i)
+            if ((i - (LOADS - LATE)) * TM / (LATE > 0 ? LATE : 1) == tm) load(i);
+        });
+        advance();
+        static_for<TM>([&](auto tmc) __attribute__((always_inline)) {
+          constexpr int tm = decltype(tmc)::value;
+          mma(S1{}, tmc);
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (tm == LEAD - 1) {
+            tile_barrier();
+            begin(st);
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn) {
+              read_q(st ^ 1u, 0, tn);
+              read_sq(st ^ 1u, tn);
+            }
+#pragma unroll
+            for (int k = 0; k < LEAD; ++k) read_p(st ^ 1u, 0, k);
+          } else if constexpr (tm >= LEAD) {
+            read_p(st ^ 1u, 0, tm);
+          }
+          // (a register of two tiles' scales is free after the second; none before the barrier)
+          if constexpr (tm >= LEAD - 1 && (tm % 2 == 1 || tm == TM - 1)) {
+            constexpr int from = tm == (LEAD - 1) / 2 * 2 + 1 || tm == LEAD - 1 ? 0 : tm / 2 * 2;
+#pragma unroll
+            for (int k = from; k <= tm; ++k) read_sp(st ^ 1u, k);
+          }
+          if constexpr (tm >= LEAD - 1) {
+#pragma unroll
+            for (int i = 0; i < LOADS - LATE; ++i)
+              if (i * (SLOTS + 1) / (LOADS - LATE) == tm - (LEAD - 1)) load(i);
+          }
+        });
+        if constexpr (EL == EL_MX) {
+#pragma unroll
+          for (int k = 0; k < NSQ; ++k) sq[k] = sqn[k];
+        }
+        st ^= 1u;
+      }
+      epilogue((int64_t)now.tp * BM, (int64_t)now.tq * BN, now.z, acc);
+      at += items.step;
+      if (at >= items.end) break;
+      now.set(items, at);
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) acc[tm][tn] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
     tile_barrier();  // nothing is in flight into LDS when the caller goes on
   }
 };
-
-// Tile number -> (tm, tn), XCD by XCD (workgroups go to the 8 XCDs in turn, each
-// with its own L2): an XCD takes a contiguous range of the tiles, in groups of 8
-// along the first axis, that axis fastest, so the tiles it runs at one time share
-// few row blocks of both operands.
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t nwg, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm,
-                                        uint32_t& tn) {
-  const uint32_t per = nwg / 8;
-  if (id < per * 8) id = (id % 8) * per + id / 8;
-  const uint32_t group = 8 * tiles_n, gi = id / group, first = gi * 8;
-  const uint32_t rows = min(tiles_m - first, 8u), in = id - gi * group;
-  tm = __builtin_amdgcn_readfirstlane(first + in % rows);
-  tn = __builtin_amdgcn_readfirstlane(in / rows);
-}
 
 }  // namespace tj2
