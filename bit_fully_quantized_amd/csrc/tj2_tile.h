@@ -152,7 +152,7 @@ struct Tile {
   static constexpr int LP = BM / RPI, LQ = BN / RPI;
   static constexpr int SCALE_DW = EL == EL_MX ? ROWS * 2 : 0;  // scale words of a chunk
   static_assert(BM % RPI == 0 && BN % RPI == 0, "whole load instructions");
-  static_assert(RPI % (16 * PB) == 0 && RPI % (16 * TN) == 0, "a thread's key is the same in all its rows");
+  static_assert(RPI >= 2 * TN && RPI % 32 == 0, "a thread's rows i * RPI + r differ from r by bits of the key above its own");
   static_assert(TN == 1 || TN % 2 == 0, "q_place pairs rows");
   static_assert(TM % PB == 0, "whole row blocks");
 
@@ -224,9 +224,11 @@ struct Tile {
 
     // what this thread loads: row i * RPI + t / 8, slot t % 8
     const int lr = t >> 3;
-    const uint32_t gp = (uint32_t)((t & 7) ^ p_key(lr)) * 16, gq = (uint32_t)((t & 7) ^ q_key(lr)) * 16;
     const int lrq = q_place(lr);
-    const uint32_t vp = (uint32_t)lr * (uint32_t)P.ld + gp, vq = (uint32_t)lrq * (uint32_t)Q.ld + gq;
+    // byte in the row of what it fetches for row i * RPI + lr
+    auto gp = [&](int i) __attribute__((always_inline)) { return (uint32_t)((t & 7) ^ p_key(lr) ^ p_key(i * RPI)) * 16u; };
+    auto gq = [&](int i) __attribute__((always_inline)) { return (uint32_t)((t & 7) ^ q_key(lr) ^ q_key(i * RPI)) * 16u; };
+    const uint32_t vp = (uint32_t)lr * (uint32_t)P.ld, vq = (uint32_t)lrq * (uint32_t)Q.ld;
     // and the uniform offset of its row i * RPI
     static_assert(128 % RPI == 0 && (BM < 128 || BM % 128 == 0) && (BN < 128 || BN % 128 == 0), "rows of a block");
     auto far_p = [&](int i) __attribute__((always_inline)) {
@@ -263,14 +265,15 @@ struct Tile {
     enter();
     // The loads of the cursor's chunk into `stage`, one at a time: begin() sets them up.
     u32x4_t dp, dq, dsp, dsq;
-    uint32_t badp, badq, bads = 0, dst = 0, sdst = 0;
+    uint32_t leftp, leftq, bads = 0, dst = 0, sdst = 0;
     auto begin = [&](uint32_t stage) __attribute__((always_inline)) {
       const uint32_t at = (uint32_t)ahead.c * 128u;
       dp = raw_buffer(pb + mul32(ahead.c, P.cs));
       dq = raw_buffer(qb + mul32(ahead.c, Q.cs));
       settle(dp, dq);
-      badp = at + gp >= (uint32_t)P.kb ? kOutside : 0u;
-      badq = at + gq >= (uint32_t)Q.kb ? kOutside : 0u;
+      // bytes of the row from the chunk on (none past the row's end)
+      leftp = (uint32_t)max(P.kb - (int32_t)at, 0);
+      leftq = (uint32_t)max(Q.kb - (int32_t)at, 0);
       dst = lds_w + stage * kStage;
       if constexpr (EL == EL_MX) {
         const uint32_t ats = (uint32_t)ahead.c * 8u;
@@ -298,9 +301,9 @@ struct Tile {
     constexpr int LOADS = LP + LQ + (EL == EL_MX ? SJ : 0);
     auto load = [&](int i) __attribute__((always_inline)) {
       if (i < LP) {
-        load_lds16(dp, lr < np - i * RPI ? vp | badp : kOutside, far_p(i), dst + i * (RPI * 128));
+        load_lds16(dp, lr < np - i * RPI && gp(i) < leftp ? vp + gp(i) : kOutside, far_p(i), dst + i * (RPI * 128));
       } else if (i < LP + LQ) {
-        load_lds16(dq, lrq < nq - (i - LP) * RPI ? vq | badq : kOutside, far_q(i - LP), dst + i * (RPI * 128));
+        load_lds16(dq, lrq < nq - (i - LP) * RPI && gq(i - LP) < leftq ? vq + gq(i - LP) : kOutside, far_q(i - LP), dst + i * (RPI * 128));
       } else if constexpr (EL == EL_MX) {
         const int j = i - LP - LQ, r0 = w * 32 + j * (NT / 2);
         const bool isp = r0 < BM;

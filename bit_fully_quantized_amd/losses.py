@@ -6,35 +6,44 @@ loss and gradient from one read; distillation_loss is its differentiable form.
 """
 from __future__ import annotations
 
-import ctypes
+from functools import lru_cache
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _BF16, _F32, _I32, _dense, _dtype_code, _ptr, check, lib, _stream
-from .mx import _on
+from . import _BF16, _F32, _I32, lib
+from .mx import _CODE, _OUT, _arg, _room, _run, _tensor
 
-_OUT = (torch.bfloat16, torch.float32)
 _I64 = (torch.int64,)
 
 
-def _rows(t, name: str, dtypes, cols: int | None = None) -> int:
-    """A matrix read with a leading dimension (unit column stride); returns the elements between rows."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in dtypes or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D CUDA (HIP) tensor of dtype {dtypes}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+def _rows(t, name: str, dtypes, index: int, cols: int | None = None) -> int:
+    """A matrix with a leading dimension (unit column stride); returns the elements between its rows."""
+    if _tensor(t, name, 2) != index:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, other arguments on cuda:{index}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    rows, n = t.shape
+    if cols is not None and n != cols:
+        raise ValueError(f"{name} has {n} columns, expected {cols}")
+    ld, unit = t.stride()
+    if unit != 1 and n > 1:
         raise ValueError(f"{name} must have unit column stride")
-    if cols is not None and t.shape[1] != cols:
-        raise ValueError(f"{name} has {t.shape[1]} columns, expected {cols}")
-    # the stride of a single row is free: any pitch that holds it will do
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], -(-t.shape[1] // 8) * 8)
-    if ld < t.shape[1]:
+    if rows <= 1:
+        return -(-n // 8) * 8  # the stride of a single row is free: any pitch that holds it will do
+    if ld < n:
         raise ValueError(f"{name} has rows that overlap")
     return ld
 
 
-def _workspace(n: int, device) -> torch.Tensor:
-    return torch.empty(max(int(n), 1), dtype=torch.uint8, device=device)
+@lru_cache(maxsize=4096)
+def _fwd_bytes(T: int, K: int, V: int) -> int:
+    return max(1, int(lib().tj2_linear_ce_fwd_workspace_size(T, K, V)))
+
+
+@lru_cache(maxsize=4096)
+def _bwd_bytes(T: int, K: int, V: int) -> int:
+    return max(1, int(lib().tj2_linear_ce_bwd_workspace_size(T, K, V)))
 
 
 def linear_ce_fwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, *, ignore_index: int = -100,
@@ -43,24 +52,18 @@ def linear_ce_fwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, *, ig
     """Per-token (loss, lse) of the logits X W^T: X [T, K], W [V, K] bf16, targets int64 [T]; fp32 [T] results.
 
     The loss of a token with targets[t] == ignore_index is 0, of one outside the vocabulary NaN."""
-    ldx = _rows(X, "X", _BF16)
+    index = _tensor(X, "X", 2)
+    ldx = _rows(X, "X", _BF16, index)
     T, K = X.shape
-    ldw = _rows(W, "W", _BF16, K)
+    ldw = _rows(W, "W", _BF16, index, K)
     V = W.shape[0]
-    _dense(targets, "targets", _I64, shape=(T,))
     if loss is None:
-        loss = torch.empty(T, dtype=torch.float32, device=X.device)
+        loss = torch.empty(T, dtype=torch.float32, device=index)
     if lse is None:
-        lse = torch.empty(T, dtype=torch.float32, device=X.device)
-    _dense(loss, "loss", _F32, shape=(T,))
-    _dense(lse, "lse", _F32, shape=(T,))
-    if workspace is None:
-        workspace = _workspace(lib().tj2_linear_ce_fwd_workspace_size(T, K, V), X.device)
-    _dense(workspace, "workspace", (torch.uint8,))
-    with _on(X, W, targets, loss, lse, workspace):
-        st = lib().tj2_linear_ce_fwd(_ptr(X), ldx, _ptr(W), ldw, _ptr(targets), T, K, V, ignore_index, _ptr(loss), _ptr(lse),
-                                     _ptr(workspace), workspace.numel(), _stream())
-    check("tj2_linear_ce_fwd", st)
+        lse = torch.empty(T, dtype=torch.float32, device=index)
+    workspace, wp, wn = _room(workspace, _fwd_bytes(T, K, V), index)
+    _run("tj2_linear_ce_fwd", index, X.data_ptr(), ldx, W.data_ptr(), ldw, _arg(targets, "targets", _I64, index, (T,)), T, K, V,
+         ignore_index, _arg(loss, "loss", _F32, index, (T,)), _arg(lse, "lse", _F32, index, (T,)), wp, wn)
     return loss, lse
 
 
@@ -71,27 +74,20 @@ def linear_ce_bwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, lse: 
     """(dX [T, K], dW [V, K]) for dloss, the gradient of each token's loss (fp32 [T]), with lse of linear_ce_fwd.
 
     need_dx / need_dw False leaves that gradient out (None)."""
-    ldx = _rows(X, "X", _BF16)
+    index = _tensor(X, "X", 2)
+    ldx = _rows(X, "X", _BF16, index)
     T, K = X.shape
-    ldw = _rows(W, "W", _BF16, K)
+    ldw = _rows(W, "W", _BF16, index, K)
     V = W.shape[0]
-    _dense(targets, "targets", _I64, shape=(T,))
-    _dense(lse, "lse", _F32, shape=(T,))
-    _dense(dloss, "dloss", _F32, shape=(T,))
     if dX is None and need_dx:
-        dX = torch.empty((T, K), dtype=dx_dtype, device=X.device)
+        dX = torch.empty((T, K), dtype=dx_dtype, device=index)
     if dW is None and need_dw:
-        dW = torch.empty((V, K), dtype=dw_dtype, device=X.device)
-    _dense(dX, "dX", _OUT, shape=(T, K), optional=True)
-    _dense(dW, "dW", _OUT, shape=(V, K), optional=True)
-    if workspace is None:
-        workspace = _workspace(lib().tj2_linear_ce_bwd_workspace_size(T, K, V), X.device)
-    _dense(workspace, "workspace", (torch.uint8,))
-    with _on(X, W, targets, lse, dloss, dX, dW, workspace):
-        st = lib().tj2_linear_ce_bwd(_ptr(X), ldx, _ptr(W), ldw, _ptr(targets), T, K, V, ignore_index, _ptr(lse), _ptr(dloss),
-                                     _ptr(dX), _dtype_code(dX) if dX is not None else 0, _ptr(dW),
-                                     _dtype_code(dW) if dW is not None else 0, _ptr(workspace), workspace.numel(), _stream())
-    check("tj2_linear_ce_bwd", st)
+        dW = torch.empty((V, K), dtype=dw_dtype, device=index)
+    workspace, wp, wn = _room(workspace, _bwd_bytes(T, K, V), index)
+    _run("tj2_linear_ce_bwd", index, X.data_ptr(), ldx, W.data_ptr(), ldw, _arg(targets, "targets", _I64, index, (T,)), T, K, V,
+         ignore_index, _arg(lse, "lse", _F32, index, (T,)), _arg(dloss, "dloss", _F32, index, (T,)),
+         _arg(dX, "dX", _OUT, index, (T, K), optional=True), _CODE[dX.dtype] if dX is not None else 0,
+         _arg(dW, "dW", _OUT, index, (V, K), optional=True), _CODE[dW.dtype] if dW is not None else 0, wp, wn)
     return dX, dW
 
 
@@ -138,30 +134,25 @@ def distill_topk(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
     teacher [T, k] of the logits' dtype): alpha * temperature^2 * KL(teacher || student) + (1 - alpha) * cross
     entropy with targets.  With grad (or dlogits given, which may be logits itself): (loss, dlogits), the
     gradient for `weight`, the gradient of each token's loss (fp32 [T], 1 if not given)."""
-    ldl = _rows(logits, "logits", _OUT)
+    index = _tensor(logits, "logits", 2)
+    ldl = _rows(logits, "logits", _OUT, index)
     T, V = logits.shape
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
-        raise ValueError("ids must be an int32 tensor [T, k]")
+    _tensor(ids, "ids", 2)
     k = ids.shape[1]
-    _dense(ids, "ids", _I32, shape=(T, k))
-    _dense(teacher, "teacher", (logits.dtype,), shape=(T, k))
-    _dense(targets, "targets", _I64, shape=(T,), optional=True)
-    _dense(weight, "weight", _F32, shape=(T,), optional=True)
     if loss is None:
-        loss = torch.empty(T, dtype=torch.float32, device=logits.device)
-    _dense(loss, "loss", _F32, shape=(T,))
+        loss = torch.empty(T, dtype=torch.float32, device=index)
     if dlogits is None and grad:
-        dlogits = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
-    ldd = V
+        dlogits = torch.empty((T, V), dtype=logits.dtype, device=index)
+    ldd, dp = V, 0
     if dlogits is not None:
-        ldd = _rows(dlogits, "dlogits", (logits.dtype,), V)
+        ldd = ldl if dlogits is logits else _rows(dlogits, "dlogits", (logits.dtype,), index, V)
         if dlogits.shape[0] != T:
             raise ValueError(f"dlogits has {dlogits.shape[0]} rows, expected {T}")
-    with _on(logits, ids, teacher, targets, weight, loss, dlogits):
-        st = lib().tj2_distill_topk(_ptr(logits), _dtype_code(logits), T, V, ldl, _ptr(ids), _ptr(teacher), k,
-                                    ctypes.c_float(temperature), ctypes.c_float(alpha), _ptr(targets), ignore_index,
-                                    _ptr(weight), _ptr(loss), _ptr(dlogits), ldd, _stream())
-    check("tj2_distill_topk", st)
+        dp = dlogits.data_ptr()
+    _run("tj2_distill_topk", index, logits.data_ptr(), _CODE[logits.dtype], T, V, ldl, _arg(ids, "ids", _I32, index, (T, k)),
+         _arg(teacher, "teacher", (logits.dtype,), index, (T, k)), k, temperature, alpha,
+         _arg(targets, "targets", _I64, index, (T,), optional=True), ignore_index,
+         _arg(weight, "weight", _F32, index, (T,), optional=True), _arg(loss, "loss", _F32, index, (T,)), dp, ldd)
     return loss if dlogits is None else (loss, dlogits)
 
 
