@@ -1138,8 +1138,12 @@ tj2_status mxfp4_linear_fwd(const void* X, int64_t M, int64_t K, int64_t N, cons
   TJ2_TRY(check_out_dtype(y_dtype, "y_dtype"));
   if (!aligned16(X) || !aligned16(W_master) || !aligned16(Y)) return fail(TJ2_ERR_ALIGN, "X, W_master and Y must be 16-byte aligned");
   TJ2_TRY(check_mx_workspace(workspace, ws_bytes, mx_gemm_workspace_bytes(M, N, K)));
-  TJ2_TRY(run_mx_quant(X, TJ2_BF16, nullptr, M, K, TJ2_GROUP_ROW, TJ2_RTN, 0, 0, 0, 0, Xq, s));
   if (W_master) TJ2_TRY(run_mx_quant(W_master, TJ2_F32, nullptr, N, K, TJ2_GROUP_ROW, TJ2_RTN, 0, 0, 0, 0, Wq, s));
+  if (launch_mx_linear_few(X, make_view(*Xq), make_view(*Wq), Y, y_dtype, s)) {
+    TJ2_TRY(hip_check(hipGetLastError(), "MXFP4 linear launch"));
+    return ok();
+  }
+  TJ2_TRY(run_mx_quant(X, TJ2_BF16, nullptr, M, K, TJ2_GROUP_ROW, TJ2_RTN, 0, 0, 0, 0, Xq, s));
   TJ2_TRY(run_mx_gemm(Xq, Wq, Y, y_dtype, N, 0, workspace, s));
   return ok();
 }

@@ -17,7 +17,7 @@
 
 #include <algorithm>
 
-#include "tj2_tile.h"
+#include "tj2_skinny.h"
 
 namespace tj2 {
 namespace {
@@ -61,7 +61,7 @@ struct CeArgs {
 // v c - r (one instruction instead of two; r the rounded m c, so nothing but the
 // result is rounded) could overflow the exponential.
 template <class T>
-__global__ __launch_bounds__(T::NT, 1) void ce_fwd_kernel(CeArgs p) {
+__global__ __launch_bounds__(T::NT, T::WAVES) void ce_fwd_kernel(CeArgs p) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
   const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, 1);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
@@ -127,16 +127,75 @@ __global__ __launch_bounds__(T::NT, 1) void ce_fwd_kernel(CeArgs p) {
   });
 }
 
-// Token by token: the parts of its sum joined (four quarters of them at a time),
+// The same for up to 64 tokens (scoring): one read of W, each lane's part of a token's
+// sum kept over the wave's groups of 16 entries, one part a workgroup and token.
+template <class S, int TN>
+__global__ __launch_bounds__(S::NT, 2) void ce_few_kernel(CeArgs p) {
+  __shared__ typename S::Smem sm;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const int px = S::pitch(p.P.kb), whole = (p.P.kb + 127) / 128 * 8, T = (int)p.Q.rows;
+  for (int i = threadIdx.x; i < S::TOKENS * whole; i += S::NT) {
+    const int t = i / whole, c = (i - t * whole) * 16;
+    uint4 v = {0u, 0u, 0u, 0u};
+    if (t < T && c < p.P.kb) v = *reinterpret_cast<const uint4*>(p.Q.p + t * p.Q.ld + c);
+    *reinterpret_cast<uint4*>(sm.x + t * px + c) = v;
+  }
+  __syncthreads();
+  float r[TN], s[TN];
+  int64_t y[TN];
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn) {
+    r[tn] = -INFINITY;
+    s[tn] = 0.0f;
+    y[tn] = tn * 16 + n < T ? p.y[tn * 16 + n] : -1;
+  }
+  S::run(p.P, sm, [&](uint32_t group, const typename S::Acc& acc) __attribute__((always_inline)) {
+    const int64_t v0 = (int64_t)group * 16 + g * 4;
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (v0 + k == y[tn]) p.zt[tn * 16 + n] = acc[tn][k];
+        if (v0 + k < p.P.rows) m = fmaxf(m, acc[tn][k]);
+      }
+      if (v0 < p.P.rows) {
+        float e = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (v0 + k < p.P.rows) e += exp_scaled(acc[tn][k], m, kLog2e);
+        join(r[tn], s[tn], m * kLog2e, e);
+      }
+    }
+  });
+  __syncthreads();  // the tokens in LDS are done with
+  float2* sh = reinterpret_cast<float2*>(sm.x);
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn) {
+    join(r[tn], s[tn], __shfl_xor(r[tn], 16), __shfl_xor(s[tn], 16));
+    join(r[tn], s[tn], __shfl_xor(r[tn], 32), __shfl_xor(s[tn], 32));
+    if (g == 0) sh[w * S::TOKENS + tn * 16 + n] = float2{r[tn], s[tn]};
+  }
+  __syncthreads();
+  if (threadIdx.x < T) {
+    float R = -INFINITY, e = 0.0f;
+#pragma unroll
+    for (int k = 0; k < S::WAVES; ++k) join(R, e, sh[k * S::TOKENS + threadIdx.x].x, sh[k * S::TOKENS + threadIdx.x].y);
+    p.part[(int64_t)blockIdx.x * T + threadIdx.x] = float2{R, e};
+  }
+}
+
+// Token by token: the parts of its sum joined (S shares of them at a time),
 // the loss from the target's logit; a target outside the vocabulary gives NaN.
-__global__ __launch_bounds__(256) void ce_join_kernel(const float2* part, int parts, const float* zt, const int64_t* y,
-                                                      int64_t T, int64_t V, int64_t ignore, float* loss, float* lse) {
-  __shared__ float2 sh[4][64];
-  const int l = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * 64 + l;
+template <int L, int S>
+__global__ __launch_bounds__(L * S) void ce_join_kernel(const float2* part, int parts, const float* zt, const int64_t* y,
+                                                       int64_t T, int64_t V, int64_t ignore, float* loss, float* lse) {
+  __shared__ float2 sh[S][L];
+  const int l = threadIdx.x % L, q = threadIdx.x / L;
+  const int64_t t = (int64_t)blockIdx.x * L + l;
   float r = -INFINITY, s = 0.0f;
   if (t < T) {
-    const int a = (int)((int64_t)parts * q / 4), b = (int)((int64_t)parts * (q + 1) / 4);
+    const int a = (int)((int64_t)parts * q / S), b = (int)((int64_t)parts * (q + 1) / S);
     const float2* at = part + (int64_t)a * T + t;
 #pragma unroll 8
     for (int i = a; i < b; ++i, at += T) {
@@ -145,10 +204,15 @@ __global__ __launch_bounds__(256) void ce_join_kernel(const float2* part, int pa
     }
   }
   sh[q][l] = float2{r, s};
-  __syncthreads();
-  if (q || t >= T) return;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) join(r, s, sh[i][l].x, sh[i][l].y);
+  for (int o = S / 2; o; o /= 2) {
+    __syncthreads();
+    if (q < o) {
+      join(r, s, sh[q + o][l].x, sh[q + o][l].y);
+      sh[q][l] = float2{r, s};
+    }
+  }
+  if (q || t >= T) return;
   const float e = (r + __builtin_amdgcn_logf(s)) * kLn2;
   lse[t] = e;
   if (loss) {
@@ -184,7 +248,7 @@ __global__ __launch_bounds__(1024) void ce_weights_kernel(const float* w, const 
 // nothing (an output modifier) and holds where the fused v c - r overflows; it turns a
 // NaN into 0, so a token whose lse is NaN gets a NaN weight instead.
 template <class T>
-__global__ __launch_bounds__(T::NT, 1) void ce_dz_kernel(CeArgs p) {
+__global__ __launch_bounds__(T::NT, T::WAVES) void ce_dz_kernel(CeArgs p) {
   static_assert(T::kTN == 4 && T::PB == 4, "64 tokens, and entries 16 a lane");
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
   const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, 1);
@@ -319,7 +383,7 @@ struct ProductArgs {
 };
 
 template <class T>
-__global__ __launch_bounds__(T::NT, 1) void ce_product_kernel(ProductArgs p) {
+__global__ __launch_bounds__(T::NT, T::WAVES) void ce_product_kernel(ProductArgs p) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
   const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
@@ -386,7 +450,83 @@ __global__ __launch_bounds__(256) void ce_fold_kernel(float* kept, const float* 
   *reinterpret_cast<float4_t*>(kept + i) = v;
 }
 
-using TileCe = Tile<EL_BF16, 2, 4, 8, 4>;
+using TileBig = Tile<EL_BF16, 2, 4, 8, 4>;  // 256 x 256
+using TileMid = Tile<EL_BF16, 2, 2, 4, 4>;  // 128 x 128
+
+int64_t tiles_of(int64_t p, int64_t q, int64_t b) { return (p + b - 1) / b * ((q + b - 1) / b); }
+
+// Estimated time (us on MI355X) of `items` tiles over `chunks` chunks of 64 elements:
+// a tile of 256 takes 2.2 a chunk and `fixed` for its start and results, one of 128
+// 1.1 alone on its CU and 1.5 beside another, and half of `fixed`.
+double tile_time(bool big, int64_t items, double chunks, double fixed) {
+  if (big) return (double)((items + kCus - 1) / kCus) * (chunks * 2.2 + fixed);
+  const int64_t full = items / (2 * kCus), rest = items % (2 * kCus);
+  return (double)full * (chunks * 1.5 + fixed / 2) + (rest ? chunks * (rest > kCus ? 1.5 : 1.1) + fixed / 2 : 0.0);
+}
+// 256 x 256 tiles for the logits of V entries and T tokens, else 128 x 128 (forward of
+// 1235 x 32003 over 528: 65.4 and 76.9 us; 777 x 5000 over 1024: 31.6 and 24.6).
+bool ce_big(int64_t V, int64_t T, int64_t K) {
+  const double chunks = (double)((K + 63) / 64);
+  return tile_time(true, tiles_of(V, T, 256), chunks, 9.0) < tile_time(false, tiles_of(V, T, 128), chunks, 9.0);
+}
+// Tile and splits of a product of p by q results over k (1235 x 528 over 32003: 192 us
+// unsplit.. of the whole backward, 174 with 8 to 16 splits).
+struct ProductPlan {
+  bool big;
+  int splits;
+};
+ProductPlan product_plan(int64_t p, int64_t q, int64_t k) {
+  ProductPlan best = {false, 1};
+  const int64_t nch = (k + 63) / 64;
+  double least = 1e30;
+  for (int big = 0; big < 2; ++big)
+    for (int z = 1; z <= 32 && z * 8 <= std::max<int64_t>(nch, 8); z *= 2) {
+      double t = tile_time(big, tiles_of(p, q, big ? 256 : 128) * z, (double)((nch + z - 1) / z), 6.0);
+      if (z > 1) t += 3.0 + (double)p * (double)q * 8.0 * z / 6e6;
+      if (t < least) {
+        least = t;
+        best = ProductPlan{big != 0, z};
+      }
+    }
+  return best;
+}
+
+template <class T>
+void launch_fwd_tile(CeArgs a, hipStream_t s) {
+  a.tiles_p = (uint32_t)((a.P.rows + T::BM - 1) / T::BM);
+  a.tiles_q = (uint32_t)((a.Q.rows + T::BN - 1) / T::BN);
+  ce_fwd_kernel<T><<<T::grid((uint64_t)a.tiles_p * a.tiles_q), T::NT, 0, s>>>(a);
+}
+// 1 to 4 tiles of 16 tokens, where their operand fits the LDS of ce_few_kernel
+template <int TN>
+bool launch_few(const CeArgs& a, uint32_t grid, hipStream_t s) {
+  using Few = Skinny<EL_BF16, TN, 66 * 1024>;
+  if (a.Q.rows > Few::TOKENS || !Few::fits(a.Q.rows, a.P.kb)) return false;
+  ce_few_kernel<Few, TN><<<grid, Few::NT, 0, s>>>(a);
+  return true;
+}
+uint32_t few_grid(int64_t V) { return Skinny<EL_BF16, 1, 66 * 1024>::grid(V); }
+bool few_fits(int64_t T, int64_t K) {
+  return Skinny<EL_BF16, 1, 66 * 1024>::fits(T, K * 2) || Skinny<EL_BF16, 2, 66 * 1024>::fits(T, K * 2) ||
+         Skinny<EL_BF16, 4, 66 * 1024>::fits(T, K * 2);
+}
+
+template <class T>
+void launch_dz_tile(CeArgs a, hipStream_t s) {
+  a.tiles_p = (uint32_t)((a.P.rows + T::BM - 1) / T::BM);
+  a.tiles_q = (uint32_t)((a.Q.rows + T::BN - 1) / T::BN);
+  ce_dz_kernel<T><<<T::grid((uint64_t)a.tiles_p * a.tiles_q), T::NT, 0, s>>>(a);
+}
+template <class T>
+void launch_product_tile(ProductArgs x, hipStream_t s) {
+  x.tiles_p = (uint32_t)((x.P.rows + T::BM - 1) / T::BM);
+  x.tiles_q = (uint32_t)((x.Q.rows + T::BN - 1) / T::BN);
+  ce_product_kernel<T><<<T::grid((uint64_t)x.tiles_p * x.tiles_q * (uint32_t)x.splits), T::NT, 0, s>>>(x);
+}
+void launch_product(const ProductArgs& x, bool big, hipStream_t s) {
+  if (big) launch_product_tile<TileBig>(x, s);
+  else launch_product_tile<TileMid>(x, s);
+}
 
 TileOp bf16_operand(const void* p, int64_t rows, int64_t cols, int64_t ld) {
   TileOp o = {};
@@ -422,24 +562,24 @@ int64_t ce_piece(int64_t T, int64_t V) {
   return std::min(up(V, 256), std::max<int64_t>(most, 1024));
 }
 
-int ce_splits(int64_t p_rows, int64_t q_rows, int64_t k) {
-  const int64_t tiles = up(p_rows, 256) / 256 * (up(q_rows, 256) / 256), nch = up(k, 64) / 64;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(256 / tiles, nch / 8));
-}
-
 // Tokens from which the operands of the logits are copied into blocks first.
 constexpr int64_t kBlockTokens = 2048;
 
 struct CeFwdSpace {
   size_t part, zt, xb, wb, bytes;
-  bool blocked;
+  int64_t parts;
+  bool few, big, blocked;
 };
 CeFwdSpace ce_fwd_space(int64_t T, int64_t K, int64_t V) {
   CeFwdSpace s;
   size_t at = 0;
   auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
   s.blocked = T >= kBlockTokens;
-  s.part = take((size_t)(up(V, TileCe::BM) / 128) * (size_t)T * 8);
+  s.few = few_fits(T, K);
+  s.big = ce_big(V, T, K);
+  const int64_t per = s.big ? 16 * TileBig::kTM : 16 * TileMid::kTM;  // entries of a part
+  s.parts = s.few ? few_grid(V) : (V + per - 1) / per;
+  s.part = take((size_t)(s.few ? s.parts : up(V, 256) / per) * (size_t)T * 8);
   s.zt = take((size_t)T * 4);
   s.xb = take(s.blocked ? blocked_bytes(T, K) : 0);
   s.wb = take(s.blocked ? blocked_bytes(V, K) : 0);
@@ -450,14 +590,14 @@ CeFwdSpace ce_fwd_space(int64_t T, int64_t K, int64_t V) {
 struct CeBwdSpace {
   size_t c, top, xb, xt, wb, wt, d, dt, dx, part, bytes;
   int64_t piece;
-  int sx, sw;
+  ProductPlan px, pw;
   bool blocked;
 };
 CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   CeBwdSpace s;
   s.piece = ce_piece(T, V);
-  s.sx = ce_splits(K, T, s.piece);
-  s.sw = ce_splits(K, s.piece, T);
+  s.px = product_plan(K, T, s.piece);
+  s.pw = product_plan(K, s.piece, T);
   s.blocked = T >= kBlockTokens;
   size_t at = 0;
   auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
@@ -470,7 +610,8 @@ CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   s.d = take(blocked_bytes(T, s.piece));
   s.dt = take(blocked_bytes(s.piece, T));
   s.dx = take((size_t)(T * K * 4));
-  s.part = take(std::max(s.sx > 1 ? (size_t)s.sx * (size_t)(T * K * 4) : 0, s.sw > 1 ? (size_t)s.sw * (size_t)(s.piece * K * 4) : 0));
+  s.part = take(std::max(s.px.splits > 1 ? (size_t)s.px.splits * (size_t)(T * K * 4) : 0,
+                         s.pw.splits > 1 ? (size_t)s.pw.splits * (size_t)(s.piece * K * 4) : 0));
   s.bytes = at;
   return s;
 }
@@ -506,15 +647,21 @@ hipError_t launch_ce_fwd(const CeParams& c, void* ws, hipStream_t s) {
     a.Q = bf16_operand(c.X, c.T, c.K, c.ldx);
   }
   a.y = c.y;
-  a.tiles_p = (uint32_t)(up(c.V, TileCe::BM) / TileCe::BM);
-  a.tiles_q = (uint32_t)(up(c.T, TileCe::BN) / TileCe::BN);
   a.nch = (int32_t)(up(c.K, 64) / 64);
   a.part = reinterpret_cast<float2*>(w + sp.part);
   a.zt = reinterpret_cast<float*>(w + sp.zt);
-  ce_fwd_kernel<TileCe><<<tile_grid((uint64_t)a.tiles_p * a.tiles_q), TileCe::NT, 0, s>>>(a);
+  if (sp.few) {
+    const uint32_t grid = few_grid(c.V);
+    if (!launch_few<1>(a, grid, s) && !launch_few<2>(a, grid, s)) launch_few<4>(a, grid, s);
+  } else if (sp.big) {
+    launch_fwd_tile<TileBig>(a, s);
+  } else {
+    launch_fwd_tile<TileMid>(a, s);
+  }
   TJ2_STEP();
-  const int parts = (int)((c.V + 127) / 128);
-  ce_join_kernel<<<(uint32_t)((c.T + 63) / 64), 256, 0, s>>>(a.part, parts, a.zt, c.y, c.T, c.V, c.ignore, c.loss, c.lse);
+  // few tokens and many parts: many threads a token
+  if (c.T <= 2048 && sp.parts > 64) ce_join_kernel<16, 64><<<(uint32_t)((c.T + 15) / 16), 1024, 0, s>>>(a.part, (int)sp.parts, a.zt, c.y, c.T, c.V, c.ignore, c.loss, c.lse);
+  else ce_join_kernel<64, 4><<<(uint32_t)((c.T + 63) / 64), 256, 0, s>>>(a.part, (int)sp.parts, a.zt, c.y, c.T, c.V, c.ignore, c.loss, c.lse);
   return hipGetLastError();
 }
 
@@ -539,8 +686,6 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
     a.P = sp.blocked ? blocked_operand(w + sp.wb, vn, c.K) : bf16_operand(W, vn, c.K, c.ldw);
     a.Q = sp.blocked ? blocked_operand(w + sp.xb, c.T, c.K) : bf16_operand(c.X, c.T, c.K, c.ldx);
     a.y = c.y;
-    a.tiles_p = (uint32_t)(up(vn, TileCe::BM) / TileCe::BM);
-    a.tiles_q = (uint32_t)(up(c.T, TileCe::BN) / TileCe::BN);
     a.nch = (int32_t)(up(c.K, 64) / 64);
     a.lse = c.lse;
     a.c = reinterpret_cast<float*>(w + sp.c);
@@ -549,16 +694,15 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
     a.dt = reinterpret_cast<uint16_t*>(w + sp.dt);
     a.nd = (int32_t)(up(vn, 64) / 64);
     a.nt = (int32_t)(up(c.T, 64) / 64);
-    ce_dz_kernel<TileCe><<<tile_grid((uint64_t)a.tiles_p * a.tiles_q), TileCe::NT, 0, s>>>(a);
+    if (ce_big(vn, c.T, c.K)) launch_dz_tile<TileBig>(a, s);
+    else launch_dz_tile<TileMid>(a, s);
     TJ2_STEP();
     if (c.dX) {
       ProductArgs x = {};
       x.P = blocked_operand(w + sp.wt, c.K, up(vn, 64));
       x.Q = blocked_operand(w + sp.d, c.T, up(vn, 64));
-      x.tiles_p = (uint32_t)(up(c.K, TileCe::BM) / TileCe::BM);
-      x.tiles_q = a.tiles_q;
       x.nch = a.nd;
-      x.splits = std::min(sp.sx, x.nch);
+      x.splits = std::min(sp.px.splits, x.nch);
       x.scale = top;
       x.bf16 = c.dx_dtype == TJ2_BF16;
       x.ldo = c.K;
@@ -566,7 +710,7 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
       if (x.splits > 1) x.sum = part;
       else if (one) x.out = c.dX;
       else x.sum = dx;
-      ce_product_kernel<TileCe><<<tile_grid((uint64_t)x.tiles_p * x.tiles_q * (uint32_t)x.splits), TileCe::NT, 0, s>>>(x);
+      launch_product(x, sp.px.big, s);
       TJ2_STEP();
       const int64_t n = c.T * c.K;
       const uint32_t grid = (uint32_t)((n / 4 + 255) / 256);
@@ -582,10 +726,8 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
       ProductArgs x = {};
       x.P = blocked_operand(w + sp.xt, c.K, up(c.T, 64));
       x.Q = blocked_operand(w + sp.dt, vn, up(c.T, 64));
-      x.tiles_p = (uint32_t)(up(c.K, TileCe::BM) / TileCe::BM);
-      x.tiles_q = (uint32_t)(up(vn, TileCe::BN) / TileCe::BN);
       x.nch = a.nt;
-      x.splits = std::min(sp.sw, x.nch);
+      x.splits = std::min(sp.pw.splits, x.nch);
       x.scale = top;
       x.bf16 = c.dw_dtype == TJ2_BF16;
       x.ldo = c.K;
@@ -593,7 +735,7 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
       uint8_t* out = reinterpret_cast<uint8_t*>(c.dW) + (size_t)(v0 * c.K) * (x.bf16 ? 2 : 4);
       if (x.splits > 1) x.sum = part;
       else x.out = out;
-      ce_product_kernel<TileCe><<<tile_grid((uint64_t)x.tiles_p * x.tiles_q * (uint32_t)x.splits), TileCe::NT, 0, s>>>(x);
+      launch_product(x, sp.pw.big, s);
       TJ2_STEP();
       const int64_t n = vn * c.K;
       if (x.splits > 1) ce_sum_kernel<<<(uint32_t)((n / 4 + 255) / 256), 256, 0, s>>>(part, x.splits, n, top, out, x.bf16);

@@ -8,7 +8,7 @@
 // decoded to f16 first.
 #include <algorithm>
 
-#include "tj2_tile.h"
+#include "tj2_skinny.h"
 
 namespace tj2 {
 namespace {
@@ -275,7 +275,9 @@ __device__ __forceinline__ void store_run(const MxGemmArgs& p, int64_t row, int6
   const bool whole = p.vec && j + N <= J;
   if (p.bf16) {
     uint16_t* o = reinterpret_cast<uint16_t*>(p.C) + row + j;
-    if (whole && N % 8 == 0) {
+    if (whole && N == 4) {
+      *reinterpret_cast<uint2*>(o) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    } else if (whole) {
 #pragma unroll
       for (int k = 0; k + 8 <= N; k += 8)
         *reinterpret_cast<uint4*>(o + k) = uint4{bf16_pair(v[k], v[k + 1]), bf16_pair(v[k + 2], v[k + 3]),
@@ -306,7 +308,7 @@ __device__ __forceinline__ void store_run(const MxGemmArgs& p, int64_t row, int6
 }
 
 template <class T>
-__global__ __launch_bounds__(T::NT, 1) void mx_gemm_kernel(MxGemmArgs p) {
+__global__ __launch_bounds__(T::NT, T::WAVES) void mx_gemm_kernel(MxGemmArgs p) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
   const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
@@ -325,6 +327,61 @@ __global__ __launch_bounds__(T::NT, 1) void mx_gemm_kernel(MxGemmArgs p) {
           store_run<4 * T::PB>(p, at + i * p.ldc, pw + tb * 16 * T::PB, v);
         }
       }
+    }
+  });
+}
+
+// Up to 16 rows of A (decoding): A whole in LDS, B read once.  From bf16 X (the
+// linear layer's forward) each workgroup quantizes X for itself, the first one
+// storing the codes too, which saves the launch that would do it.
+struct MxFewArgs {
+  MxGemmArgs g;
+  const uint16_t* x;  // quantize [I, cols] bf16 into g.Q's arrays; NULL: they are given
+  int32_t cols;
+  uint8_t* codes;
+  uint8_t* scale;
+};
+template <class S>
+__global__ __launch_bounds__(S::NT, 2) void mx_few_kernel(MxFewArgs a) {
+  __shared__ typename S::Smem sm;
+  const MxGemmArgs& p = a.g;
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, I = (int)p.Q.rows;
+  const int px = S::pitch(p.P.kb), ps = S::scale_pitch(p.P.kb);
+  const int chunks = (p.P.kb + 127) / 128, halves = chunks * 16;  // 16-element pieces of a row, whole chunks
+  for (int i = threadIdx.x; i < S::TOKENS * halves; i += S::NT) {
+    const int t = i / halves, h = i - t * halves;
+    uint2 q = {0u, 0u};
+    uint32_t byte = 0u;
+    if (a.x) {
+      float v[16];
+      if (t < I && h * 16 < a.cols) {
+        load16<uint16_t>(a.x + (int64_t)t * a.cols + h * 16, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+      }
+      uint32_t top = top_bits16(v);
+      top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0xB1, 0xF, 0xF, false));
+      byte = mx_scale_byte<false>(top);
+      q = mx_codes16<false>(v, byte, 0, 0, 0);
+      if (h * 16 >= a.cols) q = uint2{0u, 0u};
+      if (blockIdx.x == 0 && t < I && h * 8 < p.P.kb) {
+        *reinterpret_cast<uint2*>(a.codes + (int64_t)t * p.P.kb + h * 8) = q;
+        if (!(h & 1)) a.scale[(int64_t)t * p.P.sb + h / 2] = (uint8_t)byte;
+      }
+    } else if (t < I && h * 8 < p.P.kb) {
+      q = *reinterpret_cast<const uint2*>(p.Q.p + (int64_t)t * p.P.kb + h * 8);
+      byte = p.Q.s[(int64_t)t * p.P.sb + h / 2];
+    }
+    *reinterpret_cast<uint2*>(sm.x + t * px + h * 8) = q;
+    if (!(h & 1)) sm.xs[t * ps + h / 2] = (uint8_t)byte;
+  }
+  __syncthreads();
+  S::run(p.P, sm, [&](uint32_t group, const typename S::Acc& acc) __attribute__((always_inline)) {
+    static_assert(S::TOKENS == 16, "one tile of tokens");
+    if (n < I) {
+      const float v[4] = {acc[0].x, acc[0].y, acc[0].z, acc[0].w};
+      store_run<4>(p, (int64_t)n * p.ldc, (int64_t)group * 16 + g * 4, v);
     }
   });
 }
@@ -350,18 +407,20 @@ __global__ __launch_bounds__(256) void mx_join_kernel(MxGemmArgs p) {
   store_run<4>(p, i * p.ldc, j, v);
 }
 
-using TileBig = Tile<EL_MX, 2, 4, 8, 4>;
+using TileBig = Tile<EL_MX, 2, 4, 8, 4>;    // 256 x 256
+using TileMid = Tile<EL_MX, 2, 2, 4, 4>;    // 128 x 128
+using TileSmall = Tile<EL_MX, 2, 2, 2, 2>;  // 64 x 64
 
 template <class T>
 hipError_t launch_tile(MxGemmArgs a, hipStream_t s) {
   a.tiles_p = (uint32_t)((a.P.rows + T::BM - 1) / T::BM);
   a.tiles_q = (uint32_t)((a.Q.rows + T::BN - 1) / T::BN);
-  mx_gemm_kernel<T><<<tile_grid((uint64_t)a.tiles_p * a.tiles_q * (uint32_t)a.splits), T::NT, 0, s>>>(a);
+  mx_gemm_kernel<T><<<T::grid((uint64_t)a.tiles_p * a.tiles_q * (uint32_t)a.splits), T::NT, 0, s>>>(a);
   return hipGetLastError();
 }
 
 TileOp mx_operand(const QView& q) {
-  TileOp o;
+  TileOp o = {};
   o.p = q.codes;
   o.s = q.s16;
   o.rows = q.rows;
@@ -374,35 +433,103 @@ TileOp mx_operand(const QView& q) {
   return o;
 }
 
-}  // namespace
+// Rows of A that mx_few_kernel takes: one instruction tile (with more, the 64 x 64
+// tiles are as fast: 24 x 50304 over 1024 11.8 us here and 9.8 there, 64 x 4096 9.2 and
+// 5.3; 1 x 4096 4.5 and 5.0, and the quantization of A included).
+using Few = Skinny<EL_MX, 1, 64 * 1024>;
+bool mx_few(int64_t I, int64_t K) { return Few::fits(I, (K + 127) / 128 * 64); }
 
-int mx_gemm_splits(int64_t I, int64_t J, int64_t K) {
-  const int64_t tiles = ((I + 255) / 256) * ((J + 255) / 256), nch = (K + 255) / 256;
-  int64_t z = 256 / std::max<int64_t>(tiles, 1);
-  z = std::min<int64_t>(z, nch / 4);
-  return (int)std::max<int64_t>(z, 1);
+// Tile and splits of a product, by an estimate of its time from what the tiles
+// measure (us on MI355X; a chunk is 256 elements of the reduction): alone on its CU
+// a tile of 64 / 128 / 256 takes 0.6 / 1.15 / 2.3 a chunk, with the CU full (4 / 2 / 1
+// workgroups) 1.3 / 1.6 / 2.3, and 2 to 5 for its start and its results.  A split
+// costs a launch and its fp32 partial sums, written and read.  Of 4096 x 1024
+// results over 4096: 23.6, 20.8, 36.5 unsplit; over 16384: 79.8, 68.7 unsplit, 65.0
+// (128, two splits); of 256 x 4096 over 4096: 11.3 (64), 18.1, 30.7.
+struct MxPlan {
+  int tile, splits;
+};
+MxPlan mx_plan(int64_t I, int64_t J, int64_t K) {
+  constexpr double kAlone[3] = {0.6, 1.15, 2.3}, kFull[3] = {1.3, 1.6, 2.3}, kFixed[3] = {2.0, 2.5, 5.0};
+  constexpr int kSlots[3] = {4, 2, 1};
+  const int64_t nch = (K + 255) / 256;
+  MxPlan best = {0, 1};
+  double least = 1e30;
+  for (int tile = 0; tile < 3; ++tile) {
+    const int64_t b = 64 << tile, n = ((I + b - 1) / b) * ((J + b - 1) / b), slots = kCus * kSlots[tile];
+    for (int z = 1; z <= 16 && z * 4 <= std::max<int64_t>(nch, 4); z *= 2) {
+      const int64_t items = n * z, full = items / slots, rest = items % slots, deep = (rest + kCus - 1) / kCus;
+      const double chunks = (double)((nch + z - 1) / z);
+      double t = (double)full * (chunks * kFull[tile] + kFixed[tile]);
+      if (rest) {
+        const double per = kSlots[tile] > 1 ? kAlone[tile] + (kFull[tile] - kAlone[tile]) * (double)(deep - 1) / (kSlots[tile] - 1) : kFull[tile];
+        t += chunks * per + kFixed[tile];
+      }
+      if (z > 1) t += 3.0 + (double)I * (double)J * 8.0 * z / 6e6;
+      if (t < least) {
+        least = t;
+        best = MxPlan{tile, z};
+      }
+    }
+  }
+  return best;
 }
 
+}  // namespace
+
 size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K) {
-  const int z = mx_gemm_splits(I, J, K);
+  if (mx_few(I, K)) return 0;
+  const int z = mx_plan(I, J, K).splits;
   return z > 1 ? (size_t)z * (size_t)I * (size_t)J * 4 : 0;
 }
 
-hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
-                          hipStream_t s) {
+namespace {
+// The product of few rows, if it is one; x: quantize them first, into `q`.
+bool launch_mx_few(const MxGemmArgs& a, const void* x, int64_t cols, const QView* q, hipStream_t s) {
+  if (!Few::fits(a.Q.rows, a.P.kb)) return false;
+  MxFewArgs f = {};
+  f.g = a;
+  f.x = reinterpret_cast<const uint16_t*>(x);
+  f.cols = (int32_t)cols;
+  if (q) {
+    f.codes = q->codes;
+    f.scale = q->s16;
+  }
+  mx_few_kernel<Few><<<Few::grid(a.P.rows), Few::NT, 0, s>>>(f);
+  return true;
+}
+
+MxGemmArgs mx_gemm_args(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate) {
   MxGemmArgs a = {};
   a.P = mx_operand(B);
   a.Q = mx_operand(A);
   a.C = C;
   a.ldc = ldc;
   a.nch = (int32_t)((A.nb + 1) / 2);
+  a.splits = 1;
   a.bf16 = c_dtype == TJ2_BF16;
   a.accumulate = accumulate;
   const int64_t es = a.bf16 ? 2 : 4;
   a.vec = (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && (ldc * es) % 16 == 0;
+  return a;
+}
+}  // namespace
+
+bool launch_mx_linear_few(const void* X, const QView& Xq, const QView& Wq, void* Y, int y_dtype, hipStream_t s) {
+  return launch_mx_few(mx_gemm_args(Xq, Wq, Y, y_dtype, Wq.rows, 0), X, Xq.len, &Xq, s);
+}
+
+hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
+                          hipStream_t s) {
+  MxGemmArgs a = mx_gemm_args(A, B, C, c_dtype, ldc, accumulate);
+  if (launch_mx_few(a, nullptr, 0, nullptr, s)) return hipGetLastError();
   a.partial = partial;
-  a.splits = partial ? mx_gemm_splits(A.rows, B.rows, A.len) : 1;
-  if (a.splits == 1) return launch_tile<TileBig>(a, s);
+  const MxPlan plan = mx_plan(A.rows, B.rows, A.len);
+  a.splits = partial ? plan.splits : 1;
+  auto launch = [&](const MxGemmArgs& g) {
+    return plan.tile == 2 ? launch_tile<TileBig>(g, s) : plan.tile == 1 ? launch_tile<TileMid>(g, s) : launch_tile<TileSmall>(g, s);
+  };
+  if (a.splits == 1) return launch(a);
   MxGemmArgs part = a;
   part.C = partial;
   part.ldc = B.rows;
@@ -410,7 +537,7 @@ hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, 
   part.bf16 = 0;
   part.accumulate = 0;
   part.vec = (B.rows & 3) == 0;
-  if (hipError_t e = launch_tile<TileBig>(part, s); e != hipSuccess) return e;
+  if (hipError_t e = launch(part); e != hipSuccess) return e;
   const int64_t n = A.rows * ((B.rows + 3) / 4);
   mx_join_kernel<<<(uint32_t)((n + 255) / 256), 256, 0, s>>>(a);
   return hipGetLastError();

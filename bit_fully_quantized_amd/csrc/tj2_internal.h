@@ -159,8 +159,8 @@ bool gemm_image_two_segments(const GemmParams& p);
 hipError_t launch_gemm(const GemmParams& p, hipStream_t s);
 
 // MXFP4 (mx.hip): quantiser of a dense or (column grouping) MXFP4 input, the
-// values of codes, and the product C = A B^T with the reduction split over
-// mx_gemm_splits() workgroups when `partial` is given.
+// values of codes, and the product C = A B^T, whose reduction may be split when
+// `partial` (mx_gemm_workspace_bytes) is given.
 struct MxQuantParams {
   int in_dtype;  // TJ2_BF16, TJ2_F32 or TJ2_MXFP4
   const void* x;
@@ -174,10 +174,13 @@ struct MxQuantParams {
 };
 hipError_t launch_mx_quant(const MxQuantParams& q, hipStream_t s);
 hipError_t launch_mx_values(const QView& q, void* out, int dtype, hipStream_t s);
-int mx_gemm_splits(int64_t I, int64_t J, int64_t K);
 size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K);
 hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
                           hipStream_t s);
+
+// The linear layer's forward for few rows in one launch, X's quantization into Xq
+// included; false: too many rows, nothing was launched.
+bool launch_mx_linear_few(const void* X, const QView& Xq, const QView& Wq, void* Y, int y_dtype, hipStream_t s);
 
 // Cross entropy of X W^T (loss.hip): bf16 X [T, K] at pitch ldx, W [V, K] at ldw.
 struct CeParams {

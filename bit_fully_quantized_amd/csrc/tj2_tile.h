@@ -136,10 +136,7 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t 
   tn = __builtin_amdgcn_readfirstlane(in / rows);
 }
 
-// Workgroups of a launch over `items` tiles: one a CU (their LDS fills it), each
-// going on to further tiles by itself.
-constexpr uint32_t kTileGrid = 256;
-inline uint32_t tile_grid(uint64_t items) { return (uint32_t)(items < kTileGrid ? items : kTileGrid); }
+constexpr uint32_t kCus = 256;
 
 template <int EL, int WM, int WN, int TM, int TN>
 struct Tile {
@@ -155,6 +152,14 @@ struct Tile {
   static_assert(RPI >= 2 * TN && RPI % 32 == 0, "a thread's rows i * RPI + r differ from r by bits of the key above its own");
   static_assert(TN == 1 || TN % 2 == 0, "q_place pairs rows");
   static_assert(TM % PB == 0, "whole row blocks");
+
+  // Workgroups a CU holds at once (by LDS; at most 16 waves, which then have 128
+  // registers each), and those of a launch over `items` tiles: as many as run at once,
+  // each going on to further tiles itself.
+  static constexpr int kLds = (ROWS * 128 + SCALE_DW * 4) * 2;
+  static constexpr int PER_CU = 160 * 1024 / kLds < 1024 / NT ? 160 * 1024 / kLds : 1024 / NT;
+  static constexpr int WAVES = PER_CU * NT / 256;  // waves a SIMD then holds
+  static uint32_t grid(uint64_t items) { return (uint32_t)(items < kCus * PER_CU ? items : kCus * PER_CU); }
 
   struct Smem {
     uint8_t stage[2][ROWS * 128];
@@ -366,10 +371,9 @@ struct Tile {
     using S1 = std::integral_constant<int, 1>;
     // the tiles of the second step before which the barrier is crossed
     constexpr int LEAD = TM >= 4 ? 2 : 1;
-    // loads are dealt out over the instruction tiles, so that no burst of them keeps
-    // the waves from issuing: LATE of them are left for the next chunk's first step
-    constexpr int SLOTS = TM - LEAD, EARLY = (LOADS + SLOTS - 1) / SLOTS <= 1 ? LOADS : SLOTS;
-    constexpr int LATE = LOADS > EARLY ? LOADS - EARLY : 0;
+    // the next chunk's loads are dealt out over the instruction tiles after it, so that
+    // no burst of them keeps the waves from issuing
+    constexpr int SLOTS = TM - LEAD + 1;
     begin(0);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) load(i);
@@ -377,7 +381,7 @@ struct Tile {
     tile_barrier();
     begin(1);
 #pragma unroll
-    for (int i = 0; i < LOADS - LATE; ++i) load(i);
+    for (int i = 0; i < LOADS; ++i) load(i);
     // Every chunk runs the same straight line: past the last item the loads bring
     // zeros, and the fragments read then are not used.
     uint32_t st = 0, at = items.at;
@@ -407,9 +411,6 @@ struct Tile {
           mma(S0{}, tmc);
           __builtin_amdgcn_sched_barrier(0);
           read_p(st, 1, tm);
-#pragma unroll
-          for (int i = LOADS - LATE; i < LOADS; ++i)
-            if ((i - (LOADS - LATE)) * TM / (LATE > 0 ? LATE : 1) == tm) load(i);
         });
         advance();
         static_for<TM>([&](auto tmc) __attribute__((always_inline)) {
@@ -437,8 +438,8 @@ struct Tile {
           }
           if constexpr (tm >= LEAD - 1) {
 #pragma unroll
-            for (int i = 0; i < LOADS - LATE; ++i)
-              if (i * (SLOTS + 1) / (LOADS - LATE) == tm - (LEAD - 1)) load(i);
+            for (int i = 0; i < LOADS; ++i)
+              if (i * SLOTS / LOADS == tm - (LEAD - 1)) load(i);
           }
         });
         if constexpr (EL == EL_MX) {
