@@ -749,7 +749,6 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
 // ---- distillation -------------------------------------------------------------------
 namespace {
 
-constexpr int kDistillThreads = 512;
 constexpr int kDistillMaxK = 512;
 
 template <class T>
@@ -794,19 +793,6 @@ struct Vec<uint16_t> {
   }
 };
 
-template <class F>
-__device__ __forceinline__ float block_reduce(float v, float* sh, F f) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v = f(v, __shfl_xor(v, o));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = sh[0];
-#pragma unroll
-  for (int i = 1; i < kDistillThreads / 64; ++i) v = f(v, sh[i]);
-  return v;
-}
-
 struct MaxOp {
   // NaN is kept: a row with one has a NaN loss
   __device__ __forceinline__ float operator()(float a, float b) const { return a > b || a != a ? a : b; }
@@ -814,6 +800,33 @@ struct MaxOp {
 struct SumOp {
   __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
+
+// 16 bytes that pass through once: without the caches' keeping them
+__device__ __forceinline__ uint4 stream_load(const uint4* p) {
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p)));
+}
+__device__ __forceinline__ void stream_store(uint4* p, const uint4& v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), reinterpret_cast<u32x4_t*>(p));
+}
+
+// K values of every thread reduced over the workgroup (sh: its own LDS per call).
+template <int WAVES, int K, class F>
+__device__ __forceinline__ void block_reduce(float (&v)[K], float (*sh)[K], F f) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = f(v[k], __shfl_xor(v[k], o));
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) sh[threadIdx.x >> 6][k] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    v[k] = sh[threadIdx.x % WAVES][k];
+#pragma unroll
+    for (int o = WAVES / 2; o; o >>= 1) v[k] = f(v[k], __shfl_xor(v[k], o));
+  }
+}
 
 struct DistillArgs {
   const void* z;
@@ -834,29 +847,30 @@ struct DistillArgs {
 // Elements before the first and after the last aligned vector are one per thread;
 // HARD: the hard target's term is there too (a second sum of exponentials at
 // temperature 1).
-template <class T, int R, bool HARD>
-__global__ __launch_bounds__(kDistillThreads) void distill_kernel(DistillArgs p) {
-  constexpr int N = Vec<T>::N;
+template <class T, int R, bool HARD, int kThreads>
+__global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distill_kernel(DistillArgs p) {
+  constexpr int N = Vec<T>::N, WAVES = kThreads / 64;
   constexpr int RR = R > 0 ? R : 1;
-  __shared__ float sh[kDistillThreads / 64];
-  __shared__ int32_t id[kDistillMaxK];
-  __shared__ float pr[kDistillMaxK], zi[kDistillMaxK];
+  __shared__ float sh_max[WAVES][2], sh_sum[WAVES][4];
+  __shared__ __attribute__((aligned(16))) int32_t id[kDistillMaxK];
+  __shared__ float pr[kDistillMaxK];
+  __shared__ int32_t named;  // the hard target is among the teacher's entries
   const int t = threadIdx.x;
   const int64_t row = blockIdx.x;
   const T* z = reinterpret_cast<const T*>(p.z) + row * p.ldz;
   T* dz = p.dz ? reinterpret_cast<T*>(p.dz) + row * p.ldd : nullptr;
-  const int64_t V = p.V;
+  const int V = (int)p.V;  // at most 2^30
   const int64_t y = p.y ? p.y[row] : 0;
   const bool on = !p.y || y != p.ignore;
   const float w = p.w ? p.w[row] : 1.0f;
 
   // aligned middle [head, head + N * nv)
-  const int head = (int)min((int64_t)(((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / sizeof(T)), V);
-  const int64_t nv = (V - head) / N;
-  const int tail = (int)(V - head - nv * N);
+  const int head = min((int)(((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / sizeof(T)), V);
+  const int nv = (V - head) / N;
+  const int tail = V - head - nv * N;
   const uint4* zv = reinterpret_cast<const uint4*>(z + head);
   const bool edge = t < head + tail;
-  const int64_t ei = t < head ? t : V - tail + (t - head);
+  const int ei = t < head ? t : V - tail + (t - head);
   // the gradient's vectors: the same places, if its row is aligned alike
   const bool vec_out = dz && (((reinterpret_cast<uintptr_t>(dz) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0);
 
@@ -864,16 +878,16 @@ __global__ __launch_bounds__(kDistillThreads) void distill_kernel(DistillArgs p)
     if (t == 0 && p.loss) p.loss[row] = 0.0f;
     if (dz) {
       if (vec_out)
-        for (int64_t i = t; i < nv; i += kDistillThreads) reinterpret_cast<uint4*>(dz + head)[i] = uint4{0u, 0u, 0u, 0u};
+        for (int i = t; i < nv; i += kThreads) reinterpret_cast<uint4*>(dz + head)[i] = uint4{0u, 0u, 0u, 0u};
       else
-        for (int64_t i = t; i < nv * N; i += kDistillThreads) dz[head + i] = from_f32<T>(0.0f);
+        for (int i = t; i < nv * N; i += kThreads) dz[head + i] = from_f32<T>(0.0f);
       if (edge) dz[ei] = from_f32<T>(0.0f);
     }
     return;
   }
 
   uint4 q[RR];
-  auto vec = [&](int r, int64_t i) __attribute__((always_inline)) -> uint4 {
+  auto vec = [&](int r, int i) __attribute__((always_inline)) -> uint4 {
     if constexpr (R > 0) return q[r];
     return zv[i];
   };
@@ -882,18 +896,21 @@ __global__ __launch_bounds__(kDistillThreads) void distill_kernel(DistillArgs p)
     if constexpr (R > 0) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int64_t i = t + r * kDistillThreads;
+        const int i = t + r * kThreads;
         if (i < nv) f(r, i);
+        // one vector at a time: interleaved, their temporaries would take the
+        // registers that let another row share the CU
+        __builtin_amdgcn_sched_barrier(0);
       }
     } else {
-      for (int64_t i = t; i < nv; i += kDistillThreads) f(0, i);
+      for (int i = t; i < nv; i += kThreads) f(0, i);
     }
   };
   if constexpr (R > 0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t i = t + r * kDistillThreads;
-      if (i < nv) q[r] = zv[i];
+      const int i = t + r * kThreads;
+      if (i < nv) q[r] = stream_load(zv + i);
     }
   }
   const float ze = edge ? to_f32<T>(z[ei]) : 0.0f;
@@ -904,47 +921,70 @@ __global__ __launch_bounds__(kDistillThreads) void distill_kernel(DistillArgs p)
   // the teacher's probabilities: softmax of its kept logits over tau
   const bool has_k = t < p.k;
   int32_t my = -1;
-  float u = -INFINITY;
+  float u = -INFINITY, zm = 0.0f;
   if (has_k) {
     my = p.ids[row * p.k + t];
-    if (my >= 0 && my < V) u = to_f32<T>(reinterpret_cast<const T*>(p.u)[row * p.k + t]) / p.tau;
-    id[t] = my;
-    zi[t] = my >= 0 && my < V ? to_f32<T>(z[my]) : 0.0f;
+    if (my >= 0 && my < V) {
+      u = to_f32<T>(reinterpret_cast<const T*>(p.u)[row * p.k + t]) / p.tau;
+      zm = to_f32<T>(z[my]);
+    }
+  }
+  if (t < ((p.k + 3) & ~3)) id[t] = my;
+  if (HARD && t == 0) named = 0;
+  __syncthreads();
+  // an entry that is listed twice is written once, by its first place
+  bool first = true, again = false;
+  if (has_k && my >= 0 && my < V) {
+    for (int j = 0; j < p.k; j += 4) {
+      const int4 o = *reinterpret_cast<const int4*>(id + j);
+      const int same = (o.x == my) | (o.y == my) << 1 | (o.z == my) << 2 | (o.w == my) << 3;
+      if (j <= t) {
+        const int before = t - j < 4 ? same & ((1 << (t - j)) - 1) : same;
+        first &= before == 0;
+      }
+      again |= (t - j >= 0 && t - j < 4 ? same & ~(1 << (t - j)) : same) != 0;
+    }
+    if (HARD && my == y) named = 1;
   }
   const bool kept = has_k && my >= 0;
   float m = edge ? ze : -INFINITY;
-  each([&](int r, int64_t i) __attribute__((always_inline)) {
+  each([&](int r, int i) __attribute__((always_inline)) {
     float v[N];
     Vec<T>::get(vec(r, i), v);
 #pragma unroll
     for (int k = 0; k < N; ++k) m = MaxOp{}(m, v[k]);
   });
-  m = block_reduce(m, sh, MaxOp{});
-  const float mu = block_reduce(u, sh, MaxOp{});
+  float top[2] = {m, u};
+  block_reduce<WAVES>(top, sh_max, MaxOp{});
+  m = top[0];
+  const float mu = top[1];
   const bool some = mu != -INFINITY;  // the teacher kept something of this row
   const float ctau = kLog2e / p.tau;
-  float st = edge ? exp_scaled(ze, m, ctau) : 0.0f;
-  float s1 = HARD && edge ? exp_scaled(ze, m, kLog2e) : 0.0f;
-  each([&](int r, int64_t i) __attribute__((always_inline)) {
+  // sums: exp(z / tau), exp(z), the teacher's exp(u), and sum of those times
+  // (u - mu) - (z - m) / tau, of which the divergence is made
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (edge) {
+    sum[0] = exp_scaled(ze, m, ctau);
+    if constexpr (HARD) sum[1] = exp_scaled(ze, m, kLog2e);
+  }
+  each([&](int r, int i) __attribute__((always_inline)) {
     float v[N];
     Vec<T>::get(vec(r, i), v);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      st += exp_scaled(v[k], m, ctau);
-      if constexpr (HARD) s1 += exp_scaled(v[k], m, kLog2e);
+      sum[0] += exp_scaled(v[k], m, ctau);
+      if constexpr (HARD) sum[1] += exp_scaled(v[k], m, kLog2e);
     }
   });
-  st = block_reduce(st, sh, SumOp{});
-  if constexpr (HARD) s1 = block_reduce(s1, sh, SumOp{});
   const float eu = kept && some ? __builtin_amdgcn_exp2f((u - mu) * kLog2e) : 0.0f;
-  const float su = block_reduce(eu, sh, SumOp{});
+  sum[2] = eu;
+  if (eu > 0.0f || eu != eu) sum[3] = eu * ((u - mu) - (zm - m) / p.tau);
+  if (kept && my >= V) sum[3] = kNan;  // an id outside the vocabulary makes the row NaN
+  block_reduce<WAVES>(sum, sh_sum, SumOp{});
+  const float st = sum[0], s1 = sum[1], su = sum[2];
   const float pt = some ? eu / su : 0.0f;
-  const float lt = __builtin_amdgcn_logf(st) * kLn2;  // lse / tau - m / tau
-  // an id outside the vocabulary makes the row NaN
-  const float wrong = kept && my >= V ? kNan : 0.0f;
-  float kl = wrong;
-  if (pt > 0.0f || pt != pt) kl += pt * ((u - mu) - __builtin_amdgcn_logf(su) * kLn2 - ((zi[t] - m) / p.tau - lt));
-  kl = block_reduce(kl, sh, SumOp{});
+  // sum p (log p - log q) = sum p ((u - mu) - (z - m) / tau) - log su + log st
+  const float kl = some ? sum[3] / su + (__builtin_amdgcn_logf(st) - __builtin_amdgcn_logf(su)) * kLn2 : sum[3];
   float loss = p.alpha > 0.0f ? p.alpha * p.tau * p.tau * kl : 0.0f;
   if constexpr (HARD) loss += (1.0f - p.alpha) * (m + __builtin_amdgcn_logf(s1) * kLn2 - zy);
   if (t == 0 && p.loss) p.loss[row] = loss;
@@ -961,53 +1001,58 @@ __global__ __launch_bounds__(kDistillThreads) void distill_kernel(DistillArgs p)
     return g;
   };
   if (has_k) pr[t] = pt;
-  each([&](int r, int64_t i) __attribute__((always_inline)) {
+  each([&](int r, int i) __attribute__((always_inline)) {
     float v[N];
     Vec<T>::get(vec(r, i), v);
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = grad(v[k]);
     if (vec_out) {
-      reinterpret_cast<uint4*>(dz + head)[i] = Vec<T>::put(v);
+      stream_store(reinterpret_cast<uint4*>(dz + head) + i, Vec<T>::put(v));
     } else {
 #pragma unroll
       for (int k = 0; k < N; ++k) dz[head + i * N + k] = from_f32<T>(v[k]);
     }
   });
   if (edge) dz[ei] = from_f32<T>(grad(ze));
-  __syncthreads();  // the row is written, pr and id are there
-  // an entry that is listed twice is written once, by its first place
-  if (has_k && my >= 0 && my < V) {
-    float sum = 0.0f;
-    bool first = true;
-    for (int j = 0; j < p.k; ++j) {
-      if (id[j] != my) continue;
-      if (j < t) first = false;
-      sum += pr[j];
+  // the row is written before its few other entries are: by waves of their own, so the
+  // stores themselves are waited for
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (has_k && my >= 0 && my < V && first) {
+    float mass = pt;
+    if (again) {
+      mass = 0.0f;
+      for (int j = t; j < p.k; ++j)
+        if (id[j] == my) mass += pr[j];
     }
-    if (first) {
-      float g = grad(zi[t]) - at * sum;
-      if (HARD && my == y) g -= a1;
-      dz[my] = from_f32<T>(g);
-    }
+    float g = grad(zm) - at * mass;
+    if (HARD && my == y) g -= a1;
+    dz[my] = from_f32<T>(g);
   }
   if constexpr (HARD) {
-    if (t == 0 && (uint64_t)y < (uint64_t)V) {
-      bool listed = false;
-      for (int j = 0; j < p.k; ++j) listed |= id[j] == y;
-      if (!listed) dz[y] = from_f32<T>(grad(zy) - a1);
-    }
+    if (t == 0 && (uint64_t)y < (uint64_t)V && !named) dz[y] = from_f32<T>(grad(zy) - a1);
   }
 }
 
+// Few rows: 1024 threads each, so that one row takes less time; many: 512, of which
+// three rows fit a CU at R = 13 and cover each other's loads and stores.
 template <class T, bool HARD>
 void launch_distill_r(const DistillArgs& a, hipStream_t s) {
-  const int64_t nv = a.V / Vec<T>::N, r = (nv + kDistillThreads - 1) / kDistillThreads;
+  const bool few = a.T < 512;
+  const int64_t nv = a.V / Vec<T>::N, r = (nv + (few ? 1023 : 511)) / (few ? 1024 : 512);
   const uint32_t grid = (uint32_t)a.T;
-  if (r <= 4) distill_kernel<T, 4, HARD><<<grid, kDistillThreads, 0, s>>>(a);
-  else if (r <= 8) distill_kernel<T, 8, HARD><<<grid, kDistillThreads, 0, s>>>(a);
-  else if (r <= 13) distill_kernel<T, 13, HARD><<<grid, kDistillThreads, 0, s>>>(a);
-  else if (r <= 20) distill_kernel<T, 20, HARD><<<grid, kDistillThreads, 0, s>>>(a);
-  else distill_kernel<T, 0, HARD><<<grid, kDistillThreads, 0, s>>>(a);
+  if (few) {
+    if (r <= 4) distill_kernel<T, 4, HARD, 1024><<<grid, 1024, 0, s>>>(a);
+    else if (r <= 8) distill_kernel<T, 8, HARD, 1024><<<grid, 1024, 0, s>>>(a);
+    else if (r <= 13) distill_kernel<T, 13, HARD, 1024><<<grid, 1024, 0, s>>>(a);
+    else distill_kernel<T, 0, HARD, 1024><<<grid, 1024, 0, s>>>(a);
+  } else {
+    if (r <= 4) distill_kernel<T, 4, HARD, 512><<<grid, 512, 0, s>>>(a);
+    else if (r <= 8) distill_kernel<T, 8, HARD, 512><<<grid, 512, 0, s>>>(a);
+    else if (r <= 13) distill_kernel<T, 13, HARD, 512><<<grid, 512, 0, s>>>(a);
+    else if (r <= 26) distill_kernel<T, 26, HARD, 512><<<grid, 512, 0, s>>>(a);
+    else distill_kernel<T, 0, HARD, 512><<<grid, 512, 0, s>>>(a);
+  }
 }
 
 }  // namespace
