@@ -465,7 +465,7 @@ MxPlan mx_plan(int64_t I, int64_t J, int64_t K) {
         const double per = kSlots[tile] > 1 ? kAlone[tile] + (kFull[tile] - kAlone[tile]) * (double)(deep - 1) / (kSlots[tile] - 1) : kFull[tile];
         t += chunks * per + kFixed[tile];
       }
-      if (z > 1) t += 3.0 + (double)I * (double)J * 8.0 * z / 6e6;
+      if (z > 1) t += 3.0 + (double)I * (double)J * 8.0 * z / 5e6;
       if (t < least) {
         least = t;
         best = MxPlan{tile, z};

@@ -372,8 +372,10 @@ struct Tile {
     // the tiles of the second step before which the barrier is crossed
     constexpr int LEAD = TM >= 4 ? 2 : 1;
     // the next chunk's loads are dealt out over the instruction tiles after it, so that
-    // no burst of them keeps the waves from issuing
-    constexpr int SLOTS = TM - LEAD + 1;
+    // no burst of them keeps the waves from issuing; in large tiles, whose chunks take
+    // longest, two are left for the next step (forward of 16384 x 50304 over 1024: 1483
+    // us without, 1452 with; with four 1507; 128 x 128 tiles lose by it)
+    constexpr int SLOTS = TM - LEAD + 1, LATE = TM >= 8 ? 2 : 0;
     begin(0);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) load(i);
@@ -381,7 +383,7 @@ struct Tile {
     tile_barrier();
     begin(1);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) load(i);
+    for (int i = 0; i < LOADS - LATE; ++i) load(i);
     // Every chunk runs the same straight line: past the last item the loads bring
     // zeros, and the fragments read then are not used.
     uint32_t st = 0, at = items.at;
@@ -411,6 +413,9 @@ struct Tile {
           mma(S0{}, tmc);
           __builtin_amdgcn_sched_barrier(0);
           read_p(st, 1, tm);
+#pragma unroll
+          for (int i = LOADS - LATE; i < LOADS; ++i)
+            if ((i - (LOADS - LATE)) * TM / 2 == tm) load(i);
         });
         advance();
         static_for<TM>([&](auto tmc) __attribute__((always_inline)) {
@@ -438,8 +443,8 @@ struct Tile {
           }
           if constexpr (tm >= LEAD - 1) {
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i)
-              if (i * SLOTS / LOADS == tm - (LEAD - 1)) load(i);
+            for (int i = 0; i < LOADS - LATE; ++i)
+              if (i * SLOTS / (LOADS - LATE) == tm - (LEAD - 1)) load(i);
           }
         });
         if constexpr (EL == EL_MX) {
