@@ -18,6 +18,13 @@ give no OLMo-2 details; the layout here (pre-norm blocks, RoPE theta 10000,
 With linear="bf16" the same stack runs its linear layers as bf16 products
 (torch.mm, hipBLASLt) on bf16 copies of the masters, with AdamW on the
 masters: the comparator of the pages' end-to-end speed figure on this part.
+With linear="mxfp4" they are MXFP4 linears (mx.py) under the same backward
+recipe (stochastic rounding after the Hadamard transform), with AdamW on the
+masters, which are quantized once a step.
+
+With head="fused" the head is a bf16 product whose cross entropy is taken
+without the logits (losses.py), whatever the other linears are.  train_step
+learns from a teacher's top logits where it is given them (distillation).
 """
 from __future__ import annotations
 
@@ -31,6 +38,8 @@ from torch.nn.attention import SDPBackend, sdpa_kernel
 from . import (FP8, NVFP4, OSCI_ACCUM, OSCI_INIT, OSCI_WINDOW_END, MasterBatch, NextBwd, QTensor, bwd_operands,
                channel_sumsq, lib, linear_bwd, linear_fwd, master_update_step_multi, osci_reset_step,
                select_outliers)
+from .losses import distillation_loss, linear_cross_entropy
+from .mx import mx_linear_bwd, mx_linear_bwd_workspace_size, mx_linear_fwd, mx_quantize
 
 
 @dataclass
@@ -57,7 +66,10 @@ class DecoderConfig:
     norm_eps: float = 1e-6
     init_std: float = 0.02
     seed: int = 0                   # parameters and Philox stream
-    linear: str = "nvfp4"           # "nvfp4" (libtj2) or "bf16" (comparator)
+    linear: str = "nvfp4"           # "nvfp4", "mxfp4" (libtj2) or "bf16" (comparator)
+    head: str = "linear"            # "linear" (as the others) or "fused" (bf16, cross entropy without the logits)
+    distill_temperature: float = 1.0  # with a teacher: loss alpha tau^2 KL + (1 - alpha) cross entropy
+    distill_alpha: float = 0.5
 
     @property
     def tokens(self) -> int:
@@ -88,10 +100,11 @@ class _LinearFn(torch.autograd.Function):
 class Linear:
     """One linear layer Y = X W^T of the stack (W [N, K]): the fp32 master with its AdamW moments and
     OsciReset state, the forward codes under the layer's outlier plan, and the next backward's
-    re-grouped weights that the master pass forms."""
+    re-grouped weights that the master pass forms.  kind "mxfp4": the MXFP4 codes of the master instead;
+    kind "fused": a bf16 copy Wg of the master, with a gradient of its own."""
 
-    def __init__(self, stack: "Decoder", idx: int, name: str, N: int, K: int, gen: torch.Generator):
-        self.stack, self.idx, self.name, self.N, self.K = stack, idx, name, N, K
+    def __init__(self, stack: "Decoder", idx: int, name: str, N: int, K: int, gen: torch.Generator, kind: str):
+        self.stack, self.idx, self.name, self.N, self.K, self.kind = stack, idx, name, N, K, kind
         dev = stack.device
         self.W = (torch.randn(N, K, generator=gen, device=dev) * stack.cfg.init_std).contiguous()
         self.grad = torch.zeros_like(self.W)
@@ -102,6 +115,7 @@ class Linear:
         self.w_given = False
         self.Wf = None       # bf16 comparator: bf16 copies of W^T [K, N] (forward) and W [N, K] (backward)
         self.Wg = None
+        self.Wq = None       # codes of the master: NVFP4 (under the plan) or MXFP4
 
     # ---- set-up ---------------------------------------------------------------------------------
     def finalize(self):
@@ -118,11 +132,40 @@ class Linear:
         self.next = NextBwd(QTensor(NVFP4, K1, self.N), QTensor(FP8, n, self.N) if n else None,
                             seed=self.stack.cfg.seed, offset=0, rht=True)
 
+    def prepare(self):
+        """The other kinds' buffers; W.grad is the gradient that AdamW on the masters reads."""
+        self.W.grad = self.grad
+        if self.kind == "bf16":
+            self.gradb = torch.empty(self.N, self.K, dtype=torch.bfloat16, device=self.W.device)
+            self.Wf = self.W.t().contiguous().to(torch.bfloat16)
+            self.Wg = self.W.to(torch.bfloat16)
+        elif self.kind == "fused":
+            self.Wg = self.W.to(torch.bfloat16).requires_grad_(True)
+        else:
+            self.Wq = mx_quantize(self.W)
+
+    def refresh(self):
+        """The products' operands of an updated master."""
+        if self.kind == "bf16":
+            self.Wf.copy_(self.W.t())
+            self.Wg.copy_(self.W)
+        elif self.kind == "fused":
+            with torch.no_grad():
+                self.Wg.copy_(self.W)
+            self.Wg.grad = None
+        else:
+            mx_quantize(self.W, out=self.Wq)
+
     # ---- products -------------------------------------------------------------------------------
     def forward(self, X: torch.Tensor):
         st = self.stack
-        if st.cfg.linear == "bf16":
+        if self.kind == "bf16":
             return torch.mm(X, self.Wf), X
+        if self.kind == "mxfp4":
+            Y, saved = mx_linear_fwd(X, None, self.N, Wq=self.Wq)
+            if self.capture is not None:
+                self.capture.update(X=X.clone(), W=self.W.clone(), Y=Y.clone(), step=st.step)
+            return Y, saved
         if st.calibrating:
             channel_sumsq(X, self.sumsq)
             return linear_fwd(X, self.W, self.N)
@@ -134,12 +177,18 @@ class Linear:
 
     def backward(self, dY: torch.Tensor, saved):
         st = self.stack
-        if st.cfg.linear == "bf16":
+        if self.kind == "bf16":
             X = saved
             torch.mm(dY.t(), X, out=self.gradb)
             self.grad.copy_(self.gradb)
             return torch.mm(dY, self.Wg)
         offset = st.offset(self.idx, st.step)
+        if self.kind == "mxfp4":
+            dX, _ = mx_linear_bwd(dY, saved, self.K, seed=st.cfg.seed, offset=offset, dW=self.grad,
+                                  workspace=st.mx_workspace(dY.shape[0], self.N, self.K))
+            if self.capture is not None:
+                self.capture.update(dY=dY.clone(), dX=dX.clone(), dW=self.grad.clone(), offset=offset)
+            return dX
         cap = self.capture
         ops = bwd_operands(dY.shape[0], self.N, self.K, self.plan) if cap is not None else dict(st.ops_for(self))
         if self.w_given:
@@ -155,6 +204,8 @@ class Linear:
         return dX
 
     def __call__(self, X):
+        if self.kind == "fused":
+            return F.linear(X, self.Wg)
         return _LinearFn.apply(X, self)
 
 
@@ -163,7 +214,8 @@ class Decoder:
 
     def __init__(self, cfg: DecoderConfig, device="cuda"):
         self.cfg, self.device = cfg, device
-        assert cfg.d_model % cfg.heads == 0 and cfg.linear in ("nvfp4", "bf16")
+        assert cfg.d_model % cfg.heads == 0 and cfg.linear in ("nvfp4", "mxfp4", "bf16")
+        assert cfg.head in ("linear", "fused")
         g = torch.Generator(device=device)
         g.manual_seed(cfg.seed)
         d = cfg.d_model
@@ -172,8 +224,8 @@ class Decoder:
         self.blocks = []
         self.linears = []
 
-        def lin(name, N, K):
-            L = Linear(self, len(self.linears), name, N, K, g)
+        def lin(name, N, K, kind=cfg.linear):
+            L = Linear(self, len(self.linears), name, N, K, g, kind)
             self.linears.append(L)
             return L
 
@@ -184,7 +236,9 @@ class Decoder:
                 "mlp_norm": torch.ones(d, device=device, requires_grad=True),
                 "gate": lin(f"{i}.gate", cfg.ffn, d), "up": lin(f"{i}.up", cfg.ffn, d),
                 "down": lin(f"{i}.down", d, cfg.ffn)})
-        self.head = lin("head", cfg.vocab, d)
+        self.head = lin("head", cfg.vocab, d, "fused" if cfg.head == "fused" else cfg.linear)
+        self.nvfp4 = [L for L in self.linears if L.kind == "nvfp4"]   # updated by the fused master pass
+        self.others = [L for L in self.linears if L.kind != "nvfp4"]  # by AdamW on the masters
         norms = [self.final_norm] + [b[k] for b in self.blocks for k in ("attn_norm", "mlp_norm")]
         self.glue_opt = torch.optim.AdamW([{"params": [self.emb], "weight_decay": cfg.weight_decay},
                                            {"params": norms, "weight_decay": 0.0}],
@@ -198,6 +252,7 @@ class Decoder:
         self.ready = False
         self._ops = {}
         self.bwd_ws = None
+        self._mx_ws = None
         self.reset_count = torch.zeros(1, dtype=torch.int64, device=device)
 
     # ---- glue -------------------------------------------------------------------------------------
@@ -210,8 +265,8 @@ class Decoder:
         c, s = self.cos[: t.shape[2]], self.sin[: t.shape[2]]
         return torch.stack((t1 * c - t2 * s, t1 * s + t2 * c), dim=-1).flatten(-2).to(torch.bfloat16)
 
-    def forward(self, tokens: torch.Tensor) -> torch.Tensor:
-        """Logits [B*S, vocab] (bf16) of tokens [B, S]."""
+    def hidden(self, tokens: torch.Tensor) -> torch.Tensor:
+        """The head's input [B*S, d_model] (bf16) of tokens [B, S]."""
         cfg = self.cfg
         B, S = tokens.shape
         M, d, H = B * S, cfg.d_model, cfg.heads
@@ -225,7 +280,24 @@ class Decoder:
             h = self._rmsnorm(x, blk["mlp_norm"])
             a = F.silu(blk["gate"](h)) * blk["up"](h)
             x = x + blk["down"](a.contiguous())
-        return self.head(self._rmsnorm(x, self.final_norm))
+        return self._rmsnorm(x, self.final_norm)
+
+    def forward(self, tokens: torch.Tensor) -> torch.Tensor:
+        """Logits [B*S, vocab] (bf16) of tokens [B, S]."""
+        return self.head(self.hidden(tokens))
+
+    def loss(self, tokens: torch.Tensor, targets: torch.Tensor, teacher=None) -> torch.Tensor:
+        """Mean loss of next-token targets [B, S] (targets of -100 are left out): cross entropy, or with
+        teacher = (ids int32 [B, S, k], logits bf16 [B, S, k]), a teacher's top logits of each token, the
+        distillation loss under the configuration's temperature and alpha."""
+        cfg, targets = self.cfg, targets.reshape(-1)
+        if teacher is not None:
+            ids, top = (t.reshape(targets.shape[0], -1) for t in teacher)
+            return distillation_loss(self.forward(tokens), ids, top, temperature=cfg.distill_temperature,
+                                     alpha=cfg.distill_alpha, targets=targets)
+        if self.head.kind == "fused":
+            return linear_cross_entropy(self.hidden(tokens), self.head.Wg, targets)
+        return F.cross_entropy(self.forward(tokens).float(), targets)
 
     # ---- set-up -----------------------------------------------------------------------------------
     def offset(self, idx: int, step: int) -> int:
@@ -238,73 +310,80 @@ class Decoder:
             self._ops[key] = bwd_operands(self.cfg.tokens, lin.N, lin.K, lin.plan)
         return self._ops[key]
 
+    def mx_workspace(self, M: int, N: int, K: int) -> torch.Tensor:
+        """One buffer for the MXFP4 backward passes, as large as the largest so far needs."""
+        n = mx_linear_bwd_workspace_size(M, N, K)
+        if self._mx_ws is None or self._mx_ws.numel() < n:
+            self._mx_ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return self._mx_ws
+
     def calibrate(self, batches):
-        """OutControl: the top p% input channels of every linear from a short calibration window
-        (forward passes with plain NVFP4 products), then the codes and OsciReset state under the plans."""
-        if self.cfg.linear == "nvfp4":
-            for L in self.linears:
+        """OutControl: the top p% input channels of every NVFP4 linear from a short calibration window
+        (forward passes with plain NVFP4 products), then the codes and OsciReset state under the plans.
+        The other linears have nothing to calibrate: their operands are formed from the masters."""
+        if self.others:
+            self.lin_opt = torch.optim.AdamW([L.W for L in self.others], lr=self.cfg.lr_start,
+                                             betas=(self.cfg.beta1, self.cfg.beta2), eps=self.cfg.eps,
+                                             weight_decay=self.cfg.weight_decay)
+            for L in self.others:
+                L.prepare()
+        if self.nvfp4:
+            for L in self.nvfp4:
                 L.sumsq = torch.zeros(L.K, dtype=torch.float64, device=self.device)
+            run = self.forward if self.head.kind == "nvfp4" else self.hidden
             self.calibrating = True
             with torch.no_grad():
                 for tokens in batches:
-                    self.forward(tokens)
+                    run(tokens)
             self.calibrating = False
-            for L in self.linears:
+            for L in self.nvfp4:
                 L.plan = select_outliers(L.sumsq, self.cfg.p_outliers, device=self.device)
                 L.sumsq = None
                 L.finalize()
             # split-K partial sums of the backward products (the operands have buffers of their own)
             M = self.cfg.tokens
             ws = max(max(int(lib().nvfp4_gemm_workspace_size(M, L.K, L.N, 0)),
-                          int(lib().nvfp4_gemm_workspace_size(L.N, L.K, M, 0))) for L in self.linears)
+                          int(lib().nvfp4_gemm_workspace_size(L.N, L.K, M, 0))) for L in self.nvfp4)
             self.bwd_ws = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
             self.master_batch = MasterBatch([(L.W, L.m, L.v, L.grad, L.Q_prev, L.dQ, L.dM, L.Wq, L.plan, L.W8, L.next)
-                                             for L in self.linears])
-        else:
-            self.lin_opt = torch.optim.AdamW([L.W for L in self.linears], lr=self.cfg.lr_start,
-                                             betas=(self.cfg.beta1, self.cfg.beta2), eps=self.cfg.eps,
-                                             weight_decay=self.cfg.weight_decay)
-            for L in self.linears:
-                L.W.grad = L.grad
-                L.gradb = torch.empty(L.N, L.K, dtype=torch.bfloat16, device=self.device)
-                L.Wf = L.W.t().contiguous().to(torch.bfloat16)
-                L.Wg = L.W.to(torch.bfloat16)
+                                             for L in self.nvfp4])
         self.ready = True
 
     # ---- training ---------------------------------------------------------------------------------
-    def train_step(self, tokens: torch.Tensor, targets: torch.Tensor, before_update=None) -> torch.Tensor:
+    def train_step(self, tokens: torch.Tensor, targets: torch.Tensor, before_update=None, teacher=None) -> torch.Tensor:
         """One optimizer step on one batch; returns the loss (a device scalar).  before_update(self),
-        if given, runs after the backward pass and before the optimizer updates (for inspection)."""
+        if given, runs after the backward pass and before the optimizer updates (for inspection).
+        teacher: a teacher's top logits for the batch, as loss() takes them."""
         assert self.ready, "calibrate() first"
         cfg = self.cfg
         t = self.step
         lr = cfg.lr(t)
-        logits = self.forward(tokens)
-        loss = F.cross_entropy(logits.float(), targets.reshape(-1))
+        loss = self.loss(tokens, targets, teacher)
         loss.backward()
+        if self.head.kind == "fused":
+            self.head.grad.copy_(self.head.Wg.grad)
         if before_update is not None:
             before_update(self)
         for grp in self.glue_opt.param_groups:
             grp["lr"] = lr
         self.glue_opt.step()
         self.glue_opt.zero_grad(set_to_none=True)
-        if cfg.linear == "nvfp4":
+        if self.nvfp4:
             bc1, bc2 = 1.0 - cfg.beta1 ** (t + 1), 1.0 - cfg.beta2 ** (t + 1)
             end = (t + 1) % cfg.window == 0
-            self.master_batch.set_next_offsets([self.offset(L.idx, t + 1) for L in self.linears])
+            self.master_batch.set_next_offsets([self.offset(L.idx, t + 1) for L in self.nvfp4])
             master_update_step_multi(self.master_batch, lr=lr, bias_correction1=bc1, bias_correction2=bc2,
                                      beta1=cfg.beta1, beta2=cfg.beta2, eps=cfg.eps, weight_decay=cfg.weight_decay,
                                      mode=OSCI_WINDOW_END if end else OSCI_ACCUM, tau=cfg.tau,
                                      reset_enabled=lr <= cfg.reset_lr, reset_count=self.reset_count)
-            for L in self.linears:
+            for L in self.nvfp4:
                 L.w_given = True
-        else:
+        if self.others:
             for grp in self.lin_opt.param_groups:
                 grp["lr"] = lr
             self.lin_opt.step()
-            for L in self.linears:
-                L.Wf.copy_(L.W.t())
-                L.Wg.copy_(L.W)
+            for L in self.others:
+                L.refresh()
         self.step += 1
         return loss.detach()
 

@@ -119,7 +119,8 @@ def _gemm_bytes(I: int, J: int, K: int) -> int:
 
 
 @lru_cache(maxsize=4096)
-def _bwd_bytes(M: int, N: int, K: int) -> int:
+def mx_linear_bwd_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes of the workspace of mx_linear_bwd."""
     return int(lib().mxfp4_linear_bwd_workspace_size(M, N, K))
 
 
@@ -173,7 +174,7 @@ def mx_linear_fwd(X: torch.Tensor, W_master: torch.Tensor | None, N: int, *, Wq:
 
 
 def mx_linear_bwd_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
-    return torch.empty(_bwd_bytes(M, N, K), dtype=torch.uint8, device=device)
+    return torch.empty(mx_linear_bwd_workspace_size(M, N, K), dtype=torch.uint8, device=device)
 
 
 def mx_linear_bwd(dY: torch.Tensor, saved: dict, K: int, *, seed: int, offset: int, rht: bool = True, rounding: int = SR,
@@ -188,7 +189,7 @@ def mx_linear_bwd(dY: torch.Tensor, saved: dict, K: int, *, seed: int, offset: i
         dX = torch.empty((M, K), dtype=dx_dtype, device=index)
     if dW is None:
         dW = torch.empty((N, K), dtype=torch.float32, device=index)
-    workspace, sp, sn = _room(workspace, _bwd_bytes(M, N, K), index)
+    workspace, sp, sn = _room(workspace, mx_linear_bwd_workspace_size(M, N, K), index)
     _run("mxfp4_linear_bwd", index, yp, M, N, K, _q(saved["Xq"], "Xq", index, M, K), _q(saved["Wq"], "Wq", index, N, K),
          rounding, 1 if rht else 0, seed, offset, _arg(dX, "dX", _OUT, index, (M, K)), _CODE[dX.dtype],
          _arg(dW, "dW", _F32, index, (N, K)), sp, sn)
