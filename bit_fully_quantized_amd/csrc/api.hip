@@ -1176,9 +1176,9 @@ tj2_status mxfp4_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, con
   TJ2_TRY(check_mx(&Wt, "Wt", K, N));
   TJ2_TRY(check_mx(&Xt, "Xt", K, M));
   const uint32_t sx = rht ? tj2_rht_signs(seed, offset) : 0, sw = rht ? tj2_rht_signs(seed, offset + 2) : 0;
-  TJ2_TRY(run_mx_quant(dY, TJ2_BF16, nullptr, M, N, TJ2_GROUP_ROW, rounding, rht, sx, seed, offset, &dYq, s));
+  TJ2_TRY(hip_check(launch_mx_dual(dY, make_view(dYq), make_view(dYt), rounding, rht != 0, sx, sw, seed, offset, offset + 2, s),
+                    "MXFP4 quantize launch"));
   TJ2_TRY(run_mx_quant(nullptr, TJ2_MXFP4, Wq, N, K, TJ2_GROUP_COL, rounding, rht, sx, seed, offset + 1, &Wt, s));
-  TJ2_TRY(run_mx_quant(dY, TJ2_BF16, nullptr, M, N, TJ2_GROUP_COL, rounding, rht, sw, seed, offset + 2, &dYt, s));
   TJ2_TRY(run_mx_quant(nullptr, TJ2_MXFP4, Xq, M, K, TJ2_GROUP_COL, rounding, rht, sw, seed, offset + 3, &Xt, s));
   TJ2_TRY(run_mx_gemm(&dYq, &Wt, dX, dx_dtype, K, 0, cur, s));
   TJ2_TRY(run_mx_gemm(&dYt, &Xt, dW, TJ2_F32, K, 0, cur, s));

@@ -173,6 +173,9 @@ struct MxQuantParams {
   QView out;
 };
 hipError_t launch_mx_quant(const MxQuantParams& q, hipStream_t s);
+// A dense bf16 matrix grouped along its rows and along its columns from one read.
+hipError_t launch_mx_dual(const void* x, const QView& row, const QView& col, int rounding, bool rht, uint32_t row_mask,
+                          uint32_t col_mask, uint64_t seed, uint64_t row_offset, uint64_t col_offset, hipStream_t s);
 hipError_t launch_mx_values(const QView& q, void* out, int dtype, hipStream_t s);
 size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K);
 hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
