@@ -388,43 +388,43 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ce_product_kernel(ProductArgs
   const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
   T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t z, typename T::Acc& acc) __attribute__((always_inline)) {
-  const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16 + n * T::kTN;
-  const float scale = p.out ? *p.scale : 1.0f;
-  float* sum = p.sum ? p.sum + (size_t)z * (size_t)p.Q.rows * (size_t)p.P.rows : nullptr;
+    const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16 + n * T::kTN;
+    const float scale = p.out ? *p.scale : 1.0f;
+    float* sum = p.sum ? p.sum + (size_t)z * (size_t)p.Q.rows * (size_t)p.P.rows : nullptr;
 #pragma unroll
-  for (int tn = 0; tn < T::kTN; ++tn) {
-    if (qw + tn >= p.Q.rows) continue;
+    for (int tn = 0; tn < T::kTN; ++tn) {
+      if (qw + tn >= p.Q.rows) continue;
 #pragma unroll
-    for (int tb = 0; tb < T::kTM / T::PB; ++tb) {
-      const int64_t j = pw + tb * 16 * T::PB;
-      // P has a multiple of 16 rows and a lane 4 PB = 16 of them
-      if (j >= p.P.rows) continue;
-      if (p.out) {
-        float v[16];
+      for (int tb = 0; tb < T::kTM / T::PB; ++tb) {
+        const int64_t j = pw + tb * 16 * T::PB;
+        // P has a multiple of 16 rows and a lane 4 PB = 16 of them
+        if (j >= p.P.rows) continue;
+        if (p.out) {
+          float v[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = acc[tb * T::PB + k / 4][tn][k % 4] * scale;
-        if (p.bf16) {
-          uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + (qw + tn) * p.ldo + j;
+          for (int k = 0; k < 16; ++k) v[k] = acc[tb * T::PB + k / 4][tn][k % 4] * scale;
+          if (p.bf16) {
+            uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + (qw + tn) * p.ldo + j;
 #pragma unroll
-          for (int k = 0; k < 16; k += 8)
-            *reinterpret_cast<uint4*>(o + k) = uint4{bf16_pair(v[k], v[k + 1]), bf16_pair(v[k + 2], v[k + 3]),
-                                                    bf16_pair(v[k + 4], v[k + 5]), bf16_pair(v[k + 6], v[k + 7])};
+            for (int k = 0; k < 16; k += 8)
+              *reinterpret_cast<uint4*>(o + k) = uint4{bf16_pair(v[k], v[k + 1]), bf16_pair(v[k + 2], v[k + 3]),
+                                                      bf16_pair(v[k + 4], v[k + 5]), bf16_pair(v[k + 6], v[k + 7])};
+          } else {
+            float* o = reinterpret_cast<float*>(p.out) + (qw + tn) * p.ldo + j;
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(o + k) = float4{v[k], v[k + 1], v[k + 2], v[k + 3]};
+          }
         } else {
-          float* o = reinterpret_cast<float*>(p.out) + (qw + tn) * p.ldo + j;
+          float4_t* o = reinterpret_cast<float4_t*>(sum + (qw + tn) * p.P.rows + j);
 #pragma unroll
-          for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(o + k) = float4{v[k], v[k + 1], v[k + 2], v[k + 3]};
-        }
-      } else {
-        float4_t* o = reinterpret_cast<float4_t*>(sum + (qw + tn) * p.P.rows + j);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float4_t v = acc[tb * T::PB + k][tn];
-          if (!p.first) v += o[k];
-          o[k] = v;
+          for (int k = 0; k < 4; ++k) {
+            float4_t v = acc[tb * T::PB + k][tn];
+            if (!p.first) v += o[k];
+            o[k] = v;
+          }
         }
       }
     }
-  }
   });
 }
 
@@ -469,8 +469,8 @@ bool ce_big(int64_t V, int64_t T, int64_t K) {
   const double chunks = (double)((K + 63) / 64);
   return tile_time(true, tiles_of(V, T, 256), chunks, 9.0) < tile_time(false, tiles_of(V, T, 128), chunks, 9.0);
 }
-// Tile and splits of a product of p by q results over k (1235 x 528 over 32003: 192 us
-// unsplit.. of the whole backward, 174 with 8 to 16 splits).
+// Tile and splits of a product of p by q results over k (the whole backward of 1235 x
+// 32003 over 528: 192 us with unsplit products, 174 with 8 to 16 splits).
 struct ProductPlan {
   bool big;
   int splits;
@@ -590,14 +590,11 @@ CeFwdSpace ce_fwd_space(int64_t T, int64_t K, int64_t V) {
 struct CeBwdSpace {
   size_t c, top, xb, xt, wb, wt, d, dt, dx, part, bytes;
   int64_t piece;
-  ProductPlan px, pw;
   bool blocked;
 };
 CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   CeBwdSpace s;
   s.piece = ce_piece(T, V);
-  s.px = product_plan(K, T, s.piece);
-  s.pw = product_plan(K, s.piece, T);
   s.blocked = T >= kBlockTokens;
   size_t at = 0;
   auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
@@ -610,8 +607,14 @@ CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   s.d = take(blocked_bytes(T, s.piece));
   s.dt = take(blocked_bytes(s.piece, T));
   s.dx = take((size_t)(T * K * 4));
-  s.part = take(std::max(s.px.splits > 1 ? (size_t)s.px.splits * (size_t)(T * K * 4) : 0,
-                         s.pw.splits > 1 ? (size_t)s.pw.splits * (size_t)(s.piece * K * 4) : 0));
+  // partial sums of split products, of a whole piece and of the last one
+  size_t part = 0;
+  for (const int64_t vn : {s.piece, V % s.piece}) {
+    if (!vn) continue;
+    const int zx = product_plan(K, T, vn).splits, zw = product_plan(K, vn, T).splits;
+    part = std::max({part, zx > 1 ? (size_t)zx * (size_t)(T * K * 4) : 0, zw > 1 ? (size_t)zw * (size_t)(vn * K * 4) : 0});
+  }
+  s.part = take(part);
   s.bytes = at;
   return s;
 }
@@ -702,7 +705,8 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
       x.P = blocked_operand(w + sp.wt, c.K, up(vn, 64));
       x.Q = blocked_operand(w + sp.d, c.T, up(vn, 64));
       x.nch = a.nd;
-      x.splits = std::min(sp.px.splits, x.nch);
+      const ProductPlan plan = product_plan(c.K, c.T, vn);
+      x.splits = plan.splits;
       x.scale = top;
       x.bf16 = c.dx_dtype == TJ2_BF16;
       x.ldo = c.K;
@@ -710,7 +714,7 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
       if (x.splits > 1) x.sum = part;
       else if (one) x.out = c.dX;
       else x.sum = dx;
-      launch_product(x, sp.px.big, s);
+      launch_product(x, plan.big, s);
       TJ2_STEP();
       const int64_t n = c.T * c.K;
       const uint32_t grid = (uint32_t)((n / 4 + 255) / 256);
@@ -727,7 +731,8 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
       x.P = blocked_operand(w + sp.xt, c.K, up(c.T, 64));
       x.Q = blocked_operand(w + sp.dt, vn, up(c.T, 64));
       x.nch = a.nt;
-      x.splits = std::min(sp.pw.splits, x.nch);
+      const ProductPlan plan = product_plan(c.K, vn, c.T);
+      x.splits = plan.splits;
       x.scale = top;
       x.bf16 = c.dw_dtype == TJ2_BF16;
       x.ldo = c.K;
@@ -735,7 +740,7 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
       uint8_t* out = reinterpret_cast<uint8_t*>(c.dW) + (size_t)(v0 * c.K) * (x.bf16 ? 2 : 4);
       if (x.splits > 1) x.sum = part;
       else x.out = out;
-      launch_product(x, sp.pw.big, s);
+      launch_product(x, plan.big, s);
       TJ2_STEP();
       const int64_t n = vn * c.K;
       if (x.splits > 1) ce_sum_kernel<<<(uint32_t)((n / 4 + 255) / 256), 256, 0, s>>>(part, x.splits, n, top, out, x.bf16);
