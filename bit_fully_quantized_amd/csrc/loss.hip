@@ -221,29 +221,6 @@ __global__ __launch_bounds__(L * S) void ce_join_kernel(const float2* part, int 
   }
 }
 
-// c = w / max |w| (0 where the target is ignored) and that maximum: equal weights
-// become 1, so that the bf16 of (softmax - 1) near a target is as exact as can be.
-__global__ __launch_bounds__(1024) void ce_weights_kernel(const float* w, const int64_t* y, int64_t T, int64_t V, int64_t ignore,
-                                                          float* c, float* top) {
-  __shared__ float sh[16];
-  float m = 0.0f;
-  for (int64_t t = threadIdx.x; t < T; t += 1024)
-    if (y[t] != ignore) m = fmaxf(m, fabsf(w[t]));
-#pragma unroll
-  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = m;
-  __syncthreads();
-  m = sh[0];
-#pragma unroll
-  for (int i = 1; i < 16; ++i) m = fmaxf(m, sh[i]);
-  if (m == 0.0f) m = 1.0f;
-  for (int64_t t = threadIdx.x; t < T; t += 1024) {
-    const int64_t k = y[t];
-    c[t] = k == ignore ? 0.0f : (uint64_t)k < (uint64_t)V ? w[t] / m : kNan;
-  }
-  if (threadIdx.x == 0) *top = m;
-}
-
 // dz of a tile in bf16, both ways.  The exponential is clamped to [0, 1], which costs
 // nothing (an output modifier) and holds where the fused v c - r overflows; it turns a
 // NaN into 0, so a token whose lse is NaN gets a NaN weight instead.
@@ -336,36 +313,105 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ce_dz_kernel(CeArgs p) {
   });
 }
 
+// What the tile products read, in one launch: the first workgroup the tokens' weights,
+// then a workgroup per 64 x 64 elements of X and of W.  Small backward passes are as
+// long as their launches: 700 x 9000 over 96 took 49 us with a launch for each of
+// these, each product and each join, and takes 35.
+//
+// Weights: c = w / max |w| (0 where the target is ignored) and that maximum: equal
+// weights become 1, so that the bf16 of (softmax - 1) near a target is as exact as can
+// be.
+struct WeightArgs {
+  const float* w;
+  const int64_t* y;
+  int64_t T, V, ignore;
+  float *c, *top;
+};
+__device__ __forceinline__ void ce_weights(const WeightArgs& p) {
+  __shared__ float sh[4];
+  float m = 0.0f;
+  // 16 tokens a thread at once, so that their loads are in flight together
+  constexpr int N = 16;
+  int64_t y[N];
+  float w[N];
+  auto load = [&](int64_t t0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t t = min(t0 + i * 256 + threadIdx.x, p.T - 1);
+      y[i] = p.y[t];
+      w[i] = p.w[t];
+    }
+  };
+  for (int64_t t0 = 0; t0 < p.T; t0 += N * 256) {
+    load(t0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = fmaxf(m, y[i] != p.ignore ? fabsf(w[i]) : 0.0f);
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3]));
+  if (m == 0.0f) m = 1.0f;
+  for (int64_t t0 = 0; t0 < p.T; t0 += N * 256) {
+    if (p.T > N * 256) load(t0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t t = t0 + i * 256 + threadIdx.x;
+      if (t < p.T) p.c[t] = y[i] == p.ignore ? 0.0f : (uint64_t)y[i] < (uint64_t)p.V ? w[i] / m : kNan;
+    }
+  }
+  if (threadIdx.x == 0) *p.top = m;
+}
+
 // A bf16 matrix [rows, cols] (cols a multiple of 16) into blocked operands: `copy`
 // [rows, cols] and `turned` [cols, rows], zero up to whole chunks; either may be
 // NULL.  64 x 64 through LDS.
-__global__ __launch_bounds__(256) void block_kernel(const uint16_t* in, int64_t rows, int64_t cols, int64_t ldi, uint16_t* copy,
-                                                    uint16_t* turned) {
+struct BlockArgs {
+  const uint16_t* in;
+  int64_t rows, cols, ld;
+  uint16_t *copy, *turned;
+  uint32_t nr, nc;  // chunks of rows and of columns
+};
+__device__ __forceinline__ void block_tile(const BlockArgs& p, uint32_t br, uint32_t bc) {
   __shared__ uint16_t tile[64][66];
-  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
+  const int64_t r0 = (int64_t)br * 64, c0 = (int64_t)bc * 64;
   const int t = threadIdx.x;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = i * 32 + (t >> 3), c = (t & 7) * 8;
     uint4 v = {0u, 0u, 0u, 0u};
-    if (r0 + r < rows && c0 + c < cols) v = *reinterpret_cast<const uint4*>(in + (r0 + r) * ldi + c0 + c);
-    if (copy && r0 + r < rows)
-      *reinterpret_cast<uint4*>(copy + ((r0 >> 7) * gridDim.y + blockIdx.y) * 8192 + ((r0 & 127) + r) * 64 + c) = v;
+    if (r0 + r < p.rows && c0 + c < p.cols) v = *reinterpret_cast<const uint4*>(p.in + (r0 + r) * p.ld + c0 + c);
+    if (p.copy && r0 + r < p.rows)
+      *reinterpret_cast<uint4*>(p.copy + ((r0 >> 7) * p.nc + bc) * 8192 + ((r0 & 127) + r) * 64 + c) = v;
     uint32_t* s = reinterpret_cast<uint32_t*>(&tile[r][c]);
     s[0] = v.x; s[1] = v.y; s[2] = v.z; s[3] = v.w;
   }
-  if (!turned) return;
+  if (!p.turned) return;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int c = i * 32 + (t >> 3), r = (t & 7) * 8;
-    if (c0 + c >= cols) continue;
+    if (c0 + c >= p.cols) continue;
     uint32_t v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = tile[r + 2 * k][c] | ((uint32_t)tile[r + 2 * k + 1][c] << 16);
-    *reinterpret_cast<uint4*>(turned + ((c0 >> 7) * gridDim.x + blockIdx.x) * 8192 + ((c0 & 127) + c) * 64 + r) =
-        uint4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<uint4*>(p.turned + ((c0 >> 7) * p.nr + br) * 8192 + ((c0 & 127) + c) * 64 + r) = uint4{v[0], v[1], v[2], v[3]};
   }
+}
+
+// weights: whether the first workgroup takes them
+__global__ __launch_bounds__(256) void ce_prepare_kernel(WeightArgs w, int weights, BlockArgs x, BlockArgs v) {
+  uint32_t b = blockIdx.x;
+  if (weights) {
+    if (b == 0) return ce_weights(w);
+    --b;
+  }
+  const uint32_t nx = x.nr * x.nc;
+  const bool first = b < nx;
+  const BlockArgs& p = first ? x : v;
+  if (!first) b -= nx;
+  block_tile(p, b % p.nr, b / p.nr);
 }
 
 // D[q, p] = sum_k Q[q, k] P[p, k] in bf16 operands:
@@ -382,10 +428,14 @@ struct ProductArgs {
   int32_t bf16;
 };
 
+// One product or both of a piece: `na` workgroups for a, the others for b.
 template <class T>
-__global__ __launch_bounds__(T::NT, T::WAVES) void ce_product_kernel(ProductArgs p) {
+__global__ __launch_bounds__(T::NT, T::WAVES) void ce_product_kernel(ProductArgs a, ProductArgs b, uint32_t na) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
-  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits);
+  const bool is_a = blockIdx.x < na;
+  const ProductArgs& p = is_a ? a : b;
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits, is_a ? blockIdx.x : blockIdx.x - na,
+                                is_a ? na : gridDim.x - na);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
   T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t z, typename T::Acc& acc) __attribute__((always_inline)) {
     const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16 + n * T::kTN;
@@ -429,15 +479,25 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ce_product_kernel(ProductArgs
 }
 
 // out = scale * (sum of `parts` fp32 slices), in order; 4 a thread (n a multiple of 16).
-__global__ __launch_bounds__(256) void ce_sum_kernel(const float* sum, int parts, int64_t n, const float* scale, void* out, int bf16) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+// One result or two: `na` workgroups for a, the others for b.
+struct SumArgs {
+  const float* sum;
+  int parts, bf16;
+  int64_t n;
+  const float* scale;
+  void* out;
+};
+__global__ __launch_bounds__(256) void ce_sum_kernel(SumArgs a, SumArgs b, uint32_t na) {
+  const bool is_a = blockIdx.x < na;
+  const SumArgs& p = is_a ? a : b;
+  const int64_t i = ((int64_t)(is_a ? blockIdx.x : blockIdx.x - na) * 256 + threadIdx.x) * 4, n = p.n;
   if (i >= n) return;
-  float4_t v = *reinterpret_cast<const float4_t*>(sum + i);
-  for (int z = 1; z < parts; ++z) v += *reinterpret_cast<const float4_t*>(sum + (size_t)z * (size_t)n + i);
-  const float s = *scale;
+  float4_t v = *reinterpret_cast<const float4_t*>(p.sum + i);
+  for (int z = 1; z < p.parts; ++z) v += *reinterpret_cast<const float4_t*>(p.sum + (size_t)z * (size_t)n + i);
+  const float s = *p.scale;
   v *= s;
-  if (bf16) *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + i) = uint2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
-  else *reinterpret_cast<float4_t*>(reinterpret_cast<float*>(out) + i) = v;
+  if (p.bf16) *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + i) = uint2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+  else *reinterpret_cast<float4_t*>(reinterpret_cast<float*>(p.out) + i) = v;
 }
 
 // sum slice 0 (kept over the pieces) += the piece's slices, in order
@@ -518,14 +578,21 @@ void launch_dz_tile(CeArgs a, hipStream_t s) {
   ce_dz_kernel<T><<<T::grid((uint64_t)a.tiles_p * a.tiles_q), T::NT, 0, s>>>(a);
 }
 template <class T>
-void launch_product_tile(ProductArgs x, hipStream_t s) {
+uint32_t product_tiles(ProductArgs& x) {
   x.tiles_p = (uint32_t)((x.P.rows + T::BM - 1) / T::BM);
   x.tiles_q = (uint32_t)((x.Q.rows + T::BN - 1) / T::BN);
-  ce_product_kernel<T><<<T::grid((uint64_t)x.tiles_p * x.tiles_q * (uint32_t)x.splits), T::NT, 0, s>>>(x);
+  return T::grid((uint64_t)x.tiles_p * x.tiles_q * (uint32_t)x.splits);
 }
-void launch_product(const ProductArgs& x, bool big, hipStream_t s) {
-  if (big) launch_product_tile<TileBig>(x, s);
-  else launch_product_tile<TileMid>(x, s);
+// Up to two products of one tile in one launch.
+template <class T>
+void launch_products(ProductArgs* x, int n, hipStream_t s) {
+  const uint32_t na = product_tiles<T>(x[0]), nb = n > 1 ? product_tiles<T>(x[1]) : 0;
+  ce_product_kernel<T><<<na + nb, T::NT, 0, s>>>(x[0], x[n - 1], na);
+}
+void launch_sums(const SumArgs* x, int n, hipStream_t s) {
+  auto grid = [](const SumArgs& a) { return (uint32_t)((a.n / 4 + 255) / 256); };
+  const uint32_t na = grid(x[0]);
+  ce_sum_kernel<<<na + (n > 1 ? grid(x[1]) : 0), 256, 0, s>>>(x[0], x[n - 1], na);
 }
 
 TileOp bf16_operand(const void* p, int64_t rows, int64_t cols, int64_t ld) {
@@ -612,17 +679,24 @@ CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   for (const int64_t vn : {s.piece, V % s.piece}) {
     if (!vn) continue;
     const int zx = product_plan(K, T, vn).splits, zw = product_plan(K, vn, T).splits;
-    part = std::max({part, zx > 1 ? (size_t)zx * (size_t)(T * K * 4) : 0, zw > 1 ? (size_t)zw * (size_t)(vn * K * 4) : 0});
+    part = std::max(part, (zx > 1 ? (size_t)zx * (size_t)(T * K * 4) : 0) + (zw > 1 ? (size_t)zw * (size_t)(vn * K * 4) : 0));
   }
   s.part = take(part);
   s.bytes = at;
   return s;
 }
 
-void launch_block(const void* in, int64_t rows, int64_t cols, int64_t ld, void* copy, void* turned, hipStream_t s) {
-  const dim3 grid((uint32_t)((rows + 63) / 64), (uint32_t)((cols + 63) / 64));
-  block_kernel<<<grid, 256, 0, s>>>(reinterpret_cast<const uint16_t*>(in), rows, cols, ld, reinterpret_cast<uint16_t*>(copy),
-                                    reinterpret_cast<uint16_t*>(turned));
+BlockArgs block_args(const void* in, int64_t rows, int64_t cols, int64_t ld, void* copy, void* turned) {
+  return BlockArgs{reinterpret_cast<const uint16_t*>(in), rows,
+                   cols, ld, reinterpret_cast<uint16_t*>(copy),
+                   reinterpret_cast<uint16_t*>(turned), (uint32_t)((rows + 63) / 64), (uint32_t)((cols + 63) / 64)};
+}
+// w, x: NULL for none
+void launch_prepare(const WeightArgs* w, const BlockArgs* x, const BlockArgs& v, hipStream_t s) {
+  const WeightArgs no_weights = {};
+  const BlockArgs none = {};
+  const uint32_t grid = (w ? 1 : 0) + (x ? x->nr * x->nc : 0) + v.nr * v.nc;
+  ce_prepare_kernel<<<grid, 256, 0, s>>>(w ? *w : no_weights, w != nullptr, x ? *x : none, v);
 }
 
 }  // namespace
@@ -639,9 +713,8 @@ hipError_t launch_ce_fwd(const CeParams& c, void* ws, hipStream_t s) {
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   CeArgs a = {};
   if (sp.blocked) {
-    launch_block(c.W, c.V, c.K, c.ldw, w + sp.wb, nullptr, s);
-    TJ2_STEP();
-    launch_block(c.X, c.T, c.K, c.ldx, w + sp.xb, nullptr, s);
+    const BlockArgs x = block_args(c.X, c.T, c.K, c.ldx, w + sp.xb, nullptr);
+    launch_prepare(nullptr, &x, block_args(c.W, c.V, c.K, c.ldw, w + sp.wb, nullptr), s);
     TJ2_STEP();
     a.P = blocked_operand(w + sp.wb, c.V, c.K);
     a.Q = blocked_operand(w + sp.xb, c.T, c.K);
@@ -675,15 +748,14 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   float* top = reinterpret_cast<float*>(w + sp.top);
   float *dx = reinterpret_cast<float*>(w + sp.dx), *part = reinterpret_cast<float*>(w + sp.part);
-  ce_weights_kernel<<<1, 1024, 0, s>>>(c.dloss, c.y, c.T, c.V, c.ignore, reinterpret_cast<float*>(w + sp.c), top);
-  TJ2_STEP();
-  launch_block(c.X, c.T, c.K, c.ldx, sp.blocked ? w + sp.xb : nullptr, w + sp.xt, s);
-  TJ2_STEP();
+  const WeightArgs weights = {c.dloss, c.y, c.T, c.V, c.ignore, reinterpret_cast<float*>(w + sp.c), top};
+  const BlockArgs xb = block_args(c.X, c.T, c.K, c.ldx, sp.blocked ? w + sp.xb : nullptr, w + sp.xt);
   const bool one = sp.piece >= c.V;
   for (int64_t v0 = 0; v0 < c.V; v0 += sp.piece) {
     const int64_t vn = std::min(sp.piece, c.V - v0);
     const uint16_t* W = reinterpret_cast<const uint16_t*>(c.W) + v0 * c.ldw;
-    launch_block(W, vn, c.K, c.ldw, sp.blocked ? w + sp.wb : nullptr, w + sp.wt, s);
+    launch_prepare(v0 ? nullptr : &weights, v0 ? nullptr : &xb,
+                   block_args(W, vn, c.K, c.ldw, sp.blocked ? w + sp.wb : nullptr, w + sp.wt), s);
     TJ2_STEP();
     CeArgs a = {};
     a.P = sp.blocked ? blocked_operand(w + sp.wb, vn, c.K) : bf16_operand(W, vn, c.K, c.ldw);
@@ -700,52 +772,76 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
     if (ce_big(vn, c.T, c.K)) launch_dz_tile<TileBig>(a, s);
     else launch_dz_tile<TileMid>(a, s);
     TJ2_STEP();
+    // dX += dz W and dW = dz^T X of the piece; split products leave partial sums
+    ProductArgs x[2];
+    bool big[2];
+    int n = 0;
+    SumArgs sums[2];
+    int joins = 0;
+    float* at = part;
+    const int64_t nx = c.T * c.K, nw = vn * c.K;
+    const bool last = v0 + vn == c.V;
+    bool fold = false;
     if (c.dX) {
-      ProductArgs x = {};
-      x.P = blocked_operand(w + sp.wt, c.K, up(vn, 64));
-      x.Q = blocked_operand(w + sp.d, c.T, up(vn, 64));
-      x.nch = a.nd;
       const ProductPlan plan = product_plan(c.K, c.T, vn);
-      x.splits = plan.splits;
-      x.scale = top;
-      x.bf16 = c.dx_dtype == TJ2_BF16;
-      x.ldo = c.K;
-      x.first = x.splits > 1 || v0 == 0;
-      if (x.splits > 1) x.sum = part;
-      else if (one) x.out = c.dX;
-      else x.sum = dx;
-      launch_product(x, plan.big, s);
-      TJ2_STEP();
-      const int64_t n = c.T * c.K;
-      const uint32_t grid = (uint32_t)((n / 4 + 255) / 256);
-      if (x.splits > 1 && one) {
-        ce_sum_kernel<<<grid, 256, 0, s>>>(part, x.splits, n, top, c.dX, x.bf16);
+      ProductArgs& q = x[n];
+      q = {};
+      q.P = blocked_operand(w + sp.wt, c.K, up(vn, 64));
+      q.Q = blocked_operand(w + sp.d, c.T, up(vn, 64));
+      q.nch = a.nd;
+      q.splits = plan.splits;
+      q.scale = top;
+      q.bf16 = c.dx_dtype == TJ2_BF16;
+      q.ldo = c.K;
+      q.first = q.splits > 1 || v0 == 0;
+      if (q.splits > 1) {
+        q.sum = at;
+        at += (size_t)q.splits * (size_t)nx;
+      } else if (one) {
+        q.out = c.dX;
       } else {
-        if (x.splits > 1) ce_fold_kernel<<<grid, 256, 0, s>>>(dx, part, x.splits, n, v0 == 0);
-        if (!one && v0 + vn == c.V) ce_sum_kernel<<<grid, 256, 0, s>>>(dx, 1, n, top, c.dX, x.bf16);
+        q.sum = dx;
       }
-      TJ2_STEP();
+      fold = q.splits > 1 && !one;
+      if (q.splits > 1 && one) sums[joins++] = SumArgs{part, q.splits, q.bf16, nx, top, c.dX};
+      if (!one && last) sums[joins++] = SumArgs{dx, 1, q.bf16, nx, top, c.dX};
+      big[n++] = plan.big;
     }
     if (c.dW) {
-      ProductArgs x = {};
-      x.P = blocked_operand(w + sp.xt, c.K, up(c.T, 64));
-      x.Q = blocked_operand(w + sp.dt, vn, up(c.T, 64));
-      x.nch = a.nt;
       const ProductPlan plan = product_plan(c.K, vn, c.T);
-      x.splits = plan.splits;
-      x.scale = top;
-      x.bf16 = c.dw_dtype == TJ2_BF16;
-      x.ldo = c.K;
-      x.first = 1;
-      uint8_t* out = reinterpret_cast<uint8_t*>(c.dW) + (size_t)(v0 * c.K) * (x.bf16 ? 2 : 4);
-      if (x.splits > 1) x.sum = part;
-      else x.out = out;
-      launch_product(x, plan.big, s);
+      ProductArgs& q = x[n];
+      q = {};
+      q.P = blocked_operand(w + sp.xt, c.K, up(c.T, 64));
+      q.Q = blocked_operand(w + sp.dt, vn, up(c.T, 64));
+      q.nch = a.nt;
+      q.splits = plan.splits;
+      q.scale = top;
+      q.bf16 = c.dw_dtype == TJ2_BF16;
+      q.ldo = c.K;
+      q.first = 1;
+      uint8_t* out = reinterpret_cast<uint8_t*>(c.dW) + (size_t)(v0 * c.K) * (q.bf16 ? 2 : 4);
+      if (q.splits > 1) {
+        q.sum = at;
+        sums[joins++] = SumArgs{at, q.splits, q.bf16, nw, top, out};
+      } else {
+        q.out = out;
+      }
+      big[n++] = plan.big;
+    }
+    // in one launch where they take the same tile
+    for (int i = 0; i < n;) {
+      const int k = i + 1 < n && big[i] == big[i + 1] ? 2 : 1;
+      if (big[i]) launch_products<TileBig>(x + i, k, s);
+      else launch_products<TileMid>(x + i, k, s);
       TJ2_STEP();
-      const int64_t n = vn * c.K;
-      if (x.splits > 1) ce_sum_kernel<<<(uint32_t)((n / 4 + 255) / 256), 256, 0, s>>>(part, x.splits, n, top, out, x.bf16);
+      i += k;
+    }
+    if (fold) {
+      ce_fold_kernel<<<(uint32_t)((nx / 4 + 255) / 256), 256, 0, s>>>(dx, part, x[0].splits, nx, v0 == 0);
       TJ2_STEP();
     }
+    if (joins) launch_sums(sums, joins, s);
+    TJ2_STEP();
   }
   return hipSuccess;
 }

@@ -193,11 +193,13 @@ struct Tile {
   struct Items {
     uint32_t tiles_p, tiles_q, nch, splits;
     uint32_t at, end, step;
-    __device__ __forceinline__ Items(uint32_t tp, uint32_t tq, uint32_t chunks, uint32_t z)
+    // of workgroup b of n
+    __device__ __forceinline__ Items(uint32_t tp, uint32_t tq, uint32_t chunks, uint32_t z, uint32_t b = blockIdx.x,
+                                     uint32_t n = gridDim.x)
         : tiles_p(tp), tiles_q(tq), nch(chunks), splits(z) {
       // XCD x has the workgroups b = x modulo 8; its range is in proportion to their
       // number, so that no workgroup has two more items than another
-      const uint32_t total = tp * tq * z, n = gridDim.x, b = blockIdx.x, x = b % 8;
+      const uint32_t total = tp * tq * z, x = b % 8;
       const uint32_t before = x * (n / 8) + min(x, n % 8), count = n / 8 + (x < n % 8 ? 1 : 0);
       at = (uint32_t)((uint64_t)total * before / n) + b / 8;
       end = (uint32_t)((uint64_t)total * (before + count) / n);
