@@ -1043,9 +1043,8 @@ tj2_status check_mx_input(const void* x, int32_t x_dtype, const tj2_qtensor* x_q
   return TJ2_OK;
 }
 
-tj2_status run_mx_quant(const void* x, int x_dtype, const tj2_qtensor* x_q, int64_t rows, int64_t cols, int grouping,
-                        int rounding, int rht, uint32_t mask, uint64_t seed, uint64_t offset, const tj2_qtensor* out,
-                        hipStream_t s) {
+MxQuantParams mx_quant_params(const void* x, int x_dtype, const tj2_qtensor* x_q, int64_t rows, int64_t cols, int grouping,
+                              int rounding, int rht, uint32_t mask, uint64_t seed, uint64_t offset, const tj2_qtensor* out) {
   MxQuantParams p = {};
   p.in_dtype = x_dtype;
   p.x = x;
@@ -1059,7 +1058,7 @@ tj2_status run_mx_quant(const void* x, int x_dtype, const tj2_qtensor* x_q, int6
   p.seed = seed;
   p.offset = offset;
   p.out = make_view(*out);
-  return hip_check(launch_mx_quant(p, s), "MXFP4 quantize launch");
+  return p;
 }
 
 tj2_status run_mx_gemm(const tj2_qtensor* A, const tj2_qtensor* B, void* C, int c_dtype, int64_t ldc, int accumulate,
@@ -1081,7 +1080,7 @@ tj2_status check_out_dtype(int32_t dtype, const char* name) {
 }
 
 size_t mx_linear_bwd_gemm_ws(int64_t M, int64_t N, int64_t K) {
-  return std::max(mx_gemm_workspace_bytes(M, K, N), mx_gemm_workspace_bytes(N, K, M));
+  return mx_gemm_pair_workspace_bytes(M, K, N, N, K, M);
 }
 
 }  // namespace
@@ -1093,7 +1092,9 @@ tj2_status mxfp4_quantize(const void* x, int32_t x_dtype, const tj2_qtensor* x_q
                           uint64_t offset, tj2_qtensor* out, void* stream) {
   TJ2_TRY(check_mx_input(x, x_dtype, x_q, rows, cols, grouping, rounding));
   TJ2_TRY(grouping == TJ2_GROUP_ROW ? check_mx(out, "out", rows, cols) : check_mx(out, "out", cols, rows));
-  TJ2_TRY(run_mx_quant(x, x_dtype, x_q, rows, cols, grouping, rounding, rht, rht_signs, seed, offset, out, (hipStream_t)stream));
+  TJ2_TRY(hip_check(launch_mx_quant(mx_quant_params(x, x_dtype, x_q, rows, cols, grouping, rounding, rht, rht_signs, seed, offset, out),
+                                    (hipStream_t)stream),
+                    "MXFP4 quantize launch"));
   return ok();
 }
 
@@ -1138,12 +1139,14 @@ tj2_status mxfp4_linear_fwd(const void* X, int64_t M, int64_t K, int64_t N, cons
   TJ2_TRY(check_out_dtype(y_dtype, "y_dtype"));
   if (!aligned16(X) || !aligned16(W_master) || !aligned16(Y)) return fail(TJ2_ERR_ALIGN, "X, W_master and Y must be 16-byte aligned");
   TJ2_TRY(check_mx_workspace(workspace, ws_bytes, mx_gemm_workspace_bytes(M, N, K)));
-  if (W_master) TJ2_TRY(run_mx_quant(W_master, TJ2_F32, nullptr, N, K, TJ2_GROUP_ROW, TJ2_RTN, 0, 0, 0, 0, Wq, s));
-  if (launch_mx_linear_few(X, make_view(*Xq), make_view(*Wq), Y, y_dtype, s)) {
-    TJ2_TRY(hip_check(hipGetLastError(), "MXFP4 linear launch"));
+  const MxQuantParams x = mx_quant_params(X, TJ2_BF16, nullptr, M, K, TJ2_GROUP_ROW, TJ2_RTN, 0, 0, 0, 0, Xq);
+  const MxQuantParams w = mx_quant_params(W_master, TJ2_F32, nullptr, N, K, TJ2_GROUP_ROW, TJ2_RTN, 0, 0, 0, 0, Wq);
+  if (mx_is_few(M, K)) {
+    if (W_master) TJ2_TRY(hip_check(launch_mx_quant(w, s), "MXFP4 quantize launch"));
+    TJ2_TRY(hip_check(launch_mx_linear_few(X, make_view(*Xq), make_view(*Wq), Y, y_dtype, s), "MXFP4 linear launch"));
     return ok();
   }
-  TJ2_TRY(run_mx_quant(X, TJ2_BF16, nullptr, M, K, TJ2_GROUP_ROW, TJ2_RTN, 0, 0, 0, 0, Xq, s));
+  TJ2_TRY(hip_check(W_master ? launch_mx_forward_operands(x, w, s) : launch_mx_quant(x, s), "MXFP4 quantize launch"));
   TJ2_TRY(run_mx_gemm(Xq, Wq, Y, y_dtype, N, 0, workspace, s));
   return ok();
 }
@@ -1176,12 +1179,16 @@ tj2_status mxfp4_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, con
   TJ2_TRY(check_mx(&Wt, "Wt", K, N));
   TJ2_TRY(check_mx(&Xt, "Xt", K, M));
   const uint32_t sx = rht ? tj2_rht_signs(seed, offset) : 0, sw = rht ? tj2_rht_signs(seed, offset + 2) : 0;
-  TJ2_TRY(hip_check(launch_mx_dual(dY, make_view(dYq), make_view(dYt), rounding, rht != 0, sx, sw, seed, offset, offset + 2, s),
+  const int row = TJ2_GROUP_ROW, col = TJ2_GROUP_COL;
+  TJ2_TRY(hip_check(launch_mx_backward_operands(
+                        mx_quant_params(dY, TJ2_BF16, nullptr, M, N, row, rounding, rht, sx, seed, offset, &dYq),
+                        mx_quant_params(dY, TJ2_BF16, nullptr, M, N, col, rounding, rht, sw, seed, offset + 2, &dYt),
+                        mx_quant_params(nullptr, TJ2_MXFP4, Wq, N, K, col, rounding, rht, sx, seed, offset + 1, &Wt),
+                        mx_quant_params(nullptr, TJ2_MXFP4, Xq, M, K, col, rounding, rht, sw, seed, offset + 3, &Xt), s),
                     "MXFP4 quantize launch"));
-  TJ2_TRY(run_mx_quant(nullptr, TJ2_MXFP4, Wq, N, K, TJ2_GROUP_COL, rounding, rht, sx, seed, offset + 1, &Wt, s));
-  TJ2_TRY(run_mx_quant(nullptr, TJ2_MXFP4, Xq, M, K, TJ2_GROUP_COL, rounding, rht, sw, seed, offset + 3, &Xt, s));
-  TJ2_TRY(run_mx_gemm(&dYq, &Wt, dX, dx_dtype, K, 0, cur, s));
-  TJ2_TRY(run_mx_gemm(&dYt, &Xt, dW, TJ2_F32, K, 0, cur, s));
+  TJ2_TRY(hip_check(launch_mx_gemm_pair(make_view(dYq), make_view(Wt), dX, dx_dtype, make_view(dYt), make_view(Xt), dW, TJ2_F32,
+                                        reinterpret_cast<float*>(cur), s),
+                    "MXFP4 gemm launch"));
   return ok();
 }
 

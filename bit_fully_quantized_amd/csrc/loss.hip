@@ -401,16 +401,15 @@ __device__ __forceinline__ void block_tile(const BlockArgs& p, uint32_t br, uint
 }
 
 // weights: whether the first workgroup takes them
-__global__ __launch_bounds__(256) void ce_prepare_kernel(WeightArgs w, int weights, BlockArgs x, BlockArgs v) {
+__global__ __launch_bounds__(256) void ce_prepare_kernel(WeightArgs w, int weights, Pair<BlockArgs> jobs) {
   uint32_t b = blockIdx.x;
   if (weights) {
     if (b == 0) return ce_weights(w);
     --b;
   }
-  const uint32_t nx = x.nr * x.nc;
-  const bool first = b < nx;
-  const BlockArgs& p = first ? x : v;
-  if (!first) b -= nx;
+  const int job = b < jobs.first ? 0 : 1;
+  const BlockArgs& p = jobs.x[job];
+  if (job) b -= jobs.first;
   block_tile(p, b % p.nr, b / p.nr);
 }
 
@@ -428,14 +427,13 @@ struct ProductArgs {
   int32_t bf16;
 };
 
-// One product or both of a piece: `na` workgroups for a, the others for b.
+// One product or both of a piece.
 template <class T>
-__global__ __launch_bounds__(T::NT, T::WAVES) void ce_product_kernel(ProductArgs a, ProductArgs b, uint32_t na) {
+__global__ __launch_bounds__(T::NT, T::WAVES) void ce_product_kernel(Pair<ProductArgs> jobs) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
-  const bool is_a = blockIdx.x < na;
-  const ProductArgs& p = is_a ? a : b;
-  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits, is_a ? blockIdx.x : blockIdx.x - na,
-                                is_a ? na : gridDim.x - na);
+  const Share mine(jobs.first);
+  const ProductArgs& p = jobs.x[mine.job];
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits, mine.block, mine.blocks);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
   T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t z, typename T::Acc& acc) __attribute__((always_inline)) {
     const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16 + n * T::kTN;
@@ -479,7 +477,7 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ce_product_kernel(ProductArgs
 }
 
 // out = scale * (sum of `parts` fp32 slices), in order; 4 a thread (n a multiple of 16).
-// One result or two: `na` workgroups for a, the others for b.
+// One result or two.
 struct SumArgs {
   const float* sum;
   int parts, bf16;
@@ -487,10 +485,10 @@ struct SumArgs {
   const float* scale;
   void* out;
 };
-__global__ __launch_bounds__(256) void ce_sum_kernel(SumArgs a, SumArgs b, uint32_t na) {
-  const bool is_a = blockIdx.x < na;
-  const SumArgs& p = is_a ? a : b;
-  const int64_t i = ((int64_t)(is_a ? blockIdx.x : blockIdx.x - na) * 256 + threadIdx.x) * 4, n = p.n;
+__global__ __launch_bounds__(256) void ce_sum_kernel(Pair<SumArgs> jobs) {
+  const Share mine(jobs.first);
+  const SumArgs& p = jobs.x[mine.job];
+  const int64_t i = ((int64_t)mine.block * 256 + threadIdx.x) * 4, n = p.n;
   if (i >= n) return;
   float4_t v = *reinterpret_cast<const float4_t*>(p.sum + i);
   for (int z = 1; z < p.parts; ++z) v += *reinterpret_cast<const float4_t*>(p.sum + (size_t)z * (size_t)n + i);
@@ -586,13 +584,13 @@ uint32_t product_tiles(ProductArgs& x) {
 // Up to two products of one tile in one launch.
 template <class T>
 void launch_products(ProductArgs* x, int n, hipStream_t s) {
-  const uint32_t na = product_tiles<T>(x[0]), nb = n > 1 ? product_tiles<T>(x[1]) : 0;
-  ce_product_kernel<T><<<na + nb, T::NT, 0, s>>>(x[0], x[n - 1], na);
+  const uint32_t first = product_tiles<T>(x[0]), others = n > 1 ? product_tiles<T>(x[1]) : 0;
+  ce_product_kernel<T><<<first + others, T::NT, 0, s>>>(Pair<ProductArgs>{{x[0], x[n - 1]}, first});
 }
 void launch_sums(const SumArgs* x, int n, hipStream_t s) {
   auto grid = [](const SumArgs& a) { return (uint32_t)((a.n / 4 + 255) / 256); };
-  const uint32_t na = grid(x[0]);
-  ce_sum_kernel<<<na + (n > 1 ? grid(x[1]) : 0), 256, 0, s>>>(x[0], x[n - 1], na);
+  const uint32_t first = grid(x[0]);
+  ce_sum_kernel<<<first + (n > 1 ? grid(x[1]) : 0), 256, 0, s>>>(Pair<SumArgs>{{x[0], x[n - 1]}, first});
 }
 
 TileOp bf16_operand(const void* p, int64_t rows, int64_t cols, int64_t ld) {
@@ -696,7 +694,7 @@ void launch_prepare(const WeightArgs* w, const BlockArgs* x, const BlockArgs& v,
   const WeightArgs no_weights = {};
   const BlockArgs none = {};
   const uint32_t grid = (w ? 1 : 0) + (x ? x->nr * x->nc : 0) + v.nr * v.nc;
-  ce_prepare_kernel<<<grid, 256, 0, s>>>(w ? *w : no_weights, w != nullptr, x ? *x : none, v);
+  ce_prepare_kernel<<<grid, 256, 0, s>>>(w ? *w : no_weights, w != nullptr, Pair<BlockArgs>{{x ? *x : none, v}, x ? x->nr * x->nc : 0});
 }
 
 }  // namespace

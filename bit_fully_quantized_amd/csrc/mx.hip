@@ -99,8 +99,8 @@ struct MxRowArgs {
 // a group (the pair's larger top by one DPP swap), eight threads a 128-element
 // block, padding included.
 template <class T, bool SR, bool RHT>
-__global__ __launch_bounds__(256) void mx_row_kernel(MxRowArgs p) {
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__device__ __forceinline__ void mx_row(const MxRowArgs& p, uint32_t block) {
+  const int64_t id = (int64_t)block * 256 + threadIdx.x;
   const int32_t per = p.nb * 8;
   const int64_t row = id / per;
   if (row >= p.rows) return;
@@ -122,6 +122,16 @@ __global__ __launch_bounds__(256) void mx_row_kernel(MxRowArgs p) {
   if (!(h & 1)) p.scale[(row * per + h) >> 1] = (uint8_t)byte;
 }
 
+template <class T, bool SR, bool RHT>
+__global__ __launch_bounds__(256) void mx_row_kernel(MxRowArgs p) {
+  mx_row<T, SR, RHT>(p, blockIdx.x);
+}
+// The forward's operands: bf16 activations (nx workgroups) and fp32 weights.
+__global__ __launch_bounds__(256) void mx_row_pair_kernel(MxRowArgs x, MxRowArgs w, uint32_t nx) {
+  if (blockIdx.x < nx) mx_row<uint16_t, false, false>(x, blockIdx.x);
+  else mx_row<float, false, false>(w, blockIdx.x - nx);
+}
+
 struct MxColArgs {
   const void* x;       // dense [rows, cols], or codes of an MXFP4 operand [rows, cols]
   const uint8_t* xs;   // its scale bytes
@@ -139,15 +149,15 @@ struct MxIn {};  // tag: MXFP4 input
 // columns through LDS: rows are read whole, then each thread owns 32 rows of one
 // column, a group, and writes its 16 bytes (four groups of a column make a line of
 // 64).  MXFP4 input is decoded to bf16 on the way, which holds its values exactly.
+template <class T>
+using MxColElement = std::conditional_t<std::is_same<T, float>::value, float, uint16_t>;
 template <class T, bool SR, bool RHT>
-__global__ __launch_bounds__(256) void mx_col_kernel(MxColArgs p) {
+__device__ __forceinline__ void mx_col(const MxColArgs& p, uint32_t bx, uint32_t by, MxColElement<T> (*tile)[64], uint8_t (*sb)[4]) {
   constexpr bool kMx = std::is_same<T, MxIn>::value;
   constexpr bool kF32 = std::is_same<T, float>::value;
-  using E = std::conditional_t<kF32, float, uint16_t>;
-  __shared__ __attribute__((aligned(16))) E tile[128][64];
-  __shared__ __attribute__((aligned(4))) uint8_t sb[64][4];
+  using E = MxColElement<T>;
   const int t = threadIdx.x;
-  const int32_t r0 = (int32_t)blockIdx.y * 128, c0 = (int32_t)blockIdx.x * 64;
+  const int32_t r0 = (int32_t)by * 128, c0 = (int32_t)bx * 64;
   // 8 elements a load: 8 loads a row
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -207,10 +217,16 @@ __global__ __launch_bounds__(256) void mx_col_kernel(MxColArgs p) {
   const uint2 b = mx_codes16<SR>(v + 16, byte, block + 2, p.seed, p.offset);
   sb[c][rg] = (uint8_t)byte;
   if (col < p.cols)
-    *reinterpret_cast<uint4*>(p.codes + (col * p.nb + blockIdx.y) * 64 + rg * 16) = uint4{a.x, a.y, b.x, b.y};
+    *reinterpret_cast<uint4*>(p.codes + (col * p.nb + by) * 64 + rg * 16) = uint4{a.x, a.y, b.x, b.y};
   __syncthreads();
   if (t < 64 && c0 + t < p.cols)
-    *reinterpret_cast<uint32_t*>(p.scale + ((int64_t)(c0 + t) * p.nb + blockIdx.y) * 4) = *reinterpret_cast<const uint32_t*>(sb[t]);
+    *reinterpret_cast<uint32_t*>(p.scale + ((int64_t)(c0 + t) * p.nb + by) * 4) = *reinterpret_cast<const uint32_t*>(sb[t]);
+}
+template <class T, bool SR, bool RHT>
+__global__ __launch_bounds__(256) void mx_col_kernel(MxColArgs p) {
+  __shared__ __attribute__((aligned(16))) MxColElement<T> tile[128][64];
+  __shared__ __attribute__((aligned(4))) uint8_t sb[64][4];
+  mx_col<T, SR, RHT>(p, blockIdx.x, blockIdx.y, tile, sb);
 }
 
 // Both groupings of a dense bf16 matrix from one read: an output gradient is the left
@@ -231,11 +247,9 @@ struct MxDualArgs {
 };
 
 template <bool SR, bool RHT>
-__global__ __launch_bounds__(256) void mx_dual_kernel(MxDualArgs p) {
-  __shared__ __attribute__((aligned(16))) uint16_t tile[128][128];
-  __shared__ __attribute__((aligned(4))) uint8_t sb[128][4];
+__device__ __forceinline__ void mx_dual(const MxDualArgs& p, uint32_t bx, uint32_t by, uint16_t (*tile)[128], uint8_t (*sb)[4]) {
   const int t = threadIdx.x;
-  const int32_t r0 = (int32_t)blockIdx.y * 128, c0 = (int32_t)blockIdx.x * 128;
+  const int32_t r0 = (int32_t)by * 128, c0 = (int32_t)bx * 128;
   const int h = t & 7, c = c0 + h * 16;
   uint4 raw[4][2];
 #pragma unroll
@@ -264,7 +278,7 @@ __global__ __launch_bounds__(256) void mx_dual_kernel(MxDualArgs p) {
     const int64_t row = r0 + r;
     const uint2 q = mx_codes16<SR>(v, byte, (uint64_t)(row * padded_c + c) >> 3, p.seed, p.row_offset);
     if (row < p.rows) {
-      const int64_t at = (row * p.nbc + blockIdx.x) * 8 + h;
+      const int64_t at = (row * p.nbc + bx) * 8 + h;
       *reinterpret_cast<uint2*>(p.row_codes + at * 8) = c < p.cols ? q : uint2{0u, 0u};
       if (!(h & 1)) p.row_scale[at >> 1] = (uint8_t)byte;
     }
@@ -293,11 +307,29 @@ __global__ __launch_bounds__(256) void mx_dual_kernel(MxDualArgs p) {
     const uint2 b = mx_codes16<SR>(v + 16, byte, block + 2, p.seed, p.col_offset);
     sb[cc + i][rg] = (uint8_t)byte;
     if (col < p.cols)
-      *reinterpret_cast<uint4*>(p.col_codes + (col * p.nbr + blockIdx.y) * 64 + rg * 16) = uint4{a.x, a.y, b.x, b.y};
+      *reinterpret_cast<uint4*>(p.col_codes + (col * p.nbr + by) * 64 + rg * 16) = uint4{a.x, a.y, b.x, b.y};
   }
   __syncthreads();
   if (t < 128 && c0 + t < p.cols)
-    *reinterpret_cast<uint32_t*>(p.col_scale + ((int64_t)(c0 + t) * p.nbr + blockIdx.y) * 4) = *reinterpret_cast<const uint32_t*>(sb[t]);
+    *reinterpret_cast<uint32_t*>(p.col_scale + ((int64_t)(c0 + t) * p.nbr + by) * 4) = *reinterpret_cast<const uint32_t*>(sb[t]);
+}
+
+// All operands of the backward pass in one launch: nd workgroups for dY, the others for
+// the codes of the weights and of the activations.
+// (Passes over few tokens are as long as their launches: backward of 700 x 2000 over 400
+// 32 us with a launch for each operand, product and join, 20 with one for each kind.)
+template <bool SR, bool RHT>
+__global__ __launch_bounds__(256) void mx_backward_kernel(MxDualArgs d, uint32_t nd, Pair<MxColArgs> codes) {
+  __shared__ __attribute__((aligned(16))) uint16_t tile[128][128];
+  __shared__ __attribute__((aligned(4))) uint8_t sb[128][4];
+  uint32_t b = blockIdx.x;
+  if (b < nd) return mx_dual<SR, RHT>(d, b % (uint32_t)d.nbc, b / (uint32_t)d.nbc, tile, sb);
+  b -= nd;
+  const int job = b < codes.first ? 0 : 1;
+  const MxColArgs& p = codes.x[job];
+  if (job) b -= codes.first;
+  const uint32_t n = (uint32_t)(p.cols + 63) / 64;
+  mx_col<MxIn, SR, RHT>(p, b % n, b / n, reinterpret_cast<uint16_t (*)[64]>(tile), sb);
 }
 
 // ---- values ----------------------------------------------------------------------
@@ -394,10 +426,13 @@ __device__ __forceinline__ void store_run(const MxGemmArgs& p, int64_t row, int6
   }
 }
 
+// One product or two.
 template <class T>
-__global__ __launch_bounds__(T::NT, T::WAVES) void mx_gemm_kernel(MxGemmArgs p) {
+__global__ __launch_bounds__(T::NT, T::WAVES) void mx_gemm_kernel(Pair<MxGemmArgs> jobs) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
-  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits);
+  const Share mine(jobs.first);
+  const MxGemmArgs& p = jobs.x[mine.job];
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits, mine.block, mine.blocks);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
   T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t z, typename T::Acc& acc) __attribute__((always_inline)) {
     const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16;
@@ -473,10 +508,12 @@ __global__ __launch_bounds__(S::NT, 2) void mx_few_kernel(MxFewArgs a) {
   });
 }
 
-// C = (C +) the sum of the splits' results in order, 4 a thread.
-__global__ __launch_bounds__(256) void mx_join_kernel(MxGemmArgs p) {
+// C = (C +) the sum of the splits' results in order, 4 a thread; of one product or two.
+__global__ __launch_bounds__(256) void mx_join_kernel(Pair<MxGemmArgs> jobs) {
+  const Share mine(jobs.first);
+  const MxGemmArgs& p = jobs.x[mine.job];
   const int64_t I = p.Q.rows, J = p.P.rows, n = I * J, per = (J + 3) / 4;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, i = id / per, j = (id - i * per) * 4;
+  const int64_t id = (int64_t)mine.block * 256 + threadIdx.x, i = id / per, j = (id - i * per) * 4;
   if (i >= I) return;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   const float* s = p.partial + i * J + j;
@@ -499,11 +536,17 @@ using TileMid = Tile<EL_MX, 2, 2, 4, 4>;    // 128 x 128
 using TileSmall = Tile<EL_MX, 2, 2, 2, 2>;  // 64 x 64
 
 template <class T>
-hipError_t launch_tile(MxGemmArgs a, hipStream_t s) {
+uint32_t tile_grid(MxGemmArgs& a) {
   a.tiles_p = (uint32_t)((a.P.rows + T::BM - 1) / T::BM);
   a.tiles_q = (uint32_t)((a.Q.rows + T::BN - 1) / T::BN);
-  mx_gemm_kernel<T><<<T::grid((uint64_t)a.tiles_p * a.tiles_q * (uint32_t)a.splits), T::NT, 0, s>>>(a);
-  return hipGetLastError();
+  return T::grid((uint64_t)a.tiles_p * a.tiles_q * (uint32_t)a.splits);
+}
+template <class T>
+void launch_tile(const MxGemmArgs& a, const MxGemmArgs* second, hipStream_t s) {
+  Pair<MxGemmArgs> jobs = {{a, second ? *second : a}, 0};
+  jobs.first = tile_grid<T>(jobs.x[0]);
+  const uint32_t others = second ? tile_grid<T>(jobs.x[1]) : 0;
+  mx_gemm_kernel<T><<<jobs.first + others, T::NT, 0, s>>>(jobs);
 }
 
 TileOp mx_operand(const QView& q) {
@@ -524,7 +567,6 @@ TileOp mx_operand(const QView& q) {
 // tiles are as fast: 24 x 50304 over 1024 11.8 us here and 9.8 there, 64 x 4096 9.2 and
 // 5.3; 1 x 4096 4.5 and 5.0, and the quantization of A included).
 using Few = Skinny<EL_MX, 1, 64 * 1024>;
-bool mx_few(int64_t I, int64_t K) { return Few::fits(I, (K + 127) / 128 * 64); }
 
 // Tile and splits of a product, by an estimate of its time from what the tiles
 // measure (us on MI355X; a chunk is 256 elements of the reduction): alone on its CU
@@ -564,16 +606,17 @@ MxPlan mx_plan(int64_t I, int64_t J, int64_t K) {
 
 }  // namespace
 
+bool mx_is_few(int64_t M, int64_t K) { return Few::fits(M, (K + 127) / 128 * 64); }
+
 size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K) {
-  if (mx_few(I, K)) return 0;
+  if (mx_is_few(I, K)) return 0;
   const int z = mx_plan(I, J, K).splits;
   return z > 1 ? (size_t)z * (size_t)I * (size_t)J * 4 : 0;
 }
 
 namespace {
-// The product of few rows, if it is one; x: quantize them first, into `q`.
-bool launch_mx_few(const MxGemmArgs& a, const void* x, int64_t cols, const QView* q, hipStream_t s) {
-  if (!Few::fits(a.Q.rows, a.P.kb)) return false;
+// The product of few rows; x: quantize them first, into `q`.
+hipError_t launch_few(const MxGemmArgs& a, const void* x, int64_t cols, const QView* q, hipStream_t s) {
   MxFewArgs f = {};
   f.g = a;
   f.x = reinterpret_cast<const uint16_t*>(x);
@@ -583,7 +626,7 @@ bool launch_mx_few(const MxGemmArgs& a, const void* x, int64_t cols, const QView
     f.scale = q->s16;
   }
   mx_few_kernel<Few><<<Few::grid(a.P.rows), Few::NT, 0, s>>>(f);
-  return true;
+  return hipGetLastError();
 }
 
 MxGemmArgs mx_gemm_args(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate) {
@@ -602,32 +645,92 @@ MxGemmArgs mx_gemm_args(const QView& A, const QView& B, void* C, int c_dtype, in
 }
 }  // namespace
 
-bool launch_mx_linear_few(const void* X, const QView& Xq, const QView& Wq, void* Y, int y_dtype, hipStream_t s) {
-  return launch_mx_few(mx_gemm_args(Xq, Wq, Y, y_dtype, Wq.rows, 0), X, Xq.len, &Xq, s);
+hipError_t launch_mx_linear_few(const void* X, const QView& Xq, const QView& Wq, void* Y, int y_dtype, hipStream_t s) {
+  return launch_few(mx_gemm_args(Xq, Wq, Y, y_dtype, Wq.rows, 0), X, Xq.len, &Xq, s);
 }
+
+namespace {
+// A planned product; split: `part` is what the tiles write, joined into `out`.
+struct MxProduct {
+  MxGemmArgs part, out;
+  int tile;
+};
+MxProduct mx_product(const MxGemmArgs& a, int64_t K, float* partial) {
+  MxProduct x = {a, a, 0};
+  const MxPlan plan = mx_plan(a.Q.rows, a.P.rows, K);
+  x.tile = plan.tile;
+  x.part.splits = x.out.splits = partial ? plan.splits : 1;
+  x.out.partial = partial;
+  if (x.out.splits > 1) {
+    x.part.C = partial;
+    x.part.ldc = a.P.rows;
+    x.part.zstride = a.Q.rows * a.P.rows;
+    x.part.bf16 = 0;
+    x.part.accumulate = 0;
+    x.part.vec = (a.P.rows & 3) == 0;
+  }
+  return x;
+}
+// One product, or two of one tile.
+hipError_t launch_products(const MxProduct* x, int n, hipStream_t s) {
+  const MxGemmArgs* second = n > 1 ? &x[1].part : nullptr;
+  if (x[0].tile == 2) launch_tile<TileBig>(x[0].part, second, s);
+  else if (x[0].tile == 1) launch_tile<TileMid>(x[0].part, second, s);
+  else launch_tile<TileSmall>(x[0].part, second, s);
+  return hipGetLastError();
+}
+// The joins of those that are split.
+hipError_t launch_joins(const MxProduct* x, int n, hipStream_t s) {
+  Pair<MxGemmArgs> jobs = {};
+  uint32_t grid[2] = {0, 0};
+  int k = 0;
+  for (int i = 0; i < n; ++i) {
+    if (x[i].out.splits == 1) continue;
+    jobs.x[k] = x[i].out;
+    grid[k] = (uint32_t)((x[i].out.Q.rows * ((x[i].out.P.rows + 3) / 4) + 255) / 256);
+    ++k;
+  }
+  if (!k) return hipSuccess;
+  jobs.first = grid[0];
+  mx_join_kernel<<<grid[0] + grid[1], 256, 0, s>>>(jobs);
+  return hipGetLastError();
+}
+}  // namespace
 
 hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
                           hipStream_t s) {
-  MxGemmArgs a = mx_gemm_args(A, B, C, c_dtype, ldc, accumulate);
-  if (launch_mx_few(a, nullptr, 0, nullptr, s)) return hipGetLastError();
-  a.partial = partial;
-  const MxPlan plan = mx_plan(A.rows, B.rows, A.len);
-  a.splits = partial ? plan.splits : 1;
-  auto launch = [&](const MxGemmArgs& g) {
-    return plan.tile == 2 ? launch_tile<TileBig>(g, s) : plan.tile == 1 ? launch_tile<TileMid>(g, s) : launch_tile<TileSmall>(g, s);
-  };
-  if (a.splits == 1) return launch(a);
-  MxGemmArgs part = a;
-  part.C = partial;
-  part.ldc = B.rows;
-  part.zstride = A.rows * B.rows;
-  part.bf16 = 0;
-  part.accumulate = 0;
-  part.vec = (B.rows & 3) == 0;
-  if (hipError_t e = launch(part); e != hipSuccess) return e;
-  const int64_t n = A.rows * ((B.rows + 3) / 4);
-  mx_join_kernel<<<(uint32_t)((n + 255) / 256), 256, 0, s>>>(a);
-  return hipGetLastError();
+  const MxGemmArgs a = mx_gemm_args(A, B, C, c_dtype, ldc, accumulate);
+  if (mx_is_few(A.rows, A.len)) return launch_few(a, nullptr, 0, nullptr, s);
+  const MxProduct x = mx_product(a, A.len, partial);
+  if (hipError_t e = launch_products(&x, 1, s); e != hipSuccess) return e;
+  return launch_joins(&x, 1, s);
+}
+
+size_t mx_gemm_pair_workspace_bytes(int64_t I, int64_t J, int64_t K, int64_t I2, int64_t J2, int64_t K2) {
+  return (mx_gemm_workspace_bytes(I, J, K) + 255) / 256 * 256 + mx_gemm_workspace_bytes(I2, J2, K2);
+}
+
+hipError_t launch_mx_gemm_pair(const QView& A, const QView& B, void* C, int c_dtype, const QView& A2, const QView& B2, void* C2,
+                               int c2_dtype, float* partial, hipStream_t s) {
+  const MxGemmArgs a[2] = {mx_gemm_args(A, B, C, c_dtype, B.rows, 0), mx_gemm_args(A2, B2, C2, c2_dtype, B2.rows, 0)};
+  const size_t first = (mx_gemm_workspace_bytes(A.rows, B.rows, A.len) + 255) / 256 * 256;
+  float* room[2] = {partial, partial + first / 4};
+  const int64_t K[2] = {A.len, A2.len};
+  MxProduct x[2];
+  int n = 0;
+  for (int i = 0; i < 2; ++i) {
+    if (mx_is_few(a[i].Q.rows, K[i])) {
+      if (hipError_t e = launch_few(a[i], nullptr, 0, nullptr, s); e != hipSuccess) return e;
+    } else {
+      x[n++] = mx_product(a[i], K[i], room[i]);
+    }
+  }
+  for (int i = 0; i < n;) {
+    const int k = i + 1 < n && x[i].tile == x[i + 1].tile ? 2 : 1;
+    if (hipError_t e = launch_products(x + i, k, s); e != hipSuccess) return e;
+    i += k;
+  }
+  return launch_joins(x, n, s);
 }
 
 hipError_t launch_mx_values(const QView& q, void* out, int dtype, hipStream_t s) {
@@ -663,22 +766,22 @@ hipError_t launch_col(const MxColArgs& a, bool sr, bool rht, dim3 grid, hipStrea
 }
 }  // namespace
 
-hipError_t launch_mx_quant(const MxQuantParams& q, hipStream_t s) {
-  const bool sr = q.rounding == TJ2_SR;
-  if (q.grouping == TJ2_GROUP_ROW) {
-    MxRowArgs a = {};
-    a.x = q.x;
-    a.codes = q.out.codes;
-    a.scale = q.out.s16;
-    a.rows = q.rows;
-    a.cols = (int32_t)q.cols;
-    a.nb = (int32_t)q.out.nb;
-    a.mask = q.rht_mask;
-    a.seed = q.seed;
-    a.offset = q.offset;
-    const uint32_t grid = (uint32_t)((q.rows * q.out.nb * 8 + 255) / 256);
-    return q.in_dtype == TJ2_BF16 ? launch_row<uint16_t>(a, sr, q.rht, grid, s) : launch_row<float>(a, sr, q.rht, grid, s);
-  }
+namespace {
+MxRowArgs row_args(const MxQuantParams& q) {
+  MxRowArgs a = {};
+  a.x = q.x;
+  a.codes = q.out.codes;
+  a.scale = q.out.s16;
+  a.rows = q.rows;
+  a.cols = (int32_t)q.cols;
+  a.nb = (int32_t)q.out.nb;
+  a.mask = q.rht_mask;
+  a.seed = q.seed;
+  a.offset = q.offset;
+  return a;
+}
+uint32_t row_grid(const MxRowArgs& a) { return (uint32_t)((a.rows * a.nb * 8 + 255) / 256); }
+MxColArgs col_args(const MxQuantParams& q) {
   MxColArgs a = {};
   a.x = q.x;
   a.ldx = q.cols;
@@ -696,35 +799,56 @@ hipError_t launch_mx_quant(const MxQuantParams& q, hipStream_t s) {
   a.mask = q.rht_mask;
   a.seed = q.seed;
   a.offset = q.offset;
-  const dim3 grid((uint32_t)((q.cols + 63) / 64), (uint32_t)q.out.nb);
+  return a;
+}
+dim3 col_grid(const MxColArgs& a) { return dim3((uint32_t)(a.cols + 63) / 64, (uint32_t)a.nb); }
+}  // namespace
+
+hipError_t launch_mx_quant(const MxQuantParams& q, hipStream_t s) {
+  const bool sr = q.rounding == TJ2_SR;
+  if (q.grouping == TJ2_GROUP_ROW) {
+    const MxRowArgs a = row_args(q);
+    const uint32_t grid = row_grid(a);
+    return q.in_dtype == TJ2_BF16 ? launch_row<uint16_t>(a, sr, q.rht, grid, s) : launch_row<float>(a, sr, q.rht, grid, s);
+  }
+  const MxColArgs a = col_args(q);
+  const dim3 grid = col_grid(a);
   if (q.in_dtype == TJ2_MXFP4) return launch_col<MxIn>(a, sr, q.rht, grid, s);
   return q.in_dtype == TJ2_BF16 ? launch_col<uint16_t>(a, sr, q.rht, grid, s) : launch_col<float>(a, sr, q.rht, grid, s);
 }
 
-hipError_t launch_mx_dual(const void* x, const QView& row, const QView& col, int rounding, bool rht, uint32_t row_mask,
-                          uint32_t col_mask, uint64_t seed, uint64_t row_offset, uint64_t col_offset, hipStream_t s) {
-  MxDualArgs a = {};
-  a.x = reinterpret_cast<const uint16_t*>(x);
-  a.row_codes = row.codes;
-  a.row_scale = row.s16;
-  a.col_codes = col.codes;
-  a.col_scale = col.s16;
-  a.rows = (int32_t)row.rows;
-  a.cols = (int32_t)col.rows;
-  a.nbr = (int32_t)col.nb;
-  a.nbc = (int32_t)row.nb;
-  a.row_mask = row_mask & 0xFFFFu;
-  a.col_mask = col_mask & 0xFFFFu;
-  a.seed = seed;
-  a.row_offset = row_offset;
-  a.col_offset = col_offset;
-  const dim3 grid((uint32_t)a.nbc, (uint32_t)a.nbr);
-  if (rounding == TJ2_SR) {
-    if (rht) mx_dual_kernel<true, true><<<grid, 256, 0, s>>>(a);
-    else mx_dual_kernel<true, false><<<grid, 256, 0, s>>>(a);
+hipError_t launch_mx_forward_operands(const MxQuantParams& x, const MxQuantParams& w, hipStream_t s) {
+  const MxRowArgs a = row_args(x), b = row_args(w);
+  mx_row_pair_kernel<<<row_grid(a) + row_grid(b), 256, 0, s>>>(a, b, row_grid(a));
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_backward_operands(const MxQuantParams& dy_row, const MxQuantParams& dy_col, const MxQuantParams& w,
+                                       const MxQuantParams& x, hipStream_t s) {
+  MxDualArgs d = {};
+  d.x = reinterpret_cast<const uint16_t*>(dy_row.x);
+  d.row_codes = dy_row.out.codes;
+  d.row_scale = dy_row.out.s16;
+  d.col_codes = dy_col.out.codes;
+  d.col_scale = dy_col.out.s16;
+  d.rows = (int32_t)dy_row.rows;
+  d.cols = (int32_t)dy_row.cols;
+  d.nbr = (int32_t)dy_col.out.nb;
+  d.nbc = (int32_t)dy_row.out.nb;
+  d.row_mask = dy_row.rht_mask;
+  d.col_mask = dy_col.rht_mask;
+  d.seed = dy_row.seed;
+  d.row_offset = dy_row.offset;
+  d.col_offset = dy_col.offset;
+  const dim3 gw = col_grid(col_args(w)), gx = col_grid(col_args(x));
+  const Pair<MxColArgs> codes = {{col_args(w), col_args(x)}, gw.x * gw.y};
+  const uint32_t nd = (uint32_t)d.nbc * (uint32_t)d.nbr, grid = nd + codes.first + gx.x * gx.y;
+  if (dy_row.rounding == TJ2_SR) {
+    if (dy_row.rht) mx_backward_kernel<true, true><<<grid, 256, 0, s>>>(d, nd, codes);
+    else mx_backward_kernel<true, false><<<grid, 256, 0, s>>>(d, nd, codes);
   } else {
-    if (rht) mx_dual_kernel<false, true><<<grid, 256, 0, s>>>(a);
-    else mx_dual_kernel<false, false><<<grid, 256, 0, s>>>(a);
+    if (dy_row.rht) mx_backward_kernel<false, true><<<grid, 256, 0, s>>>(d, nd, codes);
+    else mx_backward_kernel<false, false><<<grid, 256, 0, s>>>(d, nd, codes);
   }
   return hipGetLastError();
 }

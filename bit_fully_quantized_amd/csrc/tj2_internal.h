@@ -173,17 +173,25 @@ struct MxQuantParams {
   QView out;
 };
 hipError_t launch_mx_quant(const MxQuantParams& q, hipStream_t s);
-// A dense bf16 matrix grouped along its rows and along its columns from one read.
-hipError_t launch_mx_dual(const void* x, const QView& row, const QView& col, int rounding, bool rht, uint32_t row_mask,
-                          uint32_t col_mask, uint64_t seed, uint64_t row_offset, uint64_t col_offset, hipStream_t s);
+// The linear layer's operands in one launch each: X (bf16) and W (fp32) along their
+// rows, rounded to nearest; dY both ways from one read, and the codes of W and X
+// regrouped (all with dy_row's rounding and rht).
+hipError_t launch_mx_forward_operands(const MxQuantParams& x, const MxQuantParams& w, hipStream_t s);
+hipError_t launch_mx_backward_operands(const MxQuantParams& dy_row, const MxQuantParams& dy_col, const MxQuantParams& w,
+                                       const MxQuantParams& x, hipStream_t s);
 hipError_t launch_mx_values(const QView& q, void* out, int dtype, hipStream_t s);
 size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K);
 hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
                           hipStream_t s);
+// C = A B^T and C2 = A2 B2^T together, `partial` of mx_gemm_pair_workspace_bytes.
+size_t mx_gemm_pair_workspace_bytes(int64_t I, int64_t J, int64_t K, int64_t I2, int64_t J2, int64_t K2);
+hipError_t launch_mx_gemm_pair(const QView& A, const QView& B, void* C, int c_dtype, const QView& A2, const QView& B2, void* C2,
+                               int c2_dtype, float* partial, hipStream_t s);
 
-// The linear layer's forward for few rows in one launch, X's quantization into Xq
-// included; false: too many rows, nothing was launched.
-bool launch_mx_linear_few(const void* X, const QView& Xq, const QView& Wq, void* Y, int y_dtype, hipStream_t s);
+// The linear layer's forward for few rows (mx_is_few) in one launch, X's quantization
+// into Xq included.
+bool mx_is_few(int64_t M, int64_t K);
+hipError_t launch_mx_linear_few(const void* X, const QView& Xq, const QView& Wq, void* Y, int y_dtype, hipStream_t s);
 
 // Cross entropy of X W^T (loss.hip): bf16 X [T, K] at pitch ldx, W [V, K] at ldw.
 struct CeParams {

@@ -138,6 +138,20 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t 
 
 constexpr uint32_t kCus = 256;
 
+// Arguments of a launch that does two jobs: `first` workgroups take x[0], the others
+// x[1].  (Indexed, so that what differs is read from the arguments as scalars.)
+template <class A>
+struct Pair {
+  A x[2];
+  uint32_t first;
+};
+// This workgroup's job, its number there and the job's workgroups.
+struct Share {
+  uint32_t job, block, blocks;
+  __device__ __forceinline__ explicit Share(uint32_t first)
+      : job(blockIdx.x < first ? 0 : 1), block(job ? blockIdx.x - first : blockIdx.x), blocks(job ? gridDim.x - first : first) {}
+};
+
 template <int EL, int WM, int WN, int TM, int TN>
 struct Tile {
   static constexpr int kWN = WN, kTM = TM, kTN = TN;
