@@ -366,12 +366,15 @@ __device__ __forceinline__ void ce_weights(const WeightArgs& p) {
 
 // A bf16 matrix [rows, cols] (cols a multiple of 16) into blocked operands: `copy`
 // [rows, cols] and `turned` [cols, rows], zero up to whole chunks; either may be
-// NULL.  64 x 64 through LDS.
+// NULL.  64 x 64 through LDS.  Rows of ignored tokens (y, if not NULL) become zero:
+// their dz is, but an infinity or NaN in them times zero would not be.
 struct BlockArgs {
   const uint16_t* in;
   int64_t rows, cols, ld;
   uint16_t *copy, *turned;
   uint32_t nr, nc;  // chunks of rows and of columns
+  const int64_t* y;
+  int64_t ignore;
 };
 __device__ __forceinline__ void block_tile(const BlockArgs& p, uint32_t br, uint32_t bc) {
   __shared__ uint16_t tile[64][66];
@@ -381,7 +384,7 @@ __device__ __forceinline__ void block_tile(const BlockArgs& p, uint32_t br, uint
   for (int i = 0; i < 2; ++i) {
     const int r = i * 32 + (t >> 3), c = (t & 7) * 8;
     uint4 v = {0u, 0u, 0u, 0u};
-    if (r0 + r < p.rows && c0 + c < p.cols) v = *reinterpret_cast<const uint4*>(p.in + (r0 + r) * p.ld + c0 + c);
+    if (r0 + r < p.rows && c0 + c < p.cols && !(p.y && p.y[r0 + r] == p.ignore)) v = *reinterpret_cast<const uint4*>(p.in + (r0 + r) * p.ld + c0 + c);
     if (p.copy && r0 + r < p.rows)
       *reinterpret_cast<uint4*>(p.copy + ((r0 >> 7) * p.nc + bc) * 8192 + ((r0 & 127) + r) * 64 + c) = v;
     uint32_t* s = reinterpret_cast<uint32_t*>(&tile[r][c]);
@@ -687,7 +690,7 @@ CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
 BlockArgs block_args(const void* in, int64_t rows, int64_t cols, int64_t ld, void* copy, void* turned) {
   return BlockArgs{reinterpret_cast<const uint16_t*>(in), rows,
                    cols, ld, reinterpret_cast<uint16_t*>(copy),
-                   reinterpret_cast<uint16_t*>(turned), (uint32_t)((rows + 63) / 64), (uint32_t)((cols + 63) / 64)};
+                   reinterpret_cast<uint16_t*>(turned), (uint32_t)((rows + 63) / 64), (uint32_t)((cols + 63) / 64), nullptr, 0};
 }
 // w, x: NULL for none
 void launch_prepare(const WeightArgs* w, const BlockArgs* x, const BlockArgs& v, hipStream_t s) {
@@ -747,7 +750,9 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
   float* top = reinterpret_cast<float*>(w + sp.top);
   float *dx = reinterpret_cast<float*>(w + sp.dx), *part = reinterpret_cast<float*>(w + sp.part);
   const WeightArgs weights = {c.dloss, c.y, c.T, c.V, c.ignore, reinterpret_cast<float*>(w + sp.c), top};
-  const BlockArgs xb = block_args(c.X, c.T, c.K, c.ldx, sp.blocked ? w + sp.xb : nullptr, w + sp.xt);
+  BlockArgs xb = block_args(c.X, c.T, c.K, c.ldx, sp.blocked ? w + sp.xb : nullptr, w + sp.xt);
+  xb.y = c.y;
+  xb.ignore = c.ignore;
   const bool one = sp.piece >= c.V;
   for (int64_t v0 = 0; v0 < c.V; v0 += sp.piece) {
     const int64_t vn = std::min(sp.piece, c.V - v0);

@@ -209,6 +209,97 @@ def test_cross_entropy_stream_graph_and_repeat():
         assert all(torch.equal(a, b) for a, b in zip(held, both(static.clone())))
 
 
+def test_cross_entropy_ignored_rows_enter_no_gradient():
+    for T in (40, 2100):  # rows read as they are, and copied into blocks first
+        X, W, y, _ = ce_inputs(T, 64, 500, 7)
+        y[3] = y[17] = -100
+        d = torch.ones(T, device="cuda")
+        d[3] = NAN
+        _, lse = tj2.linear_ce_fwd(X, W, y)
+        want = tj2.linear_ce_bwd(X, W, y, lse, torch.ones(T, device="cuda"))
+        X[3], X[17] = NAN, INF
+        _, lse = tj2.linear_ce_fwd(X, W, y)
+        got = tj2.linear_ce_bwd(X, W, y, lse, d)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert (got[0][3] == 0).all() and torch.isfinite(got[1]).all()
+
+
+@pytest.mark.parametrize("T", [15, 16, 17, 31, 33, 48, 63, 64, 65, 127])
+@pytest.mark.parametrize("K", [16, 208, 1040])
+def test_cross_entropy_few_tokens(T, K):
+    X, W, y, g = ce_inputs(T, K, 515, T * K)
+    ce_check(X, W, y, torch.randn(T, generator=g, device="cuda"))
+
+
+@pytest.mark.parametrize("T,K,V,ldx,ldw", [(2047, 80, 700, 88, 96), (2048, 80, 700, 80, 160), (2049, 144, 513, 152, 144),
+                                           (30, 80, 700, 96, 88)])
+def test_cross_entropy_pitched_with_and_without_blocks(T, K, V, ldx, ldw):
+    X, W, y, _ = ce_inputs(T, K, V, 21)
+    Xp = torch.full((T, ldx), NAN, device="cuda", dtype=torch.bfloat16)
+    Wp = torch.full((V, ldw), NAN, device="cuda", dtype=torch.bfloat16)
+    Xp[:, :K], Wp[:, :K] = X, W
+    d = torch.full((T,), 1.0 / T, device="cuda")
+    ce_check(Xp[:, :K], Wp[:, :K], y, d)
+
+
+@pytest.mark.parametrize("T,K,V", [(16384, 32, 16400), (60000, 32, 4400), (2500, 608, 6000), (1024, 272, 20001)])
+def test_cross_entropy_last_piece_and_large_tiles(T, K, V):
+    X, W, y, g = ce_inputs(T, K, V, 22)
+    ce_check(X, W, y, torch.rand(T, generator=g, device="cuda"))
+
+
+def test_cross_entropy_graphs_share_a_workspace():
+    """Two captured backward passes with one workspace, replayed in turns among eager calls that use it too."""
+    cases = []
+    ws = None
+    for seed, (T, K, V) in ((31, (300, 96, 2000)), (32, (2100, 64, 900))):
+        X, W, y, _ = ce_inputs(T, K, V, seed)
+        d = torch.full((T,), 1.0 / T, device="cuda")
+        n = int(tj2.lib().tj2_linear_ce_bwd_workspace_size(T, K, V))
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda") if ws is None or ws.numel() < n else ws
+        cases.append((X, W, y, tj2.linear_ce_fwd(X, W, y)[1], d))
+    want = [tj2.linear_ce_bwd(*c) for c in cases]
+    graphs, held = [], []
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        dX, dW = torch.empty_like(c[0]), torch.empty_like(c[1])
+        with torch.cuda.graph(g):
+            tj2.linear_ce_bwd(*c, dX=dX, dW=dW, workspace=ws)
+        graphs.append(g)
+        held.append((dX, dW))
+    for k in (0, 1, 0, 0, 1):
+        for t in held[k]:
+            t.fill_(NAN)
+        graphs[k].replay()
+        other = tj2.linear_ce_bwd(*cases[1 - k], workspace=ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held[k], want[k]))
+        assert all(torch.equal(a, b) for a, b in zip(other, want[1 - k]))
+
+
+def test_cross_entropy_on_two_streams_at_once():
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    data, want, got = [], [], [[], []]
+    for seed, (T, K, V) in ((41, (700, 128, 3001)), (42, (60, 512, 9000))):
+        X, W, y, _ = ce_inputs(T, K, V, seed)
+        data.append((X, W, y, torch.full((T,), 0.5, device="cuda")))
+
+    def both(X, W, y, d):
+        loss, lse = tj2.linear_ce_fwd(X, W, y)
+        return (loss, *tj2.linear_ce_bwd(X, W, y, lse, d))
+    for c in data:
+        want.append(both(*c))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for i, s in enumerate(sides):
+            with torch.cuda.stream(s):
+                got[i].append(both(*data[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
 # ---- distillation ----------------------------------------------------------------------------------------------
 def distill_inputs(T, V, k, dtype, seed, pitch=None):
     g = gen(seed)

@@ -208,6 +208,76 @@ def test_wrapped_weights_streams_and_graph():
         assert torch.equal(Y, tj2.mx_linear_fwd(static.clone(), None, 64, Wq=Wq)[0])
 
 
+def values(q):
+    return tj2.mx_dequantize(q, dtype=torch.float32).double()
+
+
+def near(got, A, B):
+    """close() on the GPU: K + 16 half steps of fp32 on the sum of magnitudes and half a step of a bf16 result."""
+    ref, mags = A @ B.T, A.abs() @ B.abs().T
+    tol = (A.shape[1] + 16) * 2.0 ** -24 * mags + (ref.abs() * 2.0 ** -8 if got.dtype == torch.bfloat16 else 0)
+    assert ((got.double() - ref).abs() <= tol).all(), float(((got.double() - ref).abs() - tol).max())
+
+
+@pytest.mark.parametrize("I,J,K", [(2100, 1500, 2064), (3000, 2600, 1040), (2048, 4096, 256), (16384, 1024, 528), (1100, 9001, 272),
+                                   (129, 50304, 144), (33, 17, 4096), (2049, 65, 16400)])
+def test_gemm_of_every_tile_and_split(I, J, K):
+    t, _ = to_gpu(data(I, K, 1, spread=1), torch.bfloat16)
+    w, _ = to_gpu(data(J, K, 2, spread=1), torch.float32)
+    qa, qb = tj2.mx_quantize(t), tj2.mx_quantize(w)
+    A, B = values(qa), values(qb)
+    near(tj2.mx_gemm(qa, qb, out_dtype=torch.bfloat16), A, B)
+    near(tj2.mx_gemm(qa, qb), A, B)
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 16, 16), (16, 16, 4096), (17, 48, 16), (8192, 64, 128), (300, 1024, 8192), (2100, 1040, 1488),
+                                   (5, 4096, 16), (127, 128, 129 * 16), (4097, 272, 32)])
+@pytest.mark.parametrize("rht", [True, False])
+def test_backward_products_of_every_shape(M, K, N, rht):
+    """Both products against their operands, which mx_quantize gives bit for bit as the oracle does."""
+    x, _ = to_gpu(data(M, K, 1), torch.bfloat16)
+    w, _ = to_gpu(data(N, K, 2, spread=1), torch.float32)
+    dy, _ = to_gpu(data(M, N, 3) * np.float32(1e-3), torch.bfloat16)
+    Y, saved = tj2.mx_linear_fwd(x, w, N)
+    near(Y, values(tj2.mx_quantize(x)), values(tj2.mx_quantize(w)))
+    seed, offset = 9, 24
+    for dt in (torch.bfloat16, torch.float32):
+        dX, dW = tj2.mx_linear_bwd(dy, saved, K, seed=seed, offset=offset, rht=rht, dx_dtype=dt)
+        sx, sw = (tj2.lib().tj2_rht_signs(seed, offset + o) if rht else 0 for o in (0, 2))
+        opt = dict(rounding=tj2.SR, rht=rht, seed=seed)
+        near(dX, values(tj2.mx_quantize(dy, signs=sx, offset=offset, **opt)),
+             values(tj2.mx_quantize(saved["Wq"], grouping=tj2.GROUP_COL, signs=sx, offset=offset + 1, **opt)))
+        near(dW, values(tj2.mx_quantize(dy, grouping=tj2.GROUP_COL, signs=sw, offset=offset + 2, **opt)),
+             values(tj2.mx_quantize(saved["Xq"], grouping=tj2.GROUP_COL, signs=sw, offset=offset + 3, **opt)))
+
+
+def test_backward_graphs_share_a_workspace():
+    """Two captured backward passes with one workspace, replayed in turns among eager calls that use it too."""
+    cases, ws = [], None
+    for seed, (M, K, N) in ((1, (300, 1024, 8192)), (2, (70, 48, 96))):
+        x, _ = to_gpu(data(M, K, seed), torch.bfloat16)
+        w, _ = to_gpu(data(N, K, seed + 1), torch.float32)
+        dy, _ = to_gpu(data(M, N, seed + 2), torch.bfloat16)
+        ws = tj2.mx_linear_bwd_workspace(M, N, K) if ws is None else ws
+        cases.append((dy, tj2.mx_linear_fwd(x, w, N)[1], K))
+    opt = dict(seed=3, offset=8)
+    want = [tj2.mx_linear_bwd(*c, **opt) for c in cases]
+    graphs, held = [], [tuple(torch.empty_like(t) for t in w) for w in want]
+    for c, (dX, dW) in zip(cases, held):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tj2.mx_linear_bwd(*c, **opt, dX=dX, dW=dW, workspace=ws)
+        graphs.append(g)
+    for k in (0, 1, 0, 0, 1):
+        for t in held[k]:
+            t.fill_(float("nan"))
+        graphs[k].replay()
+        other = tj2.mx_linear_bwd(*cases[1 - k], **opt, workspace=ws)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held[k], want[k]))
+        assert all(torch.equal(a, b) for a, b in zip(other, want[1 - k]))
+
+
 def test_binding_refuses():
     x = torch.zeros(4, 32, device="cuda", dtype=torch.bfloat16)
     w = torch.zeros(16, 32, device="cuda")
