@@ -39,7 +39,6 @@
 namespace tj2 {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -81,6 +80,14 @@ __device__ __forceinline__ u32x4_t raw_buffer(const uint8_t* base) {
   d.z = 0x7FFFFFFFu;
   d.w = 0x00020000u;
   return d;
+}
+
+// A value the same for all lanes, kept in a scalar register: the compiler would rather
+// read a kernel argument again, in the middle of a loop and waiting for it.
+__device__ __forceinline__ uint32_t pinned(uint32_t x) {
+  x = __builtin_amdgcn_readfirstlane(x);
+  asm volatile("" : "+s"(x));
+  return x;
 }
 
 // Descriptors written by vector instructions (readfirstlane) may be read by a
@@ -251,14 +258,21 @@ struct Tile {
     // byte in the row of what it fetches for row i * RPI + lr
     auto gp = [&](int i) __attribute__((always_inline)) { return (uint32_t)((t & 7) ^ p_key(lr) ^ p_key(i * RPI)) * 16u; };
     auto gq = [&](int i) __attribute__((always_inline)) { return (uint32_t)((t & 7) ^ q_key(lr) ^ q_key(i * RPI)) * 16u; };
-    const uint32_t vp = (uint32_t)lr * (uint32_t)P.ld, vq = (uint32_t)lrq * (uint32_t)Q.ld;
+    // (MXFP4 operands are row-major with one pitch, all of it codes)
+    constexpr bool kMx = EL == EL_MX;
+    const uint32_t ldp = pinned((uint32_t)P.ld), ldq = kMx ? ldp : pinned((uint32_t)Q.ld);
+    const uint32_t bsp = kMx ? 128 * ldp : pinned((uint32_t)P.bs), bsq = kMx ? bsp : pinned((uint32_t)Q.bs);
+    const uint32_t csp = kMx ? 128 : pinned((uint32_t)P.cs), csq = kMx ? 128 : pinned((uint32_t)Q.cs);
+    const int kbp = kMx ? (int)ldp : (int)pinned((uint32_t)P.kb), kbq = kMx ? kbp : (int)pinned((uint32_t)Q.kb);
+    const uint32_t pitch_s = ldp / 16;  // scale bytes a row
+    const uint32_t vp = (uint32_t)lr * ldp, vq = (uint32_t)lrq * ldq;
     // and the uniform offset of its row i * RPI
     static_assert(128 % RPI == 0 && (BM < 128 || BM % 128 == 0) && (BN < 128 || BN % 128 == 0), "rows of a block");
     auto far_p = [&](int i) __attribute__((always_inline)) {
-      return (uint32_t)(i * RPI / 128) * (uint32_t)P.bs + (uint32_t)(i * RPI % 128) * (uint32_t)P.ld;
+      return (uint32_t)(i * RPI / 128) * bsp + (uint32_t)(i * RPI % 128) * ldp;
     };
     auto far_q = [&](int i) __attribute__((always_inline)) {
-      return (uint32_t)(i * RPI / 128) * (uint32_t)Q.bs + (uint32_t)(i * RPI % 128) * (uint32_t)Q.ld;
+      return (uint32_t)(i * RPI / 128) * bsq + (uint32_t)(i * RPI % 128) * ldq;
     };
     const uint32_t lds_w = lds_address(sm.stage[0]) + (uint32_t)w * 1024u;
     constexpr uint32_t kStage = ROWS * 128;
@@ -267,20 +281,23 @@ struct Tile {
     // of Q: BM is a multiple of 32)
     constexpr int SJ = EL == EL_MX ? SCALE_DW / NT : 1;
     static_assert(SCALE_DW % NT == 0 && BM % 32 == 0, "whole scale loads");
-    const uint32_t vs = (uint32_t)(lane >> 1) * (uint32_t)P.lds + (lane & 1) * 4;  // P and Q have the same pitch
+    const uint32_t vs = (uint32_t)(lane >> 1) * pitch_s + (lane & 1) * 4;
 
-    // The load cursor: its item and the item's rows (none once the items are done).
+    // The load cursor: its item, the item's rows (none once the items are done), where
+    // its chunk starts and the bytes of a row from there on.
     Item ahead = now;
     uint32_t ahead_at = items.at;
     const uint8_t *pb, *qb, *psb = nullptr, *qsb = nullptr;
-    int np, nq;
+    int np, nq, leftp, leftq;
     auto enter = [&]() __attribute__((always_inline)) {
       const int64_t p0 = (int64_t)ahead.tp * BM, q0 = (int64_t)ahead.tq * BN;
-      pb = P.p + (p0 >> 7) * P.bs + (p0 & 127) * P.ld;
-      qb = Q.p + (q0 >> 7) * Q.bs + (q0 & 127) * Q.ld;
+      pb = P.p + (p0 >> 7) * P.bs + (p0 & 127) * P.ld + mul32(ahead.c, csp);
+      qb = Q.p + (q0 >> 7) * Q.bs + (q0 & 127) * Q.ld + mul32(ahead.c, csq);
+      leftp = kbp - ahead.c * 128;
+      leftq = kbq - ahead.c * 128;
       if constexpr (EL == EL_MX) {
-        psb = P.s + p0 * P.lds;
-        qsb = Q.s + q0 * Q.lds;
+        psb = P.s + p0 * P.lds + ahead.c * 8;
+        qsb = Q.s + q0 * Q.lds + ahead.c * 8;
       }
       np = __builtin_amdgcn_readfirstlane((int)min(P.rows - p0, (int64_t)BM));
       nq = __builtin_amdgcn_readfirstlane((int)min(Q.rows - q0, (int64_t)BN));
@@ -288,22 +305,17 @@ struct Tile {
     enter();
     // The loads of the cursor's chunk into `stage`, one at a time: begin() sets them up.
     u32x4_t dp, dq, dsp, dsq;
-    uint32_t leftp, leftq, bads = 0, dst = 0, sdst = 0;
+    uint32_t bads = 0, dst = 0, sdst = 0;
     auto begin = [&](uint32_t stage) __attribute__((always_inline)) {
-      const uint32_t at = (uint32_t)ahead.c * 128u;
-      dp = raw_buffer(pb + mul32(ahead.c, P.cs));
-      dq = raw_buffer(qb + mul32(ahead.c, Q.cs));
+      dp = raw_buffer(pb);
+      dq = raw_buffer(qb);
       settle(dp, dq);
-      // bytes of the row from the chunk on (none past the row's end)
-      leftp = (uint32_t)max(P.kb - (int32_t)at, 0);
-      leftq = (uint32_t)max(Q.kb - (int32_t)at, 0);
       dst = lds_w + stage * kStage;
       if constexpr (EL == EL_MX) {
-        const uint32_t ats = (uint32_t)ahead.c * 8u;
-        dsp = raw_buffer(psb + ats);
-        dsq = raw_buffer(qsb + ats);
+        dsp = raw_buffer(psb);
+        dsq = raw_buffer(qsb);
         settle(dsp, dsq);
-        bads = ats + (lane & 1) * 4 >= (uint32_t)P.sb ? kOutside : 0u;
+        bads = (lane & 1) * 64 >= leftp ? kOutside : 0u;  // 4 scale bytes stand for 64 of codes
         sdst = lds_address(sm.scale[0]) + stage * (SCALE_DW * 4) + (uint32_t)w * 256u;
       }
     };
@@ -316,17 +328,25 @@ struct Tile {
           enter();
         } else {
           np = nq = 0;
-          ahead.c = 0;
           ahead.c1 = 1 << 30;
+        }
+      } else {
+        pb += csp;
+        qb += csq;
+        leftp -= 128;
+        leftq -= 128;
+        if constexpr (kMx) {
+          psb += 8;
+          qsb += 8;
         }
       }
     };
     constexpr int LOADS = LP + LQ + (EL == EL_MX ? SJ : 0);
     auto load = [&](int i) __attribute__((always_inline)) {
       if (i < LP) {
-        load_lds16(dp, lr < np - i * RPI && gp(i) < leftp ? vp + gp(i) : kOutside, far_p(i), dst + i * (RPI * 128));
+        load_lds16(dp, lr < np - i * RPI && (int)gp(i) < leftp ? vp + gp(i) : kOutside, far_p(i), dst + i * (RPI * 128));
       } else if (i < LP + LQ) {
-        load_lds16(dq, lrq < nq - (i - LP) * RPI && gq(i - LP) < leftq ? vq + gq(i - LP) : kOutside, far_q(i - LP), dst + i * (RPI * 128));
+        load_lds16(dq, lrq < nq - (i - LP) * RPI && (int)gq(i - LP) < leftq ? vq + gq(i - LP) : kOutside, far_q(i - LP), dst + i * (RPI * 128));
       } else if constexpr (EL == EL_MX) {
         const int j = i - LP - LQ, r0 = w * 32 + j * (NT / 2);
         const bool isp = r0 < BM;
@@ -336,7 +356,7 @@ struct Tile {
         d.y = isp ? dsp.y : dsq.y;
         d.z = dsp.z;
         d.w = dsp.w;
-        load_lds4(d, (lane >> 1) < (isp ? np : nq) - first ? vs | bads : kOutside, (uint32_t)first * (uint32_t)P.lds,
+        load_lds4(d, (lane >> 1) < (isp ? np : nq) - first ? vs | bads : kOutside, (uint32_t)first * pitch_s,
                   sdst + j * (NT * 4));
       }
     };
@@ -345,9 +365,10 @@ struct Tile {
     // kept once: those of the next step are read into a tile's registers as soon
     // as its instructions have issued.  Q's, which every tile needs, twice.
     i32x4_t fp[TM], fq[2][TN];
-    // scale bytes of both steps, two tiles a register
+    // scale bytes of both steps, two tiles a register; as read (two bytes) they wait a
+    // while in rp, rq before they are paired, which would wait for the read
     constexpr int NSP = (TM + 1) / 2, NSQ = (TN + 1) / 2;
-    u16x2_t sp[NSP], sq[NSQ], sqn[NSQ];
+    uint32_t sp[NSP], sq[NSQ], rp[TM], rq[TN];
     const int pr0 = wm * TM * 16, qr0 = BM + wn * TN * 16;
     const int pk = p_key(p_row(0, n >> 2, n & 3)), qk = q_key(q_row(0, n));
     // LDS byte addresses; the two steps' pieces are neighbours, 16 bytes apart
@@ -364,10 +385,19 @@ struct Tile {
       fq[s][tn] = lds_read<i32x4_t>((((tn & 1 ? lq1 : lq0) ^ (s * 16)) + stage * kStage) + (tn & ~1) * 128);
     };
     auto read_sp = [&](uint32_t stage, int tm) __attribute__((always_inline)) {
-      if constexpr (EL == EL_MX) sp[tm / 2][tm % 2] = lds_read<uint16_t>(lsp + stage * (SCALE_DW * 4) + p_row(tm, 0, 0) * 8);
+      if constexpr (EL == EL_MX) rp[tm] = lds_read<uint16_t>(lsp + stage * (SCALE_DW * 4) + p_row(tm, 0, 0) * 8);
     };
     auto read_sq = [&](uint32_t stage, int tn) __attribute__((always_inline)) {
-      if constexpr (EL == EL_MX) sqn[tn / 2][tn % 2] = lds_read<uint16_t>(lsq + stage * (SCALE_DW * 4) + q_row(tn, 0) * 8);
+      if constexpr (EL == EL_MX) rq[tn] = lds_read<uint16_t>(lsq + stage * (SCALE_DW * 4) + q_row(tn, 0) * 8);
+    };
+    auto pair_sp = [&](int k) __attribute__((always_inline)) {
+      if constexpr (EL == EL_MX) sp[k] = 2 * k + 1 < TM ? rp[2 * k] | rp[2 * k + 1] << 16 : rp[2 * k];
+    };
+    auto pair_sq = [&]() __attribute__((always_inline)) {
+      if constexpr (EL == EL_MX) {
+#pragma unroll
+        for (int k = 0; k < NSQ; ++k) sq[k] = 2 * k + 1 < TN ? rq[2 * k] | rq[2 * k + 1] << 16 : rq[2 * k];
+      }
     };
     auto mma = [&](auto sc, auto tmc) __attribute__((always_inline)) {
       constexpr int s = decltype(sc)::value, tm = decltype(tmc)::value;
@@ -380,8 +410,7 @@ struct Tile {
           const i32x8_t a = __builtin_shufflevector(fp[tm], i32x4_t{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
           const i32x8_t b = __builtin_shufflevector(fq[s][tn], i32x4_t{0, 0, 0, 0}, 0, 1, 2, 3, 4, 5, 6, 7);
           acc[tm][tn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              a, b, acc[tm][tn], 4, 4, s + 2 * (tm % 2), __builtin_bit_cast(int, sp[tm / 2]), s + 2 * (tn % 2),
-              __builtin_bit_cast(int, sq[tn / 2]));
+              a, b, acc[tm][tn], 4, 4, s + 2 * (tm % 2), (int)sp[tm / 2], s + 2 * (tn % 2), (int)sq[tn / 2]);
         }
       });
     };
@@ -394,6 +423,8 @@ struct Tile {
     // longest, two are left for the next step (forward of 16384 x 50304 over 1024: 1483
     // us without, 1452 with; with four 1507; 128 x 128 tiles lose by it)
     constexpr int SLOTS = TM - LEAD + 1, LATE = TM >= 8 ? 2 : 0;
+    // the last pair of P's scales is made up in the next chunk, before its tiles
+    constexpr int LAZY = TM >= 8 ? 1 : 0;
     begin(0);
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) load(i);
@@ -418,10 +449,9 @@ struct Tile {
         read_p(st, 0, tm);
         read_sp(st, tm);
       }
-      if constexpr (EL == EL_MX) {
+      pair_sq();
 #pragma unroll
-        for (int k = 0; k < NSQ; ++k) sq[k] = sqn[k];
-      }
+      for (int k = 0; k < NSP - LAZY; ++k) pair_sp(k);
 #pragma nounroll
       for (; now.c < now.c1; ++now.c) {
 #pragma unroll
@@ -431,6 +461,7 @@ struct Tile {
           mma(S0{}, tmc);
           __builtin_amdgcn_sched_barrier(0);
           read_p(st, 1, tm);
+          if constexpr (LAZY && tm == TM - 4) pair_sp(NSP - 1);
 #pragma unroll
           for (int i = LOADS - LATE; i < LOADS; ++i)
             if ((i - (LOADS - LATE)) * TM / 2 == tm) load(i);
@@ -458,6 +489,7 @@ struct Tile {
             constexpr int from = tm == (LEAD - 1) / 2 * 2 + 1 || tm == LEAD - 1 ? 0 : tm / 2 * 2;
 #pragma unroll
             for (int k = from; k <= tm; ++k) read_sp(st ^ 1u, k);
+            if constexpr (from > 0) pair_sp(from / 2 - 1);
           }
           if constexpr (tm >= LEAD - 1) {
 #pragma unroll
@@ -465,10 +497,8 @@ struct Tile {
               if (i * SLOTS / (LOADS - LATE) == tm - (LEAD - 1)) load(i);
           }
         });
-        if constexpr (EL == EL_MX) {
-#pragma unroll
-          for (int k = 0; k < NSQ; ++k) sq[k] = sqn[k];
-        }
+        if constexpr (!LAZY) pair_sp(NSP - 1);
+        pair_sq();
         st ^= 1u;
       }
       epilogue((int64_t)now.tp * BM, (int64_t)now.tq * BN, now.z, acc);
