@@ -1079,6 +1079,17 @@ tj2_status check_out_dtype(int32_t dtype, const char* name) {
   return TJ2_OK;
 }
 
+// An operand of the backward's products, row-major or blocked: whole blocks of 128 rows
+// by 256 elements hold either.
+int64_t whole(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+size_t mx_carve_size(int64_t rows, int64_t len) { return carve_size(TJ2_MXFP4, whole(rows, 128), whole(len, 256)); }
+tj2_qtensor mx_carve(uint8_t*& cur, int64_t rows, int64_t len) {
+  tj2_qtensor q = carve(cur, TJ2_MXFP4, whole(rows, 128), whole(len, 256));
+  q.rows = rows;
+  q.len = len;
+  return q;
+}
+
 size_t mx_linear_bwd_gemm_ws(int64_t M, int64_t N, int64_t K) {
   return mx_gemm_pair_workspace_bytes(M, K, N, N, K, M);
 }
@@ -1153,8 +1164,8 @@ tj2_status mxfp4_linear_fwd(const void* X, int64_t M, int64_t K, int64_t N, cons
 
 size_t mxfp4_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  return carve_size(TJ2_MXFP4, M, N) + carve_size(TJ2_MXFP4, N, M) + carve_size(TJ2_MXFP4, K, N) +
-         carve_size(TJ2_MXFP4, K, M) + 256 + align256(mx_linear_bwd_gemm_ws(M, N, K));
+  return mx_carve_size(M, N) + mx_carve_size(N, M) + mx_carve_size(K, N) + mx_carve_size(K, M) + 256 +
+         align256(mx_linear_bwd_gemm_ws(M, N, K));
 }
 
 tj2_status mxfp4_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, const tj2_qtensor* Xq, const tj2_qtensor* Wq,
@@ -1172,20 +1183,20 @@ tj2_status mxfp4_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, con
   if (!aligned16(dY) || !aligned16(dX) || !aligned16(dW)) return fail(TJ2_ERR_ALIGN, "dY, dX and dW must be 16-byte aligned");
   TJ2_TRY(check_mx_workspace(workspace, ws_bytes, mxfp4_linear_bwd_workspace_size(M, N, K)));
   uint8_t* cur = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~(uintptr_t)255);
-  const tj2_qtensor dYq = carve(cur, TJ2_MXFP4, M, N), dYt = carve(cur, TJ2_MXFP4, N, M), Wt = carve(cur, TJ2_MXFP4, K, N),
-                    Xt = carve(cur, TJ2_MXFP4, K, M);
+  const tj2_qtensor dYq = mx_carve(cur, M, N), dYt = mx_carve(cur, N, M), Wt = mx_carve(cur, K, N), Xt = mx_carve(cur, K, M);
   TJ2_TRY(check_mx(&dYq, "dYq", M, N));
   TJ2_TRY(check_mx(&dYt, "dYt", N, M));
   TJ2_TRY(check_mx(&Wt, "Wt", K, N));
   TJ2_TRY(check_mx(&Xt, "Xt", K, M));
   const uint32_t sx = rht ? tj2_rht_signs(seed, offset) : 0, sw = rht ? tj2_rht_signs(seed, offset + 2) : 0;
   const int row = TJ2_GROUP_ROW, col = TJ2_GROUP_COL;
-  TJ2_TRY(hip_check(launch_mx_backward_operands(
-                        mx_quant_params(dY, TJ2_BF16, nullptr, M, N, row, rounding, rht, sx, seed, offset, &dYq),
-                        mx_quant_params(dY, TJ2_BF16, nullptr, M, N, col, rounding, rht, sw, seed, offset + 2, &dYt),
-                        mx_quant_params(nullptr, TJ2_MXFP4, Wq, N, K, col, rounding, rht, sx, seed, offset + 1, &Wt),
-                        mx_quant_params(nullptr, TJ2_MXFP4, Xq, M, K, col, rounding, rht, sw, seed, offset + 3, &Xt), s),
-                    "MXFP4 quantize launch"));
+  MxQuantParams dy_row = mx_quant_params(dY, TJ2_BF16, nullptr, M, N, row, rounding, rht, sx, seed, offset, &dYq),
+                dy_col = mx_quant_params(dY, TJ2_BF16, nullptr, M, N, col, rounding, rht, sw, seed, offset + 2, &dYt),
+                w = mx_quant_params(nullptr, TJ2_MXFP4, Wq, N, K, col, rounding, rht, sx, seed, offset + 1, &Wt),
+                x = mx_quant_params(nullptr, TJ2_MXFP4, Xq, M, K, col, rounding, rht, sw, seed, offset + 3, &Xt);
+  dy_row.blocked = w.blocked = mx_blocked(M, N);
+  dy_col.blocked = x.blocked = mx_blocked(N, M);
+  TJ2_TRY(hip_check(launch_mx_backward_operands(dy_row, dy_col, w, x, s), "MXFP4 quantize launch"));
   TJ2_TRY(hip_check(launch_mx_gemm_pair(make_view(dYq), make_view(Wt), dX, dx_dtype, make_view(dYt), make_view(Xt), dW, TJ2_F32,
                                         reinterpret_cast<float*>(cur), s),
                     "MXFP4 gemm launch"));

@@ -132,12 +132,29 @@ __global__ __launch_bounds__(256) void mx_row_pair_kernel(MxRowArgs x, MxRowArgs
   else mx_row<float, false, false>(w, blockIdx.x - nx);
 }
 
+// Where an operand's groups go: row r's block of 128 elements b has its 64 bytes of
+// codes at at(r, b) and its 4 scale bytes at a sixteenth of that.  Row-major, or (what
+// only the backward's own products read) blocked as TileOp says: with rows a power of
+// two apart a product's loads meet in few channels of the L2 (4096 x 4096 over 16384:
+// 158 us, and 144 at a pitch of 33 lines; backward of 4096 x 4096 over 1024 61.2 us
+// row-major, 59.6 blocked).
+struct MxOut {
+  uint8_t *codes, *scale;
+  int64_t ld, bs, cs;
+  __device__ __forceinline__ int64_t at(int64_t row, uint32_t block) const {
+    return (row >> 7) * bs + (row & 127) * ld + (int64_t)(block >> 1) * cs + (block & 1) * 64;
+  }
+};
+MxOut mx_out(const QView& q, bool blocked) {
+  if (blocked) return MxOut{q.codes, q.s16, 128, (q.nb + 1) / 2 * 16384, 16384};
+  return MxOut{q.codes, q.s16, q.nb * 64, q.nb * 64 * 128, 128};
+}
+
 struct MxColArgs {
   const void* x;       // dense [rows, cols], or codes of an MXFP4 operand [rows, cols]
   const uint8_t* xs;   // its scale bytes
   int64_t ldx, lds;    // codes and scale bytes per row of it
-  uint8_t* codes;      // [cols][nb * 64]
-  uint8_t* scale;      // [cols][nb * 4]
+  MxOut out;           // [cols, rows]
   int32_t rows, cols, nb;
   uint32_t mask;
   uint64_t seed, offset;
@@ -217,10 +234,10 @@ __device__ __forceinline__ void mx_col(const MxColArgs& p, uint32_t bx, uint32_t
   const uint2 b = mx_codes16<SR>(v + 16, byte, block + 2, p.seed, p.offset);
   sb[c][rg] = (uint8_t)byte;
   if (col < p.cols)
-    *reinterpret_cast<uint4*>(p.codes + (col * p.nb + by) * 64 + rg * 16) = uint4{a.x, a.y, b.x, b.y};
+    *reinterpret_cast<uint4*>(p.out.codes + p.out.at(col, by) + rg * 16) = uint4{a.x, a.y, b.x, b.y};
   __syncthreads();
   if (t < 64 && c0 + t < p.cols)
-    *reinterpret_cast<uint32_t*>(p.scale + ((int64_t)(c0 + t) * p.nb + by) * 4) = *reinterpret_cast<const uint32_t*>(sb[t]);
+    *reinterpret_cast<uint32_t*>(p.out.scale + p.out.at(c0 + t, by) / 16) = *reinterpret_cast<const uint32_t*>(sb[t]);
 }
 template <class T, bool SR, bool RHT>
 __global__ __launch_bounds__(256) void mx_col_kernel(MxColArgs p) {
@@ -239,8 +256,7 @@ __global__ __launch_bounds__(256) void mx_col_kernel(MxColArgs p) {
 // elements, then bound it.)
 struct MxDualArgs {
   const uint16_t* x;       // [rows, cols]
-  uint8_t *row_codes, *row_scale;  // [rows][nbc * 64], [rows][nbc * 4]
-  uint8_t *col_codes, *col_scale;  // [cols][nbr * 64], [cols][nbr * 4]
+  MxOut row, col;          // [rows, cols] and [cols, rows]
   int32_t rows, cols, nbr, nbc;    // 128-element blocks of a column and of a row
   uint32_t row_mask, col_mask;
   uint64_t seed, row_offset, col_offset;
@@ -278,9 +294,9 @@ __device__ __forceinline__ void mx_dual(const MxDualArgs& p, uint32_t bx, uint32
     const int64_t row = r0 + r;
     const uint2 q = mx_codes16<SR>(v, byte, (uint64_t)(row * padded_c + c) >> 3, p.seed, p.row_offset);
     if (row < p.rows) {
-      const int64_t at = (row * p.nbc + bx) * 8 + h;
-      *reinterpret_cast<uint2*>(p.row_codes + at * 8) = c < p.cols ? q : uint2{0u, 0u};
-      if (!(h & 1)) p.row_scale[at >> 1] = (uint8_t)byte;
+      const int64_t at = p.row.at(row, bx) + h * 8;
+      *reinterpret_cast<uint2*>(p.row.codes + at) = c < p.cols ? q : uint2{0u, 0u};
+      if (!(h & 1)) p.row.scale[at / 16] = (uint8_t)byte;
     }
   }
   __syncthreads();
@@ -307,11 +323,11 @@ __device__ __forceinline__ void mx_dual(const MxDualArgs& p, uint32_t bx, uint32
     const uint2 b = mx_codes16<SR>(v + 16, byte, block + 2, p.seed, p.col_offset);
     sb[cc + i][rg] = (uint8_t)byte;
     if (col < p.cols)
-      *reinterpret_cast<uint4*>(p.col_codes + (col * p.nbr + by) * 64 + rg * 16) = uint4{a.x, a.y, b.x, b.y};
+      *reinterpret_cast<uint4*>(p.col.codes + p.col.at(col, by) + rg * 16) = uint4{a.x, a.y, b.x, b.y};
   }
   __syncthreads();
   if (t < 128 && c0 + t < p.cols)
-    *reinterpret_cast<uint32_t*>(p.col_scale + ((int64_t)(c0 + t) * p.nbr + by) * 4) = *reinterpret_cast<const uint32_t*>(sb[t]);
+    *reinterpret_cast<uint32_t*>(p.col.scale + p.col.at(c0 + t, by) / 16) = *reinterpret_cast<const uint32_t*>(sb[t]);
 }
 
 // All operands of the backward pass in one launch: nd workgroups for dY, the others for
@@ -489,11 +505,11 @@ __global__ __launch_bounds__(S::NT, 2) void mx_few_kernel(MxFewArgs a) {
       if (h * 16 >= a.cols) q = uint2{0u, 0u};
       if (blockIdx.x == 0 && t < I && h * 8 < p.P.kb) {
         *reinterpret_cast<uint2*>(a.codes + (int64_t)t * p.P.kb + h * 8) = q;
-        if (!(h & 1)) a.scale[(int64_t)t * p.P.sb + h / 2] = (uint8_t)byte;
+        if (!(h & 1)) a.scale[(int64_t)t * (p.P.kb / 16) + h / 2] = (uint8_t)byte;
       }
     } else if (t < I && h * 8 < p.P.kb) {
       q = *reinterpret_cast<const uint2*>(p.Q.p + (int64_t)t * p.P.kb + h * 8);
-      byte = p.Q.s[(int64_t)t * p.P.sb + h / 2];
+      byte = p.Q.s[(int64_t)t * (p.P.kb / 16) + h / 2];
     }
     *reinterpret_cast<uint2*>(sm.x + t * px + h * 8) = q;
     if (!(h & 1)) sm.xs[t * ps + h / 2] = (uint8_t)byte;
@@ -549,17 +565,16 @@ void launch_tile(const MxGemmArgs& a, const MxGemmArgs* second, hipStream_t s) {
   mx_gemm_kernel<T><<<jobs.first + others, T::NT, 0, s>>>(jobs);
 }
 
-TileOp mx_operand(const QView& q) {
+TileOp mx_operand(const QView& q, bool blocked) {
   TileOp o = {};
   o.p = q.codes;
   o.s = q.s16;
   o.rows = q.rows;
-  o.ld = q.nb * 64;
-  o.bs = 128 * o.ld;
-  o.cs = 128;
-  o.lds = q.nb * 4;
+  const MxOut at = mx_out(q, blocked);
+  o.ld = at.ld;
+  o.bs = at.bs;
+  o.cs = (int32_t)at.cs;
   o.kb = (int32_t)(q.nb * 64);
-  o.sb = (int32_t)(q.nb * 4);
   return o;
 }
 
@@ -608,6 +623,8 @@ MxPlan mx_plan(int64_t I, int64_t J, int64_t K) {
 
 bool mx_is_few(int64_t M, int64_t K) { return Few::fits(M, (K + 127) / 128 * 64); }
 
+bool mx_blocked(int64_t I, int64_t K) { return !mx_is_few(I, K); }
+
 size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K) {
   if (mx_is_few(I, K)) return 0;
   const int z = mx_plan(I, J, K).splits;
@@ -629,10 +646,10 @@ hipError_t launch_few(const MxGemmArgs& a, const void* x, int64_t cols, const QV
   return hipGetLastError();
 }
 
-MxGemmArgs mx_gemm_args(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate) {
+MxGemmArgs mx_gemm_args(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, bool blocked = false) {
   MxGemmArgs a = {};
-  a.P = mx_operand(B);
-  a.Q = mx_operand(A);
+  a.P = mx_operand(B, blocked);
+  a.Q = mx_operand(A, blocked);
   a.C = C;
   a.ldc = ldc;
   a.nch = (int32_t)((A.nb + 1) / 2);
@@ -712,7 +729,8 @@ size_t mx_gemm_pair_workspace_bytes(int64_t I, int64_t J, int64_t K, int64_t I2,
 
 hipError_t launch_mx_gemm_pair(const QView& A, const QView& B, void* C, int c_dtype, const QView& A2, const QView& B2, void* C2,
                                int c2_dtype, float* partial, hipStream_t s) {
-  const MxGemmArgs a[2] = {mx_gemm_args(A, B, C, c_dtype, B.rows, 0), mx_gemm_args(A2, B2, C2, c2_dtype, B2.rows, 0)};
+  const MxGemmArgs a[2] = {mx_gemm_args(A, B, C, c_dtype, B.rows, 0, mx_blocked(A.rows, A.len)),
+                           mx_gemm_args(A2, B2, C2, c2_dtype, B2.rows, 0, mx_blocked(A2.rows, A2.len))};
   const size_t first = (mx_gemm_workspace_bytes(A.rows, B.rows, A.len) + 255) / 256 * 256;
   float* room[2] = {partial, partial + first / 4};
   const int64_t K[2] = {A.len, A2.len};
@@ -791,8 +809,7 @@ MxColArgs col_args(const MxQuantParams& q) {
     a.ldx = q.xq.nb * 64;
     a.lds = q.xq.nb * 4;
   }
-  a.codes = q.out.codes;
-  a.scale = q.out.s16;
+  a.out = mx_out(q.out, q.blocked);
   a.rows = (int32_t)q.rows;
   a.cols = (int32_t)q.cols;
   a.nb = (int32_t)q.out.nb;
@@ -827,10 +844,8 @@ hipError_t launch_mx_backward_operands(const MxQuantParams& dy_row, const MxQuan
                                        const MxQuantParams& x, hipStream_t s) {
   MxDualArgs d = {};
   d.x = reinterpret_cast<const uint16_t*>(dy_row.x);
-  d.row_codes = dy_row.out.codes;
-  d.row_scale = dy_row.out.s16;
-  d.col_codes = dy_col.out.codes;
-  d.col_scale = dy_col.out.s16;
+  d.row = mx_out(dy_row.out, dy_row.blocked);
+  d.col = mx_out(dy_col.out, dy_col.blocked);
   d.rows = (int32_t)dy_row.rows;
   d.cols = (int32_t)dy_row.cols;
   d.nbr = (int32_t)dy_col.out.nb;

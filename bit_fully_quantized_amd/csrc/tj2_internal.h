@@ -171,6 +171,7 @@ struct MxQuantParams {
   uint32_t rht_mask;
   uint64_t seed, offset;
   QView out;
+  bool blocked;  // out in blocks of 128 rows by 256 elements (the backward's operands)
 };
 hipError_t launch_mx_quant(const MxQuantParams& q, hipStream_t s);
 // The linear layer's operands in one launch each: X (bf16) and W (fp32) along their
@@ -183,7 +184,9 @@ hipError_t launch_mx_values(const QView& q, void* out, int dtype, hipStream_t s)
 size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K);
 hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
                           hipStream_t s);
-// C = A B^T and C2 = A2 B2^T together, `partial` of mx_gemm_pair_workspace_bytes.
+// C = A B^T and C2 = A2 B2^T together, `partial` of mx_gemm_pair_workspace_bytes; the
+// operands of a product are blocked where mx_blocked(its rows, its reduction).
+bool mx_blocked(int64_t I, int64_t K);
 size_t mx_gemm_pair_workspace_bytes(int64_t I, int64_t J, int64_t K, int64_t I2, int64_t J2, int64_t K2);
 hipError_t launch_mx_gemm_pair(const QView& A, const QView& B, void* C, int c_dtype, const QView& A2, const QView& B2, void* C2,
                                int c2_dtype, float* partial, hipStream_t s);

@@ -71,11 +71,11 @@ struct Skinny {
                           d, in && at + h * 16 < (uint32_t)P.kb ? row + at + h * 16 : kOutside, 0, 0));
       }
       if constexpr (EL == EL_MX) {
-        const auto ds = __builtin_amdgcn_make_buffer_rsrc((void*)(P.s + r0 * P.lds), 0, 0x7FFFFFFF, 0x00020000);
+        const auto ds = __builtin_amdgcn_make_buffer_rsrc((void*)(P.s + r0 * P.ld / 16), 0, 0x7FFFFFFF, 0x00020000);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const uint32_t at = (uint32_t)(b * U + u) * 8u + (uint32_t)g * 2u;
-          f.s[u] = __builtin_amdgcn_raw_buffer_load_b16(ds, in && at < (uint32_t)P.sb ? (uint32_t)n * (uint32_t)P.lds + at : kOutside, 0, 0);
+          f.s[u] = __builtin_amdgcn_raw_buffer_load_b16(ds, in && at < (uint32_t)P.kb / 16 ? (uint32_t)n * (uint32_t)(P.ld / 16) + at : kOutside, 0, 0);
         }
       }
     };

@@ -58,13 +58,13 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 //   blocked:    ld 128, cs the 16 KB of 128 rows' chunk, bs all chunks of 128 rows,
 // the latter for operands that a pass of this library writes: a chunk of a tile is
 // contiguous, where a long pitch spreads its rows over as many pages and, if it is a
-// power of two, over few memory channels.  MXFP4: `sb` scale bytes (a multiple of 4)
-// per row at a pitch of `lds` bytes, the same for both operands.
+// power of two, over few memory channels.  MXFP4: the scale bytes, one for 16 of codes,
+// lie as the codes do.
 struct TileOp {
   const uint8_t* p;
   const uint8_t* s;
-  int64_t rows, ld, bs, lds;
-  int32_t kb, sb, cs;
+  int64_t rows, ld, bs;
+  int32_t kb, cs;
 };
 
 constexpr uint32_t kOutside = 0x80000000u;  // lane offset beyond every buffer below
@@ -258,13 +258,12 @@ struct Tile {
     // byte in the row of what it fetches for row i * RPI + lr
     auto gp = [&](int i) __attribute__((always_inline)) { return (uint32_t)((t & 7) ^ p_key(lr) ^ p_key(i * RPI)) * 16u; };
     auto gq = [&](int i) __attribute__((always_inline)) { return (uint32_t)((t & 7) ^ q_key(lr) ^ q_key(i * RPI)) * 16u; };
-    // (MXFP4 operands are row-major with one pitch, all of it codes)
+    // (MXFP4 operands of a product have one layout, and their scales the same in 1/16)
     constexpr bool kMx = EL == EL_MX;
     const uint32_t ldp = pinned((uint32_t)P.ld), ldq = kMx ? ldp : pinned((uint32_t)Q.ld);
-    const uint32_t bsp = kMx ? 128 * ldp : pinned((uint32_t)P.bs), bsq = kMx ? bsp : pinned((uint32_t)Q.bs);
-    const uint32_t csp = kMx ? 128 : pinned((uint32_t)P.cs), csq = kMx ? 128 : pinned((uint32_t)Q.cs);
-    const int kbp = kMx ? (int)ldp : (int)pinned((uint32_t)P.kb), kbq = kMx ? kbp : (int)pinned((uint32_t)Q.kb);
-    const uint32_t pitch_s = ldp / 16;  // scale bytes a row
+    const uint32_t bsp = pinned((uint32_t)P.bs), bsq = kMx ? bsp : pinned((uint32_t)Q.bs);
+    const uint32_t csp = pinned((uint32_t)P.cs), csq = kMx ? csp : pinned((uint32_t)Q.cs);
+    const int kbp = (int)pinned((uint32_t)P.kb), kbq = kMx ? kbp : (int)pinned((uint32_t)Q.kb);
     const uint32_t vp = (uint32_t)lr * ldp, vq = (uint32_t)lrq * ldq;
     // and the uniform offset of its row i * RPI
     static_assert(128 % RPI == 0 && (BM < 128 || BM % 128 == 0) && (BN < 128 || BN % 128 == 0), "rows of a block");
@@ -281,7 +280,7 @@ struct Tile {
     // of Q: BM is a multiple of 32)
     constexpr int SJ = EL == EL_MX ? SCALE_DW / NT : 1;
     static_assert(SCALE_DW % NT == 0 && BM % 32 == 0, "whole scale loads");
-    const uint32_t vs = (uint32_t)(lane >> 1) * pitch_s + (lane & 1) * 4;
+    const uint32_t vs = (uint32_t)(lane >> 1) * (ldp / 16) + (lane & 1) * 4;
 
     // The load cursor: its item, the item's rows (none once the items are done), where
     // its chunk starts and the bytes of a row from there on.
@@ -296,8 +295,8 @@ struct Tile {
       leftp = kbp - ahead.c * 128;
       leftq = kbq - ahead.c * 128;
       if constexpr (EL == EL_MX) {
-        psb = P.s + p0 * P.lds + ahead.c * 8;
-        qsb = Q.s + q0 * Q.lds + ahead.c * 8;
+        psb = P.s + ((p0 >> 7) * P.bs + (p0 & 127) * P.ld + mul32(ahead.c, csp)) / 16;
+        qsb = Q.s + ((q0 >> 7) * Q.bs + (q0 & 127) * Q.ld + mul32(ahead.c, csq)) / 16;
       }
       np = __builtin_amdgcn_readfirstlane((int)min(P.rows - p0, (int64_t)BM));
       nq = __builtin_amdgcn_readfirstlane((int)min(Q.rows - q0, (int64_t)BN));
@@ -336,8 +335,8 @@ struct Tile {
         leftp -= 128;
         leftq -= 128;
         if constexpr (kMx) {
-          psb += 8;
-          qsb += 8;
+          psb += csp / 16;
+          qsb += csq / 16;
         }
       }
     };
@@ -356,7 +355,7 @@ struct Tile {
         d.y = isp ? dsp.y : dsq.y;
         d.z = dsp.z;
         d.w = dsp.w;
-        load_lds4(d, (lane >> 1) < (isp ? np : nq) - first ? vs | bads : kOutside, (uint32_t)first * pitch_s,
+        load_lds4(d, (lane >> 1) < (isp ? np : nq) - first ? vs | bads : kOutside, (uint32_t)(first >> 7) * (bsp / 16) + (uint32_t)(first & 127) * (ldp / 16),
                   sdst + j * (NT * 4));
       }
     };
