@@ -958,6 +958,9 @@ __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distil
   __shared__ float sh_max[WAVES][2], sh_sum[WAVES][4];
   __shared__ __attribute__((aligned(16))) int32_t id[kDistillMaxK];
   __shared__ float pr[kDistillMaxK];
+  // what the few entries' threads keep meanwhile: in registers it would be spilled
+  __shared__ float keep_u[kDistillMaxK], keep_z[kDistillMaxK], keep_edge[16], keep_target;
+  __shared__ uint8_t keep_flags[kDistillMaxK];  // 1: the first place that lists its entry, 2: not the only one
   __shared__ int32_t named;  // the hard target is among the teacher's entries
   const int t = threadIdx.x;
   const int64_t row = blockIdx.x;
@@ -998,9 +1001,14 @@ __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distil
   // f(r, i) for each of this thread's vectors i
   auto each = [&](auto&& f) __attribute__((always_inline)) {
     if constexpr (R > 0) {
+      // the places are worked out again in each pass: kept from the loads to the stores
+      // they would be spilled (16384 rows of 50304 bf16: 0.3 GB beside the 3.3 GB of
+      // logits, 684 us and 628 without)
+      int at = t;
+      asm volatile("" : "+v"(at));
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int i = t + r * kThreads;
+        const int i = at + r * kThreads;
         if (i < nv) f(r, i);
         // one vector at a time: interleaved, their temporaries would take the
         // registers that let another row share the CU
@@ -1018,39 +1026,49 @@ __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distil
     }
   }
   const float ze = edge ? to_f32<T>(z[ei]) : 0.0f;
+  if (edge) keep_edge[t] = ze;
   // read before anything is written: dz may be z
-  float zy = 0.0f;
-  if constexpr (HARD) zy = (uint64_t)y < (uint64_t)V ? to_f32<T>(z[y]) : kNan;
+  if (HARD && t == 0) {
+    keep_target = (uint64_t)y < (uint64_t)V ? to_f32<T>(z[y]) : kNan;
+    named = 0;
+  }
 
   // the teacher's probabilities: softmax of its kept logits over tau
   const bool has_k = t < p.k;
-  int32_t my = -1;
-  float u = -INFINITY, zm = 0.0f;
-  if (has_k) {
-    my = p.ids[row * p.k + t];
-    if (my >= 0 && my < V) {
-      u = to_f32<T>(reinterpret_cast<const T*>(p.u)[row * p.k + t]) / p.tau;
-      zm = to_f32<T>(z[my]);
+  float u = -INFINITY;
+  if (t < ((p.k + 3) & ~3)) {
+    int32_t my = -1;
+    if (has_k) {
+      my = p.ids[row * p.k + t];
+      float zm = 0.0f;
+      if (my >= 0 && my < V) {
+        u = to_f32<T>(reinterpret_cast<const T*>(p.u)[row * p.k + t]) / p.tau;
+        zm = to_f32<T>(z[my]);
+      }
+      keep_u[t] = u;
+      keep_z[t] = zm;
     }
+    id[t] = my;
   }
-  if (t < ((p.k + 3) & ~3)) id[t] = my;
-  if (HARD && t == 0) named = 0;
   __syncthreads();
   // an entry that is listed twice is written once, by its first place
-  bool first = true, again = false;
-  if (has_k && my >= 0 && my < V) {
-    for (int j = 0; j < p.k; j += 4) {
-      const int4 o = *reinterpret_cast<const int4*>(id + j);
-      const int same = (o.x == my) | (o.y == my) << 1 | (o.z == my) << 2 | (o.w == my) << 3;
-      if (j <= t) {
-        const int before = t - j < 4 ? same & ((1 << (t - j)) - 1) : same;
-        first &= before == 0;
+  if (has_k) {
+    const int32_t my = id[t];
+    bool first = my >= 0 && my < V, again = false;
+    if (first) {
+      for (int j = 0; j < p.k; j += 4) {
+        const int4 o = *reinterpret_cast<const int4*>(id + j);
+        const int same = (o.x == my) | (o.y == my) << 1 | (o.z == my) << 2 | (o.w == my) << 3;
+        if (j <= t) {
+          const int before = t - j < 4 ? same & ((1 << (t - j)) - 1) : same;
+          first &= before == 0;
+        }
+        again |= (t - j >= 0 && t - j < 4 ? same & ~(1 << (t - j)) : same) != 0;
       }
-      again |= (t - j >= 0 && t - j < 4 ? same & ~(1 << (t - j)) : same) != 0;
+      if (HARD && my == y) named = 1;
     }
-    if (HARD && my == y) named = 1;
+    keep_flags[t] = (uint8_t)(first | again << 1);
   }
-  const bool kept = has_k && my >= 0;
   float m = edge ? ze : -INFINITY;
   each([&](int r, int i) __attribute__((always_inline)) {
     float v[N];
@@ -1080,17 +1098,24 @@ __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distil
       if constexpr (HARD) sum[1] += exp_scaled(v[k], m, kLog2e);
     }
   });
-  const float eu = kept && some ? __builtin_amdgcn_exp2f((u - mu) * kLog2e) : 0.0f;
-  sum[2] = eu;
-  if (eu > 0.0f || eu != eu) sum[3] = eu * ((u - mu) - (zm - m) / p.tau);
-  if (kept && my >= V) sum[3] = kNan;  // an id outside the vocabulary makes the row NaN
+  if (has_k) {
+    const int32_t my = id[t];
+    const float ku = keep_u[t];
+    float eu = 0.0f;
+    if (my >= 0 && some) {
+      eu = __builtin_amdgcn_exp2f((ku - mu) * kLog2e);
+      if (eu > 0.0f || eu != eu) sum[3] = eu * ((ku - mu) - (keep_z[t] - m) / p.tau);
+    }
+    sum[2] = eu;
+    pr[t] = eu;
+    if (my >= V) sum[3] = kNan;  // an id outside the vocabulary makes the row NaN
+  }
   block_reduce<WAVES>(sum, sh_sum, SumOp{});
   const float st = sum[0], s1 = sum[1], su = sum[2];
-  const float pt = some ? eu / su : 0.0f;
   // sum p (log p - log q) = sum p ((u - mu) - (z - m) / tau) - log su + log st
   const float kl = some ? sum[3] / su + (__builtin_amdgcn_logf(st) - __builtin_amdgcn_logf(su)) * kLn2 : sum[3];
   float loss = p.alpha > 0.0f ? p.alpha * p.tau * p.tau * kl : 0.0f;
-  if constexpr (HARD) loss += (1.0f - p.alpha) * (m + __builtin_amdgcn_logf(s1) * kLn2 - zy);
+  if constexpr (HARD) loss += (1.0f - p.alpha) * (m + __builtin_amdgcn_logf(s1) * kLn2 - keep_target);
   if (t == 0 && p.loss) p.loss[row] = loss;
   if (!dz) return;
 
@@ -1104,7 +1129,6 @@ __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distil
     if constexpr (HARD) g = fmaf(g1, exp_scaled(v, m, kLog2e), g);
     return g;
   };
-  if (has_k) pr[t] = pt;
   each([&](int r, int i) __attribute__((always_inline)) {
     float v[N];
     Vec<T>::get(vec(r, i), v);
@@ -1117,24 +1141,23 @@ __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distil
       for (int k = 0; k < N; ++k) dz[head + i * N + k] = from_f32<T>(v[k]);
     }
   });
-  if (edge) dz[ei] = from_f32<T>(grad(ze));
+  if (edge) dz[ei] = from_f32<T>(grad(keep_edge[t]));
   // the row is written before its few other entries are: by waves of their own, so the
   // stores themselves are waited for
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (has_k && my >= 0 && my < V && first) {
-    float mass = pt;
-    if (again) {
-      mass = 0.0f;
-      for (int j = t; j < p.k; ++j)
-        if (id[j] == my) mass += pr[j];
-    }
-    float g = grad(zm) - at * mass;
+  if (has_k && (keep_flags[t] & 1)) {
+    const int32_t my = id[t];
+    float mass = some ? pr[t] / su : 0.0f;
+    if (keep_flags[t] & 2)
+      for (int j = t + 1; j < p.k; ++j)
+        if (id[j] == my) mass += some ? pr[j] / su : 0.0f;
+    float g = grad(keep_z[t]) - at * mass;
     if (HARD && my == y) g -= a1;
     dz[my] = from_f32<T>(g);
   }
   if constexpr (HARD) {
-    if (t == 0 && (uint64_t)y < (uint64_t)V && !named) dz[y] = from_f32<T>(grad(zy) - a1);
+    if (t == 0 && (uint64_t)y < (uint64_t)V && !named) dz[y] = from_f32<T>(grad(keep_target) - a1);
   }
 }
 
