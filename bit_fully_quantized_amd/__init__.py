@@ -83,10 +83,27 @@ class QTensor:
         self.fmt, self.rows, self.len = fmt, rows, length
         nb = (length + 127) // 128
         self.nb = nb
-        self.codes = torch.empty((rows, nb * (64 if fmt in (NVFP4, MXFP4) else 128)), dtype=torch.uint8, device=device)
-        self.scale16 = (torch.empty((rows, nb * (4 if fmt == MXFP4 else 8)), dtype=torch.uint8, device=device)
-                        if fmt != FP8 else None)
-        self.scale128 = torch.empty((rows, nb), dtype=torch.float32, device=device) if fmt != MXFP4 else None
+        if fmt == MXFP4:  # one allocation, the arrays are views of it made when they are asked for
+            self.buffer = torch.empty(rows * nb * 68, dtype=torch.uint8, device=device)
+            self.scale128 = None
+            return
+        self.codes = torch.empty((rows, nb * (64 if fmt == NVFP4 else 128)), dtype=torch.uint8, device=device)
+        self.scale16 = torch.empty((rows, nb * 8), dtype=torch.uint8, device=device) if fmt != FP8 else None
+        self.scale128 = torch.empty((rows, nb), dtype=torch.float32, device=device)
+
+    buffer = None
+
+    def __getattr__(self, name):
+        if self.buffer is None or name not in ("codes", "scale16"):
+            raise AttributeError(name)
+        n = self.rows * self.nb
+        for key, t in zip(("codes", "scale16"), self.buffer.split((n * 64, n * 4))):
+            self.__dict__.setdefault(key, t.view(self.rows, -1))
+        return self.__dict__[name]
+
+    def storage(self) -> torch.Tensor:
+        """The tensor the operand starts in: its one allocation as long as the arrays were not asked for."""
+        return self.__dict__.get("codes", self.buffer)
 
     @staticmethod
     def wrap(fmt: int, rows: int, length: int, codes: torch.Tensor, scale16: torch.Tensor | None,
@@ -108,6 +125,9 @@ class QTensor:
         return q
 
     def c(self) -> _lib.QTensorC:
+        if "codes" not in self.__dict__:
+            at = self.buffer.data_ptr()
+            return _lib.QTensorC(at, at + self.rows * self.nb * 64, 0, self.rows, self.len, self.fmt, 0)
         return _lib.QTensorC(self.codes.data_ptr(), 0 if self.scale16 is None else self.scale16.data_ptr(),
                              0 if self.scale128 is None else self.scale128.data_ptr(), self.rows, self.len, self.fmt, 0)
 

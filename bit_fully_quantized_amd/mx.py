@@ -21,6 +21,7 @@ _OUT = (torch.bfloat16, torch.float32)
 _U8 = (torch.uint8,)
 _CODE = {torch.bfloat16: BF16, torch.float32: F32}
 _byref = ctypes.byref
+_FN: dict = {}  # entry points by name
 _device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -52,14 +53,15 @@ def _q(q, name: str, index: int, rows: int | None = None, length: int | None = N
         raise ValueError(f"{name} must be an MXFP4 QTensor")
     if (rows is not None and q.rows != rows) or (length is not None and q.len != length):
         raise ValueError(f"{name} is [{q.rows}, {q.len}], expected [{rows}, {length}]")
-    if q.codes.get_device() != index or q.scale16.get_device() != index:
+    t = q.storage()
+    if t.get_device() != index or (t is not q.buffer and q.scale16.get_device() != index):
         raise ValueError(f"{name} must be on cuda:{index}, with the other arguments")
     return _byref(q.c())
 
 
 def _run(name: str, index: int, *args) -> None:
     """Entry point `name` on the current stream of device `index`, made current for the call if it is not."""
-    fn = getattr(lib(), name)
+    fn = _FN.get(name) or _FN.setdefault(name, getattr(lib(), name))
     if _device() == index:
         status = fn(*args, _raw_stream(index))
     else:
@@ -86,7 +88,7 @@ def mx_quantize(x, *, grouping: int = GROUP_ROW, rounding: int = RTN, rht: bool 
     scale 2^(floor(log2 amax) - 2); SR the smallest one that saturates nothing, with Philox draws of
     (seed, offset).  rht applies the 16-wide Hadamard transform with the sign mask `signs` first."""
     if isinstance(x, QTensor):
-        index = _tensor(x.codes, "x")
+        index = _tensor(x.storage(), "x")
         rows, cols, xp, xd, xq = x.rows, x.len, 0, MXFP4, _q(x, "x", index)
     else:
         index = _tensor(x, "x", 2)
@@ -105,7 +107,7 @@ def mx_dequantize(q: QTensor, *, dtype=torch.bfloat16, out: torch.Tensor | None 
     """The values of an MXFP4 QTensor as a dense [rows, len] tensor (bf16 holds them exactly)."""
     if not isinstance(q, QTensor):
         raise ValueError("q must be an MXFP4 QTensor")
-    index = _tensor(q.codes, "q")
+    index = _tensor(q.storage(), "q")
     desc = _q(q, "q", index)
     if out is None:
         out = torch.empty((q.rows, q.len), dtype=dtype, device=index)
@@ -135,7 +137,7 @@ def mx_gemm(A: QTensor, B: QTensor, *, out: torch.Tensor | None = None, out_dtyp
     """C = A B^T (accumulate: added into a float32 `out`) on MXFP4 operands grouped along the reduction."""
     if not isinstance(A, QTensor) or not isinstance(B, QTensor):
         raise ValueError("A and B must be MXFP4 QTensors")
-    index = _tensor(A.codes, "A")
+    index = _tensor(A.storage(), "A")
     a, b = _q(A, "A", index), _q(B, "B", index, B.rows, A.len)
     if out is None:
         if accumulate:

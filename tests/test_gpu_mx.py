@@ -278,6 +278,23 @@ def test_backward_graphs_share_a_workspace():
         assert all(torch.equal(a, b) for a, b in zip(other, want[1 - k]))
 
 
+def test_operand_arrays_may_be_looked_at_and_replaced():
+    """An operand's arrays are views of its storage; one that a caller puts in their place is what is used."""
+    t, x = to_gpu(data(20, 272, 4), torch.bfloat16)
+    q = tj2.mx_quantize(t)
+    want = tj2.mx_dequantize(q)
+    assert q.codes.shape == (20, 3 * 64) and q.scale16.shape == (20, 3 * 4)
+    same(q, mx.quantize(x))
+    assert torch.equal(tj2.mx_dequantize(q), want)
+    other = tj2.mx_quantize(t)
+    other.codes = torch.zeros_like(q.codes)
+    assert (tj2.mx_dequantize(other) == 0).all() and torch.equal(other.scale16, q.scale16)
+    other.codes, other.scale16 = q.codes.clone(), q.scale16.clone()
+    assert torch.equal(tj2.mx_dequantize(other), want) and torch.equal(tj2.mx_dequantize(q.clone()), want)
+    with pytest.raises(AttributeError):
+        q.scale64
+
+
 def test_binding_refuses():
     x = torch.zeros(4, 32, device="cuda", dtype=torch.bfloat16)
     w = torch.zeros(16, 32, device="cuda")
