@@ -517,10 +517,10 @@ using TileMid = Tile<EL_BF16, 2, 2, 4, 4>;  // 128 x 128
 int64_t tiles_of(int64_t p, int64_t q, int64_t b) { return (p + b - 1) / b * ((q + b - 1) / b); }
 
 // Estimated time (us on MI355X) of `items` tiles over `chunks` chunks of 64 elements:
-// a tile of 256 takes 2.2 a chunk and `fixed` for its start and results, one of 128
+// a tile of 256 takes 1.9 a chunk and `fixed` for its start and results, one of 128
 // 1.1 alone on its CU and 1.5 beside another, and half of `fixed`.
 double tile_time(bool big, int64_t items, double chunks, double fixed) {
-  if (big) return (double)((items + kCus - 1) / kCus) * (chunks * 2.2 + fixed);
+  if (big) return (double)((items + kCus - 1) / kCus) * (chunks * 1.9 + fixed);
   const int64_t full = items / (2 * kCus), rest = items % (2 * kCus);
   return (double)full * (chunks * 1.5 + fixed / 2) + (rest ? chunks * (rest > kCus ? 1.5 : 1.1) + fixed / 2 : 0.0);
 }
@@ -530,27 +530,47 @@ bool ce_big(int64_t V, int64_t T, int64_t K) {
   const double chunks = (double)((K + 63) / 64);
   return tile_time(true, tiles_of(V, T, 256), chunks, 9.0) < tile_time(false, tiles_of(V, T, 128), chunks, 9.0);
 }
-// Tile and splits of a product of p by q results over k (the whole backward of 1235 x
-// 32003 over 528: 192 us with unsplit products, 174 with 8 to 16 splits).
+// Splits of a product of p by q results over k in tiles of one size, and its time (the
+// whole backward of 1235 x 32003 over 528: 192 us with unsplit products, 174 with 8 to
+// 16 splits).
 struct ProductPlan {
   bool big;
   int splits;
+  double time;
 };
-ProductPlan product_plan(int64_t p, int64_t q, int64_t k) {
-  ProductPlan best = {false, 1};
+ProductPlan product_plan(int64_t p, int64_t q, int64_t k, bool big) {
+  ProductPlan best = {big, 1, 1e30};
   const int64_t nch = (k + 63) / 64;
-  double least = 1e30;
-  for (int big = 0; big < 2; ++big)
-    for (int z = 1; z <= 32 && z * 8 <= std::max<int64_t>(nch, 8); z *= 2) {
-      double t = tile_time(big, tiles_of(p, q, big ? 256 : 128) * z, (double)((nch + z - 1) / z), 6.0);
-      if (z > 1) t += 3.0 + (double)p * (double)q * 8.0 * z / 6e6;
-      if (t < least) {
-        least = t;
-        best = ProductPlan{big != 0, z};
-      }
-    }
+  for (int z = 1; z <= 32 && z * 8 <= std::max<int64_t>(nch, 8); z *= 2) {
+    double t = tile_time(big, tiles_of(p, q, big ? 256 : 128) * z, (double)((nch + z - 1) / z), 6.0);
+    if (z > 1) t += 3.0 + (double)p * (double)q * 8.0 * z / 6e6;
+    if (t < best.time) best = ProductPlan{big, z, t};
+  }
   return best;
 }
+// Of a piece's products, dX (x) and dW (w; either may not be asked for).  Two of one
+// tile run in one launch, where the second fills what the first leaves idle: about 10
+// us (backward of 200 x 50304 over 1024: 193 us with a tile of 128 for dX and 256 for
+// dW, 180 with 128 and 169 with 256 for both; of 500 x 8000 over 304 39.5 with 128 for
+// both, 53.7 with 256).
+struct CePlans {
+  ProductPlan x[2], w[2];  // of tiles of 128 and 256
+  CePlans(int64_t T, int64_t K, int64_t vn)
+      : x{product_plan(K, T, vn, false), product_plan(K, T, vn, true)},
+        w{product_plan(K, vn, T, false), product_plan(K, vn, T, true)} {}
+  // the tiles, as indexes of x and w
+  void pick(bool dx, bool dw, int& ix, int& iw) const {
+    double least = 1e30;
+    for (int i = 0; i < 4; ++i) {
+      const double t = (dx ? x[i & 1].time : 0.0) + (dw ? w[i >> 1].time : 0.0) - (dx && dw && (i & 1) == i >> 1 ? 10.0 : 0.0);
+      if (t < least) {
+        least = t;
+        ix = i & 1;
+        iw = i >> 1;
+      }
+    }
+  }
+};
 
 template <class T>
 void launch_fwd_tile(CeArgs a, hipStream_t s) {
@@ -675,12 +695,18 @@ CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   s.d = take(blocked_bytes(T, s.piece));
   s.dt = take(blocked_bytes(s.piece, T));
   s.dx = take((size_t)(T * K * 4));
-  // partial sums of split products, of a whole piece and of the last one
+  // partial sums of split products, of a whole piece and of the last one, whichever
+  // gradients are asked for
   size_t part = 0;
   for (const int64_t vn : {s.piece, V % s.piece}) {
     if (!vn) continue;
-    const int zx = product_plan(K, T, vn).splits, zw = product_plan(K, vn, T).splits;
-    part = std::max(part, (zx > 1 ? (size_t)zx * (size_t)(T * K * 4) : 0) + (zw > 1 ? (size_t)zw * (size_t)(vn * K * 4) : 0));
+    const CePlans plans(T, K, vn);
+    for (int want = 1; want < 4; ++want) {
+      int ix = 0, iw = 0;
+      plans.pick(want & 1, want & 2, ix, iw);
+      const int zx = want & 1 ? plans.x[ix].splits : 1, zw = want & 2 ? plans.w[iw].splits : 1;
+      part = std::max(part, (zx > 1 ? (size_t)zx * (size_t)(T * K * 4) : 0) + (zw > 1 ? (size_t)zw * (size_t)(vn * K * 4) : 0));
+    }
   }
   s.part = take(part);
   s.bytes = at;
@@ -776,6 +802,9 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
     else launch_dz_tile<TileMid>(a, s);
     TJ2_STEP();
     // dX += dz W and dW = dz^T X of the piece; split products leave partial sums
+    const CePlans plans(c.T, c.K, vn);
+    int ix = 0, iw = 0;
+    plans.pick(c.dX, c.dW, ix, iw);
     ProductArgs x[2];
     bool big[2];
     int n = 0;
@@ -786,7 +815,7 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
     const bool last = v0 + vn == c.V;
     bool fold = false;
     if (c.dX) {
-      const ProductPlan plan = product_plan(c.K, c.T, vn);
+      const ProductPlan& plan = plans.x[ix];
       ProductArgs& q = x[n];
       q = {};
       q.P = blocked_operand(w + sp.wt, c.K, up(vn, 64));
@@ -811,7 +840,7 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
       big[n++] = plan.big;
     }
     if (c.dW) {
-      const ProductPlan plan = product_plan(c.K, vn, c.T);
+      const ProductPlan& plan = plans.w[iw];
       ProductArgs& q = x[n];
       q = {};
       q.P = blocked_operand(w + sp.xt, c.K, up(c.T, 64));
