@@ -592,28 +592,49 @@ using Few = Skinny<EL_MX, 1, 64 * 1024>;
 // (128, two splits); of 256 x 4096 over 4096: 11.3 (64), 18.1, 30.7.
 struct MxPlan {
   int tile, splits;
+  double time, packed;  // packed: where other tiles take the places that it leaves idle
 };
-MxPlan mx_plan(int64_t I, int64_t J, int64_t K) {
+MxPlan mx_plan(int64_t I, int64_t J, int64_t K, int tile) {
   constexpr double kAlone[3] = {0.6, 1.15, 2.3}, kFull[3] = {1.3, 1.6, 2.3}, kFixed[3] = {2.0, 2.5, 5.0};
   constexpr int kSlots[3] = {4, 2, 1};
   const int64_t nch = (K + 255) / 256;
-  MxPlan best = {0, 1};
-  double least = 1e30;
+  const int64_t b = 64 << tile, n = ((I + b - 1) / b) * ((J + b - 1) / b), slots = kCus * kSlots[tile];
+  MxPlan best = {tile, 1, 1e30, 1e30};
+  for (int z = 1; z <= 16 && z * 4 <= std::max<int64_t>(nch, 4); z *= 2) {
+    const int64_t items = n * z, full = items / slots, rest = items % slots, deep = (rest + kCus - 1) / kCus;
+    const double chunks = (double)((nch + z - 1) / z);
+    double t = (double)full * (chunks * kFull[tile] + kFixed[tile]);
+    if (rest) {
+      const double per = kSlots[tile] > 1 ? kAlone[tile] + (kFull[tile] - kAlone[tile]) * (double)(deep - 1) / (kSlots[tile] - 1) : kFull[tile];
+      t += chunks * per + kFixed[tile];
+    }
+    const double join = z > 1 ? 3.0 + (double)I * (double)J * 8.0 * z / 5e6 : 0.0;
+    if (t + join < best.time)
+      best = MxPlan{tile, z, t + join, (double)items * (chunks * kFull[tile] + kFixed[tile]) / (double)slots + join};
+  }
+  return best;
+}
+MxPlan mx_plan(int64_t I, int64_t J, int64_t K) {
+  MxPlan best = mx_plan(I, J, K, 0);
+  for (int tile = 1; tile < 3; ++tile)
+    if (const MxPlan p = mx_plan(I, J, K, tile); p.time < best.time) best = p;
+  return best;
+}
+// Two products that do not depend on each other: of one tile they run in one launch,
+// the second in the places that the first leaves idle (backward of 16384 x 1024 over
+// 1024: 85 us with tiles of 256 and 128 in two launches, 79 with 128 for both).
+struct MxPlans {
+  MxPlan a, b;
+};
+MxPlans mx_plans(int64_t I, int64_t J, int64_t K, int64_t I2, int64_t J2, int64_t K2) {
+  MxPlans best = {mx_plan(I, J, K), mx_plan(I2, J2, K2)};
+  double least = best.a.time + best.b.time;
   for (int tile = 0; tile < 3; ++tile) {
-    const int64_t b = 64 << tile, n = ((I + b - 1) / b) * ((J + b - 1) / b), slots = kCus * kSlots[tile];
-    for (int z = 1; z <= 16 && z * 4 <= std::max<int64_t>(nch, 4); z *= 2) {
-      const int64_t items = n * z, full = items / slots, rest = items % slots, deep = (rest + kCus - 1) / kCus;
-      const double chunks = (double)((nch + z - 1) / z);
-      double t = (double)full * (chunks * kFull[tile] + kFixed[tile]);
-      if (rest) {
-        const double per = kSlots[tile] > 1 ? kAlone[tile] + (kFull[tile] - kAlone[tile]) * (double)(deep - 1) / (kSlots[tile] - 1) : kFull[tile];
-        t += chunks * per + kFixed[tile];
-      }
-      if (z > 1) t += 3.0 + (double)I * (double)J * 8.0 * z / 5e6;
-      if (t < least) {
-        least = t;
-        best = MxPlan{tile, z};
-      }
+    const MxPlans c = {mx_plan(I, J, K, tile), mx_plan(I2, J2, K2, tile)};
+    const double t = std::max({c.a.packed + c.b.packed, c.a.time, c.b.time});
+    if (t < least) {
+      least = t;
+      best = c;
     }
   }
   return best;
@@ -625,10 +646,12 @@ bool mx_is_few(int64_t M, int64_t K) { return Few::fits(M, (K + 127) / 128 * 64)
 
 bool mx_blocked(int64_t I, int64_t K) { return !mx_is_few(I, K); }
 
+namespace {
+size_t split_bytes(int z, int64_t I, int64_t J) { return z > 1 ? (size_t)z * (size_t)I * (size_t)J * 4 : 0; }
+}  // namespace
+
 size_t mx_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K) {
-  if (mx_is_few(I, K)) return 0;
-  const int z = mx_plan(I, J, K).splits;
-  return z > 1 ? (size_t)z * (size_t)I * (size_t)J * 4 : 0;
+  return mx_is_few(I, K) ? 0 : split_bytes(mx_plan(I, J, K).splits, I, J);
 }
 
 namespace {
@@ -672,10 +695,8 @@ struct MxProduct {
   MxGemmArgs part, out;
   int tile;
 };
-MxProduct mx_product(const MxGemmArgs& a, int64_t K, float* partial) {
-  MxProduct x = {a, a, 0};
-  const MxPlan plan = mx_plan(a.Q.rows, a.P.rows, K);
-  x.tile = plan.tile;
+MxProduct mx_product(const MxGemmArgs& a, const MxPlan& plan, float* partial) {
+  MxProduct x = {a, a, plan.tile};
   x.part.splits = x.out.splits = partial ? plan.splits : 1;
   x.out.partial = partial;
   if (x.out.splits > 1) {
@@ -718,29 +739,39 @@ hipError_t launch_mx_gemm(const QView& A, const QView& B, void* C, int c_dtype, 
                           hipStream_t s) {
   const MxGemmArgs a = mx_gemm_args(A, B, C, c_dtype, ldc, accumulate);
   if (mx_is_few(A.rows, A.len)) return launch_few(a, nullptr, 0, nullptr, s);
-  const MxProduct x = mx_product(a, A.len, partial);
+  const MxProduct x = mx_product(a, mx_plan(A.rows, B.rows, A.len), partial);
   if (hipError_t e = launch_products(&x, 1, s); e != hipSuccess) return e;
   return launch_joins(&x, 1, s);
 }
 
+namespace {
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+// the plans of a pair, of which either may be a product of few rows instead
+MxPlans pair_plans(int64_t I, int64_t J, int64_t K, int64_t I2, int64_t J2, int64_t K2) {
+  if (mx_is_few(I, K) || mx_is_few(I2, K2)) return MxPlans{mx_plan(I, J, K), mx_plan(I2, J2, K2)};
+  return mx_plans(I, J, K, I2, J2, K2);
+}
+}  // namespace
+
 size_t mx_gemm_pair_workspace_bytes(int64_t I, int64_t J, int64_t K, int64_t I2, int64_t J2, int64_t K2) {
-  return (mx_gemm_workspace_bytes(I, J, K) + 255) / 256 * 256 + mx_gemm_workspace_bytes(I2, J2, K2);
+  const MxPlans plans = pair_plans(I, J, K, I2, J2, K2);
+  return up256(mx_is_few(I, K) ? 0 : split_bytes(plans.a.splits, I, J)) + (mx_is_few(I2, K2) ? 0 : split_bytes(plans.b.splits, I2, J2));
 }
 
 hipError_t launch_mx_gemm_pair(const QView& A, const QView& B, void* C, int c_dtype, const QView& A2, const QView& B2, void* C2,
                                int c2_dtype, float* partial, hipStream_t s) {
   const MxGemmArgs a[2] = {mx_gemm_args(A, B, C, c_dtype, B.rows, 0, mx_blocked(A.rows, A.len)),
                            mx_gemm_args(A2, B2, C2, c2_dtype, B2.rows, 0, mx_blocked(A2.rows, A2.len))};
-  const size_t first = (mx_gemm_workspace_bytes(A.rows, B.rows, A.len) + 255) / 256 * 256;
-  float* room[2] = {partial, partial + first / 4};
-  const int64_t K[2] = {A.len, A2.len};
+  const MxPlans plans = pair_plans(A.rows, B.rows, A.len, A2.rows, B2.rows, A2.len);
+  const bool few[2] = {mx_is_few(A.rows, A.len), mx_is_few(A2.rows, A2.len)};
+  const size_t first = up256(few[0] ? 0 : split_bytes(plans.a.splits, A.rows, B.rows));
   MxProduct x[2];
   int n = 0;
   for (int i = 0; i < 2; ++i) {
-    if (mx_is_few(a[i].Q.rows, K[i])) {
+    if (few[i]) {
       if (hipError_t e = launch_few(a[i], nullptr, 0, nullptr, s); e != hipSuccess) return e;
     } else {
-      x[n++] = mx_product(a[i], K[i], room[i]);
+      x[n++] = mx_product(a[i], i ? plans.b : plans.a, i ? partial + first / 4 : partial);
     }
   }
   for (int i = 0; i < n;) {
