@@ -97,7 +97,7 @@ struct MxRowArgs {
 
 // Groups along the rows.  A thread takes 16 neighbouring elements, a pair of lanes
 // a group (the pair's larger top by one DPP swap), eight threads a 128-element
-// block, padding included.
+// block, padding included.  Bound by memory: 16384 x 1024 bf16 in 8.7 us, 4.9 TB/s.
 template <class T, bool SR, bool RHT>
 __device__ __forceinline__ void mx_row(const MxRowArgs& p, uint32_t block) {
   const int64_t id = (int64_t)block * 256 + threadIdx.x;
@@ -166,6 +166,9 @@ struct MxIn {};  // tag: MXFP4 input
 // columns through LDS: rows are read whole, then each thread owns 32 rows of one
 // column, a group, and writes its 16 bytes (four groups of a column make a line of
 // 64).  MXFP4 input is decoded to bf16 on the way, which holds its values exactly.
+// Bound by memory: 16384 x 4096 bf16 in 34 us, 5 TB/s (35 with the transform, 44 with
+// stochastic rounding too, which its draws bound; from memory that no cache holds 45
+// with the transform).  128 columns a workgroup and two a thread: 35, 37 and 46.
 template <class T>
 using MxColElement = std::conditional_t<std::is_same<T, float>::value, float, uint16_t>;
 template <class T, bool SR, bool RHT>
@@ -349,7 +352,8 @@ __global__ __launch_bounds__(256) void mx_backward_kernel(MxDualArgs d, uint32_t
 }
 
 // ---- values ----------------------------------------------------------------------
-// 8 elements (one code word) a thread; rows of the output are `len` elements.
+// 8 elements (one code word) a thread; rows of the output are `len` elements.  Bound by
+// memory: 16384 x 4096 to bf16 in 25 us, 6.7 TB/s.
 template <bool F32>
 __global__ __launch_bounds__(256) void mx_values_kernel(const uint8_t* codes, const uint8_t* scale, int64_t rows, int32_t len,
                                                         int32_t nb, void* out) {
@@ -442,7 +446,10 @@ __device__ __forceinline__ void store_run(const MxGemmArgs& p, int64_t row, int6
   }
 }
 
-// One product or two.
+// One product or two.  C = sum over groups of 2^(ea + eb) sum qa qb, the scales applied
+// by the instruction.  4096 x 4096 over 16384 in 154 us, 3.6 PFLOP/s (4.6 on operands of
+// zeros: with others the GPU's power bounds it, and the loads' way through L2 and LDS);
+// 16384 x 4096 over 1024 in 56, of which the 134 MB of results alone take 26.
 template <class T>
 __global__ __launch_bounds__(T::NT, T::WAVES) void mx_gemm_kernel(Pair<MxGemmArgs> jobs) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
@@ -471,7 +478,8 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void mx_gemm_kernel(Pair<MxGemmArg
 
 // Up to 16 rows of A (decoding): A whole in LDS, B read once.  From bf16 X (the
 // linear layer's forward) each workgroup quantizes X for itself, the first one
-// storing the codes too, which saves the launch that would do it.
+// storing the codes too, which saves the launch that would do it.  1 x 1024 to 4096 in
+// 4.5 us, which is a launch, the quantization and one round of loads.
 struct MxFewArgs {
   MxGemmArgs g;
   const uint16_t* x;  // quantize [I, cols] bf16 into g.Q's arrays; NULL: they are given
@@ -525,6 +533,7 @@ __global__ __launch_bounds__(S::NT, 2) void mx_few_kernel(MxFewArgs a) {
 }
 
 // C = (C +) the sum of the splits' results in order, 4 a thread; of one product or two.
+// Bound by memory (or, most often, the last cache): two splits of 4096 x 1024 in 10 us.
 __global__ __launch_bounds__(256) void mx_join_kernel(Pair<MxGemmArgs> jobs) {
   const Share mine(jobs.first);
   const MxGemmArgs& p = jobs.x[mine.job];

@@ -647,11 +647,12 @@ size_t tj2_linear_ce_fwd_workspace_size(int64_t T, int64_t K, int64_t V);
 /*
  * tj2_linear_ce_bwd: with dloss [T] the gradient of each token's loss and
  *   dz[t, v] = dloss[t] (exp(z[t, v] - lse[t]) - [v == targets[t]])
- * (0 for an ignored token, whatever its row of X holds, which enters nothing; NaN
- * for a target outside the vocabulary), dX [T, K] = dz W and dW [V, K] = dz^T X, contiguous, each TJ2_BF16
- * or TJ2_F32, either may be NULL.  The vocabulary is taken in pieces; dz of a
- * piece is rounded to bf16, divided by the largest |dloss|, for the two products,
- * whose sums are fp32.  The results do not depend on scheduling.  workspace:
+ * (0 for an ignored token, whatever its row of X and its dloss hold, which enter
+ * nothing; NaN for a target outside the vocabulary), dX [T, K] = dz W and dW [V, K]
+ * = dz^T X, contiguous, each TJ2_BF16 or TJ2_F32, either may be NULL.  The vocabulary
+ * is taken in pieces; dz of a piece is rounded to bf16, divided by the largest
+ * |dloss|, for the two products, whose sums are fp32 (an infinite dloss makes every
+ * gradient NaN).  The results do not depend on scheduling.  workspace:
  * tj2_linear_ce_bwd_workspace_size(T, K, V) bytes, 16-byte aligned, required.
  */
 tj2_status tj2_linear_ce_bwd(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t T,
