@@ -248,6 +248,29 @@ def test_cross_entropy_last_piece_and_large_tiles(T, K, V):
     ce_check(X, W, y, torch.rand(T, generator=g, device="cuda"))
 
 
+@pytest.mark.parametrize("T,K,V", [(16384, 48, 20000), (200, 1024, 9000), (9000, 80, 33001)])
+def test_cross_entropy_one_gradient_of_several_pieces(T, K, V):
+    """Each gradient by itself is the one of both: the same dz, summed in an order of its own."""
+    X, W, y, g = ce_inputs(T, K, V, 51)
+    d = torch.rand(T, generator=g, device="cuda") / T
+    _, lse = tj2.linear_ce_fwd(X, W, y)
+    opt = dict(dx_dtype=torch.float32, dw_dtype=torch.float32)
+    both = tj2.linear_ce_bwd(X, W, y, lse, d, **opt)
+    dX, none = tj2.linear_ce_bwd(X, W, y, lse, d, need_dw=False, **opt)
+    assert none is None
+    none, dW = tj2.linear_ce_bwd(X, W, y, lse, d, need_dx=False, **opt)
+    assert none is None
+    # two fp32 sums of the same n products, each within n + 64 half steps of the sum of magnitudes; |dz| <= d (p + 1 at
+    # the target), of which bf16 takes half a step
+    z = X.double() @ W.double().T
+    c = torch.where(y == -100, 0.0, d.double())
+    dz = torch.exp(z - lse.double()[:, None]).mul_(c[:, None])
+    dz[torch.arange(T, device="cuda"), y.clamp(min=0)] += c
+    dz *= 1 + 2 * H8
+    assert ((dX - both[0]).double().abs() <= 2 * (V + 64) * H24 * (dz @ W.double().abs()) + 2.0 ** -130).all()
+    assert ((dW - both[1]).double().abs() <= 2 * (T + 64) * H24 * (dz.T @ X.double().abs()) + 2.0 ** -130).all()
+
+
 def test_cross_entropy_graphs_share_a_workspace():
     """Two captured backward passes with one workspace, replayed in turns among eager calls that use it too."""
     cases = []
