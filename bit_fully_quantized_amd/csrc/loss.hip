@@ -986,8 +986,8 @@ struct DistillArgs {
 // are read once); R = 0: the row is read again for each of the three passes.
 // Elements before the first and after the last aligned vector are one per thread;
 // HARD: the hard target's term is there too (a second sum of exponentials at
-// temperature 1).  Bound by memory: 16384 x 50304 bf16 with 64 entries in 575 to 628 us,
-// 5.3 to 5.7 TB/s.
+// temperature 1).  Bound by memory: 16384 x 50304 bf16 with 64 entries in 635 us, 5.2
+// TB/s, a large copy's rate.
 template <class T, int R, bool HARD, int kThreads>
 __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distill_kernel(DistillArgs p) {
   constexpr int N = Vec<T>::N, WAVES = kThreads / 64;
@@ -1040,7 +1040,7 @@ __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distil
     if constexpr (R > 0) {
       // the places are worked out again in each pass: kept from the loads to the stores
       // they would be spilled (16384 rows of 50304 bf16: 0.3 GB beside the 3.3 GB of
-      // logits, 684 us and 628 without)
+      // logits, 623 to 690 us by where the buffers lie, 635 without)
       int at = t;
       asm volatile("" : "+v"(at));
 #pragma unroll
