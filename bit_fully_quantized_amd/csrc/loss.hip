@@ -485,6 +485,91 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ce_product_kernel(Pair<Produc
   });
 }
 
+// dX of up to 64 tokens from W as it lies, one read of it: no turned copy.  A wave takes
+// 64 columns of W (4 n to 4 n + 3 a lane, whole lines over 16 lanes) and 32 rows a step,
+// eight a lane, whose halves it pairs into four operand tiles (tile c: columns 4 i + c),
+// so that a lane's results are 16 neighbours of a token.  The waves of a workgroup take
+// its rows in turn and join in LDS; workgroups split the rows, joined by ce_sum_kernel.
+// Bound by the read of W: 16 x 50304 over 1024 in 19.7 us, 5.2 TB/s.
+struct DxFewArgs {
+  const uint16_t* W;
+  int64_t ldw, T, K, V;
+  const uint16_t* d;  // dz, blocked (T <= 64: rows of 64 entries in blocks of 128 rows)
+  float* part;        // [splits][T][K]
+  uint32_t blocks;    // of 64 columns
+  int32_t steps, splits;
+};
+template <int TN>
+__global__ __launch_bounds__(256, TN == 4 ? 2 : 4) void ce_dx_few_kernel(DxFewArgs p) {
+  __shared__ __attribute__((aligned(16))) float sh[16 * TN][64 + 4];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const uint32_t kb = blockIdx.x % p.blocks, z = blockIdx.x / p.blocks;
+  const int64_t k = (int64_t)kb * 64 + 4 * n;
+  const bool in = k < p.K;
+  const int s0 = (int)((int64_t)p.steps * z / p.splits), s1 = (int)((int64_t)p.steps * (z + 1) / p.splits);
+  struct Step {
+    uint2 w[8];
+    i32x4_t d[TN];
+  };
+  auto fetch = [&](Step& f, int s) __attribute__((always_inline)) {
+    const int64_t v = (int64_t)s * 32 + 8 * g;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f.w[j] = uint2{0u, 0u};
+      if (in && s < s1 && v + j < p.V) f.w[j] = *reinterpret_cast<const uint2*>(p.W + (v + j) * p.ldw + k);
+    }
+    if (s < s1) {
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+        f.d[tn] = *reinterpret_cast<const i32x4_t*>(p.d + (v >> 6) * 8192 + (tn * 16 + n) * 64 + (v & 63));
+    }
+  };
+  float4_t acc[4][TN] = {};
+  auto multiply = [&](const Step& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      i32x4_t a;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = c < 2 ? f.w[2 * j].x : f.w[2 * j].y, hi = c < 2 ? f.w[2 * j + 1].x : f.w[2 * j + 1].y;
+        a[j] = (int)__builtin_amdgcn_perm(hi, lo, c & 1 ? 0x07060302u : 0x05040100u);
+      }
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+        acc[c][tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, f.d[tn]),
+                                                             acc[c][tn], 0, 0, 0);
+    }
+  };
+  Step f0, f1;
+  fetch(f0, s0 + w);
+  for (int s = s0 + w; s < s1; s += 8) {
+    fetch(f1, s + 4);
+    multiply(f0);
+    fetch(f0, s + 8);
+    if (s + 4 < s1) multiply(f1);
+  }
+  // the waves' sums, in their order; a lane's column 16 g + 4 r + c of token 16 tn + n
+  for (int q = 0; q < 4; ++q) {
+    if (w == q) {
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float4_t* o = reinterpret_cast<float4_t*>(&sh[tn * 16 + n][16 * g + 4 * r]);
+          float4_t v = {acc[0][tn][r], acc[1][tn][r], acc[2][tn][r], acc[3][tn][r]};
+          if (q) v += *o;
+          *o = v;
+        }
+    }
+    __syncthreads();
+  }
+  float* out = p.part + (size_t)z * (size_t)(p.T * p.K);
+  for (int i = threadIdx.x; i < 16 * TN * 16; i += 256) {
+    const int64_t t = i >> 4, col = (int64_t)kb * 64 + (i & 15) * 4;
+    if (t < p.T && col < p.K) *reinterpret_cast<float4_t*>(out + t * p.K + col) = *reinterpret_cast<const float4_t*>(&sh[t][(i & 15) * 4]);
+  }
+}
+
 // out = scale * (sum of `parts` fp32 slices), in order; 4 a thread (n a multiple of 16).
 // One result or two.  Bound by memory: 16384 x 1024 fp32 to bf16 in 15 us.
 struct SumArgs {
@@ -500,6 +585,7 @@ __global__ __launch_bounds__(256) void ce_sum_kernel(Pair<SumArgs> jobs) {
   const int64_t i = ((int64_t)mine.block * 256 + threadIdx.x) * 4, n = p.n;
   if (i >= n) return;
   float4_t v = *reinterpret_cast<const float4_t*>(p.sum + i);
+#pragma unroll 8
   for (int z = 1; z < p.parts; ++z) v += *reinterpret_cast<const float4_t*>(p.sum + (size_t)z * (size_t)n + i);
   const float s = *p.scale;
   v *= s;
@@ -513,6 +599,7 @@ __global__ __launch_bounds__(256) void ce_fold_kernel(float* kept, const float* 
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= n) return;
   float4_t v = *reinterpret_cast<const float4_t*>(part + i);
+#pragma unroll 8
   for (int z = 1; z < parts; ++z) v += *reinterpret_cast<const float4_t*>(part + (size_t)z * (size_t)n + i);
   if (!first) v += *reinterpret_cast<const float4_t*>(kept + i);
   *reinterpret_cast<float4_t*>(kept + i) = v;
@@ -682,14 +769,26 @@ CeFwdSpace ce_fwd_space(int64_t T, int64_t K, int64_t V) {
   return s;
 }
 
+// Whether dX is taken from W as it lies: few tokens, and a W of 2^22 elements, whose
+// turned copy costs more than the launch that this adds (backward with the copy and
+// without: 16 x 50304 over 1024 124 and 79 us, 40 tokens 125 and 88, 30 x 8000 over 704 41
+// and 37; 50 x 20000 over 128 33 and 36, 20 x 1000 over 64 20 and 23).
+bool dx_few(int64_t T, int64_t K, int64_t V) { return T <= 64 && K * V >= (int64_t)1 << 22; }
+// Workgroups over the rows of W: as many as run at once, of 16 steps of 32 rows at least
+int dx_few_splits(int64_t K, int64_t V) {
+  const int64_t steps = (V + 31) / 32, blocks = (K + 63) / 64;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(32, steps / 16), 4 * kCus / blocks));
+}
+
 struct CeBwdSpace {
   size_t c, top, xb, xt, wb, wt, d, dt, dx, part, bytes;
   int64_t piece;
-  bool blocked;
+  bool blocked, few;
 };
 CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   CeBwdSpace s;
-  s.piece = ce_piece(T, V);
+  s.few = dx_few(T, K, V);
+  s.piece = ce_piece(T, V);  // all of V for few tokens
   s.blocked = T >= kBlockTokens;
   size_t at = 0;
   auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
@@ -698,7 +797,7 @@ CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   s.xb = take(s.blocked ? blocked_bytes(T, K) : 0);
   s.xt = take(blocked_bytes(K, T));
   s.wb = take(s.blocked ? blocked_bytes(s.piece, K) : 0);
-  s.wt = take(blocked_bytes(K, s.piece));
+  s.wt = take(s.few ? 0 : blocked_bytes(K, s.piece));
   s.d = take(blocked_bytes(T, s.piece));
   s.dt = take(blocked_bytes(s.piece, T));
   s.dx = take((size_t)(T * K * 4));
@@ -710,11 +809,12 @@ CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
     const CePlans plans(T, K, vn);
     for (int want = 1; want < 4; ++want) {
       int ix = 0, iw = 0;
-      plans.pick(want & 1, want & 2, ix, iw);
-      const int zx = want & 1 ? plans.x[ix].splits : 1, zw = want & 2 ? plans.w[iw].splits : 1;
+      plans.pick((want & 1) && !s.few, want & 2, ix, iw);
+      const int zx = s.few || !(want & 1) ? 1 : plans.x[ix].splits, zw = want & 2 ? plans.w[iw].splits : 1;
       part = std::max(part, (zx > 1 ? (size_t)zx * (size_t)(T * K * 4) : 0) + (zw > 1 ? (size_t)zw * (size_t)(vn * K * 4) : 0));
     }
   }
+  if (s.few) part += (size_t)dx_few_splits(K, V) * (size_t)(T * K * 4);
   s.part = take(part);
   s.bytes = at;
   return s;
@@ -791,7 +891,7 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
     const int64_t vn = std::min(sp.piece, c.V - v0);
     const uint16_t* W = reinterpret_cast<const uint16_t*>(c.W) + v0 * c.ldw;
     launch_prepare(v0 ? nullptr : &weights, v0 ? nullptr : &xb,
-                   block_args(W, vn, c.K, c.ldw, sp.blocked ? w + sp.wb : nullptr, w + sp.wt), s);
+                   sp.few ? BlockArgs{} : block_args(W, vn, c.K, c.ldw, sp.blocked ? w + sp.wb : nullptr, w + sp.wt), s);
     TJ2_STEP();
     CeArgs a = {};
     a.P = sp.blocked ? blocked_operand(w + sp.wb, vn, c.K) : bf16_operand(W, vn, c.K, c.ldw);
@@ -811,7 +911,7 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
     // dX += dz W and dW = dz^T X of the piece; split products leave partial sums
     const CePlans plans(c.T, c.K, vn);
     int ix = 0, iw = 0;
-    plans.pick(c.dX, c.dW, ix, iw);
+    plans.pick(c.dX && !sp.few, c.dW, ix, iw);
     ProductArgs x[2];
     bool big[2];
     int n = 0;
@@ -821,7 +921,26 @@ hipError_t launch_ce_bwd(const CeParams& c, void* ws, hipStream_t s) {
     const int64_t nx = c.T * c.K, nw = vn * c.K;
     const bool last = v0 + vn == c.V;
     bool fold = false;
-    if (c.dX) {
+    if (c.dX && sp.few) {
+      DxFewArgs x = {};
+      x.W = W;
+      x.ldw = c.ldw;
+      x.T = c.T;
+      x.K = c.K;
+      x.V = vn;
+      x.d = a.d;
+      x.part = at;
+      x.blocks = (uint32_t)((c.K + 63) / 64);
+      x.steps = (int32_t)((vn + 31) / 32);
+      x.splits = dx_few_splits(c.K, vn);
+      const uint32_t grid = x.blocks * (uint32_t)x.splits;
+      if (c.T <= 16) ce_dx_few_kernel<1><<<grid, 256, 0, s>>>(x);
+      else if (c.T <= 32) ce_dx_few_kernel<2><<<grid, 256, 0, s>>>(x);
+      else ce_dx_few_kernel<4><<<grid, 256, 0, s>>>(x);
+      TJ2_STEP();
+      sums[joins++] = SumArgs{at, x.splits, c.dx_dtype == TJ2_BF16, nx, top, c.dX};
+      at += (size_t)x.splits * (size_t)nx;
+    } else if (c.dX) {
       const ProductPlan& plan = plans.x[ix];
       ProductArgs& q = x[n];
       q = {};

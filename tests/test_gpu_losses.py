@@ -231,6 +231,20 @@ def test_cross_entropy_few_tokens(T, K):
     ce_check(X, W, y, torch.randn(T, generator=g, device="cuda"))
 
 
+@pytest.mark.parametrize("T,K,V", [(1, 1024, 5000), (15, 16, 270001), (16, 1040, 4099), (17, 208, 24001), (33, 528, 8001),
+                                   (48, 80, 60000), (64, 1040, 4100), (64, 2064, 33003)])
+def test_cross_entropy_few_tokens_large_heads(T, K, V):
+    """Few tokens and a head of 2^22 elements and more: dX from W as it lies, also with rows apart and by itself."""
+    X, W, y, g = ce_inputs(T, K, V, T * K, ignored=0.2)
+    Wp = torch.full((V, K + 8), NAN, device="cuda", dtype=torch.bfloat16)
+    Wp[:, :K] = W
+    d = torch.randn(T, generator=g, device="cuda")
+    for w in (W, Wp[:, :K]):
+        _, lse, dX, dW = ce_check(X, w, y, d)
+        assert torch.equal(dX, tj2.linear_ce_bwd(X, w, y, lse, d, need_dw=False)[0])
+    ce_check(X, W, y, d, dx_dtype=torch.float32, dw_dtype=torch.float32)
+
+
 @pytest.mark.parametrize("T,K,V,ldx,ldw", [(2047, 80, 700, 88, 96), (2048, 80, 700, 80, 160), (2049, 144, 513, 152, 144),
                                            (30, 80, 700, 96, 88)])
 def test_cross_entropy_pitched_with_and_without_blocks(T, K, V, ldx, ldw):
