@@ -772,7 +772,8 @@ CeFwdSpace ce_fwd_space(int64_t T, int64_t K, int64_t V) {
 // Whether dX is taken from W as it lies: few tokens, and a W of 2^22 elements, whose
 // turned copy costs more than the launch that this adds (backward with the copy and
 // without: 16 x 50304 over 1024 124 and 79 us, 40 tokens 125 and 88, 30 x 8000 over 704 41
-// and 37; 50 x 20000 over 128 33 and 36, 20 x 1000 over 64 20 and 23).
+// and 37; 50 x 20000 over 128 33 and 36, 20 x 1000 over 64 20 and 23; 100 x 50304 over
+// 1024, with sums that no longer fit the registers, 138 and 171).
 bool dx_few(int64_t T, int64_t K, int64_t V) { return T <= 64 && K * V >= (int64_t)1 << 22; }
 // Workgroups over the rows of W: as many as run at once, of 16 steps of 32 rows at least
 int dx_few_splits(int64_t K, int64_t V) {

@@ -232,7 +232,8 @@ def test_cross_entropy_few_tokens(T, K):
 
 
 @pytest.mark.parametrize("T,K,V", [(1, 1024, 5000), (15, 16, 270001), (16, 1040, 4099), (17, 208, 24001), (33, 528, 8001),
-                                   (48, 80, 60000), (64, 1040, 4100), (64, 2064, 33003)])
+                                   (48, 80, 60000), (64, 1040, 4100), (64, 2064, 33003), (65, 1040, 4099), (96, 256, 17001),
+                                   (127, 528, 9000), (128, 1024, 4097), (129, 1024, 4097)])
 def test_cross_entropy_few_tokens_large_heads(T, K, V):
     """Few tokens and a head of 2^22 elements and more: dX from W as it lies, also with rows apart and by itself."""
     X, W, y, g = ce_inputs(T, K, V, T * K, ignored=0.2)
