@@ -164,9 +164,11 @@ __global__ __launch_bounds__(S::NT, 2) void ce_few_kernel(CeArgs p) {
       }
       if (v0 < p.P.rows) {
         float e = 0.0f;
+        // four logits of -inf (masked entries) add nothing; their difference to m would be NaN
+        const float mb = m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (v0 + k < p.P.rows) e += exp_scaled(acc[tn][k], m, kLog2e);
+          if (v0 + k < p.P.rows) e += exp_scaled(acc[tn][k], mb, kLog2e);
         join(r[tn], s[tn], m * kLog2e, e);
       }
     }

@@ -1,0 +1,44 @@
+"""The head's losses on the GPU where a mask or a bad entry decides."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+tj2 = pytest.importorskip("bit_fully_quantized_amd")
+
+from test_gpu_losses import H8, H24, INF, ce_inputs  # noqa: E402
+
+
+@pytest.mark.parametrize("T", [1, 5, 16, 33, 64, 65, 300])
+def test_cross_entropy_masked_vocabulary(T):
+    """Entries with logits of -inf (a mask's bias of -inf against a constant feature) have probability 0."""
+    K, V = 128, 1100
+    X, W, y, g = ce_inputs(T, K, V, T, ignored=0.0)
+    masked = torch.zeros(V, dtype=torch.bool, device="cuda")
+    masked[100:104] = masked[209] = masked[300:700] = masked[1030:] = True
+    y %= 100
+    X[:, 0] = 1.0
+    W[masked, 0] = -INF
+    loss, lse = tj2.linear_ce_fwd(X, W, y)
+    x, w = X.double(), W[~masked].double()
+    z = x @ w.T
+    rlse = torch.logsumexp(z, 1)
+    rows = torch.arange(T, device="cuda")
+    place = (~masked).cumsum(0)[y] - 1
+    # as for unmasked heads: K + 16 half steps of a logit's sum of magnitudes, 16 of the arguments of exp2 and log2
+    ez = (K + 16) * H24 * (x.abs() @ w.abs().T).amax(1)
+    tol = 2 * ez + 16 * H24 * (2 * z.abs().amax(1) + rlse.abs() + 1)
+    assert ((lse.double() - rlse).abs() <= tol).all()
+    assert ((loss.double() - (rlse - z[rows, place])).abs() <= 2 * tol).all()
+    dX, dW = tj2.linear_ce_bwd(X, W, y, lse, torch.ones(T, device="cuda"), dw_dtype=torch.float32, dx_dtype=torch.float32)
+    assert (dW[masked] == 0).all() and torch.isfinite(dW).all()
+    p = torch.exp(z - rlse[:, None])
+    dz = p.clone()
+    dz[rows, place] -= 1
+    # p off by its exponent's error, dz by half a bf16 step more; sums of fp32
+    edz = p * (ez + tol + 16 * H24 * (1 + z.abs().amax(1)))[:, None] + dz.abs() * H8 + 2.0 ** -126
+    n = T + 64
+    assert ((dW[~masked].double() - dz.T @ x).abs() <= edz.T @ x.abs() + n * H24 * (dz.abs().T @ x.abs())).all()
+    # (feature 0 is 0 times -inf there, as in a product with the logits kept)
+    err = (dX.double() - dz @ w).abs()[:, 1:]
+    assert (err <= (edz @ w.abs() + (V + 64) * H24 * (dz.abs() @ w.abs()))[:, 1:]).all()
