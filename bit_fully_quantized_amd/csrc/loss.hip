@@ -230,7 +230,8 @@ __global__ __launch_bounds__(L * S) void ce_join_kernel(const float2* part, int 
 // dz of a tile in bf16, both ways: 16384 x 16384 over 1024 in 570 to 600 us, of which the
 // product takes some 460 and the 1.07 GB of dz the rest.  The exponential is clamped to [0, 1], which costs
 // nothing (an output modifier) and holds where the fused v c - r overflows; it turns a
-// NaN into 0, so a token whose lse is NaN gets a NaN weight instead.
+// NaN into 0, so a token whose lse is NaN, or -inf (all its logits are), gets a NaN weight
+// instead.
 template <class T>
 __global__ __launch_bounds__(T::NT, T::WAVES) void ce_dz_kernel(CeArgs p) {
   static_assert(T::kTN == 4 && T::PB == 4, "64 tokens, and entries 16 a lane");
@@ -249,7 +250,7 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ce_dz_kernel(CeArgs p) {
       const bool in = t0 + tn < p.Q.rows;
       const float l = in ? p.lse[t0 + tn] : 0.0f;
       c[tn] = in ? p.c[t0 + tn] : 0.0f;
-      if (l != l && c[tn] != 0.0f) c[tn] = kNan;
+      if (!(l > -INFINITY) && c[tn] != 0.0f) c[tn] = kNan;  // NaN, or no entry of the token is left
       b[tn] = l * kLog2e;
       const int64_t yw = in ? p.y[t0 + tn] - p.v0 - pw : -1;
       const bool here = yw >= 0 && yw < there;

@@ -635,8 +635,9 @@ size_t mxfp4_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
  * backward) and, if loss is not NULL, loss[t] = lse[t] - z[t, targets[t]] (fp32 [T]; 0
  * where targets[t] == ignore_index; NaN where a target lies outside the
  * vocabulary).  Logits are fp32 sums of exact products and are not rounded;
- * those of -inf (masked entries) have probability 0, and probabilities below
- * 2^-126 count as 0.
+ * those of -inf (masked entries) have probability 0 (a token with no others has
+ * lse -inf, and NaN for its loss and gradients), and probabilities below 2^-126
+ * count as 0.
  * workspace: tj2_linear_ce_fwd_workspace_size(T, K, V) bytes, 16-byte aligned,
  * required.
  */

@@ -42,3 +42,27 @@ def test_cross_entropy_masked_vocabulary(T):
     # (feature 0 is 0 times -inf there, as in a product with the logits kept)
     err = (dX.double() - dz @ w).abs()[:, 1:]
     assert (err <= (edz @ w.abs() + (V + 64) * H24 * (dz.abs() @ w.abs()))[:, 1:]).all()
+
+
+@pytest.mark.parametrize("T", [5, 64, 65, 2100])
+def test_cross_entropy_token_with_no_entry_left(T):
+    """A token whose logits are all -inf: lse -inf, loss and gradients NaN, as of a softmax of them; others are as they were."""
+    X, W, y, _ = ce_inputs(T, 64, 500, T, ignored=0.0)
+    X[:, 0] = 0.0
+    W[:, 0] = -3e38
+    d = torch.ones(T, device="cuda")
+    loss, lse = tj2.linear_ce_fwd(X, W, y)
+    dX, _ = tj2.linear_ce_bwd(X, W, y, lse, d)
+    Xm = X.clone()
+    Xm[2] = 0.0
+    Xm[2, 0] = 2.0  # 2 * -3e38: -inf in fp32
+    loss2, lse2 = tj2.linear_ce_fwd(Xm, W, y)
+    dX2, dW2 = tj2.linear_ce_bwd(Xm, W, y, lse2, d)
+    keep = torch.arange(T, device="cuda") != 2
+    assert lse2[2] == -INF and torch.isnan(loss2[2])
+    assert torch.equal(loss[keep], loss2[keep]) and torch.equal(lse[keep], lse2[keep])
+    assert torch.isnan(dX2[2]).all() and torch.equal(dX2[keep], dX[keep]) and torch.isnan(dW2).all()
+    y[2] = -100  # left out, it enters nothing
+    loss2, lse2 = tj2.linear_ce_fwd(Xm, W, y)
+    dX2, dW2 = tj2.linear_ce_bwd(Xm, W, y, lse2, d)
+    assert loss2[2] == 0 and (dX2[2] == 0).all() and torch.isfinite(dW2).all() and torch.equal(dX2[keep], dX[keep])
