@@ -655,8 +655,8 @@ struct CePlans {
   CePlans(int64_t T, int64_t K, int64_t vn)
       : x{product_plan(K, T, vn, false), product_plan(K, T, vn, true)},
         w{product_plan(K, vn, T, false), product_plan(K, vn, T, true)} {}
-  // the tiles, as indexes of x and w
-  void pick(bool dx, bool dw, int& ix, int& iw) const {
+  // the tiles, as indexes of x and w, and the time of those asked for
+  double pick(bool dx, bool dw, int& ix, int& iw) const {
     double least = 1e30;
     for (int i = 0; i < 4; ++i) {
       const double t = (dx ? x[i & 1].time : 0.0) + (dw ? w[i >> 1].time : 0.0) - (dx && dw && (i & 1) == i >> 1 ? 10.0 : 0.0);
@@ -666,6 +666,7 @@ struct CePlans {
         iw = i >> 1;
       }
     }
+    return least;
   }
 };
 
@@ -740,13 +741,6 @@ int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 size_t blocked_bytes(int64_t rows, int64_t cols) { return (size_t)(up(rows, 128) * up(cols, 64) * 2); }
 
-// Vocabulary entries of a piece of the backward (a multiple of 256): dz of a piece
-// has up to 2^28 elements.
-int64_t ce_piece(int64_t T, int64_t V) {
-  const int64_t most = ((int64_t)1 << 28) / std::max<int64_t>(up(T, 64), 1) / 256 * 256;
-  return std::min(up(V, 256), std::max<int64_t>(most, 1024));
-}
-
 // Tokens from which the operands of the logits are copied into blocks first.
 constexpr int64_t kBlockTokens = 2048;
 
@@ -784,6 +778,62 @@ int dx_few_splits(int64_t K, int64_t V) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(32, steps / 16), 4 * kCus / blocks));
 }
 
+// Partial sums of a piece's split products, whichever gradients are asked for.
+size_t split_bytes(const CePlans& plans, int64_t T, int64_t K, int64_t vn, bool few) {
+  size_t part = 0;
+  for (int want = 1; want < 4; ++want) {
+    int ix = 0, iw = 0;
+    plans.pick((want & 1) && !few, want & 2, ix, iw);
+    const int zx = few || !(want & 1) ? 1 : plans.x[ix].splits, zw = want & 2 ? plans.w[iw].splits : 1;
+    part = std::max(part, (zx > 1 ? (size_t)zx * (size_t)(T * K * 4) : 0) + (zw > 1 ? (size_t)zw * (size_t)(vn * K * 4) : 0));
+  }
+  return part;
+}
+
+// Vocabulary entries of a piece of the backward (a multiple of 256).  What the workspace
+// holds of a piece - dz twice, 4 bytes a logit, copies of its rows of W and the split
+// products' sums - takes at most half of what bf16 logits of all entries would, though 384
+// MiB may always be used and never more than 1 GiB, and 1024 entries are taken in any case.
+// Each piece costs launches, a read and write of dX's sums and rounds of tiles that it
+// leaves partly idle, so of the sizes from the largest to its half the one of the least
+// estimated time is taken.  Backward with this rule, and with pieces of 2^28 logits
+// whatever they take: 16384 x 50304 over 1024 5.01 ms in 772 MB, 4.78 in 1313; 5000 x
+// 50304 1.75 ms in 395 MB, 1.72 in 1602; 4096 x 50304 1.32 ms in 436 MB, 1.31 in 1134;
+// 9000 x 20000 over 512 0.87 ms in 407 MB, 0.72 in 958; 1024 x 131072 over 4096 3.47 ms in
+// 294 MB, 3.20 in 1703; 1235 x 32003 over 528 is one piece in both.
+int64_t ce_piece(int64_t T, int64_t K, int64_t V) {
+  const int64_t all = (V + 255) / 256;
+  if (T <= 64) return all * 256;  // dX of few tokens takes W at once; dz takes 384 bytes an entry
+  const int64_t entry = 2 * (up(T, 128) + up(T, 64) + up(K, 128) + (T >= kBlockTokens ? up(K, 64) : 0));
+  const int64_t room = std::clamp<int64_t>(T * V, (int64_t)3 << 27, (int64_t)1 << 30);
+  const int64_t most = std::min(all, std::max<int64_t>(room / (256 * entry), 4));
+  struct Cost {
+    double time;
+    size_t split;
+  };
+  auto cost = [&](int64_t vn) {
+    const double chunks = (double)((K + 63) / 64);
+    const CePlans plans(T, K, vn);
+    int ix = 0, iw = 0;
+    return Cost{std::min(tile_time(true, tiles_of(vn, T, 256), chunks, 9.0), tile_time(false, tiles_of(vn, T, 128), chunks, 9.0)) +
+                    plans.pick(true, true, ix, iw) + 20.0 + (double)(T * K) * 8.0 / 5e6,
+                split_bytes(plans, T, K, vn, false)};
+  };
+  int64_t best = 4;
+  double least = 1e30;
+  for (int64_t n = most; n >= std::max<int64_t>((most + 1) / 2, 4); n -= std::max<int64_t>(1, most / 32)) {
+    const int64_t whole = V / (n * 256), rest = V - whole * n * 256;
+    const Cost a = cost(std::min(n * 256, V)), b = rest && whole ? cost(rest) : Cost{0.0, 0};
+    if ((size_t)(n * 256 * entry) + std::max(a.split, b.split) > (size_t)room) continue;
+    if (n == all) return n * 256;
+    if (const double time = (double)std::max<int64_t>(whole, 1) * a.time + b.time; time < least) {
+      least = time;
+      best = n;
+    }
+  }
+  return std::min(best, all) * 256;
+}
+
 struct CeBwdSpace {
   size_t c, top, xb, xt, wb, wt, d, dt, dx, part, bytes;
   int64_t piece;
@@ -792,7 +842,7 @@ struct CeBwdSpace {
 CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   CeBwdSpace s;
   s.few = dx_few(T, K, V);
-  s.piece = ce_piece(T, V);  // all of V for few tokens
+  s.piece = ce_piece(T, K, V);
   s.blocked = T >= kBlockTokens;
   size_t at = 0;
   auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
@@ -804,20 +854,11 @@ CeBwdSpace ce_bwd_space(int64_t T, int64_t K, int64_t V) {
   s.wt = take(s.few ? 0 : blocked_bytes(K, s.piece));
   s.d = take(blocked_bytes(T, s.piece));
   s.dt = take(blocked_bytes(s.piece, T));
-  s.dx = take((size_t)(T * K * 4));
-  // partial sums of split products, of a whole piece and of the last one, whichever
-  // gradients are asked for
+  s.dx = take(s.piece < V ? (size_t)(T * K * 4) : 0);
+  // partial sums of split products, of a whole piece and of the last one
   size_t part = 0;
-  for (const int64_t vn : {s.piece, V % s.piece}) {
-    if (!vn) continue;
-    const CePlans plans(T, K, vn);
-    for (int want = 1; want < 4; ++want) {
-      int ix = 0, iw = 0;
-      plans.pick((want & 1) && !s.few, want & 2, ix, iw);
-      const int zx = s.few || !(want & 1) ? 1 : plans.x[ix].splits, zw = want & 2 ? plans.w[iw].splits : 1;
-      part = std::max(part, (zx > 1 ? (size_t)zx * (size_t)(T * K * 4) : 0) + (zw > 1 ? (size_t)zw * (size_t)(vn * K * 4) : 0));
-    }
-  }
+  for (const int64_t vn : {std::min(s.piece, V), V % s.piece})
+    if (vn) part = std::max(part, split_bytes(CePlans(T, K, vn), T, K, vn, s.few));
   if (s.few) part += (size_t)dx_few_splits(K, V) * (size_t)(T * K * 4);
   s.part = take(part);
   s.bytes = at;

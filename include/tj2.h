@@ -628,7 +628,7 @@ size_t mxfp4_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
  *
  * Cross entropy of the logits z = X W^T, X [T, K] (tokens' final states) and W
  * [V, K] (the head) bf16 with rows ldx and ldw elements apart (multiples of 8),
- * against one target per token, without the logits in memory.  K a multiple of
+ * against one target per token, without the logits [T, V] in memory.  K a multiple of
  * 16; T, V, K, ldx, ldw at most 2^21.
  *
  * tj2_linear_ce_fwd: lse[t] = log sum_v exp z[t, v] (fp32 [T], saved for the
@@ -655,7 +655,12 @@ size_t tj2_linear_ce_fwd_workspace_size(int64_t T, int64_t K, int64_t V);
  * is taken in pieces; dz of a piece is rounded to bf16, divided by the largest
  * |dloss|, for the two products, whose sums are fp32 (an infinite dloss makes every
  * gradient NaN).  The results do not depend on scheduling.  workspace:
- * tj2_linear_ce_bwd_workspace_size(T, K, V) bytes, 16-byte aligned, required.
+ * tj2_linear_ce_bwd_workspace_size(T, K, V) bytes, 16-byte aligned, required; the
+ * same whichever gradients are asked for.  It holds copies of X and the fp32 sums
+ * of dX (up to 8 bytes an element of X), and of a piece dz, copies of its rows of W
+ * and partial sums: half of what bf16 logits [T, V] would take at most, though up to
+ * 384 MiB in any case and never above 1 GiB (if 1024 vocabulary entries take no more;
+ * up to 64 tokens take the vocabulary at once, 384 bytes an entry).
  */
 tj2_status tj2_linear_ce_bwd(const void* X, int64_t ldx, const void* W, int64_t ldw, const int64_t* targets, int64_t T,
                              int64_t K, int64_t V, int64_t ignore_index, const float* lse, const float* dloss, void* dX,

@@ -6,7 +6,7 @@ pytestmark = pytest.mark.gpu
 
 tj2 = pytest.importorskip("bit_fully_quantized_amd")
 
-from test_gpu_losses import H8, H24, INF, ce_inputs  # noqa: E402
+from test_gpu_losses import H8, H24, INF, ce_check, ce_inputs  # noqa: E402
 
 
 @pytest.mark.parametrize("T", [1, 5, 16, 33, 64, 65, 300])
@@ -66,3 +66,19 @@ def test_cross_entropy_token_with_no_entry_left(T):
     loss2, lse2 = tj2.linear_ce_fwd(Xm, W, y)
     dX2, dW2 = tj2.linear_ce_bwd(Xm, W, y, lse2, d)
     assert loss2[2] == 0 and (dX2[2] == 0).all() and torch.isfinite(dW2).all() and torch.equal(dX2[keep], dX[keep])
+
+
+@pytest.mark.parametrize("T,K,V", [(65, 48, 800000), (130, 144, 400001), (1100, 272, 90001), (2047, 80, 60000), (2048, 80, 60001),
+                                   (5000, 208, 30011), (4100, 1040, 24001)])
+def test_cross_entropy_pieces_of_every_layout(T, K, V):
+    """Vocabularies taken in several pieces with and without blocked copies, split and unsplit, W also with rows apart."""
+    # dz twice and the copies of W, of all entries, are more than a piece's share of the workspace
+    up = lambda n, m: -(-n // m) * m  # noqa: E731
+    assert 2 * (up(T, 128) + up(T, 64) + up(K, 128) + (up(K, 64) if T >= 2048 else 0)) * V > max(3 << 27, T * V)
+    X, W, y, g = ce_inputs(T, K, V, T + K, ignored=0.05)
+    d = torch.rand(T, generator=g, device="cuda") - 0.3
+    _, lse, dX, dW = ce_check(X, W, y, d)
+    Wp = torch.full((V, K + 8), float("nan"), device="cuda", dtype=torch.bfloat16)
+    Wp[:, :K] = W
+    got = tj2.linear_ce_bwd(X, Wp[:, :K], y, lse, d)
+    assert torch.equal(got[0], dX) and torch.equal(got[1], dW)
