@@ -1281,7 +1281,7 @@ __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distil
   block_reduce<WAVES>(top, sh_max, MaxOp{});
   m = top[0];
   const float mu = top[1];
-  const bool some = mu != -INFINITY;  // the teacher kept something of this row
+  const bool some = mu != -INFINITY && p.alpha > 0.0f;  // the teacher kept something of this row, and it counts
   const float ctau = kLog2e / p.tau;
   // sums: exp(z / tau), exp(z), the teacher's exp(u), and sum of those times
   // (u - mu) - (z - m) / tau, of which the divergence is made

@@ -6,7 +6,9 @@ pytestmark = pytest.mark.gpu
 
 tj2 = pytest.importorskip("bit_fully_quantized_amd")
 
-from test_gpu_losses import H8, H24, INF, ce_check, ce_inputs  # noqa: E402
+from test_gpu_losses import H8, H24, INF, NAN, ce_check, ce_inputs, distill_inputs  # noqa: E402
+
+BF16, F32 = torch.bfloat16, torch.float32
 
 
 @pytest.mark.parametrize("T", [1, 5, 16, 33, 64, 65, 300])
@@ -82,3 +84,14 @@ def test_cross_entropy_pieces_of_every_layout(T, K, V):
     Wp[:, :K] = W
     got = tj2.linear_ce_bwd(X, Wp[:, :K], y, lse, d)
     assert torch.equal(got[0], dX) and torch.equal(got[1], dW)
+
+
+# ---- distillation ---------------------------------------------------------------------------------------------
+def test_distill_teacher_without_weight_enters_nothing():
+    """alpha 0: whatever the teacher's logits are, infinities and NaN too."""
+    z, ids, u, y, w = distill_inputs(9, 200, 5, F32, 12)
+    opt = dict(alpha=0.0, targets=y, weight=w, grad=True)
+    loss, dz = tj2.distill_topk(z, ids, u, **opt)
+    u[0], u[1, 2], u[2, 0], u[3] = NAN, NAN, INF, -INF
+    got = tj2.distill_topk(z, ids, u, **opt)
+    assert torch.isfinite(loss).all() and torch.equal(got[0], loss) and torch.equal(got[1], dz)
