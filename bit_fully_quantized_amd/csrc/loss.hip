@@ -1309,13 +1309,13 @@ __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distil
     }
     sum[2] = eu;
     pr[t] = eu;
-    if (my >= V) sum[3] = kNan;  // an id outside the vocabulary makes the row NaN
+    if (my >= V) sum[3] = kNan;  // an id outside the vocabulary makes the row NaN, also where no teacher's term is taken
   }
   block_reduce<WAVES>(sum, sh_sum, SumOp{});
   const float st = sum[0], s1 = sum[1], su = sum[2];
   // sum p (log p - log q) = sum p ((u - mu) - (z - m) / tau) - log su + log st
   const float kl = some ? sum[3] / su + (__builtin_amdgcn_logf(st) - __builtin_amdgcn_logf(su)) * kLn2 : sum[3];
-  float loss = p.alpha > 0.0f ? p.alpha * p.tau * p.tau * kl : 0.0f;
+  float loss = p.alpha > 0.0f ? p.alpha * p.tau * p.tau * kl : kl;  // (0 or NaN)
   if constexpr (HARD) loss += (1.0f - p.alpha) * (m + __builtin_amdgcn_logf(s1) * kLn2 - keep_target);
   if (t == 0 && p.loss) p.loss[row] = loss;
   if (!dz) return;

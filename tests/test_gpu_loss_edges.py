@@ -87,6 +87,22 @@ def test_cross_entropy_pieces_of_every_layout(T, K, V):
 
 
 # ---- distillation ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("alpha", [1.0, 0.5, 0.0])
+def test_distill_id_outside_is_nan(alpha):
+    """An id of V or more makes its token NaN, whatever the weight of the teacher's term; an ignored token stays 0."""
+    z, ids, u, y, w = distill_inputs(6, 100, 4, F32, 2)
+    ids[:] = torch.arange(4, device="cuda", dtype=torch.int32)
+    y[:] = 3
+    ids[1, 2] = 100
+    ids[4, 0] = 2 ** 31 - 1
+    ids[5, 1] = 100
+    y[5] = -100
+    loss, dz = tj2.distill_topk(z, ids, u, alpha=alpha, targets=y, weight=w, grad=True)
+    bad = torch.tensor([False, True, False, False, True, False], device="cuda")
+    assert torch.equal(torch.isnan(loss), bad) and torch.equal(torch.isnan(dz).any(1), bad)
+    assert torch.isnan(dz[bad]).all() and loss[5] == 0 and (dz[5] == 0).all()
+
+
 def test_distill_teacher_without_weight_enters_nothing():
     """alpha 0: whatever the teacher's logits are, infinities and NaN too."""
     z, ids, u, y, w = distill_inputs(9, 200, 5, F32, 12)
