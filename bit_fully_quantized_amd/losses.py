@@ -159,17 +159,17 @@ def distill_topk(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
 class _Distill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, teacher, temperature, alpha, targets, ignore_index):
-        ctx.args = dict(temperature=temperature, alpha=alpha, targets=targets, ignore_index=ignore_index)
-        ctx.save_for_backward(logits, ids, teacher)
-        return distill_topk(logits, ids, teacher, **ctx.args)
+        ctx.args = dict(temperature=temperature, alpha=alpha, ignore_index=ignore_index)
+        ctx.save_for_backward(logits, ids, teacher, targets)
+        return distill_topk(logits, ids, teacher, targets=targets, **ctx.args)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dloss):
         if not ctx.needs_input_grad[0]:
             return (None,) * 7
-        logits, ids, teacher = ctx.saved_tensors
-        _, dz = distill_topk(logits, ids, teacher, weight=dloss.contiguous(), grad=True, **ctx.args)
+        logits, ids, teacher, targets = ctx.saved_tensors
+        _, dz = distill_topk(logits, ids, teacher, targets=targets, weight=dloss.contiguous(), grad=True, **ctx.args)
         return (dz,) + (None,) * 6
 
 

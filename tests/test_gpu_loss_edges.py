@@ -111,3 +111,12 @@ def test_distill_teacher_without_weight_enters_nothing():
     u[0], u[1, 2], u[2, 0], u[3] = NAN, NAN, INF, -INF
     got = tj2.distill_topk(z, ids, u, **opt)
     assert torch.isfinite(loss).all() and torch.equal(got[0], loss) and torch.equal(got[1], dz)
+
+
+def test_distillation_notices_targets_changed_before_the_backward():
+    z, ids, u, y, _ = distill_inputs(8, 60, 4, F32, 11)
+    a = z.clone().requires_grad_()
+    out = tj2.distillation_loss(a, ids, u, alpha=0.5, targets=y)
+    y.fill_(1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        out.backward()
