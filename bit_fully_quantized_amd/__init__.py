@@ -102,8 +102,9 @@ class QTensor:
         return self.__dict__[name]
 
     def storage(self) -> torch.Tensor:
-        """The tensor the operand starts in: its one allocation as long as the arrays were not asked for."""
-        return self.__dict__.get("codes", self.buffer)
+        """The tensor the operand starts in: its one allocation as long as no array was asked for or replaced."""
+        at = self.__dict__
+        return self.codes if "codes" in at or "scale16" in at else self.buffer
 
     @staticmethod
     def wrap(fmt: int, rows: int, length: int, codes: torch.Tensor, scale16: torch.Tensor | None,
@@ -125,7 +126,7 @@ class QTensor:
         return q
 
     def c(self) -> _lib.QTensorC:
-        if "codes" not in self.__dict__:
+        if "codes" not in self.__dict__ and "scale16" not in self.__dict__:
             at = self.buffer.data_ptr()
             return _lib.QTensorC(at, at + self.rows * self.nb * 64, 0, self.rows, self.len, self.fmt, 0)
         return _lib.QTensorC(self.codes.data_ptr(), 0 if self.scale16 is None else self.scale16.data_ptr(),
