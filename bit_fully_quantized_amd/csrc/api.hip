@@ -1314,7 +1314,8 @@ tj2_status tj2_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_
   if (k <= 0 || k > distill_max_k()) return fail(TJ2_ERR_SHAPE, "k = %d must be from 1 to %d", k, distill_max_k());
   if (ldl < V || (dlogits && ldd < V)) return fail(TJ2_ERR_SHAPE, "rows of logits and dlogits must be at least V apart");
   if (dlogits == logits && ldd != ldl) return fail(TJ2_ERR_SHAPE, "dlogits in place of logits needs the same row pitch");
-  if (!(temperature > 0.0f) || isinf(temperature)) return fail(TJ2_ERR_ARG, "temperature must be positive and finite");
+  // (beyond, its square or the reciprocal leaves fp32, and with it the loss)
+  if (!(temperature >= 0x1p-64f && temperature <= 0x1p63f)) return fail(TJ2_ERR_ARG, "temperature must be from 2^-64 to 2^63");
   if (!(alpha >= 0.0f && alpha <= 1.0f)) return fail(TJ2_ERR_ARG, "alpha must be from 0 to 1");
   if (alpha != 1.0f && !targets) return fail(TJ2_ERR_ARG, "alpha below 1 needs targets");
   const uintptr_t es = dtype == TJ2_BF16 ? 2 : 4;

@@ -672,8 +672,9 @@ size_t tj2_linear_ce_bwd_workspace_size(int64_t T, int64_t K, int64_t V);
  * TJ2_F32, rows ldl elements apart, aligned to their elements); ids [T, k] the
  * teacher's kept entries (a negative id stands for none, so rows may keep fewer
  * than k; an entry listed twice counts twice) and teacher [T, k] their logits
- * (dtype's type), 1 <= k <= 512.  With tau = temperature, p = softmax of the kept
- * teacher logits / tau, q_tau = softmax(logits / tau) over the whole vocabulary:
+ * (dtype's type), 1 <= k <= 512.  With tau = temperature (2^-64 to 2^63), p = softmax
+ * of the kept teacher logits / tau, q_tau = softmax(logits / tau) over the whole
+ * vocabulary:
  *   loss[t]       = alpha tau^2 sum_j p_j (log p_j - log q_tau[id_j])
  *                   + (1 - alpha) (-log q_1[targets[t]])
  *   dlogits[t, v] = weight[t] (alpha tau (q_tau[v] - sum_{id_j = v} p_j)
@@ -682,9 +683,10 @@ size_t tj2_linear_ce_bwd_workspace_size(int64_t T, int64_t K, int64_t V);
  * == ldl) may be NULL; weight (fp32 [T], NULL: 1) is the gradient of each token's
  * loss.  targets may be NULL if alpha is 1; a token with targets[t] ==
  * ignore_index has loss and gradient 0 whatever its logits.  A row of which the
- * teacher kept nothing has no teacher's term.  An id of V or more, or a target
- * outside the vocabulary that is used (alpha < 1), gives NaN.  Logits of -inf
- * have probability 0.
+ * teacher kept nothing has no teacher's term (nor has any if alpha is 0, whatever
+ * the teacher's logits are).  An id of V or more, or a target outside the vocabulary
+ * that is used (alpha < 1), gives NaN.  Logits of -inf have probability 0.
+ * Statistics are fp32.
  */
 tj2_status tj2_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ldl, const int32_t* ids,
                             const void* teacher, int32_t k, float temperature, float alpha, const int64_t* targets,
