@@ -589,8 +589,14 @@ TileOp mx_operand(const QView& q, bool blocked) {
 
 // Rows of A that mx_few_kernel takes: one instruction tile (with more, the 64 x 64
 // tiles are as fast: 24 x 50304 over 1024 11.8 us here and 9.8 there, 64 x 4096 9.2 and
-// 5.3; 1 x 4096 4.5 and 5.0, and the quantization of A included).
-using Few = Skinny<EL_MX, 1, 64 * 1024>;
+// 5.3), over up to 2048 elements, whose codes fit this LDS.  Beyond, every workgroup's
+// quantization of all of A and a wave's way through whole rows of B take longer than
+// tiles, which split the reduction.  Linear forward of 1 row here and in tiles with the
+// quantization's launch, N 4096: over 256 3.5 and 5.5 us, 1024 4.9 and 6.7, 2048 7.8 and
+// 8.7, 3968 13.0 and 10.0, 7936 24.4 and 12.0; N 50304: 1024 9.4 and 10.1, 2048 17.3 and
+// 15.0, 3968 28.9 and 24.1.  16 rows, N 4096: 1024 5.7 and 7.4, 2048 9.7 and 9.7.
+using Few = Skinny<EL_MX, 1, 17 * 1024>;
+static_assert(Few::TOKENS * (2048 / 2 + 16) <= 17 * 1024 && Few::TOKENS * (2048 / 2 + 128 + 16) > 17 * 1024, "2048 elements");
 
 // Tile and splits of a product, by an estimate of its time from what the tiles
 // measure (us on MI355X; a chunk is 256 elements of the reduction): alone on its CU
