@@ -12,7 +12,8 @@
 //
 // Distillation from a teacher's top logits, on logits that are in memory (the head
 // may be quantized): one workgroup a token, which keeps the row in registers, so
-// logits are read once and the gradient is written once.
+// logits are read once and the gradient is written once (rows that no registers hold
+// are read three times: launch_distill_r).
 #include <math.h>
 
 #include <algorithm>
@@ -131,7 +132,12 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ce_fwd_kernel(CeArgs p) {
 
 // The same for up to 64 tokens (scoring): one read of W, each lane's part of a token's
 // sum kept over the wave's groups of 16 entries, one part a workgroup and token.  5 x
-// 50304 over 1024 in 23 us, 4.5 TB/s of W (50 in tiles).
+// 50304 over 1024 in 23 us, 4.5 TB/s of W.  Taken where the tokens fit the LDS: 16 over
+// up to 2048 elements, 32 over 1024, 64 over 512.  Forward here and in tiles, join
+// included, us: 5 tokens of 8000 x 1024 11.7 and 16.9, of 152000 x 1024 (W from memory)
+// 56 and 70, 16 of 152000 x 2048 128 and 155, 64 of 152000 x 512 41.6 and 41.7; of W that
+// the last cache holds from the call before, tiles catch up: 5 of 50304 x 1024 26.1 and
+// 25.6, 32 of it 31.8 and 26.1, 64 of 50304 x 512 25.6 and 19.7.
 template <class S, int TN>
 __global__ __launch_bounds__(S::NT, 2) void ce_few_kernel(CeArgs p) {
   __shared__ typename S::Smem sm;
@@ -227,11 +233,16 @@ __global__ __launch_bounds__(L * S) void ce_join_kernel(const float2* part, int 
   }
 }
 
-// dz of a tile in bf16, both ways: 16384 x 16384 over 1024 in 570 to 600 us, of which the
-// product takes some 460 and the 1.07 GB of dz the rest.  The exponential is clamped to [0, 1], which costs
-// nothing (an output modifier) and holds where the fused v c - r overflows; it turns a
-// NaN into 0, so a token whose lse is NaN, or -inf (all its logits are), gets a NaN weight
-// instead.
+// dz of a tile in bf16, both ways: 16384 x 8192 over 1024 in 290 us (16384 in 570 to 600),
+// of which the product takes some 80% and the 4 bytes a logit the rest.
+// bf16, the type of X and W, because the two products run on bf16 instructions: a third
+// operand of more bits would double their work.  Each entry is off by half a step, 2^-8
+// of itself, at most: the gradients of 16384 x 50304 in bf16 are then 2.0e-3 of their norm
+// from the exact ones, and 1.7e-3 with dz in fp32.  Gradients asked for in fp32 have this
+// dz too.
+// The exponential is clamped to [0, 1], which costs nothing (an output modifier) and holds
+// where the fused v c - r overflows; it turns a NaN into 0, so a token whose lse is NaN, or
+// -inf (all its logits are), gets a NaN weight instead.
 template <class T>
 __global__ __launch_bounds__(T::NT, T::WAVES) void ce_dz_kernel(CeArgs p) {
   static_assert(T::kTN == 4 && T::PB == 4, "64 tokens, and entries 16 a lane");
@@ -438,8 +449,9 @@ struct ProductArgs {
   int32_t bf16;
 };
 
-// One product or both of a piece: 16384 x 1024 over 16384 in 430 to 500 us, 1.10 to 1.28
-// PFLOP/s, the faster the cooler the GPU starts (2.0 GHz at first, 1.75 after some).
+// One product or both of a piece: both of 16384 x 8192 over 1024 in 490 us, 1.12 PFLOP/s
+// with the sums of dX read and written; 16384 x 1024 over 16384 alone in 430 to 500 us, 1.10
+// to 1.28 PFLOP/s, the faster the cooler the GPU starts (2.0 GHz at first, 1.75 after some).
 template <class T>
 __global__ __launch_bounds__(T::NT, T::WAVES) void ce_product_kernel(Pair<ProductArgs> jobs) {
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
@@ -1363,7 +1375,12 @@ __global__ __launch_bounds__(kThreads, R <= 8 ? 8 : R <= 13 ? 6 : 4) void distil
 }
 
 // Few rows: 1024 threads each, so that one row takes less time; many: 512, of which
-// three rows fit a CU at R = 13 and cover each other's loads and stores.
+// three rows fit a CU at R = 13 and cover each other's loads and stores.  Up to 106496
+// bf16 or 53248 fp32 entries a row stays in registers; beyond (R = 0) it is read for each
+// of the three passes.  Loss and gradient of 16384 bf16 rows: 106496 entries 1335 us (floor
+// 1326), 128256 2376 (1597), 151936 3360 (1891); of 8192 fp32 rows: 53248 650 (663), 60001
+// 1121 (747); of 37 bf16 rows: 106496 19, 128256 24.  Short rows leave threads idle: 16384
+// of 1000 entries 121 us (12).
 template <class T, bool HARD>
 void launch_distill_r(const DistillArgs& a, hipStream_t s) {
   const bool few = a.T < 512;

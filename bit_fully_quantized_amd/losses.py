@@ -1,8 +1,10 @@
 """Losses at the language-model head (tj2_linear_ce_*, tj2_distill_topk of include/tj2.h).
 
-linear_ce_fwd / linear_ce_bwd: cross entropy of X W^T without the logits in memory; linear_cross_entropy
-is the same as a differentiable function.  distill_topk: a student's logits against a teacher's top logits,
-loss and gradient from one read; distillation_loss is its differentiable form.
+linear_ce_fwd / linear_ce_bwd: cross entropy of X W^T without the logits [T, V] in memory (the backward's
+workspace holds their gradient a piece at a time); linear_cross_entropy is the same as a differentiable
+function.  distill_topk: a student's logits against a teacher's top logits, loss and gradient from one read
+(three above 106496 bf16 or 53248 fp32 entries); distillation_loss is its differentiable form, which takes one
+pass for the loss and one in the backward.
 """
 from __future__ import annotations
 
@@ -73,7 +75,8 @@ def linear_ce_bwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, lse: 
                   need_dw: bool = True, workspace: torch.Tensor | None = None):
     """(dX [T, K], dW [V, K]) for dloss, the gradient of each token's loss (fp32 [T]), with lse of linear_ce_fwd.
 
-    need_dx / need_dw False leaves that gradient out (None)."""
+    need_dx / need_dw False leaves that gradient out (None).  dx_dtype and dw_dtype are the results' types; the
+    logits' gradient that both are products of is bf16 (fp32 sums)."""
     index = _tensor(X, "X", 2)
     ldx = _rows(X, "X", _BF16, index)
     T, K = X.shape

@@ -560,7 +560,8 @@ tj2_status tj2_select_outliers(const double* scores, int64_t K, double p, int32_
  *
  * mxfp4_quantize: a logical [rows, cols] tensor, cols a multiple of 16, dense
  * (x_dtype TJ2_BF16 / TJ2_F32, contiguous) or, for TJ2_GROUP_COL, MXFP4
- * (x_dtype TJ2_MXFP4, *x_q grouped along cols, dequantized first; values exact).
+ * (x_dtype TJ2_MXFP4, *x_q grouped along cols, dequantized first; values exact, but
+ * for magnitudes of 2^128 and more, which count as infinite).
  * grouping TJ2_GROUP_ROW: groups along cols, *out is [rows, cols]; TJ2_GROUP_COL:
  * groups along rows, *out is [cols, rows] (transposed).  rows need not be a
  * multiple of 16 or 32; a group at the end of a row may hold fewer than 32.
@@ -653,7 +654,8 @@ size_t tj2_linear_ce_fwd_workspace_size(int64_t T, int64_t K, int64_t V);
  * nothing; NaN for a target outside the vocabulary), dX [T, K] = dz W and dW [V, K]
  * = dz^T X, contiguous, each TJ2_BF16 or TJ2_F32, either may be NULL.  The vocabulary
  * is taken in pieces; dz of a piece is rounded to bf16, divided by the largest
- * |dloss|, for the two products, whose sums are fp32 (an infinite dloss makes every
+ * |dloss|, for the two products, whose sums are fp32, also where fp32 gradients are
+ * asked for: an entry of dz is off by 2^-8 of itself at most (an infinite dloss makes every
  * gradient NaN).  The results do not depend on scheduling.  workspace:
  * tj2_linear_ce_bwd_workspace_size(T, K, V) bytes, 16-byte aligned, required; the
  * same whichever gradients are asked for.  It holds copies of X and the fp32 sums
@@ -668,7 +670,8 @@ tj2_status tj2_linear_ce_bwd(const void* X, int64_t ldx, const void* W, int64_t 
 size_t tj2_linear_ce_bwd_workspace_size(int64_t T, int64_t K, int64_t V);
 
 /*
- * Distillation from a teacher's top logits.  logits [T, V] (dtype TJ2_BF16 or
+ * Distillation from a teacher's top logits; they are read once, or three times where
+ * V is above 106496 (TJ2_BF16) or 53248 (TJ2_F32).  logits [T, V] (dtype TJ2_BF16 or
  * TJ2_F32, rows ldl elements apart, aligned to their elements); ids [T, k] the
  * teacher's kept entries (a negative id stands for none, so rows may keep fewer
  * than k; an entry listed twice counts twice) and teacher [T, k] their logits
