@@ -235,8 +235,8 @@ __global__ __launch_bounds__(L * S) void ce_join_kernel(const float2* part, int 
 
 // dz of a tile in bf16, both ways: 16384 x 8192 over 1024 in 290 us (16384 in 570 to 600),
 // of which the product takes some 80% and the 4 bytes a logit the rest.
-// bf16, the type of X and W, because the two products run on bf16 instructions: a third
-// operand of more bits would double their work.  Each entry is off by half a step, 2^-8
+// bf16, the type of X and W, because the two products run on bf16 instructions: dz in two
+// bf16 terms would double their work.  Each entry is off by half a step, 2^-8
 // of itself, at most: the gradients of 16384 x 50304 in bf16 are then 2.0e-3 of their norm
 // from the exact ones, and 1.7e-3 with dz in fp32.  Gradients asked for in fp32 have this
 // dz too.

@@ -86,6 +86,30 @@ def test_cross_entropy_pieces_of_every_layout(T, K, V):
     assert torch.equal(got[0], dX) and torch.equal(got[1], dW)
 
 
+@pytest.mark.parametrize("T,K,V", [(1100, 272, 90001), (2300, 528, 50001)])
+def test_cross_entropy_pieces_in_a_graph(T, K, V):
+    """A captured backward of several pieces, replayed among eager calls that share its workspace."""
+    X, W, y, g = ce_inputs(T, K, V, T, ignored=0.05)
+    d = torch.rand(T, generator=g, device="cuda") / T
+    _, lse = tj2.linear_ce_fwd(X, W, y)
+    want = tj2.linear_ce_bwd(X, W, y, lse, d)
+    ws = torch.empty(int(tj2.lib().tj2_linear_ce_bwd_workspace_size(T, K, V)), dtype=torch.uint8, device="cuda")
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    graph, weights = torch.cuda.CUDAGraph(), d.clone()
+    with torch.cuda.graph(graph):
+        tj2.linear_ce_bwd(X, W, y, lse, weights, dX=dX, dW=dW, workspace=ws)
+    for k in (1, 2, 3):
+        dX.fill_(float("nan"))
+        dW.fill_(float("nan"))
+        weights.copy_(d * 2.0 ** k)  # dz is over the largest weight: a power of two scales the results exactly
+        graph.replay()
+        other = tj2.linear_ce_bwd(X, W, y, lse, d, workspace=ws, need_dw=False)[0]
+        torch.cuda.synchronize()
+        assert torch.equal(dX, want[0] * 2.0 ** k) and torch.equal(dW, want[1] * 2.0 ** k)
+        # (dX by itself may be summed in an order of its own: two fp32 sums, each rounded once)
+        assert float((other - want[0]).float().norm() / want[0].float().norm()) <= H8
+
+
 # ---- distillation ---------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("alpha", [1.0, 0.5, 0.0])
 def test_distill_id_outside_is_nan(alpha):
