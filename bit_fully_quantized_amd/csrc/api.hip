@@ -1103,6 +1103,9 @@ tj2_status mxfp4_quantize(const void* x, int32_t x_dtype, const tj2_qtensor* x_q
                           uint64_t offset, tj2_qtensor* out, void* stream) {
   TJ2_TRY(check_mx_input(x, x_dtype, x_q, rows, cols, grouping, rounding));
   TJ2_TRY(grouping == TJ2_GROUP_ROW ? check_mx(out, "out", rows, cols) : check_mx(out, "out", cols, rows));
+  // (the transposed groups are written while others are still read)
+  if (x_dtype == TJ2_MXFP4 && (out->codes == x_q->codes || out->scale16 == x_q->scale16))
+    return fail(TJ2_ERR_ARG, "out must not be x_q");
   TJ2_TRY(hip_check(launch_mx_quant(mx_quant_params(x, x_dtype, x_q, rows, cols, grouping, rounding, rht, rht_signs, seed, offset, out),
                                     (hipStream_t)stream),
                     "MXFP4 quantize launch"));

@@ -561,7 +561,7 @@ tj2_status tj2_select_outliers(const double* scores, int64_t K, double p, int32_
  * mxfp4_quantize: a logical [rows, cols] tensor, cols a multiple of 16, dense
  * (x_dtype TJ2_BF16 / TJ2_F32, contiguous) or, for TJ2_GROUP_COL, MXFP4
  * (x_dtype TJ2_MXFP4, *x_q grouped along cols, dequantized first; values exact, but
- * for magnitudes of 2^128 and more, which count as infinite).
+ * for magnitudes of 2^128 and more, which count as infinite; *out must not be *x_q).
  * grouping TJ2_GROUP_ROW: groups along cols, *out is [rows, cols]; TJ2_GROUP_COL:
  * groups along rows, *out is [cols, rows] (transposed).  rows need not be a
  * multiple of 16 or 32; a group at the end of a row may hold fewer than 32.

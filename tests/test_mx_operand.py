@@ -35,3 +35,15 @@ def test_one_array_replaced(name):
     other.codes = torch.ones(3, 128, dtype=torch.uint8)
     other.scale16 = torch.ones(3, 8, dtype=torch.uint8)
     assert pointers(other) == (other.codes.data_ptr(), other.scale16.data_ptr())
+
+
+def test_regrouping_into_its_own_arrays_is_refused():
+    import ctypes
+    from bit_fully_quantized_amd import _lib
+    L = _lib.lib()
+
+    def run(codes, scales):
+        x, out = _lib.QTensorC(0x10000, 0x20000, 0, 64, 64, _lib.MXFP4, 0), _lib.QTensorC(codes, scales, 0, 64, 64, _lib.MXFP4, 0)
+        return L.mxfp4_quantize(None, _lib.MXFP4, ctypes.byref(x), 64, 64, 1, 0, 0, 0, 0, 0, ctypes.byref(out), None)
+    for codes, scales in ((0x10000, 0x20000), (0x10000, 0x30000), (0x30000, 0x20000)):
+        assert run(codes, scales) == _lib.TJ2_ERR_ARG and b"x_q" in L.tj2_last_error()
