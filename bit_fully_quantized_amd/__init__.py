@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import (BF16, F32, FP8, GROUP_COL, GROUP_ROW, MXFP4, NVFP4, NVFP6, OSCI_ACCUM, OSCI_INIT, OSCI_WINDOW_END, RISK_BINS, RTN,
+from ._lib import (BF16, F32, FP8, FP8_BLOCK, GROUP_COL, GROUP_ROW, MXFP4, NVFP4, NVFP6, OSCI_ACCUM, OSCI_INIT, OSCI_WINDOW_END, RISK_BINS, RTN,
                    SR, Tj2Error, check, lib)
 
 __all__ = ["QTensor", "OutlierPlan", "quantize", "gemm", "gemm_workspace", "linear_fwd", "linear_fwd_workspace",
@@ -25,7 +25,9 @@ __all__ = ["QTensor", "OutlierPlan", "quantize", "gemm", "gemm_workspace", "line
            "RTN", "SR", "OSCI_INIT", "OSCI_ACCUM", "OSCI_WINDOW_END", "RISK_BINS",
            "mx_quantize", "mx_dequantize", "mx_gemm", "mx_gemm_workspace", "mx_linear_fwd", "mx_linear_bwd",
            "mx_linear_bwd_workspace", "linear_ce_fwd", "linear_ce_bwd", "linear_cross_entropy", "distill_topk",
-           "distillation_loss"]
+           "distillation_loss",
+           "FP8_BLOCK", "fp8_quantize", "fp8_dequantize", "fp8_gemm", "fp8_gemm_workspace", "fp8_linear_fwd", "fp8_linear_bwd",
+           "fp8_linear_bwd_workspace", "rms_norm_fwd", "rms_norm_bwd", "rms_norm"]
 
 
 def _stream():
@@ -71,7 +73,7 @@ class QTensor:
 
     codes    uint8 [rows, nb*64] (NVFP4, MXFP4) or [rows, nb*128] (FP8, NVFP6), nb = ceil(len/128)
     scale16  uint8 [rows, nb*8] E4M3 (NVFP4, NVFP6); MXFP4: [rows, nb*4], 2^(byte - 127) per 32
-    scale128 float32 [rows, nb] (not MXFP4)
+    scale128 float32 [rows, nb] (not MXFP4); FP8_BLOCK: codes as FP8, [ceil(rows/128), nb], one per 128 x 128
     """
 
     def __init__(self, fmt: int, rows: int, length: int, device="cuda"):
@@ -87,16 +89,41 @@ class QTensor:
             self.buffer = torch.empty(rows * nb * 68, dtype=torch.uint8, device=device)
             self.scale128 = None
             return
+        if fmt == FP8_BLOCK:
+            self._pack(device)
+            return
         self.codes = torch.empty((rows, nb * (64 if fmt == NVFP4 else 128)), dtype=torch.uint8, device=device)
         self.scale16 = torch.empty((rows, nb * 8), dtype=torch.uint8, device=device) if fmt != FP8 else None
         self.scale128 = torch.empty((rows, nb), dtype=torch.float32, device=device)
 
     buffer = None
 
+    def _pack(self, device):
+        self.scale16 = None
+        self.buffer = torch.empty(self.rows * self.nb * 128 + self._scales() * 4, dtype=torch.uint8, device=device)
+
+    def _scales(self) -> int:
+        return (self.rows if self.fmt == FP8 else (self.rows + 127) // 128) * self.nb
+
+    @staticmethod
+    def packed(fmt: int, rows: int, length: int, device="cuda") -> "QTensor":
+        """An FP8 or FP8_BLOCK operand in one allocation."""
+        if fmt not in (FP8, FP8_BLOCK) or length % 16 or length <= 0 or rows <= 0:
+            raise ValueError("FP8 or FP8_BLOCK, len a positive multiple of 16 and rows positive")
+        q = QTensor.__new__(QTensor)
+        q.fmt, q.rows, q.len, q.nb = fmt, rows, length, (length + 127) // 128
+        q._pack(device)
+        return q
+
     def __getattr__(self, name):
-        if self.buffer is None or name not in ("codes", "scale16"):
+        if self.buffer is None or name not in ("codes", "scale16", "scale128"):
             raise AttributeError(name)
         n = self.rows * self.nb
+        if self.fmt != MXFP4:
+            m = self._scales()
+            self.__dict__.setdefault("codes", self.buffer[: n * 128].view(self.rows, -1))
+            self.__dict__.setdefault("scale128", self.buffer[n * 128: n * 128 + m * 4].view(torch.float32).view(-1, self.nb))
+            return self.__dict__[name]
         for key, t in zip(("codes", "scale16"), self.buffer.split((n * 64, n * 4))):
             self.__dict__.setdefault(key, t.view(self.rows, -1))
         return self.__dict__[name]
@@ -104,6 +131,8 @@ class QTensor:
     def storage(self) -> torch.Tensor:
         """The tensor the operand starts in: its one allocation as long as no array was asked for or replaced."""
         at = self.__dict__
+        if self.fmt != MXFP4:
+            return self.buffer if self.buffer is not None and "codes" not in at and "scale128" not in at else self.codes
         return self.codes if "codes" in at or "scale16" in at else self.buffer
 
     @staticmethod
@@ -114,18 +143,23 @@ class QTensor:
         nb = (length + 127) // 128
         if rows <= 0 or length <= 0 or (fmt != MXFP4 and length % 16):
             raise ValueError("rows must be positive and len a positive multiple of 16 (MXFP4: any positive length)")
-        if fmt not in (NVFP4, FP8, NVFP6, MXFP4):
+        if fmt not in (NVFP4, FP8, NVFP6, MXFP4, FP8_BLOCK):
             raise ValueError(f"bad format {fmt}")
         u8, f32 = (torch.uint8,), (torch.float32,)
         _dense(codes, "codes", u8, shape=(rows, nb * (64 if fmt in (NVFP4, MXFP4) else 128)))
-        _dense(scale16, "scale16", u8, shape=(rows, nb * (4 if fmt == MXFP4 else 8)), optional=fmt == FP8)
-        _dense(scale128, "scale128", f32, shape=(rows, nb), optional=fmt == MXFP4)
+        _dense(scale16, "scale16", u8, shape=(rows, nb * (4 if fmt == MXFP4 else 8)), optional=fmt in (FP8, FP8_BLOCK))
+        _dense(scale128, "scale128", f32, shape=((rows + 127) // 128 if fmt == FP8_BLOCK else rows, nb), optional=fmt == MXFP4)
         q = QTensor.__new__(QTensor)
         q.fmt, q.rows, q.len, q.nb = fmt, rows, length, nb
         q.codes, q.scale16, q.scale128 = codes, scale16, scale128
         return q
 
     def c(self) -> _lib.QTensorC:
+        if self.fmt in (FP8, FP8_BLOCK):
+            if self.buffer is not None and "codes" not in self.__dict__ and "scale128" not in self.__dict__:
+                at = self.buffer.data_ptr()
+                return _lib.QTensorC(at, 0, at + self.rows * self.nb * 128, self.rows, self.len, self.fmt, 0)
+            return _lib.QTensorC(self.codes.data_ptr(), 0, self.scale128.data_ptr(), self.rows, self.len, self.fmt, 0)
         if "codes" not in self.__dict__ and "scale16" not in self.__dict__:
             at = self.buffer.data_ptr()
             return _lib.QTensorC(at, at + self.rows * self.nb * 64, 0, self.rows, self.len, self.fmt, 0)
@@ -648,3 +682,6 @@ from .mx import (mx_dequantize, mx_gemm, mx_gemm_workspace, mx_linear_bwd, mx_li
                  mx_linear_fwd, mx_quantize)
 from .losses import (distill_topk, distillation_loss, linear_ce_bwd, linear_ce_fwd,  # noqa: E402
                      linear_cross_entropy)
+from .fp8 import (fp8_dequantize, fp8_gemm, fp8_gemm_workspace, fp8_linear_bwd, fp8_linear_bwd_workspace,  # noqa: E402
+                  fp8_linear_fwd, fp8_quantize)
+from .norm import rms_norm, rms_norm_bwd, rms_norm_fwd  # noqa: E402

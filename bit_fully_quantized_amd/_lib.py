@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtj2.so")
 MEASURE_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtj2_measure.so")
 
 TJ2_OK, TJ2_ERR_ARG, TJ2_ERR_SHAPE, TJ2_ERR_ALIGN, TJ2_ERR_HIP, TJ2_ERR_UNSUPPORTED = range(6)
-BF16, F32, NVFP4, FP8, NVFP6, MXFP4 = 0, 1, 2, 3, 4, 5
+BF16, F32, NVFP4, FP8, NVFP6, MXFP4, FP8_BLOCK = 0, 1, 2, 3, 4, 5, 6
 GROUP_ROW, GROUP_COL = 0, 1
 RTN, SR = 0, 1
 OSCI_INIT, OSCI_ACCUM, OSCI_WINDOW_END = 0, 1, 2
@@ -127,6 +127,17 @@ SIGNATURES = {
     "tj2_linear_ce_fwd_workspace_size": (SZ, [I64, I64, I64]),
     "tj2_linear_ce_bwd": (I32, [P, I64, P, I64, P, I64, I64, I64, I64, P, P, P, I32, P, I32, P, SZ, P]),
     "tj2_linear_ce_bwd_workspace_size": (SZ, [I64, I64, I64]),
+    "fp8_quantize": (I32, [P, I32, QP, I64, I64, I32, QP, P]),
+    "fp8_dequantize": (I32, [QP, P, I32, P]),
+    "fp8_gemm": (I32, [QP, QP, P, I32, I64, I32, P, SZ, P]),
+    "fp8_gemm_workspace_size": (SZ, [I64, I64, I64]),
+    "fp8_linear_fwd": (I32, [P, I64, I64, I64, P, QP, QP, P, I32, P, SZ, P]),
+    "fp8_linear_fwd_workspace_size": (SZ, [I64, I64, I64]),
+    "fp8_linear_bwd": (I32, [P, I64, I64, I64, QP, QP, P, I32, P, P, SZ, P]),
+    "fp8_linear_bwd_workspace_size": (SZ, [I64, I64, I64]),
+    "tj2_rms_norm_fwd": (I32, [P, I64, P, I64, I32, I64, I64, P, I32, ctypes.c_float, P, P, QP, P, P]),
+    "tj2_rms_norm_bwd": (I32, [P, I64, P, I64, I32, I64, I64, P, I32, P, P, I64, P, P, P, SZ, P]),
+    "tj2_rms_norm_bwd_workspace_size": (SZ, [I64, I64]),
     "tj2_distill_topk": (I32, [P, I32, I64, I64, I64, P, P, I32, ctypes.c_float, ctypes.c_float, P, I64, P, P, P, I64, P]),
 }
 

@@ -90,7 +90,8 @@ size_t qbytes(int fmt, int64_t rows, int64_t len, size_t* c, size_t* s16, size_t
   const int64_t nb = (len + 127) / 128;
   *c = (size_t)(rows * nb * (fmt == TJ2_NVFP4 || fmt == TJ2_MXFP4 ? 64 : 128));
   *s16 = fmt == TJ2_FP8 ? 0 : (size_t)(rows * nb * (fmt == TJ2_MXFP4 ? 4 : 8));
-  *s128 = fmt == TJ2_MXFP4 ? 0 : (size_t)(rows * nb * 4);
+  if (fmt == TJ2_FP8_BLOCK) *s16 = 0;
+  *s128 = fmt == TJ2_MXFP4 ? 0 : (size_t)((fmt == TJ2_FP8_BLOCK ? (rows + 127) / 128 : rows) * nb * 4);
   return *c + *s16 + *s128;
 }
 
@@ -413,8 +414,8 @@ const char* tj2_version(void) { return "tj2 0.1.0 gfx950"; }
 
 tj2_status tj2_qtensor_bytes(int32_t fmt, int64_t rows, int64_t len, size_t* codes_bytes, size_t* scale16_bytes,
                              size_t* scale128_bytes) {
-  if (fmt != TJ2_NVFP4 && fmt != TJ2_FP8 && fmt != TJ2_NVFP6 && fmt != TJ2_MXFP4)
-    return fail(TJ2_ERR_ARG, "format must be TJ2_NVFP4, TJ2_FP8, TJ2_NVFP6 or TJ2_MXFP4");
+  if (fmt != TJ2_NVFP4 && fmt != TJ2_FP8 && fmt != TJ2_NVFP6 && fmt != TJ2_MXFP4 && fmt != TJ2_FP8_BLOCK)
+    return fail(TJ2_ERR_ARG, "format must be TJ2_NVFP4, TJ2_FP8, TJ2_NVFP6, TJ2_MXFP4 or TJ2_FP8_BLOCK");
   if (rows <= 0 || len <= 0 || (fmt != TJ2_MXFP4 && len % 16))
     return fail(TJ2_ERR_SHAPE, "rows > 0 and len a positive multiple of 16 (TJ2_MXFP4: any positive len) required");
   size_t c, s16, s128;
@@ -1346,6 +1347,260 @@ tj2_status tj2_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_
   d.tau = temperature;
   d.alpha = alpha;
   TJ2_TRY(hip_check(launch_distill(d, (hipStream_t)stream), "distillation launch"));
+  return ok();
+}
+
+}  // extern "C"
+
+// ---- FP8 linears (fp8.hip) ---------------------------------------------------------------
+namespace {
+
+// Longest FP8 row: a tile's 256 rows are addressed with 31-bit byte offsets.
+constexpr int64_t kFp8MaxLen = (int64_t)1 << 22;
+
+tj2_status check_fp8_size(const char* name, int64_t rows, int64_t len) {
+  if (rows <= 0 || len <= 0) return fail(TJ2_ERR_SHAPE, "%s: rows and len must be positive", name);
+  if (len > kFp8MaxLen) return fail(TJ2_ERR_SHAPE, "%s: len %lld is above 2^22", name, (long long)len);
+  if (rows > (int64_t)1 << 30 || rows * ((len + 127) / 128) >= (int64_t)1 << 27)
+    return fail(TJ2_ERR_SHAPE, "%s: too many elements", name);
+  return TJ2_OK;
+}
+
+// fmt: TJ2_FP8, TJ2_FP8_BLOCK or -1 for either
+tj2_status check_fp8(const tj2_qtensor* q, const char* name, int fmt, int64_t rows, int64_t len) {
+  if (!q) return fail(TJ2_ERR_ARG, "%s is NULL", name);
+  if (fmt < 0 ? q->fmt != TJ2_FP8 && q->fmt != TJ2_FP8_BLOCK : q->fmt != fmt)
+    return fail(TJ2_ERR_ARG, "%s has format %d, expected %s", name, q->fmt,
+                fmt < 0 ? "TJ2_FP8 or TJ2_FP8_BLOCK" : fmt == TJ2_FP8 ? "TJ2_FP8" : "TJ2_FP8_BLOCK");
+  if (q->rows != rows || q->len != len)
+    return fail(TJ2_ERR_SHAPE, "%s is [%lld, %lld], expected [%lld, %lld]", name, (long long)q->rows, (long long)q->len,
+                (long long)rows, (long long)len);
+  TJ2_TRY(check_fp8_size(name, rows, len));
+  if (len % 16) return fail(TJ2_ERR_SHAPE, "%s: len %lld is not a multiple of 16", name, (long long)len);
+  if (!q->codes || !q->scale128) return fail(TJ2_ERR_ARG, "%s: NULL array", name);
+  if (!aligned16(q->codes) || !aligned16(q->scale128)) return fail(TJ2_ERR_ALIGN, "%s: arrays must be 16-byte aligned", name);
+  return TJ2_OK;
+}
+
+tj2_status check_linear_dims(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0) return fail(TJ2_ERR_SHAPE, "M must be positive");
+  TJ2_TRY(check_dims(K, "K"));
+  TJ2_TRY(check_dims(N, "N"));
+  return TJ2_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tj2_status fp8_quantize(const void* x, int32_t x_dtype, const tj2_qtensor* x_q, int64_t rows, int64_t cols, int32_t grouping,
+                        tj2_qtensor* out, void* stream) {
+  if (grouping != TJ2_GROUP_ROW && grouping != TJ2_GROUP_COL) return fail(TJ2_ERR_ARG, "bad grouping %d", grouping);
+  TJ2_TRY(check_fp8_size("x", rows, cols));
+  if (cols % 16) return fail(TJ2_ERR_SHAPE, "cols = %lld must be a multiple of 16", (long long)cols);
+  TJ2_TRY(grouping == TJ2_GROUP_ROW ? check_fp8(out, "out", -1, rows, cols) : check_fp8(out, "out", TJ2_FP8, cols, rows));
+  Fp8QuantParams p = {};
+  if (x_dtype == TJ2_BF16 || x_dtype == TJ2_F32) {
+    if (!x) return fail(TJ2_ERR_ARG, "x is NULL");
+    if (!aligned16(x)) return fail(TJ2_ERR_ALIGN, "x must be 16-byte aligned");
+  } else if (x_dtype == TJ2_FP8) {
+    if (grouping != TJ2_GROUP_COL) return fail(TJ2_ERR_UNSUPPORTED, "row grouping of a quantized input is not implemented");
+    TJ2_TRY(check_fp8(x_q, "x_q", TJ2_FP8, rows, cols));
+    // (the transposed groups are written while others are still read)
+    if (out->codes == x_q->codes || out->scale128 == x_q->scale128) return fail(TJ2_ERR_ARG, "out must not be x_q");
+    p.xq = make_view(*x_q);
+  } else {
+    return fail(TJ2_ERR_ARG, "bad x_dtype %d", x_dtype);
+  }
+  p.in_dtype = x_dtype;
+  p.x = x;
+  p.rows = rows;
+  p.cols = cols;
+  p.grouping = grouping;
+  p.out = make_view(*out);
+  TJ2_TRY(hip_check(launch_fp8_quant(p, (hipStream_t)stream), "FP8 quantize launch"));
+  return ok();
+}
+
+tj2_status fp8_dequantize(const tj2_qtensor* q, void* out, int32_t out_dtype, void* stream) {
+  if (!q) return fail(TJ2_ERR_ARG, "q is NULL");
+  TJ2_TRY(check_fp8(q, "q", -1, q->rows, q->len));
+  TJ2_TRY(check_out_dtype(out_dtype, "out_dtype"));
+  if (!out) return fail(TJ2_ERR_ARG, "out is NULL");
+  if (!aligned16(out)) return fail(TJ2_ERR_ALIGN, "out must be 16-byte aligned");
+  TJ2_TRY(hip_check(launch_fp8_values(make_view(*q), out, out_dtype, (hipStream_t)stream), "FP8 dequantize launch"));
+  return ok();
+}
+
+size_t fp8_gemm_workspace_size(int64_t I, int64_t J, int64_t K) {
+  if (I <= 0 || J <= 0 || K <= 0) return 0;
+  return fp8_gemm_workspace_bytes(I, J, K);
+}
+
+tj2_status fp8_gemm(const tj2_qtensor* A, const tj2_qtensor* B, void* C, int32_t c_dtype, int64_t ldc, int32_t accumulate,
+                    void* workspace, size_t ws_bytes, void* stream) {
+  if (!A || !B) return fail(TJ2_ERR_ARG, "A and B are required");
+  TJ2_TRY(check_fp8(A, "A", TJ2_FP8, A->rows, A->len));
+  TJ2_TRY(check_fp8(B, "B", -1, B->rows, A->len));
+  TJ2_TRY(check_out_dtype(c_dtype, "c_dtype"));
+  if (!C) return fail(TJ2_ERR_ARG, "C is NULL");
+  if (reinterpret_cast<uintptr_t>(C) & (c_dtype == TJ2_BF16 ? 1u : 3u)) return fail(TJ2_ERR_ALIGN, "C must be aligned to its elements");
+  if (accumulate && c_dtype != TJ2_F32) return fail(TJ2_ERR_UNSUPPORTED, "accumulate needs an fp32 output");
+  if (ldc < B->rows) return fail(TJ2_ERR_SHAPE, "ldc < J");
+  TJ2_TRY(check_mx_workspace(workspace, ws_bytes, fp8_gemm_workspace_bytes(A->rows, B->rows, A->len)));
+  TJ2_TRY(hip_check(launch_fp8_gemm(make_view(*A), make_view(*B), C, c_dtype, ldc, accumulate, reinterpret_cast<float*>(workspace),
+                                    (hipStream_t)stream),
+                    "FP8 gemm launch"));
+  return ok();
+}
+
+size_t fp8_linear_fwd_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return fp8_linear_fwd_workspace_bytes(M, N, K);
+}
+
+tj2_status fp8_linear_fwd(const void* X, int64_t M, int64_t K, int64_t N, const float* W_master, tj2_qtensor* Wq, tj2_qtensor* Xq,
+                          void* Y, int32_t y_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (!Y) return fail(TJ2_ERR_ARG, "Y is required");
+  TJ2_TRY(check_linear_dims(M, N, K));
+  TJ2_TRY(check_fp8(Xq, "Xq", TJ2_FP8, M, K));
+  TJ2_TRY(check_fp8(Wq, "Wq", TJ2_FP8_BLOCK, N, K));
+  TJ2_TRY(check_out_dtype(y_dtype, "y_dtype"));
+  if (!aligned16(X) || !aligned16(W_master) || !aligned16(Y)) return fail(TJ2_ERR_ALIGN, "X, W_master and Y must be 16-byte aligned");
+  TJ2_TRY(check_mx_workspace(workspace, ws_bytes, fp8_linear_fwd_workspace_bytes(M, N, K)));
+  TJ2_TRY(hip_check(launch_fp8_linear_fwd(X, W_master, make_view(*Xq), make_view(*Wq), Y, y_dtype, reinterpret_cast<float*>(workspace),
+                                          (hipStream_t)stream),
+                    "FP8 linear launch"));
+  return ok();
+}
+
+size_t fp8_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return fp8_linear_bwd_workspace_bytes(M, N, K);
+}
+
+tj2_status fp8_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, const tj2_qtensor* Xq, const tj2_qtensor* Wq, void* dX,
+                          int32_t dx_dtype, float* dW, void* workspace, size_t ws_bytes, void* stream) {
+  if (!dY || !dX || !dW || !workspace) return fail(TJ2_ERR_ARG, "dY, dX, dW and workspace are required");
+  TJ2_TRY(check_linear_dims(M, N, K));
+  TJ2_TRY(check_fp8(Xq, "Xq", TJ2_FP8, M, K));
+  TJ2_TRY(check_fp8(Wq, "Wq", TJ2_FP8_BLOCK, N, K));
+  // the workspace's operands: the output gradient both ways, W and X transposed
+  TJ2_TRY(check_fp8_size("dY", M, N));
+  TJ2_TRY(check_fp8_size("dY transposed", N, M));
+  TJ2_TRY(check_fp8_size("Wq transposed", K, N));
+  TJ2_TRY(check_fp8_size("Xq transposed", K, M));
+  TJ2_TRY(check_out_dtype(dx_dtype, "dx_dtype"));
+  if (!aligned16(dY) || !aligned16(dX) || !aligned16(dW)) return fail(TJ2_ERR_ALIGN, "dY, dX and dW must be 16-byte aligned");
+  TJ2_TRY(check_mx_workspace(workspace, ws_bytes, fp8_linear_bwd_workspace_bytes(M, N, K)));
+  TJ2_TRY(hip_check(launch_fp8_linear_bwd(dY, make_view(*Xq), make_view(*Wq), dX, dx_dtype, dW, workspace, (hipStream_t)stream),
+                    "FP8 linear launch"));
+  return ok();
+}
+
+}  // extern "C"
+
+// ---- root-mean-square norm (norm.hip) -------------------------------------------------------
+namespace {
+
+tj2_status check_norm(int32_t dtype, int64_t rows, int64_t cols, const void* weight, int32_t w_dtype) {
+  if (dtype != TJ2_BF16 && dtype != TJ2_F32) return fail(TJ2_ERR_ARG, "dtype must be TJ2_BF16 or TJ2_F32");
+  if (w_dtype != TJ2_BF16 && w_dtype != TJ2_F32) return fail(TJ2_ERR_ARG, "w_dtype must be TJ2_BF16 or TJ2_F32");
+  if (rows <= 0 || cols <= 0) return fail(TJ2_ERR_SHAPE, "rows and cols must be positive");
+  if (rows > (int64_t)1 << 30 || cols > (int64_t)1 << 22) return fail(TJ2_ERR_SHAPE, "rows are at most 2^30 and cols 2^22");
+  if (!weight) return fail(TJ2_ERR_ARG, "weight is NULL");
+  if (reinterpret_cast<uintptr_t>(weight) & (w_dtype == TJ2_BF16 ? 1u : 3u)) return fail(TJ2_ERR_ALIGN, "weight must be aligned to its elements");
+  return TJ2_OK;
+}
+// a matrix of the stream's type whose rows lie ld apart
+tj2_status check_stream(const void* p, int64_t ld, int32_t dtype, int64_t cols, const char* name) {
+  if (!p) return fail(TJ2_ERR_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) & (dtype == TJ2_BF16 ? 1u : 3u)) return fail(TJ2_ERR_ALIGN, "%s must be aligned to its elements", name);
+  if (ld < cols) return fail(TJ2_ERR_SHAPE, "%s: rows of %lld elements lie %lld apart", name, (long long)cols, (long long)ld);
+  return TJ2_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tj2_status tj2_rms_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t dtype, int64_t rows, int64_t cols,
+                            const void* weight, int32_t w_dtype, float eps, void* sum, void* y, tj2_qtensor* yq, float* rstd,
+                            void* stream) {
+  TJ2_TRY(check_norm(dtype, rows, cols, weight, w_dtype));
+  TJ2_TRY(check_stream(x, ldx, dtype, cols, "x"));
+  if (!(eps >= 0.0f) || isinf(eps)) return fail(TJ2_ERR_ARG, "eps must be finite and not negative");
+  if ((residual == nullptr) != (sum == nullptr)) return fail(TJ2_ERR_ARG, "residual and sum must be given together");
+  if (residual) {
+    TJ2_TRY(check_stream(residual, ldr, dtype, cols, "residual"));
+    TJ2_TRY(check_stream(sum, cols, dtype, cols, "sum"));
+  }
+  if ((y == nullptr) == (yq == nullptr)) return fail(TJ2_ERR_ARG, "one of y and yq must be given");
+  TJ2_TRY(check_f32(rstd, "rstd", false));
+  NormParams n = {};
+  if (y) {
+    TJ2_TRY(check_stream(y, cols, dtype, cols, "y"));
+  } else {
+    TJ2_TRY(check_fp8(yq, "yq", TJ2_FP8, rows, cols));
+    const int64_t es = dtype == TJ2_BF16 ? 2 : 4;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(sum) || !aligned16(weight))
+      return fail(TJ2_ERR_ALIGN, "with an FP8 result x, residual, sum and weight must be 16-byte aligned");
+    if (ldx * es % 16 || (residual && ldr * es % 16))
+      return fail(TJ2_ERR_ALIGN, "with an FP8 result the rows of x and residual must be 16-byte aligned");
+    n.yq = make_view(*yq);
+  }
+  n.x = x;
+  n.residual = residual;
+  n.ldx = ldx;
+  n.ldr = ldr;
+  n.rows = rows;
+  n.cols = cols;
+  n.dtype = dtype;
+  n.w_dtype = w_dtype;
+  n.w = weight;
+  n.eps = eps;
+  n.sum = sum;
+  n.y = y;
+  n.rstd = rstd;
+  TJ2_TRY(hip_check(launch_norm(n, (hipStream_t)stream), "norm launch"));
+  return ok();
+}
+
+size_t tj2_rms_norm_bwd_workspace_size(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return norm_grad_workspace_bytes(rows, cols);
+}
+
+tj2_status tj2_rms_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, int32_t dtype, int64_t rows, int64_t cols,
+                            const void* weight, int32_t w_dtype, const float* rstd, const void* dsum, int64_t ldd, void* ds, void* dw,
+                            void* workspace, size_t ws_bytes, void* stream) {
+  TJ2_TRY(check_norm(dtype, rows, cols, weight, w_dtype));
+  TJ2_TRY(check_stream(dy, lddy, dtype, cols, "dy"));
+  TJ2_TRY(check_stream(s, lds, dtype, cols, "s"));
+  TJ2_TRY(check_f32(rstd, "rstd", true));
+  if (!ds && !dw) return fail(TJ2_ERR_ARG, "ds or dw is required");
+  if (dsum) TJ2_TRY(check_stream(dsum, ldd, dtype, cols, "dsum"));
+  if (ds) TJ2_TRY(check_stream(ds, cols, dtype, cols, "ds"));
+  if (dw) {
+    if (reinterpret_cast<uintptr_t>(dw) & (w_dtype == TJ2_BF16 ? 1u : 3u)) return fail(TJ2_ERR_ALIGN, "dw must be aligned to its elements");
+    TJ2_TRY(check_ce_workspace(workspace, ws_bytes, norm_grad_workspace_bytes(rows, cols)));
+  }
+  NormGradParams n = {};
+  n.dy = dy;
+  n.s = s;
+  n.dsum = dsum;
+  n.lddy = lddy;
+  n.lds = lds;
+  n.ldd = ldd;
+  n.rows = rows;
+  n.cols = cols;
+  n.dtype = dtype;
+  n.w_dtype = w_dtype;
+  n.w = weight;
+  n.rstd = rstd;
+  n.ds = ds;
+  n.dw = dw;
+  TJ2_TRY(hip_check(launch_norm_grad(n, workspace, (hipStream_t)stream), "norm launch"));
   return ok();
 }
 

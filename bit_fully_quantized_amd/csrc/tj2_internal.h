@@ -29,7 +29,7 @@ inline QView make_view(const tj2_qtensor& q) {
   v.fmt = q.fmt;
   v.ld_codes = q.fmt == TJ2_NVFP4 || q.fmt == TJ2_MXFP4 ? v.nb * 64 : v.nb * 128;  // FP8 / NVFP6: one byte per element
   v.ld_s16 = q.fmt == TJ2_MXFP4 ? v.nb * 4 : v.nb * 8;
-  v.ld_s128 = q.fmt == TJ2_MXFP4 ? 0 : v.nb;
+  v.ld_s128 = q.fmt == TJ2_MXFP4 ? 0 : v.nb;  // (TJ2_FP8_BLOCK: of 128 rows)
   return v;
 }
 
@@ -196,6 +196,30 @@ hipError_t launch_mx_gemm_pair(const QView& A, const QView& B, void* C, int c_dt
 bool mx_is_few(int64_t M, int64_t K);
 hipError_t launch_mx_linear_few(const void* X, const QView& Xq, const QView& Wq, void* Y, int y_dtype, hipStream_t s);
 
+// FP8 under fp32 scales per 128 of a row (TJ2_FP8) or per 128 x 128 (TJ2_FP8_BLOCK):
+// quantisers, values, the product C = A B^T (A FP8, B either; the reduction may be split
+// when `partial` of fp8_gemm_workspace_bytes is given) and the linear layer on it.
+struct Fp8QuantParams {
+  int in_dtype;  // TJ2_BF16, TJ2_F32 or (column grouping) TJ2_FP8
+  const void* x;
+  QView xq;
+  int64_t rows, cols;
+  int grouping;
+  QView out;
+};
+hipError_t launch_fp8_quant(const Fp8QuantParams& q, hipStream_t s);
+hipError_t launch_fp8_values(const QView& q, void* out, int dtype, hipStream_t s);
+size_t fp8_gemm_workspace_bytes(int64_t I, int64_t J, int64_t K);
+hipError_t launch_fp8_gemm(const QView& A, const QView& B, void* C, int c_dtype, int64_t ldc, int accumulate, float* partial,
+                           hipStream_t s);
+// X NULL: Xq is given; W NULL: Wq is given.
+size_t fp8_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_fp8_linear_fwd(const void* X, const float* W, const QView& Xq, const QView& Wq, void* Y, int y_dtype,
+                                 float* partial, hipStream_t s);
+size_t fp8_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_fp8_linear_bwd(const void* dY, const QView& Xq, const QView& Wq, void* dX, int dx_dtype, float* dW, void* ws,
+                                 hipStream_t s);
+
 // Cross entropy of X W^T (loss.hip): bf16 X [T, K] at pitch ldx, W [V, K] at ldw.
 struct CeParams {
   const void* X;
@@ -229,6 +253,30 @@ struct DistillParams {
 };
 int distill_max_k();
 hipError_t launch_distill(const DistillParams& d, hipStream_t s);
+
+// Root-mean-square norm with the residual's addition (norm.hip) and its backward pass.
+struct NormParams {
+  const void *x, *residual;  // [rows, cols] at pitches ldx, ldr; residual may be NULL
+  int64_t ldx, ldr, rows, cols;
+  int dtype, w_dtype;
+  const void* w;
+  float eps;
+  void* sum;    // with a residual
+  void* y;      // NULL: yq
+  QView yq;
+  float* rstd;  // optional
+};
+hipError_t launch_norm(const NormParams& n, hipStream_t s);
+struct NormGradParams {
+  const void *dy, *s, *dsum;  // dsum optional
+  int64_t lddy, lds, ldd, rows, cols;
+  int dtype, w_dtype;
+  const void* w;
+  const float* rstd;
+  void *ds, *dw;  // each optional
+};
+size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols);
+hipError_t launch_norm_grad(const NormGradParams& n, void* ws, hipStream_t s);
 
 // OsciReset and the fused master-weight pass (AdamW, then OsciReset), on up to
 // kOsciMultiMax weight matrices per launch.  Parameters shared by the

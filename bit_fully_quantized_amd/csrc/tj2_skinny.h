@@ -14,13 +14,15 @@ namespace tj2 {
 
 template <int EL, int TN, int LDS_BYTES>
 struct Skinny {
+  static constexpr bool kFp8 = EL == EL_FP8BX;  // E4M3 under a scale per 128 (tokens) and 128 x 128 (W)
   static constexpr int NT = 256, WAVES = NT / 64, U = EL == EL_MX ? 4 : 8;
   static constexpr int TOKENS = 16 * TN;
   static constexpr int PER_CU = 160 * 1024 / (LDS_BYTES + LDS_BYTES / 16 + 512) >= 2 ? 2 : 1;
 
   struct Smem {
     __attribute__((aligned(16))) uint8_t x[LDS_BYTES];
-    __attribute__((aligned(16))) uint8_t xs[EL == EL_MX ? LDS_BYTES / 16 + 2 * TOKENS : 16];  // MXFP4 scale bytes
+    // MXFP4 scale bytes; FP8: a float per chunk and token
+    __attribute__((aligned(16))) uint8_t xs[EL == EL_MX ? LDS_BYTES / 16 + 2 * TOKENS : kFp8 ? LDS_BYTES / 32 : 16];
   };
 
   // LDS row pitch of a token: whole chunks and 16 bytes, so that 16 tokens' pieces lie in different banks
@@ -55,6 +57,7 @@ struct Skinny {
     struct Batch {
       i32x4_t a[U][2];
       uint16_t s[EL == EL_MX ? U : 1];
+      float w[kFp8 ? U : 1];
     };
     // batch b of group gr
     auto fetch = [&](Batch& f, uint32_t gr, int b) __attribute__((always_inline)) {
@@ -79,16 +82,34 @@ struct Skinny {
         }
       }
     };
+    auto fetch_scales = [&](Batch& f, uint32_t gr, int b) __attribute__((always_inline)) {
+      if constexpr (kFp8) {
+        const uint8_t* s = P.s + (int64_t)(gr >> 3) * P.srs;
+#pragma unroll
+        for (int u = 0; u < U; ++u) f.w[u] = b * U + u < chunks ? *reinterpret_cast<const float*>(s + (b * U + u) * P.scs) : 0.0f;
+      }
+    };
     Acc acc = {};
     auto multiply = [&](const Batch& f, int b) __attribute__((always_inline)) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = b * U + u;
         if (c >= chunks) break;
+        half8_t wt[kFp8 ? 4 : 1];  // exact products, as the reads bound this (EL_FP8BX)
+        if constexpr (kFp8) fp8_to_f16(f.a[u][0], f.a[u][1], wt);
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn) {
           const i32x4_t* x = reinterpret_cast<const i32x4_t*>(xl + tn * 16 * px + c * 128);
-          if constexpr (EL == EL_BF16) {
+          if constexpr (kFp8) {
+            const float s = reinterpret_cast<const float*>(sm.xs)[c * TOKENS + tn * 16 + n] * f.w[u];
+            half8_t xt[4];
+            fp8_to_f16(x[0], x[1], xt);
+            float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v = __builtin_amdgcn_mfma_f32_16x16x32_f16(wt[k], xt[k], v, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[tn][r] = fmaf(v[r], s, acc[tn][r]);
+          } else if constexpr (EL == EL_BF16) {
             acc[tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f.a[u][0]),
                                                               __builtin_bit_cast(bf16x8_t, x[0]), acc[tn], 0, 0, 0);
             acc[tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f.a[u][1]),
@@ -110,6 +131,7 @@ struct Skinny {
     int b = 0;
     Batch f0, f1;
     fetch(f0, gr, 0);
+    fetch_scales(f0, gr, 0);
     // two batches a turn, so that each has its own registers
     auto turn = [&](const Batch& now, Batch& next) __attribute__((always_inline)) -> bool {
       uint32_t ng = gr;
@@ -118,7 +140,10 @@ struct Skinny {
         nb = 0;
         ng += waves;
       }
-      if (ng < groups) fetch(next, ng, nb);
+      if (ng < groups) {
+        fetch(next, ng, nb);
+        fetch_scales(next, ng, nb);
+      }
       multiply(now, b);
       if (ng != gr) {
         epilogue(gr, acc);

@@ -1,5 +1,6 @@
 // Tile product of two row-major operands along their contiguous axis, shared by
-// the MXFP4 products (mx.hip) and the head's cross entropy (loss.hip):
+// the MXFP4 and FP8 products (mx.hip, fp8.hip), the head's cross entropy (loss.hip)
+// and the gated feed-forward block (ffn.hip):
 //
 //   D[q, p] = sum_k Q[q, k] P[p, k]
 //
@@ -7,7 +8,18 @@
 // with one power-of-two scale per 32; v_mfma_scale_f32_16x16x128_f8f6f4 applies
 // the scales itself).  Both instructions take 16 bytes of each operand per lane
 // and run in 16 cycles, so one loop serves both: a chunk is 128 bytes of every
-// row (64 bf16 or 256 E2M1), two instruction steps.
+// row (64 bf16 or 256 E2M1), two instruction steps.  FP8 operands (E4M3 codes, an
+// fp32 scale per 128) have a loop of their own: a chunk is one instruction of 128
+// elements, and its result is scaled as it is added to the sums.  That instruction keeps
+// some 14 bits of what neighbouring products add to the largest of them (1.4e-5 of a
+// result of normal operands, 1e-5 of the sum of magnitudes at most, measured), which is
+// less than half a step of a bf16 result but not of an fp32 one: EL_FP8X and EL_FP8BX
+// decode the codes to f16, which holds them, and use v_mfma_f32_16x16x32_f16 at half the
+// rate, whose products are exact and whose sums are fp32.
+//
+// EL_PAIR: bf16, with P's rows taken from two matrices of the same shape in turn, so
+// that a lane holds the results of a row of both (first: tiles 0 to PB - 1 of a wave's
+// P rows, second: the next PB, ...); a tile then has BM / 2 rows of each.
 //
 // Workgroups go to the 8 XCDs in turn, each with its own L2, so an XCD takes a
 // contiguous range of the tiles.
@@ -45,11 +57,27 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2v_t __attribute__((ext_vector_type(2)));
 typedef float f32x2v_t __attribute__((ext_vector_type(2)));
 
-enum { EL_BF16 = 0, EL_MX = 1 };
+// FP8B: P's scales are those of 128 rows; FP8X, FP8BX: the same with exact products
+enum { EL_BF16 = 0, EL_MX = 1, EL_FP8 = 2, EL_FP8B = 3, EL_PAIR = 4, EL_FP8X = 5, EL_FP8BX = 6 };
 
 // Two fp32 values rounded to the nearest even bf16, a in the low half.
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2v_t{a, b}, bf16x2v_t));
+}
+
+// The values of 32 E4M3 codes, which f16 holds.
+__device__ __forceinline__ void fp8_to_f16(i32x4_t a, i32x4_t b, half8_t (&x)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    half2_t h[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t u = (uint32_t)(k < 2 ? a : b)[k % 2 * 2 + i];
+      h[2 * i] = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, false));
+      h[2 * i + 1] = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, true));
+    }
+    x[k] = half8_t{h[0].x, h[0].y, h[1].x, h[1].y, h[2].x, h[2].y, h[3].x, h[3].y};
+  }
 }
 
 // An operand of a tile product: rows of `kb` bytes (a multiple of 16).  Row r's
@@ -59,12 +87,15 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 // the latter for operands that a pass of this library writes: a chunk of a tile is
 // contiguous, where a long pitch spreads its rows over as many pages and, if it is a
 // power of two, over few memory channels.  MXFP4: the scale bytes, one for 16 of codes,
-// lie as the codes do.
+// lie as the codes do.  FP8: the scale of row r (EL_FP8B's P: of rows r to r + 127) and
+// chunk c lies at s + r srs (r / 128 srs) + c scs.
 struct TileOp {
   const uint8_t* p;
   const uint8_t* s;
   int64_t rows, ld, bs;
   int32_t kb, cs;
+  const uint8_t* p2;  // EL_PAIR: the second matrix
+  int64_t srs, scs;
 };
 
 constexpr uint32_t kOutside = 0x80000000u;  // lane offset beyond every buffer below
@@ -165,10 +196,14 @@ struct Tile {
   static constexpr int NT = 64 * WM * WN;           // threads
   static constexpr int BM = 16 * WM * TM, BN = 16 * WN * TN;
   static constexpr int ROWS = BM + BN;
-  static constexpr int PB = TM < 4 ? TM : 4;        // tiles whose rows interleave
+  static constexpr bool kExact = EL == EL_FP8X || EL == EL_FP8BX, kBlockP = EL == EL_FP8B || EL == EL_FP8BX;
+  static constexpr bool kFp8 = EL == EL_FP8 || EL == EL_FP8B || kExact, kPair = EL == EL_PAIR;
   static constexpr int RPI = NT / 8;                // rows one load instruction of all threads covers
+  static constexpr int PB = kPair ? RPI / 16 : TM < 4 ? TM : 4;  // tiles whose rows interleave
   static constexpr int LP = BM / RPI, LQ = BN / RPI;
-  static constexpr int SCALE_DW = EL == EL_MX ? ROWS * 2 : 0;  // scale words of a chunk
+  static constexpr int SCALE_DW = EL == EL_MX ? ROWS * 2 : kFp8 ? ROWS : 0;  // scale words of a chunk
+  static constexpr int PROWS = kPair ? BM / 2 : BM;  // rows of P('s matrices) in a tile
+  static_assert(!kPair || (TM % (2 * PB) == 0 && PB <= 4), "a wave holds as many rows of either matrix");
   static_assert(BM % RPI == 0 && BN % RPI == 0, "whole load instructions");
   static_assert(RPI >= 2 * TN && RPI % 32 == 0, "a thread's rows i * RPI + r differ from r by bits of the key above its own");
   static_assert(TN == 1 || TN % 2 == 0, "q_place pairs rows");
@@ -184,7 +219,7 @@ struct Tile {
 
   struct Smem {
     uint8_t stage[2][ROWS * 128];
-    uint32_t scale[2][EL == EL_MX ? SCALE_DW : 1];
+    uint32_t scale[2][SCALE_DW ? SCALE_DW : 1];
   };
 
   typedef float4_t Acc[TM][TN];
@@ -276,20 +311,26 @@ struct Tile {
     const uint32_t lds_w = lds_address(sm.stage[0]) + (uint32_t)w * 1024u;
     constexpr uint32_t kStage = ROWS * 128;
 
-    // scales: [row][2] words of a chunk, a wave 32 rows at a time (all of P or all
-    // of Q: BM is a multiple of 32)
-    constexpr int SJ = EL == EL_MX ? SCALE_DW / NT : 1;
-    static_assert(SCALE_DW % NT == 0 && BM % 32 == 0, "whole scale loads");
+    // scales: MXFP4 [row][2] words of a chunk, a wave 32 rows at a time (all of P or all
+    // of Q: BM is a multiple of 32); FP8 a word a row, 64 rows at a time
+    constexpr int SJ = EL == EL_MX ? SCALE_DW / NT : kFp8 ? (SCALE_DW + NT - 1) / NT : 1;
+    static_assert(kFp8 ? BM % 64 == 0 && BN % 64 == 0 : SCALE_DW % NT == 0 && BM % 32 == 0, "whole scale loads");
     const uint32_t vs = (uint32_t)(lane >> 1) * (ldp / 16) + (lane & 1) * 4;
+    const uint32_t srp = kFp8 ? pinned((uint32_t)P.srs) : 0, srq = kFp8 ? pinned((uint32_t)Q.srs) : 0;
 
     // The load cursor: its item, the item's rows (none once the items are done), where
     // its chunk starts and the bytes of a row from there on.
     Item ahead = now;
     uint32_t ahead_at = items.at;
-    const uint8_t *pb, *qb, *psb = nullptr, *qsb = nullptr;
+    const uint8_t *pb, *qb, *psb = nullptr, *qsb = nullptr, *pb2 = nullptr;
     int np, nq, leftp, leftq;
     auto enter = [&]() __attribute__((always_inline)) {
-      const int64_t p0 = (int64_t)ahead.tp * BM, q0 = (int64_t)ahead.tq * BN;
+      const int64_t p0 = (int64_t)ahead.tp * PROWS, q0 = (int64_t)ahead.tq * BN;
+      if constexpr (kPair) pb2 = P.p2 + (p0 >> 7) * P.bs + (p0 & 127) * P.ld + mul32(ahead.c, csp);
+      if constexpr (kFp8) {
+        psb = P.s + (kBlockP ? p0 >> 7 : p0) * P.srs + (int64_t)ahead.c * P.scs;
+        qsb = Q.s + q0 * Q.srs + (int64_t)ahead.c * Q.scs;
+      }
       pb = P.p + (p0 >> 7) * P.bs + (p0 & 127) * P.ld + mul32(ahead.c, csp);
       qb = Q.p + (q0 >> 7) * Q.bs + (q0 & 127) * Q.ld + mul32(ahead.c, csq);
       leftp = kbp - ahead.c * 128;
@@ -298,18 +339,28 @@ struct Tile {
         psb = P.s + ((p0 >> 7) * P.bs + (p0 & 127) * P.ld + mul32(ahead.c, csp)) / 16;
         qsb = Q.s + ((q0 >> 7) * Q.bs + (q0 & 127) * Q.ld + mul32(ahead.c, csq)) / 16;
       }
-      np = __builtin_amdgcn_readfirstlane((int)min(P.rows - p0, (int64_t)BM));
+      np = __builtin_amdgcn_readfirstlane((int)min(P.rows - p0, (int64_t)PROWS));
       nq = __builtin_amdgcn_readfirstlane((int)min(Q.rows - q0, (int64_t)BN));
     };
     enter();
     // The loads of the cursor's chunk into `stage`, one at a time: begin() sets them up.
-    u32x4_t dp, dq, dsp, dsq;
+    u32x4_t dp, dq, dsp, dsq, dp2;
     uint32_t bads = 0, dst = 0, sdst = 0;
     auto begin = [&](uint32_t stage) __attribute__((always_inline)) {
       dp = raw_buffer(pb);
       dq = raw_buffer(qb);
       settle(dp, dq);
       dst = lds_w + stage * kStage;
+      if constexpr (kPair) {
+        dp2 = raw_buffer(pb2);
+        settle(dp, dp2);
+      }
+      if constexpr (kFp8) {
+        dsp = raw_buffer(psb);
+        dsq = raw_buffer(qsb);
+        settle(dsp, dsq);
+        sdst = lds_address(sm.scale[0]) + stage * (SCALE_DW * 4) + (uint32_t)w * 256u;
+      }
       if constexpr (EL == EL_MX) {
         dsp = raw_buffer(psb);
         dsq = raw_buffer(qsb);
@@ -334,15 +385,22 @@ struct Tile {
         qb += csq;
         leftp -= 128;
         leftq -= 128;
+        if constexpr (kPair) pb2 += csp;
         if constexpr (kMx) {
           psb += csp / 16;
           qsb += csq / 16;
         }
+        if constexpr (kFp8) {
+          psb += P.scs;
+          qsb += Q.scs;
+        }
       }
     };
-    constexpr int LOADS = LP + LQ + (EL == EL_MX ? SJ : 0);
+    constexpr int LOADS = LP + LQ + (EL == EL_MX || kFp8 ? SJ : 0);
     auto load = [&](int i) __attribute__((always_inline)) {
-      if (i < LP) {
+      if (kPair && i < LP) {
+        load_lds16(i & 1 ? dp2 : dp, lr < np - (i >> 1) * RPI && (int)gp(i) < leftp ? vp + gp(i) : kOutside, far_p(i >> 1), dst + i * (RPI * 128));
+      } else if (i < LP) {
         load_lds16(dp, lr < np - i * RPI && (int)gp(i) < leftp ? vp + gp(i) : kOutside, far_p(i), dst + i * (RPI * 128));
       } else if (i < LP + LQ) {
         load_lds16(dq, lrq < nq - (i - LP) * RPI && (int)gq(i - LP) < leftq ? vq + gq(i - LP) : kOutside, far_q(i - LP), dst + i * (RPI * 128));
@@ -357,9 +415,163 @@ struct Tile {
         d.w = dsp.w;
         load_lds4(d, (lane >> 1) < (isp ? np : nq) - first ? vs | bads : kOutside, (uint32_t)(first >> 7) * (bsp / 16) + (uint32_t)(first & 127) * (ldp / 16),
                   sdst + j * (NT * 4));
+      } else if constexpr (kFp8) {
+        const int j = i - LP - LQ, r0 = w * 64 + j * NT;
+        if (ROWS % NT && r0 >= ROWS) return;
+        const bool isp = r0 < BM;
+        const int first = isp ? r0 : r0 - BM;
+        const bool block = kBlockP && isp;
+        u32x4_t d;
+        d.x = isp ? dsp.x : dsq.x;
+        d.y = isp ? dsp.y : dsq.y;
+        d.z = dsp.z;
+        d.w = dsp.w;
+        const uint32_t sr = isp ? srp : srq;
+        load_lds4(d, lane < (isp ? np : nq) - first ? (block ? 0u : (uint32_t)lane * sr) : kOutside, (uint32_t)(block ? first >> 7 : first) * sr,
+                  sdst + j * (NT * 4));
       }
     };
 
+    const int pr0 = wm * TM * 16, qr0 = BM + wn * TN * 16;
+    const int pk = p_key(p_row(0, n >> 2, n & 3)), qk = q_key(q_row(0, n));
+    // LDS byte addresses; the two steps' pieces are neighbours, 16 bytes apart
+    const uint32_t lp = lds_address(sm.stage[0]) + (uint32_t)(pr0 + p_row(0, n >> 2, n & 3)) * 128u + ((2 * g) ^ pk) * 16;
+    // even and odd tiles of Q: a lane's rows trade places in pairs
+    const uint32_t lq0 = lds_address(sm.stage[0]) + (uint32_t)(qr0 + q_place(q_row(0, n))) * 128u + ((2 * g) ^ qk) * 16;
+    const uint32_t lq1 = lds_address(sm.stage[0]) + (uint32_t)(qr0 + q_place(q_row(TN > 1 ? 1 : 0, n))) * 128u + ((2 * g) ^ qk) * 16;
+    if constexpr (kFp8) {
+      // A chunk: TM rows of TN instructions, whose results (two rows of them in
+      // registers) are scaled and added to the sums while the next row's run.  P's
+      // fragments are read two rows ahead; Q's, which every row needs, at the start.  The
+      // barrier comes after the last row has issued: then every wave has read the whole
+      // stage, which is refilled from the start of the next chunk on.
+      constexpr int PR = 2;
+      i32x4_t fp[PR][2], fq[TN][2];
+      float4_t part[2][TN];
+      float sq[TN], sb = 0.0f;
+      float4_t sp[kBlockP ? 1 : PR];
+      // exact: the codes as f16, two rows of P's (the next one's is decoded while one runs)
+      half8_t xp[kExact ? 2 : 1][4], xq[kExact ? TN : 1][4];
+      const uint32_t lsp = lds_address(sm.scale[0]) + (uint32_t)(pr0 + (kBlockP ? 0 : p_row(0, g, 0))) * 4u;
+      const uint32_t lsq = lds_address(sm.scale[0]) + (uint32_t)(qr0 + q_row(0, n)) * 4u;
+      auto read_p = [&](uint32_t stage, int tm) __attribute__((always_inline)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) fp[tm % PR][h] = lds_read<i32x4_t>(((lp ^ (h * 16)) + stage * kStage) + p_row(tm, 0, 0) * 128);
+      };
+      auto read_q = [&](uint32_t stage) __attribute__((always_inline)) {
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) fq[tn][h] = lds_read<i32x4_t>((((tn & 1 ? lq1 : lq0) ^ (h * 16)) + stage * kStage) + (tn & ~1) * 128);
+      };
+      auto read_scales = [&](uint32_t stage) __attribute__((always_inline)) {
+        if constexpr (TN == 4) {
+          const float4_t v = lds_read<float4_t>(lsq + stage * (SCALE_DW * 4));
+          sq[0] = v.x; sq[1] = v.y; sq[2] = v.z; sq[3] = v.w;
+        } else {
+#pragma unroll
+          for (int tn = 0; tn < TN; ++tn) sq[tn] = lds_read<float>(lsq + stage * (SCALE_DW * 4) + tn * 4);
+        }
+        if constexpr (kBlockP) sb = lds_read<float>(lsp + stage * (SCALE_DW * 4));
+      };
+      auto read_sp = [&](uint32_t stage, int tm) __attribute__((always_inline)) {
+        if constexpr (!kBlockP) sp[tm % PR] = lds_read<float4_t>(lsp + stage * (SCALE_DW * 4) + p_row(tm, 0, 0) * 4);
+      };
+      auto decode_q = [&]() __attribute__((always_inline)) {
+        if constexpr (kExact) {
+#pragma unroll
+          for (int tn = 0; tn < TN; ++tn) fp8_to_f16(fq[tn][0], fq[tn][1], xq[tn]);
+          fp8_to_f16(fp[0][0], fp[0][1], xp[0]);
+        }
+      };
+      auto mma = [&](auto tmc) __attribute__((always_inline)) {
+        constexpr int tm = decltype(tmc)::value;
+        if constexpr (kExact) {
+          static_for<4>([&](auto kc) __attribute__((always_inline)) {
+            constexpr int k = decltype(kc)::value;
+            static_for<TN>([&](auto tnc) __attribute__((always_inline)) {
+              constexpr int tn = decltype(tnc)::value;
+              part[tm % 2][tn] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xp[tm % 2][k], xq[tn][k], k ? part[tm % 2][tn] : float4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
+            });
+          });
+        } else static_for<TN>([&](auto tnc) __attribute__((always_inline)) {
+          constexpr int tn = decltype(tnc)::value;
+          const i32x8_t a = __builtin_shufflevector(fp[tm % PR][0], fp[tm % PR][1], 0, 1, 2, 3, 4, 5, 6, 7);
+          const i32x8_t b = __builtin_shufflevector(fq[tn][0], fq[tn][1], 0, 1, 2, 3, 4, 5, 6, 7);
+          part[tm % 2][tn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, float4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+        });
+      };
+      auto add = [&](auto tmc) __attribute__((always_inline)) {
+        constexpr int tm = decltype(tmc)::value;
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (kBlockP) acc[tm][tn][r] = fmaf(part[tm % 2][tn][r], sq[tn], acc[tm][tn][r]);
+            else acc[tm][tn][r] = fmaf(part[tm % 2][tn][r] * sq[tn], sp[tm % PR][r], acc[tm][tn][r]);
+          }
+      };
+      auto scale_q = [&]() __attribute__((always_inline)) {
+        if constexpr (kBlockP) {
+#pragma unroll
+          for (int tn = 0; tn < TN; ++tn) sq[tn] *= sb;
+        }
+      };
+      begin(0);
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) load(i);
+      advance();
+      tile_barrier();
+      begin(1);
+      uint32_t st = 0, at = items.at;
+      constexpr int SPAN = TM >= 4 ? TM / 2 : 1;  // rows over which the next loads are dealt out
+      for (;;) {
+        read_q(st);
+        read_scales(st);
+        read_p(st, 0);
+        read_sp(st, 0);
+        if constexpr (TM > 1) read_p(st, 1);
+#pragma nounroll
+        for (; now.c < now.c1; ++now.c) {
+          decode_q();
+          static_for<TM>([&](auto tmc) __attribute__((always_inline)) {
+            constexpr int tm = decltype(tmc)::value;
+            mma(tmc);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (kExact && tm + 1 < TM) fp8_to_f16(fp[(tm + 1) % PR][0], fp[(tm + 1) % PR][1], xp[(tm + 1) % 2]);
+            if constexpr (tm < SPAN) {
+#pragma unroll
+              for (int i = 0; i < LOADS; ++i)
+                if (i * SPAN / LOADS == tm) load(i);
+              if constexpr (tm == SPAN - 1) advance();
+            }
+            if constexpr (tm == 0) scale_q();
+            if constexpr (tm > 0) add(std::integral_constant<int, tm - 1>{});
+            if constexpr (tm + 1 < TM) read_sp(st, tm + 1);
+            if constexpr (tm + 2 < TM) read_p(st, tm + 2);
+          });
+          tile_barrier();
+          begin(st);
+          st ^= 1u;
+          read_q(st);
+          read_p(st, 0);
+          if constexpr (TM > 1) read_p(st, 1);
+          add(std::integral_constant<int, TM - 1>{});
+          read_scales(st);
+          read_sp(st, 0);
+        }
+        epilogue((int64_t)now.tp * BM, (int64_t)now.tq * BN, now.z, acc);
+        at += items.step;
+        if (at >= items.end) break;
+        now.set(items, at);
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+          for (int tn = 0; tn < TN; ++tn) acc[tm][tn] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+      tile_barrier();  // nothing is in flight into LDS when the caller goes on
+      return;
+    }
     // Fragments of step s of a chunk: piece 2 g + s of the lane's rows.  P's are
     // kept once: those of the next step are read into a tile's registers as soon
     // as its instructions have issued.  Q's, which every tile needs, twice.
@@ -368,13 +580,6 @@ struct Tile {
     // while in rp, rq before they are paired, which would wait for the read
     constexpr int NSP = (TM + 1) / 2, NSQ = (TN + 1) / 2;
     uint32_t sp[NSP], sq[NSQ], rp[TM], rq[TN];
-    const int pr0 = wm * TM * 16, qr0 = BM + wn * TN * 16;
-    const int pk = p_key(p_row(0, n >> 2, n & 3)), qk = q_key(q_row(0, n));
-    // LDS byte addresses; the two steps' pieces are neighbours, 16 bytes apart
-    const uint32_t lp = lds_address(sm.stage[0]) + (uint32_t)(pr0 + p_row(0, n >> 2, n & 3)) * 128u + ((2 * g) ^ pk) * 16;
-    // even and odd tiles of Q: a lane's rows trade places in pairs
-    const uint32_t lq0 = lds_address(sm.stage[0]) + (uint32_t)(qr0 + q_place(q_row(0, n))) * 128u + ((2 * g) ^ qk) * 16;
-    const uint32_t lq1 = lds_address(sm.stage[0]) + (uint32_t)(qr0 + q_place(q_row(TN > 1 ? 1 : 0, n))) * 128u + ((2 * g) ^ qk) * 16;
     const uint32_t lsp = lds_address(sm.scale[0]) + (uint32_t)(pr0 + p_row(0, n >> 2, n & 3)) * 8u + 2 * g;
     const uint32_t lsq = lds_address(sm.scale[0]) + (uint32_t)(qr0 + q_row(0, n)) * 8u + 2 * g;
     auto read_p = [&](uint32_t stage, int s, int tm) __attribute__((always_inline)) {
@@ -402,7 +607,7 @@ struct Tile {
       constexpr int s = decltype(sc)::value, tm = decltype(tmc)::value;
       static_for<TN>([&](auto tnc) __attribute__((always_inline)) {
         constexpr int tn = decltype(tnc)::value;
-        if constexpr (EL == EL_BF16) {
+        if constexpr (EL != EL_MX) {
           acc[tm][tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, fp[tm]),
                                                                 __builtin_bit_cast(bf16x8_t, fq[s][tn]), acc[tm][tn], 0, 0, 0);
         } else {

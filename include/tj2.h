@@ -47,6 +47,7 @@ typedef int32_t tj2_status;
 #define TJ2_FP8 3
 #define TJ2_NVFP6 4 /* E2M3 elements in the NVFP4 double block (the FP6 x FP4 variant) */
 #define TJ2_MXFP4 5 /* E2M1 elements under one power-of-two scale per 32 (microscaled; the mxfp4_ entry points) */
+#define TJ2_FP8_BLOCK 6 /* E4M3FN elements under one FP32 scale per 128 x 128 (the fp8_ entry points) */
 
 /* grouping of a quantizer */
 #define TJ2_GROUP_ROW 0 /* 1x16 groups along the contiguous (column) dimension   */
@@ -81,6 +82,9 @@ typedef int32_t tj2_status;
  *              scale16  uint8 [rows][nb*4]   one byte b per 32 elements, the scale
  *                                            2^(b - 127); 255 is NaN
  *              scale128 unused (may be NULL)
+ *   TJ2_FP8_BLOCK: codes    uint8 [rows][nb*128] E4M3FN
+ *                  scale16  unused (may be NULL)
+ *                  scale128 float [ceil(rows/128)][nb], one per 128 x 128
  * Element positions beyond `len` in each row are padding; producers write
  * them as zero.  `len` must be a positive multiple of 16 (TJ2_MXFP4: any
  * positive length).
@@ -695,6 +699,100 @@ tj2_status tj2_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_
                             const void* teacher, int32_t k, float temperature, float alpha, const int64_t* targets,
                             int64_t ignore_index, const float* weight, float* loss, void* dlogits, int64_t ldd,
                             void* stream);
+
+/*
+ * FP8 linears: E4M3FN elements under one fp32 scale per 128 elements of a row (TJ2_FP8:
+ * activations, gradients) or per 128 x 128 (TJ2_FP8_BLOCK: weights), multiplied as they
+ * are stored.  Operands are at most 2^22 elements long.
+ *
+ * fp8_quantize: a logical [rows, cols] tensor, cols a multiple of 16, dense (x_dtype
+ * TJ2_BF16 / TJ2_F32, contiguous) or, for TJ2_GROUP_COL, FP8 (x_dtype TJ2_FP8, *x_q,
+ * dequantized first; *out must not be *x_q).  TJ2_GROUP_ROW: *out is [rows, cols], TJ2_FP8
+ * or TJ2_FP8_BLOCK (rows need not be a multiple of 128); TJ2_GROUP_COL: groups along rows
+ * (a multiple of 16), *out is [cols, rows], TJ2_FP8.  Per group with largest magnitude a:
+ * scale S = fl(a / 448), elements fl(x fl(1 / S)), not beyond +-448, to the nearest E4M3
+ * value, ties to even; a below 2^-100: scale 0 and codes +-0.  These are the codes of
+ * nvfp4_quantize with a TJ2_FP8 result.  A group that holds an infinity or NaN gets the
+ * scale NaN and zero codes.
+ */
+tj2_status fp8_quantize(const void* x, int32_t x_dtype, const tj2_qtensor* x_q, int64_t rows, int64_t cols, int32_t grouping,
+                        tj2_qtensor* out, void* stream);
+
+/* The values fl(q S) of q (either format) as out [rows, len], contiguous, TJ2_F32 or TJ2_BF16 (rounded to the nearest). */
+tj2_status fp8_dequantize(const tj2_qtensor* q, void* out, int32_t out_dtype, void* stream);
+
+/*
+ * C[i, j] (+)= sum_k A[i, k] B[j, k], A [I, K] TJ2_FP8 and B [J, K] TJ2_FP8 or
+ * TJ2_FP8_BLOCK.  The 128 products of a chunk are summed in fp32 and multiplied by the
+ * two scales, B's first with A's where it is a block's (a product of scales below 2^-126
+ * loses bits), then added in fp32.  A NaN scale in a row of A (or B, or a block) makes
+ * that row (column, columns) of C NaN.  c_dtype TJ2_F32 or TJ2_BF16 (nearest), ldc >= J
+ * in elements; accumulate != 0 adds into C (TJ2_F32 only).
+ * workspace: partial sums of a reduction that is split because C has few tiles,
+ * fp8_gemm_workspace_size(I, J, K) bytes (0: none needed); NULL runs unsplit, a smaller
+ * non-NULL workspace is TJ2_ERR_ARG.  The order of the sums depends on the sizes and on
+ * whether a workspace is given, and on nothing else.
+ */
+tj2_status fp8_gemm(const tj2_qtensor* A, const tj2_qtensor* B, void* C, int32_t c_dtype, int64_t ldc, int32_t accumulate,
+                    void* workspace, size_t ws_bytes, void* stream);
+size_t fp8_gemm_workspace_size(int64_t I, int64_t J, int64_t K);
+
+/*
+ * Forward of a linear layer Y = X W^T on FP8 operands: X [M, K] bf16 (or NULL: *Xq as
+ * given, a norm's result for one) to *Xq (TJ2_FP8, saved for the backward), W_master
+ * [N, K] fp32 (or NULL: *Wq as given) to *Wq (TJ2_FP8_BLOCK), Y [M, N] TJ2_BF16 or
+ * TJ2_F32, contiguous.  Any M >= 1; K and N multiples of 16.  workspace as for fp8_gemm,
+ * with fp8_linear_fwd_workspace_size(M, N, K).
+ */
+tj2_status fp8_linear_fwd(const void* X, int64_t M, int64_t K, int64_t N, const float* W_master, tj2_qtensor* Wq, tj2_qtensor* Xq,
+                          void* Y, int32_t y_dtype, void* workspace, size_t ws_bytes, void* stream);
+size_t fp8_linear_fwd_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * Its backward from dY [M, N] bf16 and the forward's quantized tensors:
+ *   dX [M, K] (TJ2_BF16 or TJ2_F32) = Q(dY) W-hat,  W's codes and scales as they are;
+ *   dW [N, K] fp32                  = Q(dY^T) Q(X-hat^T),  both grouped along the tokens.
+ * M, N and K at most 2^22.
+ * workspace: fp8_linear_bwd_workspace_size(M, N, K) bytes, 16-byte aligned, required.
+ */
+tj2_status fp8_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, const tj2_qtensor* Xq, const tj2_qtensor* Wq, void* dX,
+                          int32_t dx_dtype, float* dW, void* workspace, size_t ws_bytes, void* stream);
+size_t fp8_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * Root-mean-square norm with the residual's addition.
+ *
+ * tj2_rms_norm_fwd: x (and residual, which may be NULL) [rows, cols] of dtype TJ2_BF16 or
+ * TJ2_F32 with rows ldx (ldr) elements apart, any cols up to 2^22, weight [cols] of w_dtype
+ * (either type):
+ *   s = x + residual, rounded to dtype, into sum [rows, cols], contiguous (given with
+ *       residual and only then; it may be residual or x itself where that is contiguous);
+ *       without a residual s is x;
+ *   rstd[row] = 1 / sqrt(mean(s^2) + eps)  (fp32 [rows], may be NULL; needed for the backward);
+ *   y = s rstd weight into y [rows, cols] of dtype, contiguous, or (y NULL) *yq, TJ2_FP8,
+ *       quantized as fp8_quantize does from the unrounded fp32 values.
+ * For yq, cols is a multiple of 16 and x, residual, their rows, sum and weight are 16-byte
+ * aligned; else pointers are aligned to their elements.  Statistics are fp32: squares that
+ * leave its range are infinite (rstd 0) or 0.  eps >= 0; a row of zeros with eps 0 is NaN.
+ */
+tj2_status tj2_rms_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, int32_t dtype, int64_t rows, int64_t cols,
+                            const void* weight, int32_t w_dtype, float eps, void* sum, void* y, tj2_qtensor* yq, float* rstd,
+                            void* stream);
+
+/*
+ * tj2_rms_norm_bwd: from dy, the gradient of y, and s, weight and rstd of the forward
+ *   ds = rstd (dy weight - s rstd mean(dy weight s rstd)) + dsum,  [rows, cols] of dtype,
+ *        contiguous: the gradient of x and of residual; dsum (may be NULL) is what comes
+ *        in for s itself; ds may be dy or dsum itself where that is contiguous;
+ *   dw = sum over the rows of dy s rstd, [cols] of w_dtype, summed in fp32 in an order that
+ *        only the sizes decide.
+ * Either may be NULL.  workspace: tj2_rms_norm_bwd_workspace_size(rows, cols) bytes,
+ * 16-byte aligned, for dw.
+ */
+tj2_status tj2_rms_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, int32_t dtype, int64_t rows, int64_t cols,
+                            const void* weight, int32_t w_dtype, const float* rstd, const void* dsum, int64_t ldd, void* ds, void* dw,
+                            void* workspace, size_t ws_bytes, void* stream);
+size_t tj2_rms_norm_bwd_workspace_size(int64_t rows, int64_t cols);
 
 #ifdef __cplusplus
 }
