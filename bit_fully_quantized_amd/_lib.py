@@ -18,6 +18,7 @@ TJ2_OK, TJ2_ERR_ARG, TJ2_ERR_SHAPE, TJ2_ERR_ALIGN, TJ2_ERR_HIP, TJ2_ERR_UNSUPPOR
 BF16, F32, NVFP4, FP8, NVFP6, MXFP4, FP8_BLOCK = 0, 1, 2, 3, 4, 5, 6
 GROUP_ROW, GROUP_COL = 0, 1
 RTN, SR = 0, 1
+SILU, GELU, GELU_TANH = 0, 1, 2
 OSCI_INIT, OSCI_ACCUM, OSCI_WINDOW_END = 0, 1, 2
 
 STATUS_NAMES = {0: "TJ2_OK", 1: "TJ2_ERR_ARG", 2: "TJ2_ERR_SHAPE", 3: "TJ2_ERR_ALIGN", 4: "TJ2_ERR_HIP",
@@ -138,6 +139,10 @@ SIGNATURES = {
     "tj2_rms_norm_fwd": (I32, [P, I64, P, I64, I32, I64, I64, P, I32, ctypes.c_float, P, P, QP, P, P]),
     "tj2_rms_norm_bwd": (I32, [P, I64, P, I64, I32, I64, I64, P, I32, P, P, I64, P, P, P, SZ, P]),
     "tj2_rms_norm_bwd_workspace_size": (SZ, [I64, I64]),
+    "tj2_gated_ffn_fwd": (I32, [P, I64, P, P, I64, P, I64, I64, I64, I64, I32, P, P, I32, P, SZ, P]),
+    "tj2_gated_ffn_fwd_workspace_size": (SZ, [I64, I64, I64]),
+    "tj2_gated_ffn_bwd": (I32, [P, I64, P, I64, P, P, I64, P, I64, I64, I64, I64, I32, P, P, I32, P, P, P, I32, P, SZ, P]),
+    "tj2_gated_ffn_bwd_workspace_size": (SZ, [I64, I64, I64]),
     "tj2_distill_topk": (I32, [P, I32, I64, I64, I64, P, P, I32, ctypes.c_float, ctypes.c_float, P, I64, P, P, P, I64, P]),
 }
 

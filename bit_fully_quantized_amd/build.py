@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libtj2.so")
-SOURCES = ["api.hip", "quant.hip", "gemm.hip", "osci.hip", "mx.hip", "loss.hip", "fp8.hip", "norm.hip"]
+SOURCES = ["api.hip", "quant.hip", "gemm.hip", "osci.hip", "mx.hip", "loss.hip", "fp8.hip", "norm.hip", "ffn.hip"]
 MEASURE_LIB_PATH = os.path.join(HERE, "libtj2_measure.so")
 MEASURE_SOURCES = ["measure.hip"]
 

@@ -1605,3 +1605,92 @@ tj2_status tj2_rms_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t
 }
 
 }  // extern "C"
+
+// ---- gated feed-forward block (ffn.hip) --------------------------------------------------------
+namespace {
+
+// (256 rows of any operand, also the transposed ones, are addressed with 31-bit byte offsets)
+tj2_status check_ffn(const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, const void* Wd, int64_t ldd, int64_t T,
+                     int64_t D, int64_t F, int32_t act) {
+  if (!X || !Wg || !Wu || !Wd) return fail(TJ2_ERR_ARG, "X, Wg, Wu and Wd are required");
+  if (act != TJ2_SILU && act != TJ2_GELU && act != TJ2_GELU_TANH) return fail(TJ2_ERR_ARG, "bad activation %d", act);
+  TJ2_TRY(check_linear_dims(T, F, D));
+  constexpr int64_t most = (int64_t)1 << 21;
+  if (T > most || D > most || F > most || ldx > most || ldw > most || ldd > most)
+    return fail(TJ2_ERR_SHAPE, "T, D, F and the pitches are at most 2^21");
+  if (T * F > (int64_t)1 << 36 || T * D > (int64_t)1 << 36 || D * F > (int64_t)1 << 36)
+    return fail(TJ2_ERR_SHAPE, "T * F, T * D and D * F are at most 2^36");
+  if (ldx < D || ldw < D || ldd < F || ldx % 8 || ldw % 8 || ldd % 8)
+    return fail(TJ2_ERR_SHAPE, "ldx, ldw and ldd must be multiples of 8 and hold a row");
+  if (!aligned16(X) || !aligned16(Wg) || !aligned16(Wu) || !aligned16(Wd)) return fail(TJ2_ERR_ALIGN, "X, Wg, Wu and Wd must be 16-byte aligned");
+  return TJ2_OK;
+}
+
+FfnParams ffn_params(const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, const void* Wd, int64_t ldd, int64_t T,
+                     int64_t D, int64_t F, int32_t act) {
+  FfnParams f = {};
+  f.X = X;
+  f.Wg = Wg;
+  f.Wu = Wu;
+  f.Wd = Wd;
+  f.T = T;
+  f.D = D;
+  f.F = F;
+  f.ldx = ldx;
+  f.ldw = ldw;
+  f.ldd = ldd;
+  f.act = act;
+  return f;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tj2_gated_ffn_fwd_workspace_size(int64_t T, int64_t D, int64_t F) {
+  if (T <= 0 || D <= 0 || F <= 0) return 0;
+  return ffn_fwd_workspace_bytes(T, D, F);
+}
+
+tj2_status tj2_gated_ffn_fwd(const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, const void* Wd, int64_t ldd,
+                             int64_t T, int64_t D, int64_t F, int32_t act, void* gu, void* Y, int32_t y_dtype, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  TJ2_TRY(check_ffn(X, ldx, Wg, Wu, ldw, Wd, ldd, T, D, F, act));
+  if (!Y) return fail(TJ2_ERR_ARG, "Y is NULL");
+  TJ2_TRY(check_out_dtype(y_dtype, "y_dtype"));
+  if (!aligned16(Y) || !aligned16(gu)) return fail(TJ2_ERR_ALIGN, "Y and gu must be 16-byte aligned");
+  TJ2_TRY(check_ce_workspace(workspace, ws_bytes, ffn_fwd_workspace_bytes(T, D, F)));
+  FfnParams f = ffn_params(X, ldx, Wg, Wu, ldw, Wd, ldd, T, D, F, act);
+  f.gu = gu;
+  f.Y = Y;
+  f.y_dtype = y_dtype;
+  TJ2_TRY(hip_check(launch_ffn_fwd(f, workspace, (hipStream_t)stream), "feed-forward launch"));
+  return ok();
+}
+
+size_t tj2_gated_ffn_bwd_workspace_size(int64_t T, int64_t D, int64_t F) {
+  if (T <= 0 || D <= 0 || F <= 0) return 0;
+  return ffn_bwd_workspace_bytes(T, D, F);
+}
+
+tj2_status tj2_gated_ffn_bwd(const void* dY, int64_t ldy, const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw,
+                             const void* Wd, int64_t ldd, int64_t T, int64_t D, int64_t F, int32_t act, const void* gu, void* dX,
+                             int32_t dx_dtype, void* dWg, void* dWu, void* dWd, int32_t dw_dtype, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  TJ2_TRY(check_ffn(X, ldx, Wg, Wu, ldw, Wd, ldd, T, D, F, act));
+  if (!dY || !gu) return fail(TJ2_ERR_ARG, "dY and gu are required");
+  if (!dX && !dWg && !dWu && !dWd) return fail(TJ2_ERR_ARG, "dX, dWg, dWu or dWd is required");
+  if (ldy < D || ldy % 8 || ldy > (int64_t)1 << 21) return fail(TJ2_ERR_SHAPE, "ldy must be a multiple of 8, at least D and at most 2^21");
+  if (dX) TJ2_TRY(check_out_dtype(dx_dtype, "dx_dtype"));
+  if (dWg || dWu || dWd) TJ2_TRY(check_out_dtype(dw_dtype, "dw_dtype"));
+  if (!aligned16(dY) || !aligned16(gu) || !aligned16(dX) || !aligned16(dWg) || !aligned16(dWu) || !aligned16(dWd))
+    return fail(TJ2_ERR_ALIGN, "dY, gu, dX, dWg, dWu and dWd must be 16-byte aligned");
+  TJ2_TRY(check_ce_workspace(workspace, ws_bytes, ffn_bwd_workspace_bytes(T, D, F)));
+  FfnParams f = ffn_params(X, ldx, Wg, Wu, ldw, Wd, ldd, T, D, F, act);
+  f.gu = const_cast<void*>(gu);
+  const FfnGradParams o = {dY, ldy, dX, dWg, dWu, dWd, dx_dtype, dw_dtype};
+  TJ2_TRY(hip_check(launch_ffn_bwd(f, o, workspace, (hipStream_t)stream), "feed-forward launch"));
+  return ok();
+}
+
+}  // extern "C"

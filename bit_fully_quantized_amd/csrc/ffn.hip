@@ -1,0 +1,798 @@
+// The gated feed-forward block for gfx950 in bf16:
+//
+//   G = X Wg^T, U = X Wu^T, H = act(G) * U, Y = H Wd^T,
+//   dH = dY Wd, dG = dH U act'(G), dU = dH act(G),
+//   dX = dG Wg + dU Wu, dWg = dG^T X, dWu = dU^T X, dWd = dY^T H.
+//
+// Both projections are one tile product whose tiles hold as many rows of either weight
+// (EL_PAIR), so a lane has a gate and its factor together and the activation and the
+// product cost no pass of their own; G and U are written only for a backward pass.  There
+// the product dH has an epilogue that reads G and U and writes dG and dU in the two
+// layouts that the four products after it read, and H transposed; those four run in one
+// launch.  Sums and the activation are fp32; H, dG and dU are rounded to bf16, the type of
+// the operands, where a product takes them.  G and U are kept in 24 bits (fp32's sign,
+// exponent and 15 bits): in bf16 their rounding would enter dX and dW as much as that of
+// dG and dU does (3.0e-3 of dX's norm in all instead of 2.4e-3, 3.5e-3 of dWd's), and f16
+// would not hold what bf16 activations reach.
+#include <math.h>
+
+#include <algorithm>
+
+#include "tj2_bf16.h"
+
+namespace tj2 {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct Act {
+  float a, d;  // act(g), act'(g)
+};
+template <int ACT>
+__device__ __forceinline__ Act activate(float g) {
+  if constexpr (ACT == TJ2_SILU) {
+    const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * g));
+    return {g * p, p * fmaf(g, 1.0f - p, 1.0f)};
+  } else if constexpr (ACT == TJ2_GELU) {
+    // g Phi(g); from |g| = 14 on, where the density is 0 in fp32, its argument is kept finite
+    const float p = 0.5f * erfcf(-0.70710678118654752440f * g), c = __builtin_amdgcn_fmed3f(g, -14.0f, 14.0f);
+    return {g * p, fmaf(c * 0.39894228040143267794f, __builtin_amdgcn_exp2f(-0.5f * kLog2e * c * c), p)};
+  } else {
+    // (1 + tanh z) / 2 is the logistic function of 2 z; where it is 0 or 1, so is its
+    // slope 0, and the polynomial is kept finite
+    const float c = __builtin_amdgcn_fmed3f(g, -64.0f, 64.0f);
+    const float k = 1.59576912160573071176f, z = k * fmaf(0.044715f * c * c, c, c);
+    const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
+    return {g * p, fmaf(c * p * (1.0f - p), k * fmaf(0.134145f * c, c, 1.0f), p)};
+  }
+}
+
+// G and U as the backward pass reads them: the upper 16 bits of fp32 [2][T][F], then the
+// next 8 [2][T][F], rounded to the nearest (a NaN stays one: it is made a quiet one).
+struct Saved {
+  uint16_t *g, *u;
+  uint8_t *gl, *ul;
+};
+__device__ __forceinline__ uint32_t round24(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return v != v ? b | 0x00400000u : b + 0x80u;
+}
+template <int N>  // 2, 8 or 16 neighbours
+__device__ __forceinline__ void save24(uint16_t* hi, uint8_t* lo, const float* v) {
+  uint32_t h[N / 2], l[(N + 3) / 4];
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    const uint32_t a = round24(v[k]), b = round24(v[k + 1]);
+    h[k / 2] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+    const uint32_t two = __builtin_amdgcn_perm(b, a, 0x0C0C0501u);
+    l[k / 4] = k % 4 ? l[k / 4] | two << 16 : two;
+  }
+  if constexpr (N == 2) {
+    *reinterpret_cast<uint32_t*>(hi) = h[0];
+    *reinterpret_cast<uint16_t*>(lo) = (uint16_t)l[0];
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; k += 8) {
+      *reinterpret_cast<uint4*>(hi + k) = uint4{h[k / 2], h[k / 2 + 1], h[k / 2 + 2], h[k / 2 + 3]};
+      *reinterpret_cast<uint2*>(lo + k) = uint2{l[k / 4], l[k / 4 + 1]};
+    }
+  }
+}
+// value k (0..7) of 8 neighbours
+__device__ __forceinline__ float value24(const uint4& hi, const uint2& lo, int k) {
+  const uint32_t h = k < 2 ? hi.x : k < 4 ? hi.y : k < 6 ? hi.z : hi.w, l = k < 4 ? lo.x : lo.y;
+  // bytes: 0, l[k % 4], h's half k % 2
+  return __uint_as_float(__builtin_amdgcn_perm(h, l, (k & 1 ? 0x07060000u : 0x05040000u) | (uint32_t)(k & 3) << 8 | 0x0Cu));
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return uint4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+}
+
+// ---- both projections, the activation and the product ----------------------------------
+struct GateArgs {
+  TileOp P, Q;       // P: Wg and Wu [F, D], Q: X [T, D]
+  uint32_t tiles_p, tiles_q;
+  int32_t nch, nf;   // nf: chunks of 64 features of H
+  uint16_t* h;       // [T, F], blocked
+  Saved s;           // for the backward pass, or NULL
+};
+
+template <class T, int ACT>
+__global__ __launch_bounds__(T::NT, T::WAVES) void ffn_gate_kernel(GateArgs p) {
+  static_assert(T::kTM == 2 * T::PB, "a lane's first PB tiles are gates");
+  __shared__ __attribute__((aligned(128))) typename T::Smem sm;
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, 1);
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  constexpr int N = 4 * T::PB;  // neighbouring features of a lane
+  T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t, typename T::Acc& acc) __attribute__((always_inline)) {
+    const int64_t f = p0 / 2 + (w / T::kWN) * 16 * T::PB + g * N, t0 = q0 + (w % T::kWN) * T::kTN * 16;
+    if (f >= p.P.rows) return;  // (F is a multiple of 16: a lane's features are all there or none is)
+#pragma unroll
+    for (int tn = 0; tn < T::kTN; ++tn) {
+      const int64_t t = t0 + T::q_row(tn, n);
+      if (t >= p.Q.rows) continue;
+      float v[N];
+      if (p.s.g) {
+        const int64_t at = t * p.P.rows + f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int k = 0; k < N; ++k) v[k] = acc[half * T::PB + k / 4][tn][k % 4];
+          save24<N>((half ? p.s.u : p.s.g) + at, (half ? p.s.ul : p.s.gl) + at, v);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = activate<ACT>(acc[k / 4][tn][k % 4]).a * acc[T::PB + k / 4][tn][k % 4];
+      uint16_t* o = p.h + ((t >> 7) * p.nf + (f >> 6)) * 8192 + (t & 127) * 64 + (f & 63);
+#pragma unroll
+      for (int k = 0; k < N; k += 8) *reinterpret_cast<uint4*>(o + k) = pack8(v + k);
+    }
+  });
+}
+
+// The same for up to 64 tokens: one read of the weights, 8 rows of each a wave (lane n
+// holds a gate's row where n & 2 is 0), so that a lane's four results are two gates and
+// their factors.  H is row-major.
+struct GateFewArgs {
+  const uint16_t *x, *wg, *wu;
+  int64_t ldx, ldw;
+  int32_t T, D, F;
+  uint16_t* h;
+  Saved s;
+};
+constexpr int kFewLds = 66 * 1024;
+template <int TN>
+__host__ __device__ constexpr int64_t few_pitch(int64_t D) { return (D * 2 + 127) / 128 * 128 + 16; }
+template <int TN, int ACT>
+__global__ __launch_bounds__(256, 2) void ffn_gate_few_kernel(GateFewArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t xs[kFewLds];
+  constexpr int U = 4;  // chunks of 64 features in flight
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int px = (int)few_pitch<TN>(p.D), pieces = (p.D + 63) / 64 * 8;
+  for (int i = threadIdx.x; i < 16 * TN * pieces; i += 256) {
+    const int t = i / pieces, c = (i - t * pieces) * 8;
+    uint4 v = {0u, 0u, 0u, 0u};
+    if (t < p.T && c < p.D) v = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + c);
+    *reinterpret_cast<uint4*>(xs + t * px + c * 2) = v;
+  }
+  __syncthreads();
+  const uint32_t groups = (uint32_t)(p.F + 7) / 8, waves = gridDim.x * 4, chunks = (uint32_t)(p.D + 63) / 64;
+  struct Batch {
+    i32x4_t a[U][2];
+  };
+  const uint16_t* wrow = (n & 2 ? p.wu : p.wg) + (2 * (n >> 2) + (n & 1)) * p.ldw + g * 16;
+  auto fetch = [&](Batch& f, uint32_t gr, uint32_t c0) __attribute__((always_inline)) {
+    const uint16_t* w = wrow + (int64_t)gr * 8 * p.ldw;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = (int)(c0 + u) * 64 + h * 8;
+        f.a[u][h] = i32x4_t{0, 0, 0, 0};
+        // (F is a multiple of 16: a group's rows are all there)
+        if (gr < groups && k + g * 16 < p.D) f.a[u][h] = *reinterpret_cast<const i32x4_t*>(w + k);
+      }
+  };
+  const uint8_t* xl = xs + n * px + g * 32;
+  float4_t acc[TN] = {};
+  auto multiply = [&](const Batch& f, uint32_t c0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c0 + u >= chunks) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn)
+          acc[tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8_t, f.a[u][h]),
+              *reinterpret_cast<const bf16x8_t*>(xl + tn * 16 * px + (c0 + u) * 128 + h * 16), acc[tn], 0, 0, 0);
+    }
+  };
+  uint32_t gr = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = 0;
+  if (gr >= groups) return;
+  Batch f0, f1;
+  fetch(f0, gr, 0);
+  auto turn = [&](const Batch& now, Batch& next) __attribute__((always_inline)) -> bool {
+    const bool last = c + U >= chunks;
+    const uint32_t ng = last ? gr + waves : gr, nc = last ? 0 : c + U;
+    fetch(next, ng, nc);
+    multiply(now, c);
+    if (last) {
+      const int64_t f = (int64_t)gr * 8 + 2 * g;
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn) {
+        const int t = tn * 16 + n;
+        if (t < p.T) {
+          const float4_t v = acc[tn];
+          *reinterpret_cast<uint32_t*>(p.h + (int64_t)t * p.F + f) = bf16_pair(activate<ACT>(v.x).a * v.z, activate<ACT>(v.y).a * v.w);
+          if (p.s.g) {
+            const int64_t at = (int64_t)t * p.F + f;
+            const float gv[2] = {v.x, v.y}, uv[2] = {v.z, v.w};
+            save24<2>(p.s.g + at, p.s.gl + at, gv);
+            save24<2>(p.s.u + at, p.s.ul + at, uv);
+          }
+        }
+        acc[tn] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+    }
+    gr = ng;
+    c = nc;
+    return gr < groups;
+  };
+  while (turn(f0, f1) && turn(f1, f0)) {
+  }
+}
+
+// Y = H Wd^T of up to 64 tokens: a workgroup takes 16 rows of Wd, its 16 waves the
+// reduction in turn, joined in LDS.
+struct DownFewArgs {
+  const uint16_t *h, *wd;
+  int64_t ldw;
+  int32_t T, D, F;
+  void* y;
+  int32_t bf16;
+};
+template <int TN>
+__global__ __launch_bounds__(1024) void ffn_down_few_kernel(DownFewArgs p) {
+  __shared__ float sh[16][16 * TN][17];
+  const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int d0 = blockIdx.x * 16, steps = (p.F + 31) / 32;
+  const int s0 = steps * wave / 16, s1 = steps * (wave + 1) / 16;
+  const uint16_t* w = p.wd + (int64_t)(d0 + n) * p.ldw + g * 8;  // (D is a multiple of 16)
+  float4_t acc[TN] = {};
+  constexpr int U = 4;
+  for (int s = s0; s < s1; s += U) {
+    i32x4_t a[U], b[U][TN];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (s + u) * 32;
+      const bool in = s + u < s1 && k + g * 8 < p.F;
+      a[u] = i32x4_t{0, 0, 0, 0};
+      if (in) a[u] = *reinterpret_cast<const i32x4_t*>(w + k);
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn) {
+        b[u][tn] = i32x4_t{0, 0, 0, 0};
+        if (in && tn * 16 + n < p.T) b[u][tn] = *reinterpret_cast<const i32x4_t*>(p.h + (int64_t)(tn * 16 + n) * p.F + k + g * 8);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+        acc[tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a[u]), __builtin_bit_cast(bf16x8_t, b[u][tn]), acc[tn], 0, 0, 0);
+  }
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sh[wave][tn * 16 + n][4 * g + r] = acc[tn][r];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 256 * TN; i += 1024) {
+    const int t = i >> 4, d = i & 15;
+    float v = sh[0][t][d];
+#pragma unroll
+    for (int k = 1; k < 16; ++k) v += sh[k][t][d];
+    if (t >= p.T) continue;
+    const int64_t at = (int64_t)t * p.D + d0 + d;
+    if (p.bf16) reinterpret_cast<uint16_t*>(p.y)[at] = (uint16_t)bf16_pair(v, 0.0f);
+    else reinterpret_cast<float*>(p.y)[at] = v;
+  }
+}
+
+// ---- dH and what follows from it ---------------------------------------------------------
+struct DhArgs {
+  TileOp P, Q;            // P: Wd^T [F, D], Q: dY [T, D]
+  uint32_t tiles_p, tiles_q;
+  int32_t nch, nf, nt;    // nf, nt: chunks of 64 features and of 64 tokens
+  Saved s;                // G and U
+  uint16_t* d;            // [T, dG | dU] blocked, nf chunks each, zero past the last feature; or NULL
+  uint16_t *gt, *ut, *ht; // dG, dU, H transposed [F, T] blocked, zero past the last token; gt or ht NULL
+};
+
+template <class T, int ACT>
+__global__ __launch_bounds__(T::NT, T::WAVES) void ffn_dh_kernel(DhArgs p) {
+  static_assert(T::kTN == 4 && T::PB == 4, "64 tokens, and features 16 a lane");
+  __shared__ __attribute__((aligned(128))) typename T::Smem sm;
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, 1);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
+  T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t, typename T::Acc& acc) __attribute__((always_inline)) {
+    const int64_t F = p.P.rows, pw = p0 + (w / T::kWN) * T::kTM * 16, qw = q0 + (w % T::kWN) * 64, t0 = qw + n * 4;
+    const int ct = (int)(qw >> 6);
+    static_assert(16 * T::kTM <= 128 && 128 % (16 * T::kTM) == 0, "a wave's features are of one block");
+#pragma unroll
+    for (int tb = 0; tb < T::kTM / 4; ++tb) {
+      const int64_t f = pw + tb * 64 + g * 16;  // this lane's 16 features
+      const bool in = f < F;
+      const int64_t turned = ((pw >> 7) * p.nt + ct) * 8192 + (f & 127) * 64 + n * 4;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint4 gv[4], uv[4];
+        uint2 gl[4], ul[4];
+#pragma unroll
+        for (int tn = 0; tn < 4; ++tn) {
+          gv[tn] = uv[tn] = uint4{0u, 0u, 0u, 0u};
+          gl[tn] = ul[tn] = uint2{0u, 0u};
+          if (in && t0 + tn < p.Q.rows) {
+            const int64_t at = (t0 + tn) * F + f + half * 8;
+            gv[tn] = *reinterpret_cast<const uint4*>(p.s.g + at);
+            uv[tn] = *reinterpret_cast<const uint4*>(p.s.u + at);
+            gl[tn] = *reinterpret_cast<const uint2*>(p.s.gl + at);
+            ul[tn] = *reinterpret_cast<const uint2*>(p.s.ul + at);
+          }
+        }
+        static_for<2>([&](auto jc) __attribute__((always_inline)) {
+          constexpr int j = decltype(jc)::value;
+          const int tm = tb * 4 + half * 2 + j;
+          float dg[4][4], du[4][4], h[4][4];  // [token][feature]
+#pragma unroll
+          for (int tn = 0; tn < 4; ++tn) {
+            const bool there = in && t0 + tn < p.Q.rows;  // (zeros times a NaN of the operands would not be zero)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float gr = value24(gv[tn], gl[tn], j * 4 + r), ur = value24(uv[tn], ul[tn], j * 4 + r);
+              const Act a = activate<ACT>(gr);
+              const float dh = there ? acc[tm][tn][r] : 0.0f;
+              dg[tn][r] = dh * ur * a.d;
+              du[tn][r] = dh * a.a;
+              h[tn][r] = a.a * ur;
+            }
+            acc[tm][tn] = float4_t{__uint_as_float(bf16_pair(dg[tn][0], dg[tn][1])), __uint_as_float(bf16_pair(dg[tn][2], dg[tn][3])),
+                                   __uint_as_float(bf16_pair(du[tn][0], du[tn][1])), __uint_as_float(bf16_pair(du[tn][2], du[tn][3]))};
+          }
+          // transposed: four neighbouring tokens of a feature, 128 bytes over 16 lanes
+          if (in && ct < p.nt) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int64_t at = turned + (half * 8 + j * 4 + r) * 64;
+              if (p.gt) {
+                *reinterpret_cast<uint2*>(p.gt + at) = uint2{bf16_pair(dg[0][r], dg[1][r]), bf16_pair(dg[2][r], dg[3][r])};
+                *reinterpret_cast<uint2*>(p.ut + at) = uint2{bf16_pair(du[0][r], du[1][r]), bf16_pair(du[2][r], du[3][r])};
+              }
+              if (p.ht) *reinterpret_cast<uint2*>(p.ht + at) = uint2{bf16_pair(h[0][r], h[1][r]), bf16_pair(h[2][r], h[3][r])};
+            }
+          }
+        });
+      }
+      // as they are: 16 neighbouring features of a token
+      const int cd = (int)((pw + tb * 64) >> 6);
+      if (!p.d || cd >= p.nf) continue;
+#pragma unroll
+      for (int tn = 0; tn < 4; ++tn) {
+        const int64_t t = t0 + tn;
+        if (t >= p.Q.rows) continue;
+        uint16_t* o = p.d + ((t >> 7) * 2 * p.nf + cd) * 8192 + (t & 127) * 64 + g * 16;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float4_t a = acc[tb * 4 + half * 2][tn], b = acc[tb * 4 + half * 2 + 1][tn];
+          *reinterpret_cast<uint4*>(o + half * 8) = uint4{__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y)};
+          *reinterpret_cast<uint4*>(o + (int64_t)p.nf * 8192 + half * 8) =
+              uint4{__float_as_uint(a.z), __float_as_uint(a.w), __float_as_uint(b.z), __float_as_uint(b.w)};
+        }
+      }
+    }
+  });
+}
+
+// ---- products ----------------------------------------------------------------------------
+// D[q, p] = sum_k Q[q, k] P[p, k], up to four in one launch, each with workgroups of its
+// own; splits > 1: fp32 partial sums [z][q][p], joined by ffn_join_kernel.
+constexpr int kJobs = 4;
+struct FfnProduct {
+  TileOp P, Q;
+  uint32_t tiles_p, tiles_q;
+  int32_t nch, splits;
+  float* part;
+  void* out;  // rows of P.rows elements
+  int32_t bf16;
+};
+struct FfnProducts {
+  FfnProduct x[kJobs];
+  uint32_t first[kJobs];  // workgroup at which a job starts
+  int32_t n;
+};
+
+template <class T>
+__global__ __launch_bounds__(T::NT, T::WAVES) void ffn_product_kernel(FfnProducts jobs) {
+  __shared__ __attribute__((aligned(128))) typename T::Smem sm;
+  int job = 0;
+  while (job + 1 < jobs.n && blockIdx.x >= jobs.first[job + 1]) ++job;
+  const FfnProduct& p = jobs.x[job];
+  const uint32_t end = job + 1 < jobs.n ? jobs.first[job + 1] : gridDim.x;
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits, blockIdx.x - jobs.first[job], end - jobs.first[job]);
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t z, typename T::Acc& acc) __attribute__((always_inline)) {
+    const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 16, qw = q0 + (w % T::kWN) * T::kTN * 16;
+    static_assert(T::PB == 4, "rows of P 16 a lane");
+#pragma unroll
+    for (int tn = 0; tn < T::kTN; ++tn) {
+      const int64_t i = qw + T::q_row(tn, n);
+      if (i >= p.Q.rows) continue;
+#pragma unroll
+      for (int tb = 0; tb < T::kTM / 4; ++tb) {
+        const int64_t j = pw + tb * 64;
+        if (j >= p.P.rows) continue;  // (a multiple of 16)
+        if (p.splits == 1 && p.bf16) {
+          float v[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] = acc[tb * 4 + k / 4][tn][k % 4];
+          uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + i * p.P.rows + j;
+          *reinterpret_cast<uint4*>(o) = pack8(v);
+          *reinterpret_cast<uint4*>(o + 8) = pack8(v + 8);
+        } else {
+          float* o = p.splits == 1 ? reinterpret_cast<float*>(p.out) : p.part + (size_t)z * (size_t)(p.Q.rows * p.P.rows);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) *reinterpret_cast<float4_t*>(o + i * p.P.rows + j + 4 * k) = acc[tb * 4 + k][tn];
+        }
+      }
+    }
+  });
+}
+
+// The sums of the splits' results in order, 4 a thread.
+__global__ __launch_bounds__(256) void ffn_join_kernel(FfnProducts jobs) {
+  int job = 0;
+  while (job + 1 < jobs.n && blockIdx.x >= jobs.first[job + 1]) ++job;
+  const FfnProduct& p = jobs.x[job];
+  const int64_t n = p.Q.rows * p.P.rows, i = ((int64_t)(blockIdx.x - jobs.first[job]) * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  float4_t v = *reinterpret_cast<const float4_t*>(p.part + i);
+#pragma unroll 4
+  for (int z = 1; z < p.splits; ++z) v += *reinterpret_cast<const float4_t*>(p.part + (size_t)z * (size_t)n + i);
+  if (p.bf16) *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + i) = uint2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+  else *reinterpret_cast<float4_t*>(reinterpret_cast<float*>(p.out) + i) = v;
+}
+
+// Blocked copies and transposes, a workgroup per 64 x 64.
+constexpr int kBlocks = 5;
+struct FfnBlocks {
+  BlockArgs x[kBlocks];
+  uint32_t first[kBlocks];
+  int32_t n;
+};
+__global__ __launch_bounds__(256) void ffn_blocks_kernel(FfnBlocks jobs) {
+  int job = 0;
+  while (job + 1 < jobs.n && blockIdx.x >= jobs.first[job + 1]) ++job;
+  const BlockArgs& p = jobs.x[job];
+  const uint32_t b = blockIdx.x - jobs.first[job];
+  block_tile(p, b % p.nr, b / p.nr);
+}
+
+using TileBig = Tile<EL_BF16, 2, 4, 8, 4>;   // 256 x 256
+using TileMid = Tile<EL_BF16, 2, 2, 4, 4>;   // 128 x 128
+using PairBig = Tile<EL_PAIR, 2, 4, 8, 4>;   // 128 of either weight x 256
+using PairMid = Tile<EL_PAIR, 2, 2, 4, 4>;   // 64 of either weight x 128
+
+template <class T, class A>
+uint32_t set_tiles(A& a) {
+  a.tiles_p = (uint32_t)((a.P.rows + T::PROWS - 1) / T::PROWS);
+  a.tiles_q = (uint32_t)((a.Q.rows + T::BN - 1) / T::BN);
+  return a.tiles_p * a.tiles_q;
+}
+template <class F>
+void with_activation(int act, F&& f) {
+  if (act == TJ2_SILU) f(std::integral_constant<int, TJ2_SILU>{});
+  else if (act == TJ2_GELU) f(std::integral_constant<int, TJ2_GELU>{});
+  else f(std::integral_constant<int, TJ2_GELU_TANH>{});
+}
+
+// Tiles of 16 tokens of the few-token kernels, 0: none.
+int few_tiles(int64_t T, int64_t D) {
+  for (int tn = 1; tn <= 4; tn *= 2)
+    if (T <= 16 * tn && 16 * tn * few_pitch<1>(D) <= kFewLds) return tn;
+  return 0;
+}
+
+// Tile and splits of up to four products that run together: those of the least estimated
+// time.  Beyond one round of workgroups they are dealt out as places become free.
+struct FfnPlan {
+  bool big;
+  int splits[kJobs];
+};
+struct FfnSize {
+  int64_t p, q, k;
+};
+FfnPlan ffn_plan(const FfnSize* x, int n) {
+  FfnPlan best = {};
+  double least = 1e30;
+  for (int big = 0; big < 2; ++big) {
+    const double slots = big ? kCus : 2 * kCus, chunk = big ? 1.9 : 1.5, alone = big ? 1.9 : 1.1, fixed = big ? 6.0 : 3.0;
+    int64_t longest = 0;
+    for (int i = 0; i < n; ++i) longest = std::max(longest, (x[i].k + 63) / 64);
+    // every product in pieces of at most `most` chunks
+    for (int64_t most = longest; most >= 8 || most == longest; most = most * 2 / 3) {
+      FfnPlan c = {};
+      c.big = big;
+      double work = 0.0, tail = 0.0, join = 0.0, items = 0.0;
+      for (int i = 0; i < n; ++i) {
+        const int64_t nch = (x[i].k + 63) / 64;
+        c.splits[i] = (int)std::min<int64_t>((nch + most - 1) / most, 32);
+        const double t = (double)tiles_of(x[i].p, x[i].q, big ? 256 : 128) * c.splits[i], per = (double)((nch + c.splits[i] - 1) / c.splits[i]);
+        items += t;
+        work += t * (per * chunk + fixed);
+        tail = std::max(tail, per);
+        if (c.splits[i] > 1) join += (double)x[i].p * (double)x[i].q * 8.0 * c.splits[i] / 5e6;
+      }
+      double t = work / slots;
+      if (items <= (big ? slots : slots / 2)) t = tail * alone + fixed;  // one round
+      else t += 0.5 * (tail * chunk + fixed);                          // the last round is part empty
+      if (join > 0.0) t += join + 3.0;
+      if (t < least) {
+        least = t;
+        best = c;
+      }
+      if (most < 8) break;
+    }
+  }
+  return best;
+}
+size_t part_bytes(const FfnPlan& plan, const FfnSize* x, int n) {
+  size_t b = 0;
+  for (int i = 0; i < n; ++i)
+    if (plan.splits[i] > 1) b += up256((size_t)plan.splits[i] * (size_t)(x[i].p * x[i].q) * 4);
+  return b;
+}
+
+template <class T>
+void launch_products(FfnProducts& jobs, hipStream_t s) {
+  uint32_t items[kJobs], total = 0, grid = 0;
+  for (int i = 0; i < jobs.n; ++i) {
+    items[i] = set_tiles<T>(jobs.x[i]) * (uint32_t)jobs.x[i].splits;
+    total += items[i];
+  }
+  // few rounds: a workgroup an item, dealt out by the hardware; else each goes on itself
+  const bool each = total <= 8 * kCus * T::PER_CU;
+  for (int i = 0; i < jobs.n; ++i) {
+    jobs.first[i] = grid;
+    grid += each ? items[i] : T::grid(items[i]);
+  }
+  ffn_product_kernel<T><<<grid, T::NT, 0, s>>>(jobs);
+}
+
+// The products x under their plan, partial sums at `part`.
+hipError_t run_products(FfnProduct* x, const FfnSize* size, int n, float* part, hipStream_t s) {
+  const FfnPlan plan = ffn_plan(size, n);
+  FfnProducts jobs = {}, joins = {};
+  size_t at = 0;
+  // those with the longest tiles first
+  int order[kJobs] = {0, 1, 2, 3};
+  std::sort(order, order + n, [&](int a, int b) {
+    const int64_t ka = size[a].k / plan.splits[a], kb = size[b].k / plan.splits[b];
+    return ka != kb ? ka > kb : a < b;
+  });
+  for (int i = 0; i < n; ++i) {
+    x[i].nch = (int32_t)((size[i].k + 63) / 64);
+    x[i].splits = plan.splits[i];
+    if (x[i].splits > 1) {
+      x[i].part = part + at / 4;
+      at += up256((size_t)x[i].splits * (size_t)(size[i].p * size[i].q) * 4);
+    }
+  }
+  for (int i = 0; i < n; ++i) jobs.x[i] = x[order[i]];
+  jobs.n = n;
+  if (plan.big) launch_products<TileBig>(jobs, s);
+  else launch_products<TileMid>(jobs, s);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  uint32_t grid = 0;
+  for (int i = 0; i < n; ++i) {
+    if (x[i].splits == 1) continue;
+    joins.x[joins.n] = x[i];
+    joins.first[joins.n++] = grid;
+    grid += (uint32_t)((size[i].p * size[i].q / 4 + 255) / 256);
+  }
+  if (!grid) return hipSuccess;
+  ffn_join_kernel<<<grid, 256, 0, s>>>(joins);
+  return hipGetLastError();
+}
+
+hipError_t run_blocks(const BlockArgs* x, int n, hipStream_t s) {
+  FfnBlocks b = {};
+  uint32_t grid = 0;
+  for (int i = 0; i < n; ++i) {
+    b.x[i] = x[i];
+    b.first[i] = grid;
+    grid += x[i].nr * x[i].nc;
+  }
+  b.n = n;
+  if (!grid) return hipSuccess;
+  ffn_blocks_kernel<<<grid, 256, 0, s>>>(b);
+  return hipGetLastError();
+}
+
+Saved saved_of(const FfnParams& f) {
+  if (!f.gu) return Saved{};
+  const int64_t n = f.T * f.F;
+  uint16_t* hi = reinterpret_cast<uint16_t*>(f.gu);
+  uint8_t* lo = reinterpret_cast<uint8_t*>(hi + 2 * n);
+  return Saved{hi, hi + n, lo, lo + n};
+}
+
+// Of a product with an epilogue: 256 x 256 tiles or 128 x 128.
+bool big_tiles(int64_t p, int64_t q, int64_t k) {
+  const double chunks = (double)((k + 63) / 64);
+  return tile_time(true, tiles_of(p, q, 256), chunks, 9.0) < tile_time(false, tiles_of(p, q, 128), chunks, 9.0);
+}
+
+struct FfnFwdSpace {
+  size_t h, x, g, u, d, part, bytes;
+  bool blocked;
+  int few;
+  FfnFwdSpace(int64_t T, int64_t D, int64_t F) {
+    size_t at = 0;
+    auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
+    few = few_tiles(T, D);
+    blocked = T >= kBlockTokens;
+    h = take(few ? (size_t)(T * F * 2) : blocked_bytes(T, F));
+    x = take(blocked ? blocked_bytes(T, D) : 0);
+    g = take(blocked ? blocked_bytes(F, D) : 0);
+    u = take(blocked ? blocked_bytes(F, D) : 0);
+    d = take(blocked ? blocked_bytes(D, F) : 0);
+    const FfnSize y = {D, T, F};
+    part = take(few ? 0 : part_bytes(ffn_plan(&y, 1), &y, 1));
+    bytes = at;
+  }
+};
+
+struct FfnBwdSpace {
+  size_t wd, w, x, dy, dyb, d, gt, ut, ht, part, bytes;
+  bool blocked;
+  FfnBwdSpace(int64_t T, int64_t D, int64_t F) {
+    size_t at = 0;
+    auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
+    blocked = T >= kBlockTokens;
+    wd = take(blocked_bytes(F, D));
+    w = take(blocked_bytes(D, 2 * up(F, 64)));
+    x = take(blocked_bytes(D, T));
+    dy = take(blocked_bytes(D, T));
+    dyb = take(blocked ? blocked_bytes(T, D) : 0);
+    d = take(blocked_bytes(T, 2 * up(F, 64)));
+    gt = take(blocked_bytes(F, T));
+    ut = take(blocked_bytes(F, T));
+    ht = take(blocked_bytes(F, T));
+    size_t most = 0;
+    for (int want = 1; want < 8; ++want) {  // whichever gradients are asked for
+      FfnSize x4[kJobs];
+      const int n = sizes(T, D, F, want & 1, want & 2, want & 2, want & 4, x4);
+      most = std::max(most, part_bytes(ffn_plan(x4, n), x4, n));
+      const int m = sizes(T, D, F, want & 1, want & 2, false, want & 4, x4);
+      most = std::max(most, part_bytes(ffn_plan(x4, m), x4, m));
+    }
+    part = take(most);
+    bytes = at;
+  }
+  static int sizes(int64_t T, int64_t D, int64_t F, bool dx, bool dwg, bool dwu, bool dwd, FfnSize* x) {
+    int n = 0;
+    if (dx) x[n++] = FfnSize{D, T, 2 * up(F, 64)};
+    if (dwg) x[n++] = FfnSize{D, F, T};
+    if (dwu) x[n++] = FfnSize{D, F, T};
+    if (dwd) x[n++] = FfnSize{F, D, T};
+    return n;
+  }
+};
+
+}  // namespace
+
+#define TJ2_DO(call)                                     \
+  do {                                                   \
+    if (hipError_t e_ = (call); e_ != hipSuccess) return e_; \
+  } while (0)
+
+size_t ffn_fwd_workspace_bytes(int64_t T, int64_t D, int64_t F) { return FfnFwdSpace(T, D, F).bytes; }
+
+hipError_t launch_ffn_fwd(const FfnParams& f, void* ws, hipStream_t s) {
+  const FfnFwdSpace sp(f.T, f.D, f.F);
+  uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+  uint16_t* h = reinterpret_cast<uint16_t*>(w + sp.h);
+  if (sp.few) {
+    const GateFewArgs a = {reinterpret_cast<const uint16_t*>(f.X), reinterpret_cast<const uint16_t*>(f.Wg), reinterpret_cast<const uint16_t*>(f.Wu),
+                           f.ldx, f.ldw, (int32_t)f.T, (int32_t)f.D, (int32_t)f.F, h, saved_of(f)};
+    const DownFewArgs d = {h, reinterpret_cast<const uint16_t*>(f.Wd), f.ldd, (int32_t)f.T, (int32_t)f.D, (int32_t)f.F, f.Y, f.y_dtype == TJ2_BF16};
+    const uint32_t groups = (uint32_t)((f.F + 7) / 8), rounds = (groups + 8 * kCus - 1) / (8 * kCus), grid = (groups + rounds * 4 - 1) / (rounds * 4);
+    auto run = [&](auto tn) {
+      constexpr int TN = decltype(tn)::value;
+      with_activation(f.act, [&](auto act) { ffn_gate_few_kernel<TN, act.value><<<grid, 256, 0, s>>>(a); });
+      ffn_down_few_kernel<TN><<<(uint32_t)(f.D / 16), 1024, 0, s>>>(d);
+    };
+    if (sp.few == 1) run(std::integral_constant<int, 1>{});
+    else if (sp.few == 2) run(std::integral_constant<int, 2>{});
+    else run(std::integral_constant<int, 4>{});
+    return hipGetLastError();
+  }
+  GateArgs a = {};
+  TileOp wd;
+  if (sp.blocked) {
+    const BlockArgs b[4] = {block_args(f.X, f.T, f.D, f.ldx, w + sp.x, nullptr), block_args(f.Wg, f.F, f.D, f.ldw, w + sp.g, nullptr),
+                            block_args(f.Wu, f.F, f.D, f.ldw, w + sp.u, nullptr), block_args(f.Wd, f.D, f.F, f.ldd, w + sp.d, nullptr)};
+    TJ2_DO(run_blocks(b, 4, s));
+    a.P = blocked_operand(w + sp.g, f.F, f.D);
+    a.P.p2 = w + sp.u;
+    a.Q = blocked_operand(w + sp.x, f.T, f.D);
+    wd = blocked_operand(w + sp.d, f.D, f.F);
+  } else {
+    a.P = bf16_operand(f.Wg, f.F, f.D, f.ldw);
+    a.P.p2 = reinterpret_cast<const uint8_t*>(f.Wu);
+    a.Q = bf16_operand(f.X, f.T, f.D, f.ldx);
+    wd = bf16_operand(f.Wd, f.D, f.F, f.ldd);
+  }
+  a.nch = (int32_t)(up(f.D, 64) / 64);
+  a.nf = (int32_t)(up(f.F, 64) / 64);
+  a.h = h;
+  a.s = saved_of(f);
+  const bool big = big_tiles(2 * f.F, f.T, f.D);
+  with_activation(f.act, [&](auto act) {
+    if (big) {
+      const uint32_t items = set_tiles<PairBig>(a);
+      ffn_gate_kernel<PairBig, act.value><<<PairBig::grid(items), PairBig::NT, 0, s>>>(a);
+    } else {
+      const uint32_t items = set_tiles<PairMid>(a);
+      ffn_gate_kernel<PairMid, act.value><<<PairMid::grid(items), PairMid::NT, 0, s>>>(a);
+    }
+  });
+  TJ2_DO(hipGetLastError());
+  FfnProduct y = {};
+  y.P = wd;
+  y.Q = blocked_operand(h, f.T, f.F);
+  y.out = f.Y;
+  y.bf16 = f.y_dtype == TJ2_BF16;
+  const FfnSize size = {f.D, f.T, f.F};
+  return run_products(&y, &size, 1, reinterpret_cast<float*>(w + sp.part), s);
+}
+
+size_t ffn_bwd_workspace_bytes(int64_t T, int64_t D, int64_t F) { return FfnBwdSpace(T, D, F).bytes; }
+
+hipError_t launch_ffn_bwd(const FfnParams& f, const FfnGradParams& o, void* ws, hipStream_t s) {
+  const FfnBwdSpace sp(f.T, f.D, f.F);
+  uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+  const int64_t nf = up(f.F, 64) / 64;
+  const bool dw = o.dWg || o.dWu;
+  BlockArgs b[kBlocks];
+  int n = 0;
+  b[n++] = block_args(f.Wd, f.D, f.F, f.ldd, nullptr, w + sp.wd);
+  if (o.dX) {
+    b[n] = block_args(f.Wg, f.F, f.D, f.ldw, nullptr, w + sp.w);
+    b[n++].pitch = (uint32_t)(2 * nf);
+    b[n] = block_args(f.Wu, f.F, f.D, f.ldw, nullptr, w + sp.w + nf * 16384);
+    b[n++].pitch = (uint32_t)(2 * nf);
+  }
+  if (dw) b[n++] = block_args(f.X, f.T, f.D, f.ldx, nullptr, w + sp.x);
+  if (o.dWd || sp.blocked) b[n++] = block_args(o.dY, f.T, f.D, o.ldy, sp.blocked ? w + sp.dyb : nullptr, o.dWd ? w + sp.dy : nullptr);
+  TJ2_DO(run_blocks(b, n, s));
+  DhArgs a = {};
+  a.P = blocked_operand(w + sp.wd, f.F, f.D);
+  a.Q = sp.blocked ? blocked_operand(w + sp.dyb, f.T, f.D) : bf16_operand(o.dY, f.T, f.D, o.ldy);
+  a.nch = (int32_t)(up(f.D, 64) / 64);
+  a.nf = (int32_t)nf;
+  a.nt = (int32_t)(up(f.T, 64) / 64);
+  a.s = saved_of(f);
+  a.d = o.dX ? reinterpret_cast<uint16_t*>(w + sp.d) : nullptr;
+  a.gt = dw ? reinterpret_cast<uint16_t*>(w + sp.gt) : nullptr;
+  a.ut = reinterpret_cast<uint16_t*>(w + sp.ut);
+  a.ht = o.dWd ? reinterpret_cast<uint16_t*>(w + sp.ht) : nullptr;
+  const bool big = big_tiles(f.F, f.T, f.D);
+  with_activation(f.act, [&](auto act) {
+    if (big) {
+      const uint32_t items = set_tiles<TileBig>(a);
+      ffn_dh_kernel<TileBig, act.value><<<TileBig::grid(items), TileBig::NT, 0, s>>>(a);
+    } else {
+      const uint32_t items = set_tiles<TileMid>(a);
+      ffn_dh_kernel<TileMid, act.value><<<TileMid::grid(items), TileMid::NT, 0, s>>>(a);
+    }
+  });
+  TJ2_DO(hipGetLastError());
+  FfnProduct x[kJobs] = {};
+  FfnSize size[kJobs];
+  const int jobs = FfnBwdSpace::sizes(f.T, f.D, f.F, o.dX, o.dWg, o.dWu, o.dWd, size);
+  int k = 0;
+  auto product = [&](TileOp Q, TileOp P, void* out, int dtype) {
+    x[k].P = P;
+    x[k].Q = Q;
+    x[k].out = out;
+    x[k++].bf16 = dtype == TJ2_BF16;
+  };
+  if (o.dX) product(blocked_operand(w + sp.d, f.T, 2 * nf * 64), blocked_operand(w + sp.w, f.D, 2 * nf * 64), o.dX, o.dx_dtype);
+  if (o.dWg) product(blocked_operand(w + sp.gt, f.F, f.T), blocked_operand(w + sp.x, f.D, f.T), o.dWg, o.dw_dtype);
+  if (o.dWu) product(blocked_operand(w + sp.ut, f.F, f.T), blocked_operand(w + sp.x, f.D, f.T), o.dWu, o.dw_dtype);
+  if (o.dWd) product(blocked_operand(w + sp.dy, f.D, f.T), blocked_operand(w + sp.ht, f.F, f.T), o.dWd, o.dw_dtype);
+  return run_products(x, size, jobs, reinterpret_cast<float*>(w + sp.part), s);
+}
+
+}  // namespace tj2

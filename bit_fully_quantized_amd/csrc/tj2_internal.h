@@ -254,6 +254,27 @@ struct DistillParams {
 int distill_max_k();
 hipError_t launch_distill(const DistillParams& d, hipStream_t s);
 
+// The gated feed-forward block (ffn.hip): bf16 X [T, D] at pitch ldx, Wg and Wu [F, D] at
+// ldw, Wd [D, F] at ldd.
+struct FfnParams {
+  const void *X, *Wg, *Wu, *Wd;
+  int64_t T, D, F, ldx, ldw, ldd;
+  int act;
+  void* gu;  // G and U in 24 bits, 6 T F bytes: written by the forward (or NULL), read by the backward
+  void* Y;   // forward
+  int y_dtype;
+};
+struct FfnGradParams {
+  const void* dY;
+  int64_t ldy;
+  void *dX, *dWg, *dWu, *dWd;  // each optional
+  int dx_dtype, dw_dtype;
+};
+size_t ffn_fwd_workspace_bytes(int64_t T, int64_t D, int64_t F);
+hipError_t launch_ffn_fwd(const FfnParams& f, void* ws, hipStream_t s);
+size_t ffn_bwd_workspace_bytes(int64_t T, int64_t D, int64_t F);
+hipError_t launch_ffn_bwd(const FfnParams& f, const FfnGradParams& o, void* ws, hipStream_t s);
+
 // Root-mean-square norm with the residual's addition (norm.hip) and its backward pass.
 struct NormParams {
   const void *x, *residual;  // [rows, cols] at pitches ldx, ldr; residual may be NULL

@@ -57,6 +57,11 @@ typedef int32_t tj2_status;
 #define TJ2_RTN 0 /* round to nearest, ties to even (forward pass)            */
 #define TJ2_SR 1  /* stochastic rounding with Philox4x32-10 draws (backward)  */
 
+/* activations of the gated feed-forward block */
+#define TJ2_SILU 0      /* g / (1 + exp(-g))                                   */
+#define TJ2_GELU 1      /* g Phi(g), Phi the normal distribution's integral    */
+#define TJ2_GELU_TANH 2 /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2   */
+
 /* OsciReset modes */
 #define TJ2_OSCI_INIT 0
 #define TJ2_OSCI_ACCUM 1
@@ -793,6 +798,41 @@ tj2_status tj2_rms_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t
                             const void* weight, int32_t w_dtype, const float* rstd, const void* dsum, int64_t ldd, void* ds, void* dw,
                             void* workspace, size_t ws_bytes, void* stream);
 size_t tj2_rms_norm_bwd_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * The gated feed-forward block in bf16:
+ *   G = X Wg^T, U = X Wu^T, H = act(G) * U, Y = H Wd^T,
+ * X [T, D], Wg and Wu [F, D], Wd [D, F], with rows ldx, ldw (both), ldd elements apart
+ * (multiples of 8; 16-byte aligned).  D and F multiples of 16; T, D, F and the pitches at
+ * most 2^21, T * F at most 2^36.  Sums and the activation are fp32; H is rounded to bf16 for its product.
+ *
+ * tj2_gated_ffn_fwd: Y [T, D], contiguous, TJ2_BF16 or TJ2_F32; gu (may be NULL): 6 T F
+ * bytes that receive G and U, rounded to 24 bits (fp32 without its last 8), for the
+ * backward: their upper 16 bits [2][T][F], then the next 8 [2][T][F].  workspace: tj2_gated_ffn_fwd_workspace_size
+ * (T, D, F) bytes, 16-byte aligned, required (H, and from 2048 tokens on copies of X and the
+ * weights).
+ */
+tj2_status tj2_gated_ffn_fwd(const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, const void* Wd, int64_t ldd,
+                             int64_t T, int64_t D, int64_t F, int32_t act, void* gu, void* Y, int32_t y_dtype, void* workspace,
+                             size_t ws_bytes, void* stream);
+size_t tj2_gated_ffn_fwd_workspace_size(int64_t T, int64_t D, int64_t F);
+
+/*
+ * tj2_gated_ffn_bwd: from dY [T, D] (rows ldy apart) and the forward's gu
+ *   dH = dY Wd, dG = dH U act'(G), dU = dH act(G),
+ *   dX [T, D] = dG Wg + dU Wu, dWg, dWu [F, D] = dG^T X, dU^T X, dWd [D, F] = dY^T H,
+ * contiguous, dX of dx_dtype and the weights' of dw_dtype (TJ2_BF16 or TJ2_F32), each of
+ * the four may be NULL.  dG, dU and H (from gu) are rounded to bf16 for the products, also
+ * where fp32 gradients are asked for.  The results do not depend on scheduling.
+ * workspace: tj2_gated_ffn_bwd_workspace_size(T, D, F) bytes, 16-byte aligned, required,
+ * the same whichever gradients are asked for: dG and dU twice and H (10 T F bytes), copies
+ * of X, dY and the weights, and partial sums.
+ */
+tj2_status tj2_gated_ffn_bwd(const void* dY, int64_t ldy, const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw,
+                             const void* Wd, int64_t ldd, int64_t T, int64_t D, int64_t F, int32_t act, const void* gu, void* dX,
+                             int32_t dx_dtype, void* dWg, void* dWu, void* dWd, int32_t dw_dtype, void* workspace, size_t ws_bytes,
+                             void* stream);
+size_t tj2_gated_ffn_bwd_workspace_size(int64_t T, int64_t D, int64_t F);
 
 #ifdef __cplusplus
 }
