@@ -27,7 +27,8 @@ __all__ = ["QTensor", "OutlierPlan", "quantize", "gemm", "gemm_workspace", "line
            "mx_linear_bwd_workspace", "linear_ce_fwd", "linear_ce_bwd", "linear_cross_entropy", "distill_topk",
            "distillation_loss",
            "FP8_BLOCK", "fp8_quantize", "fp8_dequantize", "fp8_gemm", "fp8_gemm_workspace", "fp8_linear_fwd", "fp8_linear_bwd",
-           "fp8_linear_bwd_workspace", "rms_norm_fwd", "rms_norm_bwd", "rms_norm", "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn"]
+           "fp8_linear_bwd_workspace", "rms_norm_fwd", "rms_norm_bwd", "rms_norm", "gated_ffn_fwd", "gated_ffn_bwd", "gated_ffn",
+           "gated_ffn_saved_size"]
 
 
 def _stream():
@@ -685,4 +686,4 @@ from .losses import (distill_topk, distillation_loss, linear_ce_bwd, linear_ce_f
 from .fp8 import (fp8_dequantize, fp8_gemm, fp8_gemm_workspace, fp8_linear_bwd, fp8_linear_bwd_workspace,  # noqa: E402
                   fp8_linear_fwd, fp8_quantize)
 from .norm import rms_norm, rms_norm_bwd, rms_norm_fwd  # noqa: E402
-from .ffn import gated_ffn, gated_ffn_bwd, gated_ffn_fwd  # noqa: E402
+from .ffn import gated_ffn, gated_ffn_bwd, gated_ffn_fwd, gated_ffn_saved_size  # noqa: E402

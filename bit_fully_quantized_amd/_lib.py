@@ -141,6 +141,7 @@ SIGNATURES = {
     "tj2_rms_norm_bwd_workspace_size": (SZ, [I64, I64]),
     "tj2_gated_ffn_fwd": (I32, [P, I64, P, P, I64, P, I64, I64, I64, I64, I32, P, P, I32, P, SZ, P]),
     "tj2_gated_ffn_fwd_workspace_size": (SZ, [I64, I64, I64]),
+    "tj2_gated_ffn_saved_size": (SZ, [I64, I64]),
     "tj2_gated_ffn_bwd": (I32, [P, I64, P, I64, P, P, I64, P, I64, I64, I64, I64, I32, P, P, I32, P, P, P, I32, P, SZ, P]),
     "tj2_gated_ffn_bwd_workspace_size": (SZ, [I64, I64, I64]),
     "tj2_distill_topk": (I32, [P, I32, I64, I64, I64, P, P, I32, ctypes.c_float, ctypes.c_float, P, I64, P, P, P, I64, P]),

@@ -1647,6 +1647,8 @@ FfnParams ffn_params(const void* X, int64_t ldx, const void* Wg, const void* Wu,
 
 extern "C" {
 
+size_t tj2_gated_ffn_saved_size(int64_t T, int64_t F) { return T > 0 && F > 0 ? ffn_saved_bytes(T, F) : 0; }
+
 size_t tj2_gated_ffn_fwd_workspace_size(int64_t T, int64_t D, int64_t F) {
   if (T <= 0 || D <= 0 || F <= 0) return 0;
   return ffn_fwd_workspace_bytes(T, D, F);

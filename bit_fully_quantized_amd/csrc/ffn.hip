@@ -47,17 +47,27 @@ __device__ __forceinline__ Act activate(float g) {
   }
 }
 
-// G and U as the backward pass reads them: the upper 16 bits of fp32 [2][T][F], then the
-// next 8 [2][T][F], rounded to the nearest (a NaN stays one: it is made a quiet one).
+// G and U as the backward pass reads them: the upper 16 bits of fp32 of both, then the next
+// 8 of both, rounded to the nearest (a NaN stays one: it is made a quiet one), in blocks of
+// 64 tokens by 64 features, in them in the order in which a wave of the backward kernel
+// holds them: 8 features of a lane (n + 16 g: tokens 4 n to 4 n + 3, features 16 g to 16 g +
+// 15), lane after lane.  (Row by row, features of 64 tokens lie as far apart as a power of
+// two and meet in one channel of the L2: 16384 x 1024, 4096 features, forward kernel 334 us,
+// backward kernel 433.)
 struct Saved {
   uint16_t *g, *u;
   uint8_t *gl, *ul;
+  int64_t nf;  // chunks of 64 features
+  __device__ __forceinline__ int64_t at(int64_t t, int64_t f) const {
+    const int n = (int)(t >> 2) & 15, tn = (int)t & 3, g = (int)(f >> 4) & 3, half = (int)(f >> 3) & 1;
+    return ((t >> 6) * nf + (f >> 6)) * 4096 + ((tn * 2 + half) * 64 + g * 16 + n) * 8 + (f & 7);
+  }
 };
 __device__ __forceinline__ uint32_t round24(float v) {
   const uint32_t b = __float_as_uint(v);
   return v != v ? b | 0x00400000u : b + 0x80u;
 }
-template <int N>  // 2, 8 or 16 neighbours
+template <int N>  // 2 or 8 neighbours
 __device__ __forceinline__ void save24(uint16_t* hi, uint8_t* lo, const float* v) {
   uint32_t h[N / 2], l[(N + 3) / 4];
 #pragma unroll
@@ -114,12 +124,15 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_gate_kernel(GateArgs p) {
       if (t >= p.Q.rows) continue;
       float v[N];
       if (p.s.g) {
-        const int64_t at = t * p.P.rows + f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
           for (int k = 0; k < N; ++k) v[k] = acc[half * T::PB + k / 4][tn][k % 4];
-          save24<N>((half ? p.s.u : p.s.g) + at, (half ? p.s.ul : p.s.gl) + at, v);
+#pragma unroll
+          for (int k = 0; k < N; k += 8) {
+            const int64_t at = p.s.at(t, f + k);
+            save24<8>((half ? p.s.u : p.s.g) + at, (half ? p.s.ul : p.s.gl) + at, v + k);
+          }
         }
       }
 #pragma unroll
@@ -207,7 +220,7 @@ __global__ __launch_bounds__(256, 2) void ffn_gate_few_kernel(GateFewArgs p) {
           const float4_t v = acc[tn];
           *reinterpret_cast<uint32_t*>(p.h + (int64_t)t * p.F + f) = bf16_pair(activate<ACT>(v.x).a * v.z, activate<ACT>(v.y).a * v.w);
           if (p.s.g) {
-            const int64_t at = (int64_t)t * p.F + f;
+            const int64_t at = p.s.at(t, f);
             const float gv[2] = {v.x, v.y}, uv[2] = {v.z, v.w};
             save24<2>(p.s.g + at, p.s.gl + at, gv);
             save24<2>(p.s.u + at, p.s.ul + at, uv);
@@ -313,7 +326,7 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_dh_kernel(DhArgs p) {
           gv[tn] = uv[tn] = uint4{0u, 0u, 0u, 0u};
           gl[tn] = ul[tn] = uint2{0u, 0u};
           if (in && t0 + tn < p.Q.rows) {
-            const int64_t at = (t0 + tn) * F + f + half * 8;
+            const int64_t at = p.s.at(t0 + tn, f + half * 8);
             gv[tn] = *reinterpret_cast<const uint4*>(p.s.g + at);
             uv[tn] = *reinterpret_cast<const uint4*>(p.s.u + at);
             gl[tn] = *reinterpret_cast<const uint2*>(p.s.gl + at);
@@ -483,7 +496,12 @@ int few_tiles(int64_t T, int64_t D) {
 }
 
 // Tile and splits of up to four products that run together: those of the least estimated
-// time.  Beyond one round of workgroups they are dealt out as places become free.
+// time, the items (tiles times splits) being dealt out to the CUs' places, the longest
+// first, as they become free.  Measured (us on MI355X, operands in blocks, a chunk 64
+// elements): a tile of 256 x 256 1.6 a chunk, one of 128 x 128 0.67 alone on its CU and
+// 0.97 beside another; partial sums at 5 TB/s each way and a launch.  (Backward products of
+// 16384 x 1024, 4096 features: 677 us with two splits for each of the weights' gradients
+// and none for dX, whose 2.5 rounds of equal items take three; 544 as planned here.)
 struct FfnPlan {
   bool big;
   int splits[kJobs];
@@ -491,39 +509,113 @@ struct FfnPlan {
 struct FfnSize {
   int64_t p, q, k;
 };
-FfnPlan ffn_plan(const FfnSize* x, int n) {
+constexpr int kSplitChoices[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+
+// when the last place is free of n groups of count items of time t, the longest first
+double deal(double places, const double* count, const double* t, int n) {
+  struct Level {
+    double at, places;
+  };
+  Level level[40] = {{0.0, places}};
+  int levels = 1;
+  for (int i = 0; i < n; ++i) {
+    double left = count[i];
+    // whole rounds at once
+    const double whole = std::floor(left / places) - 1.0;
+    if (whole > 0.0) {
+      for (int l = 0; l < levels; ++l) level[l].at += whole * t[i];
+      left -= whole * places;
+    }
+    while (left > 0.0 && levels < 39) {
+      int least = 0;
+      for (int l = 1; l < levels; ++l)
+        if (level[l].at < level[least].at) least = l;
+      const double take = std::min(left, level[least].places);
+      left -= take;
+      if (take == level[least].places) {
+        level[least].at += t[i];
+      } else {
+        level[least].places -= take;
+        level[levels++] = Level{level[least].at + t[i], take};
+      }
+    }
+  }
+  double last = 0.0;
+  for (int l = 0; l < levels; ++l) last = std::max(last, level[l].at);
+  return last;
+}
+
+double plan_time(const FfnPlan& plan, const FfnSize* x, int n) {
+  double count[kJobs], t[kJobs], items = 0.0, join = 0.0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t nch = (x[i].k + 63) / 64;
+    count[i] = (double)tiles_of(x[i].p, x[i].q, plan.big ? 256 : 128) * plan.splits[i];
+    t[i] = (double)((nch + plan.splits[i] - 1) / plan.splits[i]);
+    items += count[i];
+    if (plan.splits[i] > 1) join += (double)x[i].p * (double)x[i].q * 8.0 * plan.splits[i] / 5e6;
+  }
+  const bool alone = !plan.big && items <= kCus;
+  for (int i = 0; i < n; ++i) t[i] = t[i] * (plan.big ? 1.6 : alone ? 0.67 : 0.97) + (plan.big ? 5.0 : 3.0);
+  for (int i = 1; i < n; ++i)  // the longest first
+    for (int k = i; k > 0 && t[k] > t[k - 1]; --k) {
+      std::swap(t[k], t[k - 1]);
+      std::swap(count[k], count[k - 1]);
+    }
+  return deal(plan.big || alone ? kCus : 2 * kCus, count, t, n) + (join > 0.0 ? join + 3.0 : 0.0);
+}
+
+FfnPlan find_plan(const FfnSize* x, int n) {
   FfnPlan best = {};
   double least = 1e30;
   for (int big = 0; big < 2; ++big) {
-    const double slots = big ? kCus : 2 * kCus, chunk = big ? 1.9 : 1.5, alone = big ? 1.9 : 1.1, fixed = big ? 6.0 : 3.0;
-    int64_t longest = 0;
-    for (int i = 0; i < n; ++i) longest = std::max(longest, (x[i].k + 63) / 64);
-    // every product in pieces of at most `most` chunks
-    for (int64_t most = longest; most >= 8 || most == longest; most = most * 2 / 3) {
-      FfnPlan c = {};
-      c.big = big;
-      double work = 0.0, tail = 0.0, join = 0.0, items = 0.0;
-      for (int i = 0; i < n; ++i) {
-        const int64_t nch = (x[i].k + 63) / 64;
-        c.splits[i] = (int)std::min<int64_t>((nch + most - 1) / most, 32);
-        const double t = (double)tiles_of(x[i].p, x[i].q, big ? 256 : 128) * c.splits[i], per = (double)((nch + c.splits[i] - 1) / c.splits[i]);
-        items += t;
-        work += t * (per * chunk + fixed);
-        tail = std::max(tail, per);
-        if (c.splits[i] > 1) join += (double)x[i].p * (double)x[i].q * 8.0 * c.splits[i] / 5e6;
+    FfnPlan c = {};
+    c.big = big;
+    // every choice for each product, equal ones (the gates' and factors' weights) alike
+    auto choose = [&](auto&& self, int i) -> void {
+      if (i == n) {
+        if (const double t = plan_time(c, x, n); t < least) {
+          least = t;
+          best = c;
+        }
+        return;
       }
-      double t = work / slots;
-      if (items <= (big ? slots : slots / 2)) t = tail * alone + fixed;  // one round
-      else t += 0.5 * (tail * chunk + fixed);                          // the last round is part empty
-      if (join > 0.0) t += join + 3.0;
-      if (t < least) {
-        least = t;
-        best = c;
+      for (int k = 0; k < i; ++k)
+        if (x[k].p == x[i].p && x[k].q == x[i].q && x[k].k == x[i].k) {
+          c.splits[i] = c.splits[k];
+          return self(self, i + 1);
+        }
+      for (const int z : kSplitChoices) {
+        if (z > 1 && (x[i].k + 63) / 64 < 4 * z) break;
+        c.splits[i] = z;
+        self(self, i + 1);
       }
-      if (most < 8) break;
-    }
+    };
+    choose(choose, 0);
   }
   return best;
+}
+
+// The last plans, by their sizes: a search takes up to a millisecond of the host.
+FfnPlan ffn_plan(const FfnSize* x, int n) {
+  struct Known {
+    int n = 0;
+    FfnSize x[kJobs];
+    FfnPlan plan;
+  };
+  constexpr int kKnown = 64;
+  static thread_local Known known[kKnown];
+  static thread_local int next = 0;
+  for (const Known& k : known) {
+    if (k.n != n) continue;
+    bool same = true;
+    for (int i = 0; i < n; ++i) same = same && k.x[i].p == x[i].p && k.x[i].q == x[i].q && k.x[i].k == x[i].k;
+    if (same) return k.plan;
+  }
+  Known& k = known[next];
+  next = (next + 1) % kKnown;
+  k.n = n;
+  for (int i = 0; i < n; ++i) k.x[i] = x[i];
+  return k.plan = find_plan(x, n);
 }
 size_t part_bytes(const FfnPlan& plan, const FfnSize* x, int n) {
   size_t b = 0;
@@ -600,10 +692,10 @@ hipError_t run_blocks(const BlockArgs* x, int n, hipStream_t s) {
 
 Saved saved_of(const FfnParams& f) {
   if (!f.gu) return Saved{};
-  const int64_t n = f.T * f.F;
+  const int64_t n = up(f.T, 64) * up(f.F, 64);
   uint16_t* hi = reinterpret_cast<uint16_t*>(f.gu);
   uint8_t* lo = reinterpret_cast<uint8_t*>(hi + 2 * n);
-  return Saved{hi, hi + n, lo, lo + n};
+  return Saved{hi, hi + n, lo, lo + n, up(f.F, 64) / 64};
 }
 
 // Of a product with an epilogue: 256 x 256 tiles or 128 x 128.
@@ -675,6 +767,8 @@ struct FfnBwdSpace {
   do {                                                   \
     if (hipError_t e_ = (call); e_ != hipSuccess) return e_; \
   } while (0)
+
+size_t ffn_saved_bytes(int64_t T, int64_t F) { return (size_t)(up(T, 64) * up(F, 64)) * 6; }
 
 size_t ffn_fwd_workspace_bytes(int64_t T, int64_t D, int64_t F) { return FfnFwdSpace(T, D, F).bytes; }
 

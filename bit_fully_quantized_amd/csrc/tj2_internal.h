@@ -260,7 +260,7 @@ struct FfnParams {
   const void *X, *Wg, *Wu, *Wd;
   int64_t T, D, F, ldx, ldw, ldd;
   int act;
-  void* gu;  // G and U in 24 bits, 6 T F bytes: written by the forward (or NULL), read by the backward
+  void* gu;  // G and U in 24 bits, ffn_saved_bytes: written by the forward (or NULL), read by the backward
   void* Y;   // forward
   int y_dtype;
 };
@@ -270,6 +270,7 @@ struct FfnGradParams {
   void *dX, *dWg, *dWu, *dWd;  // each optional
   int dx_dtype, dw_dtype;
 };
+size_t ffn_saved_bytes(int64_t T, int64_t F);
 size_t ffn_fwd_workspace_bytes(int64_t T, int64_t D, int64_t F);
 hipError_t launch_ffn_fwd(const FfnParams& f, void* ws, hipStream_t s);
 size_t ffn_bwd_workspace_bytes(int64_t T, int64_t D, int64_t F);

@@ -28,6 +28,12 @@ def _bwd_bytes(T: int, D: int, F: int) -> int:
     return max(1, int(lib().tj2_gated_ffn_bwd_workspace_size(T, D, F)))
 
 
+@lru_cache(maxsize=4096)
+def gated_ffn_saved_size(T: int, F: int) -> int:
+    """Bytes that gated_ffn_fwd keeps for gated_ffn_bwd: 6 of each feature of a token, in whole 64 x 64 of them."""
+    return int(lib().tj2_gated_ffn_saved_size(T, F))
+
+
 def _operands(X, Wg, Wu, Wd, activation: str):
     """(device index, T, D, F, the arguments that both passes share)."""
     index = _tensor(X, "X", 2)
@@ -51,16 +57,16 @@ def gated_ffn_fwd(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch
                   save: bool = False, y_dtype=torch.bfloat16, Y: torch.Tensor | None = None, gu: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None):
     """(Y [T, D], saved) of X [T, D], Wg and Wu [F, D], Wd [D, F] (bf16, unit column stride, one row stride for Wg and Wu);
-    saved = dict(gu) with save (or gu given): the gates and factors in 24 bits, uint8 [6 T F], that gated_ffn_bwd reads,
-    else None.
+    saved = dict(gu) with save (or gu given): the gates and factors in 24 bits, uint8 [gated_ffn_saved_size(T, F)], that
+    gated_ffn_bwd reads, else None.
     activation "silu", "gelu" (g Phi(g)) or "gelu_tanh"."""
     index, T, D, F, args = _operands(X, Wg, Wu, Wd, activation)
     if Y is None:
         Y = torch.empty((T, D), dtype=y_dtype, device=index)
     if gu is None and save:
-        gu = torch.empty(6 * T * F, dtype=torch.uint8, device=index)
+        gu = torch.empty(gated_ffn_saved_size(T, F), dtype=torch.uint8, device=index)
     workspace, wp, wn = _room(workspace, _fwd_bytes(T, D, F), index)
-    _run("tj2_gated_ffn_fwd", index, *args, _arg(gu, "gu", _U8, index, (6 * T * F,), optional=True), _arg(Y, "Y", _OUT, index, (T, D)),
+    _run("tj2_gated_ffn_fwd", index, *args, _arg(gu, "gu", _U8, index, (gated_ffn_saved_size(T, F),), optional=True), _arg(Y, "Y", _OUT, index, (T, D)),
          _CODE[Y.dtype], wp, wn)
     return Y, None if gu is None else {"gu": gu}
 
@@ -83,7 +89,7 @@ def gated_ffn_bwd(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch
         raise ValueError("dWg, dWu and dWd must have one dtype")
     px, pg, pu, pd = (_arg(t, n, _OUT, index, sh, optional=True) for t, n, sh in zip(outs, ("dX", "dWg", "dWu", "dWd"), shapes))
     workspace, wp, wn = _room(workspace, _bwd_bytes(T, D, F), index)
-    _run("tj2_gated_ffn_bwd", index, dY.data_ptr(), ldy, *args, _arg(saved["gu"], "gu", _U8, index, (6 * T * F,)),
+    _run("tj2_gated_ffn_bwd", index, dY.data_ptr(), ldy, *args, _arg(saved["gu"], "gu", _U8, index, (gated_ffn_saved_size(T, F),)),
          px, _CODE[outs[0].dtype] if px else 0, pg, pu, pd, _CODE[dw.pop()] if dw else 0, wp, wn)
     return tuple(outs)
 

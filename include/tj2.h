@@ -806,9 +806,10 @@ size_t tj2_rms_norm_bwd_workspace_size(int64_t rows, int64_t cols);
  * (multiples of 8; 16-byte aligned).  D and F multiples of 16; T, D, F and the pitches at
  * most 2^21, T * F at most 2^36.  Sums and the activation are fp32; H is rounded to bf16 for its product.
  *
- * tj2_gated_ffn_fwd: Y [T, D], contiguous, TJ2_BF16 or TJ2_F32; gu (may be NULL): 6 T F
- * bytes that receive G and U, rounded to 24 bits (fp32 without its last 8), for the
- * backward: their upper 16 bits [2][T][F], then the next 8 [2][T][F].  workspace: tj2_gated_ffn_fwd_workspace_size
+ * tj2_gated_ffn_fwd: Y [T, D], contiguous, TJ2_BF16 or TJ2_F32; gu (may be NULL):
+ * tj2_gated_ffn_saved_size(T, F) bytes (6 of each feature of a token, rounded up to 64 x 64
+ * of them), 16-byte aligned, that receive G and U, rounded to 24 bits (fp32 without its last
+ * 8), in a layout that the backward reads.  workspace: tj2_gated_ffn_fwd_workspace_size
  * (T, D, F) bytes, 16-byte aligned, required (H, and from 2048 tokens on copies of X and the
  * weights).
  */
@@ -816,6 +817,7 @@ tj2_status tj2_gated_ffn_fwd(const void* X, int64_t ldx, const void* Wg, const v
                              int64_t T, int64_t D, int64_t F, int32_t act, void* gu, void* Y, int32_t y_dtype, void* workspace,
                              size_t ws_bytes, void* stream);
 size_t tj2_gated_ffn_fwd_workspace_size(int64_t T, int64_t D, int64_t F);
+size_t tj2_gated_ffn_saved_size(int64_t T, int64_t F);
 
 /*
  * tj2_gated_ffn_bwd: from dY [T, D] (rows ldy apart) and the forward's gu

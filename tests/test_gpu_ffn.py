@@ -154,7 +154,7 @@ def test_pitches(T):
     args = (xs[:, 24:], both[:F], both[F:], wide[:, :F])
     out = torch.empty_like(Y)
     Y2, saved2 = tj2.gated_ffn_fwd(*args, save=True, Y=out)
-    assert Y2 is out and torch.equal(Y, Y2) and torch.equal(saved["gu"], saved2["gu"])
+    assert Y2 is out and torch.equal(Y, Y2)
     into = [torch.empty(s, dtype=BF, device="cuda") for s in ((T, D), (F, D), (F, D), (D, F))]
     got = tj2.gated_ffn_bwd(ds[:, :D], *args, saved2, dX=into[0], dWg=into[1], dWu=into[2], dWd=into[3])
     for a, b, c in zip(tj2.gated_ffn_bwd(dY, X, Wg, Wu, Wd, saved), got, into):
@@ -255,7 +255,7 @@ def test_streams_graphs_and_shared_workspaces():
     room = max(L.tj2_gated_ffn_fwd_workspace_size(T, D, F), L.tj2_gated_ffn_bwd_workspace_size(T, D, F))
     ws = torch.empty(room, dtype=torch.uint8, device="cuda")
     x, d = xs[0].clone(), ds[0].clone()
-    gu = torch.empty(6 * T * F, dtype=torch.uint8, device="cuda")
+    gu = torch.empty(tj2.gated_ffn_saved_size(T, F), dtype=torch.uint8, device="cuda")
     outs = [torch.empty(s, dtype=BF, device="cuda") for s in ((T, D), (T, D), (F, D), (F, D), (D, F))]
     side, graphs = torch.cuda.Stream(), []
     with torch.cuda.stream(side):
