@@ -144,7 +144,7 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_gate_kernel(GateArgs p) {
   });
 }
 
-// The same for up to 64 tokens: one read of the weights, 8 rows of each a wave (lane n
+// The same for up to 32 tokens: one read of the weights, 8 rows of each a wave (lane n
 // holds a gate's row where n & 2 is 0), so that a lane's four results are two gates and
 // their factors.  H is row-major.
 struct GateFewArgs {
@@ -154,23 +154,15 @@ struct GateFewArgs {
   uint16_t* h;
   Saved s;
 };
-constexpr int kFewLds = 66 * 1024;
-template <int TN>
+// LDS bytes of a token: whole chunks and 16 bytes, so that 16 tokens' pieces lie in different banks
 __host__ __device__ constexpr int64_t few_pitch(int64_t D) { return (D * 2 + 127) / 128 * 128 + 16; }
 template <int TN, int ACT>
 __global__ __launch_bounds__(256, 2) void ffn_gate_few_kernel(GateFewArgs p) {
-  __shared__ __attribute__((aligned(16))) uint8_t xs[kFewLds];
-  constexpr int U = 4;  // chunks of 64 features in flight
+  extern __shared__ __attribute__((aligned(16))) uint8_t xs[];  // [T][few_pitch(D)]
+  constexpr int U = 8;  // chunks of 64 features in flight
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-  const int px = (int)few_pitch<TN>(p.D), pieces = (p.D + 63) / 64 * 8;
-  for (int i = threadIdx.x; i < 16 * TN * pieces; i += 256) {
-    const int t = i / pieces, c = (i - t * pieces) * 8;
-    uint4 v = {0u, 0u, 0u, 0u};
-    if (t < p.T && c < p.D) v = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + c);
-    *reinterpret_cast<uint4*>(xs + t * px + c * 2) = v;
-  }
-  __syncthreads();
-  const uint32_t groups = (uint32_t)(p.F + 7) / 8, waves = gridDim.x * 4, chunks = (uint32_t)(p.D + 63) / 64;
+  const int px = (int)few_pitch(p.D), pieces = (p.D + 63) / 64 * 8;
+  const uint32_t groups = (uint32_t)(p.F + 7) / 8, per = blockDim.x >> 6, waves = gridDim.x * per, chunks = (uint32_t)(p.D + 63) / 64;
   struct Batch {
     i32x4_t a[U][2];
   };
@@ -187,7 +179,9 @@ __global__ __launch_bounds__(256, 2) void ffn_gate_few_kernel(GateFewArgs p) {
         if (gr < groups && k + g * 16 < p.D) f.a[u][h] = *reinterpret_cast<const i32x4_t*>(w + k);
       }
   };
-  const uint8_t* xl = xs + n * px + g * 32;
+  const uint8_t* xl[TN];  // (columns past the last token repeat it and are not stored)
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn) xl[tn] = xs + min(tn * 16 + n, p.T - 1) * px + g * 32;
   float4_t acc[TN] = {};
   auto multiply = [&](const Batch& f, uint32_t c0) __attribute__((always_inline)) {
 #pragma unroll
@@ -199,13 +193,21 @@ __global__ __launch_bounds__(256, 2) void ffn_gate_few_kernel(GateFewArgs p) {
         for (int tn = 0; tn < TN; ++tn)
           acc[tn] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               __builtin_bit_cast(bf16x8_t, f.a[u][h]),
-              *reinterpret_cast<const bf16x8_t*>(xl + tn * 16 * px + (c0 + u) * 128 + h * 16), acc[tn], 0, 0, 0);
+              *reinterpret_cast<const bf16x8_t*>(xl[tn] + (c0 + u) * 128 + h * 16), acc[tn], 0, 0, 0);
     }
   };
-  uint32_t gr = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = 0;
-  if (gr >= groups) return;
+  uint32_t gr = blockIdx.x * per + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = 0;
   Batch f0, f1;
   fetch(f0, gr, 0);
+  // the tokens, while the first weights are on their way
+  for (int i = threadIdx.x; i < p.T * pieces; i += blockDim.x) {
+    const int t = i / pieces, k = (i - t * pieces) * 8;
+    uint4 v = {0u, 0u, 0u, 0u};
+    if (k < p.D) v = *reinterpret_cast<const uint4*>(p.x + t * p.ldx + k);
+    *reinterpret_cast<uint4*>(xs + t * px + k * 2) = v;
+  }
+  __syncthreads();
+  if (gr >= groups) return;
   auto turn = [&](const Batch& now, Batch& next) __attribute__((always_inline)) -> bool {
     const bool last = c + U >= chunks;
     const uint32_t ng = last ? gr + waves : gr, nc = last ? 0 : c + U;
@@ -237,12 +239,14 @@ __global__ __launch_bounds__(256, 2) void ffn_gate_few_kernel(GateFewArgs p) {
   }
 }
 
-// Y = H Wd^T of up to 64 tokens: a workgroup takes 16 rows of Wd, its 16 waves the
+// Y = H Wd^T of up to 32 tokens: a workgroup takes 4 to 16 rows of Wd (fewer than the
+// instruction's 16 so that more CUs read: 1 token of D 1024, F
+// 4096 14.0 us with both kernels' waves on 64 to 128 CUs, 9.7 on all), its 16 waves the
 // reduction in turn, joined in LDS.
 struct DownFewArgs {
   const uint16_t *h, *wd;
   int64_t ldw;
-  int32_t T, D, F;
+  int32_t T, D, F, rows;
   void* y;
   int32_t bf16;
 };
@@ -250,7 +254,7 @@ template <int TN>
 __global__ __launch_bounds__(1024) void ffn_down_few_kernel(DownFewArgs p) {
   __shared__ float sh[16][16 * TN][17];
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int d0 = blockIdx.x * 16, steps = (p.F + 31) / 32;
+  const int d0 = blockIdx.x * p.rows, steps = (p.F + 31) / 32;
   const int s0 = steps * wave / 16, s1 = steps * (wave + 1) / 16;
   const uint16_t* w = p.wd + (int64_t)(d0 + n) * p.ldw + g * 8;  // (D is a multiple of 16)
   float4_t acc[TN] = {};
@@ -262,7 +266,7 @@ __global__ __launch_bounds__(1024) void ffn_down_few_kernel(DownFewArgs p) {
       const int k = (s + u) * 32;
       const bool in = s + u < s1 && k + g * 8 < p.F;
       a[u] = i32x4_t{0, 0, 0, 0};
-      if (in) a[u] = *reinterpret_cast<const i32x4_t*>(w + k);
+      if (in && n < p.rows) a[u] = *reinterpret_cast<const i32x4_t*>(w + k);
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn) {
         b[u][tn] = i32x4_t{0, 0, 0, 0};
@@ -285,7 +289,7 @@ __global__ __launch_bounds__(1024) void ffn_down_few_kernel(DownFewArgs p) {
     float v = sh[0][t][d];
 #pragma unroll
     for (int k = 1; k < 16; ++k) v += sh[k][t][d];
-    if (t >= p.T) continue;
+    if (t >= p.T || d >= p.rows) continue;
     const int64_t at = (int64_t)t * p.D + d0 + d;
     if (p.bf16) reinterpret_cast<uint16_t*>(p.y)[at] = (uint16_t)bf16_pair(v, 0.0f);
     else reinterpret_cast<float*>(p.y)[at] = v;
@@ -488,12 +492,17 @@ void with_activation(int act, F&& f) {
   else f(std::integral_constant<int, TJ2_GELU_TANH>{});
 }
 
-// Tiles of 16 tokens of the few-token kernels, 0: none.
-int few_tiles(int64_t T, int64_t D) {
-  for (int tn = 1; tn <= 4; tn *= 2)
-    if (T <= 16 * tn && 16 * tn * few_pitch<1>(D) <= kFewLds) return tn;
+// Tiles of 16 tokens of the few-token kernels, 0: none.  Forward here and in tiles, us:
+// D 1024, F 4096: 1 token 9.7 and 20.5, 16 tokens 15.5 and 22.5 (32 24 and 23.5); D 2048, F
+// 8192: 1 token 23.1 and 38.2, 16 tokens 38.2 and 40.6; D 512, F 2048: 17 tokens 10.9 and
+// 17.2, 32 tokens 13.6 and 17.1; D 512, F 8192: 16 tokens 18.9 and 19.6, 17 tokens 22.2 and
+// 19.5.
+int few_tiles(int64_t T, int64_t D, int64_t F) {
+  if (T <= 16 && D <= 2048) return 1;
+  if (T <= 32 && D <= 512 && D * F <= (int64_t)1 << 21) return 2;
   return 0;
 }
+static_assert(16 * few_pitch(2048) <= 80 * 1024 && 32 * few_pitch(512) <= 80 * 1024, "two workgroups' tokens fit the LDS");
 
 // Tile and splits of up to four products that run together: those of the least estimated
 // time, the items (tiles times splits) being dealt out to the CUs' places, the longest
@@ -711,7 +720,7 @@ struct FfnFwdSpace {
   FfnFwdSpace(int64_t T, int64_t D, int64_t F) {
     size_t at = 0;
     auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
-    few = few_tiles(T, D);
+    few = few_tiles(T, D, F);
     blocked = T >= kBlockTokens;
     h = take(few ? (size_t)(T * F * 2) : blocked_bytes(T, F));
     x = take(blocked ? blocked_bytes(T, D) : 0);
@@ -777,18 +786,21 @@ hipError_t launch_ffn_fwd(const FfnParams& f, void* ws, hipStream_t s) {
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   uint16_t* h = reinterpret_cast<uint16_t*>(w + sp.h);
   if (sp.few) {
+    const int32_t down_rows = f.D >= 16 * kCus ? 16 : f.D >= 8 * kCus ? 8 : 4;
     const GateFewArgs a = {reinterpret_cast<const uint16_t*>(f.X), reinterpret_cast<const uint16_t*>(f.Wg), reinterpret_cast<const uint16_t*>(f.Wu),
                            f.ldx, f.ldw, (int32_t)f.T, (int32_t)f.D, (int32_t)f.F, h, saved_of(f)};
-    const DownFewArgs d = {h, reinterpret_cast<const uint16_t*>(f.Wd), f.ldd, (int32_t)f.T, (int32_t)f.D, (int32_t)f.F, f.Y, f.y_dtype == TJ2_BF16};
-    const uint32_t groups = (uint32_t)((f.F + 7) / 8), rounds = (groups + 8 * kCus - 1) / (8 * kCus), grid = (groups + rounds * 4 - 1) / (rounds * 4);
+    const DownFewArgs d = {h, reinterpret_cast<const uint16_t*>(f.Wd), f.ldd, (int32_t)f.T, (int32_t)f.D, (int32_t)f.F, down_rows, f.Y, f.y_dtype == TJ2_BF16};
+    // two waves a workgroup while those reach no more CUs
+    const uint32_t groups = (uint32_t)((f.F + 7) / 8), per = groups <= 4 * kCus ? 2 : 4, rounds = (groups + 8 * kCus - 1) / (8 * kCus),
+                   grid = (groups + rounds * per - 1) / (rounds * per);
+    const size_t lds = (size_t)(f.T * few_pitch(f.D));
     auto run = [&](auto tn) {
       constexpr int TN = decltype(tn)::value;
-      with_activation(f.act, [&](auto act) { ffn_gate_few_kernel<TN, act.value><<<grid, 256, 0, s>>>(a); });
-      ffn_down_few_kernel<TN><<<(uint32_t)(f.D / 16), 1024, 0, s>>>(d);
+      with_activation(f.act, [&](auto act) { ffn_gate_few_kernel<TN, act.value><<<grid, per * 64, lds, s>>>(a); });
+      ffn_down_few_kernel<TN><<<(uint32_t)(f.D / down_rows), 1024, 0, s>>>(d);
     };
     if (sp.few == 1) run(std::integral_constant<int, 1>{});
-    else if (sp.few == 2) run(std::integral_constant<int, 2>{});
-    else run(std::integral_constant<int, 4>{});
+    else run(std::integral_constant<int, 2>{});
     return hipGetLastError();
   }
   GateArgs a = {};

@@ -404,45 +404,68 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_few_kernel(Fp8FewArgs a) {
   __shared__ typename S::Smem sm;
   const Fp8GemmArgs& p = a.g;
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4, I = (int)p.Q.rows;
-  const int px = S::pitch(p.P.kb), per = a.nb * 16;  // 8-element pieces of a row, whole chunks
+  const int px = S::pitch(p.P.kb), per = a.nb * 16, all = I * per;  // 8-element pieces of a row, whole chunks
   float* xs = reinterpret_cast<float*>(sm.xs);
-  for (int i = threadIdx.x; i < S::TOKENS * per; i += S::NT) {
-    const int t = i / per, c = (i - t * per) * 8;
-    uint2 q = {0u, 0u};
-    float s = 0.0f;
-    if (a.x) {
-      float v[8];
-      if (t < I && c < a.cols) {
-        load8(a.x + (int64_t)t * a.cols + c, v);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-      }
-      const Fp8Scale f = fp8_scale(max16_lanes(top_bits8(v)));
-      q = fp8_codes8(v, f);
-      s = f.S;
-      if (blockIdx.x == 0 && t < I) {
-        *reinterpret_cast<uint2*>(a.codes + (int64_t)t * a.nb * 128 + c) = q;
-        if ((c & 127) == 0) a.scale[(int64_t)t * a.nb + (c >> 7)] = s;
-      }
-    } else if (t < I) {
-      if (c < a.cols) q = *reinterpret_cast<const uint2*>(a.codes + (int64_t)t * a.nb * 128 + c);
-      s = a.scale[(int64_t)t * a.nb + (c >> 7)];
-    }
+  auto put = [&](int t, int c, uint2 q, float s) __attribute__((always_inline)) {
     *reinterpret_cast<uint2*>(sm.x + t * px + c) = q;
     if ((c & 127) == 0) xs[(c >> 7) * S::TOKENS + t] = s;
-  }
-  __syncthreads();
-  S::run(p.P, sm, [&](uint32_t group, const typename S::Acc& acc) __attribute__((always_inline)) {
+  };
+  auto stage = [&]() __attribute__((always_inline)) {
+    // four pieces a thread at once, so that their loads are in flight together
+    for (int i0 = threadIdx.x; i0 < all; i0 += 4 * S::NT) {
+      if (a.x) {
+        float v[4][8];
 #pragma unroll
-    for (int tn = 0; tn < S::TOKENS / 16; ++tn) {
-      const int t = tn * 16 + n;
-      if (t < I) {
-        const float v[4] = {acc[tn].x, acc[tn].y, acc[tn].z, acc[tn].w};
-        fp8_store<4>(p, (int64_t)t * p.ldc, (int64_t)group * 16 + g * 4, v);
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * S::NT, t = i / per, c = (i - t * per) * 8;
+          if (i < all && c < a.cols) {
+            load8(a.x + (int64_t)t * a.cols + c, v[u]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[u][k] = 0.0f;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * S::NT, t = i / per, c = (i - t * per) * 8;
+          const Fp8Scale f = fp8_scale(max16_lanes(top_bits8(v[u])));
+          const uint2 q = fp8_codes8(v[u], f);
+          if (i >= all) break;  // (whole groups of 16 lanes: a row's pieces are a multiple of 16)
+          if (blockIdx.x == 0) {
+            *reinterpret_cast<uint2*>(a.codes + (int64_t)t * a.nb * 128 + c) = q;
+            if ((c & 127) == 0) a.scale[(int64_t)t * a.nb + (c >> 7)] = f.S;
+          }
+          put(t, c, q, f.S);
+        }
+      } else {
+        uint2 q[4];
+        float s[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * S::NT, t = i / per, c = (i - t * per) * 8;
+          q[u] = uint2{0u, 0u};
+          s[u] = 0.0f;
+          if (i < all) {
+            if (c < a.cols) q[u] = *reinterpret_cast<const uint2*>(a.codes + (int64_t)t * a.nb * 128 + c);
+            s[u] = a.scale[(int64_t)t * a.nb + (c >> 7)];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * S::NT, t = i / per, c = (i - t * per) * 8;
+          if (i < all) put(t, c, q[u], s[u]);
+        }
       }
     }
-  });
+    __syncthreads();
+  };
+  S::run(p.P, sm, [&](uint32_t group, const typename S::Acc& acc) __attribute__((always_inline)) {
+    static_assert(S::TOKENS == 16, "one tile of tokens");
+    if (n < I) {
+      const float v[4] = {acc[0].x, acc[0].y, acc[0].z, acc[0].w};
+      fp8_store<4>(p, (int64_t)n * p.ldc, (int64_t)group * 16 + g * 4, v);
+    }
+  }, stage);
 }
 
 // C = (C +) the sum of the splits' results in order, 4 a thread.
@@ -496,15 +519,16 @@ TileOp fp8_operand(const QView& q, bool blocked) {
   return o;
 }
 
-template <int TN>
-using Few = Skinny<EL_FP8BX, TN, 66 * 1024>;
-// Tiles of 16 tokens that the few-row kernel takes, 0: none.
-int few_tiles(int64_t M, int64_t K) {
-  if (Few<1>::fits(M, K)) return 1;
-  if (Few<2>::fits(M, K)) return 2;
-  if (Few<4>::fits(M, K)) return 4;
-  return 0;
-}
+// Rows of A that fp8_few_kernel takes: up to 16, an instruction tile, of up to 8192
+// elements in all, as every workgroup quantises them.  Linear forward here and in tiles
+// with the quantisation's launch, us: N 4096, K 1024: 1 row 5.7 and 9.2, 8 rows 6.9 and
+// 10.1, 16 rows 9.1 and 10.1; K 2048: 1 row 8.5 and 9.2, 4 rows 9.6 and 9.6, 8 rows 11.7 and
+// 9.8; K 256: 16 rows 4.9 and 6.4; N 50304, K 1024: 1 row 14.4 and 14.9, 8 rows 15.7 and 15.5,
+// 16 rows 17.8 and 15.7.  (Tiles of 32 and 64 rows here: 24 rows of N 50304, K 1024 22.0
+// and 15.7, 64 rows 38.8 and 16.6.)
+using Few = Skinny<EL_FP8BX, 1, 34 * 1024>;
+static_assert(Few::TOKENS * (2048 + 16) <= 34 * 1024 && Few::TOKENS * (2048 + 128 + 16) > 34 * 1024, "2048 elements");
+bool is_few(int64_t M, int64_t K) { return Few::fits(M, K) && M * K <= 8192; }
 
 // Tile and splits of a product, by an estimate of its time from what the tiles measure
 // (us on MI355X; a chunk is 128 elements of the reduction).
@@ -594,10 +618,7 @@ hipError_t run_few(const Fp8GemmArgs& g, const QView& A, const void* x, hipStrea
   f.nb = (int32_t)A.nb;
   f.codes = A.codes;
   f.scale = A.s128;
-  const int tn = few_tiles(A.rows, A.len);
-  if (tn == 1) fp8_few_kernel<Few<1>><<<Few<1>::grid(g.P.rows), Few<1>::NT, 0, s>>>(f);
-  else if (tn == 2) fp8_few_kernel<Few<2>><<<Few<2>::grid(g.P.rows), Few<2>::NT, 0, s>>>(f);
-  else fp8_few_kernel<Few<4>><<<Few<4>::grid(g.P.rows), Few<4>::NT, 0, s>>>(f);
+  fp8_few_kernel<Few><<<Few::grid(g.P.rows), Few::NT, 0, s>>>(f);
   return hipGetLastError();
 }
 
@@ -650,17 +671,17 @@ hipError_t launch_fp8_gemm(const QView& A, const QView& B, void* C, int c_dtype,
                            hipStream_t s) {
   const Fp8GemmArgs a = fp8_args(fp8_operand(A, false), fp8_operand(B, false), A.len, C, c_dtype, ldc, accumulate);
   const bool block = B.fmt == TJ2_FP8_BLOCK;
-  if (block && few_tiles(A.rows, A.len)) return run_few(a, A, nullptr, s);
+  if (block && is_few(A.rows, A.len)) return run_few(a, A, nullptr, s);
   return run_product(a, A.len, block, partial, s);
 }
 
-size_t fp8_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K) { return few_tiles(M, K) ? 0 : fp8_gemm_workspace_bytes(M, N, K); }
+size_t fp8_linear_fwd_workspace_bytes(int64_t M, int64_t N, int64_t K) { return is_few(M, K) ? 0 : fp8_gemm_workspace_bytes(M, N, K); }
 
 hipError_t launch_fp8_linear_fwd(const void* X, const float* W, const QView& Xq, const QView& Wq, void* Y, int y_dtype,
                                  float* partial, hipStream_t s) {
   const Fp8RowArgs x = row_args(X, Xq), w = row_args(W, Wq);
   const Fp8GemmArgs a = fp8_args(fp8_operand(Xq, false), fp8_operand(Wq, false), Xq.len, Y, y_dtype, Wq.rows, 0);
-  const bool few = few_tiles(Xq.rows, Xq.len) != 0;
+  const bool few = is_few(Xq.rows, Xq.len);
   if (few || !X) {
     if (W) fp8_block_kernel<float><<<block_grid(w), 256, 0, s>>>(w);
   } else if (W) {

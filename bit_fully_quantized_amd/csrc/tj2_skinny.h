@@ -40,15 +40,22 @@ struct Skinny {
 
   typedef float4_t Acc[TN];
 
-  // The tokens are in sm (zero beyond them and beyond their kb bytes), a barrier
-  // crossed.  epilogue(group, acc): acc[tn][r] is the result of W row
-  // 16 group + 4 g + r and token 16 tn + n (lane n + 16 g).
+  // The tokens are in sm (zero beyond their kb bytes; what lies beyond the tokens enters
+  // none of theirs), a barrier crossed.  epilogue(group, acc): acc[tn][r] is the result of
+  // W row 16 group + 4 g + r and token 16 tn + n (lane n + 16 g).
   template <class Epilogue>
   static __device__ __forceinline__ void run(const TileOp& P, const Smem& sm, Epilogue&& epilogue) {
+    run(P, sm, epilogue, [] {});
+  }
+  // stage(): puts the tokens into sm, all threads of the workgroup and its barrier, while
+  // the first rows of W are on their way.
+  template <class Epilogue, class Stage>
+  static __device__ __forceinline__ void run(const TileOp& P, const Smem& sm, Epilogue&& epilogue, Stage&& stage) {
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const uint32_t wave = blockIdx.x * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = gridDim.x * WAVES;
     const uint32_t groups = (uint32_t)((P.rows + 15) >> 4);
-    if (wave >= groups) return;
+    constexpr bool kStages = !std::is_empty<std::decay_t<Stage>>::value;
+    if (!kStages && wave >= groups) return;
     const int chunks = (P.kb + 127) >> 7, batches = (chunks + U - 1) / U;
     const int px = pitch(P.kb), ps = scale_pitch(P.kb);
     const uint8_t* xl = sm.x + n * px + g * 32;
@@ -96,17 +103,18 @@ struct Skinny {
         const int c = b * U + u;
         if (c >= chunks) break;
         half8_t wt[kFp8 ? 4 : 1];  // exact products, as the reads bound this (EL_FP8BX)
-        if constexpr (kFp8) fp8_to_f16(f.a[u][0], f.a[u][1], wt);
+        if constexpr (kFp8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) wt[k] = fp8_to_f16(f.a[u][0], f.a[u][1], k);
+        }
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn) {
           const i32x4_t* x = reinterpret_cast<const i32x4_t*>(xl + tn * 16 * px + c * 128);
           if constexpr (kFp8) {
             const float s = reinterpret_cast<const float*>(sm.xs)[c * TOKENS + tn * 16 + n] * f.w[u];
-            half8_t xt[4];
-            fp8_to_f16(x[0], x[1], xt);
             float4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v = __builtin_amdgcn_mfma_f32_16x16x32_f16(wt[k], xt[k], v, 0, 0, 0);
+            for (int k = 0; k < 4; ++k) v = __builtin_amdgcn_mfma_f32_16x16x32_f16(wt[k], fp8_to_f16(x[0], x[1], k), v, 0, 0, 0);
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[tn][r] = fmaf(v[r], s, acc[tn][r]);
           } else if constexpr (EL == EL_BF16) {
@@ -130,8 +138,12 @@ struct Skinny {
     uint32_t gr = wave;   // of the batch in the matrix units
     int b = 0;
     Batch f0, f1;
-    fetch(f0, gr, 0);
-    fetch_scales(f0, gr, 0);
+    if (!kStages || wave < groups) {
+      fetch(f0, gr, 0);
+      fetch_scales(f0, gr, 0);
+    }
+    stage();
+    if (kStages && wave >= groups) return;
     // two batches a turn, so that each has its own registers
     auto turn = [&](const Batch& now, Batch& next) __attribute__((always_inline)) -> bool {
       uint32_t ng = gr;

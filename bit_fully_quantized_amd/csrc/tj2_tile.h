@@ -65,19 +65,16 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2v_t{a, b}, bf16x2v_t));
 }
 
-// The values of 32 E4M3 codes, which f16 holds.
-__device__ __forceinline__ void fp8_to_f16(i32x4_t a, i32x4_t b, half8_t (&x)[4]) {
+// The values of 8 E4M3 codes, which f16 holds, the k-th of 32 in a and b.
+__device__ __forceinline__ half8_t fp8_to_f16(i32x4_t a, i32x4_t b, int k) {
+  half2_t h[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    half2_t h[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t u = (uint32_t)(k < 2 ? a : b)[k % 2 * 2 + i];
-      h[2 * i] = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, false));
-      h[2 * i + 1] = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, true));
-    }
-    x[k] = half8_t{h[0].x, h[0].y, h[1].x, h[1].y, h[2].x, h[2].y, h[3].x, h[3].y};
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = (uint32_t)(k < 2 ? a : b)[k % 2 * 2 + i];
+    h[2 * i] = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, false));
+    h[2 * i + 1] = __builtin_bit_cast(half2_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(u, 1.0f, true));
   }
+  return half8_t{h[0].x, h[0].y, h[1].x, h[1].y, h[2].x, h[2].y, h[3].x, h[3].y};
 }
 
 // An operand of a tile product: rows of `kb` bytes (a multiple of 16).  Row r's
@@ -346,7 +343,14 @@ struct Tile {
     // The loads of the cursor's chunk into `stage`, one at a time: begin() sets them up.
     u32x4_t dp, dq, dsp, dsq, dp2;
     uint32_t bads = 0, dst = 0, sdst = 0;
+    // (FP8: the cursor's rows and bytes as they were then; it goes on before the last load,
+    // where its branch does not part a chunk's instructions)
+    int np1 = 0, nq1 = 0, leftp1 = 0, leftq1 = 0;
     auto begin = [&](uint32_t stage) __attribute__((always_inline)) {
+      np1 = np;
+      nq1 = nq;
+      leftp1 = leftp;
+      leftq1 = leftq;
       dp = raw_buffer(pb);
       dq = raw_buffer(qb);
       settle(dp, dq);
@@ -398,12 +402,13 @@ struct Tile {
     };
     constexpr int LOADS = LP + LQ + (EL == EL_MX || kFp8 ? SJ : 0);
     auto load = [&](int i) __attribute__((always_inline)) {
+      const int np_ = kFp8 ? np1 : np, nq_ = kFp8 ? nq1 : nq, leftp_ = kFp8 ? leftp1 : leftp, leftq_ = kFp8 ? leftq1 : leftq;
       if (kPair && i < LP) {
-        load_lds16(i & 1 ? dp2 : dp, lr < np - (i >> 1) * RPI && (int)gp(i) < leftp ? vp + gp(i) : kOutside, far_p(i >> 1), dst + i * (RPI * 128));
+        load_lds16(i & 1 ? dp2 : dp, lr < np_ - (i >> 1) * RPI && (int)gp(i) < leftp_ ? vp + gp(i) : kOutside, far_p(i >> 1), dst + i * (RPI * 128));
       } else if (i < LP) {
-        load_lds16(dp, lr < np - i * RPI && (int)gp(i) < leftp ? vp + gp(i) : kOutside, far_p(i), dst + i * (RPI * 128));
+        load_lds16(dp, lr < np_ - i * RPI && (int)gp(i) < leftp_ ? vp + gp(i) : kOutside, far_p(i), dst + i * (RPI * 128));
       } else if (i < LP + LQ) {
-        load_lds16(dq, lrq < nq - (i - LP) * RPI && (int)gq(i - LP) < leftq ? vq + gq(i - LP) : kOutside, far_q(i - LP), dst + i * (RPI * 128));
+        load_lds16(dq, lrq < nq_ - (i - LP) * RPI && (int)gq(i - LP) < leftq_ ? vq + gq(i - LP) : kOutside, far_q(i - LP), dst + i * (RPI * 128));
       } else if constexpr (EL == EL_MX) {
         const int j = i - LP - LQ, r0 = w * 32 + j * (NT / 2);
         const bool isp = r0 < BM;
@@ -413,7 +418,7 @@ struct Tile {
         d.y = isp ? dsp.y : dsq.y;
         d.z = dsp.z;
         d.w = dsp.w;
-        load_lds4(d, (lane >> 1) < (isp ? np : nq) - first ? vs | bads : kOutside, (uint32_t)(first >> 7) * (bsp / 16) + (uint32_t)(first & 127) * (ldp / 16),
+        load_lds4(d, (lane >> 1) < (isp ? np_ : nq_) - first ? vs | bads : kOutside, (uint32_t)(first >> 7) * (bsp / 16) + (uint32_t)(first & 127) * (ldp / 16),
                   sdst + j * (NT * 4));
       } else if constexpr (kFp8) {
         const int j = i - LP - LQ, r0 = w * 64 + j * NT;
@@ -427,7 +432,7 @@ struct Tile {
         d.z = dsp.z;
         d.w = dsp.w;
         const uint32_t sr = isp ? srp : srq;
-        load_lds4(d, lane < (isp ? np : nq) - first ? (block ? 0u : (uint32_t)lane * sr) : kOutside, (uint32_t)(block ? first >> 7 : first) * sr,
+        load_lds4(d, lane < (isp ? np_ : nq_) - first ? (block ? 0u : (uint32_t)lane * sr) : kOutside, (uint32_t)(block ? first >> 7 : first) * sr,
                   sdst + j * (NT * 4));
       }
     };
@@ -440,14 +445,15 @@ struct Tile {
     const uint32_t lq0 = lds_address(sm.stage[0]) + (uint32_t)(qr0 + q_place(q_row(0, n))) * 128u + ((2 * g) ^ qk) * 16;
     const uint32_t lq1 = lds_address(sm.stage[0]) + (uint32_t)(qr0 + q_place(q_row(TN > 1 ? 1 : 0, n))) * 128u + ((2 * g) ^ qk) * 16;
     if constexpr (kFp8) {
-      // A chunk: TM rows of TN instructions, whose results (two rows of them in
-      // registers) are scaled and added to the sums while the next row's run.  P's
-      // fragments are read two rows ahead; Q's, which every row needs, at the start.  The
-      // barrier comes after the last row has issued: then every wave has read the whole
-      // stage, which is refilled from the start of the next chunk on.
+      // A chunk: TM rows of TN instructions.  The result of one waits in registers until the
+      // next row's has its turn there and is scaled and added to the sums then, so that the
+      // wave's arithmetic fills the instructions' time (the chunk's last row among the
+      // next chunk's first).  P's fragments are read two rows ahead; Q's, which every row
+      // needs, as the last row's instructions let go of them.  The barrier comes before the
+      // last row, all of whose operands are in registers: the stage is refilled from there on.
       constexpr int PR = 2;
       i32x4_t fp[PR][2], fq[TN][2];
-      float4_t part[2][TN];
+      float4_t part[TN];
       float sq[TN], sb = 0.0f;
       float4_t sp[kBlockP ? 1 : PR];
       // exact: the codes as f16, two rows of P's (the next one's is decoded while one runs)
@@ -458,11 +464,9 @@ struct Tile {
 #pragma unroll
         for (int h = 0; h < 2; ++h) fp[tm % PR][h] = lds_read<i32x4_t>(((lp ^ (h * 16)) + stage * kStage) + p_row(tm, 0, 0) * 128);
       };
-      auto read_q = [&](uint32_t stage) __attribute__((always_inline)) {
+      auto read_q1 = [&](uint32_t stage, int tn) __attribute__((always_inline)) {
 #pragma unroll
-        for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) fq[tn][h] = lds_read<i32x4_t>((((tn & 1 ? lq1 : lq0) ^ (h * 16)) + stage * kStage) + (tn & ~1) * 128);
+        for (int h = 0; h < 2; ++h) fq[tn][h] = lds_read<i32x4_t>((((tn & 1 ? lq1 : lq0) ^ (h * 16)) + stage * kStage) + (tn & ~1) * 128);
       };
       auto read_scales = [&](uint32_t stage) __attribute__((always_inline)) {
         if constexpr (TN == 4) {
@@ -477,39 +481,38 @@ struct Tile {
       auto read_sp = [&](uint32_t stage, int tm) __attribute__((always_inline)) {
         if constexpr (!kBlockP) sp[tm % PR] = lds_read<float4_t>(lsp + stage * (SCALE_DW * 4) + p_row(tm, 0, 0) * 4);
       };
-      auto decode_q = [&]() __attribute__((always_inline)) {
-        if constexpr (kExact) {
+      auto decode_p = [&](int tm) __attribute__((always_inline)) {
+        if constexpr (kExact)
 #pragma unroll
-          for (int tn = 0; tn < TN; ++tn) fp8_to_f16(fq[tn][0], fq[tn][1], xq[tn]);
-          fp8_to_f16(fp[0][0], fp[0][1], xp[0]);
-        }
+          for (int k = 0; k < 4; ++k) xp[tm % 2][k] = fp8_to_f16(fp[tm % PR][0], fp[tm % PR][1], k);
       };
-      auto mma = [&](auto tmc) __attribute__((always_inline)) {
-        constexpr int tm = decltype(tmc)::value;
+      auto decode_q = [&]() __attribute__((always_inline)) {
+        if constexpr (kExact)
+#pragma unroll
+          for (int i = 0; i < TN * 4; ++i) xq[i / 4][i % 4] = fp8_to_f16(fq[i / 4][0], fq[i / 4][1], i % 4);
+      };
+      // instruction k of tile (tm, tn) (exact: four of 32 elements, k by k so that none waits
+      // for the one before it)
+      constexpr int KS = kExact ? 4 : 1;
+      auto mma = [&](auto tmc, auto tnc, auto kc) __attribute__((always_inline)) {
+        constexpr int tm = decltype(tmc)::value, tn = decltype(tnc)::value, k = decltype(kc)::value;
+        const float4_t z = {0.0f, 0.0f, 0.0f, 0.0f};
         if constexpr (kExact) {
-          static_for<4>([&](auto kc) __attribute__((always_inline)) {
-            constexpr int k = decltype(kc)::value;
-            static_for<TN>([&](auto tnc) __attribute__((always_inline)) {
-              constexpr int tn = decltype(tnc)::value;
-              part[tm % 2][tn] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xp[tm % 2][k], xq[tn][k], k ? part[tm % 2][tn] : float4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0);
-            });
-          });
-        } else static_for<TN>([&](auto tnc) __attribute__((always_inline)) {
-          constexpr int tn = decltype(tnc)::value;
+          part[tn] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xp[tm % 2][k], xq[tn][k], k ? part[tn] : z, 0, 0, 0);
+        } else {
           const i32x8_t a = __builtin_shufflevector(fp[tm % PR][0], fp[tm % PR][1], 0, 1, 2, 3, 4, 5, 6, 7);
           const i32x8_t b = __builtin_shufflevector(fq[tn][0], fq[tn][1], 0, 1, 2, 3, 4, 5, 6, 7);
-          part[tm % 2][tn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, float4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
-        });
+          part[tn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
+        }
       };
-      auto add = [&](auto tmc) __attribute__((always_inline)) {
-        constexpr int tm = decltype(tmc)::value;
+      // the result of tile (tm, tn)
+      auto add = [&](auto tmc, auto tnc) __attribute__((always_inline)) {
+        constexpr int tm = decltype(tmc)::value, tn = decltype(tnc)::value;
 #pragma unroll
-        for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if constexpr (kBlockP) acc[tm][tn][r] = fmaf(part[tm % 2][tn][r], sq[tn], acc[tm][tn][r]);
-            else acc[tm][tn][r] = fmaf(part[tm % 2][tn][r] * sq[tn], sp[tm % PR][r], acc[tm][tn][r]);
-          }
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (kBlockP) acc[tm][tn][r] = fmaf(part[tn][r], sq[tn], acc[tm][tn][r]);
+          else acc[tm][tn][r] = fmaf(part[tn][r] * sq[tn], sp[tm % PR][r], acc[tm][tn][r]);
+        }
       };
       auto scale_q = [&]() __attribute__((always_inline)) {
         if constexpr (kBlockP) {
@@ -517,49 +520,74 @@ struct Tile {
           for (int tn = 0; tn < TN; ++tn) sq[tn] *= sb;
         }
       };
+      // the next chunk's loads: EARLY of them in the last row, the others in the next SPAN
+      constexpr int EARLY = TM >= 4 ? 2 : 1, SPAN = TM >= 4 ? TM / 2 : 1;
       begin(0);
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) load(i);
       advance();
       tile_barrier();
       begin(1);
+#pragma unroll
+      for (int i = 0; i < EARLY; ++i) load(i);
       uint32_t st = 0, at = items.at;
-      constexpr int SPAN = TM >= 4 ? TM / 2 : 1;  // rows over which the next loads are dealt out
       for (;;) {
-        read_q(st);
-        read_scales(st);
+        // the item's first fragments (read again after an epilogue, which has the registers
+        // to itself), and nothing of a chunk before
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) read_q1(st, tn);
         read_p(st, 0);
         read_sp(st, 0);
-        if constexpr (TM > 1) read_p(st, 1);
+        read_p(st, 1);
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) {
+          part[tn] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+          sq[tn] = 0.0f;
+        }
+        if constexpr (!kBlockP) sp[(TM - 1) % PR] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma nounroll
         for (; now.c < now.c1; ++now.c) {
+          advance();
           decode_q();
+          decode_p(0);
           static_for<TM>([&](auto tmc) __attribute__((always_inline)) {
             constexpr int tm = decltype(tmc)::value;
-            mma(tmc);
-            __builtin_amdgcn_sched_barrier(0);
-            if constexpr (kExact && tm + 1 < TM) fp8_to_f16(fp[(tm + 1) % PR][0], fp[(tm + 1) % PR][1], xp[(tm + 1) % 2]);
+            using Before = std::integral_constant<int, (tm + TM - 1) % TM>;
+            static_for<KS * TN>([&](auto ic) __attribute__((always_inline)) {
+              constexpr int tn = decltype(ic)::value % TN, k = decltype(ic)::value / TN;
+              using Tn = std::integral_constant<int, tn>;
+              if constexpr (k == 0) add(Before{}, Tn{});
+              mma(tmc, Tn{}, std::integral_constant<int, k>{});
+              __builtin_amdgcn_sched_barrier(0);
+              if constexpr (tm == TM - 1 && k == KS - 1) read_q1(st, tn);
+            });
+            if constexpr (tm + 1 < TM) decode_p(tm + 1);
+            if constexpr (tm == 0) {  // (the last chunk's scales have been used)
+              read_scales(st);
+              scale_q();
+            }
             if constexpr (tm < SPAN) {
 #pragma unroll
-              for (int i = 0; i < LOADS; ++i)
-                if (i * SPAN / LOADS == tm) load(i);
-              if constexpr (tm == SPAN - 1) advance();
+              for (int i = EARLY; i < LOADS; ++i)
+                if ((i - EARLY) * SPAN / (LOADS - EARLY) == tm) load(i);
             }
-            if constexpr (tm == 0) scale_q();
-            if constexpr (tm > 0) add(std::integral_constant<int, tm - 1>{});
             if constexpr (tm + 1 < TM) read_sp(st, tm + 1);
             if constexpr (tm + 2 < TM) read_p(st, tm + 2);
+            if constexpr (tm == TM - 2) {
+              tile_barrier();
+              begin(st);
+              st ^= 1u;
+              read_p(st, 0);
+            }
+            if constexpr (tm == TM - 1) {
+              read_p(st, 1);
+              read_sp(st, 0);
+#pragma unroll
+              for (int i = 0; i < EARLY; ++i) load(i);
+            }
           });
-          tile_barrier();
-          begin(st);
-          st ^= 1u;
-          read_q(st);
-          read_p(st, 0);
-          if constexpr (TM > 1) read_p(st, 1);
-          add(std::integral_constant<int, TM - 1>{});
-          read_scales(st);
-          read_sp(st, 0);
         }
+        static_for<TN>([&](auto tnc) __attribute__((always_inline)) { add(std::integral_constant<int, TM - 1>{}, tnc); });
         epilogue((int64_t)now.tp * BM, (int64_t)now.tq * BN, now.z, acc);
         at += items.step;
         if (at >= items.end) break;

@@ -34,15 +34,22 @@ def gated_ffn_saved_size(T: int, F: int) -> int:
     return int(lib().tj2_gated_ffn_saved_size(T, F))
 
 
+def _matrix(t, name: str, index: int, cols: int) -> int:
+    """The row stride of a bf16 matrix of `cols` columns."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 2 and t.is_contiguous() and t.get_device() == index and t.shape[1] == cols:
+        return cols
+    return _rows(t, name, _BF16, index, cols)
+
+
 def _operands(X, Wg, Wu, Wd, activation: str):
     """(device index, T, D, F, the arguments that both passes share)."""
     index = _tensor(X, "X", 2)
-    ldx = _rows(X, "X", _BF16, index)
     T, D = X.shape
-    ldw = _rows(Wg, "Wg", _BF16, index, D)
-    ldu = _rows(Wu, "Wu", _BF16, index, D)
+    ldx = _matrix(X, "X", index, D)
+    ldw = _matrix(Wg, "Wg", index, D)
+    ldu = _matrix(Wu, "Wu", index, D)
     F = Wg.shape[0]
-    ldd = _rows(Wd, "Wd", _BF16, index, F)
+    ldd = _matrix(Wd, "Wd", index, F)
     if Wu.shape[0] != F or Wd.shape[0] != D:
         raise ValueError(f"Wg is [{F}, {D}]: Wu must be the same and Wd [{D}, {F}]")
     if ldu != ldw:
@@ -78,7 +85,7 @@ def gated_ffn_bwd(dY: torch.Tensor, X: torch.Tensor, Wg: torch.Tensor, Wu: torch
     """(dX, dWg, dWu, dWd) for dY [T, D] from gated_ffn_fwd's saved; `need` False leaves a gradient out (None).  The
     weights' gradients are of one type."""
     index, T, D, F, args = _operands(X, Wg, Wu, Wd, activation)
-    ldy = _rows(dY, "dY", _BF16, index, D)
+    ldy = _matrix(dY, "dY", index, D)
     if dY.shape[0] != T:
         raise ValueError(f"dY has {dY.shape[0]} rows, expected {T}")
     shapes = ((T, D), (F, D), (F, D), (D, F))

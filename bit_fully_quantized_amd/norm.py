@@ -25,10 +25,17 @@ def _stream(t, name: str, index: int, like: torch.Tensor):
     """(pointer, pitch) of a matrix of like's type and shape with a pitch of its own; (0, 0) for None."""
     if t is None:
         return 0, 0
+    if isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.shape == like.shape and t.is_contiguous() and t.get_device() == index:
+        return t.data_ptr(), like.shape[1]
     ld = _rows(t, name, (like.dtype,), index, like.shape[1])
     if t.shape[0] != like.shape[0]:
         raise ValueError(f"{name} has {t.shape[0]} rows, expected {like.shape[0]}")
     return t.data_ptr(), max(ld, like.shape[1])
+
+
+def _like(x: torch.Tensor, index: int) -> torch.Tensor:
+    """A contiguous tensor of x's shape and type."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=index)
 
 
 def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -48,9 +55,9 @@ def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tenso
     if residual is None and sum is not None:
         raise ValueError("sum needs a residual")
     if residual is not None and sum is None:
-        sum = torch.empty((rows, cols), dtype=x.dtype, device=index)
+        sum = _like(x, index)
     if y is None:
-        y = QTensor.packed(FP8, rows, cols, index) if fp8 else torch.empty((rows, cols), dtype=x.dtype, device=index)
+        y = QTensor.packed(FP8, rows, cols, index) if fp8 else _like(x, index)
     elif fp8 and not isinstance(y, QTensor):
         raise ValueError("y must be an FP8 QTensor")
     if rstd is None:
@@ -80,9 +87,9 @@ def rms_norm_bwd(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: 
     dp, ldd = _stream(dsum, "dsum", index, s)
     wp = _arg(weight, "weight", _OUT, index, (cols,))
     if ds is None and need_ds:
-        ds = torch.empty((rows, cols), dtype=s.dtype, device=index)
+        ds = _like(s, index)
     if dweight is None and need_dw:
-        dweight = torch.empty(cols, dtype=weight.dtype, device=index)
+        dweight = torch.empty_like(weight)
     workspace, ws, wn = _room(workspace, _bwd_bytes(rows, cols) if dweight is not None else 0, index)
     _run("tj2_rms_norm_bwd", index, yp, lddy, sp, lds, _CODE[s.dtype], rows, cols, wp, _CODE[weight.dtype],
          _arg(rstd, "rstd", _F32, index, (rows,)), dp, ldd, _arg(ds, "ds", (s.dtype,), index, (rows, cols), optional=True),
