@@ -149,13 +149,15 @@ __device__ __forceinline__ void quad_values(uint32_t q, float s, float v[4]) {
 }
 
 // The tile is in LDS, a barrier crossed: the columns' groups (or transposed codes).
+constexpr int kColThreads = 512;
 template <class T>
 __device__ __forceinline__ void fp8_col_out(const Fp8Out& out, int32_t cols, int32_t c0, uint32_t by,
                                             typename ColOf<T>::Quad (*tile)[ColOf<T>::CQ], const float* rs) {
   constexpr int CQ = ColOf<T>::CQ;
   const int rg = threadIdx.x & 15;
 #pragma unroll
-  for (int k = 0; k < CQ * 16; k += 256) {
+  for (int k = 0; k < CQ * 16; k += kColThreads) {
+    if (CQ * 16 < kColThreads && threadIdx.x >= CQ * 16) break;
     const int q = k / 16 + (threadIdx.x >> 4), col = c0 + q * 4;
     typename ColOf<T>::Quad raw[8];
 #pragma unroll
@@ -199,7 +201,7 @@ __device__ __forceinline__ void fp8_col(const Fp8ColArgs& p, uint32_t bx, uint32
   const int64_t r0 = (int64_t)by * 128;
   const int32_t c0 = (int32_t)bx * (4 * CQ);
 #pragma unroll
-  for (int i = t; i < 128 * CQ / VQ; i += 256) {
+  for (int i = t; i < 128 * CQ / VQ; i += kColThreads) {
     const int r = i / (CQ / VQ), q = i % (CQ / VQ) * VQ;
     const bool in = r0 + r < p.rows && c0 + q * 4 < p.cols;
     if constexpr (std::is_same<T, float>::value) {
@@ -227,7 +229,7 @@ __device__ __forceinline__ void fp8_col(const Fp8ColArgs& p, uint32_t bx, uint32
   fp8_col_out<T>(p.out, p.cols, c0, by, tile, rs);
 }
 template <class T>
-__global__ __launch_bounds__(256) void fp8_col_kernel(Fp8ColArgs p) {
+__global__ __launch_bounds__(kColThreads) void fp8_col_kernel(Fp8ColArgs p) {
   __shared__ __attribute__((aligned(16))) typename ColOf<T>::Quad tile[128][ColOf<T>::CQ];
   __shared__ float rs[128];
   fp8_col<T>(p, blockIdx.x, blockIdx.y, tile, rs);
@@ -246,16 +248,17 @@ __device__ __forceinline__ void fp8_dual(const Fp8DualArgs& p, uint32_t bx, uint
   const int t = threadIdx.x, h = t & 15;
   const int64_t r0 = (int64_t)by * 128;
   const int32_t c = (int32_t)bx * 128 + h * 8;
-  uint4 raw[8];
+  constexpr int N = 128 * 16 / kColThreads, R = kColThreads / 16;  // loads of a thread, rows of one of all threads
+  uint4 raw[N];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = r0 + i * 16 + (t >> 4);
+  for (int i = 0; i < N; ++i) {
+    const int64_t r = r0 + i * R + (t >> 4);
     raw[i] = uint4{0u, 0u, 0u, 0u};
     if (r < p.rows && c < p.cols) raw[i] = *reinterpret_cast<const uint4*>(p.x + r * p.cols + c);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = i * 16 + (t >> 4);
+  for (int i = 0; i < N; ++i) {
+    const int r = i * R + (t >> 4);
     tile[r][(2 * h) ^ (r >> 3)] = uint2{raw[i].x, raw[i].y};
     tile[r][(2 * h + 1) ^ (r >> 3)] = uint2{raw[i].z, raw[i].w};
     float v[8];
@@ -273,7 +276,7 @@ __device__ __forceinline__ void fp8_dual(const Fp8DualArgs& p, uint32_t bx, uint
 
 // All operands of the backward pass in one launch: nd workgroups for dY, nw for the
 // weights' codes turned, the others for the activations' grouped along the tokens.
-__global__ __launch_bounds__(256) void fp8_backward_kernel(Fp8DualArgs d, uint32_t nd, Fp8ColArgs w, uint32_t nw, Fp8ColArgs x) {
+__global__ __launch_bounds__(kColThreads) void fp8_backward_kernel(Fp8DualArgs d, uint32_t nd, Fp8ColArgs w, uint32_t nw, Fp8ColArgs x) {
   __shared__ __attribute__((aligned(16))) uint2 tile[128][32];
   __shared__ float rs[128];
   uint32_t b = blockIdx.x;
@@ -366,9 +369,8 @@ __device__ __forceinline__ void fp8_store(const Fp8GemmArgs& p, int64_t row, int
 }
 
 template <class T>
-__global__ __launch_bounds__(T::NT, T::WAVES) void fp8_gemm_kernel(Fp8GemmArgs p) {
-  __shared__ __attribute__((aligned(128))) typename T::Smem sm;
-  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits);
+__device__ __forceinline__ void fp8_tiles(const Fp8GemmArgs& p, typename T::Smem& sm, uint32_t block, uint32_t blocks) {
+  const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits, block, blocks);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
   T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t z, typename T::Acc& acc) __attribute__((always_inline)) {
     const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 4 * T::PB, qw = q0 + (w % T::kWN) * T::kTN * 16;
@@ -387,6 +389,20 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void fp8_gemm_kernel(Fp8GemmArgs p
       }
     }
   });
+}
+template <class T>
+__global__ __launch_bounds__(T::NT, T::WAVES) void fp8_gemm_kernel(Fp8GemmArgs p) {
+  __shared__ __attribute__((aligned(128))) typename T::Smem sm;
+  fp8_tiles<T>(p, sm, blockIdx.x, gridDim.x);
+}
+// The backward's two products in tiles of one size, where the second fills what the first
+// leaves idle: A's workgroups first.
+template <class A, class B>
+__global__ __launch_bounds__(A::NT, A::WAVES) void fp8_gemm_pair_kernel(Fp8GemmArgs a, Fp8GemmArgs b, uint32_t first) {
+  static_assert(A::NT == B::NT && sizeof(typename A::Smem) == sizeof(typename B::Smem), "one tile");
+  __shared__ __attribute__((aligned(128))) typename A::Smem sm;
+  if (blockIdx.x < first) fp8_tiles<A>(a, sm, blockIdx.x, first);
+  else fp8_tiles<B>(b, reinterpret_cast<typename B::Smem&>(sm), blockIdx.x - first, gridDim.x - first);
 }
 
 // Few rows of A (decoding): A whole in LDS, B read once.  From bf16 X (the linear layer's
@@ -468,10 +484,12 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_few_kernel(Fp8FewArgs a) {
   }, stage);
 }
 
-// C = (C +) the sum of the splits' results in order, 4 a thread.
-__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8GemmArgs p) {
+// C = (C +) the sum of the splits' results in order, 4 a thread; of one product or two.
+__global__ __launch_bounds__(256) void fp8_join_kernel(Pair<Fp8GemmArgs> jobs) {
+  const Share mine(jobs.first);
+  const Fp8GemmArgs& p = jobs.x[mine.job];
   const int64_t I = p.Q.rows, J = p.P.rows, n = I * J, per = (J + 3) / 4;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, i = id / per, j = (id - i * per) * 4;
+  const int64_t id = (int64_t)mine.block * 256 + threadIdx.x, i = id / per, j = (id - i * per) * 4;
   if (i >= I) return;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   const float* s = p.partial + i * J + j;
@@ -498,10 +516,20 @@ template <int EL>
 using TileSmall = Tile<EL, 2, 2, 2, 2>;  // 64 x 64
 
 template <class T>
-void launch_tile(Fp8GemmArgs a, hipStream_t s) {
+uint32_t tile_grid(Fp8GemmArgs& a) {
   a.tiles_p = (uint32_t)((a.P.rows + T::BM - 1) / T::BM);
   a.tiles_q = (uint32_t)((a.Q.rows + T::BN - 1) / T::BN);
-  fp8_gemm_kernel<T><<<T::grid((uint64_t)a.tiles_p * a.tiles_q * (uint32_t)a.splits), T::NT, 0, s>>>(a);
+  return T::grid((uint64_t)a.tiles_p * a.tiles_q * (uint32_t)a.splits);
+}
+template <class T>
+void launch_tile(Fp8GemmArgs a, hipStream_t s) {
+  const uint32_t grid = tile_grid<T>(a);
+  fp8_gemm_kernel<T><<<grid, T::NT, 0, s>>>(a);
+}
+template <class A, class B>
+void launch_pair(Fp8GemmArgs a, Fp8GemmArgs b, hipStream_t s) {
+  const uint32_t first = tile_grid<A>(a), others = tile_grid<B>(b);
+  fp8_gemm_pair_kernel<A, B><<<first + others, A::NT, 0, s>>>(a, b, first);
 }
 
 TileOp fp8_operand(const QView& q, bool blocked) {
@@ -531,17 +559,22 @@ static_assert(Few::TOKENS * (2048 + 16) <= 34 * 1024 && Few::TOKENS * (2048 + 12
 bool is_few(int64_t M, int64_t K) { return Few::fits(M, K) && M * K <= 8192; }
 
 // Tile and splits of a product, by an estimate of its time from what the tiles measure
-// (us on MI355X; a chunk is 128 elements of the reduction).
+// (us on MI355X; a chunk is 128 elements of the reduction): alone on its CU a tile of 64 /
+// 128 / 256 takes 0.7 / 0.98 / 1.7 a chunk, with the CU full (4 / 2 / 1 workgroups) 0.94 /
+// 1.09 / 1.7; with exact products 0.95 / 1.48 and 1.4 / 2.1 (decoded operands of a 256 x 256
+// tile would not fit the registers).  A split costs a launch and its fp32 partial sums,
+// written and read.
 struct Fp8Plan {
   int tile, splits;
-  double time;
+  double time, packed;  // packed: where other tiles take the places that it leaves idle
 };
 Fp8Plan fp8_plan(int64_t I, int64_t J, int64_t K, bool exact, int tile) {
-  const double kAlone[3] = {0.6, exact ? 1.4 : 1.0, 1.6}, kFull[3] = {exact ? 1.6 : 1.3, exact ? 2.0 : 1.4, 1.6}, kFixed[3] = {2.0, 2.5, 5.0};
+  const double kAlone[3] = {exact ? 0.95 : 0.7, exact ? 1.48 : 0.98, 1.7}, kFull[3] = {exact ? 1.4 : 0.94, exact ? 2.1 : 1.09, 1.7},
+               kFixed[3] = {2.5, 3.5, 5.0};
   constexpr int kSlots[3] = {4, 2, 1};
   const int64_t nch = (K + 127) / 128;
   const int64_t b = 64 << tile, n = ((I + b - 1) / b) * ((J + b - 1) / b), slots = kCus * kSlots[tile];
-  Fp8Plan best = {tile, 1, 1e30};
+  Fp8Plan best = {tile, 1, 1e30, 1e30};
   for (int z = 1; z <= 16 && z * 4 <= std::max<int64_t>(nch, 4); z *= 2) {
     const int64_t items = n * z, full = items / slots, rest = items % slots, deep = (rest + kCus - 1) / kCus;
     const double chunks = (double)((nch + z - 1) / z);
@@ -550,14 +583,15 @@ Fp8Plan fp8_plan(int64_t I, int64_t J, int64_t K, bool exact, int tile) {
       const double per = kSlots[tile] > 1 ? kAlone[tile] + (kFull[tile] - kAlone[tile]) * (double)(deep - 1) / (kSlots[tile] - 1) : kFull[tile];
       t += chunks * per + kFixed[tile];
     }
-    if (z > 1) t += 3.0 + (double)I * (double)J * 8.0 * z / 5e6;
-    if (t < best.time) best = Fp8Plan{tile, z, t};
+    const double join = z > 1 ? 3.0 + (double)I * (double)J * 8.0 * z / 5e6 : 0.0;
+    if (t + join < best.time)
+      best = Fp8Plan{tile, z, t + join, (double)items * (chunks * kFull[tile] + kFixed[tile]) / (double)slots + join};
   }
   return best;
 }
 Fp8Plan fp8_plan(int64_t I, int64_t J, int64_t K, bool exact) {
   Fp8Plan best = fp8_plan(I, J, K, exact, 0);
-  for (int tile = 1; tile < (exact ? 2 : 3); ++tile)  // (decoded operands of a 256 x 256 tile would not fit the registers)
+  for (int tile = 1; tile < (exact ? 2 : 3); ++tile)
     if (const Fp8Plan p = fp8_plan(I, J, K, exact, tile); p.time < best.time) best = p;
   return best;
 }
@@ -581,33 +615,58 @@ Fp8GemmArgs fp8_args(const TileOp& Q, const TileOp& P, int64_t K, void* C, int c
   return a;
 }
 
-hipError_t run_product(const Fp8GemmArgs& a, int64_t K, bool block, float* partial, hipStream_t s) {
-  const bool exact = !a.bf16;
-  const Fp8Plan plan = fp8_plan(a.Q.rows, a.P.rows, K, exact);
-  Fp8GemmArgs part = a, out = a;
-  part.splits = out.splits = partial ? plan.splits : 1;
-  if (part.splits > 1) {
-    out.partial = partial;
-    part.C = partial;
-    part.ldc = a.P.rows;
-    part.zstride = a.Q.rows * a.P.rows;
-    part.bf16 = part.accumulate = 0;
-    part.vec = (a.P.rows & 3) == 0;
+// A planned product; split: `part` is what the tiles write, joined into `out`.
+struct Fp8Product {
+  Fp8GemmArgs part, out;
+  int tile;
+  bool exact, block;
+};
+Fp8Product fp8_product(const Fp8GemmArgs& a, const Fp8Plan& plan, bool block, float* partial) {
+  Fp8Product x = {a, a, plan.tile, !a.bf16, block};
+  x.part.splits = x.out.splits = partial ? plan.splits : 1;
+  if (x.part.splits > 1) {
+    x.out.partial = partial;
+    x.part.C = partial;
+    x.part.ldc = a.P.rows;
+    x.part.zstride = a.Q.rows * a.P.rows;
+    x.part.bf16 = x.part.accumulate = 0;
+    x.part.vec = (a.P.rows & 3) == 0;
   }
+  return x;
+}
+hipError_t launch_product(const Fp8Product& x, hipStream_t s) {
   auto tiles = [&](auto el) {
     constexpr int EL = decltype(el)::value;
     if constexpr (EL == EL_FP8 || EL == EL_FP8B)
-      if (plan.tile == 2) return launch_tile<TileBig<EL>>(part, s);
-    if (plan.tile == 1) launch_tile<TileMid<EL>>(part, s);
-    else launch_tile<TileSmall<EL>>(part, s);
+      if (x.tile == 2) return launch_tile<TileBig<EL>>(x.part, s);
+    if (x.tile == 1) launch_tile<TileMid<EL>>(x.part, s);
+    else launch_tile<TileSmall<EL>>(x.part, s);
   };
-  if (exact && block) tiles(std::integral_constant<int, EL_FP8BX>{});
-  else if (exact) tiles(std::integral_constant<int, EL_FP8X>{});
-  else if (block) tiles(std::integral_constant<int, EL_FP8B>{});
+  if (x.exact && x.block) tiles(std::integral_constant<int, EL_FP8BX>{});
+  else if (x.exact) tiles(std::integral_constant<int, EL_FP8X>{});
+  else if (x.block) tiles(std::integral_constant<int, EL_FP8B>{});
   else tiles(std::integral_constant<int, EL_FP8>{});
-  if (hipError_t e = hipGetLastError(); e != hipSuccess || part.splits == 1) return e;
-  fp8_join_kernel<<<(uint32_t)((a.Q.rows * ((a.P.rows + 3) / 4) + 255) / 256), 256, 0, s>>>(out);
   return hipGetLastError();
+}
+// The joins of those that are split.
+hipError_t launch_joins(const Fp8Product* x, int n, hipStream_t s) {
+  Pair<Fp8GemmArgs> jobs = {};
+  uint32_t grid[2] = {0, 0};
+  int k = 0;
+  for (int i = 0; i < n; ++i) {
+    if (x[i].out.splits == 1) continue;
+    jobs.x[k] = x[i].out;
+    grid[k++] = (uint32_t)((x[i].out.Q.rows * ((x[i].out.P.rows + 3) / 4) + 255) / 256);
+  }
+  if (!k) return hipSuccess;
+  jobs.first = grid[0];
+  fp8_join_kernel<<<grid[0] + grid[1], 256, 0, s>>>(jobs);
+  return hipGetLastError();
+}
+hipError_t run_product(const Fp8GemmArgs& a, int64_t K, bool block, float* partial, hipStream_t s) {
+  const Fp8Product x = fp8_product(a, fp8_plan(a.Q.rows, a.P.rows, K, !a.bf16), block, partial);
+  if (hipError_t e = launch_product(x, s); e != hipSuccess) return e;
+  return launch_joins(&x, 1, s);
 }
 
 hipError_t run_few(const Fp8GemmArgs& g, const QView& A, const void* x, hipStream_t s) {
@@ -643,13 +702,13 @@ hipError_t launch_fp8_quant(const Fp8QuantParams& q, hipStream_t s) {
   } else {
     const uint32_t by = (uint32_t)((q.rows + 127) / 128);
     if (q.in_dtype == TJ2_FP8) {
-      fp8_col_kernel<Codes><<<dim3((uint32_t)((q.cols + 127) / 128), by), 256, 0, s>>>(
+      fp8_col_kernel<Codes><<<dim3((uint32_t)((q.cols + 127) / 128), by), kColThreads, 0, s>>>(
           col_args(q.xq.codes, q.xq.s128, q.xq.nb * 128, q.rows, q.cols, q.out, false));
     } else if (q.in_dtype == TJ2_BF16) {
-      fp8_col_kernel<uint16_t><<<dim3((uint32_t)((q.cols + 127) / 128), by), 256, 0, s>>>(
+      fp8_col_kernel<uint16_t><<<dim3((uint32_t)((q.cols + 127) / 128), by), kColThreads, 0, s>>>(
           col_args(q.x, nullptr, q.cols, q.rows, q.cols, q.out, false));
     } else {
-      fp8_col_kernel<float><<<dim3((uint32_t)((q.cols + 63) / 64), by), 256, 0, s>>>(
+      fp8_col_kernel<float><<<dim3((uint32_t)((q.cols + 63) / 64), by), kColThreads, 0, s>>>(
           col_args(q.x, nullptr, q.cols, q.rows, q.cols, q.out, false));
     }
   }
@@ -699,17 +758,38 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // a blocked operand of the backward pass: codes, and the scales that follow them
 size_t blocked_codes(int64_t rows, int64_t len) { return (size_t)((rows + 127) / 128 * 128) * (size_t)((len + 127) / 128 * 128); }
 size_t blocked_bytes(int64_t rows, int64_t len) { return up256(blocked_codes(rows, len)) + up256(blocked_codes(rows, len) / 32); }
+// The backward's plans: of tiles of 64 or 128 for both, they run in one launch.
+struct Fp8BwdPlan {
+  Fp8Plan x, w;
+  Fp8BwdPlan(int64_t M, int64_t N, int64_t K, bool exact_dx) : x(fp8_plan(M, K, N, exact_dx)), w(fp8_plan(N, K, M, true)) {
+    double least = x.time + w.time;
+    for (int tile = 0; tile < 2; ++tile) {
+      const Fp8Plan a = fp8_plan(M, K, N, exact_dx, tile), b = fp8_plan(N, K, M, true, tile);
+      // the launch saved, and the CUs that either leaves idle
+      const double t = std::max({a.time, b.time, a.packed + b.packed});
+      if (t < least) {
+        least = t;
+        x = a;
+        w = b;
+      }
+    }
+  }
+  bool together() const { return x.tile == w.tile; }
+};
 struct Fp8BwdSpace {
   size_t dy, dyt, wt, xt, px, pw, bytes;
   Fp8BwdSpace(int64_t M, int64_t N, int64_t K) {
+    // (of either type of dX)
+    const Fp8BwdPlan plan[2] = {{M, N, K, false}, {M, N, K, true}};
+    auto part = [](const Fp8Plan& p, int64_t I, int64_t J) { return p.splits > 1 ? (size_t)p.splits * (size_t)(I * J) * 4 : 0; };
     size_t at = 0;
     auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
     dy = take(blocked_bytes(M, N));
     dyt = take(blocked_bytes(N, M));
     wt = take(blocked_codes(K, N));
     xt = take(blocked_bytes(K, M));
-    px = take(fp8_gemm_workspace_bytes(M, K, N));
-    pw = take(split_bytes(N, K, M, true));
+    px = take(std::max(part(plan[0].x, M, K), part(plan[1].x, M, K)));
+    pw = take(std::max(part(plan[0].w, N, K), part(plan[1].w, N, K)));
     bytes = at;
   }
 };
@@ -737,16 +817,28 @@ hipError_t launch_fp8_linear_bwd(const void* dY, const QView& Xq, const QView& W
   const Fp8DualArgs d = {reinterpret_cast<const uint16_t*>(dY), fp8_out(dy, true), fp8_out(dyt, true), M, (int32_t)N, (int32_t)((N + 127) / 128)};
   const Fp8ColArgs tw = col_args(Wq.codes, nullptr, Wq.nb * 128, N, K, wt, true), tx = col_args(Xq.codes, Xq.s128, Xq.nb * 128, M, K, xt, true);
   const uint32_t kb = (uint32_t)((K + 127) / 128), mb = (uint32_t)((M + 127) / 128), nb = (uint32_t)((N + 127) / 128);
-  fp8_backward_kernel<<<nb * mb + kb * nb + kb * mb, 256, 0, s>>>(d, nb * mb, tw, kb * nb, tx);
+  fp8_backward_kernel<<<nb * mb + kb * nb + kb * mb, kColThreads, 0, s>>>(d, nb * mb, tw, kb * nb, tx);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   TileOp P = fp8_operand(wt, true);
   P.s = reinterpret_cast<const uint8_t*>(Wq.s128);  // of the turned codes: the same scales, read the other way
   P.srs = 4;
   P.scs = Wq.nb * 4;
-  const Fp8GemmArgs x = fp8_args(fp8_operand(dy, true), P, N, dX, dx_dtype, K, 0);
-  if (hipError_t e = run_product(x, N, true, reinterpret_cast<float*>(w + sp.px), s); e != hipSuccess) return e;
-  const Fp8GemmArgs g = fp8_args(fp8_operand(dyt, true), fp8_operand(xt, true), M, dW, TJ2_F32, K, 0);
-  return run_product(g, M, false, reinterpret_cast<float*>(w + sp.pw), s);
+  const Fp8BwdPlan plan(M, N, K, dx_dtype == TJ2_F32);
+  const Fp8Product x[2] = {
+      fp8_product(fp8_args(fp8_operand(dy, true), P, N, dX, dx_dtype, K, 0), plan.x, true, reinterpret_cast<float*>(w + sp.px)),
+      fp8_product(fp8_args(fp8_operand(dyt, true), fp8_operand(xt, true), M, dW, TJ2_F32, K, 0), plan.w, false,
+                  reinterpret_cast<float*>(w + sp.pw))};
+  if (plan.together()) {
+    if (x[0].exact && x[0].tile) launch_pair<TileMid<EL_FP8X>, TileMid<EL_FP8BX>>(x[1].part, x[0].part, s);
+    else if (x[0].exact) launch_pair<TileSmall<EL_FP8X>, TileSmall<EL_FP8BX>>(x[1].part, x[0].part, s);
+    else if (x[0].tile) launch_pair<TileMid<EL_FP8X>, TileMid<EL_FP8B>>(x[1].part, x[0].part, s);
+    else launch_pair<TileSmall<EL_FP8X>, TileSmall<EL_FP8B>>(x[1].part, x[0].part, s);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  } else {
+    for (const Fp8Product& p : x)
+      if (hipError_t e = launch_product(p, s); e != hipSuccess) return e;
+  }
+  return launch_joins(x, 2, s);
 }
 
 }  // namespace tj2

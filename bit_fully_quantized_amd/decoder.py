@@ -8,10 +8,11 @@ SwiGLU gate, up and down projections and the LM head -- is an NVFP4 linear
 weights updated by the fused master-weight pass (AdamW, then OsciReset,
 section 2.B, with the reset switched on once the learning rate is low).
 
-Everything outside the linear layers is glue and is plain PyTorch on the GPU:
-token embedding, RMSNorm (pre-norm), rotary position embedding, causal bf16
-attention (the fused flash / memory-efficient kernels only), SwiGLU, the
-cross-entropy loss, and AdamW on the embedding and norm weights.  The pages
+Everything outside the linear layers is glue and is plain PyTorch on the GPU
+(unless configured otherwise, below): token embedding, RMSNorm (pre-norm), rotary
+position embedding, causal bf16 attention (the fused flash / memory-efficient
+kernels only), SwiGLU, the cross-entropy loss, and AdamW on the embedding and
+norm weights.  The pages
 give no OLMo-2 details; the layout here (pre-norm blocks, RoPE theta 10000,
 16 heads of 64, untied LM head) is the plainest one of that family.
 
@@ -22,9 +23,18 @@ With linear="mxfp4" they are MXFP4 linears (mx.py) under the same backward
 recipe (stochastic rounding after the Hadamard transform), with AdamW on the
 masters, which are quantized once a step.
 
+With linear="fp8" they are FP8 linears (fp8.py: activations under a scale per
+128 elements, weights per 128 x 128), the precision the pages measure the 4-bit
+method against, with AdamW on the masters.
+
 With head="fused" the head is a bf16 product whose cross entropy is taken
 without the logits (losses.py), whatever the other linears are.  train_step
 learns from a teacher's top logits where it is given them (distillation).
+
+With norm="fused" the RMSNorms run in the library (norm.py), each with the
+addition of the residual before it; before FP8 linears the norm writes their
+operand, which is then never stored in bf16.  With mlp="fused" the feed-forward
+block is one operator on bf16 weights (ffn.py), whatever the other linears are.
 """
 from __future__ import annotations
 
@@ -33,13 +43,17 @@ from dataclasses import dataclass
 
 import torch
 import torch.nn.functional as F
+from torch.autograd.function import once_differentiable
 from torch.nn.attention import SDPBackend, sdpa_kernel
 
 from . import (FP8, NVFP4, OSCI_ACCUM, OSCI_INIT, OSCI_WINDOW_END, MasterBatch, NextBwd, QTensor, bwd_operands,
                channel_sumsq, lib, linear_bwd, linear_fwd, master_update_step_multi, osci_reset_step,
                select_outliers)
+from .ffn import gated_ffn
+from .fp8 import fp8_dequantize, fp8_linear_bwd, fp8_linear_bwd_workspace_size, fp8_linear_fwd, fp8_quantize
 from .losses import distillation_loss, linear_cross_entropy
 from .mx import mx_linear_bwd, mx_linear_bwd_workspace_size, mx_linear_fwd, mx_quantize
+from .norm import rms_norm, rms_norm_bwd, rms_norm_fwd
 
 
 @dataclass
@@ -66,8 +80,10 @@ class DecoderConfig:
     norm_eps: float = 1e-6
     init_std: float = 0.02
     seed: int = 0                   # parameters and Philox stream
-    linear: str = "nvfp4"           # "nvfp4", "mxfp4" (libtj2) or "bf16" (comparator)
+    linear: str = "nvfp4"           # "nvfp4", "mxfp4", "fp8" (libtj2) or "bf16" (comparator)
     head: str = "linear"            # "linear" (as the others) or "fused" (bf16, cross entropy without the logits)
+    norm: str = "torch"             # "torch" or "fused" (libtj2, with the residual's addition)
+    mlp: str = "linear"             # "linear" (three linears as the others) or "fused" (one bf16 operator)
     distill_temperature: float = 1.0  # with a teacher: loss alpha tau^2 KL + (1 - alpha) cross entropy
     distill_alpha: float = 0.5
 
@@ -97,11 +113,38 @@ class _LinearFn(torch.autograd.Function):
         return ctx.lin.backward(dY.contiguous(), ctx.saved), None
 
 
+class _NormLinearsFn(torch.autograd.Function):
+    """s = x + delta, its norm in FP8 and the FP8 linears on that: (s, Y of each)."""
+
+    @staticmethod
+    def forward(ctx, x, delta, weight, lins, eps):
+        ctx.set_materialize_grads(False)
+        if delta is None:
+            q, s, rstd = rms_norm_fwd(x, weight, eps=eps, fp8=True)
+        else:
+            q, s, rstd = rms_norm_fwd(delta, weight, residual=x, eps=eps, fp8=True)
+        outs = [L.forward(q) for L in lins]
+        ctx.lins, ctx.saved = lins, [saved for _, saved in outs]
+        ctx.save_for_backward(s, weight, rstd)
+        return (s if delta is not None else x.view_as(x), *(Y for Y, _ in outs))
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dsum, *dYs):
+        s, weight, rstd = ctx.saved_tensors
+        dh = None
+        for L, saved, dY in zip(ctx.lins, ctx.saved, dYs):
+            dX = L.backward(dY.contiguous(), saved)
+            dh = dX if dh is None else dh.add_(dX)
+        ds, dw = rms_norm_bwd(dh, s, weight, rstd, dsum=None if dsum is None else dsum.contiguous())
+        return ds, ds if ctx.needs_input_grad[1] else None, dw, None, None
+
+
 class Linear:
     """One linear layer Y = X W^T of the stack (W [N, K]): the fp32 master with its AdamW moments and
     OsciReset state, the forward codes under the layer's outlier plan, and the next backward's
-    re-grouped weights that the master pass forms.  kind "mxfp4": the MXFP4 codes of the master instead;
-    kind "fused": a bf16 copy Wg of the master, with a gradient of its own."""
+    re-grouped weights that the master pass forms.  kind "mxfp4" or "fp8": the MXFP4 or FP8 codes of the master
+    instead; kind "fused": a bf16 copy Wg of the master, with a gradient of its own."""
 
     def __init__(self, stack: "Decoder", idx: int, name: str, N: int, K: int, gen: torch.Generator, kind: str):
         self.stack, self.idx, self.name, self.N, self.K, self.kind = stack, idx, name, N, K, kind
@@ -115,7 +158,7 @@ class Linear:
         self.w_given = False
         self.Wf = None       # bf16 comparator: bf16 copies of W^T [K, N] (forward) and W [N, K] (backward)
         self.Wg = None
-        self.Wq = None       # codes of the master: NVFP4 (under the plan) or MXFP4
+        self.Wq = None       # codes of the master: NVFP4 (under the plan), MXFP4 or FP8
 
     # ---- set-up ---------------------------------------------------------------------------------
     def finalize(self):
@@ -141,6 +184,8 @@ class Linear:
             self.Wg = self.W.to(torch.bfloat16)
         elif self.kind == "fused":
             self.Wg = self.W.to(torch.bfloat16).requires_grad_(True)
+        elif self.kind == "fp8":
+            self.Wq = fp8_quantize(self.W, block=True)
         else:
             self.Wq = mx_quantize(self.W)
 
@@ -153,14 +198,22 @@ class Linear:
             with torch.no_grad():
                 self.Wg.copy_(self.W)
             self.Wg.grad = None
+        elif self.kind == "fp8":
+            fp8_quantize(self.W, out=self.Wq)
         else:
             mx_quantize(self.W, out=self.Wq)
 
     # ---- products -------------------------------------------------------------------------------
-    def forward(self, X: torch.Tensor):
+    def forward(self, X):
+        """(Y, what the backward needs) of X [M, K] bf16 (kind "fp8": or an FP8 operand)."""
         st = self.stack
         if self.kind == "bf16":
             return torch.mm(X, self.Wf), X
+        if self.kind == "fp8":
+            Y, saved = fp8_linear_fwd(X, None, self.N, Wq=self.Wq)
+            if self.capture is not None:
+                self.capture.update(X=fp8_dequantize(saved["Xq"], dtype=torch.float32), W=self.W.clone(), Y=Y.clone(), step=st.step)
+            return Y, saved
         if self.kind == "mxfp4":
             Y, saved = mx_linear_fwd(X, None, self.N, Wq=self.Wq)
             if self.capture is not None:
@@ -182,6 +235,11 @@ class Linear:
             torch.mm(dY.t(), X, out=self.gradb)
             self.grad.copy_(self.gradb)
             return torch.mm(dY, self.Wg)
+        if self.kind == "fp8":
+            dX, _ = fp8_linear_bwd(dY, saved, self.K, dW=self.grad, workspace=st.fp8_workspace(dY.shape[0], self.N, self.K))
+            if self.capture is not None:
+                self.capture.update(dY=dY.clone(), dX=dX.clone(), dW=self.grad.clone())
+            return dX
         offset = st.offset(self.idx, st.step)
         if self.kind == "mxfp4":
             dX, _ = mx_linear_bwd(dY, saved, self.K, seed=st.cfg.seed, offset=offset, dW=self.grad,
@@ -214,8 +272,9 @@ class Decoder:
 
     def __init__(self, cfg: DecoderConfig, device="cuda"):
         self.cfg, self.device = cfg, device
-        assert cfg.d_model % cfg.heads == 0 and cfg.linear in ("nvfp4", "mxfp4", "bf16")
-        assert cfg.head in ("linear", "fused")
+        assert cfg.d_model % cfg.heads == 0 and cfg.linear in ("nvfp4", "mxfp4", "fp8", "bf16")
+        assert cfg.head in ("linear", "fused") and cfg.norm in ("torch", "fused") and cfg.mlp in ("linear", "fused")
+        mlp = "fused" if cfg.mlp == "fused" else cfg.linear
         g = torch.Generator(device=device)
         g.manual_seed(cfg.seed)
         d = cfg.d_model
@@ -234,8 +293,8 @@ class Decoder:
                 "attn_norm": torch.ones(d, device=device, requires_grad=True),
                 "qkv": lin(f"{i}.qkv", 3 * d, d), "o": lin(f"{i}.o", d, d),
                 "mlp_norm": torch.ones(d, device=device, requires_grad=True),
-                "gate": lin(f"{i}.gate", cfg.ffn, d), "up": lin(f"{i}.up", cfg.ffn, d),
-                "down": lin(f"{i}.down", d, cfg.ffn)})
+                "gate": lin(f"{i}.gate", cfg.ffn, d, mlp), "up": lin(f"{i}.up", cfg.ffn, d, mlp),
+                "down": lin(f"{i}.down", d, cfg.ffn, mlp)})
         self.head = lin("head", cfg.vocab, d, "fused" if cfg.head == "fused" else cfg.linear)
         self.nvfp4 = [L for L in self.linears if L.kind == "nvfp4"]   # updated by the fused master pass
         self.others = [L for L in self.linears if L.kind != "nvfp4"]  # by AdamW on the masters
@@ -253,6 +312,7 @@ class Decoder:
         self._ops = {}
         self.bwd_ws = None
         self._mx_ws = None
+        self._fp8_ws = None
         self.reset_count = torch.zeros(1, dtype=torch.int64, device=device)
 
     # ---- glue -------------------------------------------------------------------------------------
@@ -265,26 +325,51 @@ class Decoder:
         c, s = self.cos[: t.shape[2]], self.sin[: t.shape[2]]
         return torch.stack((t1 * c - t2 * s, t1 * s + t2 * c), dim=-1).flatten(-2).to(torch.bfloat16)
 
-    def hidden(self, tokens: torch.Tensor) -> torch.Tensor:
-        """The head's input [B*S, d_model] (bf16) of tokens [B, S]."""
+    def _stream(self, tokens: torch.Tensor):
+        """The residual stream [B*S, d_model] (bf16) after the last block, and what that block still adds to it."""
         cfg = self.cfg
         B, S = tokens.shape
         M, d, H = B * S, cfg.d_model, cfg.heads
         x = F.embedding(tokens.reshape(-1), self.emb).to(torch.bfloat16)
+        delta = None  # what the last block adds to the residual stream x
         for blk in self.blocks:
-            qkv = blk["qkv"](self._rmsnorm(x, blk["attn_norm"]))
+            x, qkv = self._norm_linears(x, delta, blk["attn_norm"], [blk["qkv"]])
             q, k, v = qkv.view(B, S, 3, H, d // H).permute(2, 0, 3, 1, 4).unbind(0)
             with sdpa_kernel([SDPBackend.FLASH_ATTENTION, SDPBackend.EFFICIENT_ATTENTION]):
                 o = F.scaled_dot_product_attention(self._rope(q), self._rope(k), v.contiguous(), is_causal=True)
-            x = x + blk["o"](o.transpose(1, 2).reshape(M, d).contiguous())
-            h = self._rmsnorm(x, blk["mlp_norm"])
-            a = F.silu(blk["gate"](h)) * blk["up"](h)
-            x = x + blk["down"](a.contiguous())
-        return self._rmsnorm(x, self.final_norm)
+            delta = blk["o"](o.transpose(1, 2).reshape(M, d).contiguous())
+            if cfg.mlp == "fused":
+                x, h = self._norm(x, delta, blk["mlp_norm"])
+                delta = gated_ffn(h, blk["gate"].Wg, blk["up"].Wg, blk["down"].Wg)
+            else:
+                x, gate, up = self._norm_linears(x, delta, blk["mlp_norm"], [blk["gate"], blk["up"]])
+                delta = blk["down"]((F.silu(gate) * up).contiguous())
+        return x, delta
+
+    def _norm(self, x, delta, weight):
+        """(s, norm of s) of s = x + delta (x where nothing is to be added)."""
+        if self.cfg.norm == "fused":
+            if delta is None:
+                return x, rms_norm(x, weight, eps=self.cfg.norm_eps)
+            h, s = rms_norm(delta, weight, x, eps=self.cfg.norm_eps)
+            return s, h
+        s = x if delta is None else x + delta
+        return s, self._rmsnorm(s, weight)
+
+    def _norm_linears(self, x, delta, weight, lins):
+        """(s, Y of each linear on the norm of s) of s = x + delta."""
+        if self.cfg.norm == "fused" and lins[0].kind == "fp8":
+            return _NormLinearsFn.apply(x, delta, weight, lins, self.cfg.norm_eps)
+        s, h = self._norm(x, delta, weight)
+        return (s, *(L(h) for L in lins))
+
+    def hidden(self, tokens: torch.Tensor) -> torch.Tensor:
+        """The head's input [B*S, d_model] (bf16) of tokens [B, S]."""
+        return self._norm(*self._stream(tokens), self.final_norm)[1]
 
     def forward(self, tokens: torch.Tensor) -> torch.Tensor:
         """Logits [B*S, vocab] (bf16) of tokens [B, S]."""
-        return self.head(self.hidden(tokens))
+        return self._norm_linears(*self._stream(tokens), self.final_norm, [self.head])[1]
 
     def loss(self, tokens: torch.Tensor, targets: torch.Tensor, teacher=None) -> torch.Tensor:
         """Mean loss of next-token targets [B, S] (targets of -100 are left out): cross entropy, or with
@@ -316,6 +401,13 @@ class Decoder:
         if self._mx_ws is None or self._mx_ws.numel() < n:
             self._mx_ws = torch.empty(n, dtype=torch.uint8, device=self.device)
         return self._mx_ws
+
+    def fp8_workspace(self, M: int, N: int, K: int) -> torch.Tensor:
+        """The same for the FP8 backward passes."""
+        n = fp8_linear_bwd_workspace_size(M, N, K)
+        if self._fp8_ws is None or self._fp8_ws.numel() < n:
+            self._fp8_ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return self._fp8_ws
 
     def calibrate(self, batches):
         """OutControl: the top p% input channels of every NVFP4 linear from a short calibration window
@@ -360,8 +452,9 @@ class Decoder:
         lr = cfg.lr(t)
         loss = self.loss(tokens, targets, teacher)
         loss.backward()
-        if self.head.kind == "fused":
-            self.head.grad.copy_(self.head.Wg.grad)
+        for L in self.others:
+            if L.kind == "fused":
+                L.grad.copy_(L.Wg.grad)
         if before_update is not None:
             before_update(self)
         for grp in self.glue_opt.param_groups:
