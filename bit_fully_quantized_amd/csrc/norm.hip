@@ -43,29 +43,75 @@ struct NormGradArgs {
   int32_t cols, w_bf16;
 };
 
-// A thread's elements of a row: `NV` vectors of 8.  Whole rows of vectors (VEC: every row
-// is 16-byte aligned and a multiple of 8 long) are dealt out vector by vector, others
-// element by element, so that a wave's loads stay together.
-template <int TPR, bool VEC>
+// How a row's elements are dealt out over its threads, 8 and 8 or one and one:
+//   Whole   vectors of 8 neighbours, 16-byte accesses at any element's address
+//   Tail    the same where a row's last vector is part of one (bf16): its thread loads the
+//           row's last 8 elements and shifts them, without a branch, so that the loads of
+//           all vectors and tensors are on their way together
+//   Single  single elements (fp32 rows that are no multiple of 8)
+// Forward and backward with the residual's, in us: 16384 x 1023 bf16 25 and 42 as Tail, 32
+// and 42 where a branch loads the last vector's elements, 33 and 68 in pairs, 56 and 70 as
+// Single (16384 x 1024: 22 and 28); 1555 x 1003 fp32 5.7 and 10.3 as Single, 7.3 and 12.1 as Tail.
+enum class Deal { Whole, Tail, Single };
+
+template <int TPR, Deal D>
 struct Row {
-  static __device__ __forceinline__ int at(int v, int e, int t) { return VEC ? (v * TPR + t) * 8 + e : (v * 8 + e) * TPR + t; }
+  typedef uint32_t Words __attribute__((ext_vector_type(4), aligned(2)));
+  typedef float Floats __attribute__((ext_vector_type(4), aligned(4)));
+  static __device__ __forceinline__ int at(int v, int e, int t) { return D == Deal::Single ? (v * 8 + e) * TPR + t : (v * TPR + t) * 8 + e; }
+  static __device__ __forceinline__ float get(const float* p) { return *p; }
+  static __device__ __forceinline__ float get(const uint16_t* p) { return bf16_to_f32(*p); }
+  static __device__ __forceinline__ void get8(const float* p, float out[8]) {
+    const Floats a = *reinterpret_cast<const Floats*>(p), b = *reinterpret_cast<const Floats*>(p + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      out[e] = a[e];
+      out[4 + e] = b[e];
+    }
+  }
+  static __device__ __forceinline__ void get8(const uint16_t* p, float out[8]) {
+    const Words u = *reinterpret_cast<const Words*>(p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      out[2 * e] = __uint_as_float(u[e] << 16);
+      out[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ void put(float* p, float v) { *p = v; }
+  static __device__ __forceinline__ void put(uint16_t* p, float v) { *p = (uint16_t)bf16_pair(v, 0.0f); }
+  static __device__ __forceinline__ void put8(float* p, const float in[8]) {
+    *reinterpret_cast<Floats*>(p) = Floats{in[0], in[1], in[2], in[3]};
+    *reinterpret_cast<Floats*>(p + 4) = Floats{in[4], in[5], in[6], in[7]};
+  }
+  static __device__ __forceinline__ void put8(uint16_t* p, const float in[8]) {
+    *reinterpret_cast<Words*>(p) = Words{bf16_pair(in[0], in[1]), bf16_pair(in[2], in[3]), bf16_pair(in[4], in[5]), bf16_pair(in[6], in[7])};
+  }
+  // vector v of a row, zeros past its end
   template <class T>
   static __device__ __forceinline__ void load(const T* p, int v, int t, int cols, float out[8]) {
-    if constexpr (VEC) {
-      if (at(v, 0, t) < cols) {
-        load8(p + at(v, 0, t), out);
+    const int c = at(v, 0, t);
+    if constexpr (D == Deal::Whole) {
+      if (c < cols) {
+        get8(p + c, out);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) out[e] = 0.0f;
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = at(v, e, t);
-        if constexpr (std::is_same<T, float>::value) out[e] = c < cols ? p[c] : 0.0f;
-        else out[e] = c < cols ? bf16_to_f32(p[c]) : 0.0f;
-      }
+      return;
     }
+    if (D == Deal::Single || cols < 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] = at(v, e, t) < cols ? get(p + at(v, e, t)) : 0.0f;
+      return;
+    }
+    const int past = max(c + 8 - cols, 0);
+    get8(p + (c - past), out);
+#pragma unroll
+    for (int o = 1; o < 8; o *= 2)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] = past & o ? (e + o < 8 ? out[e + o] : 0.0f) : out[e];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = past < 8 ? out[e] : 0.0f;
   }
   static __device__ __forceinline__ void weight(const void* w, int bf16, int v, int t, int cols, float out[8]) {
     if (bf16) load(reinterpret_cast<const uint16_t*>(w), v, t, cols, out);
@@ -73,23 +119,13 @@ struct Row {
   }
   template <class T>
   static __device__ __forceinline__ void store(T* p, int v, int t, int cols, const float in[8]) {
-    if constexpr (VEC) {
-      if (at(v, 0, t) >= cols) return;
-      T* o = p + at(v, 0, t);
-      if constexpr (std::is_same<T, float>::value) {
-        reinterpret_cast<float4*>(o)[0] = float4{in[0], in[1], in[2], in[3]};
-        reinterpret_cast<float4*>(o)[1] = float4{in[4], in[5], in[6], in[7]};
-      } else {
-        *reinterpret_cast<uint4*>(o) = uint4{bf16_pair(in[0], in[1]), bf16_pair(in[2], in[3]), bf16_pair(in[4], in[5]), bf16_pair(in[6], in[7])};
-      }
-    } else {
+    const int c = at(v, 0, t);
+    if (D != Deal::Single && c + 8 <= cols) {
+      put8(p + c, in);
+    } else if constexpr (D != Deal::Whole) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = at(v, e, t);
-        if (c >= cols) continue;
-        if constexpr (std::is_same<T, float>::value) p[c] = in[e];
-        else p[c] = (uint16_t)bf16_pair(in[e], 0.0f);
-      }
+      for (int e = 0; e < 8; ++e)
+        if (at(v, e, t) < cols) put(p + at(v, e, t), in[e]);
     }
   }
 };
@@ -133,10 +169,12 @@ __device__ __forceinline__ void store_fp8(const NormArgs& p, int64_t row, int c,
 
 constexpr int kNormThreads = 256;
 
-// Rows whose elements the registers hold.
-template <class T, int TPR, int NV, bool RES, bool FP8, bool VEC>
+// Rows whose elements the registers hold, a wave or a workgroup a row.  Bound by memory:
+// 16384 x 1024 bf16 with the residual 22 us (134 MB at 6.0 TB/s; a copy reaches 5.1), fp32
+// 41 us (6.5 TB/s); with the FP8 result instead of the bf16 one 22 us (117 MB, 5.3 TB/s).
+template <class T, int TPR, int NV, Deal D, bool RES, bool FP8>
 __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormArgs p) {
-  using R = Row<TPR, VEC>;
+  using R = Row<TPR, D>;
   constexpr int RPW = kNormThreads / TPR;
   __shared__ float sh[4];
   const int t = threadIdx.x % TPR;
@@ -179,10 +217,11 @@ __global__ __launch_bounds__(kNormThreads) void norm_kernel(NormArgs p) {
   }
 }
 
-// Longer rows: a workgroup a row, which is read again for its results.
-template <class T, bool RES, bool FP8, bool VEC>
+// Longer rows: a workgroup a row, which is read again for its results (1000 x 20000 bf16
+// with the residual 31 us, 5.1 TB/s of the first reading and the results: L2 holds the row).
+template <class T, Deal D, bool RES, bool FP8>
 __global__ __launch_bounds__(kNormThreads) void norm_long_kernel(NormArgs p) {
-  using R = Row<kNormThreads, VEC>;
+  using R = Row<kNormThreads, D>;
   __shared__ float sh[4];
   const int t = threadIdx.x, nv = (p.cols + kNormThreads * 8 - 1) / (kNormThreads * 8);
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
@@ -218,11 +257,13 @@ __global__ __launch_bounds__(kNormThreads) void norm_long_kernel(NormArgs p) {
   }
 }
 
+// Bound by memory and, from 4 vectors a thread on, by the few waves that run: 16384 x 1024
+// bf16 with dsum 24 us (134 MB at 5.6 TB/s) and 4 us for norm_dw_kernel, fp32 47 us.
 // A thread keeps its columns' sums of dw over the workgroup's rows; each workgroup writes
 // its sums, which norm_dw_kernel adds up in order (no atomics: the same bits every run).
-template <class T, int TPR, int NV, bool DSUM, bool VEC>
+template <class T, int TPR, int NV, Deal D, bool DSUM>
 __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(NormGradArgs p) {
-  using R = Row<TPR, VEC>;
+  using R = Row<TPR, D>;
   constexpr int RPW = kNormThreads / TPR;
   __shared__ float sh[4];
   const int t = threadIdx.x % TPR;
@@ -283,25 +324,14 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(NormGradArgs p)
     if (threadIdx.x / 64 != RPW - 1) return;
   }
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    if constexpr (VEC) {
-      if (R::at(v, 0, t) < p.cols) {
-        float4* o = reinterpret_cast<float4*>(part + R::at(v, 0, t));
-        o[0] = float4{dw[v][0], dw[v][1], dw[v][2], dw[v][3]};
-        o[1] = float4{dw[v][4], dw[v][5], dw[v][6], dw[v][7]};
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (R::at(v, e, t) < p.cols) part[R::at(v, e, t)] = dw[v][e];
-    }
-  }
+  for (int v = 0; v < NV; ++v) R::store(part, v, t, p.cols, dw[v]);
 }
 
-// Longer rows: ds with the row read twice, and dw's sums over a slab of rows by columns.
-template <class T, bool DSUM, bool VEC>
+// Longer rows: ds with the row read twice (L2 holds it), and dw's sums over a slab of rows by
+// columns, which reads s and dy again (1000 x 20000 bf16 55 us, both and norm_dw_kernel).
+template <class T, Deal D, bool DSUM>
 __global__ __launch_bounds__(kNormThreads) void norm_grad_long_kernel(NormGradArgs p) {
-  using R = Row<kNormThreads, VEC>;
+  using R = Row<kNormThreads, D>;
   __shared__ float sh[4];
   const int t = threadIdx.x, nv = (p.cols + kNormThreads * 8 - 1) / (kNormThreads * 8);
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
@@ -392,6 +422,12 @@ void pick(bool b, F&& f) {
   if (b) f(Is<true>{});
   else f(Is<false>{});
 }
+template <class T, class F>
+void pick_deal(int64_t cols, F&& f) {
+  constexpr Deal odd = std::is_same<T, float>::value ? Deal::Single : Deal::Tail;
+  if (cols % 8 == 0) f(std::integral_constant<Deal, Deal::Whole>{});
+  else f(std::integral_constant<Deal, odd>{});
+}
 // f(threads a row, vectors a thread) for rows of `cols`
 template <class F>
 void pick_row(int64_t cols, F&& f) {
@@ -402,19 +438,21 @@ void pick_row(int64_t cols, F&& f) {
   else f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
 }
 
-bool vectors(const void* p, int64_t ld, int es) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * es % 16 == 0; }
-
 int64_t norm_rows_per_group(int64_t cols) { return cols <= kNormWave ? 4 : 1; }
 // Workgroups of the forward pass: up to 8 a CU, so that a weight is read for several rows.
 uint32_t norm_grid(int64_t rows, int64_t cols) {
   const int64_t per = norm_rows_per_group(cols);
   return (uint32_t)std::min<int64_t>((rows + per - 1) / per, 8 * kCus);
 }
-// Workgroups of the backward pass, each with a row of dw's sums.
+// Workgroups of the backward pass, each with a row of dw's sums: as many as the registers
+// let run at once, 2 a CU with 4 vectors a thread (8192 x 2048 bf16: 31 us, with 4 a CU 35,
+// with 1 48; 2048 x 8192: 35, 41 and 46) and else 4 (16384 x 1024: 28 us, with 2 32, with 8
+// 32; 4096 x 4096: 31, 34 and 38).
 int64_t norm_parts(int64_t rows, int64_t cols) {
   if (cols > kNormHeld) return std::min<int64_t>((rows + 63) / 64, 64);
   const int64_t per = norm_rows_per_group(cols);
-  return std::min<int64_t>((rows + per - 1) / per, 4 * kCus);
+  const bool four = (cols > 1024 && cols <= kNormWave) || cols > 4096;
+  return std::min<int64_t>((rows + per - 1) / per, (four ? 2 : 4) * kCus);
 }
 
 template <class T>
@@ -435,21 +473,17 @@ hipError_t run_norm(const NormParams& n, hipStream_t s) {
   a.rows = n.rows;
   a.cols = (int32_t)n.cols;
   a.eps = n.eps;
-  const int es = sizeof(T);
-  const bool vec = n.cols % 8 == 0 && vectors(n.x, n.ldx, es) && (!n.residual || (vectors(n.residual, n.ldr, es) && vectors(n.sum, 0, es))) &&
-                   vectors(n.w, 0, 4) && (!n.y || vectors(n.y, 0, es));
-  const bool fp8 = !n.y;
   const uint32_t grid = norm_grid(n.rows, n.cols);
-  pick(n.residual != nullptr, [&](auto res) {
-    if (fp8) {  // vectors: the entry point has checked
-      if (n.cols > kNormHeld) return (void)norm_long_kernel<T, res.value, true, true><<<grid, kNormThreads, 0, s>>>(a);
-      pick_row(n.cols, [&](auto tpr, auto nv) { norm_kernel<T, tpr.value, nv.value, res.value, true, true><<<grid, kNormThreads, 0, s>>>(a); });
-    } else {
-      pick(vec, [&](auto v) {
-        if (n.cols > kNormHeld) return (void)norm_long_kernel<T, res.value, false, v.value><<<grid, kNormThreads, 0, s>>>(a);
-        pick_row(n.cols, [&](auto tpr, auto nv) { norm_kernel<T, tpr.value, nv.value, res.value, false, v.value><<<grid, kNormThreads, 0, s>>>(a); });
+  pick_deal<T>(n.cols, [&](auto deal) {
+    pick(n.residual != nullptr, [&](auto res) {
+      pick(!n.y, [&](auto fp8) {
+        if constexpr (fp8.value && deal.value != Deal::Whole) return;  // (whole groups of 128)
+        if (n.cols > kNormHeld) return (void)norm_long_kernel<T, deal.value, res.value, fp8.value><<<grid, kNormThreads, 0, s>>>(a);
+        pick_row(n.cols, [&](auto tpr, auto nv) {
+          norm_kernel<T, tpr.value, nv.value, deal.value, res.value, fp8.value><<<grid, kNormThreads, 0, s>>>(a);
+        });
       });
-    }
+    });
   });
   return hipGetLastError();
 }
@@ -470,17 +504,14 @@ hipError_t run_norm_grad(const NormGradParams& n, float* part, hipStream_t s) {
   a.part = n.dw ? part : nullptr;
   a.rows = n.rows;
   a.cols = (int32_t)n.cols;
-  const int es = sizeof(T);
-  const bool vec = n.cols % 8 == 0 && vectors(n.dy, n.lddy, es) && vectors(n.s, n.lds, es) && (!n.dsum || vectors(n.dsum, n.ldd, es)) &&
-                   vectors(n.w, 0, 4) && (!n.ds || vectors(n.ds, 0, es));
   const int64_t parts = norm_parts(n.rows, n.cols);
-  pick(n.dsum && n.ds, [&](auto dsum) {
-    pick(vec, [&](auto v) {
+  pick_deal<T>(n.cols, [&](auto deal) {
+    pick(n.dsum && n.ds, [&](auto dsum) {
       if (n.cols > kNormHeld) {
-        if (n.ds) norm_grad_long_kernel<T, dsum.value, v.value><<<norm_grid(n.rows, n.cols), kNormThreads, 0, s>>>(a);
+        if (n.ds) norm_grad_long_kernel<T, deal.value, dsum.value><<<norm_grid(n.rows, n.cols), kNormThreads, 0, s>>>(a);
       } else {
         pick_row(n.cols, [&](auto tpr, auto nv) {
-          norm_grad_kernel<T, tpr.value, nv.value, dsum.value, v.value><<<(uint32_t)parts, kNormThreads, 0, s>>>(a);
+          norm_grad_kernel<T, tpr.value, nv.value, deal.value, dsum.value><<<(uint32_t)parts, kNormThreads, 0, s>>>(a);
         });
       }
     });
