@@ -1482,6 +1482,7 @@ size_t fp8_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K) {
 tj2_status fp8_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, const tj2_qtensor* Xq, const tj2_qtensor* Wq, void* dX,
                           int32_t dx_dtype, float* dW, void* workspace, size_t ws_bytes, void* stream) {
   if (!dY || !dX || !dW || !workspace) return fail(TJ2_ERR_ARG, "dY, dX, dW and workspace are required");
+  if (dX == dW) return fail(TJ2_ERR_ARG, "dX must not be dW");
   TJ2_TRY(check_linear_dims(M, N, K));
   TJ2_TRY(check_fp8(Xq, "Xq", TJ2_FP8, M, K));
   TJ2_TRY(check_fp8(Wq, "Wq", TJ2_FP8_BLOCK, N, K));
@@ -1519,6 +1520,13 @@ tj2_status check_stream(const void* p, int64_t ld, int32_t dtype, int64_t cols, 
   if (ld < cols) return fail(TJ2_ERR_SHAPE, "%s: rows of %lld elements lie %lld apart", name, (long long)cols, (long long)ld);
   return TJ2_OK;
 }
+// A dense result may take an input's place where the rows are the same (with another pitch a
+// row's result would lie on rows that others still read).
+tj2_status check_in_place(const void* out, const char* out_name, const void* in, int64_t ld, int64_t rows, int64_t cols, const char* name) {
+  if (out && out == in && ld != cols && rows > 1)
+    return fail(TJ2_ERR_ARG, "%s can be %s only where its rows are %lld apart", out_name, name, (long long)cols);
+  return TJ2_OK;
+}
 
 }  // namespace
 
@@ -1534,7 +1542,12 @@ tj2_status tj2_rms_norm_fwd(const void* x, int64_t ldx, const void* residual, in
   if (residual) {
     TJ2_TRY(check_stream(residual, ldr, dtype, cols, "residual"));
     TJ2_TRY(check_stream(sum, cols, dtype, cols, "sum"));
+    TJ2_TRY(check_in_place(sum, "sum", x, ldx, rows, cols, "x"));
+    TJ2_TRY(check_in_place(sum, "sum", residual, ldr, rows, cols, "residual"));
+    if (y == sum) return fail(TJ2_ERR_ARG, "y must not be sum");
+    TJ2_TRY(check_in_place(y, "y", residual, ldr, rows, cols, "residual"));
   }
+  TJ2_TRY(check_in_place(y, "y", x, ldx, rows, cols, "x"));
   if ((y == nullptr) == (yq == nullptr)) return fail(TJ2_ERR_ARG, "one of y and yq must be given");
   TJ2_TRY(check_f32(rstd, "rstd", false));
   NormParams n = {};
@@ -1581,6 +1594,9 @@ tj2_status tj2_rms_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t
   if (!ds && !dw) return fail(TJ2_ERR_ARG, "ds or dw is required");
   if (dsum) TJ2_TRY(check_stream(dsum, ldd, dtype, cols, "dsum"));
   if (ds) TJ2_TRY(check_stream(ds, cols, dtype, cols, "ds"));
+  TJ2_TRY(check_in_place(ds, "ds", dy, lddy, rows, cols, "dy"));
+  TJ2_TRY(check_in_place(ds, "ds", s, lds, rows, cols, "s"));
+  TJ2_TRY(check_in_place(ds, "ds", dsum, ldd, rows, cols, "dsum"));
   if (dw) {
     if (reinterpret_cast<uintptr_t>(dw) & (w_dtype == TJ2_BF16 ? 1u : 3u)) return fail(TJ2_ERR_ALIGN, "dw must be aligned to its elements");
     TJ2_TRY(check_ce_workspace(workspace, ws_bytes, norm_grad_workspace_bytes(rows, cols)));
@@ -1682,6 +1698,8 @@ tj2_status tj2_gated_ffn_bwd(const void* dY, int64_t ldy, const void* X, int64_t
   TJ2_TRY(check_ffn(X, ldx, Wg, Wu, ldw, Wd, ldd, T, D, F, act));
   if (!dY || !gu) return fail(TJ2_ERR_ARG, "dY and gu are required");
   if (!dX && !dWg && !dWu && !dWd) return fail(TJ2_ERR_ARG, "dX, dWg, dWu or dWd is required");
+  for (const void* w : {dWg, dWu, dWd})
+    if (w && (w == dX || (w == dWg) + (w == dWu) + (w == dWd) > 1)) return fail(TJ2_ERR_ARG, "dX, dWg, dWu and dWd must not be one another");
   if (ldy < D || ldy % 8 || ldy > (int64_t)1 << 21) return fail(TJ2_ERR_SHAPE, "ldy must be a multiple of 8, at least D and at most 2^21");
   if (dX) TJ2_TRY(check_out_dtype(dx_dtype, "dx_dtype"));
   if (dWg || dWu || dWd) TJ2_TRY(check_out_dtype(dw_dtype, "dw_dtype"));

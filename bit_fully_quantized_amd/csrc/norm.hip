@@ -505,6 +505,11 @@ hipError_t run_norm_grad(const NormGradParams& n, float* part, hipStream_t s) {
   a.rows = n.rows;
   a.cols = (int32_t)n.cols;
   const int64_t parts = norm_parts(n.rows, n.cols);
+  if (n.cols > kNormHeld && n.dw) {  // first: ds may take dy's or s' place
+    const dim3 grid((uint32_t)((n.cols + kNormThreads - 1) / kNormThreads), (uint32_t)parts);
+    norm_grad_slab_kernel<T><<<grid, kNormThreads, 0, s>>>(a, (n.rows + parts - 1) / parts);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
   pick_deal<T>(n.cols, [&](auto deal) {
     pick(n.dsum && n.ds, [&](auto dsum) {
       if (n.cols > kNormHeld) {
@@ -517,11 +522,6 @@ hipError_t run_norm_grad(const NormGradParams& n, float* part, hipStream_t s) {
     });
   });
   if (hipError_t e = hipGetLastError(); e != hipSuccess || !n.dw) return e;
-  if (n.cols > kNormHeld) {
-    const dim3 grid((uint32_t)((n.cols + kNormThreads - 1) / kNormThreads), (uint32_t)parts);
-    norm_grad_slab_kernel<T><<<grid, kNormThreads, 0, s>>>(a, (n.rows + parts - 1) / parts);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  }
   norm_dw_kernel<<<(uint32_t)((n.cols + 31) / 32), 1024, 0, s>>>(part, (int)parts, n.cols, n.dw, n.w_dtype == TJ2_BF16);
   return hipGetLastError();
 }

@@ -74,7 +74,7 @@ def rms_norm_bwd(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: 
                  ds: torch.Tensor | None = None, dweight: torch.Tensor | None = None, need_ds: bool = True, need_dw: bool = True,
                  workspace: torch.Tensor | None = None):
     """(ds, dweight) of rms_norm_fwd's y for its gradient dy [rows, cols] of s's type; dsum, the gradient that comes in
-    for s itself, is added to ds, which is the gradient of x and of residual (ds may be dy or dsum).  need_ds / need_dw
+    for s itself, is added to ds, which is the gradient of x and of residual (ds may be dy, s or dsum).  need_ds / need_dw
     False leaves that gradient out (None)."""
     index = _tensor(s, "s", 2)
     if s.dtype not in _OUT:

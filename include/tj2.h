@@ -775,7 +775,8 @@ size_t fp8_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
  *       without a residual s is x;
  *   rstd[row] = 1 / sqrt(mean(s^2) + eps)  (fp32 [rows], may be NULL; needed for the backward);
  *   y = s rstd weight into y [rows, cols] of dtype, contiguous, or (y NULL) *yq, TJ2_FP8,
- *       quantized as fp8_quantize does from the unrounded fp32 values.
+ *       quantized as fp8_quantize does from the unrounded fp32 values.  y may be x or residual
+ *       where that is contiguous, but not sum.
  * For yq, cols is a multiple of 16 and x, residual, their rows, sum and weight are 16-byte
  * aligned; else pointers are aligned to their elements.  Statistics are fp32: squares that
  * leave its range are infinite (rstd 0) or 0.  eps >= 0; a row of zeros with eps 0 is NaN.
@@ -788,7 +789,7 @@ tj2_status tj2_rms_norm_fwd(const void* x, int64_t ldx, const void* residual, in
  * tj2_rms_norm_bwd: from dy, the gradient of y, and s, weight and rstd of the forward
  *   ds = rstd (dy weight - s rstd mean(dy weight s rstd)) + dsum,  [rows, cols] of dtype,
  *        contiguous: the gradient of x and of residual; dsum (may be NULL) is what comes
- *        in for s itself; ds may be dy or dsum itself where that is contiguous;
+ *        in for s itself; ds may be dy, s or dsum itself where that is contiguous;
  *   dw = sum over the rows of dy s rstd, [cols] of w_dtype, summed in fp32 in an order that
  *        only the sizes decide.
  * Either may be NULL.  workspace: tj2_rms_norm_bwd_workspace_size(rows, cols) bytes,
@@ -828,7 +829,8 @@ size_t tj2_gated_ffn_saved_size(int64_t T, int64_t F);
  * where fp32 gradients are asked for.  The results do not depend on scheduling.
  * workspace: tj2_gated_ffn_bwd_workspace_size(T, D, F) bytes, 16-byte aligned, required,
  * the same whichever gradients are asked for: dG and dU twice and H (10 T F bytes), copies
- * of X, dY and the weights, and partial sums.
+ * of X, dY and the weights, and partial sums.  The results overlap neither one another nor
+ * an input.
  */
 tj2_status tj2_gated_ffn_bwd(const void* dY, int64_t ldy, const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw,
                              const void* Wd, int64_t ldd, int64_t T, int64_t D, int64_t F, int32_t act, const void* gu, void* dX,

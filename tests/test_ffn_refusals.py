@@ -46,3 +46,12 @@ def test_binding():
     for f in (tj2.gated_ffn, tj2.gated_ffn_fwd):
         with pytest.raises(ValueError):
             f(x, w, w, w.t().contiguous())
+
+
+def test_gradients_are_apart(lib):
+    L, need = lib.lib(), lib.lib().tj2_gated_ffn_bwd_workspace_size(5, 64, 64)
+
+    def bwd(dX=0x7000, dWg=0x8000, dWu=0x9000, dWd=0xA000):
+        return L.tj2_gated_ffn_bwd(0x1000, 64, 0x1000, 64, 0x2000, 0x3000, 64, 0x4000, 64, 5, 64, 64, 0, 0x6000, dX, lib.F32, dWg, dWu, dWd,
+                                   lib.F32, 0x10000, need, None)
+    assert bwd(dWu=0x8000) == bwd(dWd=0x8000) == bwd(dWd=0x9000) == bwd(dX=0x8000) == bwd(dX=0xA000) == lib.TJ2_ERR_ARG

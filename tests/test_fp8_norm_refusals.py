@@ -134,3 +134,21 @@ def test_binding():
         tj2.QTensor(tj2.FP8_BLOCK, 4, 40)
     with pytest.raises(ValueError):
         tj2.QTensor.packed(tj2.NVFP4, 4, 32)
+
+
+def test_results_in_an_inputs_place(lib):
+    """A dense result over an input of another pitch, or over another result, is refused."""
+    L, ARG = lib.lib(), lib.TJ2_ERR_ARG
+
+    def fwd(x=0x1000, ldx=64, res=0x6000, ldr=64, s=0x7000, y=0x4000):
+        return L.tj2_rms_norm_fwd(x, ldx, res, ldr, lib.BF16, 3, 64, 0x2000, lib.F32, ctypes.c_float(1e-6), s, y, None, 0x5000, None)
+    assert fwd(s=0x1000, ldx=72) == ARG and fwd(s=0x6000, ldr=72) == ARG and fwd(y=0x7000) == ARG
+    assert fwd(y=0x1000, ldx=72) == ARG and fwd(y=0x6000, ldr=72) == ARG
+    assert fwd(res=None, s=None, y=0x1000, ldx=72) == ARG
+    need = L.tj2_rms_norm_bwd_workspace_size(3, 64)
+
+    def bwd(dy=0x1000, lddy=64, s=0x2000, lds=64, dsum=0x8000, ldd=64, ds=0x5000):
+        return L.tj2_rms_norm_bwd(dy, lddy, s, lds, lib.F32, 3, 64, 0x3000, lib.F32, 0x4000, dsum, ldd, ds, 0x6000, 0x10000, need, None)
+    assert bwd(ds=0x1000, lddy=72) == ARG and bwd(ds=0x2000, lds=72) == ARG and bwd(ds=0x8000, ldd=72) == ARG
+    Xq, Wq, need = q(lib, lib.FP8, 3, 64), q(lib, lib.FP8_BLOCK, 48, 64), L.fp8_linear_bwd_workspace_size(3, 48, 64)
+    assert L.fp8_linear_bwd(0x1000, 3, 48, 64, ctypes.byref(Xq), ctypes.byref(Wq), 0x2000, lib.BF16, 0x2000, 0x10000, need, None) == ARG

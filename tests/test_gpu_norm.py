@@ -245,3 +245,46 @@ def test_streams_graphs_and_order():
         torch.cuda.synchronize()
         assert torch.equal(outs["y"], y) and torch.equal(gs, ds * k) and torch.equal(gw, dw * k)
         tj2.rms_norm_bwd(dy, s, w, rstd)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [1000, 1003, 9000, 9001])
+def test_gradient_over_its_inputs(cols, dtype):
+    """ds in dy's, s' or dsum's place: both gradients are what they are apart."""
+    T = DT[dtype]
+    dy, s, dsum = (normal((130, cols), i, 1.0, T) for i in (1, 2, 3))
+    w = 1.0 + normal(cols, 4, 0.1)
+    rstd = tj2.rms_norm_fwd(s, w)[2]
+    want = tj2.rms_norm_bwd(dy, s, w, rstd, dsum=dsum)
+    for i in range(3):
+        a = [dy.clone(), s.clone(), dsum.clone()]
+        ds, dw = tj2.rms_norm_bwd(a[0], a[1], w, rstd, dsum=a[2], ds=a[i])
+        assert ds is a[i] and torch.equal(ds, want[0]) and torch.equal(dw, want[1])
+
+
+@pytest.mark.parametrize("cols", [*range(1, 26), 63, 127, 129, 255, 505, 520, 1017, 1031, 2041, 2047, 4095, 4097, 8185, 8191])
+def test_lengths_about_the_vectors(cols):
+    """Rows that end within a vector, at every place of one, between others' rows that are not to be read or written."""
+    for T in (torch.bfloat16, torch.float32):
+        X = torch.full((5, cols + 16), float("nan"), device="cuda", dtype=T)
+        X[:, 8:8 + cols] = normal((5, cols), 1, 1.0, T)
+        x, w = X[:, 8:8 + cols], (1.0 + normal(cols, 2, 0.1)).to(T)
+        out = torch.full((7, cols), 5.0, device="cuda", dtype=T)
+        y, _, rstd = tj2.rms_norm_fwd(x, w, y=out[1:6])
+        ry, rs, rr = plain(x, w, None)
+        e = stat(cols)
+        assert ((rstd.double() - rr).abs() <= e * rr).all()
+        assert ((y.double() - ry).abs() <= (HALF[T] + e + 4 * H24) * ry.abs() * 1.001).all()
+        assert (out[0] == 5.0).all() and (out[6] == 5.0).all()
+        dy = normal((5, cols), 3, 1.0, T)
+        out.fill_(5.0)
+        ds, dw = tj2.rms_norm_bwd(dy, x, w, rstd, ds=out[1:6])
+        assert (out[0] == 5.0).all() and (out[6] == 5.0).all()
+        xr = x.double() * rstd.double()[:, None]
+        g = dy.double() * w.double()
+        full = rstd.double()[:, None] * (g - xr * (g * xr).mean(1, keepdim=True))
+        # the terms that cancel count: r |g| and r |x r| mean |g x r|, each step half of one, the mean a sum as rstd's
+        top = rstd.double()[:, None] * (g.abs() + xr.abs() * (g * xr).abs().mean(1, keepdim=True))
+        assert ((ds.double() - full).abs() <= HALF[T] * full.abs() * 1.001 + (e + 8 * H24) * top).all()
+        rw, tw = (dy.double() * xr).sum(0), (dy.double() * xr).abs().sum(0)
+        assert ((dw.double() - rw).abs() <= HALF[T] * rw.abs() * 1.001 + 16 * H24 * tw).all()
