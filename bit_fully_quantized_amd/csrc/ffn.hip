@@ -38,7 +38,7 @@ __device__ __forceinline__ Act activate(float g) {
     // function that varies slowly, t times a polynomial of degree 7 in t = 1 / (1 + 0.43 |g| /
     // sqrt 2): a fit to 1e-7 of itself, 7e-7 in fp32 for |g| < 4 (the library's erfc took most
     // of these kernels' time: 1235 x 528, 1552 features, backward kernel 25.0 us, and
-    // @@ERF).  From |g| = 14 on the exponential is 0 and the arguments are kept finite.
+    // 20.0 so).  From |g| = 14 on the exponential is 0 and the arguments are kept finite.
     const float c = __builtin_amdgcn_fmed3f(g, -14.0f, 14.0f), t = __builtin_amdgcn_rcpf(fmaf(0.304055929f, fabsf(c), 1.0f));
     const float e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * c * c);
     float q = 0.0368549079f;
@@ -323,7 +323,7 @@ struct DhArgs {
 
 template <class T, int ACT>
 __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_dh_kernel(DhArgs p) {
-  static_assert(T::kTN == 4 && T::PB == 4, "64 tokens, and features 16 a lane");
+  static_assert(T::kTN == 4 && (T::PB == 2 || T::PB == 4), "64 tokens, and features 8 or 16 a lane");
   __shared__ __attribute__((aligned(128))) typename T::Smem sm;
   const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, 1);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g = lane >> 4;
@@ -332,12 +332,12 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_dh_kernel(DhArgs p) {
     const int ct = (int)(qw >> 6);
     static_assert(16 * T::kTM <= 128 && 128 % (16 * T::kTM) == 0, "a wave's features are of one block");
 #pragma unroll
-    for (int tb = 0; tb < T::kTM / 4; ++tb) {
-      const int64_t f = pw + tb * 64 + g * 16;  // this lane's 16 features
+    for (int tb = 0; tb < T::kTM / T::PB; ++tb) {
+      const int64_t f = pw + tb * 16 * T::PB + g * 4 * T::PB;  // this lane's 4 PB features
       const bool in = f < F;
       const int64_t turned = ((pw >> 7) * p.nt + ct) * 8192 + (f & 127) * 64 + n * 4;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int half = 0; half < T::PB / 2; ++half) {
         uint4 gv[4], uv[4];
         uint2 gl[4], ul[4];
 #pragma unroll
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_dh_kernel(DhArgs p) {
         }
         static_for<2>([&](auto jc) __attribute__((always_inline)) {
           constexpr int j = decltype(jc)::value;
-          const int tm = tb * 4 + half * 2 + j;
+          const int tm = tb * T::PB + half * 2 + j;
           float dg[4][4], du[4][4], h[4][4];  // [token][feature]
 #pragma unroll
           for (int tn = 0; tn < 4; ++tn) {
@@ -385,17 +385,17 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_dh_kernel(DhArgs p) {
           }
         });
       }
-      // as they are: 16 neighbouring features of a token
-      const int cd = (int)((pw + tb * 64) >> 6);
+      // as they are: 8 or 16 neighbouring features of a token
+      const int cd = (int)(f >> 6);
       if (!p.d || cd >= p.nf) continue;
 #pragma unroll
       for (int tn = 0; tn < 4; ++tn) {
         const int64_t t = t0 + tn;
         if (t >= p.Q.rows) continue;
-        uint16_t* o = p.d + ((t >> 7) * 2 * p.nf + cd) * 8192 + (t & 127) * 64 + g * 16;
+        uint16_t* o = p.d + ((t >> 7) * 2 * p.nf + cd) * 8192 + (t & 127) * 64 + (f & 63);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float4_t a = acc[tb * 4 + half * 2][tn], b = acc[tb * 4 + half * 2 + 1][tn];
+        for (int half = 0; half < T::PB / 2; ++half) {
+          const float4_t a = acc[tb * T::PB + half * 2][tn], b = acc[tb * T::PB + half * 2 + 1][tn];
           *reinterpret_cast<uint4*>(o + half * 8) = uint4{__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y)};
           *reinterpret_cast<uint4*>(o + (int64_t)p.nf * 8192 + half * 8) =
               uint4{__float_as_uint(a.z), __float_as_uint(a.w), __float_as_uint(b.z), __float_as_uint(b.w)};
@@ -433,27 +433,27 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_product_kernel(FfnProduct
   const typename T::Items items(p.tiles_p, p.tiles_q, (uint32_t)p.nch, (uint32_t)p.splits, blockIdx.x - jobs.first[job], end - jobs.first[job]);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
   T::run(p.P, p.Q, items, sm, [&](int64_t p0, int64_t q0, uint32_t z, typename T::Acc& acc) __attribute__((always_inline)) {
-    const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * 16, qw = q0 + (w % T::kWN) * T::kTN * 16;
-    static_assert(T::PB == 4, "rows of P 16 a lane");
+    constexpr int N = 4 * T::PB;  // neighbouring results of a lane
+    const int64_t pw = p0 + (w / T::kWN) * T::kTM * 16 + g * N, qw = q0 + (w % T::kWN) * T::kTN * 16;
 #pragma unroll
     for (int tn = 0; tn < T::kTN; ++tn) {
       const int64_t i = qw + T::q_row(tn, n);
       if (i >= p.Q.rows) continue;
 #pragma unroll
-      for (int tb = 0; tb < T::kTM / 4; ++tb) {
-        const int64_t j = pw + tb * 64;
+      for (int tb = 0; tb < T::kTM / T::PB; ++tb) {
+        const int64_t j = pw + tb * 4 * N;
         if (j >= p.P.rows) continue;  // (a multiple of 16)
         if (p.splits == 1 && p.bf16) {
-          float v[16];
+          float v[N];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = acc[tb * 4 + k / 4][tn][k % 4];
+          for (int k = 0; k < N; ++k) v[k] = acc[tb * T::PB + k / 4][tn][k % 4];
           uint16_t* o = reinterpret_cast<uint16_t*>(p.out) + i * p.P.rows + j;
-          *reinterpret_cast<uint4*>(o) = pack8(v);
-          *reinterpret_cast<uint4*>(o + 8) = pack8(v + 8);
+#pragma unroll
+          for (int k = 0; k < N; k += 8) *reinterpret_cast<uint4*>(o + k) = pack8(v + k);
         } else {
           float* o = p.splits == 1 ? reinterpret_cast<float*>(p.out) : p.part + (size_t)z * (size_t)(p.Q.rows * p.P.rows);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) *reinterpret_cast<float4_t*>(o + i * p.P.rows + j + 4 * k) = acc[tb * 4 + k][tn];
+          for (int k = 0; k < T::PB; ++k) *reinterpret_cast<float4_t*>(o + i * p.P.rows + j + 4 * k) = acc[tb * T::PB + k][tn];
         }
       }
     }
@@ -491,8 +491,10 @@ __global__ __launch_bounds__(256) void ffn_blocks_kernel(FfnBlocks jobs) {
 
 using TileBig = Tile<EL_BF16, 2, 4, 8, 4>;   // 256 x 256
 using TileMid = Tile<EL_BF16, 2, 2, 4, 4>;   // 128 x 128
+using TileLow = Tile<EL_BF16, 2, 2, 2, 4>;   // 64 x 128
 using PairBig = Tile<EL_PAIR, 2, 4, 8, 4>;   // 128 of either weight x 256
 using PairMid = Tile<EL_PAIR, 2, 2, 4, 4>;   // 64 of either weight x 128
+using PairLow = Tile<EL_PAIR, 2, 2, 4, 2>;   // 64 of either weight x 64
 
 template <class T, class A>
 uint32_t set_tiles(A& a) {
@@ -523,11 +525,15 @@ static_assert(16 * few_pitch(2048) <= 80 * 1024 && 32 * few_pitch(512) <= 80 * 1
 // time, the items (tiles times splits) being dealt out to the CUs' places, the longest
 // first, as they become free.  Measured (us on MI355X, operands in blocks, a chunk 64
 // elements): a tile of 256 x 256 1.6 a chunk, one of 128 x 128 0.67 alone on its CU and
-// 0.97 beside another; partial sums at 5 TB/s each way and a launch.  (Backward products of
+// 0.97 beside another, one of 64 x 128 0.5 and, of three, 0.95; partial sums at 5 TB/s each
+// way and a launch.  (With the last kind and without: forward of 1235 x 528, 1552 features
+// 28.8 and 30.8 us, of 2048 x 1024, 2048 features 48.1 and 51.5, backward of 2048 x 512, 2048
+// features 58.5 and 62.1.)  (Backward products of
 // 16384 x 1024, 4096 features: 677 us with two splits for each of the weights' gradients
 // and none for dX, whose 2.5 rounds of equal items take three; 544 as planned here.)
+enum class Tiles { Big, Mid, Low };
 struct FfnPlan {
-  bool big;
+  Tiles tiles;
   int splits[kJobs];
 };
 struct FfnSize {
@@ -570,30 +576,36 @@ double deal(double places, const double* count, const double* t, int n) {
 }
 
 double plan_time(const FfnPlan& plan, const FfnSize* x, int n) {
+  // P's and Q's rows of a tile, tiles of a CU, us a chunk alone and with the CU full, us for start and results
+  struct {
+    int64_t p, q, per_cu;
+    double alone, full, fixed;
+  } const c = plan.tiles == Tiles::Big ? decltype(c){256, 256, 1, 1.6, 1.6, 5.0}
+            : plan.tiles == Tiles::Mid ? decltype(c){128, 128, 2, 0.67, 0.97, 3.0} : decltype(c){64, 128, 3, 0.5, 0.95, 3.0};
   double count[kJobs], t[kJobs], items = 0.0, join = 0.0;
   for (int i = 0; i < n; ++i) {
     const int64_t nch = (x[i].k + 63) / 64;
-    count[i] = (double)tiles_of(x[i].p, x[i].q, plan.big ? 256 : 128) * plan.splits[i];
+    count[i] = (double)((x[i].p + c.p - 1) / c.p * ((x[i].q + c.q - 1) / c.q)) * plan.splits[i];
     t[i] = (double)((nch + plan.splits[i] - 1) / plan.splits[i]);
     items += count[i];
     if (plan.splits[i] > 1) join += (double)x[i].p * (double)x[i].q * 8.0 * plan.splits[i] / 5e6;
   }
-  const bool alone = !plan.big && items <= kCus;
-  for (int i = 0; i < n; ++i) t[i] = t[i] * (plan.big ? 1.6 : alone ? 0.67 : 0.97) + (plan.big ? 5.0 : 3.0);
+  const bool alone = items <= kCus;
+  for (int i = 0; i < n; ++i) t[i] = t[i] * (alone ? c.alone : c.full) + c.fixed;
   for (int i = 1; i < n; ++i)  // the longest first
     for (int k = i; k > 0 && t[k] > t[k - 1]; --k) {
       std::swap(t[k], t[k - 1]);
       std::swap(count[k], count[k - 1]);
     }
-  return deal(plan.big || alone ? kCus : 2 * kCus, count, t, n) + (join > 0.0 ? join + 3.0 : 0.0);
+  return deal((double)(alone ? 1 : c.per_cu) * kCus, count, t, n) + (join > 0.0 ? join + 3.0 : 0.0);
 }
 
 FfnPlan find_plan(const FfnSize* x, int n) {
   FfnPlan best = {};
   double least = 1e30;
-  for (int big = 0; big < 2; ++big) {
+  for (const Tiles tiles : {Tiles::Mid, Tiles::Big, Tiles::Low}) {
     FfnPlan c = {};
-    c.big = big;
+    c.tiles = tiles;
     // every choice for each product, equal ones (the gates' and factors' weights) alike
     auto choose = [&](auto&& self, int i) -> void {
       if (i == n) {
@@ -685,7 +697,8 @@ hipError_t run_products(FfnProduct* x, const FfnSize* size, int n, float* part, 
   }
   for (int i = 0; i < n; ++i) jobs.x[i] = x[order[i]];
   jobs.n = n;
-  if (plan.big) launch_products<TileBig>(jobs, s);
+  if (plan.tiles == Tiles::Big) launch_products<TileBig>(jobs, s);
+  else if (plan.tiles == Tiles::Low) launch_products<TileLow>(jobs, s);
   else launch_products<TileMid>(jobs, s);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   uint32_t grid = 0;
@@ -722,7 +735,7 @@ Saved saved_of(const FfnParams& f) {
   return Saved{hi, hi + n, lo, lo + n, up(f.F, 64) / 64};
 }
 
-// Of a product with an epilogue: 256 x 256 tiles or 128 x 128.
+// Of a product with an epilogue: 256 x 256 tiles or smaller ones.
 bool big_tiles(int64_t p, int64_t q, int64_t k) {
   const double chunks = (double)((k + 63) / 64);
   return tile_time(true, tiles_of(p, q, 256), chunks, 9.0) < tile_time(false, tiles_of(p, q, 128), chunks, 9.0);
@@ -838,14 +851,19 @@ hipError_t launch_ffn_fwd(const FfnParams& f, void* ws, hipStream_t s) {
   a.nf = (int32_t)(up(f.F, 64) / 64);
   a.h = h;
   a.s = saved_of(f);
+  // Low where the middle tiles would leave CUs idle or few with two (forward, us, middle and
+  // low: 64 x 512, 2048 features 18.1 and 16.0 (16 middle tiles), 300 x 1024, 4096 33.4 and 32.1
+  // (192), 600 x 1024, 4096 41.9 and 40.8 (320), 2048 x 512, 2048 41.4 and 42.6 (512)).
   const bool big = big_tiles(2 * f.F, f.T, f.D);
   with_activation(f.act, [&](auto act) {
     if (big) {
       const uint32_t items = set_tiles<PairBig>(a);
       ffn_gate_kernel<PairBig, act.value><<<PairBig::grid(items), PairBig::NT, 0, s>>>(a);
-    } else {
-      const uint32_t items = set_tiles<PairMid>(a);
+    } else if (const uint32_t items = set_tiles<PairMid>(a); items > kCus * 5 / 4) {
       ffn_gate_kernel<PairMid, act.value><<<PairMid::grid(items), PairMid::NT, 0, s>>>(a);
+    } else {
+      const uint32_t few = set_tiles<PairLow>(a);
+      ffn_gate_kernel<PairLow, act.value><<<PairLow::grid(few), PairLow::NT, 0, s>>>(a);
     }
   });
   TJ2_DO(hipGetLastError());
@@ -888,14 +906,17 @@ hipError_t launch_ffn_bwd(const FfnParams& f, const FfnGradParams& o, void* ws, 
   a.gt = dw ? reinterpret_cast<uint16_t*>(w + sp.gt) : nullptr;
   a.ut = reinterpret_cast<uint16_t*>(w + sp.ut);
   a.ht = o.dWd ? reinterpret_cast<uint16_t*>(w + sp.ht) : nullptr;
+  // Tiles of 64 features where big ones do not pay: the epilogue is long, and three of them
+  // on a CU cover it in part (backward, us, with 128 x 128 and with 64 x 128: 1235 x 528, 1552
+  // features 53.5 and 49.2, 2048 x 1024, 2048 87.6 and 84.3, 8192 x 256, 1024 72.5 and 72.6).
   const bool big = big_tiles(f.F, f.T, f.D);
   with_activation(f.act, [&](auto act) {
     if (big) {
       const uint32_t items = set_tiles<TileBig>(a);
       ffn_dh_kernel<TileBig, act.value><<<TileBig::grid(items), TileBig::NT, 0, s>>>(a);
     } else {
-      const uint32_t items = set_tiles<TileMid>(a);
-      ffn_dh_kernel<TileMid, act.value><<<TileMid::grid(items), TileMid::NT, 0, s>>>(a);
+      const uint32_t items = set_tiles<TileLow>(a);
+      ffn_dh_kernel<TileLow, act.value><<<TileLow::grid(items), TileLow::NT, 0, s>>>(a);
     }
   });
   TJ2_DO(hipGetLastError());
