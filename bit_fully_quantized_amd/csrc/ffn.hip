@@ -17,6 +17,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "tj2_bf16.h"
 
@@ -168,12 +169,16 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_gate_kernel(GateArgs p) {
 // us (16.8 MB, 3.0 TB/s).
 // The same for up to 32 tokens: one read of the weights, 8 rows of each a wave (lane n
 // holds a gate's row where n & 2 is 0), so that a lane's four results are two gates and
-// their factors.  H is row-major.
+// their factors.  H is row-major; of up to 8 tokens in two bf16 parts (8 bits, and the next of
+// what these leave), since their results have few of H's roundings to average over and the
+// second part takes places of the output product's instruction that are idle (a second
+// instruction for 9 to 32 tokens would cost 2 to 7 us of 11 to 45).
+constexpr int kTwoParts = 8;
 struct GateFewArgs {
   const uint16_t *x, *wg, *wu;
   int64_t ldx, ldw;
   int32_t T, D, F;
-  uint16_t* h;
+  uint16_t* h;  // [1 or 2][T][F]
   Saved s;
 };
 // LDS bytes of a token: whole chunks and 16 bytes, so that 16 tokens' pieces lie in different banks
@@ -242,7 +247,13 @@ __global__ __launch_bounds__(256, 2) void ffn_gate_few_kernel(GateFewArgs p) {
         const int t = tn * 16 + n;
         if (t < p.T) {
           const float4_t v = acc[tn];
-          *reinterpret_cast<uint32_t*>(p.h + (int64_t)t * p.F + f) = bf16_pair(activate<ACT>(v.x).a * v.z, activate<ACT>(v.y).a * v.w);
+          const float h0 = activate<ACT>(v.x).a * v.z, h1 = activate<ACT>(v.y).a * v.w;
+          const uint32_t hi = bf16_pair(h0, h1);
+          uint16_t* o = p.h + (int64_t)t * p.F + f;
+          *reinterpret_cast<uint32_t*>(o) = hi;
+          const float r0 = h0 - __uint_as_float(hi << 16), r1 = h1 - __uint_as_float(hi & 0xFFFF0000u);
+          // (of an infinity nothing is left)
+          if (p.T <= kTwoParts) *reinterpret_cast<uint32_t*>(o + (int64_t)p.T * p.F) = bf16_pair(fabsf(r0) <= FLT_MAX ? r0 : 0.0f, fabsf(r1) <= FLT_MAX ? r1 : 0.0f);
           if (p.s.g) {
             const int64_t at = p.s.at(t, f);
             const float gv[2] = {v.x, v.y}, uv[2] = {v.z, v.w};
@@ -263,7 +274,7 @@ __global__ __launch_bounds__(256, 2) void ffn_gate_few_kernel(GateFewArgs p) {
 
 // Y = H Wd^T of up to 32 tokens: a workgroup takes 4 to 16 rows of Wd (fewer than the
 // instruction's 16 so that more CUs read: 1 token of D 1024, F
-// 4096 14.0 us with both kernels' waves on 64 to 128 CUs, 9.7 on all), its 16 waves the
+// 4096 14.0 us with both kernels' waves on 64 to 128 CUs, 9.9 on all), its 16 waves the
 // reduction in turn, joined in LDS.
 struct DownFewArgs {
   const uint16_t *h, *wd;
@@ -279,6 +290,12 @@ __global__ __launch_bounds__(1024) void ffn_down_few_kernel(DownFewArgs p) {
   const int d0 = blockIdx.x * p.rows, steps = (p.F + 31) / 32;
   const int s0 = steps * wave / 16, s1 = steps * (wave + 1) / 16;
   const uint16_t* w = p.wd + (int64_t)(d0 + n) * p.ldw + g * 8;  // (D is a multiple of 16)
+  // this lane's rows of H: tokens, and behind them from lane 8 on their second parts
+  const bool two = p.T <= kTwoParts;
+  const int rows = two ? 2 * p.T : p.T;
+  int row[TN];
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn) row[tn] = !two ? tn * 16 + n : n % 8 < p.T && tn == 0 ? n / 8 * p.T + n % 8 : rows;
   float4_t acc[TN] = {};
   constexpr int U = 4;
   for (int s = s0; s < s1; s += U) {
@@ -292,7 +309,7 @@ __global__ __launch_bounds__(1024) void ffn_down_few_kernel(DownFewArgs p) {
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn) {
         b[u][tn] = i32x4_t{0, 0, 0, 0};
-        if (in && tn * 16 + n < p.T) b[u][tn] = *reinterpret_cast<const i32x4_t*>(p.h + (int64_t)(tn * 16 + n) * p.F + k + g * 8);
+        if (in && row[tn] < rows) b[u][tn] = *reinterpret_cast<const i32x4_t*>(p.h + (int64_t)row[tn] * p.F + k + g * 8);
       }
     }
 #pragma unroll
@@ -311,6 +328,10 @@ __global__ __launch_bounds__(1024) void ffn_down_few_kernel(DownFewArgs p) {
     float v = sh[0][t][d];
 #pragma unroll
     for (int k = 1; k < 16; ++k) v += sh[k][t][d];
+    if (two && t < 8) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v += sh[k][t + 8][d];
+    }
     if (t >= p.T || d >= p.rows) continue;
     const int64_t at = (int64_t)t * p.D + d0 + d;
     if (p.bf16) reinterpret_cast<uint16_t*>(p.y)[at] = (uint16_t)bf16_pair(v, 0.0f);
@@ -528,7 +549,7 @@ void with_activation(int act, F&& f) {
 }
 
 // Tiles of 16 tokens of the few-token kernels, 0: none.  Forward here and in tiles, us:
-// D 1024, F 4096: 1 token 9.7 and 20.5, 16 tokens 15.5 and 22.5 (32 24 and 23.5); D 2048, F
+// D 1024, F 4096: 1 token 9.9 and 20.5, 16 tokens 15.5 and 22.5 (32 24 and 23.5); D 2048, F
 // 8192: 1 token 23.1 and 38.2, 16 tokens 38.2 and 40.6; D 512, F 2048: 17 tokens 10.9 and
 // 17.2, 32 tokens 13.6 and 17.1; D 512, F 8192: 16 tokens 18.9 and 19.6, 17 tokens 22.2 and
 // 19.5.
@@ -768,7 +789,7 @@ struct FfnFwdSpace {
     auto take = [&](size_t n) { const size_t a = at; at += up256(n); return a; };
     few = few_tiles(T, D, F);
     blocked = T >= kBlockTokens;
-    h = take(few ? (size_t)(T * F * 2) : blocked_bytes(T, F));
+    h = take(few ? (size_t)(T * F * (T <= kTwoParts ? 4 : 2)) : blocked_bytes(T, F));
     x = take(blocked ? blocked_bytes(T, D) : 0);
     g = take(blocked ? blocked_bytes(F, D) : 0);
     u = take(blocked ? blocked_bytes(F, D) : 0);

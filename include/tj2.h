@@ -805,7 +805,8 @@ size_t tj2_rms_norm_bwd_workspace_size(int64_t rows, int64_t cols);
  *   G = X Wg^T, U = X Wu^T, H = act(G) * U, Y = H Wd^T,
  * X [T, D], Wg and Wu [F, D], Wd [D, F], with rows ldx, ldw (both), ldd elements apart
  * (multiples of 8; 16-byte aligned).  D and F multiples of 16; T, D, F and the pitches at
- * most 2^21, T * F at most 2^36.  Sums and the activation are fp32; H is rounded to bf16 for its product.
+ * most 2^21, T * F at most 2^36.  Sums and the activation are fp32; H is rounded to bf16 for
+ * its product (of up to 8 tokens and D up to 2048 to 16 bits of mantissa).
  *
  * tj2_gated_ffn_fwd: Y [T, D], contiguous, TJ2_BF16 or TJ2_F32; gu (may be NULL):
  * tj2_gated_ffn_saved_size(T, F) bytes (6 of each feature of a token, rounded up to 64 x 64
