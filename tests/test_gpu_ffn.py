@@ -274,3 +274,36 @@ def test_streams_graphs_and_shared_workspaces():
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(want[i % 2], outs)), i
         tj2.gated_ffn_fwd(xs[1], Wg, Wu, Wd)
+
+
+@pytest.mark.parametrize("T", range(1, 10))
+@pytest.mark.parametrize("D,F", [(16, 16), (112, 336), (1024, 528)])
+def test_up_to_eight_tokens_keep_both_parts_of_h(T, D, F):
+    """H in two bf16 parts: what the first leaves is at most 2^-8 of H and rounded by 2^-8 of itself."""
+    X, Wg, Wu, Wd = make(T, D, F)
+    x, g, u, d = (t.double() for t in (X, Wg, Wu, Wd))
+    G, U = x @ g.T, x @ u.T
+    eG, eU = (D + 8) * H24 * (x.abs() @ g.abs().T), (D + 8) * H24 * (x.abs() @ u.abs().T)
+    a = act64("silu", G)[0]
+    ea = 1.2 * eG + 2.0 ** -20 * (a.abs() + G.abs())
+    H = a * U
+    eH = ea * U.abs() + a.abs() * eU + ea * eU + 2.0 ** -20 * H.abs()
+    eH = eH + (2.0 ** -16 if T <= 8 else H8) * (H.abs() + eH)
+    bound = (eH @ d.abs().T + (2 * F + 16) * H24 * (H.abs() @ d.abs().T)) * 1.01
+    Y = tj2.gated_ffn_fwd(X, Wg, Wu, Wd, y_dtype=torch.float32)[0].double()
+    assert ((Y - H @ d.T).abs() <= bound).all()
+    alone = torch.cat([tj2.gated_ffn_fwd(X[t:t + 1], Wg, Wu, Wd, y_dtype=torch.float32)[0] for t in range(T)]).double()
+    assert ((alone - H @ d.T).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 40])
+def test_products_that_leave_the_range(T):
+    """H beyond fp32 is infinite and so is Y (not a difference of infinities), for its own token."""
+    X = torch.zeros(T, 32, device="cuda", dtype=BF)
+    X[T - 1, :4] = 2.0 ** 60
+    X[0, 4:8] = 1.0
+    W = torch.full((48, 32), 2.0 ** 10, device="cuda", dtype=BF)
+    Y = tj2.gated_ffn_fwd(X, W, W, torch.full((32, 48), 0.5, device="cuda", dtype=BF))[0]
+    assert (Y[T - 1] == float("inf")).all() and torch.isfinite(Y[: T - 1]).all()
+    # 24 2^24 of 48 features: exact
+    assert T == 1 or (Y[0] == 24.0 * 2.0 ** 24).all()
