@@ -562,14 +562,15 @@ static_assert(16 * few_pitch(2048) <= 80 * 1024 && 32 * few_pitch(512) <= 80 * 1
 
 // Tile and splits of up to four products that run together: those of the least estimated
 // time, the items (tiles times splits) being dealt out to the CUs' places, the longest
-// first, as they become free.  Measured (us on MI355X, operands in blocks, a chunk 64
-// elements): a tile of 256 x 256 1.6 a chunk, one of 128 x 128 0.67 alone on its CU and
-// 0.97 beside another, one of 64 x 128 0.5 and, of three, 0.95; partial sums at 5 TB/s each
-// way and a launch.  (With the last kind and without: forward of 1235 x 528, 1552 features
-// 28.8 and 30.8 us, of 2048 x 1024, 2048 features 48.1 and 51.5, backward of 2048 x 512, 2048
-// features 58.5 and 62.1.)  (Backward products of
-// 16384 x 1024, 4096 features: 677 us with two splits for each of the weights' gradients
-// and none for dX, whose 2.5 rounds of equal items take three; 544 as planned here.)
+// first, as they become free.  What tiles and partial sums take (us on MI355X, operands in
+// blocks, a chunk 64 elements) is of two kinds.  Several products: as timed, partial sums
+// at 5 TB/s each way and a launch.  (Backward products of 16384 x 1024, 4096 features: 677 us
+// with two splits for each of the weights' gradients and none for dX, whose 2.5 rounds of
+// equal items take three; 544 as planned here.)  One product: fitted to 600 forward passes
+// of 28 sizes under all tiles and splits, of which it picks one within 0.5% of the best in
+// the mean (with the first kind's numbers 3.6%; those of the second cost backward passes
+// 1.3%): 300 x 1024, 4096 features 30.8 -> 29.0 us, 600 40.0 -> 37.6, 64 x 2048, 8192 41.7 ->
+// 38.7.  The tiles of 64 against none: backward of 2048 x 512, 2048 features 62.1 and 58.5.
 enum class Tiles { Big, Mid, Low };
 struct FfnPlan {
   Tiles tiles;
@@ -614,29 +615,36 @@ double deal(double places, const double* count, const double* t, int n) {
   return last;
 }
 
+// What a tile takes: P's and Q's rows, tiles of a CU, us a chunk alone on its CU and with
+// the CU full, us for start and results.
+struct TileCost {
+  int64_t p, q, per_cu;
+  double alone, full, fixed;
+};
+// of one product, and of several in a launch, by Tiles
+constexpr TileCost kOne[3] = {{256, 256, 1, 0.75, 0.75, 4.5}, {128, 128, 2, 0.56, 0.73, 1.1}, {64, 128, 3, 0.44, 0.52, 0.0}},
+                   kMany[3] = {{256, 256, 1, 1.6, 1.6, 5.0}, {128, 128, 2, 0.67, 0.97, 3.0}, {64, 128, 3, 0.5, 0.95, 3.0}};
+
 double plan_time(const FfnPlan& plan, const FfnSize* x, int n) {
-  // P's and Q's rows of a tile, tiles of a CU, us a chunk alone and with the CU full, us for start and results
-  struct {
-    int64_t p, q, per_cu;
-    double alone, full, fixed;
-  } const c = plan.tiles == Tiles::Big ? decltype(c){256, 256, 1, 1.6, 1.6, 5.0}
-            : plan.tiles == Tiles::Mid ? decltype(c){128, 128, 2, 0.67, 0.97, 3.0} : decltype(c){64, 128, 3, 0.5, 0.95, 3.0};
+  const TileCost c = (n == 1 ? kOne : kMany)[(int)plan.tiles];
   double count[kJobs], t[kJobs], items = 0.0, join = 0.0;
   for (int i = 0; i < n; ++i) {
     const int64_t nch = (x[i].k + 63) / 64;
     count[i] = (double)((x[i].p + c.p - 1) / c.p * ((x[i].q + c.q - 1) / c.q)) * plan.splits[i];
     t[i] = (double)((nch + plan.splits[i] - 1) / plan.splits[i]);
     items += count[i];
-    if (plan.splits[i] > 1) join += (double)x[i].p * (double)x[i].q * 8.0 * plan.splits[i] / 5e6;
+    if (plan.splits[i] > 1) join += (double)x[i].p * (double)x[i].q * plan.splits[i] * (n == 1 ? 2.3e-6 : 1.6e-6);
   }
-  const bool alone = items <= kCus;
-  for (int i = 0; i < n; ++i) t[i] = t[i] * (alone ? c.alone : c.full) + c.fixed;
+  double deep = std::min((double)c.per_cu, std::ceil(items / kCus));  // tiles of a CU at once
+  if (n > 1 && deep > 1.0) deep = (double)c.per_cu;
+  const double chunk = deep == 1.0 ? c.alone : c.alone + (c.full - c.alone) * (deep - 1.0) / (double)(c.per_cu - 1);
+  for (int i = 0; i < n; ++i) t[i] = t[i] * chunk + c.fixed;
   for (int i = 1; i < n; ++i)  // the longest first
     for (int k = i; k > 0 && t[k] > t[k - 1]; --k) {
       std::swap(t[k], t[k - 1]);
       std::swap(count[k], count[k - 1]);
     }
-  return deal((double)(alone ? 1 : c.per_cu) * kCus, count, t, n) + (join > 0.0 ? join + 3.0 : 0.0);
+  return deal(deep * kCus, count, t, n) + (join > 0.0 ? join + (n == 1 ? 0.8 : 3.0) : 0.0);
 }
 
 FfnPlan find_plan(const FfnSize* x, int n) {
