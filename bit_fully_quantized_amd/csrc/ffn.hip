@@ -442,7 +442,7 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_dh_kernel(DhArgs p) {
 // own; splits > 1: fp32 partial sums [z][q][p], joined by ffn_join_kernel.
 // 16384 x 1024, 4096 features: Y 121 us (1.14 PFLOP/s), the four of the backward pass 540 to
 // 600 us (687 GFLOP, 1.15 to 1.27: the clock falls under them; matrix units busy 59%).  Few
-// tiles are bound by each chunk's way from memory: 300 x 1024 over 4096, 8 splits 13.4 us,
+// tiles are bound by each chunk's way from memory: 300 x 1024 over 4096, 8 splits 12.0 us,
 // and 3.9 for their sums.
 constexpr int kJobs = 4;
 struct FfnProduct {
