@@ -29,6 +29,8 @@ constexpr float kLog2e = 1.44269504088896340736f;
 struct Act {
   float a, d;  // act(g), act'(g)
 };
+// v, or g's NaN, which a median with two numbers below drops
+__device__ __forceinline__ float or_nan(float g, float v) { return g != g ? g : v; }
 template <int ACT>
 __device__ __forceinline__ Act activate(float g) {
   if constexpr (ACT == TJ2_SILU) {
@@ -52,14 +54,14 @@ __device__ __forceinline__ Act activate(float g) {
     q = fmaf(q, t, 0.12125729f);
     q = q * t * e;
     const float p = g < 0.0f ? q : 1.0f - q;
-    return {g * p, fmaf(c * 0.39894228040143267794f, e, p)};
+    return {g * p, or_nan(g, fmaf(c * 0.39894228040143267794f, e, p))};
   } else {
     // (1 + tanh z) / 2 is the logistic function of 2 z; where it is 0 or 1, so is its
     // slope 0, and the polynomial is kept finite
     const float c = __builtin_amdgcn_fmed3f(g, -64.0f, 64.0f);
     const float k = 1.59576912160573071176f, z = k * fmaf(0.044715f * c * c, c, c);
     const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
-    return {g * p, fmaf(c * p * (1.0f - p), k * fmaf(0.134145f * c, c, 1.0f), p)};
+    return {g * p, or_nan(g, fmaf(c * p * (1.0f - p), k * fmaf(0.134145f * c, c, 1.0f), p))};
   }
 }
 

@@ -1,0 +1,30 @@
+"""Feed-forward block: what is not finite in the weights, gradients as autograd hands them over, and what is kept."""
+import pytest
+import torch
+
+from test_gpu_ffn import ACTS, BF, make, normal
+
+pytestmark = pytest.mark.gpu
+
+tj2 = pytest.importorskip("bit_fully_quantized_amd")
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("T", [1, 20, 150, 2100])
+def test_a_nan_gate_has_nan_gradients(T, act):
+    """A NaN in a row of Wg makes its feature's gates NaN: so are the slopes there, dWg's, dWu's and dWd's parts of that
+    feature, and no others."""
+    D, F, f = 144, 208, 37
+    X, Wg, Wu, Wd = make(T, D, F)
+    dY = normal((T, D), 9, 1e-2)
+    _, saved = tj2.gated_ffn_fwd(X, Wg, Wu, Wd, activation=act, save=True)
+    clean = tj2.gated_ffn_bwd(dY, X, Wg, Wu, Wd, saved, activation=act)
+    bad = Wg.clone()
+    bad[f, 11] = float("nan")
+    Y, saved = tj2.gated_ffn_fwd(X, bad, Wu, Wd, activation=act, save=True)
+    assert torch.isnan(Y.float()).all()
+    dX, dWg, dWu, dWd = tj2.gated_ffn_bwd(dY, X, bad, Wu, Wd, saved, activation=act)
+    assert torch.isnan(dX.float()).all() and torch.isnan(dWg[f].float()).all() and torch.isnan(dWu[f].float()).all()
+    assert torch.isnan(dWd[:, f].float()).all()
+    keep = torch.arange(F, device="cuda") != f
+    assert torch.equal(dWg[keep], clean[1][keep]) and torch.equal(dWu[keep], clean[2][keep]) and torch.equal(dWd[:, keep], clean[3][:, keep])
