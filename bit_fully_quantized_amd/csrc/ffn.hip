@@ -330,7 +330,9 @@ __global__ __launch_bounds__(1024) void ffn_down_few_kernel(DownFewArgs p) {
     float v = sh[0][t][d];
 #pragma unroll
     for (int k = 1; k < 16; ++k) v += sh[k][t][d];
-    if (two && t < 8) {
+    // (a sum that has left the range stays what it is: the second parts, 0 or of the other
+    // sign, would make a NaN of an infinite weight's)
+    if (two && t < 8 && fabsf(v) <= FLT_MAX) {
 #pragma unroll
       for (int k = 0; k < 16; ++k) v += sh[k][t + 8][d];
     }

@@ -28,3 +28,24 @@ def test_a_nan_gate_has_nan_gradients(T, act):
     assert torch.isnan(dWd[:, f].float()).all()
     keep = torch.arange(F, device="cuda") != f
     assert torch.equal(dWg[keep], clean[1][keep]) and torch.equal(dWu[keep], clean[2][keep]) and torch.equal(dWd[:, keep], clean[3][:, keep])
+
+
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 40])
+def test_an_infinite_weight_makes_its_results_infinite(T):
+    """Wd with an infinity: what it meets of H is neither 0 nor infinite, so Y there is an infinity of H's sign (also
+    where H is kept in two parts, the second of which may be 0 or of the other sign)."""
+    D, F = 64, 208
+    X, Wg, Wu, Wd = make(T, D, F)
+    Y = tj2.gated_ffn_fwd(X, Wg, Wu, Wd)[0]
+    g, u = X.double() @ Wg.double().T, X.double() @ Wu.double().T
+    h = g * torch.sigmoid(g) * u
+    assert (h.abs() > 1e-6).all()
+    bad = Wd.clone()
+    for d in range(0, D, 2):
+        bad[d, 3 * d + 1] = float("inf") if d % 4 else float("-inf")
+    got = tj2.gated_ffn_fwd(X, Wg, Wu, bad)[0]
+    for d in range(D):
+        if d % 2:
+            assert torch.equal(got[:, d], Y[:, d])
+        else:
+            assert (got[:, d].double() == bad[d, 3 * d + 1].double() * h[:, 3 * d + 1].sign()).all(), d
