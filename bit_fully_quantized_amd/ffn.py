@@ -115,8 +115,10 @@ class _GatedFfn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dY):
         X, Wg, Wu, Wd, gu = ctx.saved_tensors
-        return (*gated_ffn_bwd(dY.contiguous(), X, Wg, Wu, Wd, {"gu": gu}, activation=ctx.activation, need=ctx.needs_input_grad[:4]),
-                None)
+        dY = dY.contiguous()
+        if dY.data_ptr() % 16:  # a view into a longer gradient
+            dY = dY.clone()
+        return (*gated_ffn_bwd(dY, X, Wg, Wu, Wd, {"gu": gu}, activation=ctx.activation, need=ctx.needs_input_grad[:4]), None)
 
 
 def gated_ffn(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Tensor, *, activation: str = "silu") -> torch.Tensor:

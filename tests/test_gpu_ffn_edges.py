@@ -49,3 +49,17 @@ def test_an_infinite_weight_makes_its_results_infinite(T):
             assert torch.equal(got[:, d], Y[:, d])
         else:
             assert (got[:, d].double() == bad[d, 3 * d + 1].double() * h[:, 3 * d + 1].sign()).all(), d
+
+
+def test_gradients_at_any_address():
+    """A gradient that autograd hands over as a view into a longer tensor starts at any of its elements."""
+    leaves = [t.requires_grad_() for t in make(33, 48, 80)]
+    c = normal((33 * 48,), 9, 1.0, torch.float32)
+    want = torch.autograd.grad((tj2.gated_ffn(*leaves).flatten().float() * c).sum(), leaves)
+    for before in (1, 3, 8):
+        first = torch.zeros(before, dtype=BF, device="cuda")
+        y = torch.cat((first, tj2.gated_ffn(*leaves).flatten()))
+        got = torch.autograd.grad((y * torch.cat((first, c.to(BF)))).sum(), leaves)
+        again = torch.autograd.grad((tj2.gated_ffn(*leaves).flatten() * c.to(BF)).sum(), leaves)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
+        assert all(a.shape == b.shape for a, b in zip(got, want))
