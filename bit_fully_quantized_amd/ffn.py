@@ -123,4 +123,6 @@ class _GatedFfn(torch.autograd.Function):
 
 def gated_ffn(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Tensor, *, activation: str = "silu") -> torch.Tensor:
     """Differentiable gated_ffn_fwd: Y [T, D] in bf16."""
+    if not torch.is_grad_enabled():  # (what leaves ask for is not withdrawn then: the function would keep the gates)
+        return gated_ffn_fwd(X, Wg, Wu, Wd, activation=activation)[0]
     return _GatedFfn.apply(X, Wg, Wu, Wd, activation)

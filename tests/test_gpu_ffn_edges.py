@@ -63,3 +63,24 @@ def test_gradients_at_any_address():
         again = torch.autograd.grad((tj2.gated_ffn(*leaves).flatten() * c.to(BF)).sum(), leaves)
         assert all(torch.equal(a, b) for a, b in zip(got, again))
         assert all(a.shape == b.shape for a, b in zip(got, want))
+
+
+def test_gates_are_kept_for_a_backward_pass_only(monkeypatch):
+    """Where no gradients are recorded the forward writes no gates and factors, whatever the leaves ask for."""
+    from bit_fully_quantized_amd import ffn
+    kept, run = [], ffn.gated_ffn_fwd
+
+    def look(*a, **kw):
+        out = run(*a, **kw)
+        kept.append(out[1] is not None)
+        return out
+    monkeypatch.setattr(ffn, "gated_ffn_fwd", look)
+    leaves = [t.requires_grad_() for t in make(5, 48, 80)]
+    Y = tj2.gated_ffn(*leaves)
+    with torch.no_grad():
+        assert torch.equal(tj2.gated_ffn(*leaves), Y)
+    with torch.inference_mode():
+        assert torch.equal(tj2.gated_ffn(*leaves), Y)
+    assert torch.equal(tj2.gated_ffn(*(t.detach() for t in leaves)), Y)
+    assert kept == [True, False, False, False]
+    torch.autograd.grad(Y.float().sum(), leaves)
