@@ -134,8 +134,13 @@ class _NormLinearsFn(torch.autograd.Function):
         s, weight, rstd = ctx.saved_tensors
         dh = None
         for L, saved, dY in zip(ctx.lins, ctx.saved, dYs):
+            if dY is None:  # no loss uses this one
+                L.grad.zero_()
+                continue
             dX = L.backward(dY.contiguous(), saved)
-            dh = dX if dh is None else dh.add_(dX)
+            dh = dX if dh is None else dh.add_(dX)  # in bf16, as autograd adds the other kinds' gradients of h
+        if dh is None:  # s alone was used
+            return dsum, dsum if ctx.needs_input_grad[1] else None, None, None, None
         ds, dw = rms_norm_bwd(dh, s, weight, rstd, dsum=None if dsum is None else dsum.contiguous())
         return ds, ds if ctx.needs_input_grad[1] else None, dw, None, None
 
