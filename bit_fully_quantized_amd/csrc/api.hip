@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -1366,6 +1367,46 @@ tj2_status check_fp8_size(const char* name, int64_t rows, int64_t len) {
   return TJ2_OK;
 }
 
+// Memory that a call reads or writes: `rows` rows of `width` elements of `size` bytes, `pitch`
+// elements apart.
+struct Region {
+  const char* name;
+  const void* p;
+  int64_t rows, pitch, width, size;
+  bool dense() const { return rows <= 1 || pitch == width; }
+};
+Region dense(const char* name, const void* p, int64_t n, int64_t size) { return Region{name, p, 1, n, n, size}; }
+Region codes_of(const char* name, const tj2_qtensor& q) { return dense(name, q.codes, q.rows * ((q.len + 127) / 128), 128); }
+Region scales_of(const char* name, const tj2_qtensor& q) {
+  return dense(name, q.scale128, (q.fmt == TJ2_FP8_BLOCK ? (q.rows + 127) / 128 : q.rows) * ((q.len + 127) / 128), 4);
+}
+int64_t size_of(int32_t dtype) { return dtype == TJ2_BF16 ? 2 : 4; }
+// Whether a byte belongs to both; one of them at least is dense.  (128 bits: a pitch may be any number.)
+bool meet(const Region& x, const Region& y) {
+  if (!x.p || !y.p) return false;
+  using Wide = __int128;
+  const Region &d = x.dense() ? x : y, &o = x.dense() ? y : x;
+  const Wide d0 = reinterpret_cast<uintptr_t>(d.p), d1 = d0 + (Wide)d.rows * d.width * d.size, o0 = reinterpret_cast<uintptr_t>(o.p),
+             width = (Wide)o.width * o.size, pitch = (Wide)o.pitch * o.size;
+  if (o.dense()) return o0 < d1 && o0 + o.rows * width > d0;
+  const Wide row = o0 + width > d0 ? 0 : (d0 - o0 - width) / pitch + 1;  // the first that ends past d's start
+  return row < o.rows && o0 + row * pitch < d1;
+}
+// Results share no memory with one another or with what the call reads.
+tj2_status check_apart(const Region& out, std::initializer_list<Region> others) {
+  for (const Region& o : others)
+    if (meet(out, o)) return fail(TJ2_ERR_ARG, "%s must not overlap %s", out.name, o.name);
+  return TJ2_OK;
+}
+// A dense result may take an input's place where the rows are the same, and else none of it
+// (with another pitch a row's result would lie on rows that others still read).
+tj2_status check_in_place(const Region& out, std::initializer_list<Region> others) {
+  for (const Region& o : others)
+    if (meet(out, o) && !(out.p == o.p && o.dense()))
+      return fail(TJ2_ERR_ARG, "%s may be %s itself where its rows are %lld apart, and must not overlap it else", out.name, o.name, (long long)o.width);
+  return TJ2_OK;
+}
+
 // fmt: TJ2_FP8, TJ2_FP8_BLOCK or -1 for either
 tj2_status check_fp8(const tj2_qtensor* q, const char* name, int fmt, int64_t rows, int64_t len) {
   if (!q) return fail(TJ2_ERR_ARG, "%s is NULL", name);
@@ -1406,12 +1447,16 @@ tj2_status fp8_quantize(const void* x, int32_t x_dtype, const tj2_qtensor* x_q, 
   } else if (x_dtype == TJ2_FP8) {
     if (grouping != TJ2_GROUP_COL) return fail(TJ2_ERR_UNSUPPORTED, "row grouping of a quantized input is not implemented");
     TJ2_TRY(check_fp8(x_q, "x_q", TJ2_FP8, rows, cols));
-    // (the transposed groups are written while others are still read)
-    if (out->codes == x_q->codes || out->scale128 == x_q->scale128) return fail(TJ2_ERR_ARG, "out must not be x_q");
     p.xq = make_view(*x_q);
   } else {
     return fail(TJ2_ERR_ARG, "bad x_dtype %d", x_dtype);
   }
+  // (groups are written while others are still read)
+  const bool codes = x_dtype == TJ2_FP8;
+  const Region in = codes ? codes_of("x_q's codes", *x_q) : dense("x", x, rows * cols, size_of(x_dtype)),
+               in_s = codes ? scales_of("x_q's scales", *x_q) : Region{};
+  TJ2_TRY(check_apart(codes_of("out's codes", *out), {in, in_s}));
+  TJ2_TRY(check_apart(scales_of("out's scales", *out), {in, in_s}));
   p.in_dtype = x_dtype;
   p.x = x;
   p.rows = rows;
@@ -1428,6 +1473,7 @@ tj2_status fp8_dequantize(const tj2_qtensor* q, void* out, int32_t out_dtype, vo
   TJ2_TRY(check_out_dtype(out_dtype, "out_dtype"));
   if (!out) return fail(TJ2_ERR_ARG, "out is NULL");
   if (!aligned16(out)) return fail(TJ2_ERR_ALIGN, "out must be 16-byte aligned");
+  TJ2_TRY(check_apart(dense("out", out, q->rows * q->len, size_of(out_dtype)), {codes_of("q's codes", *q), scales_of("q's scales", *q)}));
   TJ2_TRY(hip_check(launch_fp8_values(make_view(*q), out, out_dtype, (hipStream_t)stream), "FP8 dequantize launch"));
   return ok();
 }
@@ -1448,6 +1494,8 @@ tj2_status fp8_gemm(const tj2_qtensor* A, const tj2_qtensor* B, void* C, int32_t
   if (accumulate && c_dtype != TJ2_F32) return fail(TJ2_ERR_UNSUPPORTED, "accumulate needs an fp32 output");
   if (ldc < B->rows) return fail(TJ2_ERR_SHAPE, "ldc < J");
   TJ2_TRY(check_mx_workspace(workspace, ws_bytes, fp8_gemm_workspace_bytes(A->rows, B->rows, A->len)));
+  TJ2_TRY(check_apart(Region{"C", C, A->rows, ldc, B->rows, size_of(c_dtype)},
+                      {codes_of("A's codes", *A), scales_of("A's scales", *A), codes_of("B's codes", *B), scales_of("B's scales", *B)}));
   TJ2_TRY(hip_check(launch_fp8_gemm(make_view(*A), make_view(*B), C, c_dtype, ldc, accumulate, reinterpret_cast<float*>(workspace),
                                     (hipStream_t)stream),
                     "FP8 gemm launch"));
@@ -1468,6 +1516,13 @@ tj2_status fp8_linear_fwd(const void* X, int64_t M, int64_t K, int64_t N, const 
   TJ2_TRY(check_out_dtype(y_dtype, "y_dtype"));
   if (!aligned16(X) || !aligned16(W_master) || !aligned16(Y)) return fail(TJ2_ERR_ALIGN, "X, W_master and Y must be 16-byte aligned");
   TJ2_TRY(check_mx_workspace(workspace, ws_bytes, fp8_linear_fwd_workspace_bytes(M, N, K)));
+  const Region x = dense("X", X, M * K, 2), w = dense("W_master", W_master, N * K, 4), xc = codes_of("Xq's codes", *Xq),
+               xs = scales_of("Xq's scales", *Xq), wc = codes_of("Wq's codes", *Wq), wss = scales_of("Wq's scales", *Wq);
+  TJ2_TRY(check_apart(dense("Y", Y, M * N, size_of(y_dtype)), {x, w, xc, xs, wc, wss}));
+  for (const Region* q : {&xc, &xs})
+    if (X) TJ2_TRY(check_apart(*q, {x, w, wc, wss}));
+  for (const Region* q : {&wc, &wss})
+    if (W_master) TJ2_TRY(check_apart(*q, {x, w, xc, xs}));
   TJ2_TRY(hip_check(launch_fp8_linear_fwd(X, W_master, make_view(*Xq), make_view(*Wq), Y, y_dtype, reinterpret_cast<float*>(workspace),
                                           (hipStream_t)stream),
                     "FP8 linear launch"));
@@ -1482,7 +1537,6 @@ size_t fp8_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K) {
 tj2_status fp8_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, const tj2_qtensor* Xq, const tj2_qtensor* Wq, void* dX,
                           int32_t dx_dtype, float* dW, void* workspace, size_t ws_bytes, void* stream) {
   if (!dY || !dX || !dW || !workspace) return fail(TJ2_ERR_ARG, "dY, dX, dW and workspace are required");
-  if (dX == dW) return fail(TJ2_ERR_ARG, "dX must not be dW");
   TJ2_TRY(check_linear_dims(M, N, K));
   TJ2_TRY(check_fp8(Xq, "Xq", TJ2_FP8, M, K));
   TJ2_TRY(check_fp8(Wq, "Wq", TJ2_FP8_BLOCK, N, K));
@@ -1494,6 +1548,10 @@ tj2_status fp8_linear_bwd(const void* dY, int64_t M, int64_t N, int64_t K, const
   TJ2_TRY(check_out_dtype(dx_dtype, "dx_dtype"));
   if (!aligned16(dY) || !aligned16(dX) || !aligned16(dW)) return fail(TJ2_ERR_ALIGN, "dY, dX and dW must be 16-byte aligned");
   TJ2_TRY(check_mx_workspace(workspace, ws_bytes, fp8_linear_bwd_workspace_bytes(M, N, K)));
+  const Region dy = dense("dY", dY, M * N, 2), xc = codes_of("Xq's codes", *Xq), xs = scales_of("Xq's scales", *Xq),
+               wc = codes_of("Wq's codes", *Wq), wss = scales_of("Wq's scales", *Wq), w = dense("dW", dW, N * K, 4);
+  TJ2_TRY(check_apart(dense("dX", dX, M * K, size_of(dx_dtype)), {dy, xc, xs, wc, wss, w}));
+  TJ2_TRY(check_apart(w, {dy, xc, xs, wc, wss}));
   TJ2_TRY(hip_check(launch_fp8_linear_bwd(dY, make_view(*Xq), make_view(*Wq), dX, dx_dtype, dW, workspace, (hipStream_t)stream),
                     "FP8 linear launch"));
   return ok();
@@ -1520,13 +1578,6 @@ tj2_status check_stream(const void* p, int64_t ld, int32_t dtype, int64_t cols, 
   if (ld < cols) return fail(TJ2_ERR_SHAPE, "%s: rows of %lld elements lie %lld apart", name, (long long)cols, (long long)ld);
   return TJ2_OK;
 }
-// A dense result may take an input's place where the rows are the same (with another pitch a
-// row's result would lie on rows that others still read).
-tj2_status check_in_place(const void* out, const char* out_name, const void* in, int64_t ld, int64_t rows, int64_t cols, const char* name) {
-  if (out && out == in && ld != cols && rows > 1)
-    return fail(TJ2_ERR_ARG, "%s can be %s only where its rows are %lld apart", out_name, name, (long long)cols);
-  return TJ2_OK;
-}
 
 }  // namespace
 
@@ -1542,12 +1593,7 @@ tj2_status tj2_rms_norm_fwd(const void* x, int64_t ldx, const void* residual, in
   if (residual) {
     TJ2_TRY(check_stream(residual, ldr, dtype, cols, "residual"));
     TJ2_TRY(check_stream(sum, cols, dtype, cols, "sum"));
-    TJ2_TRY(check_in_place(sum, "sum", x, ldx, rows, cols, "x"));
-    TJ2_TRY(check_in_place(sum, "sum", residual, ldr, rows, cols, "residual"));
-    if (y == sum) return fail(TJ2_ERR_ARG, "y must not be sum");
-    TJ2_TRY(check_in_place(y, "y", residual, ldr, rows, cols, "residual"));
   }
-  TJ2_TRY(check_in_place(y, "y", x, ldx, rows, cols, "x"));
   if ((y == nullptr) == (yq == nullptr)) return fail(TJ2_ERR_ARG, "one of y and yq must be given");
   TJ2_TRY(check_f32(rstd, "rstd", false));
   NormParams n = {};
@@ -1555,13 +1601,22 @@ tj2_status tj2_rms_norm_fwd(const void* x, int64_t ldx, const void* residual, in
     TJ2_TRY(check_stream(y, cols, dtype, cols, "y"));
   } else {
     TJ2_TRY(check_fp8(yq, "yq", TJ2_FP8, rows, cols));
-    const int64_t es = dtype == TJ2_BF16 ? 2 : 4;
     if (!aligned16(x) || !aligned16(residual) || !aligned16(sum) || !aligned16(weight))
       return fail(TJ2_ERR_ALIGN, "with an FP8 result x, residual, sum and weight must be 16-byte aligned");
-    if (ldx * es % 16 || (residual && ldr * es % 16))
+    if (ldx * size_of(dtype) % 16 || (residual && ldr * size_of(dtype) % 16))
       return fail(TJ2_ERR_ALIGN, "with an FP8 result the rows of x and residual must be 16-byte aligned");
     n.yq = make_view(*yq);
   }
+  const int64_t es = size_of(dtype);
+  const Region in = {"x", x, rows, ldx, cols, es}, res = {"residual", residual, rows, ldr, cols, es}, w = dense("weight", weight, cols, size_of(w_dtype)),
+               s = dense("sum", sum, rows * cols, es), r = dense("rstd", rstd, rows, 4), d = dense("y", y, rows * cols, es);
+  TJ2_TRY(check_in_place(s, {in, res}));
+  TJ2_TRY(check_apart(s, {w, r}));
+  TJ2_TRY(check_in_place(d, {in, res}));
+  TJ2_TRY(check_apart(d, {s, w, r}));
+  TJ2_TRY(check_apart(r, {in, res, w}));
+  if (yq)
+    for (const Region& q : {codes_of("yq's codes", *yq), scales_of("yq's scales", *yq)}) TJ2_TRY(check_apart(q, {in, res, w, s, r}));
   n.x = x;
   n.residual = residual;
   n.ldx = ldx;
@@ -1594,13 +1649,16 @@ tj2_status tj2_rms_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t
   if (!ds && !dw) return fail(TJ2_ERR_ARG, "ds or dw is required");
   if (dsum) TJ2_TRY(check_stream(dsum, ldd, dtype, cols, "dsum"));
   if (ds) TJ2_TRY(check_stream(ds, cols, dtype, cols, "ds"));
-  TJ2_TRY(check_in_place(ds, "ds", dy, lddy, rows, cols, "dy"));
-  TJ2_TRY(check_in_place(ds, "ds", s, lds, rows, cols, "s"));
-  TJ2_TRY(check_in_place(ds, "ds", dsum, ldd, rows, cols, "dsum"));
   if (dw) {
     if (reinterpret_cast<uintptr_t>(dw) & (w_dtype == TJ2_BF16 ? 1u : 3u)) return fail(TJ2_ERR_ALIGN, "dw must be aligned to its elements");
     TJ2_TRY(check_ce_workspace(workspace, ws_bytes, norm_grad_workspace_bytes(rows, cols)));
   }
+  const int64_t es = size_of(dtype);
+  const Region g = {"dy", dy, rows, lddy, cols, es}, x = {"s", s, rows, lds, cols, es}, d = {"dsum", dsum, rows, ldd, cols, es},
+               w = dense("weight", weight, cols, size_of(w_dtype)), r = dense("rstd", rstd, rows, 4), out = dense("ds", ds, rows * cols, es);
+  TJ2_TRY(check_in_place(out, {g, x, d}));
+  TJ2_TRY(check_apart(out, {w, r}));
+  TJ2_TRY(check_apart(dense("dw", dw, cols, size_of(w_dtype)), {out, g, x, d, w, r}));
   NormGradParams n = {};
   n.dy = dy;
   n.s = s;
@@ -1678,6 +1736,10 @@ tj2_status tj2_gated_ffn_fwd(const void* X, int64_t ldx, const void* Wg, const v
   TJ2_TRY(check_out_dtype(y_dtype, "y_dtype"));
   if (!aligned16(Y) || !aligned16(gu)) return fail(TJ2_ERR_ALIGN, "Y and gu must be 16-byte aligned");
   TJ2_TRY(check_ce_workspace(workspace, ws_bytes, ffn_fwd_workspace_bytes(T, D, F)));
+  // (X and the projections' weights have been read when Y is written)
+  const Region down = {"Wd", Wd, D, ldd, F, 2}, saved = dense("gu", gu, (int64_t)ffn_saved_bytes(T, F), 1);
+  TJ2_TRY(check_apart(dense("Y", Y, T * D, size_of(y_dtype)), {down, saved}));
+  TJ2_TRY(check_apart(saved, {Region{"X", X, T, ldx, D, 2}, Region{"Wg", Wg, F, ldw, D, 2}, Region{"Wu", Wu, F, ldw, D, 2}, down}));
   FfnParams f = ffn_params(X, ldx, Wg, Wu, ldw, Wd, ldd, T, D, F, act);
   f.gu = gu;
   f.Y = Y;
@@ -1698,14 +1760,20 @@ tj2_status tj2_gated_ffn_bwd(const void* dY, int64_t ldy, const void* X, int64_t
   TJ2_TRY(check_ffn(X, ldx, Wg, Wu, ldw, Wd, ldd, T, D, F, act));
   if (!dY || !gu) return fail(TJ2_ERR_ARG, "dY and gu are required");
   if (!dX && !dWg && !dWu && !dWd) return fail(TJ2_ERR_ARG, "dX, dWg, dWu or dWd is required");
-  for (const void* w : {dWg, dWu, dWd})
-    if (w && (w == dX || (w == dWg) + (w == dWu) + (w == dWd) > 1)) return fail(TJ2_ERR_ARG, "dX, dWg, dWu and dWd must not be one another");
   if (ldy < D || ldy % 8 || ldy > (int64_t)1 << 21) return fail(TJ2_ERR_SHAPE, "ldy must be a multiple of 8, at least D and at most 2^21");
   if (dX) TJ2_TRY(check_out_dtype(dx_dtype, "dx_dtype"));
   if (dWg || dWu || dWd) TJ2_TRY(check_out_dtype(dw_dtype, "dw_dtype"));
   if (!aligned16(dY) || !aligned16(gu) || !aligned16(dX) || !aligned16(dWg) || !aligned16(dWu) || !aligned16(dWd))
     return fail(TJ2_ERR_ALIGN, "dY, gu, dX, dWg, dWu and dWd must be 16-byte aligned");
   TJ2_TRY(check_ce_workspace(workspace, ws_bytes, ffn_bwd_workspace_bytes(T, D, F)));
+  const Region out[4] = {dense("dX", dX, T * D, size_of(dx_dtype)), dense("dWg", dWg, F * D, size_of(dw_dtype)),
+                         dense("dWu", dWu, F * D, size_of(dw_dtype)), dense("dWd", dWd, D * F, size_of(dw_dtype))};
+  for (int i = 0; i < 4; ++i) {
+    for (int k = 0; k < i; ++k) TJ2_TRY(check_apart(out[i], {out[k]}));
+    TJ2_TRY(check_apart(out[i], {Region{"dY", dY, T, ldy, D, 2}, Region{"X", X, T, ldx, D, 2}, Region{"Wg", Wg, F, ldw, D, 2},
+                                 Region{"Wu", Wu, F, ldw, D, 2}, Region{"Wd", Wd, D, ldd, F, 2},
+                                 dense("gu", gu, (int64_t)ffn_saved_bytes(T, F), 1)}));
+  }
   FfnParams f = ffn_params(X, ldx, Wg, Wu, ldw, Wd, ldd, T, D, F, act);
   f.gu = const_cast<void*>(gu);
   const FfnGradParams o = {dY, ldy, dX, dWg, dWu, dWd, dx_dtype, dw_dtype};

@@ -708,11 +708,12 @@ tj2_status tj2_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_
 /*
  * FP8 linears: E4M3FN elements under one fp32 scale per 128 elements of a row (TJ2_FP8:
  * activations, gradients) or per 128 x 128 (TJ2_FP8_BLOCK: weights), multiplied as they
- * are stored.  Operands are at most 2^22 elements long.
+ * are stored.  Operands are at most 2^22 elements long.  What a call writes (quantized
+ * operands too) must not overlap what it reads or another of its results: TJ2_ERR_ARG.
  *
  * fp8_quantize: a logical [rows, cols] tensor, cols a multiple of 16, dense (x_dtype
  * TJ2_BF16 / TJ2_F32, contiguous) or, for TJ2_GROUP_COL, FP8 (x_dtype TJ2_FP8, *x_q,
- * dequantized first; *out must not be *x_q).  TJ2_GROUP_ROW: *out is [rows, cols], TJ2_FP8
+ * dequantized first).  TJ2_GROUP_ROW: *out is [rows, cols], TJ2_FP8
  * or TJ2_FP8_BLOCK (rows need not be a multiple of 128); TJ2_GROUP_COL: groups along rows
  * (a multiple of 16), *out is [cols, rows], TJ2_FP8.  Per group with largest magnitude a:
  * scale S = fl(a / 448), elements fl(x fl(1 / S)), not beyond +-448, to the nearest E4M3
@@ -777,6 +778,7 @@ size_t fp8_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K);
  *   y = s rstd weight into y [rows, cols] of dtype, contiguous, or (y NULL) *yq, TJ2_FP8,
  *       quantized as fp8_quantize does from the unrounded fp32 values.  y may be x or residual
  *       where that is contiguous, but not sum.
+ * Any other overlap of a result with an input or another result is TJ2_ERR_ARG.
  * For yq, cols is a multiple of 16 and x, residual, their rows, sum and weight are 16-byte
  * aligned; else pointers are aligned to their elements.  Statistics are fp32: squares that
  * leave its range are infinite (rstd 0) or 0.  eps >= 0; a row of zeros with eps 0 is NaN.
@@ -792,7 +794,7 @@ tj2_status tj2_rms_norm_fwd(const void* x, int64_t ldx, const void* residual, in
  *        in for s itself; ds may be dy, s or dsum itself where that is contiguous;
  *   dw = sum over the rows of dy s rstd, [cols] of w_dtype, summed in fp32 in an order that
  *        only the sizes decide.
- * Either may be NULL.  workspace: tj2_rms_norm_bwd_workspace_size(rows, cols) bytes,
+ * Either may be NULL; other overlaps of a result with an input or the other are TJ2_ERR_ARG.  workspace: tj2_rms_norm_bwd_workspace_size(rows, cols) bytes,
  * 16-byte aligned, for dw.
  */
 tj2_status tj2_rms_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, int32_t dtype, int64_t rows, int64_t cols,
@@ -813,7 +815,7 @@ size_t tj2_rms_norm_bwd_workspace_size(int64_t rows, int64_t cols);
  * of them), 16-byte aligned, that receive G and U, rounded to 24 bits (fp32 without its last
  * 8), in a layout that the backward reads.  workspace: tj2_gated_ffn_fwd_workspace_size
  * (T, D, F) bytes, 16-byte aligned, required (H, and from 2048 tokens on copies of X and the
- * weights).
+ * weights).  Y overlaps neither Wd nor gu, and gu no other argument (TJ2_ERR_ARG).
  */
 tj2_status tj2_gated_ffn_fwd(const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, const void* Wd, int64_t ldd,
                              int64_t T, int64_t D, int64_t F, int32_t act, void* gu, void* Y, int32_t y_dtype, void* workspace,
@@ -831,7 +833,7 @@ size_t tj2_gated_ffn_saved_size(int64_t T, int64_t F);
  * workspace: tj2_gated_ffn_bwd_workspace_size(T, D, F) bytes, 16-byte aligned, required,
  * the same whichever gradients are asked for: dG and dU twice and H (10 T F bytes), copies
  * of X, dY and the weights, and partial sums.  The results overlap neither one another nor
- * an input.
+ * an input (TJ2_ERR_ARG).
  */
 tj2_status tj2_gated_ffn_bwd(const void* dY, int64_t ldy, const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw,
                              const void* Wd, int64_t ldd, int64_t T, int64_t D, int64_t F, int32_t act, const void* gu, void* dX,
