@@ -17,7 +17,9 @@
 #include <math.h>
 
 #include <algorithm>
+#include <array>
 #include <cfloat>
+#include <mutex>
 
 #include "tj2_bf16.h"
 
@@ -629,7 +631,8 @@ struct TileCost {
 constexpr TileCost kOne[3] = {{256, 256, 1, 0.75, 0.75, 4.5}, {128, 128, 2, 0.56, 0.73, 1.1}, {64, 128, 3, 0.44, 0.52, 0.0}},
                    kMany[3] = {{256, 256, 1, 1.6, 1.6, 5.0}, {128, 128, 2, 0.67, 0.97, 3.0}, {64, 128, 3, 0.5, 0.95, 3.0}};
 
-double plan_time(const FfnPlan& plan, const FfnSize* x, int n) {
+// The plan's time, or `least` where it is seen to take no less before the items are dealt out.
+double plan_time(const FfnPlan& plan, const FfnSize* x, int n, double least) {
   const TileCost c = (n == 1 ? kOne : kMany)[(int)plan.tiles];
   double count[kJobs], t[kJobs], items = 0.0, join = 0.0;
   for (int i = 0; i < n; ++i) {
@@ -642,13 +645,21 @@ double plan_time(const FfnPlan& plan, const FfnSize* x, int n) {
   double deep = std::min((double)c.per_cu, std::ceil(items / kCus));  // tiles of a CU at once
   if (n > 1 && deep > 1.0) deep = (double)c.per_cu;
   const double chunk = deep == 1.0 ? c.alone : c.alone + (c.full - c.alone) * (deep - 1.0) / (double)(c.per_cu - 1);
-  for (int i = 0; i < n; ++i) t[i] = t[i] * chunk + c.fixed;
+  if (join > 0.0) join += n == 1 ? 0.8 : 3.0;
+  double work = 0.0, longest = 0.0;
+  for (int i = 0; i < n; ++i) {
+    t[i] = t[i] * chunk + c.fixed;
+    work += count[i] * t[i];
+    longest = std::max(longest, t[i]);
+  }
+  // (a part in 10^9 for the rounding of the sums)
+  if ((std::max(longest, work / (deep * kCus)) + join) * (1.0 - 1e-9) > least) return least;
   for (int i = 1; i < n; ++i)  // the longest first
     for (int k = i; k > 0 && t[k] > t[k - 1]; --k) {
       std::swap(t[k], t[k - 1]);
       std::swap(count[k], count[k - 1]);
     }
-  return deal(deep * kCus, count, t, n) + (join > 0.0 ? join + (n == 1 ? 0.8 : 3.0) : 0.0);
+  return deal(deep * kCus, count, t, n) + join;
 }
 
 FfnPlan find_plan(const FfnSize* x, int n) {
@@ -660,7 +671,7 @@ FfnPlan find_plan(const FfnSize* x, int n) {
     // every choice for each product, equal ones (the gates' and factors' weights) alike
     auto choose = [&](auto&& self, int i) -> void {
       if (i == n) {
-        if (const double t = plan_time(c, x, n); t < least) {
+        if (const double t = plan_time(c, x, n, least); t < least) {
           least = t;
           best = c;
         }
@@ -682,27 +693,60 @@ FfnPlan find_plan(const FfnSize* x, int n) {
   return best;
 }
 
-// The last plans, by their sizes: a search takes up to a millisecond of the host.
-FfnPlan ffn_plan(const FfnSize* x, int n) {
-  struct Known {
-    int n = 0;
-    FfnSize x[kJobs];
-    FfnPlan plan;
-  };
-  constexpr int kKnown = 64;
-  static thread_local Known known[kKnown];
-  static thread_local int next = 0;
-  for (const Known& k : known) {
-    if (k.n != n) continue;
-    bool same = true;
-    for (int i = 0; i < n; ++i) same = same && k.x[i].p == x[i].p && k.x[i].q == x[i].q && k.x[i].k == x[i].k;
-    if (same) return k.plan;
+// What has been found for the last sizes, for all threads (a backward pass runs on one of its
+// own): 4 places for each of 256 remainders of the sizes, the oldest given up first.
+template <int N, class V>
+class Found {
+ public:
+  using Key = std::array<int64_t, N>;
+  bool get(const Key& key, V* v) {
+    std::lock_guard<std::mutex> lock(mu_);
+    for (const Entry& e : set(key))
+      if (e.used && e.key == key) {
+        *v = e.v;
+        return true;
+      }
+    return false;
   }
-  Known& k = known[next];
-  next = (next + 1) % kKnown;
-  k.n = n;
-  for (int i = 0; i < n; ++i) k.x[i] = x[i];
-  return k.plan = find_plan(x, n);
+  void put(const Key& key, const V& v) {
+    std::lock_guard<std::mutex> lock(mu_);
+    Entry* s = set(key);
+    std::copy_backward(s, s + kWays - 1, s + kWays);
+    s[0] = Entry{key, v, true};
+  }
+
+ private:
+  static constexpr int kWays = 4, kSets = 256;
+  struct Entry {
+    Key key;
+    V v;
+    bool used;
+  };
+  using Set = Entry[kWays];
+  Set& set(const Key& key) {
+    uint64_t h = 0;
+    for (const int64_t k : key) h = (h ^ (uint64_t)k) * 0x9E3779B97F4A7C15u;
+    return sets_[h >> 56];
+  }
+  std::mutex mu_;
+  Set sets_[kSets] = {};
+};
+
+// A search takes up to 0.1 ms of the host.
+FfnPlan ffn_plan(const FfnSize* x, int n) {
+  static Found<1 + 3 * kJobs, FfnPlan> found;
+  std::array<int64_t, 1 + 3 * kJobs> key = {n};
+  for (int i = 0; i < n; ++i) {
+    key[1 + 3 * i] = x[i].p;
+    key[2 + 3 * i] = x[i].q;
+    key[3 + 3 * i] = x[i].k;
+  }
+  FfnPlan plan;
+  if (!found.get(key, &plan)) {
+    plan = find_plan(x, n);
+    found.put(key, plan);
+  }
+  return plan;
 }
 size_t part_bytes(const FfnPlan& plan, const FfnSize* x, int n) {
   size_t b = 0;
@@ -813,7 +857,7 @@ struct FfnFwdSpace {
 };
 
 struct FfnBwdSpace {
-  size_t wd, w, x, dy, dyb, d, gt, ut, ht, part, bytes;
+  size_t wd, w, x, dy, dyb, d, gt, ut, ht, part;  // (partial sums last: part_most bytes)
   bool blocked;
   FfnBwdSpace(int64_t T, int64_t D, int64_t F) {
     size_t at = 0;
@@ -828,16 +872,22 @@ struct FfnBwdSpace {
     gt = take(blocked_bytes(F, T));
     ut = take(blocked_bytes(F, T));
     ht = take(blocked_bytes(F, T));
+    part = at;
+  }
+  // whichever gradients are asked for
+  static size_t part_most(int64_t T, int64_t D, int64_t F) {
+    static Found<3, size_t> found;
     size_t most = 0;
-    for (int want = 1; want < 8; ++want) {  // whichever gradients are asked for
-      FfnSize x4[kJobs];
-      const int n = sizes(T, D, F, want & 1, want & 2, want & 2, want & 4, x4);
-      most = std::max(most, part_bytes(ffn_plan(x4, n), x4, n));
-      const int m = sizes(T, D, F, want & 1, want & 2, false, want & 4, x4);
-      most = std::max(most, part_bytes(ffn_plan(x4, m), x4, m));
-    }
-    part = take(most);
-    bytes = at;
+    if (found.get({T, D, F}, &most)) return most;
+    for (int want = 1; want < 8; ++want)
+      for (const bool both : {true, false}) {
+        FfnSize x4[kJobs];
+        const int n = sizes(T, D, F, want & 1, want & 2, (want & 2) && both, want & 4, x4);
+        if (both || (want & 2)) most = std::max(most, part_bytes(ffn_plan(x4, n), x4, n));
+      }
+    most = up256(most);
+    found.put({T, D, F}, most);
+    return most;
   }
   static int sizes(int64_t T, int64_t D, int64_t F, bool dx, bool dwg, bool dwu, bool dwd, FfnSize* x) {
     int n = 0;
@@ -927,7 +977,9 @@ hipError_t launch_ffn_fwd(const FfnParams& f, void* ws, hipStream_t s) {
   return run_products(&y, &size, 1, reinterpret_cast<float*>(w + sp.part), s);
 }
 
-size_t ffn_bwd_workspace_bytes(int64_t T, int64_t D, int64_t F) { return FfnBwdSpace(T, D, F).bytes; }
+size_t ffn_bwd_workspace_bytes(int64_t T, int64_t D, int64_t F) {
+  return FfnBwdSpace(T, D, F).part + FfnBwdSpace::part_most(T, D, F);
+}
 
 hipError_t launch_ffn_bwd(const FfnParams& f, const FfnGradParams& o, void* ws, hipStream_t s) {
   const FfnBwdSpace sp(f.T, f.D, f.F);
