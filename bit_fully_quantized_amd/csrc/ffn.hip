@@ -169,11 +169,10 @@ __global__ __launch_bounds__(T::NT, T::WAVES) void ffn_gate_kernel(GateArgs p) {
   });
 }
 
-// Bound by that read's latency and, from 2048 wide on, its rate: 1 token of D 1024, F 4096 5.6
-// us (16.8 MB, 3.0 TB/s).
 // The same for up to 32 tokens: one read of the weights, 8 rows of each a wave (lane n
 // holds a gate's row where n & 2 is 0), so that a lane's four results are two gates and
-// their factors.  H is row-major; of up to 8 tokens in two bf16 parts (8 bits, and the next of
+// their factors.  Bound by that read's latency and, from 2048 wide on, its rate: 1 token of D
+// 1024, F 4096 5.6 us (16.8 MB, 3.0 TB/s).  H is row-major; of up to 8 tokens in two bf16 parts (8 bits, and the next of
 // what these leave), since their results have few of H's roundings to average over and the
 // second part takes places of the output product's instruction that are idle (a second
 // instruction for 9 to 32 tokens would cost 2 to 7 us of 11 to 45).
@@ -276,10 +275,10 @@ __global__ __launch_bounds__(256, 2) void ffn_gate_few_kernel(GateFewArgs p) {
   }
 }
 
-// Y = H Wd^T of up to 32 tokens: a workgroup takes 4 to 16 rows of Wd (fewer than the
-// instruction's 16 so that more CUs read: 1 token of D 1024, F
-// 4096 14.0 us with both kernels' waves on 64 to 128 CUs, 9.9 on all), its 16 waves the
-// reduction in turn, joined in LDS.
+// Y = H Wd^T of up to 32 tokens: a workgroup takes 4 or 8 rows of Wd (fewer than the
+// instruction's 16 so that more CUs read: 1 token of D 1024, F 4096 14.0 us with both
+// kernels' waves on 64 to 128 CUs, 9.9 on all), its 16 waves the reduction in turn, joined in
+// LDS.
 struct DownFewArgs {
   const uint16_t *h, *wd;
   int64_t ldw;
@@ -915,7 +914,7 @@ hipError_t launch_ffn_fwd(const FfnParams& f, void* ws, hipStream_t s) {
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
   uint16_t* h = reinterpret_cast<uint16_t*>(w + sp.h);
   if (sp.few) {
-    const int32_t down_rows = f.D >= 16 * kCus ? 16 : f.D >= 8 * kCus ? 8 : 4;
+    const int32_t down_rows = f.D >= 8 * kCus ? 8 : 4;  // (D is at most 2048 here)
     const GateFewArgs a = {reinterpret_cast<const uint16_t*>(f.X), reinterpret_cast<const uint16_t*>(f.Wg), reinterpret_cast<const uint16_t*>(f.Wu),
                            f.ldx, f.ldw, (int32_t)f.T, (int32_t)f.D, (int32_t)f.F, h, saved_of(f)};
     const DownFewArgs d = {h, reinterpret_cast<const uint16_t*>(f.Wd), f.ldd, (int32_t)f.T, (int32_t)f.D, (int32_t)f.F, down_rows, f.Y, f.y_dtype == TJ2_BF16};
