@@ -346,9 +346,10 @@ __global__ __launch_bounds__(1024) void ffn_down_few_kernel(DownFewArgs p) {
 
 // ---- dH and what follows from it ---------------------------------------------------------
 // G and U are read and dG, dU (in both layouts that the products read) and H written by the
-// lanes that hold dH, in registers throughout.  16384 x 1024, 4096 features: 315 us for 1.07
-// GB (3.4 TB/s) and 137 GFLOP (which take 108): bound by memory, which a tile's products
-// cover only in part (matrix units busy 20%).
+// lanes that hold dH.  16384 x 1024, 4096 features: 315 us for 1.07 GB (3.4 TB/s) and 137 GFLOP
+// (which take 108): bound by memory, which a tile's products cover only in part (matrix units
+// busy 20%).  A tile of 256 has no register to spare: 18 to 21 of a lane's wait in scratch (76
+// to 88 bytes) while another part of the tile has its turn; the tiles of 64 need none.
 struct DhArgs {
   TileOp P, Q;            // P: Wd^T [F, D], Q: dY [T, D]
   uint32_t tiles_p, tiles_q;

@@ -52,6 +52,9 @@ struct NormGradArgs {
 // Forward and backward with the residual's, in us: 16384 x 1023 bf16 25 and 42 as Tail, 32
 // and 42 where a branch loads the last vector's elements, 33 and 68 in pairs, 56 and 70 as
 // Single (16384 x 1024: 22 and 28); 1555 x 1003 fp32 5.7 and 10.3 as Single, 7.3 and 12.1 as Tail.
+// What Tail still costs: 16-byte accesses at odd elements, several of the L1 each (backward of
+// 16384 x 1023: 3.3 times the L1 accesses of 1024 columns for the same bytes of memory), and 1.7
+// times the vector instructions.
 enum class Deal { Whole, Tail, Single };
 
 template <int TPR, Deal D>
@@ -328,7 +331,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(NormGradArgs p)
 }
 
 // Longer rows: ds with the row read twice (L2 holds it), and dw's sums over a slab of rows by
-// columns, which reads s and dy again (1000 x 20000 bf16 55 us, both and norm_dw_kernel).
+// columns, which reads s and dy again, as a lane's columns of dw do not fit its registers (1000
+// x 20000 bf16 55 us: ds 37, the slabs 15 for 80 MB, norm_dw_kernel 5).
 template <class T, Deal D, bool DSUM>
 __global__ __launch_bounds__(kNormThreads) void norm_grad_long_kernel(NormGradArgs p) {
   using R = Row<kNormThreads, D>;

@@ -1,8 +1,9 @@
 """FP8 operands and the linear layer on them (the fp8_ entry points of include/tj2.h).
 
 E4M3 elements under one fp32 scale per 128 of a row (FP8: activations and gradients) or per 128 x 128 (FP8_BLOCK:
-weights), multiplied by gfx950's 8-bit matrix instructions as they are stored.  Names and arguments follow the MXFP4
-functions of the package; work runs on the current stream of the tensors' device.
+weights), multiplied by gfx950's 8-bit matrix instructions as they are stored (fp32 results: decoded, as exact
+products).  Names and arguments follow the MXFP4 functions of the package; work runs on the current stream of the
+tensors' device.
 """
 from __future__ import annotations
 

@@ -729,15 +729,17 @@ tj2_status fp8_dequantize(const tj2_qtensor* q, void* out, int32_t out_dtype, vo
 
 /*
  * C[i, j] (+)= sum_k A[i, k] B[j, k], A [I, K] TJ2_FP8 and B [J, K] TJ2_FP8 or
- * TJ2_FP8_BLOCK.  The 128 products of a chunk are summed in fp32 and multiplied by the
- * two scales, B's first with A's where it is a block's (a product of scales below 2^-126
- * loses bits), then added in fp32.  A NaN scale in a row of A (or B, or a block) makes
+ * TJ2_FP8_BLOCK.  The 128 products of a chunk are summed (for TJ2_F32 in fp32; for TJ2_BF16
+ * by the 8-bit instruction, which keeps 14 bits of the largest product where it adds
+ * neighbours) and multiplied by the two scales, B's first with A's where it is a block's (a
+ * product of scales below 2^-126 loses bits, one beyond fp32's range is infinite), then added
+ * in fp32.  A NaN scale in a row of A (or B, or a block) makes
  * that row (column, columns) of C NaN.  c_dtype TJ2_F32 or TJ2_BF16 (nearest), ldc >= J
  * in elements; accumulate != 0 adds into C (TJ2_F32 only).
  * workspace: partial sums of a reduction that is split because C has few tiles,
  * fp8_gemm_workspace_size(I, J, K) bytes (0: none needed); NULL runs unsplit, a smaller
- * non-NULL workspace is TJ2_ERR_ARG.  The order of the sums depends on the sizes and on
- * whether a workspace is given, and on nothing else.
+ * non-NULL workspace is TJ2_ERR_ARG.  The order of the sums depends on the sizes, c_dtype,
+ * B's format and whether a workspace is given, and on nothing else.
  */
 tj2_status fp8_gemm(const tj2_qtensor* A, const tj2_qtensor* B, void* C, int32_t c_dtype, int64_t ldc, int32_t accumulate,
                     void* workspace, size_t ws_bytes, void* stream);
