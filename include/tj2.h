@@ -796,8 +796,9 @@ tj2_status tj2_rms_norm_fwd(const void* x, int64_t ldx, const void* residual, in
  *        in for s itself; ds may be dy, s or dsum itself where that is contiguous;
  *   dw = sum over the rows of dy s rstd, [cols] of w_dtype, summed in fp32 in an order that
  *        only the sizes decide.
- * Either may be NULL; other overlaps of a result with an input or the other are TJ2_ERR_ARG.  workspace: tj2_rms_norm_bwd_workspace_size(rows, cols) bytes,
- * 16-byte aligned, for dw.
+ * Either may be NULL; other overlaps of a result with an input or the other are
+ * TJ2_ERR_ARG.  workspace: tj2_rms_norm_bwd_workspace_size(rows, cols) bytes, 16-byte
+ * aligned, for dw.
  */
 tj2_status tj2_rms_norm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, int32_t dtype, int64_t rows, int64_t cols,
                             const void* weight, int32_t w_dtype, const float* rstd, const void* dsum, int64_t ldd, void* ds, void* dw,
